@@ -24,6 +24,12 @@
  *   wf_dwt_lowpass_basis   the pyramid A_1..A_L of such a basis
  *   wf_step_basis          the whole step with such a basis
  *
+ * and, for caches in pages and the dense attentions around the path:
+ *
+ *   wf_paged_append        new rows into a paged cache, rotated on the way
+ *   wf_paged_attn          §2.1 eq. (3) of new tokens over a whole paged cache
+ *   wf_prefill_attn        §2.1 eq. (1) over packed prompts
+ *
  * Readings fixed where the pages are silent: orthonormal Haar filters
  * g = [1/√2, 1/√2] on 0-based pairs (2n, 2n+1), so coarse position p at
  * level j covers tokens [p·2^j, (p+1)·2^j); the score of a candidate is its
@@ -37,7 +43,8 @@
  *   Kg, Vg : [batch, heads, n_gen,    head_dim]   generation keys/values (I_g)
  *   Q      : [batch, heads, n_gen,    head_dim]   generation-block queries
  * Element type of Q/K/V: dims.dtype (WF_BF16 or WF_F32).  All arithmetic
- * accumulates in fp32; every float output is fp32.
+ * accumulates in fp32; every float output is fp32 (except the outputs of the
+ * dense attentions and the paged append, which have the inputs' type).
  *
  * Ownership and execution: the caller owns every buffer.  All pointers are
  * DEVICE pointers except those documented as host (k_per_level, dims).
@@ -439,6 +446,148 @@ int wf_step_basis(const wf_dims* dims, const double* lowpass, int32_t taps,
                   const void* Kg, const void* Vg, const int32_t* k_per_level,
                   float* O, float* lse, int32_t* idx_out, void* workspace,
                   size_t workspace_bytes, void* stream);
+
+/* ---- Paged cache and dense attention.  The filtering path works on dense
+ * per-sequence caches; these entry points serve the steps around it: the
+ * first step's full attention over prompt and generation block (§2.1 eq.
+ * (1)), and eq. (3) over a whole cache whose rows live in pages shared by
+ * many sequences.  Key-value heads may be shared: q_heads = g * kv_heads,
+ * query head h reads key-value head h / g.
+ *
+ * Pages: K_pages, V_pages [n_pages, kv_heads, page_size, head_dim].  Cache
+ * position n of sequence s is row n % page_size of page
+ * page_table[s][n / page_size].  New rows are token-major, [rows, heads,
+ * head_dim] with a row stride, as the projections write them (one fused
+ * projection's slices included).  Index arrays (offsets, lengths, positions,
+ * page tables) and slopes need 4-byte alignment only. */
+
+/* Most sequences of one paged call. */
+#define WF_MAX_SEQS 4096
+
+/* Sizes of a paged cache and of one call on it (host struct).
+ *   n_seqs      : sequences of the call, 1..WF_MAX_SEQS
+ *   q_heads     : query heads, a multiple of kv_heads
+ *   head_dim    : 64 or 128
+ *   page_size   : rows of a page: 8, 16, 32, 64, 128 or 256
+ *   n_pages     : pages of the pool (n_pages * kv_heads * page_size < 2^31)
+ *   table_pages : entries of a sequence's page table row
+ *   dtype       : WF_BF16 or WF_F32 (queries, keys, values, outputs) */
+typedef struct {
+  int32_t n_seqs, q_heads, kv_heads, head_dim, page_size, n_pages, table_pages, dtype;
+} wf_page_dims;
+
+/* Sizes of packed prompts (host struct): rows_q query rows and rows_k key
+ * rows of n_docs sequences in all; rows_q <= 2^26, rows_k <= 2^30. */
+typedef struct {
+  int32_t rows_q, rows_k, n_docs, q_heads, kv_heads, head_dim, dtype;
+} wf_prefill_dims;
+
+/* How scores are formed and masked (host struct; prefix and slopes are
+ * device pointers).  For the query at position p and key j of a sequence:
+ *   z = scale Q·K_j;  z <- softcap tanh(z / softcap) if softcap > 0;
+ *   z <- z - slopes[h] |p - j| if slopes is given;
+ * key j counts if not causal, or j <= p, or j < prefix[s].  A row without a
+ * visible key gets O = 0 and lse = -inf.
+ *   scale   : 0 means 1/sqrt(head_dim)
+ *   softcap : 0 means none
+ *   prefix  : nullable, [n_seqs] int32 (only read with causal)
+ *   slopes  : nullable, [q_heads] fp32 */
+typedef struct {
+  float scale, softcap;
+  int32_t causal;
+  const int32_t* prefix;
+  const float* slopes;
+} wf_attn_opts;
+
+/* Default rotation frequencies: out[i] = base^(-2i / rotary_dim) for i <
+ * rotary_dim / 2.  Host only.  Errors: WF_ERR_NULL, WF_ERR_UNSUPPORTED
+ * (rotary_dim not a multiple of 16 in 16..128, base not above 1). */
+int wf_rope_inv_freq(int32_t rotary_dim, double base, double* out);
+
+/* Appends new rows to a paged cache, rotated to their positions on the way.
+ * Row t of sequence s (cu_rows[s] <= t < cu_rows[s+1]) takes cache position
+ * n = cache_len[s] + (t - cu_rows[s]).  Keys (and queries) are rotated by
+ * the angles p * inv_freq[i], p = n or positions[t]: pair i is channels
+ * (i, i + rotary_dim/2), or (2i, 2i + 1) if interleaved; (x, y) becomes
+ * (x cos - y sin, x sin + y cos), formed in fp32 from exactly reduced angles
+ * and rounded once.  Channels from rotary_dim on, and values, are copied.
+ *   Q, K, V   : device, [n_rows, heads, d], row strides in elements (rows of
+ *               whole 16-byte chunks); Q nullable together with Q_out
+ *   cu_rows   : device, [n_seqs + 1] int32 ascending row offsets; rows from
+ *               cu_rows[n_seqs] on are neither written nor copied
+ *   cache_len : device, [n_seqs] int32, rows each cache holds already (not
+ *               updated: the caller adds its new rows)
+ *   positions : device, nullable, [n_rows] int32 rotation positions
+ *   page_table: device, [n_seqs, table_pages] int32
+ *   inv_freq  : HOST, rotary_dim/2 doubles (radians per position); read
+ *               during the call only
+ *   rotary_dim: 0 (no rotation) or a multiple of 16 up to head_dim
+ *   K_pages, V_pages : device, in/out
+ *   Q_out     : device, [n_rows, q_heads, d] contiguous (may be Q itself if
+ *               Q is contiguous)
+ *   K_out     : device, nullable, [n_rows, kv_heads, d] contiguous: the
+ *               rotated keys once more, for the prompt's own attention
+ *   workspace : device, nullable, >= 256 bytes: a position without a page
+ *               (behind the table, or a page outside [0, n_pages)) raises
+ *               WF_DEV_BAD_INDEX in its status word; its cache row is
+ *               skipped either way
+ * Two rows must not share a cache position.  n_rows = 0 is a no-op.  One
+ * launch.  Errors: WF_ERR_NULL, WF_ERR_SHAPE, WF_ERR_UNSUPPORTED,
+ * WF_ERR_ALIGNMENT, WF_ERR_WORKSPACE, WF_ERR_CUDA. */
+int wf_paged_append(const wf_page_dims* dims, int32_t n_rows, const void* Q, int64_t q_stride,
+                    const void* K, int64_t k_stride, const void* V, int64_t v_stride,
+                    const int32_t* cu_rows, const int32_t* cache_len, const int32_t* positions,
+                    const int32_t* page_table, const double* inv_freq, int32_t rotary_dim,
+                    int32_t interleaved, void* K_pages, void* V_pages, void* Q_out, void* K_out,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace wf_paged_attn needs for these sizes on the current
+ * device (status word and the partial results of split sequences).
+ * Errors: WF_ERR_NULL, WF_ERR_SHAPE, WF_ERR_UNSUPPORTED. */
+int wf_paged_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_new, size_t* bytes);
+
+/* Attention of each sequence's n_new newest tokens over its paged cache (eq.
+ * (3) over the whole cache; one new token, or a generation block).  Query i
+ * of sequence s stands at position kv_len[s] - n_new + i.
+ *   n_new      : 1..64, the same for every sequence
+ *   Q          : device, [n_seqs, n_new, q_heads, d]
+ *   kv_len     : device, [n_seqs] int32, rows of each cache, the new tokens'
+ *                included; 0 marks an idle sequence (O = 0, lse = -inf).  A
+ *                length outside [0, table_pages * page_size] is clamped and
+ *                flagged WF_DEV_BAD_INDEX
+ *   page_table : device, [n_seqs, table_pages] int32; only entries below
+ *                ceil(kv_len / page_size) are read.  The rows of a page
+ *                outside [0, n_pages) do not count (flagged)
+ *   O          : device, out, [n_seqs, n_new, q_heads, d] of dims.dtype
+ *   lse        : device, out, nullable, [n_seqs, n_new, q_heads] fp32
+ *   workspace  : device, >= wf_paged_attn_workspace_bytes(); overwritten.
+ *                Calls that overlap (captured ones included) need their own
+ * Rows behind kv_len never reach the result, whatever they hold; the values
+ * of rows below kv_len must be finite even where the mask hides them.  Two
+ * launches.  Errors: as wf_paged_append. */
+int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_new, const void* Q,
+                  const void* K_pages, const void* V_pages, const int32_t* page_table,
+                  const int32_t* kv_len, void* O, float* lse, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Attention of packed sequences over their own keys (§2.1 eq. (1) per
+ * sequence; sequences never see each other).  Sequence s has query rows
+ * cu_q[s] .. cu_q[s+1] and key rows cu_k[s] .. cu_k[s+1]; its queries are
+ * the last of its positions: query i stands at n_k - n_q + i.
+ *   Q, K, V    : device, [rows, heads, d], row strides in elements
+ *   cu_q, cu_k : device, [n_docs + 1] int32 ascending (flagged and clamped
+ *                otherwise)
+ *   O          : device, out, [rows_q, q_heads, d] of dims.dtype; rows from
+ *                cu_q[n_docs] on are left as they were
+ *   lse        : device, out, nullable, [rows_q, q_heads] fp32
+ *   workspace  : device, nullable, >= 256 bytes (status word)
+ * Rows of other sequences never reach a result, whatever they hold; a
+ * sequence's own values must be finite even where the mask hides them.  One
+ * launch.  Errors: as wf_paged_append. */
+int wf_prefill_attn(const wf_prefill_dims* dims, const wf_attn_opts* opts, const void* Q,
+                    int64_t q_stride, const void* K, int64_t k_stride, const void* V,
+                    int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, void* O,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Size of the device scratch array behind wf_step_static_scratch (48 MiB). */
 #define WF_STATIC_SCRATCH_BYTES (48u << 20)

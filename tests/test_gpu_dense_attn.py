@@ -1,0 +1,412 @@
+"""GPU checks of the paged append, the paged attention and the packed-prompt
+attention against 64-bit references, through the public entry points.  Rows no
+result may depend on hold NaN or infinities."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from dense_common import attend, check, f64, half_step, rotate, rotation_bound
+from wavelet_guided_sparse_gb300 import binding as bd
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def randn(shape, dtype, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def offsets(lens):
+    return i32([0] + list(np.cumsum(lens)))
+
+
+def make_table(lens, page, seed, spare=2, width=None):
+    """Shuffled pages per sequence, bad entries behind the used ones."""
+    need = [-(-n // page) for n in lens]
+    order = np.random.default_rng(seed).permutation(sum(need) + spare)
+    width = width or max(max(need), 1)
+    table = np.full((len(lens), width), -7, np.int64)
+    at = 0
+    for s, n in enumerate(need):
+        table[s, :n] = order[at:at + n]
+        at += n
+    return i32(table.tolist()), sum(need) + spare
+
+
+def slope_list(hq):
+    return torch.tensor([2.0 ** (-8 * (h + 1) / hq) for h in range(hq)], device="cuda")
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("dtype,d,hq,hkv,page,new,before,rotary,inter,keep,extra", [
+    (BF, 128, 32, 8, 16, [1, 1, 1], [0, 17, 8191], 128, False, False, 0),
+    (BF, 128, 4, 4, 64, [130, 0, 1, 77], [5, 3, 63, 64], 128, True, True, 3),
+    (BF, 64, 6, 2, 8, [33], [131000], 32, False, True, 0),
+    (BF, 128, 0, 1, 256, [300, 5], [0, 1], 16, True, False, 2),
+    (F32, 64, 2, 2, 32, [100, 29], [1000000, 7], 64, False, True, 1),
+    (F32, 128, 3, 1, 128, [9], [250], 48, True, False, 0),
+    (F32, 64, 1, 1, 8, [4], [0], 0, False, True, 0),
+    (BF, 128, 8, 8, 32, [3000], [0], 128, False, True, 0),   # several lines a thread
+])
+def test_append(dtype, d, hq, hkv, page, new, before, rotary, inter, keep, extra):
+    t = sum(new) + extra
+    fused = randn((t, hq + 2 * hkv, d), dtype, 3)     # one projection's slices: strided rows
+    q = fused[:, :hq] if hq else None
+    k, v = fused[:, hq:hq + hkv], fused[:, hq + hkv:]
+    # Positions past a million rows need a long table: offset it to the rows used.
+    shift = [b // page * page if b > 100000 else 0 for b in before]
+    pos_over = None
+    if any(shift):
+        pos_over = i32([b + i for b, n in zip(before, new) for i in range(n)] + [0] * extra)
+        before_dev = [b - s for b, s in zip(before, shift)]
+    else:
+        before_dev = before
+    table, pages = make_table([b + n for b, n in zip(before_dev, new)], page, 5)
+    cache = bd.alloc_paged_cache(pages, hkv, page, d, dtype, "cuda")
+    for x in cache.values():
+        x.fill_(0.25)
+    out = {"Q": torch.full((t, hq, d), 7.0, dtype=dtype, device="cuda")} if hq else {}
+    if keep:
+        out["K"] = torch.full((t, hkv, d), 7.0, dtype=dtype, device="cuda")
+    ws = bd.alloc_status_workspace("cuda")
+    freq = bd.rope_inv_freq(rotary) if rotary else None
+    res = bd.paged_append(k, v, cache, table, offsets(new), i32(before_dev), q=q, inv_freq=freq,
+                          interleaved=inter, positions=pos_over, keep_keys=keep, out=out, ws=ws)
+    assert bd.read_device_status(ws) == 0
+    pos = np.concatenate([np.arange(b, b + n) for b, n in zip(before, new)])
+    cpos = np.concatenate([np.arange(b, b + n) for b, n in zip(before_dev, new)])
+    live = sum(new)
+    fr = [] if freq is None else list(freq)
+    kx = f64(k)[:live]
+    kr = rotate(kx, pos, fr, inter)
+    kb = rotation_bound(kx, rotary, inter, kr, dtype)
+    kb[..., rotary:] = 0
+    ref_k, ref_v = f64(cache["K"]) * 0 + 0.25, f64(cache["V"]) * 0 + 0.25
+    bound = np.zeros_like(ref_k)
+    tab = table.cpu().numpy()
+    seq = np.repeat(np.arange(len(new)), new)
+    for i in range(live):
+        pg, r = tab[seq[i], cpos[i] // page], cpos[i] % page
+        ref_k[pg, :, r], ref_v[pg, :, r], bound[pg, :, r] = kr[i], f64(v[i]), kb[i]
+    check(f64(cache["K"]), ref_k, bound, "key pages")
+    np.testing.assert_array_equal(f64(cache["V"]), ref_v)
+    if hq:
+        qx = f64(q)[:live]
+        qr = rotate(qx, pos, fr, inter)
+        qb = rotation_bound(qx, rotary, inter, qr, dtype)
+        qb[..., rotary:] = 0
+        check(f64(res["Q"])[:live], qr, qb, "queries")
+        assert (res["Q"][live:] == 7).all()           # rows behind the last sequence
+    if keep:
+        check(f64(res["K"])[:live], kr, kb, "kept keys")
+        assert (res["K"][live:] == 7).all()
+
+
+def test_append_in_place_queries_and_many_sequences():
+    n, hkv, d, page = 1500, 2, 64, 8
+    new = [1 if i % 3 else 2 for i in range(n)]
+    t = sum(new)
+    q, k, v = (randn((t, hkv, d), BF, s) for s in (1, 2, 3))
+    table, pages = make_table([5 + m for m in new], page, 0)
+    cache = bd.alloc_paged_cache(pages, hkv, page, d, BF, "cuda")
+    freq = bd.rope_inv_freq(64, 500000.0)
+    q0 = f64(q)
+    bd.paged_append(k, v, cache, table, offsets(new), i32([5] * n), q=q, inv_freq=freq,
+                    out={"Q": q})
+    pos = np.concatenate([5 + np.arange(m) for m in new])
+    ref = rotate(q0, pos, list(freq), False)
+    check(f64(q), ref, rotation_bound(q0, 64, False, ref, BF), "queries in place")
+
+
+def test_append_flags_positions_without_a_page():
+    page, d = 8, 64
+    k, v = randn((12, 1, d), BF, 1), randn((12, 1, d), BF, 2)
+    table = i32([[0, 99], [1, -1]])         # 99 and -1: outside the pool of 3
+    cache = {n: torch.zeros((3, 1, page, d), dtype=BF, device="cuda") for n in ("K", "V")}
+    ws = bd.alloc_status_workspace("cuda")
+    # Sequence 0: rows 4..9 (page 0, then the bad 99); sequence 1: rows 14.. (bad, then
+    # behind the table).
+    bd.paged_append(k, v, cache, table, i32([0, 6, 12]), i32([4, 14]), ws=ws)
+    assert bd.read_device_status(ws) == bd.DEV_BAD_INDEX
+    ref = torch.zeros_like(cache["K"])
+    ref[0, 0, 4:8] = k[:4, 0]
+    assert torch.equal(cache["K"], ref)
+
+
+# ------------------------------------------------------------------ paged attention
+def run_paged(dtype, d, hq, hkv, page, lens, new, causal, prefix, cap, bias, seed=0, scale=None):
+    s = len(lens)
+    table, pages = make_table(lens, page, seed)
+    cache = {"K": randn((pages, hkv, page, d), dtype, seed + 1),
+             "V": randn((pages, hkv, page, d), dtype, seed + 2)}
+    q = randn((s, new, hq, d), dtype, seed + 3, 2.0)
+    # Rows behind the lengths (and pages nobody has) hold what must not matter.
+    tab = table.cpu().numpy()
+    live = torch.zeros((pages, page), dtype=torch.bool)
+    for i, n in enumerate(lens):
+        for j in range(n):
+            live[tab[i, j // page], j % page] = True
+    dead = ~live.cuda()
+    for x, bad in ((cache["K"], math.nan), (cache["V"], math.inf)):
+        x.masked_fill_(dead[:, None, :, None], bad)
+    pre = None if prefix is None else i32(prefix)
+    slopes = slope_list(hq) if bias else None
+    ws = bd.alloc_paged_attn_workspace(q, cache, table)
+    o, lse = bd.paged_attn(q, cache, table, i32(lens), ws, causal=causal, prefix=pre, softcap=cap,
+                           slopes=slopes, scale=scale, with_lse=True)
+    assert bd.read_device_status(ws) == 0
+    kc, vc = f64(cache["K"]), f64(cache["V"])
+    for i, n in enumerate(lens):
+        kk = np.concatenate([kc[p] for p in tab[i, :-(-n // page)]], 1)[:, :n] if n else \
+            np.zeros((hkv, 0, d))
+        vv = np.concatenate([vc[p] for p in tab[i, :-(-n // page)]], 1)[:, :n] if n else \
+            np.zeros((hkv, 0, d))
+        ro, rl, ob, lb = attend(f64(q[i]), kk.transpose(1, 0, 2), vv.transpose(1, 0, 2), dtype,
+                                causal, 0 if prefix is None else prefix[i], cap,
+                                None if slopes is None else slopes.cpu().numpy(), scale)
+        check(f64(lse[i]), rl, lb, f"lse of sequence {i}")
+        check(f64(o[i]), ro, ob, f"O of sequence {i}")
+    return o, lse, (q, cache, table, i32(lens), ws)
+
+
+PAGED = [
+    # dtype, d, hq, hkv, page, lens, new, causal, prefix, cap, bias
+    (BF, 128, 32, 8, 16, [1], 1, True, None, 0.0, False),
+    (BF, 128, 32, 8, 16, [1, 17, 64, 65, 0, 1000], 1, True, None, 0.0, False),
+    (BF, 128, 4, 4, 64, [63, 129, 300], 1, False, None, 20.0, True),
+    (BF, 64, 12, 4, 8, [5, 200, 31], 5, True, [0, 150, 31], 0.0, True),
+    (BF, 128, 8, 1, 32, [777], 3, True, None, 50.0, False),          # 24 rows a block
+    (BF, 128, 2, 2, 256, [64, 70, 4097], 64, True, None, 0.0, False),
+    (BF, 64, 6, 2, 16, [500, 90], 32, False, None, 0.0, False),      # 96 rows: two blocks
+    (BF, 128, 16, 1, 16, [260], 1, True, None, 0.0, False),
+    (BF, 128, 40, 1, 128, [513], 1, True, None, 0.0, False),         # 40 rows
+    (BF, 64, 1, 1, 8, [3, 2], 8, True, None, 0.0, False),            # rows before any key
+    (F32, 64, 2, 2, 32, [1056], 32, False, None, 0.0, False),
+    (F32, 128, 4, 1, 16, [1, 0, 333], 1, True, None, 30.0, True),
+    (F32, 64, 9, 3, 8, [100, 41], 4, True, [60, 0], 0.0, False),
+    (F32, 128, 2, 2, 64, [3, 130], 7, True, None, 0.0, True),
+]
+
+
+@pytest.mark.parametrize("case", PAGED)
+def test_paged(case):
+    run_paged(*case)
+
+
+def test_paged_long_splits_and_is_deterministic():
+    o, lse, args = run_paged(BF, 128, 8, 2, 64, [9000, 30001], 1, True, None, 0.0, False)
+    for _ in range(3):
+        o2, lse2 = bd.paged_attn(*args, with_lse=True)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_paged_many_short_sequences():
+    rng = np.random.default_rng(3)
+    run_paged(BF, 64, 2, 1, 16, rng.integers(0, 90, 700).tolist(), 1, True, None, 0.0, False)
+
+
+def test_paged_large_scores_and_scale():
+    # Scores of some hundreds: one key carries the row; nothing overflows.
+    run_paged(BF, 128, 4, 2, 16, [70, 300], 2, True, None, 0.0, False, scale=4.0)
+
+
+def test_paged_bad_pages_and_lengths_are_flagged():
+    page, d, hkv = 16, 128, 1
+    cache = {"K": randn((4, hkv, page, d), BF, 1), "V": randn((4, hkv, page, d), BF, 2)}
+    q = randn((2, 1, 2, d), BF, 3)
+    table = i32([[2, 77, 3], [0, 1, 3]])
+    ws = bd.alloc_paged_attn_workspace(q, cache, table)
+    o, lse = bd.paged_attn(q, cache, table, i32([40, 32]), ws, causal=False, with_lse=True)
+    assert bd.read_device_status(ws) == bd.DEV_BAD_INDEX
+    # The bad page's rows do not count: sequence 0 is page 2 and 8 rows of page 3.
+    good = torch.cat([cache["K"][2, 0], cache["K"][3, 0, :8]])[:, None]
+    goodv = torch.cat([cache["V"][2, 0], cache["V"][3, 0, :8]])[:, None]
+    ro, rl, ob, lb = attend(f64(q[0]), f64(good), f64(goodv), BF, False)
+    check(f64(o[0]), ro, ob, "O past a bad page")
+    check(f64(lse[0]), rl, lb, "lse past a bad page")
+    bd.clear_device_status(ws)
+    o2 = bd.paged_attn(q, cache, i32([[2, 1, 3], [0, 1, 3]]), i32([4000, -3]), ws, causal=False)
+    assert bd.read_device_status(ws) == bd.DEV_BAD_INDEX
+    full = torch.cat([cache["K"][2, 0], cache["K"][1, 0], cache["K"][3, 0]])[:, None]
+    fullv = torch.cat([cache["V"][2, 0], cache["V"][1, 0], cache["V"][3, 0]])[:, None]
+    ro, _, ob, _ = attend(f64(q[0]), f64(full), f64(fullv), BF, False)
+    check(f64(o2[0]), ro, ob, "O of a clamped length")
+    assert (o2[1] == 0).all()
+
+
+# ------------------------------------------------------------------ packed prompts
+def run_prefill(dtype, d, hq, hkv, nq, nk, causal, prefix, cap, bias, extra=0, seed=0):
+    tq, tk = sum(nq), sum(nk)
+    fused = randn((tq + extra, hq, d), dtype, seed + 1, 2.0)
+    kv = randn((tk + extra, 2 * hkv, d), dtype, seed + 2)
+    kv[tk:] = math.nan
+    k, v = kv[:, :hkv], kv[:, hkv:]
+    pre = None if prefix is None else i32(prefix)
+    slopes = slope_list(hq) if bias else None
+    out = torch.full((tq + extra, hq, d), 7.0, dtype=dtype, device="cuda")
+    ws = bd.alloc_status_workspace("cuda")
+    o, lse = bd.prefill_attn(fused, k, v, offsets(nq), None if nq == nk else offsets(nk),
+                             causal=causal, prefix=pre, softcap=cap, slopes=slopes, out=out,
+                             with_lse=True, ws=ws)
+    assert bd.read_device_status(ws) == 0
+    aq = ak = 0
+    for s, (a, b) in enumerate(zip(nq, nk)):
+        ro, rl, ob, lb = attend(f64(fused[aq:aq + a]), f64(k[ak:ak + b]), f64(v[ak:ak + b]), dtype,
+                                causal, 0 if prefix is None else prefix[s], cap,
+                                None if slopes is None else slopes.cpu().numpy())
+        check(f64(lse[aq:aq + a]), rl, lb, f"lse of sequence {s}")
+        check(f64(o[aq:aq + a]), ro, ob, f"O of sequence {s}")
+        aq, ak = aq + a, ak + b
+    assert (o[tq:] == 7).all()
+    return fused, k, v, o, lse
+
+
+PREFILL = [
+    # dtype, d, hq, hkv, n_q, n_k, causal, prefix, cap, bias, extra
+    (BF, 128, 2, 2, [1], [1], True, None, 0.0, False, 0),
+    (BF, 128, 4, 4, [128], [128], False, None, 0.0, False, 0),
+    (BF, 128, 4, 2, [129], [129], True, None, 0.0, False, 5),
+    (BF, 128, 8, 2, [700], [700], True, None, 0.0, False, 0),
+    (BF, 128, 3, 1, [300, 17, 0, 1, 257], [300, 17, 0, 1, 257], True, [100, 17, 0, 0, 5], 0.0, False, 1),
+    (BF, 128, 5, 5, [255, 40], [255, 40], False, None, 20.0, True, 0),
+    (BF, 64, 4, 2, [513, 2], [513, 2], True, None, 30.0, False, 9),
+    (BF, 64, 2, 1, [64, 90], [64, 90], False, None, 0.0, True, 0),
+    (BF, 128, 2, 1, [5, 130, 3], [300, 20, 0], True, None, 0.0, False, 0),   # empty rows
+    (BF, 128, 2, 2, [7, 3], [1000, 129], False, None, 0.0, False, 0),
+    (BF, 64, 8, 8, [1100], [1100], True, [700], 50.0, True, 0),
+    (F32, 64, 2, 2, [150, 1, 33], [150, 1, 33], True, [20, 0, 33], 0.0, False, 2),
+    (F32, 128, 4, 2, [70], [200], True, None, 30.0, True, 0),
+    (F32, 128, 3, 1, [65], [65], False, None, 0.0, False, 0),
+    (F32, 64, 2, 1, [30, 4], [10, 0], True, None, 0.0, False, 0),            # empty rows
+]
+
+
+@pytest.mark.parametrize("case", PREFILL)
+def test_prefill(case):
+    run_prefill(*case)
+
+
+def test_prefill_sequences_never_see_each_other():
+    # The middle sequence holds NaN and infinities in its keys and values.
+    d, h, lens = 128, 2, [100, 60, 77]
+    q, k, v = (randn((sum(lens), h, d), BF, s) for s in (1, 2, 3))
+    k[100:160], v[100:160] = math.inf, math.nan
+    for causal in (True, False):
+        o = bd.prefill_attn(q, k, v, offsets(lens), causal=causal)
+        for a, n in ((0, 100), (160, 77)):
+            ro, _, ob, _ = attend(f64(q[a:a + n]), f64(k[a:a + n]), f64(v[a:a + n]), BF, causal)
+            check(f64(o[a:a + n]), ro, ob, "a clean sequence")
+
+
+def test_prefill_keys_hidden_by_the_mask_may_hold_anything():
+    # Keys (not values) of hidden positions: infinities, NaN, the type's lowest.
+    d, n = 128, 200
+    q, k, v = (randn((n, 2, d), BF, s) for s in (1, 2, 3))
+    k[150], k[170], k[180] = math.nan, math.inf, torch.finfo(BF).min
+    o = bd.prefill_attn(q, k, v, offsets([n]), causal=True)
+    ro, _, ob, _ = attend(f64(q[:150]), f64(k[:150]), f64(v[:150]), BF, True)
+    check(f64(o[:150]), ro, ob, "rows that do not see them")
+
+
+@pytest.mark.parametrize("offs", [[0, 40, 20, 60], [0, 30, 90], [-5, 30]])
+def test_prefill_bad_offsets_are_flagged(offs):
+    q, k, v = (randn((60, 1, 64), BF, s) for s in (1, 2, 3))
+    ws = bd.alloc_status_workspace("cuda")
+    bd.prefill_attn(q, k, v, i32(offs), ws=ws)
+    assert bd.read_device_status(ws) == bd.DEV_BAD_INDEX
+
+
+# ------------------------------------------------------------------ as used together
+def test_serving_run_and_the_filtering_path_agree():
+    """Prompt in (append + prefill), one generation block (append + paged
+    attention), and the filtering path's own attention over the same rotated
+    cache: with every prompt row selected it is the paged attention."""
+    h, d, n, g, page, dt = 4, 128, 512, 32, 16, BF
+    freq = bd.rope_inv_freq(d)
+    q, k, v = (randn((n + g, h, d), dt, s) for s in (1, 2, 3))
+    table, pages = make_table([n + g], page, 4)
+    cache = bd.alloc_paged_cache(pages, h, page, d, dt, "cuda")
+    zero = i32([0])
+    first = bd.paged_append(k[:n], v[:n], cache, table, offsets([n]), zero, q=q[:n],
+                            inv_freq=freq, keep_keys=True)
+    o1 = bd.prefill_attn(first["Q"], first["K"], v[:n], offsets([n]), causal=False)
+    ro, _, ob, _ = attend(f64(first["Q"]), f64(first["K"]), f64(v[:n]), dt, False)
+    check(f64(o1), ro, ob, "prompt attention")
+    block = bd.paged_append(k[n:], v[n:], cache, table, offsets([g]), i32([n]), q=q[n:],
+                            inv_freq=freq, keep_keys=True)
+    o2, lse2 = bd.paged_attn(block["Q"][None], cache, table, i32([n + g]), causal=False,
+                             with_lse=True)
+    keys = torch.cat([first["K"], block["K"]])
+    ro, rl, ob, lb = attend(f64(block["Q"]), f64(keys), f64(v), dt, False)
+    check(f64(o2[0]), ro, ob, "block attention")
+    check(f64(lse2[0]), rl, lb, "block lse")
+    # The dense cache of the filtering path from the same rotated keys.
+    dense = bd.cache_init(keys[None].contiguous(), v[None].contiguous(), n, 3)
+    qh = block["Q"].transpose(0, 1)[None].contiguous()
+    idx = torch.arange(n, dtype=torch.int32, device="cuda").expand(1, h, n).contiguous()
+    o3, lse3 = bd.sparse_gather_attn(qh, dense["Kp"], dense["Vp"], dense["Kg"], dense["Vg"], idx, 3,
+                                     bd.alloc_status_workspace("cuda"), with_lse=True)
+    assert (o3[0].transpose(0, 1) - o2[0].float()).abs().max() < 2e-2
+    assert (lse3[0].t() - lse2[0]).abs().max() < 1e-3
+
+
+def test_captured_run_replays_with_new_lengths():
+    """A decoding step captured once and replayed as the cache grows: lengths
+    are device data, so the same graph serves every step."""
+    s, hq, hkv, d, page, steps = 3, 8, 2, 128, 16, 20
+    start = [1, 15, 100]
+    table, pages = make_table([n + steps for n in start], page, 1)
+    cache = bd.alloc_paged_cache(pages, hkv, page, d, BF, "cuda")
+    for x in cache.values():
+        x.zero_()
+    hist_k = [randn((n, hkv, d), BF, 10 + i) for i, n in enumerate(start)]
+    hist_v = [randn((n, hkv, d), BF, 20 + i) for i, n in enumerate(start)]
+    bd.paged_append(torch.cat(hist_k), torch.cat(hist_v), cache, table, offsets(start),
+                    i32([0] * s))
+    q, k, v = (torch.zeros((s, h, d), dtype=BF, device="cuda") for h in (hq, hkv, hkv))
+    cu, held, lens = offsets([1] * s), i32(start), i32([n + 1 for n in start])
+    ws = bd.alloc_paged_attn_workspace(q[:, None], cache, table)
+    o = torch.empty((s, 1, hq, d), dtype=BF, device="cuda")
+
+    def step():
+        bd.paged_append(k, v, cache, table, cu, held)
+        bd.paged_attn(q[:, None], cache, table, lens, ws, out=o)
+        held.add_(1)
+        lens.add_(1)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for t in range(steps):
+        for x, seed in ((q, 100), (k, 200), (v, 300)):
+            x.copy_(randn(x.shape, BF, seed + t))
+        graph.replay()
+        hist_k = [torch.cat([a, k[i:i + 1]]) for i, a in enumerate(hist_k)]
+        hist_v = [torch.cat([a, v[i:i + 1]]) for i, a in enumerate(hist_v)]
+        for i in range(s):
+            ro, _, ob, _ = attend(f64(q[i:i + 1]), f64(hist_k[i]), f64(hist_v[i]), BF, True)
+            check(f64(o[i]), ro, ob, f"step {t}, sequence {i}")
+
+
+def test_streams_and_two_calls_at_once():
+    args = run_paged(BF, 64, 4, 2, 16, [3000, 500], 1, True, None, 0.0, False)[2]
+    q, cache, table, lens, ws = args
+    ref = bd.paged_attn(*args)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for _ in range(5):
+        for st in streams:
+            outs.append(bd.paged_attn(q, cache, table, lens, stream=st))   # own workspaces
+    torch.cuda.synchronize()
+    assert all(torch.equal(ref, x) for x in outs)

@@ -32,7 +32,9 @@ EXPORTS = ("wf_status_string", "wf_last_error_string", "wf_default_k_per_level",
            "wf_step_host", "wf_step_static_scratch", "wf_step_cached_al",
            "wf_cache_init", "wf_cache_update", "wf_cache_scatter", "wf_decode_step_host",
            "wf_daubechies_lowpass", "wf_basis_workspace_bytes", "wf_dwt_lowpass_basis",
-           "wf_step_basis")
+           "wf_step_basis",
+           "wf_rope_inv_freq", "wf_paged_append", "wf_paged_attn_workspace_bytes",
+           "wf_paged_attn", "wf_prefill_attn")
 
 
 class WfError(RuntimeError):
@@ -59,6 +61,26 @@ class Dims(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class PageDims(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("table_pages", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class PrefillDims(ctypes.Structure):
+    _fields_ = [("rows_q", ctypes.c_int32), ("rows_k", ctypes.c_int32),
+                ("n_docs", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class AttnOpts(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("causal", ctypes.c_int32), ("prefix", ctypes.c_void_p),
+                ("slopes", ctypes.c_void_p)]
+
+
 _LIB = None
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -66,6 +88,9 @@ _i32p = ctypes.POINTER(ctypes.c_int32)
 _sz = ctypes.c_size_t
 _DIMSP = ctypes.POINTER(Dims)
 _f64p = ctypes.POINTER(ctypes.c_double)
+_i64 = ctypes.c_int64
+_PDIMSP = ctypes.POINTER(PageDims)
+_OPTSP = ctypes.POINTER(AttnOpts)
 
 _SIGS = {
     "wf_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -101,6 +126,15 @@ _SIGS = {
     "wf_dwt_lowpass_basis": (ctypes.c_int, [_DIMSP, _f64p, _i32, _vp, _vp, _vp]),
     "wf_step_basis": (ctypes.c_int, [_DIMSP, _f64p, _i32, _vp, _vp, _vp, _vp, _vp, _i32p, _vp,
                                      _vp, _vp, _vp, _sz, _vp]),
+    "wf_rope_inv_freq": (ctypes.c_int, [_i32, ctypes.c_double, _f64p]),
+    "wf_paged_append": (ctypes.c_int, [_PDIMSP, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
+                                       _vp, _vp, _f64p, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz,
+                                       _vp]),
+    "wf_paged_attn_workspace_bytes": (ctypes.c_int, [_PDIMSP, _i32, ctypes.POINTER(_sz)]),
+    "wf_paged_attn": (ctypes.c_int, [_PDIMSP, _OPTSP, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _vp, _sz, _vp]),
+    "wf_prefill_attn": (ctypes.c_int, [ctypes.POINTER(PrefillDims), _OPTSP, _vp, _i64, _vp, _i64,
+                                       _vp, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -491,6 +525,236 @@ def step_basis(q, kp, vp, kg, vg, levels: int, k_per_level: Sequence[int],
         _k_array(k_per_level), _ptr(out), _ptr(lse), _ptr(idx_out), _ptr(ws), ws.numel(),
         _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- paged cache, dense attention
+def rope_inv_freq(rotary_dim: int, base: float = 10000.0):
+    """Default rotation frequencies base^(-2i / rotary_dim) as the HOST array
+    (rotary_dim / 2 doubles) paged_append takes; any other sequence of
+    frequencies (radians per position) serves as well."""
+    out = (ctypes.c_double * max(rotary_dim // 2, 1))()
+    _check("wf_rope_inv_freq", lib().wf_rope_inv_freq(rotary_dim, base, out))
+    return out
+
+
+def alloc_paged_cache(n_pages: int, kv_heads: int, page_size: int, head_dim: int,
+                      dtype: torch.dtype, device) -> dict:
+    """Uninitialised pages {"K", "V"}: [n_pages, kv_heads, page_size, head_dim]."""
+    shape = (n_pages, kv_heads, page_size, head_dim)
+    return {n: torch.empty(shape, dtype=dtype, device=device) for n in ("K", "V")}
+
+
+class _Call:
+    """Device and stream of one call: every tensor must live on one device,
+    which becomes the current one for the call (streams and launches belong to
+    a device); outputs are allocated with the call's stream current, so the
+    allocator knows which stream uses them first."""
+
+    def __init__(self, first: torch.Tensor, stream):
+        self.device = first.device
+        if self.device.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"stream is on {stream.device}, tensors on {self.device}")
+        self.stream = torch.cuda.current_stream(self.device) if stream is None else stream
+        same = (torch.cuda.current_device() == self.device.index and
+                (stream is None or stream == torch.cuda.current_stream(self.device)))
+        self.ctx = None if same else torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return None if self.ctx is None else self.ctx.__exit__(*exc)
+
+    @property
+    def handle(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def need(self, t: torch.Tensor, name: str, shape, dtype) -> None:
+        """A contiguous tensor of this shape and type on the call's device."""
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, not {self.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+    def rows(self, t: torch.Tensor, name: str, heads: int, d: int, dtype) -> int:
+        """A [rows, heads, d] tensor whose rows may lie apart; its row stride."""
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, not {self.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+            raise ValueError(f"{name} must be [rows, {heads}, {d}], got {tuple(t.shape)}")
+        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+            raise ValueError(f"{name}: the heads of a row must be contiguous")
+        return t.stride(0) if t.shape[0] > 1 else heads * d
+
+    def out(self, t: Optional[torch.Tensor], name: str, shape, dtype) -> torch.Tensor:
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        self.need(t, name, shape, dtype)
+        return t
+
+
+def _page_dims(call: _Call, cache: dict, page_table: torch.Tensor, q_heads: int,
+               dtype) -> PageDims:
+    k = cache["K"]
+    if k.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("pages must be [n_pages, kv_heads, page_size, head_dim], "
+                         "the page table [n_seqs, table_pages]")
+    call.need(k, "cache K", k.shape, dtype)
+    call.need(cache["V"], "cache V", k.shape, dtype)
+    call.need(page_table, "page_table", page_table.shape, torch.int32)
+    return PageDims(page_table.shape[0], q_heads, k.shape[1], k.shape[3], k.shape[2], k.shape[0],
+                    page_table.shape[1], dtype_code(dtype))
+
+
+def _attn_opts(call: _Call, causal, prefix, softcap, slopes, scale, n_seqs: int,
+               q_heads: int) -> AttnOpts:
+    if prefix is not None:
+        call.need(prefix, "prefix", (n_seqs,), torch.int32)
+    if slopes is not None:
+        call.need(slopes, "slopes", (q_heads,), torch.float32)
+    if scale is not None and scale == 0.0:
+        raise ValueError("scale must not be 0 (None means 1/sqrt(head_dim))")
+    return AttnOpts(0.0 if scale is None else scale, softcap, int(causal), _ptr(prefix),
+                    _ptr(slopes))
+
+
+def _ws_args(call: _Call, ws: Optional[torch.Tensor]):
+    if ws is None:
+        return None, 0
+    call.need(ws, "workspace", (ws.numel(),), torch.uint8)
+    return _ptr(ws), ws.numel()
+
+
+def paged_append(k: torch.Tensor, v: torch.Tensor, cache: dict, page_table: torch.Tensor,
+                 cu_rows: torch.Tensor, cache_len: torch.Tensor,
+                 q: Optional[torch.Tensor] = None, inv_freq: Optional[Sequence[float]] = None,
+                 interleaved: bool = False, positions: Optional[torch.Tensor] = None,
+                 keep_keys: bool = False, out: Optional[dict] = None,
+                 ws: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """wf_paged_append: new rows k, v [T, kv_heads, d] (and queries q [T,
+    q_heads, d]), rows cu_rows[s] .. cu_rows[s+1] of sequence s at cache
+    positions cache_len[s].., keys and queries rotated by ``inv_freq``
+    (rope_inv_freq; None: no rotation), into cache {"K", "V"} in place.
+    Returns {"Q": rotated queries} if q is given and {"K": rotated keys} if
+    ``keep_keys``; ``out`` may supply those tensors."""
+    with _Call(k, stream) as call:
+        t, hkv, d = k.shape if k.dim() == 3 else (0, 0, 0)
+        ks = call.rows(k, "k", hkv, d, k.dtype)
+        vs = call.rows(v, "v", hkv, d, k.dtype)
+        hq = hkv if q is None else q.shape[1] if q.dim() == 3 else 0
+        qs = 0 if q is None else call.rows(q, "q", hq, d, k.dtype)
+        dims = _page_dims(call, cache, page_table, hq, k.dtype)
+        if v.shape[0] != t or (q is not None and q.shape[0] != t):
+            raise ValueError("q, k and v must have the same rows")
+        if dims.kv_heads != hkv or dims.head_dim != d:
+            raise ValueError("the cache's heads or head_dim differ from k's")
+        call.need(cu_rows, "cu_rows", (dims.n_seqs + 1,), torch.int32)
+        call.need(cache_len, "cache_len", (dims.n_seqs,), torch.int32)
+        if positions is not None:
+            call.need(positions, "positions", (t,), torch.int32)
+        freq, half = inv_freq, 0
+        if freq is not None:
+            half = len(freq)
+            if not isinstance(freq, ctypes.Array):
+                freq = (ctypes.c_double * half)(*[float(x) for x in freq])
+        res = dict(out or {})
+        if q is not None:
+            res["Q"] = call.out(res.get("Q"), "out Q", (t, hq, d), k.dtype)
+        if keep_keys:
+            res["K"] = call.out(res.get("K"), "out K", (t, hkv, d), k.dtype)
+        _check("wf_paged_append", lib().wf_paged_append(
+            ctypes.byref(dims), t, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(cu_rows),
+            _ptr(cache_len), _ptr(positions), _ptr(page_table), freq, 2 * half, int(interleaved),
+            _ptr(cache["K"]), _ptr(cache["V"]), _ptr(res["Q"]) if q is not None else None,
+            _ptr(res["K"]) if keep_keys else None, *_ws_args(call, ws), call.handle))
+        return res
+
+
+def alloc_paged_attn_workspace(q: torch.Tensor, cache: dict, page_table: torch.Tensor,
+                               stream=None) -> torch.Tensor:
+    """Workspace of paged_attn for these tensors' sizes (status word cleared);
+    calls that may overlap need one each."""
+    with _Call(q, stream) as call:
+        dims = _page_dims(call, cache, page_table, q.shape[2], q.dtype)
+        n = ctypes.c_size_t(0)
+        _check("wf_paged_attn_workspace_bytes", lib().wf_paged_attn_workspace_bytes(
+            ctypes.byref(dims), q.shape[1], ctypes.byref(n)))
+        ws = torch.empty(n.value, dtype=torch.uint8, device=q.device)
+        _check("wf_clear_device_status", lib().wf_clear_device_status(_ptr(ws), ws.numel(),
+                                                                      call.handle))
+        return ws
+
+
+def paged_attn(q: torch.Tensor, cache: dict, page_table: torch.Tensor, kv_len: torch.Tensor,
+               ws: Optional[torch.Tensor] = None, causal: bool = True,
+               prefix: Optional[torch.Tensor] = None, softcap: float = 0.0,
+               slopes: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+               out: Optional[torch.Tensor] = None, with_lse: bool = False, stream=None):
+    """wf_paged_attn: q [n_seqs, n_new, q_heads, d], the newest n_new rows of
+    each sequence's paged cache {"K", "V"} of kv_len [n_seqs] rows; returns O
+    like q (and lse [n_seqs, n_new, q_heads] fp32 if ``with_lse``).  ``ws``
+    defaults to a fresh workspace."""
+    with _Call(q, stream) as call:
+        if q.dim() != 4:
+            raise ValueError("q must be [n_seqs, n_new, q_heads, head_dim]")
+        s, n_new, hq, d = q.shape
+        dims = _page_dims(call, cache, page_table, hq, q.dtype)
+        call.need(q, "q", (dims.n_seqs, n_new, hq, dims.head_dim), q.dtype)
+        call.need(kv_len, "kv_len", (s,), torch.int32)
+        opts = _attn_opts(call, causal, prefix, softcap, slopes, scale, s, hq)
+        if ws is None:
+            ws = alloc_paged_attn_workspace(q, cache, page_table, call.stream)
+        o = call.out(out, "out", (s, n_new, hq, d), q.dtype)
+        lse = call.out(None, "lse", (s, n_new, hq), torch.float32) if with_lse else None
+        _check("wf_paged_attn", lib().wf_paged_attn(
+            ctypes.byref(dims), ctypes.byref(opts), n_new, _ptr(q), _ptr(cache["K"]),
+            _ptr(cache["V"]), _ptr(page_table), _ptr(kv_len), _ptr(o), _ptr(lse),
+            *_ws_args(call, ws), call.handle))
+        return (o, lse) if with_lse else o
+
+
+def prefill_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                 cu_k: Optional[torch.Tensor] = None, causal: bool = True,
+                 prefix: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                 slopes: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                 out: Optional[torch.Tensor] = None, with_lse: bool = False,
+                 ws: Optional[torch.Tensor] = None, stream=None):
+    """wf_prefill_attn: packed sequences q [T, q_heads, d] over k, v [T_k,
+    kv_heads, d], sequence s in rows cu_q[s] .. cu_q[s+1] and keys cu_k[s] ..
+    cu_k[s+1] (cu_k defaults to cu_q); returns O like q (and lse [T, q_heads]
+    fp32 if ``with_lse``).  Rows behind the last sequence are not written."""
+    with _Call(q, stream) as call:
+        if q.dim() != 3 or k.dim() != 3:
+            raise ValueError("q, k and v must be [rows, heads, head_dim]")
+        t, hq, d = q.shape
+        hkv = k.shape[1]
+        qs = call.rows(q, "q", hq, d, q.dtype)
+        ks = call.rows(k, "k", hkv, d, q.dtype)
+        vs = call.rows(v, "v", hkv, d, q.dtype)
+        if v.shape[0] != k.shape[0]:
+            raise ValueError("k and v must have the same rows")
+        docs = cu_q.numel() - 1
+        call.need(cu_q, "cu_q", (docs + 1,), torch.int32)
+        cu_k = cu_q if cu_k is None else cu_k
+        call.need(cu_k, "cu_k", (docs + 1,), torch.int32)
+        dims = PrefillDims(t, k.shape[0], docs, hq, hkv, d, dtype_code(q.dtype))
+        opts = _attn_opts(call, causal, prefix, softcap, slopes, scale, docs, hq)
+        o = call.out(out, "out", (t, hq, d), q.dtype)
+        lse = call.out(None, "lse", (t, hq), torch.float32) if with_lse else None
+        _check("wf_prefill_attn", lib().wf_prefill_attn(
+            ctypes.byref(dims), ctypes.byref(opts), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+            _ptr(cu_q), _ptr(cu_k), _ptr(o), _ptr(lse), *_ws_args(call, ws), call.handle))
+        return (o, lse) if with_lse else o
 
 
 def raw_call(name: str, *args) -> int:

@@ -1,0 +1,247 @@
+// New rows into a paged cache, with the position rotation on the way.
+//
+// Each new row t of sequence s (cu_rows[s] <= t < cu_rows[s + 1]) takes cache
+// position n = cache_len[s] + (t - cu_rows[s]): row n % page_size of page
+// table[s][n / page_size].  Pages are [n_pages, kv_heads, page_size, d], so
+// one head's rows of a page are contiguous.  Keys (and queries) are rotated,
+// pair i of the first rotary_dim channels by the angle p f_i.
+//
+// Angles.  The caller's f_i become turns per position, f_i / 2π, as 64-bit
+// binary fractions F_i.  p F_i mod 2^64 is then the angle's fraction of a
+// turn, exactly reduced for every p (error p 2^-65 turns), and its top bits
+// go to sincospi: no angle is ever formed whose rounding grows with p.
+//
+// HBM-bound: every byte is read once and written once.  One thread moves two
+// 16-byte chunks that rotate together ((c, c + r/2) of the halves form,
+// neighbours otherwise); a block takes 32 * ITERS consecutive (row, head)
+// lines of the flattened [rows][q heads, k heads, v heads] order, issues all
+// its loads first, resolves its rows' pages (one warp a row) and forms their
+// sines once for all heads while the loads fly.  Four lines a thread keep
+// 128 bytes in flight; below 4 blocks per SM, one line a thread, so that a
+// decoding step's few rows spread over more SMs.
+#include <algorithm>
+
+#include "wf_common.cuh"
+#include "wf_internal.h"
+
+namespace wf {
+
+namespace {
+
+struct AppendParams {
+  AppendArgs a;
+  RopeTurns turns;
+};
+
+// The sequence of row t: the last s < n_seqs with cu[s] <= t, or -1 when t
+// is at or behind cu[n_seqs] (or before cu[0]).  Whole warp, 32-way search.
+__device__ __forceinline__ int row_sequence(const int32_t* cu, int n_seqs, int t) {
+  const int lane = threadIdx.x & 31;
+  if (t < __ldg(cu) || t >= __ldg(cu + n_seqs)) return -1;
+  int lo = 0, n = n_seqs;  // cu[lo] <= t, the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = lane * step < n && __ldg(cu + at) <= t;
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
+    const int left = n - k * step;
+    lo += k * step;
+    n = min(step, left);
+  }
+  return lo;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float* f);
+template <>
+__device__ __forceinline__ uint4 pack16<__nv_bfloat16>(const float* f) {
+  uint4 v;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return v;
+}
+template <>
+__device__ __forceinline__ uint4 pack16<float>(const float* f) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                    __float_as_uint(f[3]));
+}
+
+struct TokenInfo {
+  int64_t line;  // first cache line index ((page * kv_heads) * page_size + row), -1: no write
+  int32_t pos;   // rotation position
+  int32_t live;  // row belongs to a sequence
+};
+
+template <typename T, int D, int ITERS>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int V = Elem<T>::kPer16B;     // elements per chunk
+  constexpr int C2 = D / (2 * V);         // chunk pairs per line
+  constexpr int LANES = kThreads / C2;    // lines per pass
+  constexpr int LINES = LANES * ITERS;    // lines per block
+  extern __shared__ float2 s_cs[];        // [tokens][rotary_dim / 2] cosine, sine
+  __shared__ TokenInfo s_tok[LINES + 1];
+  const AppendArgs& a = p.a;
+  const int qh = a.q != nullptr ? a.q_heads : 0;
+  const int per_row = qh + 2 * a.kv_heads;
+  const int64_t total = static_cast<int64_t>(a.rows) * per_row;
+  const int64_t line0 = static_cast<int64_t>(blockIdx.x) * LINES;
+  const int t0 = static_cast<int>(line0 / per_row);
+  const int64_t last = min(line0 + LINES, total) - 1;
+  const int n_tok = static_cast<int>(last / per_row) - t0 + 1;
+  const int c = threadIdx.x % C2;
+  const int rot_pairs = a.rotary_dim / (2 * V);  // rotated chunk pairs per line
+  // The two chunks of this thread: halves (c, c + r/2V), else neighbours.
+  const bool rotate = c < rot_pairs;
+  const bool halves = rotate && !a.interleaved;
+  const int ca = halves ? c : 2 * c;
+  const int cb = halves ? c + rot_pairs : 2 * c + 1;
+
+  uint4 xa[ITERS], xb[ITERS];
+#pragma unroll
+  for (int i = 0; i < ITERS; ++i) {
+    const int64_t line = line0 + i * LANES + threadIdx.x / C2;
+    if (line < total) {
+      const int64_t t = line / per_row;
+      const int h = static_cast<int>(line - t * per_row);
+      const T* src = h < qh ? static_cast<const T*>(a.q) + t * a.q_stride + h * D
+                     : h < qh + a.kv_heads
+                         ? static_cast<const T*>(a.k) + t * a.k_stride + (h - qh) * D
+                         : static_cast<const T*>(a.v) + t * a.v_stride + (h - qh - a.kv_heads) * D;
+      xa[i] = ldg16_stream(src + ca * V);
+      xb[i] = ldg16_stream(src + cb * V);
+    }
+  }
+
+  for (int i = threadIdx.x >> 5; i < n_tok; i += kWarps) {
+    const int t = t0 + i;
+    const int s = row_sequence(a.cu_rows, a.n_seqs, t);
+    if ((threadIdx.x & 31) == 0) {
+      TokenInfo info = {-1, 0, 0};
+      if (s >= 0) {
+        info.live = 1;
+        const int64_t n = static_cast<int64_t>(__ldg(a.cache_len + s)) + (t - __ldg(a.cu_rows + s));
+        info.pos = a.positions != nullptr ? __ldg(a.positions + t) : static_cast<int32_t>(n);
+        const int64_t slot = n / a.page_size;
+        int page = -1;
+        if (n >= 0 && slot < a.table_pages)
+          page = __ldg(a.table + static_cast<int64_t>(s) * a.table_pages + slot);
+        if (page >= 0 && page < a.n_pages)
+          info.line = static_cast<int64_t>(page) * a.kv_heads * a.page_size + (n % a.page_size);
+        else
+          raise_flag(a.status, WF_DEV_BAD_INDEX);
+      }
+      s_tok[i] = info;
+    }
+  }
+  __syncthreads();
+  const int half = a.rotary_dim / 2;
+  for (int e = threadIdx.x; e < n_tok * half; e += kThreads) {
+    const int i = e / half, j = e - i * half;
+    // The fraction of a turn, in [-1/2, 1/2), rounded once to fp32.
+    const int64_t frac =
+        static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(s_tok[i].pos)) * p.turns.f[j]);
+    float sn, cs;
+    sincospif(static_cast<float>(frac) * 0x1p-63f, &sn, &cs);
+    s_cs[e] = make_float2(cs, sn);
+  }
+  __syncthreads();
+
+#pragma unroll
+  for (int i = 0; i < ITERS; ++i) {
+    const int64_t line = line0 + i * LANES + threadIdx.x / C2;
+    if (line >= total) continue;
+    const int64_t t = line / per_row;
+    int h = static_cast<int>(line - t * per_row);
+    const TokenInfo info = s_tok[t - t0];
+    if (!info.live) continue;
+    uint4 ya = xa[i], yb = xb[i];
+    if (rotate && h < qh + a.kv_heads) {
+      float fa[V], fb[V];
+      widen16(ya, static_cast<const T*>(nullptr), fa);
+      widen16(yb, static_cast<const T*>(nullptr), fb);
+      const float2* cs = s_cs + (t - t0) * half + c * V;
+      if (halves) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float x = fa[e], y = fb[e];
+          fa[e] = x * cs[e].x - y * cs[e].y;
+          fb[e] = x * cs[e].y + y * cs[e].x;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float2 w0 = cs[e / 2], w1 = cs[V / 2 + e / 2];
+          const float x0 = fa[e], x1 = fb[e];
+          fa[e] = x0 * w0.x - fa[e + 1] * w0.y;
+          fa[e + 1] = x0 * w0.y + fa[e + 1] * w0.x;
+          fb[e] = x1 * w1.x - fb[e + 1] * w1.y;
+          fb[e + 1] = x1 * w1.y + fb[e + 1] * w1.x;
+        }
+      }
+      ya = pack16<T>(fa);
+      yb = pack16<T>(fb);
+    }
+    T* dst = nullptr;
+    if (h < qh) {
+      dst = static_cast<T*>(a.q_out) + (t * qh + h) * D;
+    } else {
+      h -= qh;
+      const bool is_k = h < a.kv_heads;
+      if (!is_k) h -= a.kv_heads;
+      if (is_k && a.k_out != nullptr) {
+        T* ko = static_cast<T*>(a.k_out) + (t * a.kv_heads + h) * D;
+        *reinterpret_cast<uint4*>(ko + ca * V) = ya;
+        *reinterpret_cast<uint4*>(ko + cb * V) = yb;
+      }
+      if (info.line < 0) continue;
+      dst = static_cast<T*>(is_k ? a.k_pages : a.v_pages) +
+            (info.line + static_cast<int64_t>(h) * a.page_size) * D;
+    }
+    *reinterpret_cast<uint4*>(dst + ca * V) = ya;
+    *reinterpret_cast<uint4*>(dst + cb * V) = yb;
+  }
+}
+
+template <typename T, int D, int ITERS>
+cudaError_t launch_iters(const AppendParams& p, cudaStream_t stream) {
+  constexpr int LINES = kThreads / (D / (2 * Elem<T>::kPer16B)) * ITERS;
+  const int per_row = (p.a.q != nullptr ? p.a.q_heads : 0) + 2 * p.a.kv_heads;
+  const int64_t total = static_cast<int64_t>(p.a.rows) * per_row;
+  const size_t tokens = (LINES - 1 + per_row - 1) / per_row + 1;
+  const size_t smem = tokens * (p.a.rotary_dim / 2) * sizeof(float2);
+  const cudaError_t e = ensure_max_smem<append_kernel<T, D, ITERS>>();
+  if (e != cudaSuccess) return e;
+  append_kernel<T, D, ITERS>
+      <<<static_cast<unsigned>((total + LINES - 1) / LINES), kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const AppendParams& p, cudaStream_t stream) {
+  constexpr int LANES = kThreads / (D / (2 * Elem<T>::kPer16B));
+  const int per_row = (p.a.q != nullptr ? p.a.q_heads : 0) + 2 * p.a.kv_heads;
+  const int64_t total = static_cast<int64_t>(p.a.rows) * per_row;
+  if (total >= static_cast<int64_t>(LANES) * 4 * 4 * device_sm_count())
+    return launch_iters<T, D, 4>(p, stream);
+  return launch_iters<T, D, 1>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendArgs& a, const RopeTurns& turns, cudaStream_t stream) {
+  AppendParams p;
+  p.a = a;
+  p.turns = turns;
+  if (a.dtype == WF_BF16) {
+    if (a.head_dim == 128) return launch_typed<__nv_bfloat16, 128>(p, stream);
+    return launch_typed<__nv_bfloat16, 64>(p, stream);
+  }
+  if (a.head_dim == 128) return launch_typed<float, 128>(p, stream);
+  return launch_typed<float, 64>(p, stream);
+}
+
+}  // namespace wf

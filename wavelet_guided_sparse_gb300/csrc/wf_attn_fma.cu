@@ -1,0 +1,488 @@
+// Dense attention on the FMA pipes: fp32 inputs over a paged cache and over
+// packed prompts (bf16 inputs run on the tensor cores, wf_paged_attn.cu and
+// wf_prefill.cu), and the join of the paged attention's partials.
+//
+// A row block is RT rows of one key-value head: row r = i g + h is query i of
+// the block's sequence at head h of the g query heads sharing the keys, so
+// shared keys are read once for all of them.  256 threads as 16 x 16: thread
+// (ty, tx) owns RT/16 rows and, of a 64-key tile, keys tx, tx + 16, ...; then
+// of the output columns float4s tx, tx + 16.  One pass over the keys with the
+// running maximum and sum; the weights pass through shared memory within a
+// half warp.  The paged form divides the tiles evenly over the grid (see
+// wf_attn.cuh); the packed form takes one row block a CTA.
+#include <algorithm>
+
+#include "wf_attn.cuh"
+
+namespace wf {
+
+namespace {
+
+constexpr int KT = kPagedTile;  // keys per tile
+
+template <int D, int RT>
+struct FmaSmem {
+  float q[RT][D + 4];
+  float k[KT][D + 4];
+  float v[KT][D + 4];
+  float p[RT][KT + 4];
+};
+
+// One row block's running state in registers.
+template <int D, int RT>
+struct FmaState {
+  static constexpr int RPT = RT / 16;
+  float m[RPT], l[RPT], o[RPT][D / 16];
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[r][c] = 0.f;
+    }
+  }
+};
+
+// What a row block needs to know of its rows and sequence.
+struct RowBlock {
+  int row0, rows;  // first row and row count within the unit
+  int g, n_q, len, prefix, head0;
+  __device__ __forceinline__ int pos(int r) const { return len - n_q + (row0 + r) / g; }
+  __device__ __forceinline__ int head(int r) const { return head0 + (row0 + r) % g; }
+};
+
+// One 64-key tile (keys key0 .. key0 + 63, staged in shared memory, rows past
+// `len` and bad pages zero with ok[j] false) into the running state.
+template <int D, int RT>
+__device__ __forceinline__ void fma_tile(FmaSmem<D, RT>& s, const bool* ok, const RowBlock& b,
+                                         const ScoreOpts& o, int key0, FmaState<D, RT>& st) {
+  constexpr int RPT = RT / 16;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float z[RPT][4];
+#pragma unroll
+  for (int r = 0; r < RPT; ++r)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[r][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < D; d += 4) {
+    float4 qv[RPT], kv[4];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) qv[r] = *reinterpret_cast<const float4*>(&s.q[ty * RPT + r][d]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&s.k[tx + 16 * j][d]);
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        z[r][j] = fmaf(qv[r].x, kv[j].x, z[r][j]);
+        z[r][j] = fmaf(qv[r].y, kv[j].y, z[r][j]);
+        z[r][j] = fmaf(qv[r].z, kv[j].z, z[r][j]);
+        z[r][j] = fmaf(qv[r].w, kv[j].w, z[r][j]);
+      }
+  }
+#pragma unroll
+  for (int r = 0; r < RPT; ++r) {
+    const int row = ty * RPT + r;
+    const int pos = b.pos(row);
+    const float slope = o.slopes != nullptr && row < b.rows ? __ldg(o.slopes + b.head(row)) : 0.f;
+    float mx = st.m[r];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int key = key0 + tx + 16 * j;
+      float x = z[r][j] * o.scale;
+      if (o.cap > 0.f) x = o.cap * tanhf(x);
+      x -= slope * kLog2e * fabsf(static_cast<float>(pos - key));
+      const bool seen = key < b.len && (ok == nullptr || ok[tx + 16 * j]) &&
+                        (!o.causal || key <= pos || key < b.prefix);
+      z[r][j] = seen ? x : -INFINITY;
+      mx = fmaxf(mx, z[r][j]);
+    }
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+    const float base = mx == -INFINITY ? 0.f : mx;
+    const float corr = fast_exp2(st.m[r] - base);  // m = -inf: 0
+    st.m[r] = mx;
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float e = fast_exp2(z[r][j] - base);
+      s.p[row][tx + 16 * j] = e;
+      sum += e;
+    }
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    st.l[r] = st.l[r] * corr + sum;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) st.o[r][c] *= corr;
+  }
+  __syncwarp();
+#pragma unroll 4
+  for (int j = 0; j < KT; ++j) {
+    float pv[RPT];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) pv[r] = s.p[ty * RPT + r][j];
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const float4 vv = *reinterpret_cast<const float4*>(&s.v[j][tx * 4 + 64 * c]);
+#pragma unroll
+      for (int r = 0; r < RPT; ++r) {
+        st.o[r][4 * c] = fmaf(pv[r], vv.x, st.o[r][4 * c]);
+        st.o[r][4 * c + 1] = fmaf(pv[r], vv.y, st.o[r][4 * c + 1]);
+        st.o[r][4 * c + 2] = fmaf(pv[r], vv.z, st.o[r][4 * c + 2]);
+        st.o[r][4 * c + 3] = fmaf(pv[r], vv.w, st.o[r][4 * c + 3]);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void store4(float* dst, const float* f) {
+  *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* dst, const float* f) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), c = __floats2bfloat162_rn(f[2], f[3]);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                              *reinterpret_cast<const uint32_t*>(&c));
+}
+
+// Finished rows: O and lse of the unit's rows at o/lse rows (i * hq + head).
+template <typename T, int D, int RT>
+__device__ __forceinline__ void fma_store(const FmaState<D, RT>& st, const RowBlock& b, T* o,
+                                          float* lse, int hq) {
+  constexpr int RPT = RT / 16;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int r = 0; r < RPT; ++r) {
+    const int row = ty * RPT + r;
+    if (row >= b.rows) continue;
+    const int64_t at = static_cast<int64_t>((b.row0 + row) / b.g) * hq + b.head(row);
+    const float inv = inv_or_zero(st.l[r]);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = st.o[r][4 * c + e] * inv;
+      store4(o + at * D + tx * 4 + 64 * c, f);
+    }
+    if (lse != nullptr && tx == 0)
+      lse[at] = row_lse(st.m[r], st.l[r]);
+  }
+}
+
+template <typename T, int D, int RT>
+__device__ __forceinline__ void fma_load_q(FmaSmem<D, RT>& s, const RowBlock& b, const T* q,
+                                           int64_t stride) {
+  constexpr int V = Elem<T>::kPer16B, C = D / V;
+  for (int e = threadIdx.x; e < RT * C; e += kThreads) {
+    const int r = e / C, c = e % C;
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = 0.f;
+    if (r < b.rows)
+      load16_f32(q + static_cast<int64_t>((b.row0 + r) / b.g) * stride + b.head(r) * D + c * V, f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) s.q[r][c * V + i] = f[i];
+  }
+}
+
+// Stages one key or value row chunk (zero when src is null).
+template <typename T, int D, int RT>
+__device__ __forceinline__ void fma_stage(FmaSmem<D, RT>& s, int j, int c, const T* k, const T* v) {
+  constexpr int V = Elem<T>::kPer16B;
+  float f[V], h[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = h[i] = 0.f;
+  if (k != nullptr) {
+    load16_f32(k + c * V, f);
+    load16_f32(v + c * V, h);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    s.k[j][c * V + i] = f[i];
+    s.v[j][c * V + i] = h[i];
+  }
+}
+
+struct PagedParams {
+  PagedArgs a;
+  WorkShape w;
+  ScoreOpts o;
+  int row_blocks;
+};
+
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(kThreads) paged_fma_kernel(PagedParams p) {
+  extern __shared__ float4 smem4[];
+  FmaSmem<D, RT>& s = *reinterpret_cast<FmaSmem<D, RT>*>(smem4);
+  int* pre = reinterpret_cast<int*>(&s + 1);
+  __shared__ int scratch[kWarps + 1];
+  __shared__ bool ok[KT];
+  const PagedArgs& a = p.a;
+  const int g = a.q_heads / a.kv_heads;
+  work_prefix(p.w, a.kv_len, pre, scratch);
+  const int64_t total = static_cast<int64_t>(pre[a.n_seqs]) * p.w.units_per_seq;
+  const int64_t w0 = work_bound(total, blockIdx.x, gridDim.x);
+  const int64_t w1 = work_bound(total, blockIdx.x + 1, gridDim.x);
+
+  // Idle sequences: zero rows, lse -inf.
+  for (int sq = blockIdx.x; sq < a.n_seqs; sq += gridDim.x) {
+    const int len = __ldg(a.kv_len + sq);
+    if (threadIdx.x == 0 && (len < 0 || len > p.w.max_len)) raise_flag(a.status, WF_DEV_BAD_INDEX);
+    if (len > 0) continue;
+    const int64_t n = static_cast<int64_t>(a.n_new) * a.q_heads;
+    for (int64_t e = threadIdx.x; e < n * D; e += kThreads)
+      static_cast<T*>(a.o)[sq * n * D + e] = static_cast<T>(0.f);
+    if (a.lse != nullptr)
+      for (int64_t e = threadIdx.x; e < n; e += kThreads) a.lse[sq * n + e] = -INFINITY;
+  }
+
+  FmaState<D, RT> st;
+  for (int64_t at = w0; at < w1;) {
+    const WorkUnit u = find_unit(p.w, pre, at);
+    const int64_t end = min(w1, u.begin + u.tiles);
+    RowBlock b;
+    b.g = g;
+    b.n_q = a.n_new;
+    b.len = seq_len_clamped(a.kv_len, u.seq, p.w.max_len);
+    b.prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + u.seq) : 0;
+    const int kvh = u.unit / p.row_blocks;
+    b.row0 = (u.unit % p.row_blocks) * RT;
+    b.rows = min(RT, g * a.n_new - b.row0);
+    b.head0 = kvh * g;
+    const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(u.seq) * a.n_new * a.q_heads * D;
+    __syncthreads();
+    fma_load_q<T, D, RT>(s, b, q, static_cast<int64_t>(a.q_heads) * D);
+    st.reset();
+    for (int64_t t = at; t < end; ++t) {
+      const int key0 = static_cast<int>(t - u.begin) * KT;
+      __syncthreads();
+      constexpr int C = D / Elem<T>::kPer16B;
+      for (int e = threadIdx.x; e < KT * C; e += kThreads) {
+        const int j = e / C, c = e % C, key = key0 + j;
+        const T *k = nullptr, *v = nullptr;
+        if (key < b.len) {
+          const int page = __ldg(a.table + static_cast<int64_t>(u.seq) * a.table_pages +
+                                 key / a.page_size);
+          if (page >= 0 && page < a.n_pages) {
+            const int64_t line = (static_cast<int64_t>(page) * a.kv_heads + kvh) * a.page_size +
+                                 key % a.page_size;
+            k = static_cast<const T*>(a.k_pages) + line * D;
+            v = static_cast<const T*>(a.v_pages) + line * D;
+          } else if (c == 0) {
+            raise_flag(a.status, WF_DEV_BAD_INDEX);
+          }
+        }
+        if (c == 0) ok[j] = k != nullptr;
+        fma_stage<T, D, RT>(s, j, c, k, v);
+      }
+      __syncthreads();
+      fma_tile<D, RT>(s, ok, b, p.o, key0, st);
+    }
+    if (at == u.begin && end == u.begin + u.tiles) {
+      const int64_t base = static_cast<int64_t>(u.seq) * a.n_new * a.q_heads;
+      fma_store<T, D, RT>(st, b, static_cast<T*>(a.o) + base * D,
+                          a.lse != nullptr ? a.lse + base : nullptr, a.q_heads);
+    } else {
+      // A partial: slot 2c when the unit began before this CTA, else 2c + 1.
+      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (at == u.begin ? 1 : 0);
+      float* dst = a.part + slot * RT * (D + 2);
+      const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+      for (int r = 0; r < RT / 16; ++r) {
+        const int row = ty * (RT / 16) + r;
+        if (row >= b.rows) continue;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) store4(dst + row * D + tx * 4 + 64 * c, &st.o[r][4 * c]);
+        if (tx == 0) {
+          dst[RT * D + 2 * row] = st.m[r];
+          dst[RT * D + 2 * row + 1] = st.l[r];
+        }
+      }
+    }
+    at = end;
+  }
+}
+
+// Join: CTA c merges the unit that starts inside its range and ends behind
+// it, from slot 2c + 1 and the slots 2(c + 1), ... of the CTAs that hold the
+// unit's other tiles, in that order.  gridDim.y CTAs share the rows.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedParams p, int ctas, int RT) {
+  extern __shared__ int pre[];
+  __shared__ int scratch[kWarps + 1];
+  const PagedArgs& a = p.a;
+  const int g = a.q_heads / a.kv_heads;
+  work_prefix(p.w, a.kv_len, pre, scratch);
+  const int64_t total = static_cast<int64_t>(pre[a.n_seqs]) * p.w.units_per_seq;
+  const int c0 = blockIdx.x;
+  const int64_t w0 = work_bound(total, c0, ctas), w1 = work_bound(total, c0 + 1, ctas);
+  if (w0 >= w1) return;
+  const WorkUnit u = find_unit(p.w, pre, w1 - 1);
+  const int64_t end = u.begin + u.tiles;
+  if (u.begin < w0 || end <= w1) return;
+  int c1 = c0 + 1;  // last CTA with a tile of the unit
+  while (work_bound(total, c1 + 1, ctas) < end) ++c1;
+  const int kvh = u.unit / p.row_blocks;
+  const int row0 = (u.unit % p.row_blocks) * RT;
+  const int rows = min(RT, g * a.n_new - row0);
+  const int64_t stride = static_cast<int64_t>(RT) * (D + 2);
+  constexpr int C = D / 4;
+  for (int e = blockIdx.y * kThreads + threadIdx.x; e < rows * C; e += gridDim.y * kThreads) {
+    const int row = e / C, c = e % C;
+    float m = -INFINITY;
+    for (int i = c0; i <= c1; ++i) {
+      const float* s = a.part + (2 * static_cast<int64_t>(i) + (i == c0 ? 1 : 0)) * stride;
+      m = fmaxf(m, s[RT * D + 2 * row]);
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, f[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = c0; i <= c1; ++i) {
+      const float* s = a.part + (2 * static_cast<int64_t>(i) + (i == c0 ? 1 : 0)) * stride;
+      const float w = fast_exp2(s[RT * D + 2 * row] - base);
+      const float4 x = *reinterpret_cast<const float4*>(s + row * D + c * 4);
+      l = fmaf(w, s[RT * D + 2 * row + 1], l);
+      f[0] = fmaf(w, x.x, f[0]);
+      f[1] = fmaf(w, x.y, f[1]);
+      f[2] = fmaf(w, x.z, f[2]);
+      f[3] = fmaf(w, x.w, f[3]);
+    }
+    const float inv = inv_or_zero(l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] *= inv;
+    const int64_t at = (static_cast<int64_t>(u.seq) * a.n_new + (row0 + row) / g) * a.q_heads +
+                       kvh * g + (row0 + row) % g;
+    store4(static_cast<T*>(a.o) + at * D + c * 4, f);
+    if (a.lse != nullptr && c == 0) a.lse[at] = row_lse(m, l);
+  }
+}
+
+struct PrefillParams {
+  PrefillArgs a;
+  ScoreOpts o;
+};
+
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(kThreads) prefill_fma_kernel(PrefillParams p) {
+  extern __shared__ float4 smem4[];
+  FmaSmem<D, RT>& s = *reinterpret_cast<FmaSmem<D, RT>*>(smem4);
+  const PrefillArgs& a = p.a;
+  const int g = a.q_heads / a.kv_heads;
+  const int kvh = blockIdx.y;
+  if (blockIdx.x == 0 && kvh == 0) {
+    check_offsets(a.cu_q, a.n_docs, a.rows_q, a.status);
+    check_offsets(a.cu_k, a.n_docs, a.rows_k, a.status);
+  }
+  DocBlock d;
+  if (!find_doc_block(a, static_cast<int64_t>(blockIdx.x), RT, g, &d)) return;
+  RowBlock b;
+  b.g = g;
+  b.n_q = d.n_q;
+  b.len = d.n_k;
+  b.prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + d.doc) : 0;
+  b.row0 = d.block * RT;
+  b.rows = min(RT, d.n_q * g - b.row0);
+  b.head0 = kvh * g;
+  fma_load_q<T, D, RT>(s, b, static_cast<const T*>(a.q) + d.q0 * a.q_stride, a.q_stride);
+  FmaState<D, RT> st;
+  st.reset();
+  const int end = visible_end(b.len, b.pos(b.rows - 1), p.o.causal, b.prefix);
+  const T* kb = static_cast<const T*>(a.k) + d.k0 * a.k_stride + kvh * D;
+  const T* vb = static_cast<const T*>(a.v) + d.k0 * a.v_stride + kvh * D;
+  for (int key0 = 0; key0 < end; key0 += KT) {
+    __syncthreads();
+    constexpr int C = D / Elem<T>::kPer16B;
+    for (int e = threadIdx.x; e < KT * C; e += kThreads) {
+      const int j = e / C, c = e % C, key = key0 + j;
+      const bool in = key < b.len;
+      fma_stage<T, D, RT>(s, j, c, in ? kb + key * a.k_stride : nullptr,
+                          in ? vb + key * a.v_stride : nullptr);
+    }
+    __syncthreads();
+    fma_tile<D, RT>(s, nullptr, b, p.o, key0, st);
+  }
+  const int64_t base = d.q0 * a.q_heads;
+  fma_store<T, D, RT>(st, b, static_cast<T*>(a.o) + base * D,
+                      a.lse != nullptr ? a.lse + base : nullptr, a.q_heads);
+}
+
+template <typename T, int D, int RT>
+cudaError_t launch_paged_rt(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream) {
+  const cudaError_t e = ensure_max_smem<paged_fma_kernel<T, D, RT>>();
+  if (e != cudaSuccess) return e;
+  const size_t smem = sizeof(FmaSmem<D, RT>) + sizeof(int) * (p.a.n_seqs + 1);
+  paged_fma_kernel<T, D, RT><<<plan.ctas, kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_paged_typed(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream) {
+  return plan.row_block == 16 ? launch_paged_rt<T, D, 16>(p, plan, stream)
+                              : launch_paged_rt<T, D, 64>(p, plan, stream);
+}
+
+PagedParams paged_params(const PagedArgs& a, const PagedPlan& plan, int tile) {
+  PagedParams p;
+  p.a = a;
+  p.row_blocks = (a.q_heads / a.kv_heads * a.n_new + plan.row_block - 1) / plan.row_block;
+  p.w.n_seqs = a.n_seqs;
+  p.w.units_per_seq = a.kv_heads * p.row_blocks;
+  p.w.tile = tile;
+  p.w.max_len = a.table_pages * a.page_size;
+  p.o = score_opts(a.scale, a.softcap, a.causal, a.prefix, a.slopes);
+  return p;
+}
+
+template <typename T, int D>
+cudaError_t launch_prefill_typed(const PrefillParams& p, cudaStream_t stream) {
+  constexpr int RT = 64;
+  const cudaError_t e = ensure_max_smem<prefill_fma_kernel<T, D, RT>>();
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = doc_blocks(p.a.rows_q, p.a.n_docs, RT, p.a.q_heads / p.a.kv_heads);
+  prefill_fma_kernel<T, D, RT>
+      <<<dim3(static_cast<unsigned>(blocks), p.a.kv_heads), kThreads, sizeof(FmaSmem<D, RT>),
+         stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_fma(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
+  const PagedParams p = paged_params(a, plan, KT);
+  if (a.dtype == WF_BF16)
+    return a.head_dim == 128 ? launch_paged_typed<__nv_bfloat16, 128>(p, plan, stream)
+                             : launch_paged_typed<__nv_bfloat16, 64>(p, plan, stream);
+  return a.head_dim == 128 ? launch_paged_typed<float, 128>(p, plan, stream)
+                           : launch_paged_typed<float, 64>(p, plan, stream);
+}
+
+cudaError_t launch_paged_join(const PagedArgs& a, const PagedPlan& plan, int tile,
+                              cudaStream_t stream) {
+  const PagedParams p = paged_params(a, plan, tile);
+  const size_t smem = sizeof(int) * (a.n_seqs + 1);
+  const int rows = std::min(plan.row_block, a.q_heads / a.kv_heads * a.n_new);
+  const dim3 grid(plan.ctas, (rows * a.head_dim / 4 + kThreads - 1) / kThreads);
+  if (a.dtype == WF_BF16) {
+    if (a.head_dim == 128)
+      paged_join_kernel<__nv_bfloat16, 128><<<grid, kThreads, smem, stream>>>(p, plan.ctas, plan.row_block);
+    else
+      paged_join_kernel<__nv_bfloat16, 64><<<grid, kThreads, smem, stream>>>(p, plan.ctas, plan.row_block);
+  } else if (a.head_dim == 128) {
+    paged_join_kernel<float, 128><<<grid, kThreads, smem, stream>>>(p, plan.ctas, plan.row_block);
+  } else {
+    paged_join_kernel<float, 64><<<grid, kThreads, smem, stream>>>(p, plan.ctas, plan.row_block);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prefill_fma(const PrefillArgs& a, cudaStream_t stream) {
+  PrefillParams p;
+  p.a = a;
+  p.o = score_opts(a.scale, a.softcap, a.causal, a.prefix, a.slopes);
+  if (a.dtype == WF_BF16)
+    return a.head_dim == 128 ? launch_prefill_typed<__nv_bfloat16, 128>(p, stream)
+                             : launch_prefill_typed<__nv_bfloat16, 64>(p, stream);
+  return a.head_dim == 128 ? launch_prefill_typed<float, 128>(p, stream)
+                           : launch_prefill_typed<float, 64>(p, stream);
+}
+
+}  // namespace wf

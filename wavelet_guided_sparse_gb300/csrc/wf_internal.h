@@ -162,6 +162,73 @@ int basis_cascade_len(int taps, int levels);
 cudaError_t launch_basis_coarse(const LaunchDims& ld, const BasisCoarseParams& p,
                                 cudaStream_t stream);
 
+// ---------------------------------------------------------------- dense attention
+// Paged cache and packed prompts (wf_append.cu, wf_paged_attn.cu,
+// wf_prefill.cu, wf_attn_fma.cu; entry points in wf_attn_api.cu).
+
+// Rotation frequencies in turns per position as 64-bit binary fractions
+// (kernel parameter; head_dim <= 128, so at most 64 pairs).
+struct RopeTurns {
+  uint64_t f[64];
+};
+
+struct AppendArgs {
+  const void *q, *k, *v;                  // [rows, heads, d], row strides below (elements)
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *cu_rows, *cache_len, *positions, *table;  // positions nullable
+  void *k_pages, *v_pages, *q_out, *k_out;                 // q_out / k_out nullable
+  int32_t* status;                        // nullable
+  int rows, n_seqs, q_heads, kv_heads, head_dim, page_size, n_pages, table_pages, dtype;
+  int rotary_dim, interleaved;
+};
+cudaError_t launch_append(const AppendArgs& a, const RopeTurns& turns, cudaStream_t stream);
+
+// Attention over a paged cache: n_new query rows per sequence.
+struct PagedArgs {
+  const void *q, *k_pages, *v_pages;
+  const int32_t *table, *kv_len;
+  void* o;
+  float* lse;                             // nullable
+  int32_t* status;
+  float* part;                            // partials (workspace)
+  int n_seqs, n_new, q_heads, kv_heads, head_dim, page_size, n_pages, table_pages, dtype;
+  float scale, softcap;
+  int causal;
+  const int32_t* prefix;
+  const float* slopes;
+};
+// CTAs of the persistent grid, rows of a row block and workspace bytes of
+// the partials: functions of the sizes and the device alone.
+struct PagedPlan {
+  int ctas, row_block;
+  size_t part_bytes;
+};
+PagedPlan plan_paged(const PagedArgs& a, int sm_count);
+cudaError_t launch_paged_attn(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
+cudaError_t launch_paged_fma(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
+cudaError_t launch_paged_join(const PagedArgs& a, const PagedPlan& plan, int tile,
+                              cudaStream_t stream);
+
+// Attention over packed sequences with contiguous keys and values.
+struct PrefillArgs {
+  const void *q, *k, *v;                  // [rows, heads, d], row strides below (elements)
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *cu_q, *cu_k;
+  void* o;
+  float* lse;                             // nullable
+  int32_t* status;                        // nullable
+  int rows_q, rows_k, n_docs, q_heads, kv_heads, head_dim, dtype;
+  float scale, softcap;
+  int causal;
+  const int32_t* prefix;
+  const float* slopes;
+};
+cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
+cudaError_t launch_prefill_fma(const PrefillArgs& a, cudaStream_t stream);
+
+// Keys per tile of the paged attention's work list.
+constexpr int kPagedTile = 64;
+
 // Dynamic shared memory the planners allow per CTA (the sm_103a opt-in limit
 // is 227 KB; a little is left for static shared memory).
 constexpr size_t kMaxSmem = 225 * 1024;
