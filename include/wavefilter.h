@@ -488,7 +488,7 @@ typedef struct {
  *   z <- z - slopes[h] |p - j| if slopes is given;
  * key j counts if not causal, or j <= p, or j < prefix[s].  A row without a
  * visible key gets O = 0 and lse = -inf.
- *   scale   : 0 means 1/sqrt(head_dim)
+ *   scale   : not negative; 0 means 1/sqrt(head_dim)
  *   softcap : 0 means none
  *   prefix  : nullable, [n_seqs] int32 (only read with causal)
  *   slopes  : nullable, [q_heads] fp32 */

@@ -62,7 +62,7 @@ bool bad_stride(int64_t stride, int heads, int head_dim, int dtype) {
 
 int check_opts(const wf_attn_opts* o) {
   if (o == nullptr) return WF_ERR_NULL;
-  if (!std::isfinite(o->scale) || !std::isfinite(o->softcap) || o->softcap < 0.f)
+  if (!std::isfinite(o->scale) || !std::isfinite(o->softcap) || o->scale < 0.f || o->softcap < 0.f)
     return WF_ERR_SHAPE;
   if (!aligned4(o->prefix) || !aligned4(o->slopes)) return WF_ERR_ALIGNMENT;
   return WF_OK;

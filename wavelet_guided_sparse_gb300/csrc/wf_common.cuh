@@ -17,7 +17,7 @@ namespace wf {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;  // every kernel of this library uses 256-thread CTAs
+constexpr int kThreads = 256;  // CTA size of the library's kernels unless they say otherwise
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 // Bounded waits: an mbarrier that has not completed after this many polls
