@@ -50,6 +50,35 @@ __device__ __forceinline__ int visible_end(int len, int last_pos, int causal, in
   return causal ? min(len, max(last_pos + 1, prefix)) : len;
 }
 
+inline ScoreOpts score_opts(float scale, float softcap, int causal, const int32_t* prefix,
+                            const float* slopes) {
+  ScoreOpts o;
+  o.cap = softcap > 0.f ? softcap * kLog2e : 0.f;
+  o.scale = softcap > 0.f ? scale / softcap : scale * kLog2e;
+  o.causal = causal;
+  o.prefix = prefix;
+  o.slopes = slopes;
+  return o;
+}
+
+__device__ __forceinline__ void store4(float* dst, const float* f) {
+  *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* dst, const float* f) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), c = __floats2bfloat162_rn(f[2], f[3]);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                              *reinterpret_cast<const uint32_t*>(&c));
+}
+
+// Programmatic dependent launch: the next kernel of the stream (launched with
+// that attribute) may start its prologue; it waits for this one's results.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_primary() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- paged work list
 // The key tiles of every unit (sequence, key-value head, row block) in one
 // line: sequence by sequence, unit by unit, tile by tile.  CTA c of C takes
@@ -72,22 +101,17 @@ __device__ __forceinline__ int seq_len_clamped(const int32_t* lens, int s, int m
   return min(max(__ldg(lens + s), 0), max_len);
 }
 
-// Exclusive prefix sums of the sequences' tile counts into pre[0..n_seqs]
-// (shared memory).  Whole block; contains __syncthreads.
-__device__ __forceinline__ void work_prefix(const WorkShape& w, const int32_t* lens, int* pre,
-                                            int* scratch) {
-  int base = 0;
-  for (int s0 = 0; s0 < w.n_seqs; s0 += kThreads) {
-    const int s = s0 + threadIdx.x;
-    const int t =
-        s < w.n_seqs ? (seq_len_clamped(lens, s, w.max_len) + w.tile - 1) / w.tile : 0;
-    int total;
-    const int e = block_excl_scan(t, scratch, &total);
-    if (s < w.n_seqs) pre[s] = base + e;
-    base += total;
-  }
-  if (threadIdx.x == 0) pre[w.n_seqs] = base;
-  __syncthreads();
+__device__ __forceinline__ int seq_tiles(const WorkShape& w, const int32_t* lens, int s) {
+  return (seq_len_clamped(lens, s, w.max_len) + w.tile - 1) / w.tile;
+}
+
+// Tiles of the whole call.  Whole warp.
+__device__ __forceinline__ int64_t work_total(const WorkShape& w, const int32_t* lens) {
+  int n = 0;  // fits: the host bounds n_seqs times the longest sequence's tiles
+  for (int s = threadIdx.x & 31; s < w.n_seqs; s += 32) n += seq_tiles(w, lens, s);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return static_cast<int64_t>(n) * w.units_per_seq;
 }
 
 // First tile of CTA c of n.  With fewer tiles than CTAs, one tile each for
@@ -96,28 +120,86 @@ __device__ __forceinline__ int64_t work_bound(int64_t total, int c, int n) {
   return total < n ? min(static_cast<int64_t>(c), total) : total * c / n;
 }
 
-// The unit that holds tile `at` (0 <= at < total): its sequence, its index
-// within the sequence, its first tile and its tile count.
+// A unit: its sequence, its index within the sequence, its tiles and the
+// first of them.
 struct WorkUnit {
   int seq, unit, tiles;
   int64_t begin;
 };
-__device__ __forceinline__ WorkUnit find_unit(const WorkShape& w, const int* pre, int64_t at) {
-  int lo = 0, hi = w.n_seqs;  // last s with pre[s] * units <= at
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (static_cast<int64_t>(pre[mid]) * w.units_per_seq <= at) lo = mid; else hi = mid;
+// The unit that holds tile `at` (0 <= at < total).  Whole warp, 32 sequences
+// a step.
+__device__ __forceinline__ WorkUnit find_unit(const WorkShape& w, const int32_t* lens,
+                                              int64_t at) {
+  const int lane = threadIdx.x & 31;
+  int base = 0;
+  WorkUnit u = {0, 0, 1, 0};
+  for (int s0 = 0; s0 < w.n_seqs; s0 += 32) {
+    const int t = s0 + lane < w.n_seqs ? seq_tiles(w, lens, s0 + lane) : 0;
+    const int incl = warp_incl_scan(t);
+    const unsigned hit = __ballot_sync(
+        0xffffffffu, static_cast<int64_t>(base + incl) * w.units_per_seq > at);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      const int64_t first = static_cast<int64_t>(base + __shfl_sync(0xffffffffu, incl - t, src)) *
+                            w.units_per_seq;
+      u.seq = s0 + src;
+      u.tiles = __shfl_sync(0xffffffffu, t, src);
+      u.unit = static_cast<int>((at - first) / u.tiles);
+      u.begin = first + static_cast<int64_t>(u.unit) * u.tiles;
+      return u;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  // Sequences without tiles share their start with the next one: the last
-  // with pre[s] * units <= at has tiles, because `at` is below its end.
-  WorkUnit u;
-  u.seq = lo;
-  u.tiles = pre[lo + 1] - pre[lo];
-  const int64_t off = at - static_cast<int64_t>(pre[lo]) * w.units_per_seq;
-  u.unit = static_cast<int>(off / u.tiles);
-  u.begin = static_cast<int64_t>(pre[lo]) * w.units_per_seq +
-            static_cast<int64_t>(u.unit) * u.tiles;
   return u;
+}
+// The unit after u (there is one: the caller stays below the total).
+__device__ __forceinline__ void next_unit(const WorkShape& w, const int32_t* lens, WorkUnit& u) {
+  u.begin += u.tiles;
+  if (++u.unit < w.units_per_seq) return;
+  u.unit = 0;
+  do {
+    ++u.seq;
+    u.tiles = u.seq < w.n_seqs ? seq_tiles(w, lens, u.seq) : 1;
+  } while (u.tiles == 0);
+}
+
+// Rows of a sequence without keys: O = 0, lse = -inf.  CTA c of n, threads
+// thread, thread + threads, ...; flags lengths outside the table.
+template <typename T>
+__device__ __forceinline__ void idle_sequences(const PagedArgs& a, int max_len, int c, int n,
+                                               int thread, int threads) {
+  for (int s = c; s < a.n_seqs; s += n) {
+    const int len = __ldg(a.kv_len + s);
+    if (thread == 0 && (len < 0 || len > max_len)) raise_flag(a.status, WF_DEV_BAD_INDEX);
+    if (len > 0) continue;
+    const int rows = a.n_new * a.q_heads;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) +
+                                        static_cast<int64_t>(s) * rows * a.head_dim);
+    const int chunks = rows * (a.head_dim / Elem<T>::kPer16B);
+    for (int e = thread; e < chunks; e += threads) o[e] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.lse != nullptr)
+      for (int e = thread; e < rows; e += threads)
+        a.lse[static_cast<int64_t>(s) * rows + e] = -INFINITY;
+  }
+}
+
+// Kernel parameters of the paged attention.
+struct PagedParams {
+  PagedArgs a;
+  WorkShape w;
+  ScoreOpts o;
+  int row_blocks;
+};
+inline PagedParams paged_params(const PagedArgs& a, const PagedPlan& plan) {
+  PagedParams p;
+  p.a = a;
+  p.row_blocks = (a.q_heads / a.kv_heads * a.n_new + plan.row_block - 1) / plan.row_block;
+  p.w.n_seqs = a.n_seqs;
+  p.w.units_per_seq = a.kv_heads * p.row_blocks;
+  p.w.tile = kPagedTile;
+  p.w.max_len = a.table_pages * a.page_size;
+  p.o = score_opts(a.scale, a.softcap, a.causal, a.prefix, a.slopes);
+  return p;
 }
 
 // ---------------------------------------------------------------- packed row blocks
@@ -173,17 +255,6 @@ __device__ __forceinline__ void check_offsets(const int32_t* cu, int n, int rows
     const int a = __ldg(cu + i), b = __ldg(cu + i + 1);
     if (a < 0 || b < a || b > rows) raise_flag(status, WF_DEV_BAD_INDEX);
   }
-}
-
-inline ScoreOpts score_opts(float scale, float softcap, int causal, const int32_t* prefix,
-                            const float* slopes) {
-  ScoreOpts o;
-  o.cap = softcap > 0.f ? softcap * kLog2e : 0.f;
-  o.scale = softcap > 0.f ? scale / softcap : scale * kLog2e;
-  o.causal = causal;
-  o.prefix = prefix;
-  o.slopes = slopes;
-  return o;
 }
 
 }  // namespace wf

@@ -1,6 +1,6 @@
 // Dense attention on the FMA pipes: fp32 inputs over a paged cache and over
 // packed prompts (bf16 inputs run on the tensor cores, wf_paged_attn.cu and
-// wf_prefill.cu), and the join of the paged attention's partials.
+// wf_prefill.cu).
 //
 // A row block is RT rows of one key-value head: row r = i g + h is query i of
 // the block's sequence at head h of the g query heads sharing the keys, so
@@ -136,15 +136,6 @@ __device__ __forceinline__ void fma_tile(FmaSmem<D, RT>& s, const bool* ok, cons
   }
 }
 
-__device__ __forceinline__ void store4(float* dst, const float* f) {
-  *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* dst, const float* f) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), c = __floats2bfloat162_rn(f[2], f[3]);
-  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                              *reinterpret_cast<const uint32_t*>(&c));
-}
-
 // Finished rows: O and lse of the unit's rows at o/lse rows (i * hq + head).
 template <typename T, int D, int RT>
 __device__ __forceinline__ void fma_store(const FmaState<D, RT>& st, const RowBlock& b, T* o,
@@ -203,42 +194,22 @@ __device__ __forceinline__ void fma_stage(FmaSmem<D, RT>& s, int j, int c, const
   }
 }
 
-struct PagedParams {
-  PagedArgs a;
-  WorkShape w;
-  ScoreOpts o;
-  int row_blocks;
-};
-
 template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kThreads) paged_fma_kernel(PagedParams p) {
   extern __shared__ float4 smem4[];
   FmaSmem<D, RT>& s = *reinterpret_cast<FmaSmem<D, RT>*>(smem4);
-  int* pre = reinterpret_cast<int*>(&s + 1);
-  __shared__ int scratch[kWarps + 1];
   __shared__ bool ok[KT];
   const PagedArgs& a = p.a;
   const int g = a.q_heads / a.kv_heads;
-  work_prefix(p.w, a.kv_len, pre, scratch);
-  const int64_t total = static_cast<int64_t>(pre[a.n_seqs]) * p.w.units_per_seq;
+  const int64_t total = work_total(p.w, a.kv_len);
   const int64_t w0 = work_bound(total, blockIdx.x, gridDim.x);
   const int64_t w1 = work_bound(total, blockIdx.x + 1, gridDim.x);
-
-  // Idle sequences: zero rows, lse -inf.
-  for (int sq = blockIdx.x; sq < a.n_seqs; sq += gridDim.x) {
-    const int len = __ldg(a.kv_len + sq);
-    if (threadIdx.x == 0 && (len < 0 || len > p.w.max_len)) raise_flag(a.status, WF_DEV_BAD_INDEX);
-    if (len > 0) continue;
-    const int64_t n = static_cast<int64_t>(a.n_new) * a.q_heads;
-    for (int64_t e = threadIdx.x; e < n * D; e += kThreads)
-      static_cast<T*>(a.o)[sq * n * D + e] = static_cast<T>(0.f);
-    if (a.lse != nullptr)
-      for (int64_t e = threadIdx.x; e < n; e += kThreads) a.lse[sq * n + e] = -INFINITY;
-  }
+  idle_sequences<T>(a, p.w.max_len, blockIdx.x, gridDim.x, threadIdx.x, kThreads);
+  launch_dependents();
 
   FmaState<D, RT> st;
-  for (int64_t at = w0; at < w1;) {
-    const WorkUnit u = find_unit(p.w, pre, at);
+  WorkUnit u = find_unit(p.w, a.kv_len, w0);
+  for (int64_t at = w0; at < w1; next_unit(p.w, a.kv_len, u)) {
     const int64_t end = min(w1, u.begin + u.tiles);
     RowBlock b;
     b.g = g;
@@ -303,59 +274,6 @@ __global__ void __launch_bounds__(kThreads) paged_fma_kernel(PagedParams p) {
   }
 }
 
-// Join: CTA c merges the unit that starts inside its range and ends behind
-// it, from slot 2c + 1 and the slots 2(c + 1), ... of the CTAs that hold the
-// unit's other tiles, in that order.  gridDim.y CTAs share the rows.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedParams p, int ctas, int RT) {
-  extern __shared__ int pre[];
-  __shared__ int scratch[kWarps + 1];
-  const PagedArgs& a = p.a;
-  const int g = a.q_heads / a.kv_heads;
-  work_prefix(p.w, a.kv_len, pre, scratch);
-  const int64_t total = static_cast<int64_t>(pre[a.n_seqs]) * p.w.units_per_seq;
-  const int c0 = blockIdx.x;
-  const int64_t w0 = work_bound(total, c0, ctas), w1 = work_bound(total, c0 + 1, ctas);
-  if (w0 >= w1) return;
-  const WorkUnit u = find_unit(p.w, pre, w1 - 1);
-  const int64_t end = u.begin + u.tiles;
-  if (u.begin < w0 || end <= w1) return;
-  int c1 = c0 + 1;  // last CTA with a tile of the unit
-  while (work_bound(total, c1 + 1, ctas) < end) ++c1;
-  const int kvh = u.unit / p.row_blocks;
-  const int row0 = (u.unit % p.row_blocks) * RT;
-  const int rows = min(RT, g * a.n_new - row0);
-  const int64_t stride = static_cast<int64_t>(RT) * (D + 2);
-  constexpr int C = D / 4;
-  for (int e = blockIdx.y * kThreads + threadIdx.x; e < rows * C; e += gridDim.y * kThreads) {
-    const int row = e / C, c = e % C;
-    float m = -INFINITY;
-    for (int i = c0; i <= c1; ++i) {
-      const float* s = a.part + (2 * static_cast<int64_t>(i) + (i == c0 ? 1 : 0)) * stride;
-      m = fmaxf(m, s[RT * D + 2 * row]);
-    }
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, f[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = c0; i <= c1; ++i) {
-      const float* s = a.part + (2 * static_cast<int64_t>(i) + (i == c0 ? 1 : 0)) * stride;
-      const float w = fast_exp2(s[RT * D + 2 * row] - base);
-      const float4 x = *reinterpret_cast<const float4*>(s + row * D + c * 4);
-      l = fmaf(w, s[RT * D + 2 * row + 1], l);
-      f[0] = fmaf(w, x.x, f[0]);
-      f[1] = fmaf(w, x.y, f[1]);
-      f[2] = fmaf(w, x.z, f[2]);
-      f[3] = fmaf(w, x.w, f[3]);
-    }
-    const float inv = inv_or_zero(l);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] *= inv;
-    const int64_t at = (static_cast<int64_t>(u.seq) * a.n_new + (row0 + row) / g) * a.q_heads +
-                       kvh * g + (row0 + row) % g;
-    store4(static_cast<T*>(a.o) + at * D + c * 4, f);
-    if (a.lse != nullptr && c == 0) a.lse[at] = row_lse(m, l);
-  }
-}
-
 struct PrefillParams {
   PrefillArgs a;
   ScoreOpts o;
@@ -409,7 +327,7 @@ template <typename T, int D, int RT>
 cudaError_t launch_paged_rt(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream) {
   const cudaError_t e = ensure_max_smem<paged_fma_kernel<T, D, RT>>();
   if (e != cudaSuccess) return e;
-  const size_t smem = sizeof(FmaSmem<D, RT>) + sizeof(int) * (p.a.n_seqs + 1);
+  const size_t smem = sizeof(FmaSmem<D, RT>);
   paged_fma_kernel<T, D, RT><<<plan.ctas, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
@@ -418,18 +336,6 @@ template <typename T, int D>
 cudaError_t launch_paged_typed(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream) {
   return plan.row_block == 16 ? launch_paged_rt<T, D, 16>(p, plan, stream)
                               : launch_paged_rt<T, D, 64>(p, plan, stream);
-}
-
-PagedParams paged_params(const PagedArgs& a, const PagedPlan& plan, int tile) {
-  PagedParams p;
-  p.a = a;
-  p.row_blocks = (a.q_heads / a.kv_heads * a.n_new + plan.row_block - 1) / plan.row_block;
-  p.w.n_seqs = a.n_seqs;
-  p.w.units_per_seq = a.kv_heads * p.row_blocks;
-  p.w.tile = tile;
-  p.w.max_len = a.table_pages * a.page_size;
-  p.o = score_opts(a.scale, a.softcap, a.causal, a.prefix, a.slopes);
-  return p;
 }
 
 template <typename T, int D>
@@ -447,40 +353,15 @@ cudaError_t launch_prefill_typed(const PrefillParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_paged_fma(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
-  const PagedParams p = paged_params(a, plan, KT);
-  if (a.dtype == WF_BF16)
-    return a.head_dim == 128 ? launch_paged_typed<__nv_bfloat16, 128>(p, plan, stream)
-                             : launch_paged_typed<__nv_bfloat16, 64>(p, plan, stream);
+  const PagedParams p = paged_params(a, plan);
   return a.head_dim == 128 ? launch_paged_typed<float, 128>(p, plan, stream)
                            : launch_paged_typed<float, 64>(p, plan, stream);
-}
-
-cudaError_t launch_paged_join(const PagedArgs& a, const PagedPlan& plan, int tile,
-                              cudaStream_t stream) {
-  const PagedParams p = paged_params(a, plan, tile);
-  const size_t smem = sizeof(int) * (a.n_seqs + 1);
-  const int rows = std::min(plan.row_block, a.q_heads / a.kv_heads * a.n_new);
-  const dim3 grid(plan.ctas, (rows * a.head_dim / 4 + kThreads - 1) / kThreads);
-  if (a.dtype == WF_BF16) {
-    if (a.head_dim == 128)
-      paged_join_kernel<__nv_bfloat16, 128><<<grid, kThreads, smem, stream>>>(p, plan.ctas, plan.row_block);
-    else
-      paged_join_kernel<__nv_bfloat16, 64><<<grid, kThreads, smem, stream>>>(p, plan.ctas, plan.row_block);
-  } else if (a.head_dim == 128) {
-    paged_join_kernel<float, 128><<<grid, kThreads, smem, stream>>>(p, plan.ctas, plan.row_block);
-  } else {
-    paged_join_kernel<float, 64><<<grid, kThreads, smem, stream>>>(p, plan.ctas, plan.row_block);
-  }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_prefill_fma(const PrefillArgs& a, cudaStream_t stream) {
   PrefillParams p;
   p.a = a;
   p.o = score_opts(a.scale, a.softcap, a.causal, a.prefix, a.slopes);
-  if (a.dtype == WF_BF16)
-    return a.head_dim == 128 ? launch_prefill_typed<__nv_bfloat16, 128>(p, stream)
-                             : launch_prefill_typed<__nv_bfloat16, 64>(p, stream);
   return a.head_dim == 128 ? launch_prefill_typed<float, 128>(p, stream)
                            : launch_prefill_typed<float, 64>(p, stream);
 }

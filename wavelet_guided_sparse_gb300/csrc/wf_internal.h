@@ -206,8 +206,6 @@ struct PagedPlan {
 PagedPlan plan_paged(const PagedArgs& a, int sm_count);
 cudaError_t launch_paged_attn(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
 cudaError_t launch_paged_fma(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
-cudaError_t launch_paged_join(const PagedArgs& a, const PagedPlan& plan, int tile,
-                              cudaStream_t stream);
 
 // Attention over packed sequences with contiguous keys and values.
 struct PrefillArgs {

@@ -1,27 +1,551 @@
-// Attention of new tokens over a paged key-value cache: plan and dispatch.
+// Attention of new tokens over a paged key-value cache (eq. (3) over the
+// whole cache): bf16 kernel, the join of split sequences, plan and dispatch.
+// fp32 inputs run on the FMA pipes (wf_attn_fma.cu) with the same work list
+// and join.
+//
+// HBM-bound: each key-value row is read once for all g n_new query rows that
+// share it (16 to 64 flop a byte at bf16), so everything serves the stream.
+// The 64-key tiles of all sequences and heads form one line that a
+// persistent grid divides evenly (wf_attn.cuh).  In each CTA one producer
+// warp keeps a ring of tiles full by tensor copies (whole pages, or 64-row
+// parts of them, 128-byte swizzle), reading the page table one tile ahead;
+// the consumer warps hold 16 query rows each and split a tile's keys:
+//   rows <= 16: 4 warps x 16 keys, two CTAs an SM (3 stages of 32 KB each);
+//   rows <= 32: 2 row tiles x 4 warps x 16 keys, one CTA, 6 stages;
+//   otherwise : 4 row tiles x 2 warps x 32 keys, one CTA, 5 stages.
+// The products are mma.sync m16n8k16 (bf16 in, fp32 accumulate): at 16 rows a
+// 128-row tcgen05 tile would be seven eighths empty, and the pipe is far
+// from the bound.  Every warp keeps its own running (max, sum, O) over its
+// keys, the maximum raised lazily as in wf_prefill.cu; the warps of a row
+// tile add up once per unit, in a fixed order.
+//
+// Rows behind a sequence's end (the tail of its last page, stale stages) and
+// rows of bad pages get weights of exactly 0 and their value rows are
+// cleared in shared memory before the product.
 #include <algorithm>
 
 #include "wf_attn.cuh"
+#include "wf_mma.cuh"
+#include "wf_tensormap.h"
+#include "wf_umma.cuh"
 
 namespace wf {
+
+namespace {
+
+constexpr int KT = kPagedTile;  // keys per tile
+
+// R: 16-row query tiles per CTA.
+template <int D, int R>
+struct PagedShape {
+  static constexpr int kConsumers = R == 1 ? 4 : 8;     // warps
+  static constexpr int kKeyGroups = kConsumers / R;
+  static constexpr int kKeys = KT / kKeyGroups;         // keys per warp and tile
+  static constexpr int kThreadCount = (kConsumers + 1) * 32;
+  static constexpr int kCtasPerSm = R == 1 ? 2 : 1;
+  static constexpr int kTileBytes = KT * D * 2;         // keys or values of a stage
+  static constexpr int kStages = (R == 1 ? 3 : R == 2 ? 6 : 5) * (D == 64 ? 2 : 1);
+  static constexpr int kPitch = D + 4;                  // floats per merge row
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * 2 * kTileBytes +
+                                  16 * R * kPitch * sizeof(float);
+};
+
+struct PagedTcParams {
+  CUtensorMap tk, tv;
+  PagedParams p;
+  int box_rows;
+};
+
+template <int STAGES>
+struct PagedBarriers {
+  uint64_t full[STAGES], empty[STAGES];
+  int valid[STAGES];  // one bit per box of a stage
+  int abort;
+};
+
+// A bounded wait that also ends when another warp has given up.
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, int* abort,
+                                          int32_t* status) {
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255) == 255 && *reinterpret_cast<volatile int*>(abort) != 0) return false;
+  }
+  raise_flag(status, WF_DEV_WAIT_TIMEOUT);
+  *reinterpret_cast<volatile int*>(abort) = 1;
+  return false;
+}
+
+template <int D, int R, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, R>::kCtasPerSm)
+    paged_tc_kernel(const __grid_constant__ PagedTcParams tp) {
+  using Shape = PagedShape<D, R>;
+  constexpr int kStages = Shape::kStages, kTileBytes = Shape::kTileBytes;
+  constexpr int kStageBytes = 2 * kTileBytes, RT = 16 * R;
+  constexpr int kConsumerThreads = Shape::kConsumers * 32;
+  constexpr int KB = D / 64;  // 64-column blocks of a row
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) PagedBarriers<kStages> bars;
+  __shared__ float s_ml[Shape::kKeyGroups][RT][2];
+  unsigned char* ring = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float* merge = reinterpret_cast<float*>(ring + kStages * kStageBytes);
+  const PagedParams& p = tp.p;
+  const PagedArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = a.q_heads / a.kv_heads;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], Shape::kConsumers);
+    }
+    bars.abort = 0;
+    fence_mbar_init();
+  }
+  const int64_t total = work_total(p.w, a.kv_len);
+  const int64_t w0 = work_bound(total, blockIdx.x, gridDim.x);
+  const int64_t w1 = work_bound(total, blockIdx.x + 1, gridDim.x);
+  WorkUnit u = find_unit(p.w, a.kv_len, w0);
+  __syncthreads();
+  launch_dependents();
+
+  if (warp == Shape::kConsumers) {
+    // ---- producer: lane = (box of the stage, keys or values, column block)
+    const int boxes = KT / tp.box_rows;
+    const int kb = lane % KB, which = (lane / KB) & 1, sub = lane / (2 * KB);
+    const bool active = sub < boxes;
+    const uint32_t box_bytes = static_cast<uint32_t>(tp.box_rows) * 128;
+    const CUtensorMap* map = which ? &tp.tv : &tp.tk;
+    if (lane == 0) {
+      prefetch_tensormap(&tp.tk);
+      prefetch_tensormap(&tp.tv);
+    }
+    // Page-table entry of this lane's box of a tile (-1: nothing to copy).
+    const auto page_of = [&](const WorkUnit& x, int64_t at) {
+      const int key = static_cast<int>(at - x.begin) * KT + sub * tp.box_rows;
+      if (!active || key >= seq_len_clamped(a.kv_len, x.seq, p.w.max_len)) return -1;
+      const int page =
+          __ldg(a.table + static_cast<int64_t>(x.seq) * a.table_pages + key / a.page_size);
+      if (page >= 0 && page < a.n_pages) return page;
+      raise_flag(a.status, WF_DEV_BAD_INDEX);
+      return -1;
+    };
+    int fill = 0;
+    bool ok = true;
+    int page = w0 < w1 ? page_of(u, w0) : -1;
+    for (int64_t at = w0; at < w1; ++at, ++fill) {
+      const int st = fill % kStages;
+      const int key = static_cast<int>(at - u.begin) * KT + sub * tp.box_rows;
+      const int kvh = u.unit / p.row_blocks;
+      // The next tile's entry, on its way while this one waits for its stage.
+      WorkUnit nu = u;
+      if (at + 1 == u.begin + u.tiles) next_unit(p.w, a.kv_len, nu);
+      const int next_page = at + 1 < w1 ? page_of(nu, at + 1) : -1;
+      if (fill >= kStages) {
+        ok = ring_wait(&bars.empty[st], (fill / kStages - 1) & 1, &bars.abort, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+      const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
+      const unsigned firsts = __ballot_sync(0xffffffffu, page >= 0 && which == 0 && kb == 0);
+      if (lane == 0) {
+        int valid = 0;
+        for (int i = 0; i < boxes; ++i) valid |= ((firsts >> (i * 2 * KB)) & 1) << i;
+        bars.valid[st] = valid;
+        mbar_arrive_expect_tx(&bars.full[st], __popc(live) * box_bytes);
+      }
+      __syncwarp();
+      if (page >= 0) {
+        const int y = (page * a.kv_heads + kvh) * a.page_size + (key & (a.page_size - 1));
+        tma_load_2d(ring + st * kStageBytes + which * kTileBytes + kb * (KT * 128) +
+                        sub * box_bytes,
+                    map, kb * 64, y, &bars.full[st]);
+      }
+      page = next_page;
+      u = nu;
+    }
+    if (!ok) {  // no copy may land after the CTA has gone
+      for (int f = max(0, fill - kStages); f < fill; ++f)
+        mbar_wait_bounded(&bars.full[f % kStages], (f / kStages) & 1, a.status);
+    }
+  } else {
+    // ---- consumers
+    const int rt = warp % R, kg = warp / R;      // row tile, key group
+    const int gid = lane >> 2, tig = lane & 3;
+    idle_sequences<__nv_bfloat16>(a, p.w.max_len, blockIdx.x, gridDim.x, threadIdx.x,
+                                  kConsumerThreads);
+    const float mul = CAP ? p.o.cap : p.o.scale;
+    // ldmatrix lane addresses within a tile: keys as B (rows = keys), values
+    // transposed (rows = keys).
+    const int krow = kg * Shape::kKeys + ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;
+    const int vrow = kg * Shape::kKeys + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
+    const uint32_t koff = static_cast<uint32_t>(krow) * 128, voff = static_cast<uint32_t>(vrow) * 128;
+    const int ksw = krow & 7, vsw = vrow & 7;
+    int fill = 0;
+    bool ok = true;
+    for (int64_t at = w0; at < w1; next_unit(p.w, a.kv_len, u)) {
+      const int64_t end = min(w1, u.begin + u.tiles);
+      const int len = seq_len_clamped(a.kv_len, u.seq, p.w.max_len);
+      const int prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + u.seq) : 0;
+      const int kvh = u.unit / p.row_blocks;
+      const int row0 = (u.unit % p.row_blocks) * RT;
+      const int rows = min(RT, g * a.n_new - row0);
+      const int64_t base = static_cast<int64_t>(u.seq) * a.n_new * a.q_heads + kvh * g;
+      // This lane's two query rows: position, key limit, slope, fragments.
+      int limit[2];
+      float posf[2], slope[2];
+      uint32_t qf[D / 16][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = row0 + rt * 16 + gid + 8 * h;
+        const bool live = r - row0 < rows;
+        const int i = live ? r / g : 0, hd = live ? r - i * g : 0;
+        const int pos = len - a.n_new + i;
+        limit[h] = p.o.causal ? min(len, max(pos + 1, prefix)) : len;
+        posf[h] = static_cast<float>(pos);
+        slope[h] = BIAS ? __ldg(p.o.slopes + kvh * g + hd) * kLog2e / mul : 0.f;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
+                                 (base + static_cast<int64_t>(i) * a.q_heads + hd) * D + 2 * tig;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            qf[ks][h + 2 * c] =
+                live ? __ldg(reinterpret_cast<const unsigned int*>(q + ks * 16 + 8 * c)) : 0u;
+      }
+      float o[D / 8][4];
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+      for (; at < end; ++at, ++fill) {
+        const int st = fill % kStages;
+        ok = ok && ring_wait(&bars.full[st], (fill / kStages) & 1, &bars.abort, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {  // given up: only the barriers below, in step with the other warps
+          at = end;
+          break;
+        }
+        const int key0 = static_cast<int>(at - u.begin) * KT + kg * Shape::kKeys;
+        const uint32_t kt = smem_u32(ring + st * kStageBytes), vt = kt + kTileBytes;
+        const int valid = *reinterpret_cast<volatile int*>(&bars.valid[st]);
+        const bool whole = valid == (1 << (KT / tp.box_rows)) - 1;
+        if (!whole || key0 + Shape::kKeys > len) {
+          // Clear the value rows whose weight is 0 by their place.
+          for (int e = lane; e < Shape::kKeys * (D / 8); e += 32) {
+            const int r = e / (D / 8), c = e % (D / 8);
+            const int tr = kg * Shape::kKeys + r;
+            if (key0 + r >= len || !((valid >> (tr / tp.box_rows)) & 1))
+              *reinterpret_cast<uint4*>(ring + st * kStageBytes + kTileBytes +
+                                        (c >> 3) * (KT * 128) + tr * 128 + (c & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        constexpr int NB = Shape::kKeys / 8;  // 8-key blocks
+        float s[NB][4];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+          for (int n = 0; n < NB; n += 2) {
+            uint32_t b[4];
+            const int ch = ks * 2 + kch;
+            ldsm_x4(kt + (ch >> 3) * (KT * 128) + koff + n * 1024 + (((ch & 7) ^ ksw) << 4), b);
+            mma_bf16(s[n], qf[ks], b);
+            mma_bf16(s[n + 1], qf[ks], b + 2);
+          }
+        }
+        if (CAP) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = tanh_exp2(s[n][e] * p.o.scale);
+        }
+        if (BIAS) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float key = static_cast<float>(key0 + n * 8 + 2 * tig + (e & 1));
+              s[n][e] = fmaf(-slope[e >> 1], fabsf(posf[e >> 1] - key), s[n][e]);
+            }
+        }
+        if (!whole || key0 + Shape::kKeys > min(limit[0], limit[1])) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = n * 8 + 2 * tig + (e & 1);
+              const bool there = (valid >> ((kg * Shape::kKeys + r) / tp.box_rows)) & 1;
+              s[n][e] = there && key0 + r < limit[e >> 1] ? s[n][e] : -INFINITY;
+            }
+        }
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          mx[0] = fmaxf(mx[0], fmaxf(s[n][0], s[n][1]));
+          mx[1] = fmaxf(mx[1], fmaxf(s[n][2], s[n][3]));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * mul;
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float mn = fmaxf(m[h], mx[h]);
+            const float f = mn == -INFINITY ? 1.f : fast_exp2(m[h] - mn);
+            m[h] = mn;
+            l[h] *= f;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              o[n][2 * h] *= f;
+              o[n][2 * h + 1] *= f;
+            }
+          }
+        }
+        const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
+        uint32_t pf[NB][2];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const float e0 = fast_exp2(fmaf(s[n][0], mul, -b0)), e1 = fast_exp2(fmaf(s[n][1], mul, -b0));
+          const float e2 = fast_exp2(fmaf(s[n][2], mul, -b1)), e3 = fast_exp2(fmaf(s[n][3], mul, -b1));
+          l[0] += e0 + e1;
+          l[1] += e2 + e3;
+          // Weights meet the values in bf16 (half a step, 2^-8 relative each).
+          pf[n][0] = pack_bf16(e0, e1);
+          pf[n][1] = pack_bf16(e2, e3);
+        }
+#pragma unroll
+        for (int kk = 0; kk < NB / 2; ++kk) {
+          const uint32_t af[4] = {pf[2 * kk][0], pf[2 * kk][1], pf[2 * kk + 1][0], pf[2 * kk + 1][1]};
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) {
+            uint32_t b[4];
+            const int ch = 2 * n + vch;
+            ldsm_x4_t(vt + (ch >> 3) * (KT * 128) + voff + kk * 2048 + (((ch & 7) ^ vsw) << 4), b);
+            mma_bf16(o[2 * n], af, b);
+            mma_bf16(o[2 * n + 1], af, b + 2);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.empty[st]);
+      }
+
+      // The warps of a row tile add up, in key-group order.
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        if (tig == 0) {
+          s_ml[kg][rt * 16 + gid + 8 * h][0] = m[h];
+          s_ml[kg][rt * 16 + gid + 8 * h][1] = l[h];
+        }
+      }
+      named_bar_sync(1, kConsumerThreads);
+      float f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = rt * 16 + gid + 8 * h;
+        float gm = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < Shape::kKeyGroups; ++k) gm = fmaxf(gm, s_ml[k][r][0]);
+        f[h] = gm == -INFINITY ? 0.f : fast_exp2(m[h] - gm);
+      }
+      for (int k = 0; k < Shape::kKeyGroups; ++k) {
+        if (k == kg) {
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float2* dst = reinterpret_cast<float2*>(
+                  merge + (rt * 16 + gid + 8 * h) * Shape::kPitch + n * 8 + 2 * tig);
+              float2 x = k == 0 ? make_float2(0.f, 0.f) : *dst;
+              x.x = fmaf(o[n][2 * h], f[h], x.x);
+              x.y = fmaf(o[n][2 * h + 1], f[h], x.y);
+              *dst = x;
+            }
+        }
+        named_bar_sync(1, kConsumerThreads);
+      }
+      const bool all = end == u.begin + u.tiles && end - u.tiles >= w0;
+      // A partial: slot 2c when the unit began before this CTA, else 2c + 1.
+      float* part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (u.begin >= w0 ? 1 : 0)) *
+                                 RT * (D + 2);
+      for (int e = threadIdx.x; e < rows * (D / 4); e += kConsumerThreads) {
+        const int r = e / (D / 4), c = e % (D / 4);
+        float gm = -INFINITY, gl = 0.f;
+#pragma unroll
+        for (int k = 0; k < Shape::kKeyGroups; ++k) gm = fmaxf(gm, s_ml[k][r][0]);
+        const float b = gm == -INFINITY ? 0.f : gm;
+#pragma unroll
+        for (int k = 0; k < Shape::kKeyGroups; ++k)
+          gl = fmaf(fast_exp2(s_ml[k][r][0] - b), s_ml[k][r][1], gl);
+        const float4 x = *reinterpret_cast<const float4*>(merge + r * Shape::kPitch + c * 4);
+        if (all) {
+          const float inv = inv_or_zero(gl);
+          const float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
+          const int i = (row0 + r) / g, hd = (row0 + r) - i * g;
+          const int64_t to = base + static_cast<int64_t>(i) * a.q_heads + hd;
+          store4(static_cast<__nv_bfloat16*>(a.o) + to * D + c * 4, y);
+          if (a.lse != nullptr && c == 0) a.lse[to] = row_lse(gm, gl);
+        } else {
+          *reinterpret_cast<float4*>(part + r * D + c * 4) = x;
+          if (c == 0) *reinterpret_cast<float2*>(part + RT * D + 2 * r) = make_float2(gm, gl);
+        }
+      }
+      named_bar_sync(1, kConsumerThreads);  // the merge buffer is free again
+    }
+  }
+}
+
+// Join: CTA c merges the unit that starts inside its range and ends behind
+// it, from slot 2c + 1 and the slots 2(c + 1), ... of the CTAs that hold the
+// unit's other tiles, in that order.  gridDim.y CTAs share the rows.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedParams p, int ctas, int RT) {
+  const PagedArgs& a = p.a;
+  const int g = a.q_heads / a.kv_heads;
+  const int64_t total = work_total(p.w, a.kv_len);
+  const int c0 = blockIdx.x;
+  const int64_t w0 = work_bound(total, c0, ctas), w1 = work_bound(total, c0 + 1, ctas);
+  if (w0 >= w1) return;
+  const WorkUnit u = find_unit(p.w, a.kv_len, w1 - 1);
+  const int64_t end = u.begin + u.tiles;
+  if (u.begin < w0 || end <= w1) return;
+  int c1 = c0 + 1;  // last CTA with a tile of the unit
+  while (work_bound(total, c1 + 1, ctas) < end) ++c1;
+  const int kvh = u.unit / p.row_blocks;
+  const int row0 = (u.unit % p.row_blocks) * RT;
+  const int rows = min(RT, g * a.n_new - row0);
+  const int64_t stride = static_cast<int64_t>(RT) * (D + 2);
+  wait_for_primary();
+  constexpr int C = D / 4;
+  for (int e = blockIdx.y * kThreads + threadIdx.x; e < rows * C; e += gridDim.y * kThreads) {
+    const int row = e / C, c = e % C;
+    const float* first = a.part + (2 * static_cast<int64_t>(c0) + 1) * stride;
+    const float* rest = a.part + 2 * static_cast<int64_t>(c0 + 1) * stride;
+    const float2* ml = reinterpret_cast<const float2*>(first + RT * D) + row;
+    float m = ml->x;
+    for (int i = 0; i < c1 - c0; ++i)
+      m = fmaxf(m, rest[2 * i * stride + RT * D + 2 * row]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float w = fast_exp2(ml->x - base);
+    float4 x = *reinterpret_cast<const float4*>(first + row * D + c * 4);
+    float l = w * ml->y, f[4] = {w * x.x, w * x.y, w * x.z, w * x.w};
+#pragma unroll 4
+    for (int i = 0; i < c1 - c0; ++i) {
+      const float* s = rest + 2 * i * stride;
+      const float2 y = *reinterpret_cast<const float2*>(s + RT * D + 2 * row);
+      w = fast_exp2(y.x - base);
+      x = *reinterpret_cast<const float4*>(s + row * D + c * 4);
+      l = fmaf(w, y.y, l);
+      f[0] = fmaf(w, x.x, f[0]);
+      f[1] = fmaf(w, x.y, f[1]);
+      f[2] = fmaf(w, x.z, f[2]);
+      f[3] = fmaf(w, x.w, f[3]);
+    }
+    const float inv = inv_or_zero(l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] *= inv;
+    const int64_t at = (static_cast<int64_t>(u.seq) * a.n_new + (row0 + row) / g) * a.q_heads +
+                       kvh * g + (row0 + row) % g;
+    store4(static_cast<T*>(a.o) + at * D + c * 4, f);
+    if (a.lse != nullptr && c == 0) a.lse[at] = row_lse(m, l);
+  }
+}
+
+template <int D, int R, bool CAP, bool BIAS>
+cudaError_t launch_tc(const PagedTcParams& p, const PagedPlan& plan, cudaStream_t stream) {
+  using Shape = PagedShape<D, R>;
+  const cudaError_t e = ensure_max_smem<paged_tc_kernel<D, R, CAP, BIAS>>();
+  if (e != cudaSuccess) return e;
+  paged_tc_kernel<D, R, CAP, BIAS><<<plan.ctas, Shape::kThreadCount, Shape::kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, int R>
+cudaError_t launch_tc_opts(const PagedTcParams& p, const PagedPlan& plan, cudaStream_t stream) {
+  const bool bias = p.p.o.slopes != nullptr;
+  if (p.p.o.cap > 0.f)
+    return bias ? launch_tc<D, R, true, true>(p, plan, stream)
+                : launch_tc<D, R, true, false>(p, plan, stream);
+  return bias ? launch_tc<D, R, false, true>(p, plan, stream)
+              : launch_tc<D, R, false, false>(p, plan, stream);
+}
+
+template <int D>
+cudaError_t launch_tc_rows(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
+  PagedTcParams p;
+  p.p = paged_params(a, plan);
+  p.box_rows = std::min(a.page_size, KT);
+  const cuuint64_t dims[2] = {D, static_cast<cuuint64_t>(a.n_pages) * a.kv_heads * a.page_size};
+  const cuuint64_t strides[1] = {D * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(p.box_rows)};
+  if (!encode_bf16_map(&p.tk, a.k_pages, 2, dims, strides, box) ||
+      !encode_bf16_map(&p.tv, a.v_pages, 2, dims, strides, box))
+    return cudaErrorInvalidValue;
+  if (plan.row_block == 16) return launch_tc_opts<D, 1>(p, plan, stream);
+  if (plan.row_block == 32) return launch_tc_opts<D, 2>(p, plan, stream);
+  return launch_tc_opts<D, 4>(p, plan, stream);
+}
+
+// The join starts while the split kernel still runs (programmatic dependent
+// launch) and waits for its partials in the kernel.
+template <typename T, int D>
+cudaError_t launch_join(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
+  const int rows = std::min(plan.row_block, a.q_heads / a.kv_heads * a.n_new);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(plan.ctas, (rows * D / 4 + kThreads - 1) / kThreads);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D>, paged_params(a, plan), plan.ctas,
+                            plan.row_block);
+}
+
+}  // namespace
 
 PagedPlan plan_paged(const PagedArgs& a, int sm_count) {
   PagedPlan p;
   const int rows = a.q_heads / a.kv_heads * a.n_new;
-  p.row_block = rows <= 16 ? 16 : 64;
+  if (a.dtype == WF_BF16)
+    p.row_block = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  else
+    p.row_block = rows <= 16 ? 16 : 64;
   const int64_t units = static_cast<int64_t>(a.n_seqs) * a.kv_heads *
                         ((rows + p.row_block - 1) / p.row_block);
   const int64_t tiles =
-      units * ((static_cast<int64_t>(a.table_pages) * a.page_size + kPagedTile - 1) / kPagedTile);
+      units * ((static_cast<int64_t>(a.table_pages) * a.page_size + KT - 1) / KT);
   p.ctas = static_cast<int>(std::min<int64_t>(sm_count * (p.row_block == 16 ? 2 : 1), tiles));
   p.part_bytes = static_cast<size_t>(p.ctas) * 2 * p.row_block * (a.head_dim + 2) * sizeof(float);
   return p;
 }
 
 cudaError_t launch_paged_attn(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
-  const cudaError_t e = launch_paged_fma(a, plan, stream);
+  if (a.dtype == WF_F32) {
+    const cudaError_t e = launch_paged_fma(a, plan, stream);
+    if (e != cudaSuccess) return e;
+    return a.head_dim == 128 ? launch_join<float, 128>(a, plan, stream)
+                             : launch_join<float, 64>(a, plan, stream);
+  }
+  const cudaError_t e = a.head_dim == 128 ? launch_tc_rows<128>(a, plan, stream)
+                                          : launch_tc_rows<64>(a, plan, stream);
   if (e != cudaSuccess) return e;
-  return launch_paged_join(a, plan, kPagedTile, stream);
+  return a.head_dim == 128 ? launch_join<__nv_bfloat16, 128>(a, plan, stream)
+                           : launch_join<__nv_bfloat16, 64>(a, plan, stream);
 }
 
 }  // namespace wf

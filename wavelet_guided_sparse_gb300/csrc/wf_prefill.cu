@@ -30,12 +30,10 @@
 // Rows behind the sequence's last key in a stage (another sequence's, or the
 // copy's zero fill) meet weights of exactly 0: the softmax group clears up to
 // 15 value rows there, and the product stops at the next multiple of 16.
-#include <cuda.h>
-
 #include <algorithm>
-#include <atomic>
 
 #include "wf_attn.cuh"
+#include "wf_tensormap.h"
 #include "wf_umma.cuh"
 
 namespace wf {
@@ -513,42 +511,16 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// cuTensorMapEncodeTiled from the driver, looked up once.
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled() {
-  static std::atomic<void*> cached{nullptr};
-  void* f = cached.load(std::memory_order_acquire);
-  if (f == nullptr) {
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || f == nullptr) {
-      (void)cudaGetLastError();
-      return nullptr;
-    }
-    cached.store(f, std::memory_order_release);
-  }
-  return reinterpret_cast<EncodeTiledFn>(f);
-}
-
 // [rows, heads, d] bf16 with a row stride, boxes of 64 columns x 1 head x 128
 // rows, 128-byte swizzle; rows outside read as zero.
 bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int heads, int d,
                  int64_t stride) {
-  const EncodeTiledFn enc = encode_tiled();
-  if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2,
                                  static_cast<cuuint64_t>(stride) * 2};
   const cuuint32_t box[3] = {64, 1, kTileRows};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_bf16_map(map, base, 3, dims, strides, box);
 }
 
 template <int D, bool CAP, bool BIAS>
