@@ -114,16 +114,34 @@ __device__ __forceinline__ int64_t work_total(const WorkShape& w, const int32_t*
   return static_cast<int64_t>(n) * w.units_per_seq;
 }
 
-// First tile of CTA c of n.  With fewer tiles than CTAs, one tile each for
-// the first ones: no CTA between two that share a unit is ever idle.
-__device__ __forceinline__ int64_t work_bound(int64_t total, int c, int n) {
-  return total < n ? min(static_cast<int64_t>(c), total) : total * c / n;
-}
+// First tiles of the CTAs' ranges: CTA c of n starts at c q + c r / n with
+// total = q n + r.  With fewer tiles than CTAs, one tile each for the first
+// ones: no CTA between two that share a unit is ever idle.
+struct WorkSplit {
+  int64_t total, q;
+  uint32_t r, n;
+  __device__ __forceinline__ WorkSplit(int64_t total_, int n_)
+      : total(total_), n(static_cast<uint32_t>(n_)) {
+    if (total < n) {
+      q = 1;
+      r = 0;
+    } else if (total >> 32 == 0) {  // 32-bit division where it does
+      q = static_cast<uint32_t>(total) / n;
+      r = static_cast<uint32_t>(total) - static_cast<uint32_t>(q) * n;
+    } else {
+      q = total / n;
+      r = static_cast<uint32_t>(total - q * n);
+    }
+  }
+  __device__ __forceinline__ int64_t begin(int c) const {
+    return min(total, c * q + static_cast<uint32_t>(c) * r / n);
+  }
+};
 
-// A unit: its sequence, its index within the sequence, its tiles and the
-// first of them.
+// A unit: its sequence and length, its index within the sequence, its tiles
+// and the first of them.
 struct WorkUnit {
-  int seq, unit, tiles;
+  int seq, len, unit, tiles;
   int64_t begin;
 };
 // The unit that holds tile `at` (0 <= at < total).  Whole warp, 32 sequences
@@ -132,9 +150,10 @@ __device__ __forceinline__ WorkUnit find_unit(const WorkShape& w, const int32_t*
                                               int64_t at) {
   const int lane = threadIdx.x & 31;
   int base = 0;
-  WorkUnit u = {0, 0, 1, 0};
+  WorkUnit u = {0, 0, 0, 1, 0};
   for (int s0 = 0; s0 < w.n_seqs; s0 += 32) {
-    const int t = s0 + lane < w.n_seqs ? seq_tiles(w, lens, s0 + lane) : 0;
+    const int len = s0 + lane < w.n_seqs ? seq_len_clamped(lens, s0 + lane, w.max_len) : 0;
+    const int t = (len + w.tile - 1) / w.tile;
     const int incl = warp_incl_scan(t);
     const unsigned hit = __ballot_sync(
         0xffffffffu, static_cast<int64_t>(base + incl) * w.units_per_seq > at);
@@ -143,8 +162,12 @@ __device__ __forceinline__ WorkUnit find_unit(const WorkShape& w, const int32_t*
       const int64_t first = static_cast<int64_t>(base + __shfl_sync(0xffffffffu, incl - t, src)) *
                             w.units_per_seq;
       u.seq = s0 + src;
+      u.len = __shfl_sync(0xffffffffu, len, src);
       u.tiles = __shfl_sync(0xffffffffu, t, src);
-      u.unit = static_cast<int>((at - first) / u.tiles);
+      const int64_t off = at - first;  // below units_per_seq tiles
+      u.unit = off >> 32 == 0
+                   ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(u.tiles))
+                   : static_cast<int>(off / u.tiles);
       u.begin = first + static_cast<int64_t>(u.unit) * u.tiles;
       return u;
     }
@@ -159,8 +182,9 @@ __device__ __forceinline__ void next_unit(const WorkShape& w, const int32_t* len
   u.unit = 0;
   do {
     ++u.seq;
-    u.tiles = u.seq < w.n_seqs ? seq_tiles(w, lens, u.seq) : 1;
-  } while (u.tiles == 0);
+    u.len = u.seq < w.n_seqs ? seq_len_clamped(lens, u.seq, w.max_len) : 1;
+  } while (u.len == 0);
+  u.tiles = (u.len + w.tile - 1) / w.tile;
 }
 
 // Rows of a sequence without keys: O = 0, lse = -inf.  CTA c of n, threads

@@ -201,9 +201,8 @@ __global__ void __launch_bounds__(kThreads) paged_fma_kernel(PagedParams p) {
   __shared__ bool ok[KT];
   const PagedArgs& a = p.a;
   const int g = a.q_heads / a.kv_heads;
-  const int64_t total = work_total(p.w, a.kv_len);
-  const int64_t w0 = work_bound(total, blockIdx.x, gridDim.x);
-  const int64_t w1 = work_bound(total, blockIdx.x + 1, gridDim.x);
+  const WorkSplit split(work_total(p.w, a.kv_len), gridDim.x);
+  const int64_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
   idle_sequences<T>(a, p.w.max_len, blockIdx.x, gridDim.x, threadIdx.x, kThreads);
   launch_dependents();
 
@@ -214,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) paged_fma_kernel(PagedParams p) {
     RowBlock b;
     b.g = g;
     b.n_q = a.n_new;
-    b.len = seq_len_clamped(a.kv_len, u.seq, p.w.max_len);
+    b.len = u.len;
     b.prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + u.seq) : 0;
     const int kvh = u.unit / p.row_blocks;
     b.row0 = (u.unit % p.row_blocks) * RT;

@@ -102,9 +102,8 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
     bars.abort = 0;
     fence_mbar_init();
   }
-  const int64_t total = work_total(p.w, a.kv_len);
-  const int64_t w0 = work_bound(total, blockIdx.x, gridDim.x);
-  const int64_t w1 = work_bound(total, blockIdx.x + 1, gridDim.x);
+  const WorkSplit split(work_total(p.w, a.kv_len), gridDim.x);
+  const int64_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
   WorkUnit u = find_unit(p.w, a.kv_len, w0);
   __syncthreads();
   launch_dependents();
@@ -123,7 +122,7 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
     // Page-table entry of this lane's box of a tile (-1: nothing to copy).
     const auto page_of = [&](const WorkUnit& x, int64_t at) {
       const int key = static_cast<int>(at - x.begin) * KT + sub * tp.box_rows;
-      if (!active || key >= seq_len_clamped(a.kv_len, x.seq, p.w.max_len)) return -1;
+      if (!active || key >= x.len) return -1;
       const int page =
           __ldg(a.table + static_cast<int64_t>(x.seq) * a.table_pages + key / a.page_size);
       if (page >= 0 && page < a.n_pages) return page;
@@ -137,10 +136,6 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
       const int st = fill % kStages;
       const int key = static_cast<int>(at - u.begin) * KT + sub * tp.box_rows;
       const int kvh = u.unit / p.row_blocks;
-      // The next tile's entry, on its way while this one waits for its stage.
-      WorkUnit nu = u;
-      if (at + 1 == u.begin + u.tiles) next_unit(p.w, a.kv_len, nu);
-      const int next_page = at + 1 < w1 ? page_of(nu, at + 1) : -1;
       if (fill >= kStages) {
         ok = ring_wait(&bars.empty[st], (fill / kStages - 1) & 1, &bars.abort, a.status);
         ok = __all_sync(0xffffffffu, ok);
@@ -161,8 +156,9 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
                         sub * box_bytes,
                     map, kb * 64, y, &bars.full[st]);
       }
-      page = next_page;
-      u = nu;
+      // The next tile's entry, on its way before its stage is waited for.
+      if (at + 1 == u.begin + u.tiles) next_unit(p.w, a.kv_len, u);
+      page = at + 1 < w1 ? page_of(u, at + 1) : -1;
     }
     if (!ok) {  // no copy may land after the CTA has gone
       for (int f = max(0, fill - kStages); f < fill; ++f)
@@ -185,7 +181,7 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
     bool ok = true;
     for (int64_t at = w0; at < w1; next_unit(p.w, a.kv_len, u)) {
       const int64_t end = min(w1, u.begin + u.tiles);
-      const int len = seq_len_clamped(a.kv_len, u.seq, p.w.max_len);
+      const int len = u.len;
       const int prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + u.seq) : 0;
       const int kvh = u.unit / p.row_blocks;
       const int row0 = (u.unit % p.row_blocks) * RT;
@@ -407,60 +403,66 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
   }
 }
 
-// Join: CTA c merges the unit that starts inside its range and ends behind
-// it, from slot 2c + 1 and the slots 2(c + 1), ... of the CTAs that hold the
-// unit's other tiles, in that order.  gridDim.y CTAs share the rows.
+// Join: CTA (c, y) merges row y of the unit that starts inside CTA c's range
+// and ends behind it, from slot 2c + 1 and the slots 2(c + 1), ... of the
+// CTAs that hold the unit's other tiles.  Latency-bound (a row is some tens
+// of partials of d floats): the lanes read all maxima at once, then each of
+// the eight warps adds up every eighth partial, in order, and the warps add
+// up in theirs.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedParams p, int ctas, int RT) {
+  __shared__ float s_o[kWarps][D];
+  __shared__ float s_l[kWarps];
   const PagedArgs& a = p.a;
   const int g = a.q_heads / a.kv_heads;
-  const int64_t total = work_total(p.w, a.kv_len);
-  const int c0 = blockIdx.x;
-  const int64_t w0 = work_bound(total, c0, ctas), w1 = work_bound(total, c0 + 1, ctas);
+  const WorkSplit split(work_total(p.w, a.kv_len), ctas);
+  const int c0 = blockIdx.x, row = blockIdx.y;
+  const int64_t w0 = split.begin(c0), w1 = split.begin(c0 + 1);
   if (w0 >= w1) return;
   const WorkUnit u = find_unit(p.w, a.kv_len, w1 - 1);
   const int64_t end = u.begin + u.tiles;
-  if (u.begin < w0 || end <= w1) return;
-  int c1 = c0 + 1;  // last CTA with a tile of the unit
-  while (work_bound(total, c1 + 1, ctas) < end) ++c1;
-  const int kvh = u.unit / p.row_blocks;
   const int row0 = (u.unit % p.row_blocks) * RT;
-  const int rows = min(RT, g * a.n_new - row0);
+  if (u.begin < w0 || end <= w1 || row0 + row >= g * a.n_new) return;
+  int n = 2;  // CTAs with tiles of the unit
+  while (split.begin(c0 + n) < end) ++n;
   const int64_t stride = static_cast<int64_t>(RT) * (D + 2);
+  const float* first = a.part + (2 * static_cast<int64_t>(c0) + 1) * stride;
+  const auto slot = [&](int i) { return first + (i == 0 ? 0 : (2 * i - 1) * stride); };
   wait_for_primary();
-  constexpr int C = D / 4;
-  for (int e = blockIdx.y * kThreads + threadIdx.x; e < rows * C; e += gridDim.y * kThreads) {
-    const int row = e / C, c = e % C;
-    const float* first = a.part + (2 * static_cast<int64_t>(c0) + 1) * stride;
-    const float* rest = a.part + 2 * static_cast<int64_t>(c0 + 1) * stride;
-    const float2* ml = reinterpret_cast<const float2*>(first + RT * D) + row;
-    float m = ml->x;
-    for (int i = 0; i < c1 - c0; ++i)
-      m = fmaxf(m, rest[2 * i * stride + RT * D + 2 * row]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float w = fast_exp2(ml->x - base);
-    float4 x = *reinterpret_cast<const float4*>(first + row * D + c * 4);
-    float l = w * ml->y, f[4] = {w * x.x, w * x.y, w * x.z, w * x.w};
-#pragma unroll 4
-    for (int i = 0; i < c1 - c0; ++i) {
-      const float* s = rest + 2 * i * stride;
-      const float2 y = *reinterpret_cast<const float2*>(s + RT * D + 2 * row);
-      w = fast_exp2(y.x - base);
-      x = *reinterpret_cast<const float4*>(s + row * D + c * 4);
-      l = fmaf(w, y.y, l);
-      f[0] = fmaf(w, x.x, f[0]);
-      f[1] = fmaf(w, x.y, f[1]);
-      f[2] = fmaf(w, x.z, f[2]);
-      f[3] = fmaf(w, x.w, f[3]);
-    }
-    const float inv = inv_or_zero(l);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int V = D / 32;  // columns per lane
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, slot(i)[RT * D + 2 * row]);
+  m = warp_max(m);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f, f[V];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] *= inv;
-    const int64_t at = (static_cast<int64_t>(u.seq) * a.n_new + (row0 + row) / g) * a.q_heads +
-                       kvh * g + (row0 + row) % g;
-    store4(static_cast<T*>(a.o) + at * D + c * 4, f);
-    if (a.lse != nullptr && c == 0) a.lse[at] = row_lse(m, l);
+  for (int v = 0; v < V; ++v) f[v] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += kWarps) {
+    const float* s = slot(i);
+    const float2 y = *reinterpret_cast<const float2*>(s + RT * D + 2 * row);
+    const float w = fast_exp2(y.x - base);
+    l = fmaf(w, y.y, l);
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = fmaf(w, s[row * D + lane + 32 * v], f[v]);
   }
+#pragma unroll
+  for (int v = 0; v < V; ++v) s_o[warp][lane + 32 * v] = f[v];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float sum = 0.f, x = 0.f;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    sum += s_l[i];
+    x += s_o[i][threadIdx.x];
+  }
+  const int kvh = u.unit / p.row_blocks;
+  const int64_t at = (static_cast<int64_t>(u.seq) * a.n_new + (row0 + row) / g) * a.q_heads +
+                     kvh * g + (row0 + row) % g;
+  static_cast<T*>(a.o)[at * D + threadIdx.x] = static_cast<T>(x * inv_or_zero(sum));
+  if (a.lse != nullptr && threadIdx.x == 0) a.lse[at] = row_lse(m, sum);
 }
 
 template <int D, int R, bool CAP, bool BIAS>
@@ -504,7 +506,7 @@ template <typename T, int D>
 cudaError_t launch_join(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
   const int rows = std::min(plan.row_block, a.q_heads / a.kv_heads * a.n_new);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(plan.ctas, (rows * D / 4 + kThreads - 1) / kThreads);
+  cfg.gridDim = dim3(plan.ctas, rows);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
