@@ -136,6 +136,15 @@ struct WorkSplit {
   __device__ __forceinline__ int64_t begin(int c) const {
     return min(total, c * q + static_cast<uint32_t>(c) * r / n);
   }
+  // The CTA whose range holds tile t: the largest c with begin(c) <= t, that
+  // is floor(c total / n) <= t, c < (t + 1) n / total.
+  __device__ __forceinline__ int owner(int64_t t) const {
+    if (total < n) return static_cast<int>(t);
+    const uint64_t x = static_cast<uint64_t>(t + 1) * n + static_cast<uint64_t>(total) - 1;
+    return static_cast<int>(x >> 32 == 0
+                                ? static_cast<uint32_t>(x) / static_cast<uint32_t>(total)
+                                : x / static_cast<uint64_t>(total)) - 1;
+  }
 };
 
 // A unit: its sequence and length, its index within the sequence, its tiles

@@ -46,19 +46,20 @@ struct PagedShape {
   static constexpr int kTileBytes = KT * D * 2;         // keys or values of a stage
   static constexpr int kStages = (R == 1 ? 3 : R == 2 ? 6 : 5) * (D == 64 ? 2 : 1);
   static constexpr int kPitch = D + 4;                  // floats per merge row
+  static constexpr int kQueryBytes = 16 * R * D * 2;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * 2 * kTileBytes +
-                                  16 * R * kPitch * sizeof(float);
+                                  16 * R * kPitch * sizeof(float) + kQueryBytes;
 };
 
 struct PagedTcParams {
   CUtensorMap tk, tv;
   PagedParams p;
-  int box_rows;
+  int box_rows, page_shift;
 };
 
 template <int STAGES>
 struct PagedBarriers {
-  uint64_t full[STAGES], empty[STAGES];
+  uint64_t full[STAGES], empty[STAGES], q_empty;
   int valid[STAGES];  // one bit per box of a stage
   int abort;
 };
@@ -89,6 +90,7 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
   unsigned char* ring = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* merge = reinterpret_cast<float*>(ring + kStages * kStageBytes);
+  __nv_bfloat16* s_q = reinterpret_cast<__nv_bfloat16*>(merge + RT * Shape::kPitch);
   const PagedParams& p = tp.p;
   const PagedArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -99,6 +101,7 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
       mbar_init(&bars.full[i], 1);
       mbar_init(&bars.empty[i], Shape::kConsumers);
     }
+    mbar_init(&bars.q_empty, Shape::kConsumers);
     bars.abort = 0;
     fence_mbar_init();
   }
@@ -119,20 +122,30 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
       prefetch_tensormap(&tp.tk);
       prefetch_tensormap(&tp.tv);
     }
-    // Page-table entry of this lane's box of a tile (-1: nothing to copy).
-    const auto page_of = [&](const WorkUnit& x, int64_t at) {
+    // Page-table entry of this lane's box of a tile (-1: nothing to copy),
+    // only looked at when its copy is issued: the load flies meanwhile.
+    const auto entry_of = [&](const WorkUnit& x, int64_t at) {
       const int key = static_cast<int>(at - x.begin) * KT + sub * tp.box_rows;
       if (!active || key >= x.len) return -1;
-      const int page =
-          __ldg(a.table + static_cast<int64_t>(x.seq) * a.table_pages + key / a.page_size);
-      if (page >= 0 && page < a.n_pages) return page;
-      raise_flag(a.status, WF_DEV_BAD_INDEX);
-      return -1;
+      return __ldg(a.table + static_cast<int64_t>(x.seq) * a.table_pages + (key >> tp.page_shift));
     };
-    int fill = 0;
+    const auto wanted = [&](const WorkUnit& x, int64_t at) {
+      return active && static_cast<int>(at - x.begin) * KT + sub * tp.box_rows < x.len;
+    };
+    int fill = 0, units = 0;
     bool ok = true;
-    int page = w0 < w1 ? page_of(u, w0) : -1;
+    int page = w0 < w1 ? entry_of(u, w0) : -1;
     for (int64_t at = w0; at < w1; ++at, ++fill) {
+      // A unit's query rows arrive with its first tile: the runs of rows that
+      // one query's heads (or a part of them) form, one bulk copy each.
+      const bool first = at == w0 || at == u.begin;
+      const int row0 = (u.unit % p.row_blocks) * RT;
+      const int rows = min(RT, g * a.n_new - row0);
+      if (first && units++ > 0) {
+        ok = ring_wait(&bars.q_empty, (units - 2) & 1, &bars.abort, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
       const int st = fill % kStages;
       const int key = static_cast<int>(at - u.begin) * KT + sub * tp.box_rows;
       const int kvh = u.unit / p.row_blocks;
@@ -141,24 +154,38 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
+      if (page < 0 || page >= a.n_pages) {
+        if (wanted(u, at)) raise_flag(a.status, WF_DEV_BAD_INDEX);
+        page = -1;
+      }
       const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
       const unsigned firsts = __ballot_sync(0xffffffffu, page >= 0 && which == 0 && kb == 0);
       if (lane == 0) {
         int valid = 0;
         for (int i = 0; i < boxes; ++i) valid |= ((firsts >> (i * 2 * KB)) & 1) << i;
         bars.valid[st] = valid;
-        mbar_arrive_expect_tx(&bars.full[st], __popc(live) * box_bytes);
+        mbar_arrive_expect_tx(&bars.full[st],
+                              __popc(live) * box_bytes + (first ? rows * D * 2 : 0));
       }
       __syncwarp();
+      if (first) {
+        const int i0 = row0 / g, i1 = (row0 + rows - 1) / g;
+        for (int i = i0 + lane; i <= i1; i += 32) {
+          const int r0 = max(i * g, row0), r1 = min((i + 1) * g, row0 + rows);
+          const int64_t from = (static_cast<int64_t>(u.seq) * a.n_new + i) * a.q_heads + kvh * g +
+                               (r0 - i * g);
+          bulk_g2s(s_q + (r0 - row0) * D, static_cast<const __nv_bfloat16*>(a.q) + from * D,
+                   (r1 - r0) * D * 2, &bars.full[st]);
+        }
+      }
       if (page >= 0) {
         const int y = (page * a.kv_heads + kvh) * a.page_size + (key & (a.page_size - 1));
         tma_load_2d(ring + st * kStageBytes + which * kTileBytes + kb * (KT * 128) +
                         sub * box_bytes,
                     map, kb * 64, y, &bars.full[st]);
       }
-      // The next tile's entry, on its way before its stage is waited for.
       if (at + 1 == u.begin + u.tiles) next_unit(p.w, a.kv_len, u);
-      page = at + 1 < w1 ? page_of(u, at + 1) : -1;
+      page = at + 1 < w1 ? entry_of(u, at + 1) : -1;
     }
     if (!ok) {  // no copy may land after the CTA has gone
       for (int f = max(0, fill - kStages); f < fill; ++f)
@@ -187,10 +214,9 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
       const int row0 = (u.unit % p.row_blocks) * RT;
       const int rows = min(RT, g * a.n_new - row0);
       const int64_t base = static_cast<int64_t>(u.seq) * a.n_new * a.q_heads + kvh * g;
-      // This lane's two query rows: position, key limit, slope, fragments.
+      // This lane's two query rows: position, key limit, slope.
       int limit[2];
       float posf[2], slope[2];
-      uint32_t qf[D / 16][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = row0 + rt * 16 + gid + 8 * h;
@@ -200,15 +226,22 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
         limit[h] = p.o.causal ? min(len, max(pos + 1, prefix)) : len;
         posf[h] = static_cast<float>(pos);
         slope[h] = BIAS ? __ldg(p.o.slopes + kvh * g + hd) * kLog2e / mul : 0.f;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                                 (base + static_cast<int64_t>(i) * a.q_heads + hd) * D + 2 * tig;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            qf[ks][h + 2 * c] =
-                live ? __ldg(reinterpret_cast<const unsigned int*>(q + ks * 16 + 8 * c)) : 0u;
       }
+      // The unit's query rows arrive with its first tile.
+      ok = ok && ring_wait(&bars.full[fill % kStages], (fill / kStages) & 1, &bars.abort, a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      uint32_t qf[D / 16][4];
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int r = rt * 16 + gid + 8 * (c & 1);
+          qf[ks][c] = r < rows ? *reinterpret_cast<const uint32_t*>(s_q + r * D + ks * 16 +
+                                                                    8 * (c >> 1) + 2 * tig)
+                               : 0u;
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q_empty);
       float o[D / 8][4];
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
@@ -336,28 +369,49 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
         if (lane == 0) mbar_arrive(&bars.empty[st]);
       }
 
-      // The warps of a row tile add up, in key-group order.
+      // The warps of a row tile add up, in key-group order: every warp leaves
+      // its O (relative to its own maximum) in a slot of the merge buffer,
+      // all slots at once where the unit's rows leave room, else one group
+      // after the other.
+      const bool at_once = rows * Shape::kKeyGroups <= RT;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        if (tig == 0) {
+      }
+      named_bar_sync(1, kConsumerThreads);  // the last unit's output has left the buffer
+      if (tig == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           s_ml[kg][rt * 16 + gid + 8 * h][0] = m[h];
           s_ml[kg][rt * 16 + gid + 8 * h][1] = l[h];
         }
       }
-      named_bar_sync(1, kConsumerThreads);
-      float f[2];
+      if (at_once) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = rt * 16 + gid + 8 * h;
-        float gm = -INFINITY;
+        for (int h = 0; h < 2; ++h) {
+          const int r = rt * 16 + gid + 8 * h;
+          if (r < rows) {
 #pragma unroll
-        for (int k = 0; k < Shape::kKeyGroups; ++k) gm = fmaxf(gm, s_ml[k][r][0]);
-        f[h] = gm == -INFINITY ? 0.f : fast_exp2(m[h] - gm);
-      }
-      for (int k = 0; k < Shape::kKeyGroups; ++k) {
-        if (k == kg) {
+            for (int n = 0; n < D / 8; ++n)
+              *reinterpret_cast<float2*>(merge + (kg * rows + r) * Shape::kPitch + n * 8 + 2 * tig) =
+                  make_float2(o[n][2 * h], o[n][2 * h + 1]);
+          }
+        }
+      } else {
+        named_bar_sync(1, kConsumerThreads);
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = rt * 16 + gid + 8 * h;
+          float gm = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < Shape::kKeyGroups; ++k) gm = fmaxf(gm, s_ml[k][r][0]);
+          f[h] = gm == -INFINITY ? 0.f : fast_exp2(m[h] - gm);
+        }
+        for (int k = 0; k < Shape::kKeyGroups; ++k) {
+          if (k > 0) named_bar_sync(1, kConsumerThreads);
+          if (k != kg) continue;
 #pragma unroll
           for (int n = 0; n < D / 8; ++n)
 #pragma unroll
@@ -370,8 +424,8 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
               *dst = x;
             }
         }
-        named_bar_sync(1, kConsumerThreads);
       }
+      named_bar_sync(1, kConsumerThreads);
       const bool all = end == u.begin + u.tiles && end - u.tiles >= w0;
       // A partial: slot 2c when the unit began before this CTA, else 2c + 1.
       float* part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (u.begin >= w0 ? 1 : 0)) *
@@ -382,10 +436,21 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
 #pragma unroll
         for (int k = 0; k < Shape::kKeyGroups; ++k) gm = fmaxf(gm, s_ml[k][r][0]);
         const float b = gm == -INFINITY ? 0.f : gm;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < Shape::kKeyGroups; ++k)
-          gl = fmaf(fast_exp2(s_ml[k][r][0] - b), s_ml[k][r][1], gl);
-        const float4 x = *reinterpret_cast<const float4*>(merge + r * Shape::kPitch + c * 4);
+        for (int k = 0; k < Shape::kKeyGroups; ++k) {
+          const float w = fast_exp2(s_ml[k][r][0] - b);
+          gl = fmaf(w, s_ml[k][r][1], gl);
+          if (at_once) {
+            const float4 y = *reinterpret_cast<const float4*>(
+                merge + (k * rows + r) * Shape::kPitch + c * 4);
+            x.x = fmaf(w, y.x, x.x);
+            x.y = fmaf(w, y.y, x.y);
+            x.z = fmaf(w, y.z, x.z);
+            x.w = fmaf(w, y.w, x.w);
+          }
+        }
+        if (!at_once) x = *reinterpret_cast<const float4*>(merge + r * Shape::kPitch + c * 4);
         if (all) {
           const float inv = inv_or_zero(gl);
           const float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
@@ -398,71 +463,98 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
           if (c == 0) *reinterpret_cast<float2*>(part + RT * D + 2 * r) = make_float2(gm, gl);
         }
       }
-      named_bar_sync(1, kConsumerThreads);  // the merge buffer is free again
     }
   }
 }
 
-// Join: CTA (c, y) merges row y of the unit that starts inside CTA c's range
-// and ends behind it, from slot 2c + 1 and the slots 2(c + 1), ... of the
-// CTAs that hold the unit's other tiles.  Latency-bound (a row is some tens
-// of partials of d floats): the lanes read all maxima at once, then each of
-// the eight warps adds up every eighth partial, in order, and the warps add
-// up in theirs.
+// Join: the CTAs (c, .) merge the rows of the unit that starts inside CTA c's
+// range and ends behind it, from slot 2c + 1 and the slots 2(c + 1), ... of
+// the CTAs that hold the unit's other tiles.  Latency-bound (a row is two to
+// some tens of partials of d floats): as many of the eight warps share a row
+// as leave each about four partials, whose loads fly together; the lanes read
+// all maxima at once, and the warps of a row add up in their order.  Its
+// registers are bounded so that its CTAs fit beside the split kernel's and
+// have found their unit when that kernel ends.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedParams p, int ctas, int RT) {
-  __shared__ float s_o[kWarps][D];
-  __shared__ float s_l[kWarps];
+__global__ void __launch_bounds__(kThreads, 6)
+    paged_join_kernel(PagedParams p, int ctas, int RT) {
+  __shared__ float4 s_o[kWarps][D / 4];
+  __shared__ float s_l[kWarps], s_m[kWarps];
   const PagedArgs& a = p.a;
   const int g = a.q_heads / a.kv_heads;
   const WorkSplit split(work_total(p.w, a.kv_len), ctas);
-  const int c0 = blockIdx.x, row = blockIdx.y;
+  const int c0 = blockIdx.x;
   const int64_t w0 = split.begin(c0), w1 = split.begin(c0 + 1);
   if (w0 >= w1) return;
   const WorkUnit u = find_unit(p.w, a.kv_len, w1 - 1);
   const int64_t end = u.begin + u.tiles;
+  if (u.begin < w0 || end <= w1) return;
+  const int n = split.owner(end - 1) - c0 + 1;  // CTAs with tiles of the unit
+  const int share = n <= 4 ? 1 : n <= 8 ? 2 : n <= 16 ? 4 : 8;  // warps per row
+  const int at_once = kWarps / share;                           // rows per pass
   const int row0 = (u.unit % p.row_blocks) * RT;
-  if (u.begin < w0 || end <= w1 || row0 + row >= g * a.n_new) return;
-  int n = 2;  // CTAs with tiles of the unit
-  while (split.begin(c0 + n) < end) ++n;
+  const int rows = min(RT, g * a.n_new - row0);
   const int64_t stride = static_cast<int64_t>(RT) * (D + 2);
   const float* first = a.part + (2 * static_cast<int64_t>(c0) + 1) * stride;
   const auto slot = [&](int i) { return first + (i == 0 ? 0 : (2 * i - 1) * stride); };
-  wait_for_primary();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int V = D / 32;  // columns per lane
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, slot(i)[RT * D + 2 * row]);
-  m = warp_max(m);
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f, f[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) f[v] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += kWarps) {
-    const float* s = slot(i);
-    const float2 y = *reinterpret_cast<const float2*>(s + RT * D + 2 * row);
-    const float w = fast_exp2(y.x - base);
-    l = fmaf(w, y.y, l);
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = fmaf(w, s[row * D + lane + 32 * v], f[v]);
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) s_o[warp][lane + 32 * v] = f[v];
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  float sum = 0.f, x = 0.f;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    sum += s_l[i];
-    x += s_o[i][threadIdx.x];
-  }
   const int kvh = u.unit / p.row_blocks;
-  const int64_t at = (static_cast<int64_t>(u.seq) * a.n_new + (row0 + row) / g) * a.q_heads +
-                     kvh * g + (row0 + row) % g;
-  static_cast<T*>(a.o)[at * D + threadIdx.x] = static_cast<T>(x * inv_or_zero(sum));
-  if (a.lse != nullptr && threadIdx.x == 0) a.lse[at] = row_lse(m, sum);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_for_primary();
+  for (int r0 = blockIdx.y * at_once; r0 < rows; r0 += gridDim.y * at_once) {
+    const int row = r0 + warp / share;
+    constexpr int V = 128 / D;  // partials a warp reads at once (16 bytes a lane)
+    if (row < rows) {
+      float m = -INFINITY;
+      for (int i = lane; i < n; i += 32) m = fmaxf(m, slot(i)[RT * D + 2 * row]);
+      m = warp_max(m);
+      const float base = m == -INFINITY ? 0.f : m;
+      float l = 0.f, f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int i = (warp % share) * V + lane / (D / 4); i < n; i += share * V) {
+        const float* s = slot(i);
+        const float2 y = *reinterpret_cast<const float2*>(s + RT * D + 2 * row);
+        const float4 x = *reinterpret_cast<const float4*>(s + row * D + lane % (D / 4) * 4);
+        const float w = fast_exp2(y.x - base);
+        l = fmaf(w, y.y, l);
+        f[0] = fmaf(w, x.x, f[0]);
+        f[1] = fmaf(w, x.y, f[1]);
+        f[2] = fmaf(w, x.z, f[2]);
+        f[3] = fmaf(w, x.w, f[3]);
+      }
+      if (D == 64) {
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] += __shfl_xor_sync(0xffffffffu, f[e], 16);
+      }
+      if (lane < D / 4) s_o[warp][lane] = make_float4(f[0], f[1], f[2], f[3]);
+      if (lane == 0) {
+        s_l[warp] = l;
+        s_m[warp] = m;
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < at_once * (D / 4); e += kThreads) {
+      const int k = e / (D / 4), c = e % (D / 4), r = r0 + k;
+      if (r >= rows) break;
+      float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int i = k * share; i < (k + 1) * share; ++i) {
+        sum += s_l[i];
+        const float4 y = s_o[i][c];
+        x[0] += y.x;
+        x[1] += y.y;
+        x[2] += y.z;
+        x[3] += y.w;
+      }
+      const float inv = inv_or_zero(sum);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] *= inv;
+      const int64_t at = (static_cast<int64_t>(u.seq) * a.n_new + (row0 + r) / g) * a.q_heads +
+                         kvh * g + (row0 + r) % g;
+      store4(static_cast<T*>(a.o) + at * D + c * 4, x);
+      if (a.lse != nullptr && c == 0) a.lse[at] = row_lse(s_m[k * share], sum);
+    }
+    __syncthreads();
+  }
 }
 
 template <int D, int R, bool CAP, bool BIAS>
@@ -489,6 +581,8 @@ cudaError_t launch_tc_rows(const PagedArgs& a, const PagedPlan& plan, cudaStream
   PagedTcParams p;
   p.p = paged_params(a, plan);
   p.box_rows = std::min(a.page_size, KT);
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
   const cuuint64_t dims[2] = {D, static_cast<cuuint64_t>(a.n_pages) * a.kv_heads * a.page_size};
   const cuuint64_t strides[1] = {D * 2};
   const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(p.box_rows)};
@@ -506,7 +600,8 @@ template <typename T, int D>
 cudaError_t launch_join(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
   const int rows = std::min(plan.row_block, a.q_heads / a.kv_heads * a.n_new);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(plan.ctas, rows);
+  // About eight CTAs an SM in all; each loops over its share of the rows.
+  cfg.gridDim = dim3(plan.ctas, std::max(1, std::min(rows, 8 * device_sm_count() / plan.ctas)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
