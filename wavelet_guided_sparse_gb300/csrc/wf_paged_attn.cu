@@ -34,6 +34,7 @@ namespace wf {
 namespace {
 
 constexpr int KT = kPagedTile;  // keys per tile
+constexpr float kLazy = 8.f;    // log2 growth of a maximum that is tolerated
 
 // R: 16-row query tiles per CTA.
 template <int D, int R>
@@ -129,40 +130,42 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
       if (!active || key >= x.len) return -1;
       return __ldg(a.table + static_cast<int64_t>(x.seq) * a.table_pages + (key >> tp.page_shift));
     };
-    const auto wanted = [&](const WorkUnit& x, int64_t at) {
-      return active && static_cast<int>(at - x.begin) * KT + sub * tp.box_rows < x.len;
-    };
-    int fill = 0, units = 0;
+    const unsigned every = __ballot_sync(0xffffffffu, active);
+    int fill = 0, units = 0, st = 0;
+    uint32_t phase = 1;  // of the stage's last release (first round: none yet)
+    int row0 = 0, rows = 0, kvh = 0;
     bool ok = true;
     int page = w0 < w1 ? entry_of(u, w0) : -1;
-    for (int64_t at = w0; at < w1; ++at, ++fill) {
+    for (int64_t at = w0; at < w1; ++at) {
       // A unit's query rows arrive with its first tile: the runs of rows that
       // one query's heads (or a part of them) form, one bulk copy each.
       const bool first = at == w0 || at == u.begin;
-      const int row0 = (u.unit % p.row_blocks) * RT;
-      const int rows = min(RT, g * a.n_new - row0);
-      if (first && units++ > 0) {
-        ok = ring_wait(&bars.q_empty, (units - 2) & 1, &bars.abort, a.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+      if (first) {
+        kvh = u.unit / p.row_blocks;
+        row0 = (u.unit - kvh * p.row_blocks) * RT;
+        rows = min(RT, g * a.n_new - row0);
+        if (units++ > 0) {
+          ok = ring_wait(&bars.q_empty, (units - 2) & 1, &bars.abort, a.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
       }
-      const int st = fill % kStages;
       const int key = static_cast<int>(at - u.begin) * KT + sub * tp.box_rows;
-      const int kvh = u.unit / p.row_blocks;
       if (fill >= kStages) {
-        ok = ring_wait(&bars.empty[st], (fill / kStages - 1) & 1, &bars.abort, a.status);
+        ok = ring_wait(&bars.empty[st], phase, &bars.abort, a.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
       if (page < 0 || page >= a.n_pages) {
-        if (wanted(u, at)) raise_flag(a.status, WF_DEV_BAD_INDEX);
+        if (active && key < u.len) raise_flag(a.status, WF_DEV_BAD_INDEX);
         page = -1;
       }
       const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
-      const unsigned firsts = __ballot_sync(0xffffffffu, page >= 0 && which == 0 && kb == 0);
       if (lane == 0) {
-        int valid = 0;
-        for (int i = 0; i < boxes; ++i) valid |= ((firsts >> (i * 2 * KB)) & 1) << i;
+        int valid = (1 << boxes) - 1;
+        if (live != every)
+          for (int i = 0; i < boxes; ++i)
+            if (!((live >> (i * 2 * KB)) & 1)) valid &= ~(1 << i);
         bars.valid[st] = valid;
         mbar_arrive_expect_tx(&bars.full[st],
                               __popc(live) * box_bytes + (first ? rows * D * 2 : 0));
@@ -184,6 +187,11 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
                         sub * box_bytes,
                     map, kb * 64, y, &bars.full[st]);
       }
+      ++fill;
+      if (++st == kStages) {
+        st = 0;
+        phase ^= 1;
+      }
       if (at + 1 == u.begin + u.tiles) next_unit(p.w, a.kv_len, u);
       page = at + 1 < w1 ? entry_of(u, at + 1) : -1;
     }
@@ -199,12 +207,17 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
                                   kConsumerThreads);
     const float mul = CAP ? p.o.cap : p.o.scale;
     // ldmatrix lane addresses within a tile: keys as B (rows = keys), values
-    // transposed (rows = keys).
-    const int krow = kg * Shape::kKeys + ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;
-    const int vrow = kg * Shape::kKeys + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
-    const uint32_t koff = static_cast<uint32_t>(krow) * 128, voff = static_cast<uint32_t>(vrow) * 128;
-    const int ksw = krow & 7, vsw = vrow & 7;
-    int fill = 0;
+    // transposed (rows = keys); 16-byte chunk c of row r sits at c ^ (r % 8),
+    // so a step along a row is an exclusive or of bits 5-6 (and a column
+    // block every four).
+    const int krow = kg * Shape::kKeys + ((lane >> 4) << 3) + (lane & 7);
+    const int vrow = kg * Shape::kKeys + (((lane >> 3) & 1) << 3) + (lane & 7);
+    const uint32_t koff = krow * 128 + ((((lane >> 3) & 1) ^ (krow & 7)) << 4);
+    const uint32_t voff = vrow * 128 + (((lane >> 4) ^ (vrow & 7)) << 4);
+    const uint32_t ring_addr = smem_u32(ring);
+    const int kAllValid = (1 << (KT / tp.box_rows)) - 1;
+    int st = 0;
+    uint32_t phase = 0;
     bool ok = true;
     for (int64_t at = w0; at < w1; next_unit(p.w, a.kv_len, u)) {
       const int64_t end = min(w1, u.begin + u.tiles);
@@ -228,7 +241,7 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
         slope[h] = BIAS ? __ldg(p.o.slopes + kvh * g + hd) * kLog2e / mul : 0.f;
       }
       // The unit's query rows arrive with its first tile.
-      ok = ok && ring_wait(&bars.full[fill % kStages], (fill / kStages) & 1, &bars.abort, a.status);
+      ok = ok && ring_wait(&bars.full[st], phase, &bars.abort, a.status);
       ok = __all_sync(0xffffffffu, ok);
       uint32_t qf[D / 16][4];
 #pragma unroll
@@ -249,19 +262,22 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
         for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-      for (; at < end; ++at, ++fill) {
-        const int st = fill % kStages;
-        ok = ok && ring_wait(&bars.full[st], (fill / kStages) & 1, &bars.abort, a.status);
+      const int tiles = static_cast<int>(end - at);
+      int key0 = static_cast<int>(at - u.begin) * KT + kg * Shape::kKeys;
+      at = end;
+      // Keys below `open` are visible to every row of the warp.
+      int open = min(limit[0], limit[1]);
+#pragma unroll
+      for (int w = 4; w < 32; w <<= 1) open = min(open, __shfl_xor_sync(0xffffffffu, open, w));
+      for (int i = 0; i < tiles; ++i, key0 += KT) {
+        ok = ok && ring_wait(&bars.full[st], phase, &bars.abort, a.status);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {  // given up: only the barriers below, in step with the other warps
-          at = end;
-          break;
-        }
-        const int key0 = static_cast<int>(at - u.begin) * KT + kg * Shape::kKeys;
-        const uint32_t kt = smem_u32(ring + st * kStageBytes), vt = kt + kTileBytes;
+        if (!ok) break;  // given up: only the barriers below, in step with the other warps
+        const uint32_t kt = ring_addr + st * kStageBytes + koff;
+        const uint32_t vt = ring_addr + st * kStageBytes + kTileBytes + voff;
         const int valid = *reinterpret_cast<volatile int*>(&bars.valid[st]);
-        const bool whole = valid == (1 << (KT / tp.box_rows)) - 1;
-        if (!whole || key0 + Shape::kKeys > len) {
+        const bool edge = valid != kAllValid || key0 + Shape::kKeys > open;
+        if (edge && (valid != kAllValid || key0 + Shape::kKeys > len)) {
           // Clear the value rows whose weight is 0 by their place.
           for (int e = lane; e < Shape::kKeys * (D / 8); e += 32) {
             const int r = e / (D / 8), c = e % (D / 8);
@@ -275,22 +291,26 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
           __syncwarp();
         }
         constexpr int NB = Shape::kKeys / 8;  // 8-key blocks
-        float s[NB][4];
+        // Two accumulators a block halve the chain of dependent products.
+        float s[NB][4], s2[NB][4];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
 #pragma unroll
           for (int n = 0; n < NB; n += 2) {
             uint32_t b[4];
-            const int ch = ks * 2 + kch;
-            ldsm_x4(kt + (ch >> 3) * (KT * 128) + koff + n * 1024 + (((ch & 7) ^ ksw) << 4), b);
-            mma_bf16(s[n], qf[ks], b);
-            mma_bf16(s[n + 1], qf[ks], b + 2);
+            ldsm_x4((kt ^ ((ks & 3) << 5)) + (ks >> 2) * (KT * 128) + n * 1024, b);
+            mma_bf16(ks & 1 ? s2[n] : s[n], qf[ks], b);
+            mma_bf16(ks & 1 ? s2[n + 1] : s[n + 1], qf[ks], b + 2);
           }
         }
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
         if (CAP) {
 #pragma unroll
           for (int n = 0; n < NB; ++n)
@@ -306,7 +326,7 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
               s[n][e] = fmaf(-slope[e >> 1], fabsf(posf[e >> 1] - key), s[n][e]);
             }
         }
-        if (!whole || key0 + Shape::kKeys > min(limit[0], limit[1])) {
+        if (edge) {
 #pragma unroll
           for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -322,14 +342,13 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
           mx[0] = fmaxf(mx[0], fmaxf(s[n][0], s[n][1]));
           mx[1] = fmaxf(mx[1], fmaxf(s[n][2], s[n][3]));
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * mul;
-        }
-        if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+        // A row's lanes must agree on its maximum; whether any has grown too
+        // far, every lane can tell from its own part.
+        if (__any_sync(0xffffffffu, mx[0] * mul > m[0] + kLazy || mx[1] * mul > m[1] + kLazy)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * mul;
             const float mn = fmaxf(m[h], mx[h]);
             const float f = mn == -INFINITY ? 1.f : fast_exp2(m[h] - mn);
             m[h] = mn;
@@ -359,14 +378,17 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
 #pragma unroll
           for (int n = 0; n < D / 16; ++n) {
             uint32_t b[4];
-            const int ch = 2 * n + vch;
-            ldsm_x4_t(vt + (ch >> 3) * (KT * 128) + voff + kk * 2048 + (((ch & 7) ^ vsw) << 4), b);
+            ldsm_x4_t((vt ^ ((n & 3) << 5)) + (n >> 2) * (KT * 128) + kk * 2048, b);
             mma_bf16(o[2 * n], af, b);
             mma_bf16(o[2 * n + 1], af, b + 2);
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.empty[st]);
+        if (++st == kStages) {
+          st = 0;
+          phase ^= 1;
+        }
       }
 
       // The warps of a row tile add up, in key-group order: every warp leaves
