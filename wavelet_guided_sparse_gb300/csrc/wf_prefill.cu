@@ -144,6 +144,17 @@ __device__ __forceinline__ uint64_t umma_desc_rows(uint32_t saddr, uint32_t bloc
          (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
@@ -279,66 +290,97 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
       }
     } else if (warp == 8) {
-      if (lane == 0) {
-        bool ok = true;
-        constexpr uint32_t kRowDesc = umma_idesc_bf16(kTileRows, D) | (1u << 16);  // B: N-major
-        // S_t = Q_t K_jᵀ over the keys some row sees, rounded up to 16.
-        const auto issue_qk = [&](int t, int j) {
-          const int n = min(kTileRows, (qt[t].end - j * kTileRows + 15) & ~15);
-          const uint32_t q0 = smem_u32(smem + t * kTileBytes);
-          const uint32_t k0 = smem_u32(ring + ((2 * j) % kStages) * kTileBytes);
+      // The whole warp walks the loop (uniform addresses and descriptors), one
+      // elected lane issues.
+      const bool leader = elect_one();
+      bool ok = true;
+      constexpr uint32_t kRowDesc = umma_idesc_bf16(kTileRows, D) | (1u << 16);  // B: N-major
+      const uint64_t q_desc[2] = {umma_desc_sw128(smem_u32(smem)),
+                                  umma_desc_sw128(smem_u32(smem + kTileBytes))};
+      const uint64_t k_desc = umma_desc_sw128(smem_u32(ring));
+      const uint64_t v_desc = umma_desc_rows(smem_u32(ring), kTileRows * 128);
+      // S_t = Q_t K_jᵀ over the keys some row sees, rounded up to 16.
+      const auto issue_qk = [&](int t, int j, int st) {
+        const int n = min(kTileRows, (qt[t].end - j * kTileRows + 15) & ~15);
+        const uint32_t idesc = umma_idesc_bf16(kTileRows, n);
+        const uint64_t kd = k_desc + static_cast<uint32_t>(st * (kTileBytes >> 4));
+        if (leader) {
+#pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * (kTileRows * 128) + (ks & 3) * 32;
-            umma_bf16(tS[t], umma_desc_sw128(q0 + off), umma_desc_sw128(k0 + off),
-                      umma_idesc_bf16(kTileRows, n), ks != 0);
+            constexpr int kBlock = kTileRows * 128;
+            const uint32_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+            umma_bf16(tS[t], q_desc[t] + off, kd + off, idesc, ks != 0);
           }
           umma_commit(&bars.s[t]);
-        };
-        const auto issue_pv = [&](int t, int j) {
-          const int steps = min(kTileRows, qt[t].end - j * kTileRows + 15) / 16;
-          const uint32_t v0 = smem_u32(ring + ((2 * j + 1) % kStages) * kTileBytes);
-          for (int ks = 0; ks < steps; ++ks)
-            umma_bf16_ts(tO[t], tS[t] + ks * 8, umma_desc_rows(v0 + ks * 2048, kTileRows * 128),
-                         kRowDesc, (j | ks) != 0);
-        };
-        const auto wait_fill = [&](int f) {
-          return pre_wait(bars, &bars.full[f % kStages], (f / kStages) & 1, a.status);
-        };
-        if (tiles > 0) {
-          ok = wait_fill(0);
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (qt[t].tiles == 0) continue;
-            ok = pre_wait(bars, &bars.q[t], 0, a.status);
-            if (ok) issue_qk(t, 0);
-          }
-          if (ok) umma_commit(&bars.empty[0]);
         }
-        for (int j = 0; j < tiles && ok; ++j) {
-          ok = wait_fill(2 * j + 1);
-          const bool more = j + 1 < tiles;
-          bool key_ready = false;
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (j >= qt[t].tiles) continue;
-            ok = pre_wait(bars, &bars.p[t], j & 1, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(t, j);
-            if (j + 1 == qt[t].tiles) umma_commit(&bars.o[t]);
-            if (j + 1 < qt[t].tiles) {
-              if (!key_ready) {
-                ok = wait_fill(2 * j + 2);
-                if (!ok) break;
-                key_ready = true;
-              }
-              issue_qk(t, j + 1);
-            }
+      };
+      const auto issue_pv = [&](int t, int j, int st) {
+        const int steps = min(kTileRows, qt[t].end - j * kTileRows + 15) / 16;
+        const uint64_t vd = v_desc + static_cast<uint32_t>(st * (kTileBytes >> 4));
+        if (leader) {
+          if (steps == 8) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              umma_bf16_ts(tO[t], tS[t] + ks * 8, vd + ks * (2048 >> 4), kRowDesc, (j | ks) != 0);
+          } else {
+            for (int ks = 0; ks < steps; ++ks)
+              umma_bf16_ts(tO[t], tS[t] + ks * 8, vd + ks * (2048 >> 4), kRowDesc, (j | ks) != 0);
           }
-          if (ok) {
-            umma_commit(&bars.empty[(2 * j + 1) % kStages]);
-            if (more) umma_commit(&bars.empty[(2 * j + 2) % kStages]);
+          if (j + 1 == qt[t].tiles) umma_commit(&bars.o[t]);
+        }
+      };
+      const auto release = [&](int st) {
+        if (leader) umma_commit(&bars.empty[st]);
+      };
+      // Stage and parity of the ring's fills in order: K_0 V_0 K_1 V_1 ...
+      int st = 0;
+      uint32_t parity = 0;
+      const auto advance = [&]() {
+        if (++st == kStages) {
+          st = 0;
+          parity ^= 1;
+        }
+      };
+      if (tiles > 0) {
+        ok = pre_wait(bars, &bars.full[0], 0, a.status);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (qt[t].tiles == 0 || !ok) continue;
+          ok = pre_wait(bars, &bars.q[t], 0, a.status);
+          if (ok) issue_qk(t, 0, 0);
+        }
+        if (ok) release(0);
+        advance();
+      }
+      for (int j = 0; j < tiles && ok; ++j) {
+        const int vs = st;
+        ok = pre_wait(bars, &bars.full[vs], parity, a.status);
+        advance();
+        const int ks = st;
+        const uint32_t kpar = parity;
+        const bool more = j + 1 < tiles;
+        if (more) advance();
+        bool key_ready = false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (j >= qt[t].tiles || !ok) continue;
+          ok = pre_wait(bars, &bars.p[t], j & 1, a.status);
+          if (!ok) continue;
+          tc_fence_after();
+          issue_pv(t, j, vs);
+          if (j + 1 < qt[t].tiles) {
+            if (!key_ready) ok = pre_wait(bars, &bars.full[ks], kpar, a.status);
+            key_ready = true;
+            if (ok) issue_qk(t, j + 1, ks);
           }
         }
-        if (!ok) {  // the products in flight end before tensor memory is freed
+        if (ok) {
+          release(vs);
+          if (more) release(ks);
+        }
+      }
+      if (!ok) {  // the products in flight end before tensor memory is freed
+        if (leader) {
           umma_commit(&bars.drain);
           mbar_wait_bounded(&bars.drain, 0, a.status);
         }
