@@ -91,7 +91,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
       : "memory");
 }
 
-#define WF_R8(a, i) a[i], a[i + 1], a[i + 2], a[i + 3], a[i + 4], a[i + 5], a[i + 6], a[i + 7]
 #define WF_O8(a, i)                                                                      \
   "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), \
       "=r"(a[i + 6]), "=r"(a[i + 7])
@@ -99,12 +98,27 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
   "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), \
       "r"(a[i + 6]), "r"(a[i + 7])
 
-// 32 columns of this thread's tensor-memory lane (issue only; tmem_wait_ld).
+// 64 (or 32) columns of this thread's tensor-memory lane.  The load and its
+// wait are one statement: the registers of an asynchronous load must not be
+// touched, moved or spilled before it.
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+      "%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,"
+      "%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : WF_O8(r, 0), WF_O8(r, 8), WF_O8(r, 16), WF_O8(r, 24), WF_O8(r, 32), WF_O8(r, 40),
+        WF_O8(r, 48), WF_O8(r, 56)
+      : "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
-      "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : WF_O8(r, 0), WF_O8(r, 8), WF_O8(r, 16), WF_O8(r, 24)
       : "r"(addr)
       : "memory");
@@ -117,7 +131,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       WF_I8(r, 8), WF_I8(r, 16), WF_I8(r, 24), "r"(addr)
       : "memory");
 }
-#undef WF_R8
 #undef WF_O8
 #undef WF_I8
 __device__ __forceinline__ void tmem_wait_st() {
@@ -178,6 +191,48 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// z = [cap tanh(s / cap) or scale s] - slope |d0 - i|, in the log2 domain,
+// for the keys i = 0..31 of a chunk; d0 = position minus the chunk's first
+// key.  `side`: every row of the warp lies behind the chunk (1: the distance
+// is linear in i), before it (-1), or neither (0).
+//
+// cap tanh(x) = cap - 2 cap / (1 + e^(2x)).  The special-function unit is what
+// bounds these variants (two powers of two and a reciprocal a score), so two
+// scores share one reciprocal: 1/a = b / (a b).  With 2x log2 e clamped at 60
+// the product stays finite, and 2 / (1 + 2^60) is far below fp32's step at 1.
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ void map_scores(float* s, const ScoreOpts& o, float slope, float d0,
+                                           int side) {
+  const float step = side > 0 ? slope : -slope;
+  const float base = (CAP ? o.cap : 0.f) - (BIAS ? step * d0 : 0.f);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float add[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (!BIAS)
+        add[e] = base;
+      else if (side != 0)
+        add[e] = fmaf(step, static_cast<float>(i + e), base);
+      else
+        add[e] = fmaf(-slope, fabsf(d0 - static_cast<float>(i + e)), CAP ? o.cap : 0.f);
+    }
+    if (CAP) {
+      const float k = o.scale * (2.f * kLog2e);
+      const float a = 1.f + fast_exp2(fminf(s[i] * k, 60.f));
+      const float b = 1.f + fast_exp2(fminf(s[i + 1] * k, 60.f));
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+      r *= -2.f * o.cap;
+      s[i] = fmaf(r, b, add[0]);
+      s[i + 1] = fmaf(r, a, add[1]);
+    } else {
+      s[i] = fmaf(s[i], o.scale, add[0]);
+      s[i + 1] = fmaf(s[i + 1], o.scale, add[1]);
+    }
+  }
 }
 
 // What a query tile of this CTA covers.
@@ -399,8 +454,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                           ? (p.o.causal ? min(doc.n_k, max(pos + 1, prefix)) : doc.n_k)
                           : me.end;
     const float slope = BIAS ? __ldg(p.o.slopes + me.head) * kLog2e : 0.f;
-    // Scores enter the exponent as fma(s, mul, -m).
-    const float mul = CAP ? p.o.cap : p.o.scale;
+    // Scores (with cap or bias: mapped scores) enter the exponent as
+    // fma(s, mul, -m).
+    const float mul = CAP || BIAS ? 1.f : p.o.scale;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < me.tiles; ++j) {
@@ -412,19 +468,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       tc_fence_after();
       const int k0 = j * kTileRows;
       uint32_t sr[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, sr + 32 * c);
-      tmem_wait_ld();
+      tmem_ld64(s_addr, sr);
+      tmem_ld64(s_addr + 64, sr + 64);
       float* s = reinterpret_cast<float*>(sr);
-      if (CAP) {
+      if (CAP || BIAS) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i) s[i] = tanh_exp2(s[i] * p.o.scale);
-      }
-      if (BIAS) {
-        // In units of the multiplier, so that the exponent stays one fma.
-        const float w = slope / mul, d0 = static_cast<float>(pos - k0);
-#pragma unroll
-        for (int i = 0; i < 128; ++i) s[i] = fmaf(-w, fabsf(d0 - static_cast<float>(i)), s[i]);
+        for (int c = 0; c < 4; ++c) {
+          const float d0 = static_cast<float>(pos - k0 - 32 * c);
+          const int side = !BIAS ? 1
+                           : __all_sync(0xffffffffu, d0 >= 31.f) ? 1
+                           : __all_sync(0xffffffffu, d0 <= 0.f)  ? -1 : 0;
+          map_scores<CAP, BIAS>(s + 32 * c, p.o, slope, d0, side);
+        }
       }
       const int rel = limit - k0;
       if (__any_sync(0xffffffffu, rel < 128)) {
@@ -452,7 +507,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(o_addr + 32 * c, o);
-          tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             float x, y;
@@ -523,7 +577,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         uint32_t o[32];
         if (me.tiles > 0) {
           tmem_ld32(o_addr + 32 * c, o);
-          tmem_wait_ld();
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0;
