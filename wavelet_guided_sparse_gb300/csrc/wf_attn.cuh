@@ -70,6 +70,30 @@ __device__ __forceinline__ void store4(__nv_bfloat16* dst, const float* f) {
                                               *reinterpret_cast<const uint32_t*>(&c));
 }
 
+// A bounded wait on an mbarrier phase by a whole converged warp, which also
+// ends when another warp of the CTA has given up (*abort); true when the
+// phase has completed.  The first tries stand alone, outside any loop: a try
+// sleeps until the phase completes or its time limit, so it usually
+// suffices, and a wait that is over already costs 70 cycles this way against
+// 220 in the loop (measured in the packed-prompt kernel, whose products wait
+// four times a key tile).  `nap`: nanoseconds between the later polls, for
+// warps with time to spare.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort,
+                                          int32_t* status, uint32_t nap = 0) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (nap != 0) __nanosleep(nap);
+    if ((i & 255) == 255 &&
+        __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(abort) != 0))
+      return false;
+  }
+  raise_flag(status, WF_DEV_WAIT_TIMEOUT);
+  *reinterpret_cast<volatile int*>(abort) = 1;
+  return false;
+}
+
 // Programmatic dependent launch: the next kernel of the stream (launched with
 // that attribute) may start its prologue; it waits for this one's results.
 __device__ __forceinline__ void launch_dependents() {
@@ -239,7 +263,7 @@ inline PagedParams paged_params(const PagedArgs& a, const PagedPlan& plan) {
 // Row blocks of packed sequences: `rows` rows of one key-value head a block
 // (n_q g rows in a sequence).  A grid of doc_blocks() blocks covers any split
 // of the rows into sequences; find_doc_block maps a block index to its
-// sequence (whole block; false: past the last block).  Offsets are clamped
+// sequence (whole warp; false: past the last block).  Offsets are clamped
 // into the arrays, and a bad one is flagged.
 inline int64_t doc_blocks(int64_t rows_q, int n_docs, int rows, int g) {
   return rows_q * g / rows + n_docs;
@@ -254,12 +278,18 @@ __device__ __forceinline__ int doc_span(const int32_t* cu, int i, int rows, int*
   *first = a;
   return max(b - a, 0);
 }
+// Where the last search ended: its 32 sequences and the blocks before them.
+struct DocCursor {
+  int d0;
+  int64_t base;
+};
 __device__ __forceinline__ bool find_doc_block(const PrefillArgs& a, int64_t at, int rows, int g,
-                                               DocBlock* out) {
+                                               DocCursor& cursor, DocBlock* out) {
   const int lane = threadIdx.x & 31;
-  // Every warp scans the sequences, 32 at a time.
-  int64_t base = 0;
-  for (int d0 = 0; d0 < a.n_docs; d0 += 32) {
+  // The warp scans the sequences, 32 at a time.
+  if (at < cursor.base) cursor = {0, 0};
+  int64_t base = cursor.base;
+  for (int d0 = cursor.d0; d0 < a.n_docs; d0 += 32) {
     int first = 0, n = 0;
     if (d0 + lane < a.n_docs) n = doc_span(a.cu_q, d0 + lane, a.rows_q, &first);
     const int blocks = static_cast<int>((static_cast<int64_t>(n) * g + rows - 1) / rows);
@@ -274,6 +304,7 @@ __device__ __forceinline__ bool find_doc_block(const PrefillArgs& a, int64_t at,
       int k0 = 0;
       out->n_k = doc_span(a.cu_k, out->doc, a.rows_k, &k0);
       out->k0 = k0;
+      cursor = {d0, base};
       return true;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -282,9 +313,9 @@ __device__ __forceinline__ bool find_doc_block(const PrefillArgs& a, int64_t at,
 }
 
 // Flags offsets that are not ascending within [0, rows] (one block checks).
-__device__ __forceinline__ void check_offsets(const int32_t* cu, int n, int rows,
-                                              int32_t* status) {
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+__device__ __forceinline__ void check_offsets(const int32_t* cu, int n, int rows, int32_t* status,
+                                              int thread, int threads) {
+  for (int i = thread; i < n; i += threads) {
     const int a = __ldg(cu + i), b = __ldg(cu + i + 1);
     if (a < 0 || b < a || b > rows) raise_flag(status, WF_DEV_BAD_INDEX);
   }

@@ -286,11 +286,12 @@ __global__ void __launch_bounds__(kThreads) prefill_fma_kernel(PrefillParams p) 
   const int g = a.q_heads / a.kv_heads;
   const int kvh = blockIdx.y;
   if (blockIdx.x == 0 && kvh == 0) {
-    check_offsets(a.cu_q, a.n_docs, a.rows_q, a.status);
-    check_offsets(a.cu_k, a.n_docs, a.rows_k, a.status);
+    check_offsets(a.cu_q, a.n_docs, a.rows_q, a.status, threadIdx.x, kThreads);
+    check_offsets(a.cu_k, a.n_docs, a.rows_k, a.status, threadIdx.x, kThreads);
   }
   DocBlock d;
-  if (!find_doc_block(a, static_cast<int64_t>(blockIdx.x), RT, g, &d)) return;
+  DocCursor cursor = {0, 0};
+  if (!find_doc_block(a, static_cast<int64_t>(blockIdx.x), RT, g, cursor, &d)) return;
   RowBlock b;
   b.g = g;
   b.n_q = d.n_q;

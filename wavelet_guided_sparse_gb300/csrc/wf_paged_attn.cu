@@ -65,18 +65,6 @@ struct PagedBarriers {
   int abort;
 };
 
-// A bounded wait that also ends when another warp has given up.
-__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, int* abort,
-                                          int32_t* status) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255) == 255 && *reinterpret_cast<volatile int*>(abort) != 0) return false;
-  }
-  raise_flag(status, WF_DEV_WAIT_TIMEOUT);
-  *reinterpret_cast<volatile int*>(abort) = 1;
-  return false;
-}
-
 template <int D, int R, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, R>::kCtasPerSm)
     paged_tc_kernel(const __grid_constant__ PagedTcParams tp) {
@@ -145,15 +133,13 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
         row0 = (u.unit - kvh * p.row_blocks) * RT;
         rows = min(RT, g * a.n_new - row0);
         if (units++ > 0) {
-          ok = ring_wait(&bars.q_empty, (units - 2) & 1, &bars.abort, a.status);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = warp_wait(&bars.q_empty, (units - 2) & 1, &bars.abort, a.status);
           if (!ok) break;
         }
       }
       const int key = static_cast<int>(at - u.begin) * KT + sub * tp.box_rows;
       if (fill >= kStages) {
-        ok = ring_wait(&bars.empty[st], phase, &bars.abort, a.status);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_wait(&bars.empty[st], phase, &bars.abort, a.status);
         if (!ok) break;
       }
       if (page < 0 || page >= a.n_pages) {
@@ -241,8 +227,7 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
         slope[h] = BIAS ? __ldg(p.o.slopes + kvh * g + hd) * kLog2e / mul : 0.f;
       }
       // The unit's query rows arrive with its first tile.
-      ok = ok && ring_wait(&bars.full[st], phase, &bars.abort, a.status);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = ok && warp_wait(&bars.full[st], phase, &bars.abort, a.status);
       uint32_t qf[D / 16][4];
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
@@ -270,8 +255,7 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
 #pragma unroll
       for (int w = 4; w < 32; w <<= 1) open = min(open, __shfl_xor_sync(0xffffffffu, open, w));
       for (int i = 0; i < tiles; ++i, key0 += KT) {
-        ok = ok && ring_wait(&bars.full[st], phase, &bars.abort, a.status);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = ok && warp_wait(&bars.full[st], phase, &bars.abort, a.status);
         if (!ok) break;  // given up: only the barriers below, in step with the other warps
         const uint32_t kt = ring_addr + st * kStageBytes + koff;
         const uint32_t vt = ring_addr + st * kStageBytes + kTileBytes + voff;

@@ -3,7 +3,7 @@
 // cap and bias of wf_attn.cuh.  fp32 inputs run on the FMA pipes
 // (wf_attn_fma.cu).
 //
-// A CTA owns two 128-row query tiles that share their keys: two query heads
+// An item is two 128-row query tiles that share their keys: two query heads
 // of one key-value head where the group is even (same rows, same masks, no
 // half-empty pair in short sequences), else two consecutive row blocks of
 // one head.  Warps 0-3 and 4-7 are the softmax groups of the two
@@ -12,8 +12,9 @@
 //     S_t = Q_t K_jᵀ              (tcgen05, both operands in shared memory)
 //     P_t = 2^(z - m)             (softmax group: registers, P over S's columns)
 //     O_t += P_t V_j              (tcgen05, P from tensor memory, V row-major)
-// issued as PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1): while one group works on its
-// scores the tensor cores run the other tile's products.  Tensor memory:
+// issued as PV_0(j) QK_0(j-1) PV_1(j) QK_1(j-1), from the last key tile to the
+// first: while one group works on its scores the tensor cores run the other
+// tile's products.  Tensor memory:
 // S_0 S_1 O_0 O_1 (512 columns of fp32 at d = 128); keys and values pass
 // through one ring of 128-row stages (tensor copies, 128-byte swizzle).
 //
@@ -26,6 +27,12 @@
 // the first tiles O is hardly ever touched.  Weights are rounded to bf16 for
 // the product with the values (half a step, 2^-8 relative each, as any bf16
 // operand); their sum is taken in fp32 before that rounding.
+//
+// A CTA stays on its SM: warp 2 claims blocks of the grid that have not
+// started yet (cluster launch control: dynamic balance without a counter in
+// memory) as soon as the current item's copies are all issued, so that the
+// next item's queries, keys and first scores come in behind the current
+// one's last tiles and output.
 //
 // Rows behind the sequence's last key in a stage (another sequence's, or the
 // copy's zero fill) meet weights of exactly 0: the softmax group clears up to
@@ -47,6 +54,8 @@ namespace {
 constexpr int kPreThreads = 384;
 constexpr int kIssueRegs = 80, kSoftmaxRegs = 208;
 static_assert(8 * kSoftmaxRegs + 4 * kIssueRegs <= 12 * 168, "beyond the launch's registers");
+// Warps 0-3 issue, 4-7 and 8-11 are the softmax groups.
+constexpr int kProducts = 0, kCopies = 1, kItems = 2;
 constexpr int kTileRows = 128;  // query rows of a tile, keys of a tile
 constexpr float kLazy = 8.f;    // log2 growth of a maximum that is tolerated
 
@@ -64,22 +73,35 @@ struct PrefillTcParams {
   int pair_heads;  // 1: tiles are heads h, h + 1; 0: row blocks 2b, 2b + 1
 };
 
+// What a query tile of an item covers.
+struct QueryTile {
+  int head, row0, rows;  // head, first row within the sequence, rows (0: none)
+  int end;               // keys some row sees
+  int tiles;             // key tiles
+};
+// One unit of work: two query tiles over their sequence's keys.
+struct Item {
+  QueryTile qt[2];
+  int q0, k0, n_k, shift, prefix;  // first row and key, keys, position of row 0
+  int kvh, live;                   // key-value head; 0: no more items
+};
+
 struct PreBarriers {
-  uint64_t full[8], empty[8], q[2], s[2], p[2], o[2], drain;
+  uint64_t full[8], empty[8];  // ring stages
+  uint64_t q[2], q_empty[2];   // query tiles in shared memory
+  uint64_t s[2], p[2];         // scores ready; weights ready
+  uint64_t o[2], o_empty[2];   // output finished; read
+  uint64_t item, item_empty;   // item published; read by every role
+  uint64_t claim, drain;
+  uint4 claimed;               // response of a claim
+  Item it;
   uint32_t tmem;
   int abort;
 };
 
-// A bounded wait that also ends when another role has given up.
 __device__ __forceinline__ bool pre_wait(PreBarriers& b, uint64_t* bar, uint32_t parity,
-                                         int32_t* status) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255) == 255 && *reinterpret_cast<volatile int*>(&b.abort) != 0) return false;
-  }
-  raise_flag(status, WF_DEV_WAIT_TIMEOUT);
-  *reinterpret_cast<volatile int*>(&b.abort) = 1;
-  return false;
+                                         int32_t* status, uint32_t nap = 0) {
+  return warp_wait(bar, parity, &b.abort, status, nap);
 }
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z,
@@ -129,6 +151,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
       "%24,%25,%26,%27,%28,%29,%30,%31};" ::WF_I8(r, 0),
       WF_I8(r, 8), WF_I8(r, 16), WF_I8(r, 24), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::WF_I8(r, 0),
+      WF_I8(r, 8), "r"(addr)
       : "memory");
 }
 #undef WF_O8
@@ -235,12 +264,68 @@ __device__ __forceinline__ void map_scores(float* s, const ScoreOpts& o, float s
   }
 }
 
-// What a query tile of this CTA covers.
-struct QueryTile {
-  int head, row0, rows;  // head, first row within the sequence, rows (0: none)
-  int end;               // keys some row sees
-  int tiles;             // key tiles
-};
+// Claims a block of this grid that has not started (cluster launch control):
+// the 16-byte response lands at `to`, counted on `bar`.
+__device__ __forceinline__ void claim_block(uint4* to, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+      "[%0], [%1];" ::"r"(smem_u32(to)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The claimed block's index, or -1 when none was left.
+__device__ __forceinline__ int64_t claimed_block(const uint4* from) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(from))
+      : "memory");
+  return ok ? static_cast<int64_t>(x) : -1;
+}
+
+// The item of a block: heads run fastest, a sequence's row blocks from its
+// last (the longest under the causal mask) to its first.  False: behind the
+// last sequence.  Whole warp.
+__device__ __forceinline__ bool make_item(const PrefillTcParams& p, int64_t block,
+                                          DocCursor& cursor, Item* out) {
+  const PrefillArgs& a = p.a;
+  Item& it = *out;
+  const int heads = p.pair_heads ? a.q_heads / 2 : a.q_heads;
+  const int block_rows = p.pair_heads ? kTileRows : 2 * kTileRows;
+  if (block == 0) {
+    check_offsets(a.cu_q, a.n_docs, a.rows_q, a.status, threadIdx.x & 31, 32);
+    check_offsets(a.cu_k, a.n_docs, a.rows_k, a.status, threadIdx.x & 31, 32);
+  }
+  DocBlock doc;
+  if (!find_doc_block(a, block / heads, block_rows, 1, cursor, &doc)) return false;
+  it.live = 1;
+  const int hx = static_cast<int>(block % heads);
+  doc.block = (doc.n_q + block_rows - 1) / block_rows - 1 - doc.block;
+  it.q0 = static_cast<int>(doc.q0);
+  it.k0 = static_cast<int>(doc.k0);
+  it.n_k = doc.n_k;
+  it.prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + doc.doc) : 0;
+  it.shift = doc.n_k - doc.n_q;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    QueryTile& q = it.qt[t];
+    q.head = p.pair_heads ? 2 * hx + t : hx;
+    q.row0 = doc.block * block_rows + (p.pair_heads ? 0 : t * kTileRows);
+    q.rows = max(0, min(kTileRows, doc.n_q - q.row0));
+    q.end = q.rows == 0 ? 0
+                        : max(0, visible_end(doc.n_k, it.shift + q.row0 + q.rows - 1, p.o.causal,
+                                             it.prefix));
+    q.tiles = (q.end + kTileRows - 1) / kTileRows;
+  }
+  it.kvh = it.qt[0].head / (a.q_heads / a.kv_heads);
+  return true;
+}
 
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kPreThreads, 1)
@@ -255,34 +340,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const PrefillArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (blockIdx.x == 0) {
-    check_offsets(a.cu_q, a.n_docs, a.rows_q, a.status);
-    check_offsets(a.cu_k, a.n_docs, a.rows_k, a.status);
-  }
-  // The item: heads run fastest, a sequence's row blocks from its last (the
-  // longest under the causal mask) to its first.
-  const int heads = p.pair_heads ? a.q_heads / 2 : a.q_heads;
-  const int block_rows = p.pair_heads ? kTileRows : 2 * kTileRows;
-  DocBlock doc;
-  if (!find_doc_block(a, blockIdx.x / heads, block_rows, 1, &doc)) return;
-  const int hx = blockIdx.x % heads;
-  doc.block = (doc.n_q + block_rows - 1) / block_rows - 1 - doc.block;
-  const int prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + doc.doc) : 0;
-  const int shift = doc.n_k - doc.n_q;  // position of row 0
-  QueryTile qt[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    qt[t].head = p.pair_heads ? 2 * hx + t : hx;
-    qt[t].row0 = doc.block * block_rows + (p.pair_heads ? 0 : t * kTileRows);
-    qt[t].rows = max(0, min(kTileRows, doc.n_q - qt[t].row0));
-    qt[t].end = qt[t].rows == 0 ? 0
-                                : max(0, visible_end(doc.n_k, shift + qt[t].row0 + qt[t].rows - 1,
-                                                     p.o.causal, prefix));
-    qt[t].tiles = (qt[t].end + kTileRows - 1) / kTileRows;
-  }
-  const int tiles = max(qt[0].tiles, qt[1].tiles);
-  const int kvh = qt[0].head / (a.q_heads / a.kv_heads);
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars.full[i], 1);
@@ -290,16 +347,21 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars.q[t], 1);
+      mbar_init(&bars.q_empty[t], 1);
       mbar_init(&bars.s[t], 1);
       mbar_init(&bars.p[t], 128);
       mbar_init(&bars.o[t], 1);
+      mbar_init(&bars.o_empty[t], 128);
     }
+    mbar_init(&bars.item, 1);
+    mbar_init(&bars.item_empty, 10);
+    mbar_init(&bars.claim, 1);
     mbar_init(&bars.drain, 1);
     bars.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 8) tmem_alloc(&bars.tmem, 512);
-  if (warp == 9 && lane == 0) {
+  if (warp == kProducts) tmem_alloc(&bars.tmem, 512);
+  if (warp == kCopies && lane == 0) {
     prefetch_tensormap(&p.tq);
     prefetch_tensormap(&p.tk);
     prefetch_tensormap(&p.tv);
@@ -311,43 +373,95 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const uint32_t tS[2] = {tmem, tmem + 128};
   const uint32_t tO[2] = {tmem + 256, tmem + 256 + D};
 
-  if (warp >= 8) {
+  if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-    if (warp == 9) {
-      if (lane == 0) {
-        bool ok = true;
-        int fills = 0;
-        for (int t = 0; t < 2; ++t) {
-          if (qt[t].tiles == 0) continue;
-          mbar_arrive_expect_tx(&bars.q[t], kTileBytes);
-          for (int kb = 0; kb < D / 64; ++kb)
-            tma_load_3d(smem + t * kTileBytes + kb * (kTileRows * 128), &p.tq, kb * 64, qt[t].head,
-                        static_cast<int>(doc.q0) + qt[t].row0, &bars.q[t]);
-        }
-        for (int f = 0; f < 2 * tiles && ok; ++f) {
-          const int st = f % kStages;
-          if (f >= kStages) {
-            ok = pre_wait(bars, &bars.empty[st], (f / kStages - 1) & 1, a.status);
-            if (!ok) break;
+    const bool leader = elect_one();
+    if (warp == kItems) {
+      // ---- items: this CTA's own block, then blocks of the grid not started yet
+      bool ok = true;
+      int64_t block = blockIdx.x;
+      uint32_t claims = 0;
+      DocCursor cursor = {0, 0};
+      for (uint32_t k = 0; ok; ++k) {
+        // The last item has been read by all, and its copies are all issued.
+        if (k > 0) ok = pre_wait(bars, &bars.item_empty, (k - 1) & 1, a.status, 500);
+        if (!ok) break;
+        Item it = {};
+        // Blocks behind the last sequence's (the grid is sized for any split
+        // of the rows) are claimed and dropped.
+        for (bool mine = k == 0;; mine = false) {
+          if (!mine) {
+            if (leader) {
+              fence_proxy_async();
+              mbar_arrive_expect_tx(&bars.claim, 16);
+              claim_block(&bars.claimed, &bars.claim);
+            }
+            __syncwarp();
+            // Not cut short: the response must have landed before the CTA may go.
+            ok = mbar_wait_bounded(&bars.claim, claims++ & 1, a.status);
+            block = ok ? claimed_block(&bars.claimed) : -1;
           }
-          unsigned char* dst = ring + st * kTileBytes;
-          mbar_arrive_expect_tx(&bars.full[st], kTileBytes);
-          for (int kb = 0; kb < D / 64; ++kb)
-            tma_load_3d(dst + kb * (kTileRows * 128), (f & 1) ? &p.tv : &p.tk, kb * 64, kvh,
-                        static_cast<int>(doc.k0) + (f >> 1) * kTileRows, &bars.full[st]);
-          fills = f + 1;
+          if (block < 0 || make_item(p, block, cursor, &it)) break;
         }
-        if (!ok) {  // nothing of this CTA's copies may land after it has gone
-          for (int t = 0; t < 2; ++t)
-            if (qt[t].tiles != 0) mbar_wait_bounded(&bars.q[t], 0, a.status);
-          for (int f = max(0, fills - kStages); f < fills; ++f)
-            mbar_wait_bounded(&bars.full[f % kStages], (f / kStages) & 1, a.status);
+        if (leader) {
+          bars.it = it;
+          mbar_arrive(&bars.item);
         }
+        __syncwarp();
+        if (!it.live) break;
       }
-    } else if (warp == 8) {
-      // The whole warp walks the loop (uniform addresses and descriptors), one
-      // elected lane issues.
-      const bool leader = elect_one();
+    } else if (warp == kCopies) {
+      // ---- copies
+      bool ok = true;
+      uint32_t used[2] = {0, 0}, fills = 0, parity = 1;
+      int st = 0;
+      for (uint32_t k = 0; ok; ++k) {
+        ok = pre_wait(bars, &bars.item, k & 1, a.status);
+        if (!ok) break;
+        const Item it = bars.it;
+        if (!it.live) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (it.qt[t].tiles == 0 || !ok) continue;
+          if (used[t] > 0) ok = pre_wait(bars, &bars.q_empty[t], (used[t] - 1) & 1, a.status, 100);
+          if (!ok) continue;
+          ++used[t];
+          if (leader) {
+            mbar_arrive_expect_tx(&bars.q[t], kTileBytes);
+            for (int kb = 0; kb < D / 64; ++kb)
+              tma_load_3d(smem + t * kTileBytes + kb * (kTileRows * 128), &p.tq, kb * 64,
+                          it.qt[t].head, it.q0 + it.qt[t].row0, &bars.q[t]);
+          }
+        }
+        const int tiles = max(it.qt[0].tiles, it.qt[1].tiles);
+        for (int f = 0; f < 2 * tiles && ok; ++f) {
+          if (fills >= kStages) ok = pre_wait(bars, &bars.empty[st], parity, a.status, 100);
+          if (!ok) break;
+          if (leader) {
+            unsigned char* dst = ring + st * kTileBytes;
+            mbar_arrive_expect_tx(&bars.full[st], kTileBytes);
+            for (int kb = 0; kb < D / 64; ++kb)
+              tma_load_3d(dst + kb * (kTileRows * 128), (f & 1) ? &p.tv : &p.tk, kb * 64, it.kvh,
+                          it.k0 + (tiles - 1 - (f >> 1)) * kTileRows, &bars.full[st]);
+          }
+          ++fills;
+          if (++st == kStages) {
+            st = 0;
+            parity ^= 1;
+          }
+        }
+        __syncwarp();
+        if (leader) mbar_arrive(&bars.item_empty);
+      }
+      if (!ok && leader) {  // nothing of this CTA's copies may land after it has gone
+        for (int t = 0; t < 2; ++t)
+          if (used[t] > 0) mbar_wait_bounded(&bars.q[t], (used[t] - 1) & 1, a.status);
+        for (uint32_t f = fills > kStages ? fills - kStages : 0; f < fills; ++f)
+          mbar_wait_bounded(&bars.full[f % kStages], (f / kStages) & 1, a.status);
+      }
+    } else if (warp == kProducts) {
+      // ---- products: the whole warp walks the loop (uniform addresses and
+      // descriptors), one elected lane issues
       bool ok = true;
       constexpr uint32_t kRowDesc = umma_idesc_bf16(kTileRows, D) | (1u << 16);  // B: N-major
       const uint64_t q_desc[2] = {umma_desc_sw128(smem_u32(smem)),
@@ -355,8 +469,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const uint64_t k_desc = umma_desc_sw128(smem_u32(ring));
       const uint64_t v_desc = umma_desc_rows(smem_u32(ring), kTileRows * 128);
       // S_t = Q_t K_jᵀ over the keys some row sees, rounded up to 16.
-      const auto issue_qk = [&](int t, int j, int st) {
-        const int n = min(kTileRows, (qt[t].end - j * kTileRows + 15) & ~15);
+      const auto issue_qk = [&](int t, int keys, int st) {
+        const int n = min(kTileRows, (keys + 15) & ~15);
         const uint32_t idesc = umma_idesc_bf16(kTileRows, n);
         const uint64_t kd = k_desc + static_cast<uint32_t>(st * (kTileBytes >> 4));
         if (leader) {
@@ -369,19 +483,20 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           umma_commit(&bars.s[t]);
         }
       };
-      const auto issue_pv = [&](int t, int j, int st) {
-        const int steps = min(kTileRows, qt[t].end - j * kTileRows + 15) / 16;
+      // O_t += P_t V_j over `steps` 16-key steps; `fresh`: the first replaces O.
+      const auto issue_pv = [&](int t, int steps, int st, bool fresh) {
         const uint64_t vd = v_desc + static_cast<uint32_t>(st * (kTileBytes >> 4));
         if (leader) {
           if (steps == 8) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              umma_bf16_ts(tO[t], tS[t] + ks * 8, vd + ks * (2048 >> 4), kRowDesc, (j | ks) != 0);
+              umma_bf16_ts(tO[t], tS[t] + ks * 8, vd + ks * (2048 >> 4), kRowDesc,
+                           !(fresh && ks == 0));
           } else {
             for (int ks = 0; ks < steps; ++ks)
-              umma_bf16_ts(tO[t], tS[t] + ks * 8, vd + ks * (2048 >> 4), kRowDesc, (j | ks) != 0);
+              umma_bf16_ts(tO[t], tS[t] + ks * 8, vd + ks * (2048 >> 4), kRowDesc,
+                           !(fresh && ks == 0));
           }
-          if (j + 1 == qt[t].tiles) umma_commit(&bars.o[t]);
         }
       };
       const auto release = [&](int st) {
@@ -396,205 +511,257 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           parity ^= 1;
         }
       };
-      if (tiles > 0) {
-        ok = pre_wait(bars, &bars.full[0], 0, a.status);
+      uint32_t used[2] = {0, 0};  // items with tiles of query tile t so far
+      uint32_t np[2] = {0, 0};    // key tiles of query tile t so far
+      for (uint32_t k = 0; ok; ++k) {
+        ok = pre_wait(bars, &bars.item, k & 1, a.status);
+        if (!ok) break;
+        const int live = bars.it.live;
+        const int end[2] = {bars.it.qt[0].end, bars.it.qt[1].end};
+        const int nt[2] = {bars.it.qt[0].tiles, bars.it.qt[1].tiles};
+        __syncwarp();
+        if (leader) mbar_arrive(&bars.item_empty);
+        if (!live) break;
+        const int tiles = max(nt[0], nt[1]);
+        if (tiles == 0) continue;
+        // The scores of key tile j (stage st): query tile t's first ones wait
+        // for its queries, its last ones release them.
+        const auto scores = [&](int t, int j, int st) {
+          if (j == nt[t] - 1) ok = pre_wait(bars, &bars.q[t], used[t] & 1, a.status);
+          if (!ok) return;
+          issue_qk(t, end[t] - j * kTileRows, st);
+          if (j == 0 && leader) umma_commit(&bars.q_empty[t]);
+        };
+        ok = pre_wait(bars, &bars.full[st], parity, a.status);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (qt[t].tiles == 0 || !ok) continue;
-          ok = pre_wait(bars, &bars.q[t], 0, a.status);
-          if (ok) issue_qk(t, 0, 0);
-        }
-        if (ok) release(0);
+        for (int t = 0; t < 2; ++t)
+          if (ok && nt[t] == tiles) scores(t, tiles - 1, st);
+        if (ok) release(st);
         advance();
-      }
-      for (int j = 0; j < tiles && ok; ++j) {
-        const int vs = st;
-        ok = pre_wait(bars, &bars.full[vs], parity, a.status);
-        advance();
-        const int ks = st;
-        const uint32_t kpar = parity;
-        const bool more = j + 1 < tiles;
-        if (more) advance();
-        bool key_ready = false;
+        for (int j = tiles - 1; j >= 0 && ok; --j) {
+          const int vs = st;
+          ok = pre_wait(bars, &bars.full[vs], parity, a.status);
+          advance();
+          const int ks = st;
+          const uint32_t kpar = parity;
+          if (j > 0) {
+            advance();
+            ok = ok && pre_wait(bars, &bars.full[ks], kpar, a.status);
+          }
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (j >= qt[t].tiles || !ok) continue;
-          ok = pre_wait(bars, &bars.p[t], j & 1, a.status);
-          if (!ok) continue;
-          tc_fence_after();
-          issue_pv(t, j, vs);
-          if (j + 1 < qt[t].tiles) {
-            if (!key_ready) ok = pre_wait(bars, &bars.full[ks], kpar, a.status);
-            key_ready = true;
-            if (ok) issue_qk(t, j + 1, ks);
+          for (int t = 0; t < 2; ++t) {
+            if (ok && j < nt[t]) {
+              // The last item's output must have been read.
+              if (j == nt[t] - 1 && used[t] > 0)
+                ok = pre_wait(bars, &bars.o_empty[t], (used[t] - 1) & 1, a.status);
+              ok = ok && pre_wait(bars, &bars.p[t], np[t] & 1, a.status);
+              if (!ok) continue;
+              ++np[t];
+              tc_fence_after();
+              issue_pv(t, min(kTileRows, end[t] - j * kTileRows + 15) / 16, vs, j == nt[t] - 1);
+              if (j == 0 && leader) umma_commit(&bars.o[t]);
+            }
+            if (ok && j > 0 && j - 1 < nt[t]) scores(t, j - 1, ks);
+          }
+          if (ok) {
+            release(vs);
+            if (j > 0) release(ks);
           }
         }
-        if (ok) {
-          release(vs);
-          if (more) release(ks);
-        }
+        used[0] += nt[0] > 0;
+        used[1] += nt[1] > 0;
       }
-      if (!ok) {  // the products in flight end before tensor memory is freed
-        if (leader) {
-          umma_commit(&bars.drain);
-          mbar_wait_bounded(&bars.drain, 0, a.status);
-        }
-      }
+      // Every product, and every arrival it still owes, ends before tensor
+      // memory is freed and the CTA goes.
+      if (leader) umma_commit(&bars.drain);
+      __syncwarp();
+      mbar_wait_bounded(&bars.drain, 0, a.status);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int t = warp >> 2;
-    const QueryTile me = t == 0 ? qt[0] : qt[1];
+    // ---- softmax and output of query tile t, one row a thread
+    const int t = (warp >> 2) - 1;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = (t == 0 ? tS[0] : tS[1]) + lanes;
     const uint32_t o_addr = (t == 0 ? tO[0] : tO[1]) + lanes;
-    const int pos = shift + me.row0 + row;
-    const int limit = row < me.rows
-                          ? (p.o.causal ? min(doc.n_k, max(pos + 1, prefix)) : doc.n_k)
-                          : me.end;
-    const float slope = BIAS ? __ldg(p.o.slopes + me.head) * kLog2e : 0.f;
     // Scores (with cap or bias: mapped scores) enter the exponent as
     // fma(s, mul, -m).
     const float mul = CAP || BIAS ? 1.f : p.o.scale;
-    float m = -INFINITY, l = 0.f;
+    uint32_t ns = 0, used = 0, fill = 0;  // key tiles, items with tiles, ring fills so far
     bool ok = true;
-    for (int j = 0; j < me.tiles; ++j) {
-      ok = pre_wait(bars, &bars.s[t], j & 1, a.status);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const int k0 = j * kTileRows;
-      uint32_t sr[128];
-      tmem_ld64(s_addr, sr);
-      tmem_ld64(s_addr + 64, sr + 64);
-      float* s = reinterpret_cast<float*>(sr);
-      if (CAP || BIAS) {
+    for (uint32_t k = 0; ok; ++k) {
+      ok = pre_wait(bars, &bars.item, k & 1, a.status);
+      if (!ok) break;
+      // This thread's row: its place in the output, whether it exists (a row
+      // outside the arrays is never written), its visible keys.
+      const int mine = bars.it.qt[t].tiles, end = bars.it.qt[t].end, n_k = bars.it.n_k;
+      const int tiles = max(bars.it.qt[0].tiles, bars.it.qt[1].tiles);
+      const int row_at = bars.it.qt[t].row0 + row, head = bars.it.qt[t].head;
+      const int64_t out_row = static_cast<int64_t>(bars.it.q0) + row_at;
+      const bool live =
+          row < bars.it.qt[t].rows && static_cast<uint64_t>(out_row) < static_cast<uint64_t>(a.rows_q) &&
+          static_cast<uint32_t>(head) < static_cast<uint32_t>(a.q_heads);
+      const int64_t at = out_row * a.q_heads + head;
+      const int pos = bars.it.shift + row_at, live_item = bars.it.live;
+      const int limit =
+          live ? (p.o.causal ? min(n_k, max(pos + 1, bars.it.prefix)) : n_k) : end;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.item_empty);
+      if (!live_item) break;
+      const float slope = BIAS ? __ldg(p.o.slopes + max(0, min(head, a.q_heads - 1))) * kLog2e : 0.f;
+      float m = -INFINITY, l = 0.f;
+      // From the last key tile (under the causal mask the nearest keys, whose
+      // scores a distance bias leaves highest) to the first.
+      for (int j = mine - 1; j >= 0; --j) {
+        ok = pre_wait(bars, &bars.s[t], ns & 1, a.status);
+          if (!ok) break;
+        ++ns;
+        tc_fence_after();
+        const int k0 = j * kTileRows;
+        // Two passes over the tile in chunks of CH scores, as rolled loops: with
+        // the tile unrolled the code of the softmax groups would not stay in
+        // the instruction caches, and every role, the products' warp first,
+        // would wait for its fetches.  First the maximum (with cap or bias
+        // the mapped scores go back in place) ...
+        constexpr int CH = CAP || BIAS ? 32 : 64;
+        const int rel = limit - k0;
+        const bool edge = __any_sync(0xffffffffu, rel < 128);
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += CH) {
+          uint32_t r[CH];
+          if (CH == 64) tmem_ld64(s_addr + c, r); else tmem_ld32(s_addr + c, r);
+          float* s = reinterpret_cast<float*>(r);
+          if (CAP || BIAS) {
+            const float d0 = static_cast<float>(pos - k0 - c);
+            const int side = !BIAS ? 1
+                             : __all_sync(0xffffffffu, d0 >= 31.f) ? 1
+                             : __all_sync(0xffffffffu, d0 <= 0.f)  ? -1 : 0;
+            map_scores<CAP, BIAS>(s, p.o, slope, d0, side);
+          }
+          if (edge) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float d0 = static_cast<float>(pos - k0 - 32 * c);
-          const int side = !BIAS ? 1
-                           : __all_sync(0xffffffffu, d0 >= 31.f) ? 1
-                           : __all_sync(0xffffffffu, d0 <= 0.f)  ? -1 : 0;
-          map_scores<CAP, BIAS>(s + 32 * c, p.o, slope, d0, side);
+            for (int i = 0; i < CH; ++i) s[i] = i < rel - c ? s[i] : -INFINITY;
+          }
+#pragma unroll
+          for (int i = 0; i < CH; i += 4) {
+            mx0 = fmaxf(mx0, fmaxf(s[i], s[i + 1]));
+            mx1 = fmaxf(mx1, fmaxf(s[i + 2], s[i + 3]));
+          }
+          if (CAP || BIAS) tmem_st32(s_addr + c, r);
         }
-      }
-      const int rel = limit - k0;
-      if (__any_sync(0xffffffffu, rel < 128)) {
+        if (CAP || BIAS) tmem_wait_st();
+        const float mt = fmaxf(mx0, mx1) * mul;
+        if (j == mine - 1) {
+          m = mt;
+        } else if (__any_sync(0xffffffffu, mt > m + kLazy)) {
+          const float mn = fmaxf(m, mt);
+          const float f = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
+          m = mn;
+          l *= f;
+          const uint64_t f2 = pack2(f, f);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c, o);
 #pragma unroll
-        for (int i = 0; i < 128; ++i) s[i] = i < rel ? s[i] : -INFINITY;
-      }
-      float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+            for (int i = 0; i < 32; i += 2) {
+              float x, y;
+              unpack2(mul2(pack2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2), x, y);
+              o[i] = __float_as_uint(x);
+              o[i + 1] = __float_as_uint(y);
+            }
+            tmem_st32(o_addr + c, o);
+          }
+        }
+        // ... then the weights, each chunk's over columns already read.
+        const float base = m == -INFINITY ? 0.f : m;
+        const uint64_t mul2v = pack2(mul, mul), base2 = pack2(-base, -base);
+        uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += CH) {
+          uint32_t r[CH], pk[CH / 2];
+          if (CH == 64) tmem_ld64(s_addr + c, r); else tmem_ld32(s_addr + c, r);
+          if (!CAP && !BIAS && edge) {
 #pragma unroll
-      for (int i = 4; i < 128; i += 4) {
-        mx0 = fmaxf(mx0, s[i]);
-        mx1 = fmaxf(mx1, s[i + 1]);
-        mx2 = fmaxf(mx2, s[i + 2]);
-        mx3 = fmaxf(mx3, s[i + 3]);
-      }
-      const float mt = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * mul;
-      if (j == 0) {
-        m = mt;
-      } else if (__any_sync(0xffffffffu, mt > m + kLazy)) {
-        const float mn = fmaxf(m, mt);
-        const float f = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
-        m = mn;
-        l *= f;
-        const uint64_t f2 = pack2(f, f);
+            for (int i = 0; i < CH; ++i)
+              r[i] = i < rel - c ? r[i] : __float_as_uint(-INFINITY);
+          }
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + 32 * c, o);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
+          for (int i = 0; i < CH / 2; ++i) {
             float x, y;
-            unpack2(mul2(pack2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2), x, y);
-            o[i] = __float_as_uint(x);
-            o[i + 1] = __float_as_uint(y);
+            unpack2(fma2(pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), mul2v,
+                         base2),
+                    x, y);
+            x = fast_exp2(x);
+            y = fast_exp2(y);
+            if (i & 1) sum1 = add2(sum1, pack2(x, y)); else sum0 = add2(sum0, pack2(x, y));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+            pk[i] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          tmem_st32(o_addr + 32 * c, o);
+          if (CH == 64) tmem_st32(s_addr + c / 2, pk); else tmem_st16(s_addr + c / 2, pk);
         }
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      const uint64_t mul2v = pack2(mul, mul), base2 = pack2(-base, -base);
-      uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int e = 64 * c + 2 * i;
-          float x, y;
-          unpack2(fma2(pack2(s[e], s[e + 1]), mul2v, base2), x, y);
-          x = fast_exp2(x);
-          y = fast_exp2(y);
-          if (i & 1) sum1 = add2(sum1, pack2(x, y)); else sum0 = add2(sum0, pack2(x, y));
-          const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-          pk[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        tmem_st32(s_addr + 32 * c, pk);
-      }
-      float a0, a1;
-      unpack2(add2(sum0, sum1), a0, a1);
-      l += a0 + a1;
-      // Value rows behind the last key of the sequence, up to the product's end.
-      if (doc.n_k - k0 < kTileRows) {
-        const int r0 = doc.n_k - k0, r1 = min(kTileRows, (me.end - k0 + 15) & ~15);
-        if (r0 < r1) {
-          const int f = 2 * j + 1;
-          ok = pre_wait(bars, &bars.full[f % kStages], (f / kStages) & 1, a.status);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
+        float a0, a1;
+        unpack2(add2(sum0, sum1), a0, a1);
+        l += a0 + a1;
+        // Value rows behind the last key of the sequence, up to the product's end.
+        if (n_k - k0 < kTileRows) {
+          const int r0 = n_k - k0, r1 = min(kTileRows, (end - k0 + 15) & ~15);
+          if (r0 < r1) {
+            const uint32_t f = fill + 2 * (tiles - 1 - j) + 1;
+            ok = pre_wait(bars, &bars.full[f % kStages], (f / kStages) & 1, a.status);
+            if (!ok) break;
+            unsigned char* v = ring + (f % kStages) * kTileBytes;
+            for (int e = row; e < (r1 - r0) * (D / 8); e += 128) {
+              const int r = r0 + e / (D / 8), c = e % (D / 8);
+              *reinterpret_cast<uint4*>(v + (c >> 3) * (kTileRows * 128) + r * 128 + (c & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async();
           }
-          unsigned char* v = ring + (f % kStages) * kTileBytes;
-          for (int e = row; e < (r1 - r0) * (D / 8); e += 128) {
-            const int r = r0 + e / (D / 8), c = e % (D / 8);
-            *reinterpret_cast<uint4*>(v + (c >> 3) * (kTileRows * 128) + r * 128 + (c & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async();
         }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars.p[t]);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bars.p[t]);
-    }
-    if (ok && me.tiles > 0) {
-      ok = pre_wait(bars, &bars.o[t], 0, a.status);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
-    if (ok) {
+      fill += 2 * tiles;
+      if (!ok) break;
+      if (mine > 0) {
+        ok = pre_wait(bars, &bars.o[t], used & 1, a.status);
+          if (!ok) break;
+        ++used;
+        tc_fence_after();
+      }
+      // A row without a visible key: nothing was summed, 0 whatever O holds.
       const float inv = inv_or_zero(l);
-      const bool live = row < me.rows;
-      const int64_t at = (doc.q0 + me.row0 + row) * a.q_heads + me.head;
+      const bool none = l == 0.f;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + at * D;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (me.tiles > 0) {
-          tmem_ld32(o_addr + 32 * c, o);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32], w[16];
+        if (mine > 0) {
+          tmem_ld32(o_addr + c, o);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0;
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (c == D - 32 && mine > 0) {
+          tc_fence_before();
+          mbar_arrive(&bars.o_empty[t]);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = none ? 0.f : __uint_as_float(o[2 * i]) * inv;
+          const float y = none ? 0.f : __uint_as_float(o[2 * i + 1]) * inv;
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+          w[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
         if (live) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // A row without a visible key: nothing was summed, 0 whatever O holds.
-              const float x = l == 0.f ? 0.f : __uint_as_float(o[i + 2 * e]) * inv;
-              const float y = l == 0.f ? 0.f : __uint_as_float(o[i + 2 * e + 1]) * inv;
-              const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-              w[e] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(dst + c + 8 * i) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
       }
       if (live && a.lse != nullptr) a.lse[at] = row_lse(m, l);
@@ -603,7 +770,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   __syncwarp();  // the issuing lanes rejoin their warps
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == kProducts) tmem_dealloc(tmem, 512);
 }
 
 // [rows, heads, d] bf16 with a row stride, boxes of 64 columns x 1 head x 128
