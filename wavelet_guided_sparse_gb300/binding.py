@@ -8,6 +8,7 @@ the library has not been built, :func:`lib` raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -544,95 +545,116 @@ def alloc_paged_cache(n_pages: int, kv_heads: int, page_size: int, head_dim: int
     return {n: torch.empty(shape, dtype=dtype, device=device) for n in ("K", "V")}
 
 
-class _Call:
-    """Device and stream of one call: every tensor must live on one device,
-    which becomes the current one for the call (streams and launches belong to
-    a device); outputs are allocated with the call's stream current, so the
-    allocator knows which stream uses them first."""
+def _raw_stream(device: torch.device, stream) -> int:
+    """The stream a call runs on: the given one, which must belong to the
+    tensors' device, or that device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, tensors on {device}")
+    return stream.cuda_stream
 
-    def __init__(self, first: torch.Tensor, stream):
-        self.device = first.device
-        if self.device.type != "cuda":
+
+class _On:
+    """Makes the tensors' device (and a given stream) current for a call, when
+    they are not already: launches belong to the current device, and outputs
+    must be allocated for the stream that writes them."""
+
+    __slots__ = ("ctx",)
+
+    def __init__(self, t: torch.Tensor, stream):
+        if not t.is_cuda:
             raise ValueError("expected CUDA tensors")
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"stream is on {stream.device}, tensors on {self.device}")
-        self.stream = torch.cuda.current_stream(self.device) if stream is None else stream
-        same = (torch.cuda.current_device() == self.device.index and
-                (stream is None or stream == torch.cuda.current_stream(self.device)))
-        self.ctx = None if same else torch.cuda.stream(self.stream)
+        self.ctx = None
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)
+        elif torch._C._cuda_getDevice() != t.device.index:
+            self.ctx = torch.cuda.device(t.device)
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return self
 
     def __exit__(self, *exc):
-        return None if self.ctx is None else self.ctx.__exit__(*exc)
-
-    @property
-    def handle(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
-
-    def need(self, t: torch.Tensor, name: str, shape, dtype) -> None:
-        """A contiguous tensor of this shape and type on the call's device."""
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, not {self.device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-
-    def rows(self, t: torch.Tensor, name: str, heads: int, d: int, dtype) -> int:
-        """A [rows, heads, d] tensor whose rows may lie apart; its row stride."""
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, not {self.device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-            raise ValueError(f"{name} must be [rows, {heads}, {d}], got {tuple(t.shape)}")
-        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-            raise ValueError(f"{name}: the heads of a row must be contiguous")
-        return t.stride(0) if t.shape[0] > 1 else heads * d
-
-    def out(self, t: Optional[torch.Tensor], name: str, shape, dtype) -> torch.Tensor:
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        self.need(t, name, shape, dtype)
-        return t
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
 
 
-def _page_dims(call: _Call, cache: dict, page_table: torch.Tensor, q_heads: int,
-               dtype) -> PageDims:
+def _need(t: torch.Tensor, name: str, shape: tuple, dtype, device) -> int:
+    """Address of a contiguous tensor of this shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _out(t: Optional[torch.Tensor], name: str, shape: tuple, dtype, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, shape, dtype, device)
+    return t
+
+
+def _row_stride(t: torch.Tensor, name: str, rows: int, heads: int, d: int, dtype, device) -> int:
+    """Row stride of a [rows, heads, d] tensor whose rows may lie apart."""
+    if t.shape != (rows, heads, d) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor {(rows, heads, d)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return s0 if rows > 1 else heads * d
+
+
+_DTYPES = {torch.bfloat16: WF_BF16, torch.float32: WF_F32}
+
+
+@functools.lru_cache(maxsize=256)
+def _page_dims(n_seqs, q_heads, kv_heads, head_dim, page_size, n_pages, table_pages, dtype):
+    """The dims struct of these sizes and its by-reference argument."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    d = PageDims(n_seqs, q_heads, kv_heads, head_dim, page_size, n_pages, table_pages,
+                 _DTYPES[dtype])
+    return d, ctypes.byref(d)
+
+
+@functools.lru_cache(maxsize=256)
+def _prefill_dims(rows_q, rows_k, docs, q_heads, kv_heads, head_dim, dtype):
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    d = PrefillDims(rows_q, rows_k, docs, q_heads, kv_heads, head_dim, _DTYPES[dtype])
+    return d, ctypes.byref(d)
+
+
+def _pages(cache: dict, page_table: torch.Tensor, dtype, device):
+    """Sizes and addresses of a cache's pages and of a page table."""
     k = cache["K"]
-    if k.dim() != 4 or page_table.dim() != 2:
+    shape = k.shape
+    if len(shape) != 4 or page_table.dim() != 2:
         raise ValueError("pages must be [n_pages, kv_heads, page_size, head_dim], "
                          "the page table [n_seqs, table_pages]")
-    call.need(k, "cache K", k.shape, dtype)
-    call.need(cache["V"], "cache V", k.shape, dtype)
-    call.need(page_table, "page_table", page_table.shape, torch.int32)
-    return PageDims(page_table.shape[0], q_heads, k.shape[1], k.shape[3], k.shape[2], k.shape[0],
-                    page_table.shape[1], dtype_code(dtype))
+    return (shape, page_table.shape, _need(k, "cache K", shape, dtype, device),
+            _need(cache["V"], "cache V", shape, dtype, device),
+            _need(page_table, "page_table", page_table.shape, torch.int32, device))
 
 
-def _attn_opts(call: _Call, causal, prefix, softcap, slopes, scale, n_seqs: int,
-               q_heads: int) -> AttnOpts:
-    if prefix is not None:
-        call.need(prefix, "prefix", (n_seqs,), torch.int32)
-    if slopes is not None:
-        call.need(slopes, "slopes", (q_heads,), torch.float32)
+def _attn_opts(causal, prefix, softcap, slopes, scale, n_seqs: int, q_heads: int,
+               device) -> AttnOpts:
     if scale is not None and scale == 0.0:
         raise ValueError("scale must not be 0 (None means 1/sqrt(head_dim))")
-    return AttnOpts(0.0 if scale is None else scale, softcap, int(causal), _ptr(prefix),
-                    _ptr(slopes))
+    return AttnOpts(0.0 if scale is None else scale, softcap, 1 if causal else 0,
+                    None if prefix is None else _need(prefix, "prefix", (n_seqs,), torch.int32,
+                                                      device),
+                    None if slopes is None else _need(slopes, "slopes", (q_heads,), torch.float32,
+                                                      device))
 
 
-def _ws_args(call: _Call, ws: Optional[torch.Tensor]):
+def _ws_args(ws: Optional[torch.Tensor], device):
     if ws is None:
         return None, 0
-    call.need(ws, "workspace", (ws.numel(),), torch.uint8)
-    return _ptr(ws), ws.numel()
+    n = ws.numel()
+    return _need(ws, "workspace", (n,), torch.uint8, device), n
 
 
 def paged_append(k: torch.Tensor, v: torch.Tensor, cache: dict, page_table: torch.Tensor,
@@ -647,36 +669,36 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, cache: dict, page_table: torc
     (rope_inv_freq; None: no rotation), into cache {"K", "V"} in place.
     Returns {"Q": rotated queries} if q is given and {"K": rotated keys} if
     ``keep_keys``; ``out`` may supply those tensors."""
-    with _Call(k, stream) as call:
-        t, hkv, d = k.shape if k.dim() == 3 else (0, 0, 0)
-        ks = call.rows(k, "k", hkv, d, k.dtype)
-        vs = call.rows(v, "v", hkv, d, k.dtype)
-        hq = hkv if q is None else q.shape[1] if q.dim() == 3 else 0
-        qs = 0 if q is None else call.rows(q, "q", hq, d, k.dtype)
-        dims = _page_dims(call, cache, page_table, hq, k.dtype)
-        if v.shape[0] != t or (q is not None and q.shape[0] != t):
-            raise ValueError("q, k and v must have the same rows")
-        if dims.kv_heads != hkv or dims.head_dim != d:
-            raise ValueError("the cache's heads or head_dim differ from k's")
-        call.need(cu_rows, "cu_rows", (dims.n_seqs + 1,), torch.int32)
-        call.need(cache_len, "cache_len", (dims.n_seqs,), torch.int32)
-        if positions is not None:
-            call.need(positions, "positions", (t,), torch.int32)
+    with _On(k, stream):
+        dev, dt = k.device, k.dtype
+        shape, table, kp, vp, tp = _pages(cache, page_table, dt, dev)
+        t, (hkv, d), n = k.shape[0], (shape[1], shape[3]), table[0]
+        ks = _row_stride(k, "k", t, hkv, d, dt, dev)
+        vs = _row_stride(v, "v", t, hkv, d, dt, dev)
+        hq, qs, qp, qo, ko = hkv, 0, None, None, None
+        res = {} if out is None else dict(out)
+        if q is not None:
+            hq = q.shape[1] if q.dim() == 3 else 0
+            qs, qp = _row_stride(q, "q", t, hq, d, dt, dev), q.data_ptr()
+            res["Q"] = _out(res.get("Q"), "out Q", (t, hq, d), dt, dev)
+            qo = res["Q"].data_ptr()
+        if keep_keys:
+            res["K"] = _out(res.get("K"), "out K", (t, hkv, d), dt, dev)
+            ko = res["K"].data_ptr()
         freq, half = inv_freq, 0
         if freq is not None:
             half = len(freq)
             if not isinstance(freq, ctypes.Array):
                 freq = (ctypes.c_double * half)(*[float(x) for x in freq])
-        res = dict(out or {})
-        if q is not None:
-            res["Q"] = call.out(res.get("Q"), "out Q", (t, hq, d), k.dtype)
-        if keep_keys:
-            res["K"] = call.out(res.get("K"), "out K", (t, hkv, d), k.dtype)
+        wp, wn = _ws_args(ws, dev)
         _check("wf_paged_append", lib().wf_paged_append(
-            ctypes.byref(dims), t, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(cu_rows),
-            _ptr(cache_len), _ptr(positions), _ptr(page_table), freq, 2 * half, int(interleaved),
-            _ptr(cache["K"]), _ptr(cache["V"]), _ptr(res["Q"]) if q is not None else None,
-            _ptr(res["K"]) if keep_keys else None, *_ws_args(call, ws), call.handle))
+            _page_dims(n, hq, hkv, d, shape[2], shape[0], table[1], dt)[1], t, qp, qs,
+            k.data_ptr(), ks, v.data_ptr(), vs,
+            _need(cu_rows, "cu_rows", (n + 1,), torch.int32, dev),
+            _need(cache_len, "cache_len", (n,), torch.int32, dev),
+            None if positions is None else _need(positions, "positions", (t,), torch.int32, dev),
+            tp, freq, 2 * half, 1 if interleaved else 0, kp, vp, qo, ko, wp, wn,
+            _raw_stream(dev, stream)))
         return res
 
 
@@ -684,14 +706,15 @@ def alloc_paged_attn_workspace(q: torch.Tensor, cache: dict, page_table: torch.T
                                stream=None) -> torch.Tensor:
     """Workspace of paged_attn for these tensors' sizes (status word cleared);
     calls that may overlap need one each."""
-    with _Call(q, stream) as call:
-        dims = _page_dims(call, cache, page_table, q.shape[2], q.dtype)
+    with _On(q, stream):
+        shape, table = _pages(cache, page_table, q.dtype, q.device)[:2]
         n = ctypes.c_size_t(0)
         _check("wf_paged_attn_workspace_bytes", lib().wf_paged_attn_workspace_bytes(
-            ctypes.byref(dims), q.shape[1], ctypes.byref(n)))
+            _page_dims(table[0], q.shape[2], shape[1], shape[3], shape[2], shape[0], table[1],
+                       q.dtype)[1], q.shape[1], ctypes.byref(n)))
         ws = torch.empty(n.value, dtype=torch.uint8, device=q.device)
-        _check("wf_clear_device_status", lib().wf_clear_device_status(_ptr(ws), ws.numel(),
-                                                                      call.handle))
+        _check("wf_clear_device_status", lib().wf_clear_device_status(
+            ws.data_ptr(), ws.numel(), _raw_stream(q.device, stream)))
         return ws
 
 
@@ -704,22 +727,24 @@ def paged_attn(q: torch.Tensor, cache: dict, page_table: torch.Tensor, kv_len: t
     each sequence's paged cache {"K", "V"} of kv_len [n_seqs] rows; returns O
     like q (and lse [n_seqs, n_new, q_heads] fp32 if ``with_lse``).  ``ws``
     defaults to a fresh workspace."""
-    with _Call(q, stream) as call:
+    with _On(q, stream):
         if q.dim() != 4:
             raise ValueError("q must be [n_seqs, n_new, q_heads, head_dim]")
-        s, n_new, hq, d = q.shape
-        dims = _page_dims(call, cache, page_table, hq, q.dtype)
-        call.need(q, "q", (dims.n_seqs, n_new, hq, dims.head_dim), q.dtype)
-        call.need(kv_len, "kv_len", (s,), torch.int32)
-        opts = _attn_opts(call, causal, prefix, softcap, slopes, scale, s, hq)
+        dev, dt = q.device, q.dtype
+        shape, table, kp, vp, tp = _pages(cache, page_table, dt, dev)
+        n, n_new, hq, d = q.shape
+        qp = _need(q, "q", (table[0], n_new, hq, shape[3]), dt, dev)
+        opts = _attn_opts(causal, prefix, softcap, slopes, scale, n, hq, dev)
         if ws is None:
-            ws = alloc_paged_attn_workspace(q, cache, page_table, call.stream)
-        o = call.out(out, "out", (s, n_new, hq, d), q.dtype)
-        lse = call.out(None, "lse", (s, n_new, hq), torch.float32) if with_lse else None
+            ws = alloc_paged_attn_workspace(q, cache, page_table, stream)
+        wp, wn = _ws_args(ws, dev)
+        o = _out(out, "out", (n, n_new, hq, d), dt, dev)
+        lse = torch.empty((n, n_new, hq), dtype=torch.float32, device=dev) if with_lse else None
         _check("wf_paged_attn", lib().wf_paged_attn(
-            ctypes.byref(dims), ctypes.byref(opts), n_new, _ptr(q), _ptr(cache["K"]),
-            _ptr(cache["V"]), _ptr(page_table), _ptr(kv_len), _ptr(o), _ptr(lse),
-            *_ws_args(call, ws), call.handle))
+            _page_dims(n, hq, shape[1], d, shape[2], shape[0], table[1], dt)[1],
+            ctypes.byref(opts), n_new, qp, kp, vp, tp,
+            _need(kv_len, "kv_len", (n,), torch.int32, dev), o.data_ptr(),
+            None if lse is None else lse.data_ptr(), wp, wn, _raw_stream(dev, stream)))
         return (o, lse) if with_lse else o
 
 
@@ -733,27 +758,26 @@ def prefill_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.
     kv_heads, d], sequence s in rows cu_q[s] .. cu_q[s+1] and keys cu_k[s] ..
     cu_k[s+1] (cu_k defaults to cu_q); returns O like q (and lse [T, q_heads]
     fp32 if ``with_lse``).  Rows behind the last sequence are not written."""
-    with _Call(q, stream) as call:
+    with _On(q, stream):
         if q.dim() != 3 or k.dim() != 3:
             raise ValueError("q, k and v must be [rows, heads, head_dim]")
+        dev, dt = q.device, q.dtype
         t, hq, d = q.shape
-        hkv = k.shape[1]
-        qs = call.rows(q, "q", hq, d, q.dtype)
-        ks = call.rows(k, "k", hkv, d, q.dtype)
-        vs = call.rows(v, "v", hkv, d, q.dtype)
-        if v.shape[0] != k.shape[0]:
-            raise ValueError("k and v must have the same rows")
+        tk, hkv = k.shape[0], k.shape[1]
+        qs = _row_stride(q, "q", t, hq, d, dt, dev)
+        ks = _row_stride(k, "k", tk, hkv, d, dt, dev)
+        vs = _row_stride(v, "v", tk, hkv, d, dt, dev)
         docs = cu_q.numel() - 1
-        call.need(cu_q, "cu_q", (docs + 1,), torch.int32)
-        cu_k = cu_q if cu_k is None else cu_k
-        call.need(cu_k, "cu_k", (docs + 1,), torch.int32)
-        dims = PrefillDims(t, k.shape[0], docs, hq, hkv, d, dtype_code(q.dtype))
-        opts = _attn_opts(call, causal, prefix, softcap, slopes, scale, docs, hq)
-        o = call.out(out, "out", (t, hq, d), q.dtype)
-        lse = call.out(None, "lse", (t, hq), torch.float32) if with_lse else None
+        cq = _need(cu_q, "cu_q", (docs + 1,), torch.int32, dev)
+        ck = cq if cu_k is None else _need(cu_k, "cu_k", (docs + 1,), torch.int32, dev)
+        opts = _attn_opts(causal, prefix, softcap, slopes, scale, docs, hq, dev)
+        o = _out(out, "out", (t, hq, d), dt, dev)
+        lse = torch.empty((t, hq), dtype=torch.float32, device=dev) if with_lse else None
+        wp, wn = _ws_args(ws, dev)
         _check("wf_prefill_attn", lib().wf_prefill_attn(
-            ctypes.byref(dims), ctypes.byref(opts), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
-            _ptr(cu_q), _ptr(cu_k), _ptr(o), _ptr(lse), *_ws_args(call, ws), call.handle))
+            _prefill_dims(t, tk, docs, hq, hkv, d, dt)[1], ctypes.byref(opts), q.data_ptr(), qs,
+            k.data_ptr(), ks, v.data_ptr(), vs, cq, ck, o.data_ptr(),
+            None if lse is None else lse.data_ptr(), wp, wn, _raw_stream(dev, stream)))
         return (o, lse) if with_lse else o
 
 
