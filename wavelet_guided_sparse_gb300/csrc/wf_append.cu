@@ -31,6 +31,7 @@ namespace {
 struct AppendParams {
   AppendArgs a;
   RopeTurns turns;
+  int page_shift;  // log2 page_size
 };
 
 // The sequence of row t: the last s < n_seqs with cu[s] <= t, or -1 when t
@@ -77,21 +78,29 @@ struct TokenInfo {
 };
 
 template <typename T, int D, int ITERS>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, ITERS == 1 ? 6 : 4)
+    append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int V = Elem<T>::kPer16B;     // elements per chunk
   constexpr int C2 = D / (2 * V);         // chunk pairs per line
   constexpr int LANES = kThreads / C2;    // lines per pass
   constexpr int LINES = LANES * ITERS;    // lines per block
-  extern __shared__ float2 s_cs[];        // [tokens][rotary_dim / 2] cosine, sine
+  // Cosines and sines of the block's rows, two pairs a float4: those of chunk
+  // pair c lie C2 apart, so that the threads of a line read side by side.
+  extern __shared__ float4 s_cs[];        // [tokens][V / 2][C2]
   __shared__ TokenInfo s_tok[LINES + 1];
   const AppendArgs& a = p.a;
   const int qh = a.q != nullptr ? a.q_heads : 0;
   const int per_row = qh + 2 * a.kv_heads;
   const int64_t total = static_cast<int64_t>(a.rows) * per_row;
   const int64_t line0 = static_cast<int64_t>(blockIdx.x) * LINES;
-  const int t0 = static_cast<int>(line0 / per_row);
-  const int64_t last = min(line0 + LINES, total) - 1;
-  const int n_tok = static_cast<int>(last / per_row) - t0 + 1;
+  // Row and line within it of the block's first line; every other line of the
+  // block is a 32-bit step away.
+  const int t0 = line0 >> 32 == 0
+                     ? static_cast<int>(static_cast<uint32_t>(line0) / static_cast<uint32_t>(per_row))
+                     : static_cast<int>(line0 / per_row);
+  const uint32_t rest = static_cast<uint32_t>(line0 - static_cast<int64_t>(t0) * per_row);
+  const int lines = static_cast<int>(min(static_cast<int64_t>(LINES), total - line0));
+  const int n_tok = static_cast<int>((rest + lines - 1) / static_cast<uint32_t>(per_row)) + 1;
   const int c = threadIdx.x % C2;
   const int rot_pairs = a.rotary_dim / (2 * V);  // rotated chunk pairs per line
   // The two chunks of this thread: halves (c, c + r/2V), else neighbours.
@@ -101,12 +110,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const int cb = halves ? c + rot_pairs : 2 * c + 1;
 
   uint4 xa[ITERS], xb[ITERS];
+  int tok[ITERS], head[ITERS];  // row within the block, line within the row (-1: none)
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
-    const int64_t line = line0 + i * LANES + threadIdx.x / C2;
-    if (line < total) {
-      const int64_t t = line / per_row;
-      const int h = static_cast<int>(line - t * per_row);
+    const int line = i * LANES + threadIdx.x / C2;
+    const uint32_t at = rest + line;
+    tok[i] = static_cast<int>(at / static_cast<uint32_t>(per_row));
+    head[i] = line < lines ? static_cast<int>(at) - tok[i] * per_row : -1;
+    if (line < lines) {
+      const int64_t t = t0 + tok[i];
+      const int h = head[i];
       const T* src = h < qh ? static_cast<const T*>(a.q) + t * a.q_stride + h * D
                      : h < qh + a.kv_heads
                          ? static_cast<const T*>(a.k) + t * a.k_stride + (h - qh) * D
@@ -125,12 +138,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         info.live = 1;
         const int64_t n = static_cast<int64_t>(__ldg(a.cache_len + s)) + (t - __ldg(a.cu_rows + s));
         info.pos = a.positions != nullptr ? __ldg(a.positions + t) : static_cast<int32_t>(n);
-        const int64_t slot = n / a.page_size;
+        const int64_t slot = n >> p.page_shift;
         int page = -1;
         if (n >= 0 && slot < a.table_pages)
           page = __ldg(a.table + static_cast<int64_t>(s) * a.table_pages + slot);
         if (page >= 0 && page < a.n_pages)
-          info.line = static_cast<int64_t>(page) * a.kv_heads * a.page_size + (n % a.page_size);
+          info.line = static_cast<int64_t>(page) * a.kv_heads * a.page_size +
+                      (n & (a.page_size - 1));
         else
           raise_flag(a.status, WF_DEV_BAD_INDEX);
       }
@@ -146,40 +160,48 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(s_tok[i].pos)) * p.turns.f[j]);
     float sn, cs;
     sincospif(static_cast<float>(frac) * 0x1p-63f, &sn, &cs);
-    s_cs[e] = make_float2(cs, sn);
+    reinterpret_cast<float2*>(s_cs + (i * (V / 2) + (j % V) / 2) * C2 + j / V)[j % 2] =
+        make_float2(cs, sn);
   }
   __syncthreads();
 
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
-    const int64_t line = line0 + i * LANES + threadIdx.x / C2;
-    if (line >= total) continue;
-    const int64_t t = line / per_row;
-    int h = static_cast<int>(line - t * per_row);
-    const TokenInfo info = s_tok[t - t0];
+    if (head[i] < 0) continue;
+    const int64_t t = t0 + tok[i];
+    int h = head[i];
+    const TokenInfo info = s_tok[tok[i]];
     if (!info.live) continue;
     uint4 ya = xa[i], yb = xb[i];
     if (rotate && h < qh + a.kv_heads) {
       float fa[V], fb[V];
       widen16(ya, static_cast<const T*>(nullptr), fa);
       widen16(yb, static_cast<const T*>(nullptr), fb);
-      const float2* cs = s_cs + (t - t0) * half + c * V;
+      const float4* cs = s_cs + tok[i] * (V / 2) * C2 + c;
       if (halves) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float x = fa[e], y = fb[e];
-          fa[e] = x * cs[e].x - y * cs[e].y;
-          fb[e] = x * cs[e].y + y * cs[e].x;
+        for (int e = 0; e < V; e += 2) {
+          const float4 w = cs[e / 2 * C2];
+          const float x0 = fa[e], y0 = fb[e], x1 = fa[e + 1], y1 = fb[e + 1];
+          fa[e] = x0 * w.x - y0 * w.y;
+          fb[e] = x0 * w.y + y0 * w.x;
+          fa[e + 1] = x1 * w.z - y1 * w.w;
+          fb[e + 1] = x1 * w.w + y1 * w.z;
         }
       } else {
+        // Pairs 0 .. V/2 - 1 of the thread lie in chunk a, the rest in b.
+        const auto turn = [](float& x, float& y, float cs, float sn) {
+          const float u = x;
+          x = u * cs - y * sn;
+          y = u * sn + y * cs;
+        };
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
-          const float2 w0 = cs[e / 2], w1 = cs[V / 2 + e / 2];
-          const float x0 = fa[e], x1 = fb[e];
-          fa[e] = x0 * w0.x - fa[e + 1] * w0.y;
-          fa[e + 1] = x0 * w0.y + fa[e + 1] * w0.x;
-          fb[e] = x1 * w1.x - fb[e + 1] * w1.y;
-          fb[e + 1] = x1 * w1.y + fb[e + 1] * w1.x;
+          const float4 w = cs[e / 2 * C2];
+          float* f = e < V / 2 ? fa : fb;
+          const int o = 2 * (e % (V / 2));
+          turn(f[o], f[o + 1], w.x, w.y);
+          turn(f[o + 2], f[o + 3], w.z, w.w);
         }
       }
       ya = pack16<T>(fa);
@@ -212,7 +234,7 @@ cudaError_t launch_iters(const AppendParams& p, cudaStream_t stream) {
   const int per_row = (p.a.q != nullptr ? p.a.q_heads : 0) + 2 * p.a.kv_heads;
   const int64_t total = static_cast<int64_t>(p.a.rows) * per_row;
   const size_t tokens = (LINES - 1 + per_row - 1) / per_row + 1;
-  const size_t smem = tokens * (p.a.rotary_dim / 2) * sizeof(float2);
+  const size_t smem = p.a.rotary_dim > 0 ? tokens * (D / 2) * sizeof(float2) : 0;
   const cudaError_t e = ensure_max_smem<append_kernel<T, D, ITERS>>();
   if (e != cudaSuccess) return e;
   append_kernel<T, D, ITERS>
@@ -236,6 +258,8 @@ cudaError_t launch_append(const AppendArgs& a, const RopeTurns& turns, cudaStrea
   AppendParams p;
   p.a = a;
   p.turns = turns;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
   if (a.dtype == WF_BF16) {
     if (a.head_dim == 128) return launch_typed<__nv_bfloat16, 128>(p, stream);
     return launch_typed<__nv_bfloat16, 64>(p, stream);
