@@ -157,6 +157,12 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
                               __popc(live) * box_bytes + (first ? rows * D * 2 : 0));
       }
       __syncwarp();
+      if (page >= 0) {
+        const int y = (page * a.kv_heads + kvh) * a.page_size + (key & (a.page_size - 1));
+        tma_load_2d(ring + st * kStageBytes + which * kTileBytes + kb * (KT * 128) +
+                        sub * box_bytes,
+                    map, kb * 64, y, &bars.full[st]);
+      }
       if (first) {
         const int i0 = row0 / g, i1 = (row0 + rows - 1) / g;
         for (int i = i0 + lane; i <= i1; i += 32) {
@@ -166,12 +172,6 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
           bulk_g2s(s_q + (r0 - row0) * D, static_cast<const __nv_bfloat16*>(a.q) + from * D,
                    (r1 - r0) * D * 2, &bars.full[st]);
         }
-      }
-      if (page >= 0) {
-        const int y = (page * a.kv_heads + kvh) * a.page_size + (key & (a.page_size - 1));
-        tma_load_2d(ring + st * kStageBytes + which * kTileBytes + kb * (KT * 128) +
-                        sub * box_bytes,
-                    map, kb * 64, y, &bars.full[st]);
       }
       ++fill;
       if (++st == kStages) {
