@@ -87,7 +87,9 @@ struct Item {
 };
 
 struct PreBarriers {
-  uint64_t full[8], empty[8];  // ring stages
+  uint64_t full[8];            // ring stages
+  uint64_t done[8];            // steps (below) whose stages are free again: at most
+                               // five lie between a copy's wait and the products
   uint64_t q[2], q_empty[2];   // query tiles in shared memory
   uint64_t s[2], p[2];         // scores ready; weights ready
   uint64_t o[2], o_empty[2];   // output finished; read
@@ -341,10 +343,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&bars.full[i], 1);
-      mbar_init(&bars.empty[i], 1);
-    }
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars.full[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&bars.done[i], 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars.q[t], 1);
       mbar_init(&bars.q_empty[t], 1);
@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     } else if (warp == kCopies) {
       // ---- copies
       bool ok = true;
-      uint32_t used[2] = {0, 0}, fills = 0, parity = 1;
+      uint32_t used[2] = {0, 0}, fills = 0, steps = 0;
+      uint32_t step_of[kStages] = {};  // the step that frees each stage
       int st = 0;
       for (uint32_t k = 0; ok; ++k) {
         ok = pre_wait(bars, &bars.item, k & 1, a.status);
@@ -435,8 +436,16 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         const int tiles = max(it.qt[0].tiles, it.qt[1].tiles);
         for (int f = 0; f < 2 * tiles && ok; ++f) {
-          if (fills >= kStages) ok = pre_wait(bars, &bars.empty[st], parity, a.status, 100);
+          if (fills >= kStages) {
+            uint32_t r = 0;
+#pragma unroll
+            for (int i = 0; i < kStages; ++i) r = i == st ? step_of[i] : r;
+            ok = pre_wait(bars, &bars.done[r & 7], (r >> 3) & 1, a.status, 100);
+          }
           if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < kStages; ++i)
+            if (i == st) step_of[i] = steps + (f > 0 ? (f - 1) >> 1 : 0);
           if (leader) {
             unsigned char* dst = ring + st * kTileBytes;
             mbar_arrive_expect_tx(&bars.full[st], kTileBytes);
@@ -445,11 +454,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                           it.k0 + (tiles - 1 - (f >> 1)) * kTileRows, &bars.full[st]);
           }
           ++fills;
-          if (++st == kStages) {
-            st = 0;
-            parity ^= 1;
-          }
+          if (++st == kStages) st = 0;
         }
+        steps += tiles;
         __syncwarp();
         if (leader) mbar_arrive(&bars.item_empty);
       }
@@ -460,8 +467,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           mbar_wait_bounded(&bars.full[f % kStages], (f / kStages) & 1, a.status);
       }
     } else if (warp == kProducts) {
-      // ---- products: the whole warp walks the loop (uniform addresses and
-      // descriptors), one elected lane issues
+      // ---- products: the whole warp walks the loop, one elected lane issues.
+      // A step is one key tile j: each query tile's product with V_j, then its
+      // scores of K_{j-1} (before an item's first step, those of its first key
+      // tile).  One arrival a step frees its stages: an arrival costs the
+      // issuing warp 130 cycles.
       bool ok = true;
       constexpr uint32_t kRowDesc = umma_idesc_bf16(kTileRows, D) | (1u << 16);  // B: N-major
       const uint64_t q_desc[2] = {umma_desc_sw128(smem_u32(smem)),
@@ -499,9 +509,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           }
         }
       };
-      const auto release = [&](int st) {
-        if (leader) umma_commit(&bars.empty[st]);
-      };
       // Stage and parity of the ring's fills in order: K_0 V_0 K_1 V_1 ...
       int st = 0;
       uint32_t parity = 0;
@@ -513,6 +520,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       };
       uint32_t used[2] = {0, 0};  // items with tiles of query tile t so far
       uint32_t np[2] = {0, 0};    // key tiles of query tile t so far
+      uint32_t step = 0;          // steps so far
       for (uint32_t k = 0; ok; ++k) {
         ok = pre_wait(bars, &bars.item, k & 1, a.status);
         if (!ok) break;
@@ -536,7 +544,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (ok && nt[t] == tiles) scores(t, tiles - 1, st);
-        if (ok) release(st);
         advance();
         for (int j = tiles - 1; j >= 0 && ok; --j) {
           const int vs = st;
@@ -563,10 +570,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             }
             if (ok && j > 0 && j - 1 < nt[t]) scores(t, j - 1, ks);
           }
-          if (ok) {
-            release(vs);
-            if (j > 0) release(ks);
-          }
+          if (ok && leader) umma_commit(&bars.done[step & 7]);
+          ++step;
         }
         used[0] += nt[0] > 0;
         used[1] += nt[1] > 0;
