@@ -294,6 +294,21 @@ def test_prefill(case):
     run_prefill(*case)
 
 
+@pytest.mark.parametrize("cap,bias,spread", [(5.0, False, 4.0), (5.0, True, 4.0), (1.0, True, 0.5),
+                                             (200.0, False, 8.0)])
+def test_prefill_caps_far_into_their_bend(cap, bias, spread):
+    # Scores up to many times the cap, some rows small and some large at once.
+    d, n, h = 128, 300, 4
+    q, k, v = (randn((n, h, d), BF, s) for s in (1, 2, 3))
+    q = (q.float() * torch.linspace(0.01, spread, n, device="cuda")[:, None, None]).to(BF)
+    slopes = slope_list(h) if bias else None
+    o, lse = bd.prefill_attn(q, k, v, offsets([n]), softcap=cap, slopes=slopes, with_lse=True)
+    ro, rl, ob, lb = attend(f64(q), f64(k), f64(v), BF, True, 0, cap,
+                            None if slopes is None else slopes.cpu().numpy())
+    check(f64(lse), rl, lb, "lse")
+    check(f64(o), ro, ob, "O")
+
+
 def test_prefill_sequences_never_see_each_other():
     # The middle sequence holds NaN and infinities in its keys and values.
     d, h, lens = 128, 2, [100, 60, 77]

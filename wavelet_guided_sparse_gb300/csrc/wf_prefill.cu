@@ -224,46 +224,88 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// What maps a query row's scores, kept over an item (pairs: both lanes of an
+// f32x2 operation).
+struct ScoreMap {
+  uint64_t scale, cap;   // scale / cap (or scale log2 e), cap log2 e
+  uint64_t steps[16];    // slope times (2 i, 2 i + 1)
+  float slope;           // slope log2 e
+};
+
 // z = [cap tanh(s / cap) or scale s] - slope |d0 - i|, in the log2 domain,
 // for the keys i = 0..31 of a chunk; d0 = position minus the chunk's first
 // key.  `side`: every row of the warp lies behind the chunk (1: the distance
 // is linear in i), before it (-1), or neither (0).
 //
-// cap tanh(x) = cap - 2 cap / (1 + e^(2x)).  The special-function unit is what
-// bounds these variants (two powers of two and a reciprocal a score), so two
-// scores share one reciprocal: 1/a = b / (a b).  With 2x log2 e clamped at 60
-// the product stays finite, and 2 / (1 + 2^60) is far below fp32's step at 1.
-template <bool CAP, bool BIAS>
-__device__ __forceinline__ void map_scores(float* s, const ScoreOpts& o, float slope, float d0,
-                                           int side) {
-  const float step = side > 0 ? slope : -slope;
-  const float base = (CAP ? o.cap : 0.f) - (BIAS ? step * d0 : 0.f);
+// tanh: while every |x| of the warp's chunk is at most 3/4, the usual case
+// for scores, a polynomial on the FMA pipe, two scores an operation: x + x^3
+// P(x^2), P of degree 4 fitted by Chebyshev interpolation, error below 2^-23.
+// Otherwise tanh(x) = 1 - 2 / (1 + e^(2x)) on the special-function unit, two
+// scores sharing one reciprocal (1/a = b / (a b)); with 2x log2 e clamped at
+// 60 the product stays finite, and 2 / (1 + 2^60) is far below fp32's step
+// at 1.
+template <bool CAP, bool BIAS, bool LINEAR>
+__device__ __forceinline__ void map_chunk(float* s, const ScoreOpts& o, const ScoreMap& c,
+                                          float d0, float sg) {
+  const float base = BIAS && LINEAR ? -sg * c.slope * d0 : 0.f;
+  const uint64_t base2 = pack2(base, base), sign2 = pack2(sg, sg);
+  const auto bias = [&](int i) {  // of keys i, i + 1
+    if (LINEAR) return fma2(c.steps[i / 2], sign2, base2);
+    return pack2(-c.slope * fabsf(d0 - static_cast<float>(i)),
+                 -c.slope * fabsf(d0 - static_cast<float>(i + 1)));
+  };
+  if (!CAP) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      unpack2(fma2(pack2(s[i], s[i + 1]), c.scale, bias(i)), s[i], s[i + 1]);
+    return;
+  }
+  float big0 = 0.f, big1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    big0 = fmaxf(big0, fmaxf(fabsf(s[i]), fabsf(s[i + 1])));
+    big1 = fmaxf(big1, fmaxf(fabsf(s[i + 2]), fabsf(s[i + 3])));
+  }
+  if (__all_sync(0xffffffffu, fmaxf(big0, big1) * o.scale <= 0.75f)) {
+    constexpr float kP[5] = {-0.333329678f, 0.133255154f, -0.053349819f, 0.0195937864f, -0.00472395215f};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const uint64_t x = mul2(pack2(s[i], s[i + 1]), c.scale), u = mul2(x, x);
+      uint64_t q = pack2(kP[4], kP[4]);
+#pragma unroll
+      for (int e = 3; e >= 0; --e) q = fma2(q, u, pack2(kP[e], kP[e]));
+      const uint64_t t = fma2(mul2(x, u), q, x);
+      unpack2(BIAS ? fma2(t, c.cap, bias(i)) : mul2(t, c.cap), s[i], s[i + 1]);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
-    float add[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (!BIAS)
-        add[e] = base;
-      else if (side != 0)
-        add[e] = fmaf(step, static_cast<float>(i + e), base);
-      else
-        add[e] = fmaf(-slope, fabsf(d0 - static_cast<float>(i + e)), CAP ? o.cap : 0.f);
+    float add0 = o.cap, add1 = o.cap;
+    if (BIAS) {
+      float x, y;
+      unpack2(bias(i), x, y);
+      add0 += x;
+      add1 += y;
     }
-    if (CAP) {
-      const float k = o.scale * (2.f * kLog2e);
-      const float a = 1.f + fast_exp2(fminf(s[i] * k, 60.f));
-      const float b = 1.f + fast_exp2(fminf(s[i + 1] * k, 60.f));
-      float r;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
-      r *= -2.f * o.cap;
-      s[i] = fmaf(r, b, add[0]);
-      s[i + 1] = fmaf(r, a, add[1]);
-    } else {
-      s[i] = fmaf(s[i], o.scale, add[0]);
-      s[i + 1] = fmaf(s[i + 1], o.scale, add[1]);
-    }
+    const float k = o.scale * (2.f * kLog2e);
+    const float a = 1.f + fast_exp2(fminf(s[i] * k, 60.f));
+    const float b = 1.f + fast_exp2(fminf(s[i + 1] * k, 60.f));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+    r *= -2.f * o.cap;
+    s[i] = fmaf(r, b, add0);
+    s[i + 1] = fmaf(r, a, add1);
   }
+}
+// One branch a chunk, none between its scores.
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ void map_scores(float* s, const ScoreOpts& o, const ScoreMap& c,
+                                           float d0, int side) {
+  if (!BIAS || side != 0)
+    map_chunk<CAP, BIAS, true>(s, o, c, d0, side > 0 ? 1.f : -1.f);
+  else
+    map_chunk<CAP, BIAS, false>(s, o, c, d0, 0.f);
 }
 
 // Claims a block of this grid that has not started (cluster launch control):
@@ -614,7 +656,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.item_empty);
       if (!live_item) break;
-      const float slope = BIAS ? __ldg(p.o.slopes + max(0, min(head, a.q_heads - 1))) * kLog2e : 0.f;
+      ScoreMap map;
+      if (CAP || BIAS) {
+        map.scale = pack2(p.o.scale, p.o.scale);
+        map.cap = pack2(p.o.cap, p.o.cap);
+        map.slope = BIAS ? __ldg(p.o.slopes + max(0, min(head, a.q_heads - 1))) * kLog2e : 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          map.steps[i] = pack2(map.slope * (2 * i), map.slope * (2 * i + 1));
+      }
       float m = -INFINITY, l = 0.f;
       // From the last key tile (under the causal mask the nearest keys, whose
       // scores a distance bias leaves highest) to the first.
@@ -643,7 +693,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             const int side = !BIAS ? 1
                              : __all_sync(0xffffffffu, d0 >= 31.f) ? 1
                              : __all_sync(0xffffffffu, d0 <= 0.f)  ? -1 : 0;
-            map_scores<CAP, BIAS>(s, p.o, slope, d0, side);
+            map_scores<CAP, BIAS>(s, p.o, map, d0, side);
           }
           if (edge) {
 #pragma unroll
