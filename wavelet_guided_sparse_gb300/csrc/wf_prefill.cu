@@ -227,7 +227,8 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // What maps a query row's scores, kept over an item (pairs: both lanes of an
 // f32x2 operation).
 struct ScoreMap {
-  uint64_t scale, cap;   // scale / cap (or scale log2 e), cap log2 e
+  uint64_t scale;        // no cap: scale log2 e
+  uint64_t bend[5];      // cap: coefficients of cap log2 e tanh(s scale / cap) / s in s^2
   uint64_t steps[16];    // slope times (2 i, 2 i + 1)
   float slope;           // slope log2 e
 };
@@ -237,9 +238,11 @@ struct ScoreMap {
 // key.  `side`: every row of the warp lies behind the chunk (1: the distance
 // is linear in i), before it (-1), or neither (0).
 //
-// tanh: while every |x| of the warp's chunk is at most 3/4, the usual case
-// for scores, a polynomial on the FMA pipe, two scores an operation: x + x^3
-// P(x^2), P of degree 4 fitted by Chebyshev interpolation, error below 2^-23.
+// The cap: while every |s scale / cap| of the warp's chunk is at most 1/2, the
+// usual case, an odd polynomial on the FMA pipe, two scores an operation:
+// tanh(x) / x of degree 4 in x^2, fitted by Chebyshev interpolation on [0,
+// 1/4] (error of tanh below 2^-22 with the fp32 roundings), its coefficients
+// scaled so that it takes s itself.
 // Otherwise tanh(x) = 1 - 2 / (1 + e^(2x)) on the special-function unit, two
 // scores sharing one reciprocal (1/a = b / (a b)); with 2x log2 e clamped at
 // 60 the product stays finite, and 2 / (1 + 2^60) is far below fp32's step
@@ -266,16 +269,14 @@ __device__ __forceinline__ void map_chunk(float* s, const ScoreOpts& o, const Sc
     big0 = fmaxf(big0, fmaxf(fabsf(s[i]), fabsf(s[i + 1])));
     big1 = fmaxf(big1, fmaxf(fabsf(s[i + 2]), fabsf(s[i + 3])));
   }
-  if (__all_sync(0xffffffffu, fmaxf(big0, big1) * o.scale <= 0.75f)) {
-    constexpr float kP[5] = {-0.333329678f, 0.133255154f, -0.053349819f, 0.0195937864f, -0.00472395215f};
+  if (__all_sync(0xffffffffu, fmaxf(big0, big1) * o.scale <= 0.5f)) {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      const uint64_t x = mul2(pack2(s[i], s[i + 1]), c.scale), u = mul2(x, x);
-      uint64_t q = pack2(kP[4], kP[4]);
+      const uint64_t x = pack2(s[i], s[i + 1]), u = mul2(x, x);
+      uint64_t q = c.bend[4];
 #pragma unroll
-      for (int e = 3; e >= 0; --e) q = fma2(q, u, pack2(kP[e], kP[e]));
-      const uint64_t t = fma2(mul2(x, u), q, x);
-      unpack2(BIAS ? fma2(t, c.cap, bias(i)) : mul2(t, c.cap), s[i], s[i + 1]);
+      for (int e = 3; e >= 0; --e) q = fma2(q, u, c.bend[e]);
+      unpack2(BIAS ? fma2(x, q, bias(i)) : mul2(x, q), s[i], s[i + 1]);
     }
     return;
   }
@@ -659,7 +660,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       ScoreMap map;
       if (CAP || BIAS) {
         map.scale = pack2(p.o.scale, p.o.scale);
-        map.cap = pack2(p.o.cap, p.o.cap);
+        constexpr float kBend[5] = {1.f, -0.333330721f, 0.133248284f, -0.0529892407f, 0.0171413198f};
+        float unit = p.o.cap * p.o.scale;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+          map.bend[i] = pack2(kBend[i] * unit, kBend[i] * unit);
+          unit *= p.o.scale * p.o.scale;
+        }
         map.slope = BIAS ? __ldg(p.o.slopes + max(0, min(head, a.q_heads - 1))) * kLog2e : 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
