@@ -93,10 +93,10 @@ struct PreBarriers {
   uint64_t q[2], q_empty[2];   // query tiles in shared memory
   uint64_t s[2], p[2];         // scores ready; weights ready
   uint64_t o[2], o_empty[2];   // output finished; read
-  uint64_t item, item_empty;   // item published; read by every role
+  uint64_t item[2], item_empty[2];  // item published; read by every role
   uint64_t claim, drain;
   uint4 claimed;               // response of a claim
-  Item it;
+  Item it[2];
   uint32_t tmem;
   int abort;
 };
@@ -154,6 +154,10 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "%24,%25,%26,%27,%28,%29,%30,%31};" ::WF_I8(r, 0),
       WF_I8(r, 8), WF_I8(r, 16), WF_I8(r, 24), "r"(addr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st64(uint32_t addr, const uint32_t* r) {
+  tmem_st32(addr, r);
+  tmem_st32(addr + 32, r + 32);
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -396,8 +400,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       mbar_init(&bars.o[t], 1);
       mbar_init(&bars.o_empty[t], 128);
     }
-    mbar_init(&bars.item, 1);
-    mbar_init(&bars.item_empty, 10);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.item[i], 1);
+      mbar_init(&bars.item_empty[i], 10);
+    }
     mbar_init(&bars.claim, 1);
     mbar_init(&bars.drain, 1);
     bars.abort = 0;
@@ -426,8 +432,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       uint32_t claims = 0;
       DocCursor cursor = {0, 0};
       for (uint32_t k = 0; ok; ++k) {
-        // The last item has been read by all, and its copies are all issued.
-        if (k > 0) ok = pre_wait(bars, &bars.item_empty, (k - 1) & 1, a.status, 500);
+        // The item before the last one has been read by all.
+        if (k > 1) ok = pre_wait(bars, &bars.item_empty[k & 1], ((k >> 1) - 1) & 1, a.status, 200);
         if (!ok) break;
         Item it = {};
         // Blocks behind the last sequence's (the grid is sized for any split
@@ -447,8 +453,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (block < 0 || make_item(p, block, cursor, &it)) break;
         }
         if (leader) {
-          bars.it = it;
-          mbar_arrive(&bars.item);
+          bars.it[k & 1] = it;
+          mbar_arrive(&bars.item[k & 1]);
         }
         __syncwarp();
         if (!it.live) break;
@@ -460,9 +466,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       uint32_t step_of[kStages] = {};  // the step that frees each stage
       int st = 0;
       for (uint32_t k = 0; ok; ++k) {
-        ok = pre_wait(bars, &bars.item, k & 1, a.status);
+        ok = pre_wait(bars, &bars.item[k & 1], (k >> 1) & 1, a.status);
         if (!ok) break;
-        const Item it = bars.it;
+        const Item it = bars.it[k & 1];
+        __syncwarp();
+        if (leader) mbar_arrive(&bars.item_empty[k & 1]);
         if (!it.live) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -500,8 +508,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (++st == kStages) st = 0;
         }
         steps += tiles;
-        __syncwarp();
-        if (leader) mbar_arrive(&bars.item_empty);
       }
       if (!ok && leader) {  // nothing of this CTA's copies may land after it has gone
         for (int t = 0; t < 2; ++t)
@@ -565,13 +571,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       uint32_t np[2] = {0, 0};    // key tiles of query tile t so far
       uint32_t step = 0;          // steps so far
       for (uint32_t k = 0; ok; ++k) {
-        ok = pre_wait(bars, &bars.item, k & 1, a.status);
+        ok = pre_wait(bars, &bars.item[k & 1], (k >> 1) & 1, a.status);
         if (!ok) break;
-        const int live = bars.it.live;
-        const int end[2] = {bars.it.qt[0].end, bars.it.qt[1].end};
-        const int nt[2] = {bars.it.qt[0].tiles, bars.it.qt[1].tiles};
+        const Item& it = bars.it[k & 1];
+        const int live = it.live;
+        const int end[2] = {it.qt[0].end, it.qt[1].end};
+        const int nt[2] = {it.qt[0].tiles, it.qt[1].tiles};
         __syncwarp();
-        if (leader) mbar_arrive(&bars.item_empty);
+        if (leader) mbar_arrive(&bars.item_empty[k & 1]);
         if (!live) break;
         const int tiles = max(nt[0], nt[1]);
         if (tiles == 0) continue;
@@ -639,23 +646,24 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     uint32_t ns = 0, used = 0, fill = 0;  // key tiles, items with tiles, ring fills so far
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
-      ok = pre_wait(bars, &bars.item, k & 1, a.status);
+      ok = pre_wait(bars, &bars.item[k & 1], (k >> 1) & 1, a.status);
       if (!ok) break;
       // This thread's row: its place in the output, whether it exists (a row
       // outside the arrays is never written), its visible keys.
-      const int mine = bars.it.qt[t].tiles, end = bars.it.qt[t].end, n_k = bars.it.n_k;
-      const int tiles = max(bars.it.qt[0].tiles, bars.it.qt[1].tiles);
-      const int row_at = bars.it.qt[t].row0 + row, head = bars.it.qt[t].head;
-      const int64_t out_row = static_cast<int64_t>(bars.it.q0) + row_at;
-      const bool live =
-          row < bars.it.qt[t].rows && static_cast<uint64_t>(out_row) < static_cast<uint64_t>(a.rows_q) &&
-          static_cast<uint32_t>(head) < static_cast<uint32_t>(a.q_heads);
+      const Item& it = bars.it[k & 1];
+      const int mine = it.qt[t].tiles, end = it.qt[t].end, n_k = it.n_k;
+      const int tiles = max(it.qt[0].tiles, it.qt[1].tiles);
+      const int row_at = it.qt[t].row0 + row, head = it.qt[t].head, rows = it.qt[t].rows;
+      const int64_t out_row = static_cast<int64_t>(it.q0) + row_at;
+      const bool sound = static_cast<uint64_t>(out_row - row) + rows <=
+                             static_cast<uint64_t>(a.rows_q) &&
+                         static_cast<uint32_t>(head) < static_cast<uint32_t>(a.q_heads);
+      const bool live = row < rows && sound;
       const int64_t at = out_row * a.q_heads + head;
-      const int pos = bars.it.shift + row_at, live_item = bars.it.live;
-      const int limit =
-          live ? (p.o.causal ? min(n_k, max(pos + 1, bars.it.prefix)) : n_k) : end;
+      const int pos = it.shift + row_at, live_item = it.live;
+      const int limit = live ? (p.o.causal ? min(n_k, max(pos + 1, it.prefix)) : n_k) : end;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.item_empty);
+      if (lane == 0) mbar_arrive(&bars.item_empty[k & 1]);
       if (!live_item) break;
       ScoreMap map;
       if (CAP || BIAS) {
@@ -684,8 +692,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         // Two passes over the tile in chunks of CH scores, as rolled loops: with
         // the tile unrolled the code of the softmax groups would not stay in
         // the instruction caches, and every role, the products' warp first,
-        // would wait for its fetches.  First the maximum (with cap or bias
-        // the mapped scores go back in place) ...
+        // would wait for its fetches.  First the maximum (mapped or masked
+        // scores go back in place) ...
         constexpr int CH = CAP || BIAS ? 32 : 64;
         const int rel = limit - k0;
         const bool edge = __any_sync(0xffffffffu, rel < 128);
@@ -703,8 +711,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             map_scores<CAP, BIAS>(s, p.o, map, d0, side);
           }
           if (edge) {
+            // One bit a key: bits of a register become predicates eight at once.
 #pragma unroll
-            for (int i = 0; i < CH; ++i) s[i] = i < rel - c ? s[i] : -INFINITY;
+            for (int h = 0; h < CH; h += 32) {
+              const int n = rel - c - h;
+              const uint32_t seen = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                s[h + i] = (seen & (1u << i)) != 0 ? s[h + i] : -INFINITY;
+            }
+            if (!CAP && !BIAS) {
+              if (CH == 64) tmem_st64(s_addr + c, r); else tmem_st32(s_addr + c, r);
+            }
           }
 #pragma unroll
           for (int i = 0; i < CH; i += 4) {
@@ -713,7 +731,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           }
           if (CAP || BIAS) tmem_st32(s_addr + c, r);
         }
-        if (CAP || BIAS) tmem_wait_st();
+        if (CAP || BIAS || edge) tmem_wait_st();
         const float mt = fmaxf(mx0, mx1) * mul;
         if (j == mine - 1) {
           m = mt;
@@ -745,11 +763,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         for (int c = 0; c < 128; c += CH) {
           uint32_t r[CH], pk[CH / 2];
           if (CH == 64) tmem_ld64(s_addr + c, r); else tmem_ld32(s_addr + c, r);
-          if (!CAP && !BIAS && edge) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-              r[i] = i < rel - c ? r[i] : __float_as_uint(-INFINITY);
-          }
 #pragma unroll
           for (int i = 0; i < CH / 2; ++i) {
             float x, y;
@@ -795,13 +808,17 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         ++used;
         tc_fence_after();
       }
-      // A row without a visible key: nothing was summed, 0 whatever O holds.
+      // A row without a visible key has l = 0: its O, products of zeros, stays 0.
       const float inv = inv_or_zero(l);
-      const bool none = l == 0.f;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + at * D;
+      const uint64_t inv2 = pack2(inv, inv);
+      // Four lanes exchange 16-byte parts of their rows, so that a store covers
+      // 64 bytes of each of eight rows instead of 16 of 32.
+      const int row4 = row & ~3, part = lane & 3;
+      __nv_bfloat16* dst =
+          static_cast<__nv_bfloat16*>(a.o) + (at - part * static_cast<int64_t>(a.q_heads)) * D;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
-        uint32_t o[32], w[16];
+        uint32_t o[32], w[4][4];
         if (mine > 0) {
           tmem_ld32(o_addr + c, o);
         } else {
@@ -814,17 +831,31 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float x = none ? 0.f : __uint_as_float(o[2 * i]) * inv;
-          const float y = none ? 0.f : __uint_as_float(o[2 * i + 1]) * inv;
+          float x, y;
+          unpack2(mul2(pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), inv2), x, y);
           const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-          w[i] = *reinterpret_cast<const uint32_t*>(&b);
+          w[i / 4][i % 4] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        if (live) {
+        // w[j] of lane i becomes part i of the row of lane j (of the four).
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(dst + c + 8 * i) =
-                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int b = 1; b < 4; b <<= 1) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j & b) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool up = part & b;
+              const uint32_t got =
+                  __shfl_xor_sync(0xffffffffu, up ? w[j][e] : w[j | b][e], b);
+              if (up) w[j][e] = got; else w[j | b][e] = got;
+            }
+          }
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (sound && row4 + j < rows)
+            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(j) * a.q_heads * D + c + 8 * part) =
+                make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
       }
       if (live && a.lse != nullptr) a.lse[at] = row_lse(m, l);
     }
