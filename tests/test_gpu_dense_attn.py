@@ -189,6 +189,7 @@ PAGED = [
     (BF, 128, 16, 1, 16, [260], 1, True, None, 0.0, False),
     (BF, 128, 40, 1, 128, [513], 1, True, None, 0.0, False),         # 40 rows
     (BF, 64, 1, 1, 8, [3, 2], 8, True, None, 0.0, False),            # rows before any key
+    (BF, 128, 8, 2, 64, [200, 64, 33, 0], 64, True, [0, 64, 7, 0], 30.0, True),  # 4 blocks
     (F32, 64, 2, 2, 32, [1056], 32, False, None, 0.0, False),
     (F32, 128, 4, 1, 16, [1, 0, 333], 1, True, None, 30.0, True),
     (F32, 64, 9, 3, 8, [100, 41], 4, True, [60, 0], 0.0, False),
@@ -216,6 +217,40 @@ def test_paged_many_short_sequences():
 def test_paged_large_scores_and_scale():
     # Scores of some hundreds: one key carries the row; nothing overflows.
     run_paged(BF, 128, 4, 2, 16, [70, 300], 2, True, None, 0.0, False, scale=4.0)
+
+
+def test_paged_sequences_share_pages():
+    # A common beginning: the same pages in three tables, one page twice in one.
+    page, d, hkv = 16, 128, 2
+    cache = {n: randn((6, hkv, page, d), BF, s) for s, n in enumerate(("K", "V"))}
+    table = [[4, 0, 1], [4, 0, 2], [4, 4, 0]]
+    lens = [48, 37, 40]
+    q = randn((3, 1, 8, d), BF, 5, 2.0)
+    o = bd.paged_attn(q, cache, i32(table), i32(lens))
+    for i, n in enumerate(lens):
+        kk, vv = (f64(cache[x])[table[i]].transpose(0, 2, 1, 3).reshape(-1, hkv, d)[:n]
+                  for x in ("K", "V"))
+        ro, _, ob, _ = attend(f64(q[i]), kk, vv, BF, True)
+        check(f64(o[i]), ro, ob, f"O of sequence {i}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_append_and_attention_behind_the_first_2_to_31_elements(dtype):
+    # The pages in use lie past 2^31 elements of the cache.
+    page, d, hkv, hq, lens = 256, 128, 8, 16, [300, 70]
+    pages = 2 ** 31 // (page * d * hkv) + 8
+    cache = bd.alloc_paged_cache(pages, hkv, page, d, dtype, "cuda")
+    table = i32([[pages - 1, pages - 5], [pages - 3, 0]])
+    k, v = (randn((sum(lens), hkv, d), dtype, s) for s in (1, 2))
+    bd.paged_append(k, v, cache, table, offsets(lens), i32([0, 0]))
+    assert torch.equal(cache["K"][pages - 5, :, :44], k[256:300].transpose(0, 1))
+    q = randn((2, 1, hq, d), dtype, 3, 2.0)
+    o = bd.paged_attn(q, cache, table, i32(lens))
+    at = 0
+    for i, n in enumerate(lens):
+        ro, _, ob, _ = attend(f64(q[i]), f64(k[at:at + n]), f64(v[at:at + n]), dtype, True)
+        check(f64(o[i]), ro, ob, f"O of sequence {i}")
+        at += n
 
 
 def test_paged_bad_pages_and_lengths_are_flagged():
@@ -331,6 +366,44 @@ def test_prefill_keys_hidden_by_the_mask_may_hold_anything():
     check(f64(o[:150]), ro, ob, "rows that do not see them")
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (3, 1, 128), (8, 8, 64)])
+def test_prefill_many_short_sequences(hq, hkv, d):
+    # Several items a CTA, empty sequences among them.
+    lens = np.random.default_rng(hq).integers(0, 40, 300).tolist()
+    run_prefill(BF, d, hq, hkv, lens, lens, True, None, 0.0, False, extra=3)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_rows_behind_the_first_2_to_31_elements(dtype):
+    # A row stride of 2^17 elements: the last rows start past 2^31 elements.
+    n, d, doc = 16500, 64, 100
+    wide = torch.empty((n, 2 ** 17 // d, d), dtype=dtype, device="cuda")
+    q, k, v = wide[:, :4], wide[:, 4:6], wide[:, 6:8]
+    wide[:, :8] = randn((n, 8, d), dtype, 1)
+    assert (n - doc) * wide.stride(0) > 2 ** 31
+    o = bd.prefill_attn(q, k, v, offsets([doc] * (n // doc)))
+    for a in (0, n - doc):
+        ro, _, ob, _ = attend(f64(q[a:a + doc]), f64(k[a:a + doc]), f64(v[a:a + doc]), dtype, True)
+        check(f64(o[a:a + doc]), ro, ob, f"O of rows {a}..")
+
+
+@pytest.mark.parametrize("cap", [0.0, 1.0])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_visible_nan_shows_in_every_row_that_sees_it(dtype, cap):
+    n, d, at = 200, 64, 50
+    q, k, v = (randn((n, 2, d), dtype, s) for s in (1, 2, 3))
+    k[at] = math.nan
+    o, lse = bd.prefill_attn(q, k, v, offsets([n]), softcap=cap, with_lse=True)
+    assert o[at:].isnan().all() and lse[at:].isnan().all()
+    assert not o[:at].isnan().any() and not lse[:at].isnan().any()
+    table, pages = make_table([n], 16, 0)
+    cache = bd.alloc_paged_cache(pages, 2, 16, d, dtype, "cuda")
+    bd.paged_append(k, v, cache, table, offsets([n]), i32([0]))
+    for m in (at, n):
+        o, lse = bd.paged_attn(q[None, m - 1:m], cache, table, i32([m]), softcap=cap, with_lse=True)
+        assert o.isnan().all() == (m > at) and lse.isnan().all() == (m > at)
+
+
 @pytest.mark.parametrize("offs", [[0, 40, 20, 60], [0, 30, 90], [-5, 30]])
 def test_prefill_bad_offsets_are_flagged(offs):
     q, k, v = (randn((60, 1, 64), BF, s) for s in (1, 2, 3))
@@ -425,3 +498,79 @@ def test_streams_and_two_calls_at_once():
             outs.append(bd.paged_attn(q, cache, table, lens, stream=st))   # own workspaces
     torch.cuda.synchronize()
     assert all(torch.equal(ref, x) for x in outs)
+
+
+def test_two_captured_graphs_share_a_workspace():
+    # Replayed in turn (never at once): each leaves nothing the other minds.
+    runs = [run_paged(BF, 128, 8, 2, 16, lens, new, True, None, 0.0, False, seed=new)
+            for lens, new in (([900, 40], 1), ([33, 2000], 3))]
+    sizes = [r[2][4].numel() for r in runs]
+    ws = runs[int(sizes[1] > sizes[0])][2][4]
+    graphs = []
+    for o, _, (q, cache, table, lens, _) in runs:
+        out = torch.zeros_like(o)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            bd.paged_attn(q, cache, table, lens, ws, out=out)
+        graphs.append((graph, out, o))
+    for _ in range(3):
+        for graph, out, ref in graphs:
+            out.fill_(7.0)
+            graph.replay()
+            assert torch.equal(out, ref)
+
+
+def test_captured_prompt_replays_with_new_offsets():
+    h, d, n = 4, 128, 500
+    q, k, v = (randn((n, h, d), BF, s) for s in (1, 2, 3))
+    cu, out = offsets([n, 0, 0]), torch.empty((n, h, d), dtype=BF, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        bd.prefill_attn(q, k, v, cu, out=out)
+    for lens in ([n, 0, 0], [100, 300, 100], [1, 0, 2]):
+        cu.copy_(offsets(lens))
+        out.fill_(7.0)
+        graph.replay()
+        assert torch.equal(out[:sum(lens)], bd.prefill_attn(q, k, v, offsets(lens))[:sum(lens)])
+        assert (out[sum(lens):] == 7).all()
+
+
+def test_binding_refuses_what_the_kernels_do_not_take():
+    d, page = 64, 16
+    k, v, q = (randn((6, h, d), BF, h) for h in (2, 2, 4))
+    cache = bd.alloc_paged_cache(4, 2, page, d, BF, "cuda")
+    table, cu, held = i32([[0, 1], [2, 3]]), i32([0, 3, 6]), i32([0, 0])
+    ok = dict(k=k, v=v, cache=cache, page_table=table, cu_rows=cu, cache_len=held)
+    for bad in (dict(k=k.float()), dict(v=v[:5]), dict(k=k.cpu()), dict(v=v.cpu()),
+                dict(k=k.transpose(1, 2).contiguous().transpose(1, 2)), dict(cu_rows=cu[:2]),
+                dict(cu_rows=cu.long()), dict(cache_len=held.cpu()), dict(page_table=table.t()),
+                dict(positions=i32([0] * 5)), dict(q=q, out={"Q": q[:5]}),
+                dict(cache={"K": cache["K"], "V": cache["V"][:3]})):
+        with pytest.raises(ValueError):
+            bd.paged_append(**{**ok, **bad})
+    half = {n: x.half() for n, x in cache.items()}
+    with pytest.raises(ValueError):
+        bd.paged_append(**{**ok, "k": k.half(), "v": v.half(), "cache": half})
+    lens = i32([3, 3])
+    ok = dict(q=q[:2, None], cache=cache, page_table=table, kv_len=lens)
+    for bad in (dict(q=q[:2]), dict(q=q[:1, None]), dict(kv_len=lens[:1]), dict(scale=0.0),
+                dict(prefix=lens.float()), dict(slopes=torch.ones(2, device="cuda")),
+                dict(out=torch.empty((2, 1, 4, d), device="cuda"))):
+        with pytest.raises(ValueError):
+            bd.paged_attn(**{**ok, **bad})
+    with pytest.raises(bd.WfError):
+        bd.paged_attn(**{**ok, "ws": torch.empty(64, dtype=torch.uint8, device="cuda")})
+    with pytest.raises(bd.WfError):
+        bd.paged_attn(**{**ok, "softcap": -1.0})
+    ok = dict(q=q, k=k, v=v, cu_q=cu)
+    for bad in (dict(q=q[None]), dict(v=v[:5]), dict(cu_k=cu[:2]), dict(k=k.expand(6, 2, d).cpu()),
+                dict(slopes=torch.ones(3, device="cuda"))):
+        with pytest.raises(ValueError):
+            bd.prefill_attn(**{**ok, **bad})
+    for bad in (dict(q=q[:, :3]), dict(k=k[:1].expand(6, 2, d), v=v), dict(scale=-1.0)):
+        with pytest.raises((ValueError, bd.WfError)):
+            bd.prefill_attn(**{**ok, **bad})
