@@ -22,11 +22,12 @@
 // (limit = max(position + 1, prefix) under the causal mask), so a mask is a
 // word of bits per 32 keys, only on tiles that cross some limit, and tiles
 // behind every limit are never loaded.  The running maximum is only raised
-// when a score exceeds it by more than 8 (in log2), and O rescaled in tensor
-// memory then: the weights stay below 2^8, which costs no accuracy in fp32 or
-// bf16, and after the first tiles O is hardly ever touched.  Weights are
-// rounded to bf16 for the product with the values (half a step, 2^-8 relative
-// each, as any bf16 operand); their sum is taken in fp32 before that rounding.
+// when a score exceeds it by more than 8 (in log2), to a whole number, and O
+// rescaled in tensor memory then, by a power of two: the weights stay below
+// 2^8, which costs no accuracy in fp32 or bf16, and after the first tiles O
+// is hardly ever touched.  Weights are rounded to bf16 for the product with
+// the values (half a step, 2^-8 relative each, as any bf16 operand); their sum
+// is taken in fp32 before that rounding.
 //
 // A CTA stays on its SM: warp 2 claims blocks of the grid that have not
 // started yet (cluster launch control: dynamic balance without a counter in
@@ -44,9 +45,10 @@
 // which the products fill 2048; the exponentials, FMAs and conversions of
 // 2 x 128 x 128 scores and the two hand-overs between the roles fill the
 // rest.  A short sequence adds per item its first tile (2200 cycles, whose
-// masks cost twice), and the output (2700): packed prompts of 20 to 3000 rows
-// 194 us, 53 %.  With cap and bias the mapping of the scores (7 FMA results
-// each, at 128 a cycle and SM) is the bound: 644 us for 8192 causal rows.
+// masks cost twice) and the output (2700): packed prompts of 20 to 3000 rows
+// 195 us, 53 %.  With cap and bias the mapping of the scores (8 FMA results
+// each, at 128 a cycle and SM) lies on the same chain: 614 us for 8192 causal
+// rows, 2294 us (50 %) for 16384.
 #include <algorithm>
 
 #include "wf_attn.cuh"
@@ -131,7 +133,7 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
   "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), \
       "r"(a[i + 6]), "r"(a[i + 7])
 
-// 64 (or 32) columns of this thread's tensor-memory lane.  The load and its
+// 64 (32, 16) columns of this thread's tensor-memory lane.  The load and its
 // wait are one statement: the registers of an asynchronous load must not be
 // touched, moved or spilled before it.
 __device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t* r) {
@@ -156,6 +158,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : WF_O8(r, 0), WF_O8(r, 8)
+      : "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -163,10 +174,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "%24,%25,%26,%27,%28,%29,%30,%31};" ::WF_I8(r, 0),
       WF_I8(r, 8), WF_I8(r, 16), WF_I8(r, 24), "r"(addr)
       : "memory");
-}
-__device__ __forceinline__ void tmem_st64(uint32_t addr, const uint32_t* r) {
-  tmem_st32(addr, r);
-  tmem_st32(addr + 32, r + 32);
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -328,6 +335,72 @@ __device__ __forceinline__ void map_scores(float* s, const ScoreOpts& o, const S
     map_chunk<CAP, BIAS, true>(s, o, c, d0, side > 0 ? 1.f : -1.f);
   else
     map_chunk<CAP, BIAS, false>(s, o, c, d0, 0.f);
+}
+
+// A chunk's keys from `n` on are hidden.  One bit a key: bits of a register
+// become predicates eight at once.
+__device__ __forceinline__ void hide_keys(float* s, int n) {
+  const uint32_t seen = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s[i] = (seen & (1u << i)) != 0 ? s[i] : -INFINITY;
+}
+
+template <int N>
+__device__ __forceinline__ float chunk_max(const float* s) {
+  float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    a = fmaxf(a, fmaxf(s[i], s[i + 1]));
+    b = fmaxf(b, fmaxf(s[i + 2], s[i + 3]));
+  }
+  return fmaxf(a, b);
+}
+
+// Weights 2^(s mul - m), packed to bf16; their sum in fp32, in two parts.
+template <int N>
+__device__ __forceinline__ void chunk_weights(const float* s, float mul, float m, uint32_t* pk,
+                                              uint64_t& sum0, uint64_t& sum1) {
+  const float base = m == -INFINITY ? 0.f : m;
+  const uint64_t mul2v = pack2(mul, mul), base2 = pack2(-base, -base);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    float x, y;
+    unpack2(fma2(pack2(s[2 * i], s[2 * i + 1]), mul2v, base2), x, y);
+    x = fast_exp2(x);
+    y = fast_exp2(y);
+    if (i & 1) sum1 = add2(sum1, pack2(x, y)); else sum0 = add2(sum0, pack2(x, y));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    pk[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+}
+
+// Rows whose new score exceeds the maximum by more than kLazy raise it to the
+// next whole number; the factor for what has been summed is a power of two,
+// exact (0 where it would be below 2^-126).
+__device__ __forceinline__ float raise_max(float& m, float mt) {
+  if (!(mt > m + kLazy)) return 1.f;
+  const float old = m;
+  m = ceilf(mt);
+  return __int_as_float((127 + static_cast<int>(fmaxf(old - m, -127.f))) << 23);
+}
+
+template <int D>
+__device__ __forceinline__ void scale_output(uint32_t o_addr, float f) {
+  const uint64_t f2 = pack2(f, f);
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t o[32];
+    tmem_ld32(o_addr + c, o);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      float x, y;
+      unpack2(mul2(pack2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2), x, y);
+      o[i] = __float_as_uint(x);
+      o[i + 1] = __float_as_uint(y);
+    }
+    tmem_st32(o_addr + c, o);
+  }
+  tmem_wait_st();
 }
 
 // Claims a block of this grid that has not started (cluster launch control):
@@ -657,9 +730,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = (t == 0 ? tS[0] : tS[1]) + lanes;
     const uint32_t o_addr = (t == 0 ? tO[0] : tO[1]) + lanes;
-    // Scores (with cap or bias: mapped scores) enter the exponent as
-    // fma(s, mul, -m).
-    const float mul = CAP || BIAS ? 1.f : p.o.scale;
+    const float mul = p.o.scale;  // unmapped scores enter the exponent as fma(s, mul, -m)
     uint32_t ns = 0, used = 0, fill = 0;  // key tiles, items with tiles, ring fills so far
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
@@ -706,93 +777,95 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         ++ns;
         tc_fence_after();
         const int k0 = j * kTileRows;
-        // Two passes over the tile in chunks of CH scores, as rolled loops: with
-        // the tile unrolled the code of the softmax groups would not stay in
-        // the instruction caches, and every role, the products' warp first,
-        // would wait for its fetches.  First the maximum (mapped or masked
-        // scores go back in place) ...
-        constexpr int CH = CAP || BIAS ? 32 : 64;
+        // Chunks of scores in rolled loops: with the tile unrolled the code of the
+        // softmax groups would not stay in the instruction caches, and every
+        // role, the products' warp first, would wait for its fetches.  A chunk's
+        // weights go over columns already read.
         const int rel = limit - k0;
         const bool edge = __any_sync(0xffffffffu, rel < 128);
-        float mx0 = -INFINITY, mx1 = -INFINITY;
+        uint64_t sum0 = 0, sum1 = 0;
+        if constexpr (CAP || BIAS) {
+          // One pass.  The weights of a chunk are formed before the test on its
+          // maximum, beside the maximum's own chain of operations, and once more
+          // after the rare raise.  (Two passes, as below, would carry the mapped
+          // scores through tensor memory: 644 against 610 us for 8192 causal rows
+          // with cap and bias.)
 #pragma unroll 1
-        for (int c = 0; c < 128; c += CH) {
-          uint32_t r[CH];
-          if (CH == 64) tmem_ld64(s_addr + c, r); else tmem_ld32(s_addr + c, r);
-          float* s = reinterpret_cast<float*>(r);
-          if (CAP || BIAS) {
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t r[32], pk[16];
+            tmem_ld32(s_addr + c, r);
+            float* s = reinterpret_cast<float*>(r);
             const float d0 = static_cast<float>(pos - k0 - c);
             const int side = !BIAS ? 1
                              : __all_sync(0xffffffffu, d0 >= 31.f) ? 1
                              : __all_sync(0xffffffffu, d0 <= 0.f)  ? -1 : 0;
             map_scores<CAP, BIAS>(s, p.o, map, d0, side);
-          }
-          if (edge) {
-            // One bit a key: bits of a register become predicates eight at once.
-#pragma unroll
-            for (int h = 0; h < CH; h += 32) {
-              const int n = rel - c - h;
-              const uint32_t seen = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                s[h + i] = (seen & (1u << i)) != 0 ? s[h + i] : -INFINITY;
-            }
-            if (!CAP && !BIAS) {
-              if (CH == 64) tmem_st64(s_addr + c, r); else tmem_st32(s_addr + c, r);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < CH; i += 4) {
-            mx0 = fmaxf(mx0, fmaxf(s[i], s[i + 1]));
-            mx1 = fmaxf(mx1, fmaxf(s[i + 2], s[i + 3]));
-          }
-          if (CAP || BIAS) tmem_st32(s_addr + c, r);
-        }
-        if (CAP || BIAS || edge) tmem_wait_st();
-        const float mt = fmaxf(mx0, mx1) * mul;
-        if (j == mine - 1) {
-          m = mt;
-        } else if (__any_sync(0xffffffffu, mt > m + kLazy)) {
-          const float mn = fmaxf(m, mt);
-          const float f = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
-          m = mn;
-          l *= f;
-          const uint64_t f2 = pack2(f, f);
+            if (edge) hide_keys(s, rel - c);
+            const float mc = chunk_max<32>(s);
+            uint64_t add0, add1;
+            while (true) {
+              add0 = add1 = 0;
+              chunk_weights<32>(s, 1.f, m, pk, add0, add1);
+              if (__builtin_expect(!__any_sync(0xffffffffu, mc > m + kLazy), 1)) break;
+              // The sum, this tile's weights so far and O follow the maximum.
+              const float f = raise_max(m, mc);
+              float a0, a1;
+              unpack2(add2(sum0, sum1), a0, a1);
+              l = (l + (a0 + a1)) * f;
+              sum0 = sum1 = 0;
+              if (c > 0) tmem_wait_st();
+              const __nv_bfloat162 fb = __float2bfloat162_rn(f);
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_addr + c, o);
+              for (int e = 0; e < c / 2; e += 16) {
+                uint32_t w[16];
+                tmem_ld16(s_addr + e, w);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float x, y;
-              unpack2(mul2(pack2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2), x, y);
-              o[i] = __float_as_uint(x);
-              o[i + 1] = __float_as_uint(y);
+                for (int i = 0; i < 16; ++i) {
+                  const __nv_bfloat162 x =
+                      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), fb);
+                  w[i] = *reinterpret_cast<const uint32_t*>(&x);
+                }
+                tmem_st16(s_addr + e, w);
+              }
+              if (j < mine - 1) scale_output<D>(o_addr, f);
             }
-            tmem_st32(o_addr + c, o);
+            sum0 = add2(sum0, add0);
+            sum1 = add2(sum1, add1);
+            tmem_st16(s_addr + c / 2, pk);
           }
-        }
-        // ... then the weights, each chunk's over columns already read.
-        const float base = m == -INFINITY ? 0.f : m;
-        const uint64_t mul2v = pack2(mul, mul), base2 = pack2(-base, -base);
-        uint64_t sum0 = 0, sum1 = 0;
+        } else {
+          // Two passes: the maximum (masked scores go back in place), then the
+          // weights.  (One pass, as above: 722 against 703 us for 8192 rows.)
+          float mt = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += CH) {
-          uint32_t r[CH], pk[CH / 2];
-          if (CH == 64) tmem_ld64(s_addr + c, r); else tmem_ld32(s_addr + c, r);
-#pragma unroll
-          for (int i = 0; i < CH / 2; ++i) {
-            float x, y;
-            unpack2(fma2(pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), mul2v,
-                         base2),
-                    x, y);
-            x = fast_exp2(x);
-            y = fast_exp2(y);
-            if (i & 1) sum1 = add2(sum1, pack2(x, y)); else sum0 = add2(sum0, pack2(x, y));
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-            pk[i] = *reinterpret_cast<const uint32_t*>(&b);
+          for (int c = 0; c < 128; c += 64) {
+            uint32_t r[64];
+            tmem_ld64(s_addr + c, r);
+            float* s = reinterpret_cast<float*>(r);
+            if (edge) {
+              hide_keys(s, rel - c);
+              hide_keys(s + 32, rel - c - 32);
+              tmem_st32(s_addr + c, r);
+              tmem_st32(s_addr + c + 32, r + 32);
+            }
+            mt = fmaxf(mt, chunk_max<64>(s));
           }
-          if (CH == 64) tmem_st32(s_addr + c / 2, pk); else tmem_st16(s_addr + c / 2, pk);
+          if (edge) tmem_wait_st();
+          mt *= mul;
+          if (j == mine - 1) {
+            m = ceilf(mt);  // whole, as raise_max keeps it
+          } else if (__any_sync(0xffffffffu, mt > m + kLazy)) {
+            const float f = raise_max(m, mt);
+            l *= f;
+            scale_output<D>(o_addr, f);
+          }
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 64) {
+            uint32_t r[64], pk[32];
+            tmem_ld64(s_addr + c, r);
+            chunk_weights<64>(reinterpret_cast<const float*>(r), mul, m, pk, sum0, sum1);
+            tmem_st32(s_addr + c / 2, pk);
+          }
         }
         float a0, a1;
         unpack2(add2(sum0, sum1), a0, a1);
