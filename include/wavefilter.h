@@ -563,8 +563,8 @@ int wf_paged_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_new, size_
  *   workspace  : device, >= wf_paged_attn_workspace_bytes(); overwritten.
  *                Calls that overlap (captured ones included) need their own
  * Rows behind kv_len never reach the result, whatever they hold; the values
- * of rows below kv_len must be finite even where the mask hides them.  Two
- * launches.  Errors: as wf_paged_append. */
+ * of rows below kv_len must be finite even where the mask hides them (keys
+ * only where it does not).  Two launches.  Errors: as wf_paged_append. */
 int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_new, const void* Q,
                   const void* K_pages, const void* V_pages, const int32_t* page_table,
                   const int32_t* kv_len, void* O, float* lse, void* workspace,

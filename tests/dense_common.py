@@ -58,7 +58,9 @@ def attend(q, k, v, dtype, causal, prefix=0, cap=0.0, slopes=None, scale=None):
     2^-24 |z|) and the cap its tanh (cap 2^-20).  2^x: 2^-22 relative plus the
     rounding of its argument, in all e = the score error twice over (numerator
     and sum) + 2^-20.  Weights of bf16 inputs are rounded to bf16 once before
-    they meet the values: half a step of sum p|v|.  O rounds once to dtype."""
+    they meet the values: half a step of sum p|v|.  O rounds once to dtype.
+    fp32 operands taken as two tf32 parts lose 2^-20 of a product: below
+    d 2^-23 |q||k| of the scores and inside the e of the weighted values."""
     n_q, hq, d = q.shape
     n_k, hkv = k.shape[:2]
     g = hq // hkv

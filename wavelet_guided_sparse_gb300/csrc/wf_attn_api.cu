@@ -1,6 +1,6 @@
 // C ABI of the paged cache and the dense attentions: argument validation,
 // workspace layout and dispatch.  Kernels: wf_append.cu, wf_paged_attn.cu,
-// wf_prefill.cu (tensor cores) and wf_attn_fma.cu (fp32 inputs, join).
+// wf_prefill.cu (bf16) and wf_attn_fma.cu (fp32).
 //
 // As everywhere in this library every entry point validates on the host
 // first, enqueues nothing on a validation error, and neither allocates nor

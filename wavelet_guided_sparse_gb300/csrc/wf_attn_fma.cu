@@ -1,15 +1,15 @@
-// Dense attention on the FMA pipes: fp32 inputs over a paged cache and over
-// packed prompts (bf16 inputs run on the tensor cores, wf_paged_attn.cu and
-// wf_prefill.cu).
+// Attention over packed sequences on the FMA pipes: fp32 inputs (bf16 ones
+// run on the tensor cores, wf_prefill.cu).
 //
-// A row block is RT rows of one key-value head: row r = i g + h is query i of
+// A row block is 64 rows of one key-value head: row r = i g + h is query i of
 // the block's sequence at head h of the g query heads sharing the keys, so
 // shared keys are read once for all of them.  256 threads as 16 x 16: thread
-// (ty, tx) owns RT/16 rows and, of a 64-key tile, keys tx, tx + 16, ...; then
+// (ty, tx) owns four rows and, of a 64-key tile, keys tx, tx + 16, ...; then
 // of the output columns float4s tx, tx + 16.  One pass over the keys with the
 // running maximum and sum; the weights pass through shared memory within a
-// half warp.  The paged form divides the tiles evenly over the grid (see
-// wf_attn.cuh); the packed form takes one row block a CTA.
+// half warp.  Bound by the operand reads from shared memory: five 16-byte
+// reads a thread per 16 (QK) to 32 FMAs; 32 heads, 2048 keys, d = 128:
+// 2246 us, 30.6 TFLOP/s of the pipes' 80.
 #include <algorithm>
 
 #include "wf_attn.cuh"
@@ -18,7 +18,7 @@ namespace wf {
 
 namespace {
 
-constexpr int KT = kPagedTile;  // keys per tile
+constexpr int KT = 64;  // keys per tile
 
 template <int D, int RT>
 struct FmaSmem {
@@ -53,9 +53,9 @@ struct RowBlock {
 };
 
 // One 64-key tile (keys key0 .. key0 + 63, staged in shared memory, rows past
-// `len` and bad pages zero with ok[j] false) into the running state.
+// `len` zero) into the running state.
 template <int D, int RT>
-__device__ __forceinline__ void fma_tile(FmaSmem<D, RT>& s, const bool* ok, const RowBlock& b,
+__device__ __forceinline__ void fma_tile(FmaSmem<D, RT>& s, const RowBlock& b,
                                          const ScoreOpts& o, int key0, FmaState<D, RT>& st) {
   constexpr int RPT = RT / 16;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -93,8 +93,7 @@ __device__ __forceinline__ void fma_tile(FmaSmem<D, RT>& s, const bool* ok, cons
       float x = z[r][j] * o.scale;
       if (o.cap > 0.f) x = o.cap * tanhf(x);
       x -= slope * kLog2e * fabsf(static_cast<float>(pos - key));
-      const bool seen = key < b.len && (ok == nullptr || ok[tx + 16 * j]) &&
-                        (!o.causal || key <= pos || key < b.prefix);
+      const bool seen = key < b.len && (!o.causal || key <= pos || key < b.prefix);
       z[r][j] = seen ? x : -INFINITY;
       mx = fmaxf(mx, z[r][j]);
     }
@@ -194,85 +193,6 @@ __device__ __forceinline__ void fma_stage(FmaSmem<D, RT>& s, int j, int c, const
   }
 }
 
-template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kThreads) paged_fma_kernel(PagedParams p) {
-  extern __shared__ float4 smem4[];
-  FmaSmem<D, RT>& s = *reinterpret_cast<FmaSmem<D, RT>*>(smem4);
-  __shared__ bool ok[KT];
-  const PagedArgs& a = p.a;
-  const int g = a.q_heads / a.kv_heads;
-  const WorkSplit split(work_total(p.w, a.kv_len), gridDim.x);
-  const int64_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
-  idle_sequences<T>(a, p.w.max_len, blockIdx.x, gridDim.x, threadIdx.x, kThreads);
-  launch_dependents();
-
-  FmaState<D, RT> st;
-  WorkUnit u = find_unit(p.w, a.kv_len, w0);
-  for (int64_t at = w0; at < w1; next_unit(p.w, a.kv_len, u)) {
-    const int64_t end = min(w1, u.begin + u.tiles);
-    RowBlock b;
-    b.g = g;
-    b.n_q = a.n_new;
-    b.len = u.len;
-    b.prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + u.seq) : 0;
-    const int kvh = u.unit / p.row_blocks;
-    b.row0 = (u.unit % p.row_blocks) * RT;
-    b.rows = min(RT, g * a.n_new - b.row0);
-    b.head0 = kvh * g;
-    const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(u.seq) * a.n_new * a.q_heads * D;
-    __syncthreads();
-    fma_load_q<T, D, RT>(s, b, q, static_cast<int64_t>(a.q_heads) * D);
-    st.reset();
-    for (int64_t t = at; t < end; ++t) {
-      const int key0 = static_cast<int>(t - u.begin) * KT;
-      __syncthreads();
-      constexpr int C = D / Elem<T>::kPer16B;
-      for (int e = threadIdx.x; e < KT * C; e += kThreads) {
-        const int j = e / C, c = e % C, key = key0 + j;
-        const T *k = nullptr, *v = nullptr;
-        if (key < b.len) {
-          const int page = __ldg(a.table + static_cast<int64_t>(u.seq) * a.table_pages +
-                                 key / a.page_size);
-          if (page >= 0 && page < a.n_pages) {
-            const int64_t line = (static_cast<int64_t>(page) * a.kv_heads + kvh) * a.page_size +
-                                 key % a.page_size;
-            k = static_cast<const T*>(a.k_pages) + line * D;
-            v = static_cast<const T*>(a.v_pages) + line * D;
-          } else if (c == 0) {
-            raise_flag(a.status, WF_DEV_BAD_INDEX);
-          }
-        }
-        if (c == 0) ok[j] = k != nullptr;
-        fma_stage<T, D, RT>(s, j, c, k, v);
-      }
-      __syncthreads();
-      fma_tile<D, RT>(s, ok, b, p.o, key0, st);
-    }
-    if (at == u.begin && end == u.begin + u.tiles) {
-      const int64_t base = static_cast<int64_t>(u.seq) * a.n_new * a.q_heads;
-      fma_store<T, D, RT>(st, b, static_cast<T*>(a.o) + base * D,
-                          a.lse != nullptr ? a.lse + base : nullptr, a.q_heads);
-    } else {
-      // A partial: slot 2c when the unit began before this CTA, else 2c + 1.
-      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (at == u.begin ? 1 : 0);
-      float* dst = a.part + slot * RT * (D + 2);
-      const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll
-      for (int r = 0; r < RT / 16; ++r) {
-        const int row = ty * (RT / 16) + r;
-        if (row >= b.rows) continue;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) store4(dst + row * D + tx * 4 + 64 * c, &st.o[r][4 * c]);
-        if (tx == 0) {
-          dst[RT * D + 2 * row] = st.m[r];
-          dst[RT * D + 2 * row + 1] = st.l[r];
-        }
-      }
-    }
-    at = end;
-  }
-}
-
 struct PrefillParams {
   PrefillArgs a;
   ScoreOpts o;
@@ -316,26 +236,11 @@ __global__ void __launch_bounds__(kThreads) prefill_fma_kernel(PrefillParams p) 
                           in ? vb + key * a.v_stride : nullptr);
     }
     __syncthreads();
-    fma_tile<D, RT>(s, nullptr, b, p.o, key0, st);
+    fma_tile<D, RT>(s, b, p.o, key0, st);
   }
   const int64_t base = d.q0 * a.q_heads;
   fma_store<T, D, RT>(st, b, static_cast<T*>(a.o) + base * D,
                       a.lse != nullptr ? a.lse + base : nullptr, a.q_heads);
-}
-
-template <typename T, int D, int RT>
-cudaError_t launch_paged_rt(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream) {
-  const cudaError_t e = ensure_max_smem<paged_fma_kernel<T, D, RT>>();
-  if (e != cudaSuccess) return e;
-  const size_t smem = sizeof(FmaSmem<D, RT>);
-  paged_fma_kernel<T, D, RT><<<plan.ctas, kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
-}
-
-template <typename T, int D>
-cudaError_t launch_paged_typed(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream) {
-  return plan.row_block == 16 ? launch_paged_rt<T, D, 16>(p, plan, stream)
-                              : launch_paged_rt<T, D, 64>(p, plan, stream);
 }
 
 template <typename T, int D>
@@ -351,12 +256,6 @@ cudaError_t launch_prefill_typed(const PrefillParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
-
-cudaError_t launch_paged_fma(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
-  const PagedParams p = paged_params(a, plan);
-  return a.head_dim == 128 ? launch_paged_typed<float, 128>(p, plan, stream)
-                           : launch_paged_typed<float, 64>(p, plan, stream);
-}
 
 cudaError_t launch_prefill_fma(const PrefillArgs& a, cudaStream_t stream) {
   PrefillParams p;

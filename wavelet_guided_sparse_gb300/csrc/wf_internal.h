@@ -205,7 +205,6 @@ struct PagedPlan {
 };
 PagedPlan plan_paged(const PagedArgs& a, int sm_count);
 cudaError_t launch_paged_attn(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
-cudaError_t launch_paged_fma(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
 
 // Attention over packed sequences with contiguous keys and values.
 struct PrefillArgs {

@@ -1,27 +1,39 @@
 // Attention of new tokens over a paged key-value cache (eq. (3) over the
-// whole cache): bf16 kernel, the join of split sequences, plan and dispatch.
-// fp32 inputs run on the FMA pipes (wf_attn_fma.cu) with the same work list
-// and join.
+// whole cache): the split kernel, the join of split sequences, plan and
+// dispatch.
 //
-// HBM-bound: each key-value row is read once for all g n_new query rows that
-// share it (16 to 64 flop a byte at bf16), so everything serves the stream.
+// HBM-bound at bf16: each key-value row is read once for all g n_new query
+// rows that share it (16 to 64 flop a byte), so everything serves the stream.
 // The 64-key tiles of all sequences and heads form one line that a
 // persistent grid divides evenly (wf_attn.cuh).  In each CTA one producer
 // warp keeps a ring of tiles full by tensor copies (whole pages, or 64-row
 // parts of them, 128-byte swizzle), reading the page table one tile ahead;
 // the consumer warps hold 16 query rows each and split a tile's keys:
 //   rows <= 16: 4 warps x 16 keys, two CTAs an SM (3 stages of 32 KB each);
-//   rows <= 32: 2 row tiles x 4 warps x 16 keys, one CTA, 6 stages;
-//   otherwise : 4 row tiles x 2 warps x 32 keys, one CTA, 5 stages.
+//               fp32: 8 warps x 8 keys, one CTA, 3 stages of 64 KB;
+//   rows <= 32: 2 row tiles x 4 warps x 16 keys, one CTA, 6 stages (fp32: 3);
+//   otherwise : 4 row tiles x 2 warps x 32 keys, one CTA, 5 stages (fp32: 2).
 // The products are mma.sync m16n8k16 (bf16 in, fp32 accumulate): at 16 rows a
 // 128-row tcgen05 tile would be seven eighths empty, and the pipe is far
 // from the bound.  Every warp keeps its own running (max, sum, O) over its
-// keys, the maximum raised lazily as in wf_prefill.cu; the warps of a row
-// tile add up once per unit, in a fixed order.
+// keys, the maximum raised lazily (only past 2^8); the warps of a row tile
+// add up once per unit, in a fixed order.
+//
+// fp32 operands meet the tensor cores as two tf32 parts each (x = hi + lo to
+// 2^-22; hi hi + hi lo + lo hi): the error of a product stays below
+// 2^-20 |a||b|, the order of the fp32 sums around it.
 //
 // Rows behind a sequence's end (the tail of its last page, stale stages) and
 // rows of bad pages get weights of exactly 0 and their value rows are
 // cleared in shared memory before the product.
+//
+// Measured (32 query heads, d = 128; the stream's share of the measured copy
+// rate).  8 heads of keys, one new token: 64 sequences of 200 to 16384 keys
+// 146 us, 91 %; one of 131072 keys with capped scores 85 us, 93 %.  32 heads
+// of keys, a block of 32 tokens, two sequences of 65536 keys: 328 us, 97 %.
+// A few hundred keys: 14 us, of which the split kernel's code, tables and
+// first tile take 9 and the join 5.  fp32, 16 sequences of 8192 keys: 320 us,
+// 49 %, bound by the tf32 products (the FMA pipes took 783).
 #include <algorithm>
 
 #include "wf_attn.cuh"
@@ -36,20 +48,43 @@ namespace {
 constexpr int KT = kPagedTile;  // keys per tile
 constexpr float kLazy = 8.f;    // log2 growth of a maximum that is tolerated
 
+// An fp32 word as two tf32 parts, x = hi + lo to 2^-22 relative.
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(x)));
+  const float rest = __uint_as_float(x) - __uint_as_float(hi);
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
+}
+// D = A(16x8, row) * B(8x8, col) + D; tf32 inputs, fp32 accumulators.
+__device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
 // R: 16-row query tiles per CTA.
-template <int D, int R>
+template <typename T, int D, int R>
 struct PagedShape {
-  static constexpr int kConsumers = R == 1 ? 4 : 8;     // warps
+  static constexpr bool kWide = sizeof(T) == 4;         // fp32: twice the bytes a tile
+  static constexpr int kConsumers = R == 1 && !kWide ? 4 : 8;  // warps
   static constexpr int kKeyGroups = kConsumers / R;
   static constexpr int kKeys = KT / kKeyGroups;         // keys per warp and tile
   static constexpr int kThreadCount = (kConsumers + 1) * 32;
-  static constexpr int kCtasPerSm = R == 1 ? 2 : 1;
-  static constexpr int kTileBytes = KT * D * 2;         // keys or values of a stage
-  static constexpr int kStages = (R == 1 ? 3 : R == 2 ? 6 : 5) * (D == 64 ? 2 : 1);
+  static constexpr int kCtasPerSm = kConsumers == 4 ? 2 : 1;
+  static constexpr int kTileBytes = KT * D * static_cast<int>(sizeof(T));  // keys or values
+  static constexpr int kStages =
+      (kWide ? (R == 4 ? 2 : 3) : R == 1 ? 3 : R == 2 ? 6 : 5) * (D == 64 ? 2 : 1);
   static constexpr int kPitch = D + 4;                  // floats per merge row
-  static constexpr int kQueryBytes = 16 * R * D * 2;
+  static constexpr int kMergeRows = R == 1 ? 4 * kConsumers : 16 * R;
+  static constexpr int kQueryBytes = 16 * R * D * static_cast<int>(sizeof(T));
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * 2 * kTileBytes +
-                                  16 * R * kPitch * sizeof(float) + kQueryBytes;
+                                  kMergeRows * kPitch * sizeof(float) + kQueryBytes;
 };
 
 struct PagedTcParams {
@@ -65,21 +100,23 @@ struct PagedBarriers {
   int abort;
 };
 
-template <int D, int R, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, R>::kCtasPerSm)
+template <typename T, int D, int R, bool CAP, bool BIAS>
+__global__ void
+__launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasPerSm)
     paged_tc_kernel(const __grid_constant__ PagedTcParams tp) {
-  using Shape = PagedShape<D, R>;
+  using Shape = PagedShape<T, D, R>;
+  constexpr bool kWide = Shape::kWide;
   constexpr int kStages = Shape::kStages, kTileBytes = Shape::kTileBytes;
   constexpr int kStageBytes = 2 * kTileBytes, RT = 16 * R;
   constexpr int kConsumerThreads = Shape::kConsumers * 32;
-  constexpr int KB = D / 64;  // 64-column blocks of a row
+  constexpr int KC = 128 / sizeof(T), KB = D / KC;  // columns of a 128-byte block, blocks of a row
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) PagedBarriers<kStages> bars;
   __shared__ float s_ml[Shape::kKeyGroups][RT][2];
   unsigned char* ring = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* merge = reinterpret_cast<float*>(ring + kStages * kStageBytes);
-  __nv_bfloat16* s_q = reinterpret_cast<__nv_bfloat16*>(merge + RT * Shape::kPitch);
+  T* s_q = reinterpret_cast<T*>(merge + Shape::kMergeRows * Shape::kPitch);
   const PagedParams& p = tp.p;
   const PagedArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -101,29 +138,36 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
   launch_dependents();
 
   if (warp == Shape::kConsumers) {
-    // ---- producer: lane = (box of the stage, keys or values, column block)
+    // ---- producer: lane = (box of the stage, keys or values, column block);
+    // where a stage has more than 32 such parts, a lane has NS of them
     const int boxes = KT / tp.box_rows;
+    constexpr int NS = KB > 2 ? 2 : 1, kSubs = 32 / (2 * KB);
     const int kb = lane % KB, which = (lane / KB) & 1, sub = lane / (2 * KB);
-    const bool active = sub < boxes;
     const uint32_t box_bytes = static_cast<uint32_t>(tp.box_rows) * 128;
     const CUtensorMap* map = which ? &tp.tv : &tp.tk;
     if (lane == 0) {
       prefetch_tensormap(&tp.tk);
       prefetch_tensormap(&tp.tv);
     }
-    // Page-table entry of this lane's box of a tile (-1: nothing to copy),
-    // only looked at when its copy is issued: the load flies meanwhile.
-    const auto entry_of = [&](const WorkUnit& x, int64_t at) {
-      const int key = static_cast<int>(at - x.begin) * KT + sub * tp.box_rows;
-      if (!active || key >= x.len) return -1;
-      return __ldg(a.table + static_cast<int64_t>(x.seq) * a.table_pages + (key >> tp.page_shift));
+    // Page-table entries of this lane's boxes of a tile (-1: nothing to copy),
+    // only looked at when their copies are issued: the loads fly meanwhile.
+    int page[NS];
+    const auto read_entries = [&](const WorkUnit& x, int64_t at) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int box = sub + i * kSubs;
+        const int key = static_cast<int>(at - x.begin) * KT + box * tp.box_rows;
+        page[i] = -1;
+        if (box < boxes && key < x.len)
+          page[i] = __ldg(a.table + static_cast<int64_t>(x.seq) * a.table_pages +
+                          (key >> tp.page_shift));
+      }
     };
-    const unsigned every = __ballot_sync(0xffffffffu, active);
     int fill = 0, units = 0, st = 0;
-    uint32_t phase = 1;  // of the stage's last release (first round: none yet)
+    uint32_t phase = 1;  // of the stage's last release (first time: none yet)
     int row0 = 0, rows = 0, kvh = 0;
     bool ok = true;
-    int page = w0 < w1 ? entry_of(u, w0) : -1;
+    if (w0 < w1) read_entries(u, w0);
     for (int64_t at = w0; at < w1; ++at) {
       // A unit's query rows arrive with its first tile: the runs of rows that
       // one query's heads (or a part of them) form, one bulk copy each.
@@ -137,31 +181,39 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
           if (!ok) break;
         }
       }
-      const int key = static_cast<int>(at - u.begin) * KT + sub * tp.box_rows;
       if (fill >= kStages) {
         ok = warp_wait(&bars.empty[st], phase, &bars.abort, a.status);
         if (!ok) break;
       }
-      if (page < 0 || page >= a.n_pages) {
-        if (active && key < u.len) raise_flag(a.status, WF_DEV_BAD_INDEX);
-        page = -1;
+      const int key0 = static_cast<int>(at - u.begin) * KT;
+      int valid = 0, parts = 0;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int box = sub + i * kSubs;
+        if (page[i] < 0 || page[i] >= a.n_pages) {
+          if (box < boxes && key0 + box * tp.box_rows < u.len)
+            raise_flag(a.status, WF_DEV_BAD_INDEX);
+          page[i] = -1;
+        }
+        const unsigned live = __ballot_sync(0xffffffffu, page[i] >= 0);
+        parts += __popc(live);
+#pragma unroll
+        for (int e = 0; e < kSubs; ++e) valid |= ((live >> (e * 2 * KB)) & 1) << (i * kSubs + e);
       }
-      const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
       if (lane == 0) {
-        int valid = (1 << boxes) - 1;
-        if (live != every)
-          for (int i = 0; i < boxes; ++i)
-            if (!((live >> (i * 2 * KB)) & 1)) valid &= ~(1 << i);
         bars.valid[st] = valid;
-        mbar_arrive_expect_tx(&bars.full[st],
-                              __popc(live) * box_bytes + (first ? rows * D * 2 : 0));
+        mbar_arrive_expect_tx(&bars.full[st], parts * box_bytes +
+                                                  (first ? rows * D * static_cast<int>(sizeof(T)) : 0));
       }
       __syncwarp();
-      if (page >= 0) {
-        const int y = (page * a.kv_heads + kvh) * a.page_size + (key & (a.page_size - 1));
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        if (page[i] < 0) continue;
+        const int box = sub + i * kSubs, key = key0 + box * tp.box_rows;
+        const int y = (page[i] * a.kv_heads + kvh) * a.page_size + (key & (a.page_size - 1));
         tma_load_2d(ring + st * kStageBytes + which * kTileBytes + kb * (KT * 128) +
-                        sub * box_bytes,
-                    map, kb * 64, y, &bars.full[st]);
+                        box * box_bytes,
+                    map, kb * KC, y, &bars.full[st]);
       }
       if (first) {
         const int i0 = row0 / g, i1 = (row0 + rows - 1) / g;
@@ -169,8 +221,8 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
           const int r0 = max(i * g, row0), r1 = min((i + 1) * g, row0 + rows);
           const int64_t from = (static_cast<int64_t>(u.seq) * a.n_new + i) * a.q_heads + kvh * g +
                                (r0 - i * g);
-          bulk_g2s(s_q + (r0 - row0) * D, static_cast<const __nv_bfloat16*>(a.q) + from * D,
-                   (r1 - r0) * D * 2, &bars.full[st]);
+          bulk_g2s(s_q + (r0 - row0) * D, static_cast<const T*>(a.q) + from * D,
+                   (r1 - r0) * D * static_cast<int>(sizeof(T)), &bars.full[st]);
         }
       }
       ++fill;
@@ -179,7 +231,7 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
         phase ^= 1;
       }
       if (at + 1 == u.begin + u.tiles) next_unit(p.w, a.kv_len, u);
-      page = at + 1 < w1 ? entry_of(u, at + 1) : -1;
+      if (at + 1 < w1) read_entries(u, at + 1);
     }
     if (!ok) {  // no copy may land after the CTA has gone
       for (int f = max(0, fill - kStages); f < fill; ++f)
@@ -189,17 +241,23 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
     // ---- consumers
     const int rt = warp % R, kg = warp / R;      // row tile, key group
     const int gid = lane >> 2, tig = lane & 3;
-    idle_sequences<__nv_bfloat16>(a, p.w.max_len, blockIdx.x, gridDim.x, threadIdx.x,
+    idle_sequences<T>(a, p.w.max_len, blockIdx.x, gridDim.x, threadIdx.x,
                                   kConsumerThreads);
     const float mul = CAP ? p.o.cap : p.o.scale;
     // ldmatrix lane addresses within a tile: keys as B (rows = keys), values
     // transposed (rows = keys); 16-byte chunk c of row r sits at c ^ (r % 8),
     // so a step along a row is an exclusive or of bits 5-6 (and a column
     // block every four).
-    const int krow = kg * Shape::kKeys + ((lane >> 4) << 3) + (lane & 7);
-    const int vrow = kg * Shape::kKeys + (((lane >> 3) & 1) << 3) + (lane & 7);
-    const uint32_t koff = krow * 128 + ((((lane >> 3) & 1) ^ (krow & 7)) << 4);
-    const uint32_t voff = vrow * 128 + (((lane >> 4) ^ (vrow & 7)) << 4);
+    // fp32: an ldmatrix reads four 16-byte chunks of eight keys (two steps of 8
+    // channels); a weight's register pair (keys 2 tig, 2 tig + 1) is taken as
+    // rows tig and tig + 4 of the product, so values come as words of rows
+    // 2 tig and 2 tig + 1, whose chunks lie in different banks.
+    const int krow = kg * Shape::kKeys + (kWide ? 0 : (lane >> 4) << 3) + (lane & 7);
+    const int vrow = kg * Shape::kKeys + (kWide ? 2 * tig : (((lane >> 3) & 1) << 3) + (lane & 7));
+    const uint32_t koff =
+        krow * 128 + (((kWide ? lane >> 3 : (lane >> 3) & 1) ^ (krow & 7)) << 4);
+    const uint32_t voff = kWide ? vrow * 128 + (((gid >> 2) ^ (vrow & 7)) << 4) + (gid & 3) * 4
+                                : vrow * 128 + (((lane >> 4) ^ (vrow & 7)) << 4);
     const uint32_t ring_addr = smem_u32(ring);
     const int kAllValid = (1 << (KT / tp.box_rows)) - 1;
     int st = 0;
@@ -228,14 +286,16 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
       }
       // The unit's query rows arrive with its first tile.
       ok = ok && warp_wait(&bars.full[st], phase, &bars.abort, a.status);
-      uint32_t qf[D / 16][4];
+      constexpr int KS = D * static_cast<int>(sizeof(T)) / 32;  // steps of a score's product
+      constexpr int kHalf = 16 / static_cast<int>(sizeof(T));   // channels of half a step
+      uint32_t qf[KS][4];
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
+      for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int r = rt * 16 + gid + 8 * (c & 1);
-          qf[ks][c] = r < rows ? *reinterpret_cast<const uint32_t*>(s_q + r * D + ks * 16 +
-                                                                    8 * (c >> 1) + 2 * tig)
+          qf[ks][c] = r < rows ? *reinterpret_cast<const uint32_t*>(
+                                     s_q + r * D + (2 * ks + (c >> 1)) * kHalf + tig * (kHalf / 4))
                                : 0u;
         }
       __syncwarp();
@@ -263,8 +323,9 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
         const bool edge = valid != kAllValid || key0 + Shape::kKeys > open;
         if (edge && (valid != kAllValid || key0 + Shape::kKeys > len)) {
           // Clear the value rows whose weight is 0 by their place.
-          for (int e = lane; e < Shape::kKeys * (D / 8); e += 32) {
-            const int r = e / (D / 8), c = e % (D / 8);
+          constexpr int C = D * static_cast<int>(sizeof(T)) / 16;  // chunks of a row
+          for (int e = lane; e < Shape::kKeys * C; e += 32) {
+            const int r = e / C, c = e % C;
             const int tr = kg * Shape::kKeys + r;
             if (key0 + r >= len || !((valid >> (tr / tp.box_rows)) & 1))
               *reinterpret_cast<uint4*>(ring + st * kStageBytes + kTileBytes +
@@ -275,20 +336,45 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
           __syncwarp();
         }
         constexpr int NB = Shape::kKeys / 8;  // 8-key blocks
-        // Two accumulators a block halve the chain of dependent products.
+        // Two accumulators a block halve the chain of dependent products; for
+        // fp32 the second one takes the small terms.
         float s[NB][4], s2[NB][4];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
+        if constexpr (kWide) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
+          for (int j = 0; j < KS / 2; ++j) {
+            uint32_t qh[2][4], ql[2][4];
 #pragma unroll
-          for (int n = 0; n < NB; n += 2) {
-            uint32_t b[4];
-            ldsm_x4((kt ^ ((ks & 3) << 5)) + (ks >> 2) * (KT * 128) + n * 1024, b);
-            mma_bf16(ks & 1 ? s2[n] : s[n], qf[ks], b);
-            mma_bf16(ks & 1 ? s2[n + 1] : s[n + 1], qf[ks], b + 2);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) split_tf32(qf[2 * j + h][c], qh[h][c], ql[h][c]);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              uint32_t b[4], bh[4], bl[4];
+              ldsm_x4((kt ^ ((j & 1) << 6)) + (j >> 1) * (KT * 128) + n * 1024, b);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) split_tf32(b[e], bh[e], bl[e]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                mma_tf32(s[n], qh[h], bh + 2 * h);
+                mma_tf32(s2[n], qh[h], bl + 2 * h);
+                mma_tf32(s2[n], ql[h], bh + 2 * h);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+            for (int n = 0; n < NB; n += 2) {
+              uint32_t b[4];
+              ldsm_x4((kt ^ ((ks & 3) << 5)) + (ks >> 2) * (KT * 128) + n * 1024, b);
+              mma_bf16(ks & 1 ? s2[n] : s[n], qf[ks], b);
+              mma_bf16(ks & 1 ? s2[n + 1] : s[n + 1], qf[ks], b + 2);
+            }
           }
         }
 #pragma unroll
@@ -345,26 +431,54 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
           }
         }
         const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
-        uint32_t pf[NB][2];
+        uint32_t pf[NB][kWide ? 4 : 2];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           const float e0 = fast_exp2(fmaf(s[n][0], mul, -b0)), e1 = fast_exp2(fmaf(s[n][1], mul, -b0));
           const float e2 = fast_exp2(fmaf(s[n][2], mul, -b1)), e3 = fast_exp2(fmaf(s[n][3], mul, -b1));
           l[0] += e0 + e1;
           l[1] += e2 + e3;
-          // Weights meet the values in bf16 (half a step, 2^-8 relative each).
-          pf[n][0] = pack_bf16(e0, e1);
-          pf[n][1] = pack_bf16(e2, e3);
+          if constexpr (kWide) {
+            pf[n][0] = __float_as_uint(e0);
+            pf[n][1] = __float_as_uint(e2);
+            pf[n][2] = __float_as_uint(e1);
+            pf[n][3] = __float_as_uint(e3);
+          } else {
+            // Weights meet the values in bf16 (half a step, 2^-8 relative each).
+            pf[n][0] = pack_bf16(e0, e1);
+            pf[n][1] = pack_bf16(e2, e3);
+          }
         }
+        if constexpr (kWide) {
 #pragma unroll
-        for (int kk = 0; kk < NB / 2; ++kk) {
-          const uint32_t af[4] = {pf[2 * kk][0], pf[2 * kk][1], pf[2 * kk + 1][0], pf[2 * kk + 1][1]};
+          for (int kk = 0; kk < NB; ++kk) {
+            uint32_t ah[4], al[4];
 #pragma unroll
-          for (int n = 0; n < D / 16; ++n) {
-            uint32_t b[4];
-            ldsm_x4_t((vt ^ ((n & 3) << 5)) + (n >> 2) * (KT * 128) + kk * 2048, b);
-            mma_bf16(o[2 * n], af, b);
-            mma_bf16(o[2 * n + 1], af, b + 2);
+            for (int e = 0; e < 4; ++e) split_tf32(pf[kk][e], ah[e], al[e]);
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              // Rows 2 tig and 2 tig + 1: the odd row's chunk is the even one's
+              // neighbour in its pair.
+              const uint32_t at = (vt ^ ((n & 3) << 5)) + (n >> 2) * (KT * 128) + kk * 1024;
+              uint32_t bh[2], bl[2];
+              split_tf32(lds32(at), bh[0], bl[0]);
+              split_tf32(lds32((at ^ 16) + 128), bh[1], bl[1]);
+              mma_tf32(o[n], ah, bl);
+              mma_tf32(o[n], al, bh);
+              mma_tf32(o[n], ah, bh);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < NB / 2; ++kk) {
+            const uint32_t af[4] = {pf[2 * kk][0], pf[2 * kk][1], pf[2 * kk + 1][0], pf[2 * kk + 1][1]};
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+              uint32_t b[4];
+              ldsm_x4_t((vt ^ ((n & 3) << 5)) + (n >> 2) * (KT * 128) + kk * 2048, b);
+              mma_bf16(o[2 * n], af, b);
+              mma_bf16(o[2 * n + 1], af, b + 2);
+            }
           }
         }
         __syncwarp();
@@ -379,7 +493,7 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
       // its O (relative to its own maximum) in a slot of the merge buffer,
       // all slots at once where the unit's rows leave room, else one group
       // after the other.
-      const bool at_once = rows * Shape::kKeyGroups <= RT;
+      const bool at_once = rows * Shape::kKeyGroups <= Shape::kMergeRows;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -462,7 +576,7 @@ __global__ void __launch_bounds__(PagedShape<D, R>::kThreadCount, PagedShape<D, 
           const float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
           const int i = (row0 + r) / g, hd = (row0 + r) - i * g;
           const int64_t to = base + static_cast<int64_t>(i) * a.q_heads + hd;
-          store4(static_cast<__nv_bfloat16*>(a.o) + to * D + c * 4, y);
+          store4(static_cast<T*>(a.o) + to * D + c * 4, y);
           if (a.lse != nullptr && c == 0) a.lse[to] = row_lse(gm, gl);
         } else {
           *reinterpret_cast<float4*>(part + r * D + c * 4) = x;
@@ -563,26 +677,26 @@ __global__ void __launch_bounds__(kThreads, 6)
   }
 }
 
-template <int D, int R, bool CAP, bool BIAS>
+template <typename T, int D, int R, bool CAP, bool BIAS>
 cudaError_t launch_tc(const PagedTcParams& p, const PagedPlan& plan, cudaStream_t stream) {
-  using Shape = PagedShape<D, R>;
-  const cudaError_t e = ensure_max_smem<paged_tc_kernel<D, R, CAP, BIAS>>();
+  using Shape = PagedShape<T, D, R>;
+  const cudaError_t e = ensure_max_smem<paged_tc_kernel<T, D, R, CAP, BIAS>>();
   if (e != cudaSuccess) return e;
-  paged_tc_kernel<D, R, CAP, BIAS><<<plan.ctas, Shape::kThreadCount, Shape::kSmem, stream>>>(p);
+  paged_tc_kernel<T, D, R, CAP, BIAS><<<plan.ctas, Shape::kThreadCount, Shape::kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <int D, int R>
+template <typename T, int D, int R>
 cudaError_t launch_tc_opts(const PagedTcParams& p, const PagedPlan& plan, cudaStream_t stream) {
   const bool bias = p.p.o.slopes != nullptr;
   if (p.p.o.cap > 0.f)
-    return bias ? launch_tc<D, R, true, true>(p, plan, stream)
-                : launch_tc<D, R, true, false>(p, plan, stream);
-  return bias ? launch_tc<D, R, false, true>(p, plan, stream)
-              : launch_tc<D, R, false, false>(p, plan, stream);
+    return bias ? launch_tc<T, D, R, true, true>(p, plan, stream)
+                : launch_tc<T, D, R, true, false>(p, plan, stream);
+  return bias ? launch_tc<T, D, R, false, true>(p, plan, stream)
+              : launch_tc<T, D, R, false, false>(p, plan, stream);
 }
 
-template <int D>
+template <typename T, int D>
 cudaError_t launch_tc_rows(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
   PagedTcParams p;
   p.p = paged_params(a, plan);
@@ -590,14 +704,16 @@ cudaError_t launch_tc_rows(const PagedArgs& a, const PagedPlan& plan, cudaStream
   p.page_shift = 0;
   while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
   const cuuint64_t dims[2] = {D, static_cast<cuuint64_t>(a.n_pages) * a.kv_heads * a.page_size};
-  const cuuint64_t strides[1] = {D * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(p.box_rows)};
-  if (!encode_bf16_map(&p.tk, a.k_pages, 2, dims, strides, box) ||
-      !encode_bf16_map(&p.tv, a.v_pages, 2, dims, strides, box))
+  const cuuint64_t strides[1] = {D * sizeof(T)};
+  const cuuint32_t box[2] = {128 / sizeof(T), static_cast<cuuint32_t>(p.box_rows)};
+  const CUtensorMapDataType type =
+      sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (!encode_tile_map(&p.tk, type, a.k_pages, 2, dims, strides, box) ||
+      !encode_tile_map(&p.tv, type, a.v_pages, 2, dims, strides, box))
     return cudaErrorInvalidValue;
-  if (plan.row_block == 16) return launch_tc_opts<D, 1>(p, plan, stream);
-  if (plan.row_block == 32) return launch_tc_opts<D, 2>(p, plan, stream);
-  return launch_tc_opts<D, 4>(p, plan, stream);
+  if (plan.row_block == 16) return launch_tc_opts<T, D, 1>(p, plan, stream);
+  if (plan.row_block == 32) return launch_tc_opts<T, D, 2>(p, plan, stream);
+  return launch_tc_opts<T, D, 4>(p, plan, stream);
 }
 
 // The join starts while the split kernel still runs (programmatic dependent
@@ -624,31 +740,30 @@ cudaError_t launch_join(const PagedArgs& a, const PagedPlan& plan, cudaStream_t 
 PagedPlan plan_paged(const PagedArgs& a, int sm_count) {
   PagedPlan p;
   const int rows = a.q_heads / a.kv_heads * a.n_new;
-  if (a.dtype == WF_BF16)
-    p.row_block = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  else
-    p.row_block = rows <= 16 ? 16 : 64;
+  p.row_block = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   const int64_t units = static_cast<int64_t>(a.n_seqs) * a.kv_heads *
                         ((rows + p.row_block - 1) / p.row_block);
   const int64_t tiles =
       units * ((static_cast<int64_t>(a.table_pages) * a.page_size + KT - 1) / KT);
-  p.ctas = static_cast<int>(std::min<int64_t>(sm_count * (p.row_block == 16 ? 2 : 1), tiles));
+  p.ctas = static_cast<int>(std::min<int64_t>(sm_count * (p.row_block == 16 && a.dtype == WF_BF16 ? 2 : 1), tiles));
   p.part_bytes = static_cast<size_t>(p.ctas) * 2 * p.row_block * (a.head_dim + 2) * sizeof(float);
   return p;
 }
 
+namespace {
+template <typename T, int D>
+cudaError_t launch_paged(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
+  const cudaError_t e = launch_tc_rows<T, D>(a, plan, stream);
+  return e != cudaSuccess ? e : launch_join<T, D>(a, plan, stream);
+}
+}  // namespace
+
 cudaError_t launch_paged_attn(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
-  if (a.dtype == WF_F32) {
-    const cudaError_t e = launch_paged_fma(a, plan, stream);
-    if (e != cudaSuccess) return e;
-    return a.head_dim == 128 ? launch_join<float, 128>(a, plan, stream)
-                             : launch_join<float, 64>(a, plan, stream);
-  }
-  const cudaError_t e = a.head_dim == 128 ? launch_tc_rows<128>(a, plan, stream)
-                                          : launch_tc_rows<64>(a, plan, stream);
-  if (e != cudaSuccess) return e;
-  return a.head_dim == 128 ? launch_join<__nv_bfloat16, 128>(a, plan, stream)
-                           : launch_join<__nv_bfloat16, 64>(a, plan, stream);
+  if (a.dtype == WF_F32)
+    return a.head_dim == 128 ? launch_paged<float, 128>(a, plan, stream)
+                             : launch_paged<float, 64>(a, plan, stream);
+  return a.head_dim == 128 ? launch_paged<__nv_bfloat16, 128>(a, plan, stream)
+                           : launch_paged<__nv_bfloat16, 64>(a, plan, stream);
 }
 
 }  // namespace wf

@@ -965,7 +965,7 @@ bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int heads, in
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2,
                                  static_cast<cuuint64_t>(stride) * 2};
   const cuuint32_t box[3] = {64, 1, kTileRows};
-  return encode_bf16_map(map, base, 3, dims, strides, box);
+  return encode_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dims, strides, box);
 }
 
 template <int D, bool CAP, bool BIAS>

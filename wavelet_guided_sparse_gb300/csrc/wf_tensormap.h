@@ -30,14 +30,15 @@ inline EncodeTiledFn tensormap_encoder() {
   return reinterpret_cast<EncodeTiledFn>(f);
 }
 
-// bf16 tensor of `rank` dimensions (innermost first; strides in bytes of the
+// Tensor of `rank` dimensions (innermost first; strides in bytes of the
 // outer ones) with 128-byte-swizzled boxes; elements outside read as zero.
-inline bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
-                            const cuuint64_t* strides, const cuuint32_t* box) {
+inline bool encode_tile_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank,
+                            const cuuint64_t* dims, const cuuint64_t* strides,
+                            const cuuint32_t* box) {
   const EncodeTiledFn enc = tensormap_encoder();
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc != nullptr &&
-         enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides,
+         enc(map, type, rank, const_cast<void*>(base), dims, strides,
              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
