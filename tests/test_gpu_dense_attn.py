@@ -404,6 +404,21 @@ def test_a_visible_nan_shows_in_every_row_that_sees_it(dtype, cap):
         assert o.isnan().all() == (m > at) and lse.isnan().all() == (m > at)
 
 
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, False), (0.0, True), (20.0, True)])
+def test_the_only_visible_key_has_weight_one(cap, bias):
+    # Its value comes back bit for bit: no rounding of the weight stays in O.
+    n, h, d = 70, 3, 128
+    q, k, v = (randn((n, h, d), BF, s) for s in (1, 2, 3))
+    slopes = slope_list(h) if bias else None
+    o = bd.prefill_attn(q, k, v, offsets([1] * n), softcap=cap, slopes=slopes)
+    assert torch.equal(o, v)
+    table, pages = make_table([1] * n, 16, 0)
+    cache = bd.alloc_paged_cache(pages, h, 16, d, BF, "cuda")
+    bd.paged_append(k, v, cache, table, offsets([1] * n), i32([0] * n))
+    o = bd.paged_attn(q[:, None], cache, table, i32([1] * n), softcap=cap, slopes=slopes)
+    assert torch.equal(o[:, 0], v)
+
+
 @pytest.mark.parametrize("offs", [[0, 40, 20, 60], [0, 30, 90], [-5, 30]])
 def test_prefill_bad_offsets_are_flagged(offs):
     q, k, v = (randn((60, 1, 64), BF, s) for s in (1, 2, 3))

@@ -22,10 +22,9 @@
 // (limit = max(position + 1, prefix) under the causal mask), so a mask is a
 // word of bits per 32 keys, only on tiles that cross some limit, and tiles
 // behind every limit are never loaded.  The running maximum is only raised
-// when a score exceeds it by more than 8 (in log2), to a whole number, and O
-// rescaled in tensor memory then, by a power of two: the weights stay below
-// 2^8, which costs no accuracy in fp32 or bf16, and after the first tiles O
-// is hardly ever touched.  Weights are rounded to bf16 for the product with
+// when a score exceeds it by more than 8 (in log2), and O rescaled in tensor
+// memory then: the weights stay below 2^8, which costs no accuracy in fp32 or
+// bf16, and after the first tiles O is hardly ever touched.  Weights are rounded to bf16 for the product with
 // the values (half a step, 2^-8 relative each, as any bf16 operand); their sum
 // is taken in fp32 before that rounding.
 //
@@ -47,8 +46,8 @@
 // rest.  A short sequence adds per item its first tile (2200 cycles, whose
 // masks cost twice) and the output (2700): packed prompts of 20 to 3000 rows
 // 195 us, 53 %.  With cap and bias the mapping of the scores (8 FMA results
-// each, at 128 a cycle and SM) lies on the same chain: 614 us for 8192 causal
-// rows, 2294 us (50 %) for 16384.
+// each, at 128 a cycle and SM) lies on the same chain: 618 us for 8192 causal
+// rows, 2288 us (50 %) for 16384.
 #include <algorithm>
 
 #include "wf_attn.cuh"
@@ -374,14 +373,14 @@ __device__ __forceinline__ void chunk_weights(const float* s, float mul, float m
   }
 }
 
-// Rows whose new score exceeds the maximum by more than kLazy raise it to the
-// next whole number; the factor for what has been summed is a power of two,
-// exact (0 where it would be below 2^-126).
+// Rows whose new score exceeds the maximum by more than kLazy raise it to that
+// score, exactly: the weight of a row's only (or outstanding) key is then 1
+// and meets no rounding.  Returns the factor for what has been summed.
 __device__ __forceinline__ float raise_max(float& m, float mt) {
   if (!(mt > m + kLazy)) return 1.f;
   const float old = m;
-  m = ceilf(mt);
-  return __int_as_float((127 + static_cast<int>(fmaxf(old - m, -127.f))) << 23);
+  m = mt;
+  return fast_exp2(old - mt);
 }
 
 template <int D>
@@ -788,7 +787,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           // One pass.  The weights of a chunk are formed before the test on its
           // maximum, beside the maximum's own chain of operations, and once more
           // after the rare raise.  (Two passes, as below, would carry the mapped
-          // scores through tensor memory: 644 against 610 us for 8192 causal rows
+          // scores through tensor memory: 644 against 618 us for 8192 causal rows
           // with cap and bias.)
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
@@ -807,7 +806,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               add0 = add1 = 0;
               chunk_weights<32>(s, 1.f, m, pk, add0, add1);
               if (__builtin_expect(!__any_sync(0xffffffffu, mc > m + kLazy), 1)) break;
-              // The sum, this tile's weights so far and O follow the maximum.
+              // The sum, this tile's weights so far and O follow the maximum.  The
+              // weights, 2^8 below what is to come, are rounded a second time.
               const float f = raise_max(m, mc);
               float a0, a1;
               unpack2(add2(sum0, sum1), a0, a1);
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (edge) tmem_wait_st();
           mt *= mul;
           if (j == mine - 1) {
-            m = ceilf(mt);  // whole, as raise_max keeps it
+            m = mt;
           } else if (__any_sync(0xffffffffu, mt > m + kLazy)) {
             const float f = raise_max(m, mt);
             l *= f;
