@@ -48,14 +48,15 @@ def rotation_bound(x, r, interleaved, ref, dtype):
     return bound
 
 
-def attend(q, k, v, dtype, causal, prefix=0, cap=0.0, slopes=None, scale=None):
+def attend(q, k, v, dtype, causal, prefix=0, cap=0.0, slopes=None, scale=None, bend=None):
     """q [n_q, hq, d] at the last n_q positions of k, v [n_k, hkv, d] (float64
     arrays): O, lse, and the bounds of their errors on the GPU.
 
     Score error (natural units): a dot product of d terms accumulated in fp32,
     each step truncated at worst (2^-23), at most d 2^-23 |q||k|; scaling, cap,
     bias and the log2-domain factor add roundings of the score itself (8 *
-    2^-24 |z|) and the cap its tanh (cap 2^-20).  2^x: 2^-22 relative plus the
+    2^-24 |z|) and the cap its tanh (cap 2^-20, or `bend` 2^-20 for a smaller
+    `bend`: the largest |z| where tanh is good to 2^-20 relative).  2^x: 2^-22 relative plus the
     rounding of its argument, in all e = the score error twice over (numerator
     and sum) + 2^-20.  Weights of bf16 inputs are rounded to bf16 once before
     they meet the values: half a step of sum p|v|.  O rounds once to dtype.
@@ -100,7 +101,7 @@ def attend(q, k, v, dtype, causal, prefix=0, cap=0.0, slopes=None, scale=None):
         kn = np.linalg.norm(kk[used], axis=1).max()
         zmax = np.abs(np.where(seen[live], zl, 0)).max(1)
         raw = scale * d * 2.0 ** -23 * qn * kn
-        ez = raw + 8 * 2.0 ** -24 * (zmax + scale * qn * kn) + cap * 2.0 ** -20
+        ez = raw + 8 * 2.0 ** -24 * (zmax + scale * qn * kn) + (cap if bend is None else bend) * 2.0 ** -20
         e = (2 * ez + 2.0 ** -20)[:, None]
         a = p @ np.abs(vs)
         hs = half_step(dtype)

@@ -122,7 +122,8 @@ def test_paged_refusals(lib):
     for name in ("table", "lens", "lse"):
         assert paged(lib, d, opts(), **{name: ODD2}) == ALIGNMENT, name
     assert paged(lib, d, opts(), wsb=300) == WORKSPACE
-    for kw in (dict(softcap=-1.0), dict(softcap=math.nan), dict(scale=math.inf), dict(scale=-1.0)):
+    for kw in (dict(softcap=-1.0), dict(softcap=math.nan), dict(scale=math.inf), dict(scale=-1.0),
+               dict(scale=3e38), dict(softcap=3e38), dict(scale=2.0, softcap=1e-39)):
         assert paged(lib, d, opts(**kw)) == SHAPE, kw
     assert paged(lib, d, opts(prefix=ODD2.value)) == ALIGNMENT
     assert paged(lib, d, opts(slopes=ODD2.value)) == ALIGNMENT

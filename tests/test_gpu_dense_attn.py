@@ -192,6 +192,9 @@ PAGED = [
     (BF, 128, 8, 2, 64, [200, 64, 33, 0], 64, True, [0, 64, 7, 0], 30.0, True),  # 4 blocks
     (F32, 64, 2, 2, 32, [1056], 32, False, None, 0.0, False),
     (F32, 128, 4, 1, 16, [1, 0, 333], 1, True, None, 30.0, True),
+    (F32, 128, 8, 2, 8, [500, 77, 0, 6], 5, True, None, 0.0, False),         # 20 rows, 8 boxes
+    (F32, 128, 4, 1, 8, [333, 20], 16, True, [9, 20], 25.0, True),           # 64 rows
+    (F32, 128, 4, 4, 256, [1000, 1], 20, False, None, 0.0, False),
     (F32, 64, 9, 3, 8, [100, 41], 4, True, [60, 0], 0.0, False),
     (F32, 128, 2, 2, 64, [3, 130], 7, True, None, 0.0, True),
 ]
@@ -212,6 +215,12 @@ def test_paged_long_splits_and_is_deterministic():
 def test_paged_many_short_sequences():
     rng = np.random.default_rng(3)
     run_paged(BF, 64, 2, 1, 16, rng.integers(0, 90, 700).tolist(), 1, True, None, 0.0, False)
+
+
+def test_paged_the_most_sequences():
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 40, 4096).tolist()
+    run_paged(BF, 64, 1, 1, 32, lens, 1, True, None, 0.0, False)
 
 
 def test_paged_large_scores_and_scale():
@@ -342,6 +351,35 @@ def test_prefill_caps_far_into_their_bend(cap, bias, spread):
                             None if slopes is None else slopes.cpu().numpy())
     check(f64(lse), rl, lb, "lse")
     check(f64(o), ro, ob, "O")
+
+
+@pytest.mark.parametrize("cap,scale,spread", [(1e7, 1.0, 2e5), (1e-7, None, 1e-8), (1e30, None, 1.0)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_caps_far_from_one(dtype, cap, scale, spread):
+    # Scores about the cap's bend (or far below it) at extreme caps: there every
+    # score is good to 2^-20 of itself.
+    d, n, h = 128, 200, 2
+    q, k, v = (randn((n, h, d), dtype, s) for s in (1, 2, 3))
+    q = (q.float() * spread).to(dtype)
+    o, lse = bd.prefill_attn(q, k, v, offsets([n]), softcap=cap, scale=scale, with_lse=True)
+    z = np.einsum("qhd,khd->hqk", f64(q), f64(k)) * (scale or d ** -0.5)
+    bend = min(cap, np.abs(z).max())
+    ro, rl, ob, lb = attend(f64(q), f64(k), f64(v), dtype, True, 0, cap, scale=scale, bend=bend)
+    check(f64(lse), rl, lb, "lse")
+    check(f64(o), ro, ob, "O")
+    table, pages = make_table([n], 16, 0)
+    cache = bd.alloc_paged_cache(pages, h, 16, d, dtype, "cuda")
+    bd.paged_append(k, v, cache, table, offsets([n]), i32([0]))
+    o, lse = bd.paged_attn(q[None, -9:], cache, table, i32([n]), softcap=cap, scale=scale,
+                           with_lse=True)
+    check(f64(lse[0]), rl[-9:], lb[-9:], "lse over pages")
+    check(f64(o[0]), ro[-9:], ob[-9:], "O over pages")
+
+
+def test_prefill_a_multitude_of_sequences():
+    # One row each: every row is its own value.
+    q, k, v = (randn((50000, 2, 64), BF, s) for s in (1, 2, 3))
+    assert torch.equal(bd.prefill_attn(q, k, v, offsets([1] * 50000)), v)
 
 
 def test_prefill_sequences_never_see_each_other():
@@ -511,6 +549,13 @@ def test_streams_and_two_calls_at_once():
     for _ in range(5):
         for st in streams:
             outs.append(bd.paged_attn(q, cache, table, lens, stream=st))   # own workspaces
+    torch.cuda.synchronize()
+    assert all(torch.equal(ref, x) for x in outs)
+    x, cu = randn((1500, 8, 64), BF, 9), offsets([900, 600])
+    ref = bd.prefill_attn(x, x[:, :4], x[:, 4:], cu)
+    torch.cuda.synchronize()
+    outs = [bd.prefill_attn(x, x[:, :4], x[:, 4:], cu, stream=st) for _ in range(5)
+            for st in streams]
     torch.cuda.synchronize()
     assert all(torch.equal(ref, x) for x in outs)
 

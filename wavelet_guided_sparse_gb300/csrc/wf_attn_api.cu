@@ -64,6 +64,11 @@ int check_opts(const wf_attn_opts* o) {
   if (o == nullptr) return WF_ERR_NULL;
   if (!std::isfinite(o->scale) || !std::isfinite(o->softcap) || o->scale < 0.f || o->softcap < 0.f)
     return WF_ERR_SHAPE;
+  // As the kernels take them: in the log2 domain, the scale over the cap.
+  constexpr float kLog2e = 1.4426950408889634f;
+  if (!std::isfinite(o->scale * kLog2e) || !std::isfinite(o->softcap * kLog2e) ||
+      (o->softcap > 0.f && !std::isfinite(std::max(o->scale, 1.f) / o->softcap)))
+    return WF_ERR_SHAPE;
   if (!aligned4(o->prefix) || !aligned4(o->slopes)) return WF_ERR_ALIGNMENT;
   return WF_OK;
 }

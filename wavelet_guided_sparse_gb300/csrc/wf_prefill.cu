@@ -266,14 +266,13 @@ struct ScoreMap {
 // is linear in i), before it (-1), or neither (0).
 //
 // The cap: while every |s scale / cap| of the warp's chunk is at most 1/2, the
-// usual case, an odd polynomial on the FMA pipe, two scores an operation:
-// tanh(x) / x of degree 4 in x^2, fitted by Chebyshev interpolation on [0,
-// 1/4] (error of tanh below 2^-22 with the fp32 roundings), its coefficients
-// scaled so that it takes s itself.
-// Otherwise tanh(x) = 1 - 2 / (1 + e^(2x)) on the special-function unit, two
-// scores sharing one reciprocal (1/a = b / (a b)); with 2x log2 e clamped at
-// 60 the product stays finite, and 2 / (1 + 2^60) is far below fp32's step
-// at 1.
+// usual case, the polynomial of tanh_exp2 on the FMA pipe, two scores an
+// operation, its coefficients scaled so that it takes s itself.  Otherwise
+// tanh(x) = 1 - 2 / (1 + e^(2x)) on the special-function unit, two scores
+// sharing one reciprocal (1/a = b / (a b)); with 2x log2 e clamped at 60 the
+// product stays finite, and 2 / (1 + 2^60) is far below fp32's step at 1.
+// Caps so far from the scale that the scaled coefficients would leave fp32's
+// range (above some thousands, below a thousandth) take tanh_exp2 as it is.
 template <bool CAP, bool BIAS, bool LINEAR>
 __device__ __forceinline__ void map_chunk(float* s, const ScoreOpts& o, const ScoreMap& c,
                                           float d0, float sg) {
@@ -296,7 +295,7 @@ __device__ __forceinline__ void map_chunk(float* s, const ScoreOpts& o, const Sc
     big0 = fmaxf(big0, fmaxf(fabsf(s[i]), fabsf(s[i + 1])));
     big1 = fmaxf(big1, fmaxf(fabsf(s[i + 2]), fabsf(s[i + 3])));
   }
-  if (__all_sync(0xffffffffu, fmaxf(big0, big1) * o.scale <= 0.5f)) {
+  if (__all_sync(0xffffffffu, fmaxf(big0, big1) * o.scale <= o.bend_max)) {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       const uint64_t x = pack2(s[i], s[i + 1]), u = mul2(x, x);
@@ -304,6 +303,16 @@ __device__ __forceinline__ void map_chunk(float* s, const ScoreOpts& o, const Sc
 #pragma unroll
       for (int e = 3; e >= 0; --e) q = fma2(q, u, c.bend[e]);
       unpack2(BIAS ? fma2(x, q, bias(i)) : mul2(x, q), s[i], s[i + 1]);
+    }
+    return;
+  }
+  if (o.bend_max < 0.f) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      float x = 0.f, y = 0.f;
+      if (BIAS) unpack2(bias(i), x, y);
+      s[i] = fmaf(o.cap, tanh_exp2(s[i] * o.scale), x);
+      s[i + 1] = fmaf(o.cap, tanh_exp2(s[i + 1] * o.scale), y);
     }
     return;
   }
@@ -755,11 +764,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       ScoreMap map;
       if (CAP || BIAS) {
         map.scale = pack2(p.o.scale, p.o.scale);
-        constexpr float kBend[5] = {1.f, -0.333330721f, 0.133248284f, -0.0529892407f, 0.0171413198f};
+        constexpr float bend[5] = {kBend[0], kBend[1], kBend[2], kBend[3], kBend[4]};
         float unit = p.o.cap * p.o.scale;
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
-          map.bend[i] = pack2(kBend[i] * unit, kBend[i] * unit);
+          map.bend[i] = pack2(bend[i] * unit, bend[i] * unit);
           unit *= p.o.scale * p.o.scale;
         }
         map.slope = BIAS ? __ldg(p.o.slopes + max(0, min(head, a.q_heads - 1))) * kLog2e : 0.f;
