@@ -7,9 +7,10 @@
 // (ty, tx) owns four rows and, of a 64-key tile, keys tx, tx + 16, ...; then
 // of the output columns float4s tx, tx + 16.  One pass over the keys with the
 // running maximum and sum; the weights pass through shared memory within a
-// half warp.  Bound by the operand reads from shared memory: five 16-byte
-// reads a thread per 16 (QK) to 32 FMAs; 32 heads, 2048 keys, d = 128:
-// 2246 us, 30.6 TFLOP/s of the pipes' 80.
+// half warp.  32 heads, 2048 rows and keys, d = 128: 2246 us, 30.6 TFLOP/s of
+// the pipes' 80.  At 119 KB of shared memory eight warps share an SM, whose
+// chains of shared-memory reads and FMAs bound it: fetching the next tile into
+// registers meanwhile (2215 us) or four weights a read (2302) changed little.
 #include <algorithm>
 
 #include "wf_attn.cuh"
