@@ -39,7 +39,7 @@
 // 15 value rows there, and the product stops at the next multiple of 16.
 //
 // Measured (32 query heads, 8 of keys, d = 128): 8192 rows over 8192 keys
-// 703 us, 1564 TFLOP/s, 81 % of cuBLAS's bf16 rate; causal 371 us.  The
+// 709 us, 1551 TFLOP/s, 80 % of cuBLAS's bf16 rate; causal 374 us.  The
 // softmax bounds it: a step of 128 keys for both tiles takes 2930 cycles, of
 // which the products fill 2048; the exponentials, FMAs and conversions of
 // 2 x 128 x 128 scores and the two hand-overs between the roles fill the
