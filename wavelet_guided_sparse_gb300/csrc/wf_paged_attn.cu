@@ -202,8 +202,9 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
       }
       if (lane == 0) {
         bars.valid[st] = valid;
-        mbar_arrive_expect_tx(&bars.full[st], parts * box_bytes +
-                                                  (first ? rows * D * static_cast<int>(sizeof(T)) : 0));
+        mbar_arrive_expect_tx(&bars.full[st],
+                              parts * box_bytes +
+                                  (first ? rows * D * static_cast<int>(sizeof(T)) : 0));
       }
       __syncwarp();
 #pragma unroll
@@ -745,7 +746,8 @@ PagedPlan plan_paged(const PagedArgs& a, int sm_count) {
                         ((rows + p.row_block - 1) / p.row_block);
   const int64_t tiles =
       units * ((static_cast<int64_t>(a.table_pages) * a.page_size + KT - 1) / KT);
-  p.ctas = static_cast<int>(std::min<int64_t>(sm_count * (p.row_block == 16 && a.dtype == WF_BF16 ? 2 : 1), tiles));
+  const int per_sm = p.row_block == 16 && a.dtype == WF_BF16 ? 2 : 1;
+  p.ctas = static_cast<int>(std::min<int64_t>(sm_count * per_sm, tiles));
   p.part_bytes = static_cast<size_t>(p.ctas) * 2 * p.row_block * (a.head_dim + 2) * sizeof(float);
   return p;
 }

@@ -24,9 +24,9 @@
 // behind every limit are never loaded.  The running maximum is only raised
 // when a score exceeds it by more than 8 (in log2), and O rescaled in tensor
 // memory then: the weights stay below 2^8, which costs no accuracy in fp32 or
-// bf16, and after the first tiles O is hardly ever touched.  Weights are rounded to bf16 for the product with
-// the values (half a step, 2^-8 relative each, as any bf16 operand); their sum
-// is taken in fp32 before that rounding.
+// bf16, and after the first tiles O is hardly ever touched.  Weights are
+// rounded to bf16 for the product with the values (half a step, 2^-8 relative
+// each, as any bf16 operand); their sum is taken in fp32 before that rounding.
 //
 // A CTA stays on its SM: warp 2 claims blocks of the grid that have not
 // started yet (cluster launch control: dynamic balance without a counter in
