@@ -163,6 +163,9 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
                           (key >> tp.page_shift));
       }
     };
+    unsigned every[NS];  // the lanes with a part of a full stage
+#pragma unroll
+    for (int i = 0; i < NS; ++i) every[i] = __ballot_sync(0xffffffffu, sub + i * kSubs < boxes);
     int fill = 0, units = 0, st = 0;
     uint32_t phase = 1;  // of the stage's last release (first time: none yet)
     int row0 = 0, rows = 0, kvh = 0;
@@ -186,7 +189,8 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         if (!ok) break;
       }
       const int key0 = static_cast<int>(at - u.begin) * KT;
-      int valid = 0, parts = 0;
+      unsigned live[NS];
+      int parts = 0;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int box = sub + i * kSubs;
@@ -195,12 +199,16 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
             raise_flag(a.status, WF_DEV_BAD_INDEX);
           page[i] = -1;
         }
-        const unsigned live = __ballot_sync(0xffffffffu, page[i] >= 0);
-        parts += __popc(live);
-#pragma unroll
-        for (int e = 0; e < kSubs; ++e) valid |= ((live >> (e * 2 * KB)) & 1) << (i * kSubs + e);
+        live[i] = __ballot_sync(0xffffffffu, page[i] >= 0);
+        parts += __popc(live[i]);
       }
       if (lane == 0) {
+        int valid = (1 << boxes) - 1;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+          if (live[i] != every[i])
+            for (int e = 0; e < kSubs; ++e)
+              if (!((live[i] >> (e * 2 * KB)) & 1)) valid &= ~(1 << (i * kSubs + e));
         bars.valid[st] = valid;
         mbar_arrive_expect_tx(&bars.full[st],
                               parts * box_bytes +
