@@ -1,0 +1,44 @@
+"""GPU checks of calls at the edges of the paged append and the dense
+attentions: positions that fp32 does not hold, what follows a call in a graph,
+visible infinities and largest values, tables of high frequencies, extreme
+scales and caps."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from dense_common import attend, check, f64, half_step, rotation_bound
+from test_gpu_dense_attn import BF, F32, i32, make_table, offsets, randn, slope_list
+from wavelet_guided_sparse_gb300 import binding as bd
+
+pytestmark = pytest.mark.gpu
+
+
+def one_cache(k, v, page=16, seed=0):
+    """A paged cache holding one sequence's rows k, v [n, hkv, d], and its table."""
+    n, hkv, d = k.shape
+    table, pages = make_table([n], page, seed)
+    cache = bd.alloc_paged_cache(pages, hkv, page, d, k.dtype, "cuda")
+    bd.paged_append(k, v, cache, table, offsets([n]), i32([0]))
+    return cache, table
+
+
+@pytest.mark.parametrize("dtype,cap,new", [(BF, 0.0, 1), (BF, 30.0, 3), (F32, 0.0, 2)])
+def test_paged_bias_counts_distances_past_2_to_24(dtype, cap, new):
+    # A cache of more than 2^24 rows: one page repeated, but for a window of
+    # distinct pages at its end.  Rows before the window weigh e^-400 at most.
+    page, d, n, tail = 256, 64, 2 ** 24 + 65, 17
+    need = -(-n // page)
+    table = torch.zeros((1, need), dtype=torch.int32, device="cuda")
+    table[0, -tail:] = torch.arange(1, tail + 1, dtype=torch.int32)
+    cache = {x: randn((tail + 1, 1, page, d), dtype, s) for s, x in enumerate(("K", "V"))}
+    slopes = torch.tensor([0.84, 0.5, 0.25, 0.1], device="cuda")
+    q = randn((1, new, 4, d), dtype, 5)
+    o, lse = bd.paged_attn(q, cache, table, i32([n]), softcap=cap, slopes=slopes, with_lse=True)
+    w = n - (need - tail) * page
+    k, v = (f64(cache[x][1:]).reshape(-1, 1, d)[:w] for x in ("K", "V"))
+    ro, rl, ob, lb = attend(f64(q[0]), k, v, dtype, True, 0, cap, slopes.cpu().numpy())
+    check(f64(lse[0]), rl, lb, "lse")
+    check(f64(o[0]), ro, ob, "O")

@@ -281,16 +281,15 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
       const int rows = min(RT, g * a.n_new - row0);
       const int64_t base = static_cast<int64_t>(u.seq) * a.n_new * a.q_heads + kvh * g;
       // This lane's two query rows: position, key limit, slope.
-      int limit[2];
-      float posf[2], slope[2];
+      int pos[2], limit[2];
+      float slope[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = row0 + rt * 16 + gid + 8 * h;
         const bool live = r - row0 < rows;
         const int i = live ? r / g : 0, hd = live ? r - i * g : 0;
-        const int pos = len - a.n_new + i;
-        limit[h] = p.o.causal ? min(len, max(pos + 1, prefix)) : len;
-        posf[h] = static_cast<float>(pos);
+        pos[h] = len - a.n_new + i;
+        limit[h] = p.o.causal ? min(len, max(pos[h] + 1, prefix)) : len;
         slope[h] = BIAS ? __ldg(p.o.slopes + kvh * g + hd) * kLog2e / mul : 0.f;
       }
       // The unit's query rows arrive with its first tile.
@@ -397,13 +396,16 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
             for (int e = 0; e < 4; ++e) s[n][e] = tanh_exp2(s[n][e] * p.o.scale);
         }
         if (BIAS) {
+          // Distances from the tile's first key as whole numbers: positions past
+          // 2^24 do not fit fp32, the distances that weigh anything do.
+          const float d0[2] = {static_cast<float>(pos[0] - key0 - 2 * tig),
+                               static_cast<float>(pos[1] - key0 - 2 * tig)};
 #pragma unroll
           for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float key = static_cast<float>(key0 + n * 8 + 2 * tig + (e & 1));
-              s[n][e] = fmaf(-slope[e >> 1], fabsf(posf[e >> 1] - key), s[n][e]);
-            }
+            for (int e = 0; e < 4; ++e)
+              s[n][e] = fmaf(-slope[e >> 1],
+                             fabsf(d0[e >> 1] - static_cast<float>(n * 8 + (e & 1))), s[n][e]);
         }
         if (edge) {
 #pragma unroll
