@@ -42,3 +42,34 @@ def test_paged_bias_counts_distances_past_2_to_24(dtype, cap, new):
     ro, rl, ob, lb = attend(f64(q[0]), k, v, dtype, True, 0, cap, slopes.cpu().numpy())
     check(f64(lse[0]), rl, lb, "lse")
     check(f64(o[0]), ro, ob, "O")
+
+
+@pytest.mark.parametrize("lens", [[0] * 7, [1 + i % 64 for i in range(2000)], [64] * 38])
+def test_what_follows_in_a_graph_sees_finished_outputs(lens):
+    # Contexts of at most one tile: no unit is split, so nothing is left to the
+    # joining launch, and the nodes behind it read and overwrite at once.
+    hq, hkv, d, page = 8, 4, 128, 32
+    s = len(lens)
+    table, pages = make_table([64] * s, page, 3)
+    cache = {x: randn((pages, hkv, page, d), BF, i) for i, x in enumerate(("K", "V"))}
+    q = randn((s, 1, hq, d), BF, 4)
+    ws = bd.alloc_paged_attn_workspace(q, cache, table)
+    first, held = i32(lens), i32(lens)
+    ref, ref_lse = bd.paged_attn(q, cache, table, first, ws, with_lse=True)
+    torch.cuda.synchronize()
+    o, seen = torch.empty_like(ref), torch.empty_like(ref)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        held.copy_(first)
+        bd.paged_attn(q, cache, table, held, ws, out=o)
+        held.add_(1)
+        seen.copy_(o)
+        o.fill_(7.0)
+    for _ in range(50):
+        seen.fill_(7.0)
+        graph.replay()
+        assert torch.equal(seen, ref) and torch.equal(held, first + 1)
+    if s == 7:
+        assert (ref == 0).all() and (ref_lse == -math.inf).all()
