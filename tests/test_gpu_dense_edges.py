@@ -73,3 +73,41 @@ def test_what_follows_in_a_graph_sees_finished_outputs(lens):
         assert torch.equal(seen, ref) and torch.equal(held, first + 1)
     if s == 7:
         assert (ref == 0).all() and (ref_lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_paged_largest_values_behind_a_lower_maximum(dtype):
+    # The key of the largest value scores 5 above all others, far behind them: its
+    # weight must not exceed 1 on the way.  Many tiles a CTA: 64 like sequences.
+    s, h, d, n, at = 64, 4, 64, 700, 690
+    q, k, v = torch.zeros((s, 1, h, d), device="cuda"), torch.zeros((n, h, d), device="cuda"), \
+        randn((n, h, d), F32, 1)
+    q[..., 0] = 1.0
+    k[at, :, 0] = 5.0 * math.sqrt(d)
+    v[at, :, 1] = 3e38
+    q, k, v = q.to(dtype), k.to(dtype), v.to(dtype)
+    cache, table = one_cache(k, v)
+    o, lse = bd.paged_attn(q, cache, table.expand(s, -1).contiguous(), i32([n] * s), with_lse=True)
+    ro, rl, ob, lb = attend(f64(q[0]), f64(k), f64(v), dtype, True)
+    for i in range(s):
+        check(f64(lse[i]), rl, lb, "lse")
+        check(f64(o[i]), ro, ob, "O")
+
+
+@pytest.mark.parametrize("at", [0, 150, 299])
+@pytest.mark.parametrize("dtype,cap,bias", [(BF, 0.0, False), (BF, 50.0, False), (BF, 0.0, True),
+                                            (F32, 0.0, False)])
+def test_prefill_largest_values_behind_a_lower_maximum(dtype, cap, bias, at):
+    n, h, d = 300, 2, 128
+    q, k, v = torch.zeros((n, h, d), device="cuda"), torch.zeros((n, h, d), device="cuda"), \
+        randn((n, h, d), F32, 1)
+    q[..., 0] = 1.0
+    k[at, :, 0] = 5.0 * math.sqrt(d)
+    v[at, :, 1] = 3e38
+    q, k, v = q.to(dtype), k.to(dtype), v.to(dtype)
+    slopes = torch.zeros(h, device="cuda") if bias else None
+    o, lse = bd.prefill_attn(q, k, v, offsets([n]), causal=False, softcap=cap, slopes=slopes,
+                             with_lse=True)
+    ro, rl, ob, lb = attend(f64(q), f64(k), f64(v), dtype, False, 0, cap)
+    check(f64(lse), rl, lb, "lse")
+    check(f64(o), ro, ob, "O")

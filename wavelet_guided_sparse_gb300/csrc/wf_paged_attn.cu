@@ -16,8 +16,10 @@
 // The products are mma.sync m16n8k16 (bf16 in, fp32 accumulate): at 16 rows a
 // 128-row tcgen05 tile would be seven eighths empty, and the pipe is far
 // from the bound.  Every warp keeps its own running (max, sum, O) over its
-// keys, the maximum raised lazily (only past 2^8); the warps of a row tile
-// add up once per unit, in a fixed order.
+// keys, in weights of at most 1 (a value of the type's largest must not
+// overflow on the way); the maximum is raised lazily: 8 (in log2; fp32: 1)
+// above the score that raised it, so that only a score beyond that raises it
+// again.  The warps of a row tile add up once per unit, in a fixed order.
 //
 // fp32 operands meet the tensor cores as two tf32 parts each (x = hi + lo to
 // 2^-22; hi hi + hi lo + lo hi): the error of a product stays below
@@ -46,7 +48,10 @@ namespace wf {
 namespace {
 
 constexpr int KT = kPagedTile;  // keys per tile
-constexpr float kLazy = 8.f;    // log2 growth of a maximum that is tolerated
+// What a raised maximum is set above the score that raised it (log2).  fp32: 1,
+// since the exponents' arguments round in proportion to their size.
+template <typename T>
+constexpr float kHeadroom = sizeof(T) == 2 ? 8.f : 1.f;
 
 // An fp32 word as two tf32 parts, x = hi + lo to 2^-22 relative.
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
@@ -425,12 +430,12 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         }
         // A row's lanes must agree on its maximum; whether any has grown too
         // far, every lane can tell from its own part.
-        if (__any_sync(0xffffffffu, mx[0] * mul > m[0] + kLazy || mx[1] * mul > m[1] + kLazy)) {
+        if (__any_sync(0xffffffffu, mx[0] * mul > m[0] || mx[1] * mul > m[1])) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * mul;
-            const float mn = fmaxf(m[h], mx[h]);
+            const float mn = mx[h] > m[h] ? mx[h] + kHeadroom<T> : m[h];
             const float f = mn == -INFINITY ? 1.f : fast_exp2(m[h] - mn);
             m[h] = mn;
             l[h] *= f;

@@ -21,10 +21,11 @@
 // Visible keys of a row are always a prefix [0, limit) of its sequence
 // (limit = max(position + 1, prefix) under the causal mask), so a mask is a
 // word of bits per 32 keys, only on tiles that cross some limit, and tiles
-// behind every limit are never loaded.  The running maximum is only raised
-// when a score exceeds it by more than 8 (in log2), and O rescaled in tensor
-// memory then: the weights stay below 2^8, which costs no accuracy in fp32 or
-// bf16, and after the first tiles O is hardly ever touched.  Weights are
+// behind every limit are never loaded.  The running maximum is set 8 (in log2)
+// above the score that raises it and raised again, O rescaled in tensor memory,
+// only by a score beyond that: after the first tiles O is hardly ever touched,
+// and the weights stay below 1, so that a value of the type's largest does not
+// overflow on the way.  Weights are
 // rounded to bf16 for the product with the values (half a step, 2^-8 relative
 // each, as any bf16 operand); their sum is taken in fp32 before that rounding.
 //
@@ -67,7 +68,7 @@ static_assert(8 * kSoftmaxRegs + 4 * kIssueRegs <= 12 * 168, "beyond the launch'
 // Warps 0-3 issue, 4-7 and 8-11 are the softmax groups.
 constexpr int kProducts = 0, kCopies = 1, kItems = 2;
 constexpr int kTileRows = 128;  // query rows of a tile, keys of a tile
-constexpr float kLazy = 8.f;    // log2 growth of a maximum that is tolerated
+constexpr float kHeadroom = 8.f;  // a maximum above the score that raised it (log2)
 
 template <int D>
 struct PreShape {
@@ -382,14 +383,14 @@ __device__ __forceinline__ void chunk_weights(const float* s, float mul, float m
   }
 }
 
-// Rows whose new score exceeds the maximum by more than kLazy raise it to that
-// score, exactly: the weight of a row's only (or outstanding) key is then 1
-// and meets no rounding.  Returns the factor for what has been summed.
+// Rows whose new score exceeds the maximum raise it to kHeadroom above that
+// score: the weight of a row's only (or outstanding) key is then 2^-8 and meets
+// no rounding.  Returns the factor for what has been summed.
 __device__ __forceinline__ float raise_max(float& m, float mt) {
-  if (!(mt > m + kLazy)) return 1.f;
+  if (!(mt > m)) return 1.f;
   const float old = m;
-  m = mt;
-  return fast_exp2(old - mt);
+  m = mt + kHeadroom;
+  return fast_exp2(old - m);
 }
 
 template <int D>
@@ -814,7 +815,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             while (true) {
               add0 = add1 = 0;
               chunk_weights<32>(s, 1.f, m, pk, add0, add1);
-              if (__builtin_expect(!__any_sync(0xffffffffu, mc > m + kLazy), 1)) break;
+              if (__builtin_expect(!__any_sync(0xffffffffu, mc > m), 1)) break;
               // The sum, this tile's weights so far and O follow the maximum.  The
               // weights, 2^8 below what is to come, are rounded a second time.
               const float f = raise_max(m, mc);
@@ -862,8 +863,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (edge) tmem_wait_st();
           mt *= mul;
           if (j == mine - 1) {
-            m = mt;
-          } else if (__any_sync(0xffffffffu, mt > m + kLazy)) {
+            m = mt + kHeadroom;
+          } else if (__any_sync(0xffffffffu, mt > m)) {
             const float f = raise_max(m, mt);
             l *= f;
             scale_output<D>(o_addr, f);
