@@ -562,9 +562,10 @@ int wf_paged_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_new, size_
  *   lse        : device, out, nullable, [n_seqs, n_new, q_heads] fp32
  *   workspace  : device, >= wf_paged_attn_workspace_bytes(); overwritten.
  *                Calls that overlap (captured ones included) need their own
- * Rows behind kv_len never reach the result, whatever they hold; the values
- * of rows below kv_len must be finite even where the mask hides them (keys
- * only where it does not).  Two launches.  Errors: as wf_paged_append. */
+ * Rows behind kv_len never reach the result, whatever they hold, nor do keys
+ * that the mask hides; the values of rows below kv_len must be finite where
+ * the mask hides them.  What is visible counts as the formula has it,
+ * infinities included.  Two launches.  Errors: as wf_paged_append. */
 int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_new, const void* Q,
                   const void* K_pages, const void* V_pages, const int32_t* page_table,
                   const int32_t* kv_len, void* O, float* lse, void* workspace,
@@ -581,9 +582,9 @@ int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_
  *                cu_q[n_docs] on are left as they were
  *   lse        : device, out, nullable, [rows_q, q_heads] fp32
  *   workspace  : device, nullable, >= 256 bytes (status word)
- * Rows of other sequences never reach a result, whatever they hold; a
- * sequence's own values must be finite even where the mask hides them.  One
- * launch.  Errors: as wf_paged_append. */
+ * Rows of other sequences never reach a result, whatever they hold, nor do
+ * keys that the mask hides; a sequence's own values must be finite where the
+ * mask hides them.  One launch.  Errors: as wf_paged_append. */
 int wf_prefill_attn(const wf_prefill_dims* dims, const wf_attn_opts* opts, const void* Q,
                     int64_t q_stride, const void* K, int64_t k_stride, const void* V,
                     int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, void* O,

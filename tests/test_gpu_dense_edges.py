@@ -111,3 +111,51 @@ def test_prefill_largest_values_behind_a_lower_maximum(dtype, cap, bias, at):
     ro, rl, ob, lb = attend(f64(q), f64(k), f64(v), dtype, False, 0, cap)
     check(f64(lse), rl, lb, "lse")
     check(f64(o), ro, ob, "O")
+
+
+@pytest.mark.parametrize("d,hq,hkv,new", [(64, 2, 2, 1), (128, 4, 1, 16), (128, 8, 2, 5),
+                                          (128, 8, 1, 4)])
+def test_paged_fp32_visible_infinities_and_largest_values(d, hq, hkv, new):
+    n, big = 300, torch.finfo(F32).max
+    q, k, v = randn((1, new, hq, d), F32, 1), randn((n, hkv, d), F32, 2), randn((n, hkv, d), F32, 3)
+    q[..., 3] = -q[..., 3].abs() - 0.5
+    k[40, :, 3] = math.inf                    # score -inf: weight 0
+    tiny = 2.0 ** -124
+    q[..., 5] = tiny
+    k[100], k[150] = 0.0, 0.0
+    k[100, :, 5], k[150, :, 5] = big, -big    # scores of +-16 / sqrt(d)
+    v[7, :, 2], v[9, :, 4] = big, math.inf
+    cache, table = one_cache(k, v)
+    o, lse = bd.paged_attn(q, cache, table, i32([n]), causal=False, with_lse=True)
+    # The same products with channel 5 at ordinary size, without the key of weight 0
+    # (scaling by powers of two changes no rounding).
+    keep = np.arange(n) != 40
+    qr, kr, vr = f64(q[0]), f64(k)[keep], f64(v)[keep]
+    qr[..., 5], kr[..., 5] = 1.0, kr[..., 5] * tiny
+    vr[..., 4] = 0.0
+    ro, rl, ob, lb = attend(qr, kr, vr, F32, False)
+    rest = np.arange(d) != 4
+    check(f64(lse[0]), rl, lb, "lse")
+    check(f64(o[0])[..., rest], ro[..., rest], ob[..., rest], "O")
+    assert (o[0, ..., 4] == math.inf).all()
+
+
+@pytest.mark.parametrize("hq,new", [(1, 1), (4, 5), (8, 8)])
+def test_paged_fp32_capped_scores_of_an_infinite_query(hq, new):
+    # Its scores are the cap, either way: two weights, e^cap and e^-cap.
+    n, d, cap = 200, 64, 3.0
+    q, k, v = randn((1, new, hq, d), F32, 1), randn((n, 1, d), F32, 2), randn((n, 1, d), F32, 3)
+    q[..., 9] = math.inf
+    k[..., 9] += torch.where(k[..., 9] < 0, -0.1, 0.1)
+    cache, table = one_cache(k, v)
+    o, lse = bd.paged_attn(q, cache, table, i32([n]), causal=False, softcap=cap, with_lse=True)
+    z = cap * np.sign(f64(k)[:, 0, 9])
+    p = np.exp(z) / np.exp(z).sum()
+    ref, a = p @ f64(v)[:, 0], p @ np.abs(f64(v)[:, 0])
+    # tanh, scaling and the log2 domain: cap (2^-20 + 8 2^-24) of a score, twice; 2^x
+    # 2^-20; the sum of n terms n 2^-24; the last rounding.
+    ez = cap * (2.0 ** -20 + 2.0 ** -21)
+    bound = a * (2 * ez + 2.0 ** -20 + n * 2.0 ** -24) * 1.01 + 2.0 ** -24 * (np.abs(ref) + a)
+    rl = math.log(np.exp(z).sum())
+    check(f64(o[0]), np.broadcast_to(ref, (new, hq, d)), bound, "O")
+    check(f64(lse[0]), np.full((new, hq), rl), ez + 2.0 ** -20 + 2.0 ** -22 * abs(rl), "lse")

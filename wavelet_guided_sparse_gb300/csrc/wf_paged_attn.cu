@@ -22,8 +22,8 @@
 // again.  The warps of a row tile add up once per unit, in a fixed order.
 //
 // fp32 operands meet the tensor cores as two tf32 parts each (x = hi + lo to
-// 2^-22; hi hi + hi lo + lo hi): the error of a product stays below
-// 2^-20 |a||b|, the order of the fp32 sums around it.
+// 2^-22, and no finer than 2^-137; hi hi + hi lo + lo hi): the error of a
+// product stays below 2^-20 |a||b|, the order of the fp32 sums around it.
 //
 // Rows behind a sequence's end (the tail of its last page, stale stages) and
 // rows of bad pages get weights of exactly 0 and their value rows are
@@ -34,8 +34,8 @@
 // 146 us, 91 %; one of 131072 keys with capped scores 85 us, 93 %.  32 heads
 // of keys, a block of 32 tokens, two sequences of 65536 keys: 328 us, 97 %.
 // A few hundred keys: 14 us, of which the split kernel's code, tables and
-// first tile take 9 and the join 5.  fp32, 16 sequences of 8192 keys: 320 us,
-// 49 %, bound by the tf32 products (the FMA pipes took 783).
+// first tile take 9 and the join 5.  fp32, 16 sequences of 8192 keys: 319 us,
+// 50 %, bound by the tf32 products (the FMA pipes took 783).
 #include <algorithm>
 
 #include "wf_attn.cuh"
@@ -53,9 +53,17 @@ constexpr int KT = kPagedTile;  // keys per tile
 template <typename T>
 constexpr float kHeadroom = sizeof(T) == 2 ? 8.f : 1.f;
 
-// An fp32 word as two tf32 parts, x = hi + lo to 2^-22 relative.
+// An fp32 word as two tf32 parts, x = hi + lo to 2^-22 relative.  FINITE: hi
+// stays finite, whatever x.  The largest numbers keep their rest in lo, and an
+// infinity is lo alone, so that of its products only that with the other
+// operand's hi, which has that operand's sign, is infinite (an infinite hi
+// would meet lo's of either sign, or 0).
+template <bool FINITE>
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(x)));
+  if (FINITE)
+    asm("cvt.rna.satfinite.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(x)));
+  else
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(x)));
   const float rest = __uint_as_float(x) - __uint_as_float(hi);
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
 }
@@ -352,6 +360,10 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         // Two accumulators a block halve the chain of dependent products; for
         // fp32 the second one takes the small terms.
         float s[NB][4], s2[NB][4];
+        // Finite first parts cost a 16-row unit, whose queries are split again
+        // every 8 keys, 8 % (16 sequences of 8192 keys: 345 us against 319), more
+        // rows 1 to 6 %, less than the second way below would cost them.
+        constexpr bool kFinite = R > 1;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -363,13 +375,13 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) split_tf32(qf[2 * j + h][c], qh[h][c], ql[h][c]);
+              for (int c = 0; c < 4; ++c) split_tf32<kFinite>(qf[2 * j + h][c], qh[h][c], ql[h][c]);
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
               uint32_t b[4], bh[4], bl[4];
               ldsm_x4((kt ^ ((j & 1) << 6)) + (j >> 1) * (KT * 128) + n * 1024, b);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) split_tf32(b[e], bh[e], bl[e]);
+              for (int e = 0; e < 4; ++e) split_tf32<kFinite>(b[e], bh[e], bl[e]);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 mma_tf32(s[n], qh[h], bh + 2 * h);
@@ -394,6 +406,40 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
+        if constexpr (kWide && !kFinite) {
+          // A score that is not finite shows operands whose first part may not be
+          // (infinities, the largest numbers): once more, by fp32 products.
+          bool odd = false;
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd |= !(fabsf(s[n][e]) < INFINITY);
+          if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {
+            const float* row[2];  // this lane's query rows (dead ones: the unit's first)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r = rt * 16 + gid + 8 * h < rows ? row0 + rt * 16 + gid + 8 * h : row0;
+              row[h] = static_cast<const float*>(a.q) +
+                       (base + static_cast<int64_t>(r / g) * a.q_heads + r % g) * D;
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int r = kg * Shape::kKeys + n * 8 + 2 * tig + (e & 1);
+                const unsigned char* key = ring + st * kStageBytes + r * 128;
+                float sum = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < D / 4; ++c) {
+                  const float4 x = *reinterpret_cast<const float4*>(
+                      key + (c >> 3) * (KT * 128) + (((c & 7) ^ (r & 7)) << 4));
+                  const float4 y = __ldg(reinterpret_cast<const float4*>(row[e >> 1]) + c);
+                  sum = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, sum))));
+                }
+                s[n][e] = sum;
+              }
+          }
+        }
         if (CAP) {
 #pragma unroll
           for (int n = 0; n < NB; ++n)
@@ -470,15 +516,15 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
           for (int kk = 0; kk < NB; ++kk) {
             uint32_t ah[4], al[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split_tf32(pf[kk][e], ah[e], al[e]);
+            for (int e = 0; e < 4; ++e) split_tf32<false>(pf[kk][e], ah[e], al[e]);
 #pragma unroll
             for (int n = 0; n < D / 8; ++n) {
               // Rows 2 tig and 2 tig + 1: the odd row's chunk is the even one's
               // neighbour in its pair.
               const uint32_t at = (vt ^ ((n & 3) << 5)) + (n >> 2) * (KT * 128) + kk * 1024;
               uint32_t bh[2], bl[2];
-              split_tf32(lds32(at), bh[0], bl[0]);
-              split_tf32(lds32((at ^ 16) + 128), bh[1], bl[1]);
+              split_tf32<true>(lds32(at), bh[0], bl[0]);
+              split_tf32<true>(lds32((at ^ 16) + 128), bh[1], bl[1]);
               mma_tf32(o[n], ah, bl);
               mma_tf32(o[n], al, bh);
               mma_tf32(o[n], ah, bh);
