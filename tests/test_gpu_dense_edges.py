@@ -159,3 +159,17 @@ def test_paged_fp32_capped_scores_of_an_infinite_query(hq, new):
     rl = math.log(np.exp(z).sum())
     check(f64(o[0]), np.broadcast_to(ref, (new, hq, d)), bound, "O")
     check(f64(lse[0]), np.full((new, hq), rl), ez + 2.0 ** -20 + 2.0 ** -22 * abs(rl), "lse")
+
+
+@pytest.mark.parametrize("dtype,d,hq,inter,t", [(BF, 128, 8, False, 700), (BF, 64, 4, True, 33),
+                                                (F32, 64, 2, False, 1), (F32, 128, 6, True, 900)])
+def test_append_in_place_queries_are_those_out_of_place(dtype, d, hq, inter, t):
+    page, hkv = 16, 2
+    q, k, v = randn((t, hq, d), dtype, 1), randn((t, hkv, d), dtype, 2), randn((t, hkv, d), dtype, 3)
+    table, pages = make_table([t + 3], page, 0)
+    cache = bd.alloc_paged_cache(pages, hkv, page, d, dtype, "cuda")
+    call = dict(inv_freq=bd.rope_inv_freq(d), interleaved=inter)
+    args = (k, v, cache, table, offsets([t]), i32([3]))
+    ref = bd.paged_append(*args, q=q, **call)["Q"]
+    assert bd.paged_append(*args, q=q, out={"Q": q}, **call)["Q"] is q
+    assert torch.equal(q, ref)

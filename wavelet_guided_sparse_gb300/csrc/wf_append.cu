@@ -124,8 +124,9 @@ __global__ void __launch_bounds__(kThreads, ITERS == 1 ? 6 : 4)
                      : h < qh + a.kv_heads
                          ? static_cast<const T*>(a.k) + t * a.k_stride + (h - qh) * D
                          : static_cast<const T*>(a.v) + t * a.v_stride + (h - qh - a.kv_heads) * D;
-      xa[i] = ldg16_stream(src + ca * V);
-      xb[i] = ldg16_stream(src + cb * V);
+      // Ordinary loads: the queries may be rotated in place.
+      xa[i] = ld16_stream(src + ca * V);
+      xb[i] = ld16_stream(src + cb * V);
     }
   }
 

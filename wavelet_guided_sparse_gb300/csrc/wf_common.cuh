@@ -69,6 +69,14 @@ __device__ __forceinline__ uint4 ldg16_stream(const void* p) {
                : "l"(p));
   return v;
 }
+// The same as an ordinary load, for memory that the kernel also writes.
+__device__ __forceinline__ uint4 ld16_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 __device__ __forceinline__ void widen16(const uint4& v, const __nv_bfloat16*, float* f) {
   f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x);
   f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
