@@ -173,3 +173,23 @@ def test_append_in_place_queries_are_those_out_of_place(dtype, d, hq, inter, t):
     ref = bd.paged_append(*args, q=q, **call)["Q"]
     assert bd.paged_append(*args, q=q, out={"Q": q}, **call)["Q"] is q
     assert torch.equal(q, ref)
+
+
+def test_append_turns_by_high_frequencies_at_far_positions():
+    # Whole-number frequencies, so that the angle of a position is exact in 64 bits.
+    # The bound is that of any rotation: the reduction adds nothing to it.
+    d, h, pos = 64, 2, [2 ** 31 - 1, 2 ** 30 + 12345, 10 ** 9 + 7, -10 ** 9, 3]
+    t = len(pos)
+    freq = [1000.0 - 7 * i for i in range(30)] + [1.0, 2.0]
+    x = randn((t, h, d), F32, 1)
+    table, pages = make_table([t], 8, 0)
+    cache = bd.alloc_paged_cache(pages, h, 8, d, F32, "cuda")
+    got = bd.paged_append(x, x, cache, table, offsets([t]), i32([0]), inv_freq=freq,
+                          positions=i32(pos), keep_keys=True)["K"]
+    ref, a = np.empty((t, h, d)), f64(x)
+    for i, p in enumerate(pos):
+        for j, f in enumerate(freq):
+            c, s = math.cos(p * f), math.sin(p * f)
+            ref[i, :, j] = a[i, :, j] * c - a[i, :, j + 32] * s
+            ref[i, :, j + 32] = a[i, :, j] * s + a[i, :, j + 32] * c
+    check(f64(got), ref, rotation_bound(a, d, False, ref, F32), "keys")

@@ -7,9 +7,10 @@
 // pair i of the first rotary_dim channels by the angle p f_i.
 //
 // Angles.  The caller's f_i become turns per position, f_i / 2π, as 64-bit
-// binary fractions F_i.  p F_i mod 2^64 is then the angle's fraction of a
-// turn, exactly reduced for every p (error p 2^-65 turns), and its top bits
-// go to sincospi: no angle is ever formed whose rounding grows with p.
+// binary fractions F_i, rounded to their last place.  p F_i mod 2^64 is then
+// the angle's fraction of a turn, reduced without error, off by about p 2^-65
+// turns for F_i's sake, and its top bits go to sincospi: no angle is ever
+// formed whose rounding grows with p.
 //
 // HBM-bound: every byte is read once and written once.  One thread moves two
 // 16-byte chunks that rotate together ((c, c + r/2) of the halves form,

@@ -73,6 +73,36 @@ int check_opts(const wf_attn_opts* o) {
   return WF_OK;
 }
 
+// |y| mod 1 as a 64-bit binary fraction, cut; what was cut is added to *below
+// in units of its last place.
+uint64_t fraction_bits(double y, double* below) {
+  y = std::fabs(y);
+  const double f = (y - std::floor(y)) * 0x1p64, cut = std::floor(f);
+  *below += f - cut;
+  return static_cast<uint64_t>(cut);
+}
+
+// x / 2 pi mod 1 as a 64-bit binary fraction, to about half its last place for
+// |x| up to 2^40.  The quotient is the sum of two doubles, formed with 2 pi as
+// the sum of three: positions multiply its error, so that one double's (2^-56
+// at x = 1) would show at far positions and high frequencies.
+uint64_t turn_fraction(double x) {
+  constexpr double kTwoPi[3] = {0x1.921fb54442d18p+2, 0x1.1a62633145c07p-52, -0x1.f1976b7ed8fbcp-108};
+  const double y = std::fabs(x), hi = y / kTwoPi[0];
+  // What hi leaves of y; the first step is exact.
+  const double rest = std::fma(-hi, kTwoPi[1], std::fma(-hi, kTwoPi[0], y)) - hi * kTwoPi[2];
+  const double lo = rest / kTwoPi[0];
+  double below = 0.0, minus = 0.0;
+  uint64_t bits = fraction_bits(hi, &below);
+  if (lo < 0.0) {
+    bits -= fraction_bits(lo, &minus);
+  } else {
+    bits += fraction_bits(lo, &below);
+  }
+  bits += static_cast<uint64_t>(std::llround(below - minus));
+  return x < 0.0 ? 0 - bits : bits;
+}
+
 float scale_of(const wf_attn_opts* o, int head_dim) {
   return o->scale != 0.f ? o->scale : 1.f / std::sqrt(static_cast<float>(head_dim));
 }
@@ -129,13 +159,9 @@ int wf_paged_append(const wf_page_dims* dims, int32_t n_rows, const void* Q, int
     return WF_ERR_ALIGNMENT;
   if (workspace != nullptr && workspace_bytes < kHeaderBytes) return WF_ERR_WORKSPACE;
   wf::RopeTurns turns = {};
-  constexpr double kTwoPi = 6.283185307179586476925286766559;
   for (int i = 0; i < rotary_dim / 2; ++i) {
     if (!std::isfinite(inv_freq[i])) return WF_ERR_SHAPE;
-    double f = inv_freq[i] / kTwoPi;  // turns per position, its fraction in [0, 1)
-    f -= std::floor(f);
-    f = std::ldexp(f, 64);
-    turns.f[i] = f < 18446744073709551616.0 ? static_cast<uint64_t>(f) : 0;
+    turns.f[i] = turn_fraction(inv_freq[i]);
   }
   wf::AppendArgs a = {};
   a.q = Q;
