@@ -193,3 +193,24 @@ def test_append_turns_by_high_frequencies_at_far_positions():
             ref[i, :, j] = a[i, :, j] * c - a[i, :, j + 32] * s
             ref[i, :, j + 32] = a[i, :, j] * s + a[i, :, j + 32] * c
     check(f64(got), ref, rotation_bound(a, d, False, ref, F32), "keys")
+
+
+@pytest.mark.parametrize("cap,scale", [(1e-38, None), (0.0, 1e-38), (1e30, None)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_bias_beside_extreme_scales_and_caps(dtype, cap, scale):
+    # Scores that vanish beside the bias (or meet an ordinary one under a far cap).
+    d, n, h = 128, 200, 2
+    q, k, v = (randn((n, h, d), dtype, s) for s in (1, 2, 3))
+    slopes = torch.tensor([0.5, 0.03125], device="cuda")
+    sl = slopes.cpu().numpy()
+    bend = min(cap, 20.0) if cap else None
+    ro, rl, ob, lb = attend(f64(q), f64(k), f64(v), dtype, True, 0, cap, sl, scale, bend=bend)
+    o, lse = bd.prefill_attn(q, k, v, offsets([n]), softcap=cap, scale=scale, slopes=slopes,
+                             with_lse=True)
+    check(f64(lse), rl, lb, "lse")
+    check(f64(o), ro, ob, "O")
+    cache, table = one_cache(k, v)
+    o, lse = bd.paged_attn(q[None, -9:], cache, table, i32([n]), softcap=cap, scale=scale,
+                           slopes=slopes, with_lse=True)
+    check(f64(lse[0]), rl[-9:], lb[-9:], "lse over pages")
+    check(f64(o[0]), ro[-9:], ob[-9:], "O over pages")

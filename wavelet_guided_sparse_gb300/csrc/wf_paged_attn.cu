@@ -265,7 +265,8 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
     const int gid = lane >> 2, tig = lane & 3;
     idle_sequences<T>(a, p.w.max_len, blockIdx.x, gridDim.x, threadIdx.x,
                                   kConsumerThreads);
-    const float mul = CAP ? p.o.cap : p.o.scale;
+    // Scores enter the exponent as fma(s, mul, -m); biased ones are whole before.
+    const float unit = CAP ? p.o.cap : p.o.scale, mul = BIAS ? 1.f : unit;
     // ldmatrix lane addresses within a tile: keys as B (rows = keys), values
     // transposed (rows = keys); 16-byte chunk c of row r sits at c ^ (r % 8),
     // so a step along a row is an exclusive or of bits 5-6 (and a column
@@ -303,7 +304,7 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         const int i = live ? r / g : 0, hd = live ? r - i * g : 0;
         pos[h] = len - a.n_new + i;
         limit[h] = p.o.causal ? min(len, max(pos[h] + 1, prefix)) : len;
-        slope[h] = BIAS ? __ldg(p.o.slopes + kvh * g + hd) * kLog2e / mul : 0.f;
+        slope[h] = BIAS ? __ldg(p.o.slopes + kvh * g + hd) * kLog2e : 0.f;
       }
       // The unit's query rows arrive with its first tile.
       ok = ok && warp_wait(&bars.full[st], phase, &bars.abort, a.status);
@@ -455,8 +456,8 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
           for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              s[n][e] = fmaf(-slope[e >> 1],
-                             fabsf(d0[e >> 1] - static_cast<float>(n * 8 + (e & 1))), s[n][e]);
+              s[n][e] = fmaf(s[n][e], unit, -slope[e >> 1] *
+                             fabsf(d0[e >> 1] - static_cast<float>(n * 8 + (e & 1))));
         }
         if (edge) {
 #pragma unroll
