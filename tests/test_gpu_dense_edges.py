@@ -214,3 +214,23 @@ def test_bias_beside_extreme_scales_and_caps(dtype, cap, scale):
                            slopes=slopes, with_lse=True)
     check(f64(lse[0]), rl[-9:], lb[-9:], "lse over pages")
     check(f64(o[0]), ro[-9:], ob[-9:], "O over pages")
+
+
+@pytest.mark.parametrize("scale,low,top,value", [
+    (0.5584592656208399, 1.234375, 13.375, 1.25), (0.4848162855389709, 1.421875, 15.625, 1.4375),
+    (0.47954654330485164, 1.4375, 12.875, 1.5), (0.4644029682531195, 1.484375, 13.375, 1.6875)])
+def test_prefill_weights_meet_one_rounding(scale, low, top, value):
+    # 95 like weights just short of a rounding midpoint, and behind them in the same
+    # tile one key that outweighs them by 2^8 to 2^11: rounded once more when they are
+    # rescaled (or by a factor that is itself rounded), they leave the bound.
+    h, d, n = 2, 128, 97
+    q, k, v = (torch.zeros((n, h, d), device="cuda") for _ in range(3))
+    q[..., 0] = 1.0
+    k[1:96, :, 0], k[96, :, 0] = -low, top
+    v[1:96] = value
+    q, k, v = q.to(BF), k.to(BF), v.to(BF)
+    o, lse = bd.prefill_attn(q, k, v, offsets([n]), causal=False, scale=scale,
+                             slopes=torch.zeros(h, device="cuda"), with_lse=True)
+    ro, rl, ob, lb = attend(f64(q), f64(k), f64(v), BF, False, scale=float(np.float32(scale)))
+    check(f64(lse), rl, lb, "lse")
+    check(f64(o), ro, ob, "O")

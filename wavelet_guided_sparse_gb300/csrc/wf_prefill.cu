@@ -386,11 +386,22 @@ __device__ __forceinline__ void chunk_weights(const float* s, float mul, float m
 // Rows whose new score exceeds the maximum raise it to kHeadroom above that
 // score: the weight of a row's only (or outstanding) key is then 2^-8 and meets
 // no rounding.  Returns the factor for what has been summed.
-__device__ __forceinline__ float raise_max(float& m, float mt) {
+//
+// `rounded`: the sum of weights that are in bf16 already and follow by the same
+// factor.  It is a power of two and rounds them no further, with the maximum up
+// to 1 lower, unless they come to less than 2^-9 of the new score's weight: a
+// second rounding of theirs is then lost in that of the result.  (Powers of two
+// always: relative error 0.0022 in place of 0.0021 on a 16384-token prompt with
+// cap and bias, for the outstanding keys' own rounding.)
+__device__ __forceinline__ float raise_max(float& m, float mt, float rounded = 0.f) {
   if (!(mt > m)) return 1.f;
   const float old = m;
   m = mt + kHeadroom;
-  return fast_exp2(old - m);
+  const float f = fast_exp2(old - m);
+  if (!(rounded * f > 0x1p-17f)) return f;  // the new score's weight is 2^-8
+  const float steps = ceilf(old - m);
+  m = old - steps;
+  return __int_as_float((127 + static_cast<int>(steps)) << 23);
 }
 
 template <int D>
@@ -816,11 +827,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               add0 = add1 = 0;
               chunk_weights<32>(s, 1.f, m, pk, add0, add1);
               if (__builtin_expect(!__any_sync(0xffffffffu, mc > m), 1)) break;
-              // The sum, this tile's weights so far and O follow the maximum.  The
-              // weights, 2^8 below what is to come, are rounded a second time.
-              const float f = raise_max(m, mc);
+              // The sum, this tile's weights so far and O follow the maximum.
               float a0, a1;
               unpack2(add2(sum0, sum1), a0, a1);
+              const float f = raise_max(m, mc, a0 + a1);
               l = (l + (a0 + a1)) * f;
               sum0 = sum1 = 0;
               if (c > 0) tmem_wait_st();
