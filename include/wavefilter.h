@@ -489,7 +489,8 @@ typedef struct {
  * key j counts if not causal, or j <= p, or j < prefix[s].  A row without a
  * visible key gets O = 0 and lse = -inf.
  *   scale   : not negative; 0 means 1/sqrt(head_dim)
- *   softcap : 0 means none; max(scale, 1) / softcap must be a finite float
+ *   softcap : 0 means none; max(scale, 1) / softcap must be a finite float,
+ *             scale / softcap a normal one
  *   prefix  : nullable, [n_seqs] int32 (only read with causal)
  *   slopes  : nullable, [q_heads] fp32 */
 typedef struct {

@@ -60,14 +60,19 @@ bool bad_stride(int64_t stride, int heads, int head_dim, int dtype) {
          stride * elem_bytes(dtype) % 16 != 0 || stride > (int64_t{1} << 36);
 }
 
-int check_opts(const wf_attn_opts* o) {
+float scale_of(const wf_attn_opts* o, int head_dim) {
+  return o->scale != 0.f ? o->scale : 1.f / std::sqrt(static_cast<float>(head_dim));
+}
+
+int check_opts(const wf_attn_opts* o, int head_dim) {
   if (o == nullptr) return WF_ERR_NULL;
   if (!std::isfinite(o->scale) || !std::isfinite(o->softcap) || o->scale < 0.f || o->softcap < 0.f)
     return WF_ERR_SHAPE;
   // As the kernels take them: in the log2 domain, the scale over the cap.
   constexpr float kLog2e = 1.4426950408889634f;
   if (!std::isfinite(o->scale * kLog2e) || !std::isfinite(o->softcap * kLog2e) ||
-      (o->softcap > 0.f && !std::isfinite(std::max(o->scale, 1.f) / o->softcap)))
+      (o->softcap > 0.f && (!std::isfinite(std::max(o->scale, 1.f) / o->softcap) ||
+                            !std::isnormal(scale_of(o, head_dim) / o->softcap))))
     return WF_ERR_SHAPE;
   if (!aligned4(o->prefix) || !aligned4(o->slopes)) return WF_ERR_ALIGNMENT;
   return WF_OK;
@@ -101,10 +106,6 @@ uint64_t turn_fraction(double x) {
   }
   bits += static_cast<uint64_t>(std::llround(below - minus));
   return x < 0.0 ? 0 - bits : bits;
-}
-
-float scale_of(const wf_attn_opts* o, int head_dim) {
-  return o->scale != 0.f ? o->scale : 1.f / std::sqrt(static_cast<float>(head_dim));
 }
 
 wf::PagedArgs paged_args(const wf_page_dims* d, int n_new) {
@@ -210,7 +211,7 @@ int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_
   size_t need = 0;
   int st = wf_paged_attn_workspace_bytes(dims, n_new, &need);
   if (st != WF_OK) return st;
-  st = check_opts(opts);
+  st = check_opts(opts, dims->head_dim);
   if (st != WF_OK) return st;
   if (Q == nullptr || K_pages == nullptr || V_pages == nullptr || page_table == nullptr ||
       kv_len == nullptr || O == nullptr || workspace == nullptr)
@@ -249,7 +250,7 @@ int wf_prefill_attn(const wf_prefill_dims* dims, const wf_attn_opts* opts, const
   // Row blocks are counted in 32 bits; rows stay below a grid's limits.
   if (dims->rows_q > (1 << 26) || dims->rows_k > (1 << 30) || dims->n_docs > (1 << 20))
     return WF_ERR_UNSUPPORTED;
-  st = check_opts(opts);
+  st = check_opts(opts, dims->head_dim);
   if (st != WF_OK) return st;
   if (dims->rows_q == 0) return WF_OK;
   if (Q == nullptr || cu_q == nullptr || cu_k == nullptr || O == nullptr ||
