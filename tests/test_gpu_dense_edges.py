@@ -234,3 +234,13 @@ def test_prefill_weights_meet_one_rounding(scale, low, top, value):
     ro, rl, ob, lb = attend(f64(q), f64(k), f64(v), BF, False, scale=float(np.float32(scale)))
     check(f64(lse), rl, lb, "lse")
     check(f64(o), ro, ob, "O")
+
+
+def test_append_returns_what_it_wrote():
+    k, v = randn((4, 2, 64), BF, 1), randn((4, 2, 64), BF, 2)
+    cache = bd.alloc_paged_cache(1, 2, 16, 64, BF, "cuda")
+    spare = {x: torch.empty((4, 2, 64), dtype=BF, device="cuda") for x in ("Q", "K")}
+    args = (k, v, cache, i32([[0]]), offsets([4]), i32([0]))
+    assert bd.paged_append(*args, out=spare) == {}
+    res = bd.paged_append(*args, out=spare, keep_keys=True)
+    assert set(res) == {"K"} and res["K"] is spare["K"] and torch.equal(res["K"], k)

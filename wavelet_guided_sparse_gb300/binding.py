@@ -676,14 +676,14 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, cache: dict, page_table: torc
         ks = _row_stride(k, "k", t, hkv, d, dt, dev)
         vs = _row_stride(v, "v", t, hkv, d, dt, dev)
         hq, qs, qp, qo, ko = hkv, 0, None, None, None
-        res = {} if out is None else dict(out)
+        given, res = out or {}, {}
         if q is not None:
             hq = q.shape[1] if q.dim() == 3 else 0
             qs, qp = _row_stride(q, "q", t, hq, d, dt, dev), q.data_ptr()
-            res["Q"] = _out(res.get("Q"), "out Q", (t, hq, d), dt, dev)
+            res["Q"] = _out(given.get("Q"), "out Q", (t, hq, d), dt, dev)
             qo = res["Q"].data_ptr()
         if keep_keys:
-            res["K"] = _out(res.get("K"), "out K", (t, hkv, d), dt, dev)
+            res["K"] = _out(given.get("K"), "out K", (t, hkv, d), dt, dev)
             ko = res["K"].data_ptr()
         freq, half = inv_freq, 0
         if freq is not None:
