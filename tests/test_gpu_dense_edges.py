@@ -244,3 +244,11 @@ def test_append_returns_what_it_wrote():
     assert bd.paged_append(*args, out=spare) == {}
     res = bd.paged_append(*args, out=spare, keep_keys=True)
     assert set(res) == {"K"} and res["K"] is spare["K"] and torch.equal(res["K"], k)
+
+
+def test_paged_workspace_refuses_queries_without_a_block_axis():
+    q = randn((2, 4, 64), BF, 1)
+    cache = bd.alloc_paged_cache(2, 2, 16, 64, BF, "cuda")
+    for bad in (q, q[0], q[None, :, None]):
+        with pytest.raises(ValueError):
+            bd.alloc_paged_attn_workspace(bad, cache, i32([[0], [1]]))

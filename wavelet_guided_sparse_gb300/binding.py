@@ -707,6 +707,8 @@ def alloc_paged_attn_workspace(q: torch.Tensor, cache: dict, page_table: torch.T
     """Workspace of paged_attn for these tensors' sizes (status word cleared);
     calls that may overlap need one each."""
     with _On(q, stream):
+        if q.dim() != 4:
+            raise ValueError("q must be [n_seqs, n_new, q_heads, head_dim]")
         shape, table = _pages(cache, page_table, q.dtype, q.device)[:2]
         n = ctypes.c_size_t(0)
         _check("wf_paged_attn_workspace_bytes", lib().wf_paged_attn_workspace_bytes(
