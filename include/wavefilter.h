@@ -173,11 +173,11 @@ int wf_step_plan(const wf_dims* dims, const int32_t* k_per_level, wf_plan* plan)
 
 /* Fault injection for tests of the bounded device waits (no counterpart in
  * the paper).  Arms a one-shot injection consumed by the next kernel launch
- * that streams K_p through mbarrier-counted bulk copies (the separate DWT
- * launch of wf_step / wf_dwt_lowpass, or the single-launch wf_step): in its
- * first CTA the first copy of the ring is never issued and the wait for it
- * gives up after `polls` polls (polls >= 1), which raises WF_DEV_WAIT_TIMEOUT
- * in the workspace status word.  Every copy that was issued is still waited
+ * that streams keys through mbarrier-counted copies (the separate DWT launch
+ * of wf_step / wf_dwt_lowpass, the single-launch wf_step, wf_paged_attn, or
+ * wf_prefill_attn of bf16): in its first CTA the first copy of the ring is
+ * never issued and the wait for it gives up after `polls` polls (polls >= 1),
+ * which raises WF_DEV_WAIT_TIMEOUT in the workspace status word.  Every copy that was issued is still waited
  * for, so none is in flight when the kernel ends; the launch returns WF_OK,
  * its outputs are meaningless, and later calls behave normally.
  * polls = 0 disarms.  Process-wide; not for concurrent use with other calls.

@@ -252,3 +252,44 @@ def test_paged_workspace_refuses_queries_without_a_block_axis():
     for bad in (q, q[0], q[None, :, None]):
         with pytest.raises(ValueError):
             bd.alloc_paged_attn_workspace(bad, cache, i32([[0], [1]]))
+
+
+@pytest.mark.parametrize("dtype,new,lens", [(BF, 1, [40]), (BF, 1, [9000, 30000, 70]), (BF, 64, [200]),
+                                            (BF, 9, [5000] * 40), (F32, 1, [64, 64]),
+                                            (F32, 16, [3000] * 30)])
+def test_paged_wait_that_runs_out_is_reported_and_recovers(dtype, new, lens):
+    # The first tile's copies of the first CTA are never issued (nothing else is in
+    # flight when its wait gives up, or it is waited for): the call ends, says so,
+    # and the next one is as before.
+    page, hq, hkv, d = 64, 4, 2, 128
+    table, pages = make_table(lens, page, 1)
+    cache = {x: randn((pages, hkv, page, d), dtype, i) for i, x in enumerate(("K", "V"))}
+    q, n = randn((len(lens), new, hq, d), dtype, 3), i32(lens)
+    ws = bd.alloc_paged_attn_workspace(q, cache, table)
+    ref, lse = bd.paged_attn(q, cache, table, n, ws, with_lse=True)
+    assert bd.read_device_status(ws) == 0
+    bd.inject_wait_timeout(1000)
+    bd.paged_attn(q, cache, table, n, ws)
+    bd.inject_wait_timeout(0)
+    assert bd.read_device_status(ws) == bd.DEV_WAIT_TIMEOUT    # synchronises
+    bd.clear_device_status(ws)
+    o, lse2 = bd.paged_attn(q, cache, table, n, ws, with_lse=True)
+    assert bd.read_device_status(ws) == 0
+    assert torch.equal(o, ref) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("d,hq,lens,cap", [(128, 4, [100], 0.0), (64, 3, [2000, 5, 700], 20.0),
+                                           (128, 8, [6000, 1000], 0.0), (64, 2, [90] * 400, 0.0)])
+def test_prefill_wait_that_runs_out_is_reported_and_recovers(d, hq, lens, cap):
+    q, k, v = (randn((sum(lens), hq, d), BF, s) for s in (1, 2, 3))
+    cu, ws = offsets(lens), bd.alloc_status_workspace("cuda")
+    ref, lse = bd.prefill_attn(q, k, v, cu, softcap=cap, with_lse=True, ws=ws)
+    assert bd.read_device_status(ws) == 0
+    bd.inject_wait_timeout(1000)
+    bd.prefill_attn(q, k, v, cu, softcap=cap, ws=ws)
+    bd.inject_wait_timeout(0)
+    assert bd.read_device_status(ws) == bd.DEV_WAIT_TIMEOUT
+    bd.clear_device_status(ws)
+    o, lse2 = bd.prefill_attn(q, k, v, cu, softcap=cap, with_lse=True, ws=ws)
+    assert bd.read_device_status(ws) == 0
+    assert torch.equal(o, ref) and torch.equal(lse, lse2)

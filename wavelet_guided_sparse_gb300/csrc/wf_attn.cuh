@@ -84,27 +84,38 @@ __device__ __forceinline__ void store4(__nv_bfloat16* dst, const float* f) {
                                               *reinterpret_cast<const uint32_t*>(&c));
 }
 
+// What the bounded waits of a CTA share (shared memory).
+struct WaitState {
+  int abort;       // a wait of this CTA has given up
+  uint32_t polls;  // the limit of each
+  __device__ __forceinline__ void init(uint32_t limit) {
+    abort = 0;
+    polls = limit;
+  }
+};
+
 // A bounded wait on an mbarrier phase by a whole converged warp, which also
-// ends when another warp of the CTA has given up (*abort); true when the
-// phase has completed.  The first tries stand alone, outside any loop: a try
+// ends when another warp of the CTA has given up; true when the phase has
+// completed.  The first tries stand alone, outside any loop: a try
 // sleeps until the phase completes or its time limit, so it usually
 // suffices, and a wait that is over already costs 70 cycles this way against
 // 220 in the loop (measured in the packed-prompt kernel, whose products wait
 // four times a key tile).  `nap`: nanoseconds between the later polls, for
 // warps with time to spare.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort,
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, WaitState& w,
                                           int32_t* status, uint32_t nap = 0) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+  const uint32_t polls = w.polls;
+  for (uint32_t i = 0; i < polls; ++i) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if (nap != 0) __nanosleep(nap);
     if ((i & 255) == 255 &&
-        __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(abort) != 0))
+        __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&w.abort) != 0))
       return false;
   }
   raise_flag(status, WF_DEV_WAIT_TIMEOUT);
-  *reinterpret_cast<volatile int*>(abort) = 1;
+  *reinterpret_cast<volatile int*>(&w.abort) = 1;
   return false;
 }
 

@@ -104,13 +104,14 @@ struct PagedTcParams {
   CUtensorMap tk, tv;
   PagedParams p;
   int box_rows, page_shift;
+  uint32_t inject_polls;  // fault injection (tests): see the kernel's start
 };
 
 template <int STAGES>
 struct PagedBarriers {
   uint64_t full[STAGES], empty[STAGES], q_empty;
   int valid[STAGES];  // one bit per box of a stage
-  int abort;
+  WaitState wait;
 };
 
 template <typename T, int D, int R, bool CAP, bool BIAS>
@@ -135,13 +136,16 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = a.q_heads / a.kv_heads;
 
+  // Fault injection (tests of the bounded waits): the first CTA's first tile is
+  // never issued, and its waits give up after inject_polls polls.
+  const bool inject = tp.inject_polls != 0 && blockIdx.x == 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars.full[i], 1);
       mbar_init(&bars.empty[i], Shape::kConsumers);
     }
     mbar_init(&bars.q_empty, Shape::kConsumers);
-    bars.abort = 0;
+    bars.wait.init(inject ? tp.inject_polls : kWaitPolls);
     fence_mbar_init();
   }
   const WorkSplit split(work_total(p.w, a.kv_len), gridDim.x);
@@ -193,12 +197,12 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         row0 = (u.unit - kvh * p.row_blocks) * RT;
         rows = min(RT, g * a.n_new - row0);
         if (units++ > 0) {
-          ok = warp_wait(&bars.q_empty, (units - 2) & 1, &bars.abort, a.status);
+          ok = warp_wait(&bars.q_empty, (units - 2) & 1, bars.wait, a.status);
           if (!ok) break;
         }
       }
       if (fill >= kStages) {
-        ok = warp_wait(&bars.empty[st], phase, &bars.abort, a.status);
+        ok = warp_wait(&bars.empty[st], phase, bars.wait, a.status);
         if (!ok) break;
       }
       const int key0 = static_cast<int>(at - u.begin) * KT;
@@ -215,7 +219,8 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         live[i] = __ballot_sync(0xffffffffu, page[i] >= 0);
         parts += __popc(live[i]);
       }
-      if (lane == 0) {
+      const bool issue = !(inject && fill == 0);
+      if (lane == 0 && issue) {
         int valid = (1 << boxes) - 1;
 #pragma unroll
         for (int i = 0; i < NS; ++i)
@@ -230,14 +235,14 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        if (page[i] < 0) continue;
+        if (page[i] < 0 || !issue) continue;
         const int box = sub + i * kSubs, key = key0 + box * tp.box_rows;
         const int y = (page[i] * a.kv_heads + kvh) * a.page_size + (key & (a.page_size - 1));
         tma_load_2d(ring + st * kStageBytes + which * kTileBytes + kb * (KT * 128) +
                         box * box_bytes,
                     map, kb * KC, y, &bars.full[st]);
       }
-      if (first) {
+      if (first && issue) {
         const int i0 = row0 / g, i1 = (row0 + rows - 1) / g;
         for (int i = i0 + lane; i <= i1; i += 32) {
           const int r0 = max(i * g, row0), r1 = min((i + 1) * g, row0 + rows);
@@ -255,10 +260,10 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
       if (at + 1 == u.begin + u.tiles) next_unit(p.w, a.kv_len, u);
       if (at + 1 < w1) read_entries(u, at + 1);
     }
-    if (!ok) {  // no copy may land after the CTA has gone
-      for (int f = max(0, fill - kStages); f < fill; ++f)
-        mbar_wait_bounded(&bars.full[f % kStages], (f / kStages) & 1, a.status);
-    }
+    // No copy may land after the CTA has gone, also where the consumers have
+    // given up behind this warp's last wait.
+    for (int f = max(inject ? 1 : 0, fill - kStages); f < fill; ++f)
+      mbar_wait_bounded(&bars.full[f % kStages], (f / kStages) & 1, a.status);
   } else {
     // ---- consumers
     const int rt = warp % R, kg = warp / R;      // row tile, key group
@@ -307,7 +312,7 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         slope[h] = BIAS ? __ldg(p.o.slopes + kvh * g + hd) * kLog2e : 0.f;
       }
       // The unit's query rows arrive with its first tile.
-      ok = ok && warp_wait(&bars.full[st], phase, &bars.abort, a.status);
+      ok = ok && warp_wait(&bars.full[st], phase, bars.wait, a.status);
       constexpr int KS = D * static_cast<int>(sizeof(T)) / 32;  // steps of a score's product
       constexpr int kHalf = 16 / static_cast<int>(sizeof(T));   // channels of half a step
       uint32_t qf[KS][4];
@@ -337,7 +342,7 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
 #pragma unroll
       for (int w = 4; w < 32; w <<= 1) open = min(open, __shfl_xor_sync(0xffffffffu, open, w));
       for (int i = 0; i < tiles; ++i, key0 += KT) {
-        ok = ok && warp_wait(&bars.full[st], phase, &bars.abort, a.status);
+        ok = ok && warp_wait(&bars.full[st], phase, bars.wait, a.status);
         if (!ok) break;  // given up: only the barriers below, in step with the other warps
         const uint32_t kt = ring_addr + st * kStageBytes + koff;
         const uint32_t vt = ring_addr + st * kStageBytes + kTileBytes + voff;
@@ -772,6 +777,7 @@ cudaError_t launch_tc_rows(const PagedArgs& a, const PagedPlan& plan, cudaStream
   p.box_rows = std::min(a.page_size, KT);
   p.page_shift = 0;
   while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
+  p.inject_polls = consume_wait_injection();
   const cuuint64_t dims[2] = {D, static_cast<cuuint64_t>(a.n_pages) * a.kv_heads * a.page_size};
   const cuuint64_t strides[1] = {D * sizeof(T)};
   const cuuint32_t box[2] = {128 / sizeof(T), static_cast<cuuint32_t>(p.box_rows)};

@@ -82,6 +82,7 @@ struct PrefillTcParams {
   PrefillArgs a;
   ScoreOpts o;
   int pair_heads;  // 1: tiles are heads h, h + 1; 0: row blocks 2b, 2b + 1
+  uint32_t inject_polls;  // fault injection (tests): see the kernel's start
 };
 
 // What a query tile of an item covers.
@@ -109,12 +110,12 @@ struct PreBarriers {
   uint4 claimed;               // response of a claim
   Item it[2];
   uint32_t tmem;
-  int abort;
+  WaitState wait;
 };
 
 __device__ __forceinline__ bool pre_wait(PreBarriers& b, uint64_t* bar, uint32_t parity,
                                          int32_t* status, uint32_t nap = 0) {
-  return warp_wait(bar, parity, &b.abort, status, nap);
+  return warp_wait(bar, parity, b.wait, status, nap);
 }
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z,
@@ -499,6 +500,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const PrefillArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // Fault injection (tests of the bounded waits): the first CTA's first key tile
+  // is never issued, and its waits give up after inject_polls polls.
+  const bool inject = p.inject_polls != 0 && blockIdx.x == 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&bars.full[i], 1);
     for (int i = 0; i < 8; ++i) mbar_init(&bars.done[i], 1);
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     }
     mbar_init(&bars.claim, 1);
     mbar_init(&bars.drain, 1);
-    bars.abort = 0;
+    bars.wait.init(inject ? p.inject_polls : kWaitPolls);
     fence_mbar_init();
   }
   if (warp == kProducts) tmem_alloc(&bars.tmem, 512);
@@ -607,7 +611,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll
           for (int i = 0; i < kStages; ++i)
             if (i == st) step_of[i] = steps + (f > 0 ? (f - 1) >> 1 : 0);
-          if (leader) {
+          if (leader && !(inject && fills == 0)) {
             unsigned char* dst = ring + st * kTileBytes;
             mbar_arrive_expect_tx(&bars.full[st], kTileBytes);
             for (int kb = 0; kb < D / 64; ++kb)
@@ -619,10 +623,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         steps += tiles;
       }
-      if (!ok && leader) {  // nothing of this CTA's copies may land after it has gone
+      // Nothing of this CTA's copies may land after it has gone, also where another
+      // role has given up behind this warp's last wait.
+      if (leader) {
         for (int t = 0; t < 2; ++t)
           if (used[t] > 0) mbar_wait_bounded(&bars.q[t], (used[t] - 1) & 1, a.status);
-        for (uint32_t f = fills > kStages ? fills - kStages : 0; f < fills; ++f)
+        for (uint32_t f = max(inject ? 1 : 0, static_cast<int>(fills) - kStages); f < fills; ++f)
           mbar_wait_bounded(&bars.full[f % kStages], (f / kStages) & 1, a.status);
       }
     } else if (warp == kProducts) {
@@ -1017,6 +1023,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   p.a = a;
   p.o = score_opts(a.scale, a.softcap, a.causal, a.prefix, a.slopes);
   p.pair_heads = (a.q_heads / a.kv_heads) % 2 == 0;
+  p.inject_polls = consume_wait_injection();
   // Without keys no copy of them is ever issued; the maps only have to exist.
   const bool keys = a.rows_k > 0;
   if (!encode_rows(&p.tq, a.q, a.rows_q, a.q_heads, a.head_dim, a.q_stride) ||
