@@ -293,3 +293,71 @@ def test_prefill_wait_that_runs_out_is_reported_and_recovers(d, hq, lens, cap):
     o, lse2 = bd.prefill_attn(q, k, v, cu, softcap=cap, with_lse=True, ws=ws)
     assert bd.read_device_status(ws) == 0
     assert torch.equal(o, ref) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("cap,scale,spread", [(1e-2, 50.0, 3e-5), (1e-2, 2.0, 5e-4), (2e3, 1.0, 40.0)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_small_and_large_caps_form_the_scores(dtype, cap, scale, spread, bias):
+    # Scores about the cap's bend, of a size that the lse shows: its bound is far
+    # below them (small caps), or they decide the row (large ones).
+    d, n, h = 128, 200, 2
+    q, k, v = (randn((n, h, d), dtype, s) for s in (1, 2, 3))
+    q = (q.float() * spread).to(dtype)
+    slopes = torch.tensor([cap / 100, cap / 1000], device="cuda") if bias else None
+    sl = None if slopes is None else slopes.cpu().numpy()
+    ro, rl, ob, lb = attend(f64(q), f64(k), f64(v), dtype, True, 0, cap, sl, scale)
+    flat = np.log(np.arange(1, n + 1))[:, None]          # the lse of scores of 0
+    assert np.median(np.abs(rl - flat) / lb) > 20
+    o, lse = bd.prefill_attn(q, k, v, offsets([n]), softcap=cap, scale=scale, slopes=slopes,
+                             with_lse=True)
+    check(f64(lse), rl, lb, "lse")
+    check(f64(o), ro, ob, "O")
+    cache, table = one_cache(k, v)
+    o, lse = bd.paged_attn(q[None, -9:], cache, table, i32([n]), softcap=cap, scale=scale,
+                           slopes=slopes, with_lse=True)
+    check(f64(lse[0]), rl[-9:], lb[-9:], "lse over pages")
+    check(f64(o[0]), ro[-9:], ob[-9:], "O over pages")
+
+
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, False), (0.0, True), (20.0, True)])
+def test_bf16_visible_infinities_and_largest_values(cap, bias):
+    d, h, n, big, tiny = 128, 4, 300, torch.finfo(BF).max, 2.0 ** -124
+    q, k, v = (randn((n, h, d), BF, s) for s in (1, 2, 3))
+    q[..., 3] = -q[..., 3].abs() - 0.5
+    q[..., 5] = tiny
+    k[100], k[150] = 0.0, 0.0
+    k[100, :, 5], k[150, :, 5] = big, -big    # scores of +-16 / sqrt(d)
+    v[7, :, 2], v[9, :, 4] = big, math.inf
+    keep = np.ones(n, bool)
+    if cap == 0.0 and not bias:
+        k[40, :, 3], keep[40] = math.inf, False       # a score of -inf: weight 0
+    slopes = slope_list(h) / 16 if bias else None
+    # The same products with channel 5 at ordinary size, without the key of weight 0.
+    qr, kr, vr = f64(q), f64(k)[keep], f64(v)[keep]
+    qr[..., 5], kr[..., 5], vr[..., 4] = 1.0, kr[..., 5] * tiny, 0.0
+    rest = np.arange(d) != 4
+    o, lse = bd.prefill_attn(q, k, v, offsets([n]), causal=False, softcap=cap, slopes=slopes,
+                             with_lse=True)
+    ro, rl, ob, lb = attend(qr, kr, vr, BF, False, 0, cap,
+                            None if slopes is None else slopes.cpu().numpy())
+    check(f64(lse), rl, lb, "lse")
+    check(f64(o)[..., rest], ro[..., rest], ob[..., rest], "O")
+    assert (o[..., 4] == math.inf).all()
+    cache, table = one_cache(k, v)
+    o, lse = bd.paged_attn(q[None, -9:], cache, table, i32([n]), causal=False, softcap=cap,
+                           slopes=slopes, with_lse=True)
+    check(f64(lse[0]), rl[-9:], lb[-9:], "lse over pages")
+    check(f64(o[0])[..., rest], ro[-9:][..., rest], ob[-9:][..., rest], "O over pages")
+    assert (o[0, ..., 4] == math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_without_any_key(dtype):
+    q, none = randn((70, 4, 64), dtype, 1), torch.empty((0, 2, 64), dtype=dtype, device="cuda")
+    for causal in (True, False):
+        o, lse = bd.prefill_attn(q, none, none, offsets([50, 20]), offsets([0, 0]), causal=causal,
+                                 with_lse=True)
+        assert (o == 0).all() and (lse == -math.inf).all()
+    o, lse = bd.prefill_attn(q[:0], none, none, offsets([0]), with_lse=True)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
