@@ -361,3 +361,21 @@ def test_prefill_without_any_key(dtype):
         assert (o == 0).all() and (lse == -math.inf).all()
     o, lse = bd.prefill_attn(q[:0], none, none, offsets([0]), with_lse=True)
     assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+@pytest.mark.parametrize("d,hq,hkv,new,n,cap,bias", [
+    (128, 8, 2, 1, 900, 0.0, False), (128, 4, 4, 1, 5000, 20.0, True), (64, 16, 1, 1, 333, 0.0, True),
+    (64, 4, 1, 4, 2000, 0.0, False), (128, 2, 2, 5, 700, 30.0, False)])
+def test_paged_up_to_16_rows_only_the_output_is_rounded(d, hq, hkv, new, n, cap, bias):
+    # Weights in two bf16 parts are good to 2^-15: what is left are fp32's roundings
+    # (attend()'s bound at that type) and the output's half a step.
+    q = randn((1, new, hq, d), BF, 1)
+    k, v = randn((n, hkv, d), BF, 2), randn((n, hkv, d), BF, 3)
+    slopes = slope_list(hq) if bias else None
+    cache, table = one_cache(k, v)
+    o = bd.paged_attn(q, cache, table, i32([n]), softcap=cap, slopes=slopes)
+    args = (F32, True, 0, cap, None if slopes is None else slopes.cpu().numpy())
+    ro, _, ob, _ = attend(f64(q[0]), f64(k), f64(v), *args)
+    ra = attend(f64(q[0]), f64(k), np.abs(f64(v)), *args)[0]
+    inner = ob + ra * 2.0 ** -15 * 1.01
+    check(f64(o[0]), ro, inner + half_step(BF) * (np.abs(ro) + inner), "O")
