@@ -379,3 +379,27 @@ def test_paged_up_to_16_rows_only_the_output_is_rounded(d, hq, hkv, new, n, cap,
     ra = attend(f64(q[0]), f64(k), np.abs(f64(v)), *args)[0]
     inner = ob + ra * 2.0 ** -15 * 1.01
     check(f64(o[0]), ro, inner + half_step(BF) * (np.abs(ro) + inner), "O")
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_sines_and_cosines_are_good_to_their_last_places(inter):
+    # Pairs (1, 0) become the cosine and the sine themselves.  Two units of each
+    # (2^-23, twice that beside the correction for the angle's last bits), and what
+    # the correction's own roundings leave where a value is near 0: 2^-24 of 2^-24.
+    d, t = 64, 4000
+    freq = list(bd.rope_inv_freq(d, 10000.0))
+    pos = np.random.default_rng(1).integers(0, 2 ** 20, t)
+    pos[:7] = [0, 1, 22, 333, 355, 103993, 104348]      # 355: 113 half turns and 3e-5
+    x = torch.zeros((t, 1, d), device="cuda")
+    x[..., slice(0, d, 2) if inter else slice(0, d // 2)] = 1.0
+    cache = bd.alloc_paged_cache(-(-t // 256), 1, 256, d, F32, "cuda")
+    table = torch.arange(-(-t // 256), dtype=torch.int32, device="cuda")[None]
+    got = f64(bd.paged_append(x, x, cache, table, offsets([t]), i32([0]), inv_freq=freq,
+                              interleaved=inter, positions=i32(pos.tolist()), keep_keys=True)["K"])[:, 0]
+    cs, sn = (got[:, 0::2], got[:, 1::2]) if inter else (got[:, :d // 2], got[:, d // 2:])
+    # The reference's own product p f rounds by 2^-53 of it.
+    a = pos[:, None] * np.asarray(freq)[None]
+    for g, ref in ((cs, np.cos(a)), (sn, np.sin(a))):
+        err = np.abs(g - ref)
+        bound = 2.0 ** -22 * np.abs(ref) + 2.0 ** -46 + 2.0 ** -53 * np.abs(a)
+        assert (err <= bound).all(), (err / bound).max()

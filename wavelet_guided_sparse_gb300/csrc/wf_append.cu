@@ -9,8 +9,8 @@
 // Angles.  The caller's f_i become turns per position, f_i / 2π, as 64-bit
 // binary fractions F_i, rounded to their last place.  p F_i mod 2^64 is then
 // the angle's fraction of a turn, reduced without error, off by about p 2^-65
-// turns for F_i's sake, and its top bits go to sincospi: no angle is ever
-// formed whose rounding grows with p.
+// turns for F_i's sake, and its top 54 bits go to the sine and cosine: no angle
+// is ever formed whose rounding grows with p.
 //
 // HBM-bound: every byte is read once and written once.  One thread moves two
 // 16-byte chunks that rotate together ((c, c + r/2) of the halves form,
@@ -157,11 +157,19 @@ __global__ void __launch_bounds__(kThreads, ITERS == 1 ? 6 : 4)
   const int half = a.rotary_dim / 2;
   for (int e = threadIdx.x; e < n_tok * half; e += kThreads) {
     const int i = e / half, j = e - i * half;
-    // The fraction of a turn, in [-1/2, 1/2), rounded once to fp32.
-    const int64_t frac =
-        static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(s_tok[i].pos)) * p.turns.f[j]);
+    // The fraction of a turn, in [-1/2, 1/2): its first 24 bits as half turns
+    // (exact in fp32), the rest (below 2^-25 half turns) by the first term of
+    // the sine's and cosine's series.  At the end of the range the first part
+    // comes out as -1/2 turn, with the rest below 0.
+    const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(s_tok[i].pos)) * p.turns.f[j];
+    const int32_t head = static_cast<int32_t>(static_cast<int64_t>(frac + (1ull << 38)) >> 39);
+    const int64_t rest = static_cast<int64_t>(frac - (static_cast<uint64_t>(head) << 39));
     float sn, cs;
-    sincospif(static_cast<float>(frac) * 0x1p-63f, &sn, &cs);
+    sincospif(static_cast<float>(head) * 0x1p-24f, &sn, &cs);
+    const float d = static_cast<float>(static_cast<int32_t>(rest >> 8)) * (0x1p-55f * 3.14159265f);
+    const float sn0 = sn;
+    sn = fmaf(d, cs, sn);
+    cs = fmaf(-d, sn0, cs);
     reinterpret_cast<float2*>(s_cs + (i * (V / 2) + (j % V) / 2) * C2 + j / V)[j % 2] =
         make_float2(cs, sn);
   }
