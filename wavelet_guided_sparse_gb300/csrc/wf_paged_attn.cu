@@ -2,8 +2,9 @@
 // whole cache): the split kernel, the join of split sequences, plan and
 // dispatch.
 //
-// HBM-bound at bf16: each key-value row is read once for all g n_new query
-// rows that share it (16 to 64 flop a byte), so everything serves the stream.
+// HBM-bound at bf16 while all g n_new query rows that share a key head fit one
+// row block of at most 64: each key-value row is then read once (16 to 64 flop
+// a byte), and everything serves the stream.  More rows read it once a block.
 // The 64-key tiles of all sequences and heads form one line that a
 // persistent grid divides evenly (wf_attn.cuh).  In each CTA one producer
 // warp keeps a ring of tiles full by tensor copies (whole pages, or 64-row
@@ -31,8 +32,10 @@
 //
 // Measured (32 query heads, d = 128; the stream's share of the measured copy
 // rate).  8 heads of keys, one new token: 64 sequences of 200 to 16384 keys
-// 146 us, 91 %; one of 131072 keys with capped scores 85 us, 93 %.  32 heads
-// of keys, a block of 32 tokens, two sequences of 65536 keys: 328 us, 97 %.
+// 146 to 148 us, 89 %; one of 131072 keys with capped scores or a bias 87 us,
+// 91 %.  32 heads of keys, a block of 32 tokens, two sequences of 65536 keys:
+// 324 us, 98 %.  The same block over 8 heads of keys (128 rows, two row blocks),
+// 16 sequences of 8192 keys: 233 us, 34 % of one read.
 // A few hundred keys: 14 us, of which the split kernel's code, tables and
 // first tile take 9 and the join 5.  fp32, 16 sequences of 8192 keys: 319 us,
 // 50 %, bound by the tf32 products (the FMA pipes took 783).

@@ -39,16 +39,16 @@
 // copy's zero fill) meet weights of exactly 0: the softmax group clears up to
 // 15 value rows there, and the product stops at the next multiple of 16.
 //
-// Measured (32 query heads, 8 of keys, d = 128): 8192 rows over 8192 keys
-// 709 us, 1551 TFLOP/s, 80 % of cuBLAS's bf16 rate; causal 374 us.  The
+// Measured (32 query heads, 8 of keys, d = 128): 8192 rows over 8192 keys 682
+// to 701 us, 1590 TFLOP/s, 82 % of cuBLAS's bf16 rate; causal 368 us.  The
 // softmax bounds it: a step of 128 keys for both tiles takes 2930 cycles, of
 // which the products fill 2048; the exponentials, FMAs and conversions of
 // 2 x 128 x 128 scores and the two hand-overs between the roles fill the
 // rest.  A short sequence adds per item its first tile (2200 cycles, whose
 // masks cost twice) and the output (2700): packed prompts of 20 to 3000 rows
-// 195 us, 53 %.  With cap and bias the mapping of the scores (8 FMA results
-// each, at 128 a cycle and SM) lies on the same chain: 618 us for 8192 causal
-// rows, 2288 us (50 %) for 16384.
+// 192 us, 54 %.  With cap and bias the mapping of the scores (8 FMA results
+// each, at 128 a cycle and SM) lies on the same chain: 608 us for 8192 causal
+// rows, 2301 us (49 %) for 16384.
 #include <algorithm>
 
 #include "wf_attn.cuh"
@@ -273,8 +273,10 @@ struct ScoreMap {
 // tanh(x) = 1 - 2 / (1 + e^(2x)) on the special-function unit, two scores
 // sharing one reciprocal (1/a = b / (a b)); with 2x log2 e clamped at 60 the
 // product stays finite, and 2 / (1 + 2^60) is far below fp32's step at 1.
+// That branch's error is one of the cap (2^-21 of it), not of a small score.
 // Caps so far from the scale that the scaled coefficients would leave fp32's
-// range (above some thousands, below a thousandth) take tanh_exp2 as it is.
+// range (at 1/sqrt(d): above 384 for d = 128, 567 for 64, and below 2e-5) take
+// tanh_exp2 as it is.
 template <bool CAP, bool BIAS, bool LINEAR>
 __device__ __forceinline__ void map_chunk(float* s, const ScoreOpts& o, const ScoreMap& c,
                                           float d0, float sg) {
