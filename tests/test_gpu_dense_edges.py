@@ -403,3 +403,73 @@ def test_append_sines_and_cosines_are_good_to_their_last_places(inter):
         err = np.abs(g - ref)
         bound = 2.0 ** -22 * np.abs(ref) + 2.0 ** -46 + 2.0 ** -53 * np.abs(a)
         assert (err <= bound).all(), (err / bound).max()
+
+
+@pytest.mark.parametrize("where", ["front", "spread", "back"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_padded_batch_is_the_compact_one(dtype, where):
+    # Four prompts among 4096 sequences, the rest empty: the same bits, and not the
+    # milliseconds that a block for each empty sequence and head would cost.
+    lens, slots = [300, 1, 128, 83], 4096
+    at = {"front": [0, 1, 2, 3], "spread": [5, 1000, 1001, 4000], "back": [4092, 4093, 4094, 4095]}[where]
+    padded = [0] * slots
+    for i, n in zip(at, lens):
+        padded[i] = n
+    q, k, v = (randn((sum(lens), h, 128), dtype, h) for h in (32, 8, 8))
+    v = v + 1
+    times, outs = [], []
+    for cu in (offsets(lens), offsets(padded)):
+        ws = bd.alloc_status_workspace("cuda")
+        outs.append(bd.prefill_attn(q, k, v, cu, with_lse=True, ws=ws))
+        assert bd.read_device_status(ws) == 0
+        best = math.inf
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            bd.prefill_attn(q, k, v, cu)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert times[1] < 4 * times[0] + 0.5, times
+
+
+@pytest.mark.parametrize("dtype,hq,hkv", [(BF, 4, 1), (BF, 3, 3), (F32, 2, 1)])
+def test_prefill_more_row_blocks_than_the_grid_takes(dtype, hq, hkv):
+    # 40000 sequences of 0 to 3 rows: several row blocks a block of the grid.
+    lens = np.random.default_rng(7).integers(0, 4, 40000)
+    t, d = int(lens.sum()), 64
+    q, k, v = (randn((t, h, d), dtype, s) for s, h in ((1, hq), (2, hkv), (3, hkv)))
+    o = bd.prefill_attn(q, k, v, offsets(lens.tolist()))
+    first = np.repeat(np.cumsum(lens) - lens, lens)
+    pos = torch.arange(t, device="cuda")
+    start = torch.tensor(first, device="cuda")
+    # Each row sees at most three keys: its own and the two before it.
+    z, vals = [], []
+    for back in range(3):
+        j = (pos - back).clamp(min=0)
+        kk = k[j].double().repeat_interleave(hq // hkv, 1)
+        zz = (q.double() * kk).sum(-1) / d ** 0.5
+        z.append(zz.masked_fill((pos - back < start)[:, None], -math.inf))
+        vals.append(v[j].double().repeat_interleave(hq // hkv, 1))
+    p = torch.softmax(torch.stack(z), 0)
+    ref = sum(p[i][..., None] * vals[i] for i in range(3))
+    bound = sum(p[i][..., None] * vals[i].abs() for i in range(3))
+    # As in attend(): the score's dot product d 2^-23 |q||k|, its other roundings, 2^x;
+    # the weights' and the output's one rounding each.
+    hs = half_step(dtype)
+    big = q.double().norm(dim=-1).max().item() * k.double().norm(dim=-1).max().item() / d ** 0.5
+    e = 2 * (d * 2.0 ** -23 * big + 8 * 2.0 ** -24 * 2 * big) + 2.0 ** -20
+    bound = bound * (hs + e) * 1.01 + hs * (ref.abs() + bound * (hs + e))
+    assert ((o.double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_checks_the_offsets_of_a_batch_without_rows(dtype):
+    q, k, v = (randn((60, 8, 64), dtype, s) for s in (1, 2, 3))
+    ws, out = bd.alloc_status_workspace("cuda"), torch.full((60, 8, 64), 7.0, dtype=dtype, device="cuda")
+    bd.prefill_attn(q, k, v, i32([0] * 4097), out=out, ws=ws)
+    assert bd.read_device_status(ws) == 0 and (out == 7).all()
+    bd.prefill_attn(q, k, v, i32([0] * 4096 + [-1]), out=out, ws=ws)
+    assert bd.read_device_status(ws) == bd.DEV_BAD_INDEX and (out == 7).all()

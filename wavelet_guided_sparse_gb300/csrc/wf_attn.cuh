@@ -286,10 +286,12 @@ inline PagedParams paged_params(const PagedArgs& a, const PagedPlan& plan) {
 
 // ---------------------------------------------------------------- packed row blocks
 // Row blocks of packed sequences: `rows` rows of one key-value head a block
-// (n_q g rows in a sequence).  A grid of doc_blocks() blocks covers any split
-// of the rows into sequences; find_doc_block maps a block index to its
-// sequence (whole warp; false: past the last block).  Offsets are clamped
-// into the arrays, and a bad one is flagged.
+// (n_q g rows in a sequence).  doc_blocks() blocks cover any split of the rows
+// into sequences; a padded batch (many empty sequences) has far fewer, so that
+// grids are capped and their blocks then share out what doc_total() counts.
+// find_doc_block maps a block index to its sequence (whole warp; false: past
+// the last block).  Offsets are clamped into the arrays, and a bad one is
+// flagged.
 inline int64_t doc_blocks(int64_t rows_q, int n_docs, int rows, int g) {
   return rows_q * g / rows + n_docs;
 }
@@ -303,7 +305,20 @@ __device__ __forceinline__ int doc_span(const int32_t* cu, int i, int rows, int*
   *first = a;
   return max(b - a, 0);
 }
-// Where the last search ended: its 32 sequences and the blocks before them.
+// Row blocks of all sequences.  Whole warp.
+__device__ __forceinline__ int64_t doc_total(const PrefillArgs& a, int rows, int g) {
+  int64_t n = 0;
+#pragma unroll 4
+  for (int d = threadIdx.x & 31; d < a.n_docs; d += 32) {
+    int first;
+    n += (static_cast<int64_t>(doc_span(a.cu_q, d, a.rows_q, &first)) * g + rows - 1) / rows;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+// Where the last search ended: its 32 sequences and the blocks before them
+// (behind the last sequence: all).
 struct DocCursor {
   int d0;
   int64_t base;
@@ -334,6 +349,7 @@ __device__ __forceinline__ bool find_doc_block(const PrefillArgs& a, int64_t at,
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
+  cursor = {a.n_docs, base};
   return false;
 }
 

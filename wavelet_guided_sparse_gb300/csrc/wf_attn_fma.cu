@@ -198,6 +198,7 @@ __device__ __forceinline__ void fma_stage(FmaSmem<D, RT>& s, int j, int c, const
 struct PrefillParams {
   PrefillArgs a;
   ScoreOpts o;
+  int capped;  // 1: the grid has fewer blocks than row blocks there might be
 };
 
 template <typename T, int D, int RT>
@@ -211,48 +212,56 @@ __global__ void __launch_bounds__(kThreads) prefill_fma_kernel(PrefillParams p) 
     check_offsets(a.cu_q, a.n_docs, a.rows_q, a.status, threadIdx.x, kThreads);
     check_offsets(a.cu_k, a.n_docs, a.rows_k, a.status, threadIdx.x, kThreads);
   }
-  DocBlock d;
   DocCursor cursor = {0, 0};
-  if (!find_doc_block(a, static_cast<int64_t>(blockIdx.x), RT, g, cursor, &d)) return;
-  RowBlock b;
-  b.g = g;
-  b.n_q = d.n_q;
-  b.len = d.n_k;
-  b.prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + d.doc) : 0;
-  b.row0 = d.block * RT;
-  b.rows = min(RT, d.n_q * g - b.row0);
-  b.head0 = kvh * g;
-  fma_load_q<T, D, RT>(s, b, static_cast<const T*>(a.q) + d.q0 * a.q_stride, a.q_stride);
-  FmaState<D, RT> st;
-  st.reset();
-  const int end = visible_end(b.len, b.pos(b.rows - 1), p.o.causal, b.prefix);
-  const T* kb = static_cast<const T*>(a.k) + d.k0 * a.k_stride + kvh * D;
-  const T* vb = static_cast<const T*>(a.v) + d.k0 * a.v_stride + kvh * D;
-  for (int key0 = 0; key0 < end; key0 += KT) {
-    __syncthreads();
-    constexpr int C = D / Elem<T>::kPer16B;
-    for (int e = threadIdx.x; e < KT * C; e += kThreads) {
-      const int j = e / C, c = e % C, key = key0 + j;
-      const bool in = key < b.len;
-      fma_stage<T, D, RT>(s, j, c, in ? kb + key * a.k_stride : nullptr,
-                          in ? vb + key * a.v_stride : nullptr);
+  const int64_t total = p.capped ? doc_total(a, RT, g) : gridDim.x;
+  for (int64_t at = blockIdx.x; at < total; at += gridDim.x) {
+    DocBlock d;
+    if (!find_doc_block(a, at, RT, g, cursor, &d)) return;
+    if (at != blockIdx.x) __syncthreads();  // the last block's rows have been read
+    RowBlock b;
+    b.g = g;
+    b.n_q = d.n_q;
+    b.len = d.n_k;
+    b.prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + d.doc) : 0;
+    b.row0 = d.block * RT;
+    b.rows = min(RT, d.n_q * g - b.row0);
+    b.head0 = kvh * g;
+    fma_load_q<T, D, RT>(s, b, static_cast<const T*>(a.q) + d.q0 * a.q_stride, a.q_stride);
+    FmaState<D, RT> st;
+    st.reset();
+    const int end = visible_end(b.len, b.pos(b.rows - 1), p.o.causal, b.prefix);
+    const T* kb = static_cast<const T*>(a.k) + d.k0 * a.k_stride + kvh * D;
+    const T* vb = static_cast<const T*>(a.v) + d.k0 * a.v_stride + kvh * D;
+    for (int key0 = 0; key0 < end; key0 += KT) {
+      __syncthreads();
+      constexpr int C = D / Elem<T>::kPer16B;
+      for (int e = threadIdx.x; e < KT * C; e += kThreads) {
+        const int j = e / C, c = e % C, key = key0 + j;
+        const bool in = key < b.len;
+        fma_stage<T, D, RT>(s, j, c, in ? kb + key * a.k_stride : nullptr,
+                            in ? vb + key * a.v_stride : nullptr);
+      }
+      __syncthreads();
+      fma_tile<D, RT>(s, b, p.o, key0, st);
     }
-    __syncthreads();
-    fma_tile<D, RT>(s, b, p.o, key0, st);
+    const int64_t base = d.q0 * a.q_heads;
+    fma_store<T, D, RT>(st, b, static_cast<T*>(a.o) + base * D,
+                        a.lse != nullptr ? a.lse + base : nullptr, a.q_heads);
   }
-  const int64_t base = d.q0 * a.q_heads;
-  fma_store<T, D, RT>(st, b, static_cast<T*>(a.o) + base * D,
-                      a.lse != nullptr ? a.lse + base : nullptr, a.q_heads);
 }
 
 template <typename T, int D>
-cudaError_t launch_prefill_typed(const PrefillParams& p, cudaStream_t stream) {
+cudaError_t launch_prefill_typed(PrefillParams& p, cudaStream_t stream) {
   constexpr int RT = 64;
   const cudaError_t e = ensure_max_smem<prefill_fma_kernel<T, D, RT>>();
   if (e != cudaSuccess) return e;
   const int64_t blocks = doc_blocks(p.a.rows_q, p.a.n_docs, RT, p.a.q_heads / p.a.kv_heads);
+  // At most about 32 CTAs an SM (one runs at a time), each with every so many
+  // row blocks.
+  const int64_t most = std::max(1, 32 * device_sm_count() / p.a.kv_heads);
+  p.capped = most < blocks;
   prefill_fma_kernel<T, D, RT>
-      <<<dim3(static_cast<unsigned>(blocks), p.a.kv_heads), kThreads, sizeof(FmaSmem<D, RT>),
+      <<<dim3(static_cast<unsigned>(std::min(blocks, most)), p.a.kv_heads), kThreads, sizeof(FmaSmem<D, RT>),
          stream>>>(p);
   return cudaGetLastError();
 }
