@@ -473,3 +473,38 @@ def test_prefill_checks_the_offsets_of_a_batch_without_rows(dtype):
     assert bd.read_device_status(ws) == 0 and (out == 7).all()
     bd.prefill_attn(q, k, v, i32([0] * 4096 + [-1]), out=out, ws=ws)
     assert bd.read_device_status(ws) == bd.DEV_BAD_INDEX and (out == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_paged_padded_batch_is_the_compact_one(dtype):
+    # Four sequences in front of 4092 idle slots: the same rows, and the idle slots
+    # cost no walk of one after the other.
+    live, slots, hq, hkv, d, page, n = 4, 4096, 32, 8, 128, 16, 1000
+    table, pages = make_table([n] * live, page, 3)
+    wide = torch.full((slots, table.shape[1]), -7, dtype=torch.int32, device="cuda")
+    wide[:live] = table
+    cache = {x: randn((pages, hkv, page, d), dtype, i) for i, x in enumerate(("K", "V"))}
+    q = torch.zeros((slots, 1, hq, d), dtype=dtype, device="cuda")
+    q[:live] = randn((live, 1, hq, d), dtype, 5)
+    lens = i32([n] * live + [0] * (slots - live))
+    times, outs = [], []
+    for m, t in ((live, table), (slots, wide)):
+        ws = bd.alloc_paged_attn_workspace(q[:m], cache, t)
+        call = dict(q=q[:m], cache=cache, page_table=t, kv_len=lens[:m], ws=ws)
+        outs.append(bd.paged_attn(with_lse=True, **call))
+        assert bd.read_device_status(ws) == 0
+        best = math.inf
+        for _ in range(10):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            bd.paged_attn(**call)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+    # The work is divided differently: fp32 sums in another order.
+    for x, y in zip(outs[0], outs[1]):
+        tol = 2 * half_step(dtype) if x.dtype == dtype else 2.0 ** -18
+        assert ((x - y[:live]).abs() <= tol * x.abs() + 2.0 ** -18).all()
+        assert (y[live:] == (0 if x.dim() == 4 else -math.inf)).all()
+    assert times[1] < times[0] + 0.15, times

@@ -233,15 +233,23 @@ __device__ __forceinline__ WorkUnit find_unit(const WorkShape& w, const int32_t*
   }
   return u;
 }
-// The unit after u (there is one: the caller stays below the total).
+// The unit after u (there is one: the caller stays below the total).  Whole
+// warp, which looks at 32 sequences a step for one with keys where the next one
+// is idle.
 __device__ __forceinline__ void next_unit(const WorkShape& w, const int32_t* lens, WorkUnit& u) {
   u.begin += u.tiles;
   if (++u.unit < w.units_per_seq) return;
   u.unit = 0;
-  do {
-    ++u.seq;
-    u.len = u.seq < w.n_seqs ? seq_len_clamped(lens, u.seq, w.max_len) : 1;
-  } while (u.len == 0);
+  const int lane = threadIdx.x & 31;
+  ++u.seq;
+  u.len = u.seq < w.n_seqs ? seq_len_clamped(lens, u.seq, w.max_len) : 0;
+  for (int s0 = u.seq + 1; u.len == 0 && s0 < w.n_seqs; s0 += 32) {
+    const int len = s0 + lane < w.n_seqs ? seq_len_clamped(lens, s0 + lane, w.max_len) : 0;
+    const unsigned live = __ballot_sync(0xffffffffu, len > 0);
+    if (live == 0) continue;
+    u.seq = s0 + __ffs(live) - 1;
+    u.len = __shfl_sync(0xffffffffu, len, __ffs(live) - 1);
+  }
   u.tiles = (u.len + w.tile - 1) / w.tile;
 }
 

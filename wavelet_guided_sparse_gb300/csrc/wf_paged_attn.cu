@@ -269,8 +269,10 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         st = 0;
         phase ^= 1;
       }
-      if (at + 1 == u.begin + u.tiles) next_unit(p.w, a.kv_len, u);
-      if (at + 1 < w1) read_entries(u, at + 1);
+      if (at + 1 < w1) {
+        if (at + 1 == u.begin + u.tiles) next_unit(p.w, a.kv_len, u);
+        read_entries(u, at + 1);
+      }
     }
     // No copy may land after the CTA has gone, also where the consumers have
     // given up behind this warp's last wait.
@@ -303,7 +305,7 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
     int st = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int64_t at = w0; at < w1; next_unit(p.w, a.kv_len, u)) {
+    for (int64_t at = w0; at < w1;) {
       const int64_t end = min(w1, u.begin + u.tiles);
       const int len = u.len;
       const int prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + u.seq) : 0;
@@ -677,6 +679,7 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
           if (c == 0) *reinterpret_cast<float2*>(part + RT * D + 2 * r) = make_float2(gm, gl);
         }
       }
+      if (at < w1) next_unit(p.w, a.kv_len, u);
     }
   }
 }
