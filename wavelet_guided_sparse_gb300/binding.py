@@ -641,13 +641,17 @@ def _pages(cache: dict, page_table: torch.Tensor, dtype, device):
 
 def _attn_opts(causal, prefix, softcap, slopes, scale, n_seqs: int, q_heads: int,
                device) -> AttnOpts:
-    if scale is not None and scale == 0.0:
-        raise ValueError("scale must not be 0 (None means 1/sqrt(head_dim))")
-    return AttnOpts(0.0 if scale is None else scale, softcap, 1 if causal else 0,
+    opts = AttnOpts(0.0 if scale is None else scale, softcap, 1 if causal else 0,
                     None if prefix is None else _need(prefix, "prefix", (n_seqs,), torch.int32,
                                                       device),
                     None if slopes is None else _need(slopes, "slopes", (q_heads,), torch.float32,
                                                       device))
+    # In the struct 0 stands for the defaults: also what fp32 rounds to it.
+    if scale is not None and opts.scale == 0.0:
+        raise ValueError("scale must not be 0 in fp32 (None means 1/sqrt(head_dim))")
+    if softcap != 0.0 and opts.softcap == 0.0:
+        raise ValueError("softcap must not round to 0 in fp32 (0 means none)")
+    return opts
 
 
 def _ws_args(ws: Optional[torch.Tensor], device):
