@@ -508,3 +508,38 @@ def test_paged_padded_batch_is_the_compact_one(dtype):
         assert ((x - y[:live]).abs() <= tol * x.abs() + 2.0 ** -18).all()
         assert (y[live:] == (0 if x.dim() == 4 else -math.inf)).all()
     assert times[1] < times[0] + 0.15, times
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, False), (0.0, True), (20.0, True)])
+def test_prefill_what_is_hidden_changes_no_bit(dtype, cap, bias):
+    # Keys that the mask hides from the first rows, and all of the next sequence.  (128
+    # rows: a capped score's form is chosen for 32 rows at a time, by what these see.)
+    d, h, lens, seen = 128, 4, [300, 77, 41], 128
+    t = sum(lens)
+    q, k, v = (randn((t, h, d), dtype, s) for s in (1, 2, 3))
+    slopes = slope_list(h) if bias else None
+    outs = []
+    for junk in (0.0, 300.0, -1e30, math.nan):
+        k[seen:300], k[377:] = junk, junk
+        v[377:] = junk
+        o, lse = bd.prefill_attn(q, k, v, offsets(lens), softcap=cap, slopes=slopes, with_lse=True)
+        outs.append([x[a:b].clone() for x in (o, lse) for a, b in ((0, seen), (300, 377))])
+    for other in outs[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(other, outs[0]))
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("n", [76, 77, 128 + 45])
+def test_prefill_capped_scores_beside_another_sequences_nan(n, bias):
+    # Scores far into the cap's bend, and in the next sequence's keys, right behind
+    # the last one that counts, NaN.
+    d, h, cap = 128, 2, 2.0
+    q, k, v = (randn((n + 90, h, d), BF, s) for s in (1, 2, 3))
+    q, k[n:], v[n:] = q * 4, math.nan, math.nan
+    slopes = slope_list(h) if bias else None
+    o, lse = bd.prefill_attn(q, k, v, offsets([n, 90]), softcap=cap, slopes=slopes, with_lse=True)
+    ro, rl, ob, lb = attend(f64(q[:n]), f64(k[:n]), f64(v[:n]), BF, True, 0, cap,
+                            None if slopes is None else slopes.cpu().numpy())
+    check(f64(lse[:n]), rl, lb, "lse")
+    check(f64(o[:n]), ro, ob, "O")

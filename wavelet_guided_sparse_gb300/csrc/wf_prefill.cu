@@ -277,7 +277,8 @@ struct ScoreMap {
 // That branch's error is one of the cap (2^-21 of it), not of a small score.
 // Caps so far from the scale that the scaled coefficients would leave fp32's
 // range (at 1/sqrt(d): above 384 for d = 128, 567 for 64, and below 2e-5) take
-// tanh_exp2 as it is.
+// tanh_exp2 as it is.  Hidden scores come as 0: they must neither choose the
+// form nor share a reciprocal.
 template <bool CAP, bool BIAS, bool LINEAR>
 __device__ __forceinline__ void map_chunk(float* s, const ScoreOpts& o, const ScoreMap& c,
                                           float d0, float sg) {
@@ -350,12 +351,12 @@ __device__ __forceinline__ void map_scores(float* s, const ScoreOpts& o, const S
     map_chunk<CAP, BIAS, false>(s, o, c, d0, 0.f);
 }
 
-// A chunk's keys from `n` on are hidden.  One bit a key: bits of a register
-// become predicates eight at once.
-__device__ __forceinline__ void hide_keys(float* s, int n) {
+// A chunk's keys from `n` on are hidden: their scores become `with`.  One bit a
+// key: bits of a register become predicates eight at once.
+__device__ __forceinline__ void hide_keys(float* s, int n, float with = -INFINITY) {
   const uint32_t seen = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) s[i] = (seen & (1u << i)) != 0 ? s[i] : -INFINITY;
+  for (int i = 0; i < 32; ++i) s[i] = (seen & (1u << i)) != 0 ? s[i] : with;
 }
 
 template <int N>
@@ -828,6 +829,19 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           // after the rare raise.  (Two passes, as below, would carry the mapped
           // scores through tensor memory: 644 against 618 us for 8192 causal rows
           // with cap and bias.)
+          if (CAP && edge) {
+            // Hidden scores become 0 in place (they may be NaN, and columns without a
+            // key hold what an earlier item left): beside, not in, the loop below,
+            // whose code they would slow by a tenth.
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t r[32];
+              tmem_ld32(s_addr + c, r);
+              hide_keys(reinterpret_cast<float*>(r), rel - c, 0.f);
+              tmem_st32(s_addr + c, r);
+            }
+            tmem_wait_st();
+          }
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
             uint32_t r[32], pk[16];
@@ -849,8 +863,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               float a0, a1;
               unpack2(add2(sum0, sum1), a0, a1);
               const float f = raise_max(m, mc, a0 + a1);
-              l = (l + (a0 + a1)) * f;
-              sum0 = sum1 = 0;
+              if (f != 1.f) {  // other rows' sums go on in their order
+                l = (l + (a0 + a1)) * f;
+                sum0 = sum1 = 0;
+              }
               if (c > 0) tmem_wait_st();
               const __nv_bfloat162 fb = __float2bfloat162_rn(f);
 #pragma unroll 1
