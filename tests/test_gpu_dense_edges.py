@@ -543,3 +543,24 @@ def test_prefill_capped_scores_beside_another_sequences_nan(n, bias):
                             None if slopes is None else slopes.cpu().numpy())
     check(f64(lse[:n]), rl, lb, "lse")
     check(f64(o[:n]), ro, ob, "O")
+
+
+@pytest.mark.parametrize("dtype,new", [(BF, 1), (BF, 12), (F32, 1), (F32, 12)])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, False), (20.0, True)])
+def test_paged_what_lies_behind_a_sequence_changes_no_bit(dtype, new, cap, bias):
+    page, hq, hkv, d, lens = 64, 4, 2, 128, [50, 90, 1000, 200]
+    table, pages = make_table(lens, page, 1)
+    cache = {x: randn((pages, hkv, page, d), dtype, i) for i, x in enumerate(("K", "V"))}
+    q = randn((len(lens), new, hq, d), dtype, 3)
+    slopes = slope_list(hq) if bias else None
+    outs = []
+    for junk_k, junk_v in ((0.0, 0.0), (1e30, -1e30), (math.nan, math.inf)):
+        for s, n in enumerate(lens):
+            if n % page:
+                last = table[s, n // page]
+                cache["K"][last, :, n % page:] = junk_k
+                cache["V"][last, :, n % page:] = junk_v
+        outs.append(bd.paged_attn(q, cache, table, i32(lens), softcap=cap, slopes=slopes,
+                                  with_lse=True))
+    for o, lse in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])

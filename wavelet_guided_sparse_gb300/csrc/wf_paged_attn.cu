@@ -135,6 +135,10 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
   constexpr int kStages = Shape::kStages, kTileBytes = Shape::kTileBytes;
   constexpr int kStageBytes = 2 * kTileBytes, RT = 16 * R;
   constexpr int kConsumerThreads = Shape::kConsumers * 32;
+  // fp32: first parts that are always finite.  They cost a 16-row unit, whose
+  // queries are split again every 8 keys, 8 % (16 sequences of 8192 keys: 345 us
+  // against 319), more rows 1 to 6 %, less than the other way, below, would.
+  constexpr bool kFinite = R > 1;
   constexpr int KC = 128 / sizeof(T), KB = D / KC;  // columns of a 128-byte block, blocks of a row
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) PagedBarriers<kStages> bars;
@@ -363,15 +367,18 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         const int valid = *reinterpret_cast<volatile int*>(&bars.valid[st]);
         const bool edge = valid != kAllValid || key0 + Shape::kKeys > open;
         if (edge && (valid != kAllValid || key0 + Shape::kKeys > len)) {
-          // Clear the value rows whose weight is 0 by their place.
+          // Clear the value rows whose weight is 0 by their place (and the keys
+          // where a score that is not finite would choose the form of the tile's).
           constexpr int C = D * static_cast<int>(sizeof(T)) / 16;  // chunks of a row
           for (int e = lane; e < Shape::kKeys * C; e += 32) {
             const int r = e / C, c = e % C;
             const int tr = kg * Shape::kKeys + r;
-            if (key0 + r >= len || !((valid >> (tr / tp.box_rows)) & 1))
-              *reinterpret_cast<uint4*>(ring + st * kStageBytes + kTileBytes +
-                                        (c >> 3) * (KT * 128) + tr * 128 + (c & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+            if (key0 + r >= len || !((valid >> (tr / tp.box_rows)) & 1)) {
+              uint4* chunk = reinterpret_cast<uint4*>(ring + st * kStageBytes + (c >> 3) * (KT * 128) +
+                                                      tr * 128 + (c & 7) * 16);
+              chunk[kTileBytes / 16] = make_uint4(0u, 0u, 0u, 0u);
+              if (kWide && !kFinite) *chunk = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
           fence_proxy_async();
           __syncwarp();
@@ -380,10 +387,6 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         // Two accumulators a block halve the chain of dependent products; for
         // fp32 the second one takes the small terms.
         float s[NB][4], s2[NB][4];
-        // Finite first parts cost a 16-row unit, whose queries are split again
-        // every 8 keys, 8 % (16 sequences of 8192 keys: 345 us against 319), more
-        // rows 1 to 6 %, less than the second way below would cost them.
-        constexpr bool kFinite = R > 1;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
