@@ -7,7 +7,7 @@
 // (ty, tx) owns four rows and, of a 64-key tile, keys tx, tx + 16, ...; then
 // of the output columns float4s tx, tx + 16.  One pass over the keys with the
 // running maximum and sum; the weights pass through shared memory within a
-// half warp.  32 heads, 2048 rows and keys, d = 128: 2482 us, 27.7 TFLOP/s of
+// half warp.  32 heads, 2048 rows and keys, d = 128: 2490 us, 27.6 TFLOP/s of
 // the pipes' 80.  At 119 KB of shared memory eight warps share an SM, whose
 // chains of shared-memory reads and FMAs bound it: fetching the next tile into
 // registers meanwhile (1 % less) or four weights a read (2 % more) changed

@@ -35,10 +35,10 @@
 // 146 to 148 us, 89 %; one of 131072 keys with capped scores or a bias 87 us,
 // 91 %.  32 heads of keys, a block of 32 tokens, two sequences of 65536 keys:
 // 324 us, 98 %.  The same block over 8 heads of keys (128 rows, two row blocks),
-// 16 sequences of 8192 keys: 233 us, 34 % of one read.
+// 16 sequences of 8192 keys: 238 us, 33 % of one read.
 // A few hundred keys: 14 us, of which the split kernel's code, tables and
-// first tile take 9 and the join 5.  fp32, 16 sequences of 8192 keys: 319 us,
-// 50 %, bound by the tf32 products (the FMA pipes took 783).
+// first tile take 9 and the join 5.  fp32, 16 sequences of 8192 keys: 320 us,
+// 49 %, bound by the tf32 products (the FMA pipes took 783).
 #include <algorithm>
 
 #include "wf_attn.cuh"

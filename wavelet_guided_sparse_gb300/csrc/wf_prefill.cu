@@ -39,16 +39,16 @@
 // copy's zero fill) meet weights of exactly 0: the softmax group clears up to
 // 15 value rows there, and the product stops at the next multiple of 16.
 //
-// Measured (32 query heads, 8 of keys, d = 128): 8192 rows over 8192 keys 682
-// to 701 us, 1590 TFLOP/s, 82 % of cuBLAS's bf16 rate; causal 368 us.  The
+// Measured (32 query heads, 8 of keys, d = 128): 8192 rows over 8192 keys 690
+// us, 1593 TFLOP/s, 82 % of cuBLAS's bf16 rate; causal 362 to 368 us.  The
 // softmax bounds it: a step of 128 keys for both tiles takes 2930 cycles, of
 // which the products fill 2048; the exponentials, FMAs and conversions of
 // 2 x 128 x 128 scores and the two hand-overs between the roles fill the
 // rest.  A short sequence adds per item its first tile (2200 cycles, whose
 // masks cost twice) and the output (2700): packed prompts of 20 to 3000 rows
-// 192 us, 54 %.  With cap and bias the mapping of the scores (8 FMA results
-// each, at 128 a cycle and SM) lies on the same chain: 608 us for 8192 causal
-// rows, 2301 us (49 %) for 16384.
+// 194 us, 53 %.  With cap and bias the mapping of the scores (8 FMA results
+// each, at 128 a cycle and SM) lies on the same chain: 616 us for 8192 causal
+// rows, 2329 us (49 %) for 16384.
 #include <algorithm>
 
 #include "wf_attn.cuh"
