@@ -564,3 +564,20 @@ def test_paged_what_lies_behind_a_sequence_changes_no_bit(dtype, new, cap, bias)
                                   with_lse=True))
     for o, lse in outs[1:]:
         assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (4, 2)])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, False), (20.0, True)])
+def test_prefill_the_next_sequences_queries_change_no_bit(hq, hkv, cap, bias):
+    # They lie in the same query tile as this one's last rows.
+    d, lens = 128, [300, 77, 41]
+    t = sum(lens)
+    q, k, v = randn((t, hq, d), BF, 1), randn((t, hkv, d), BF, 2), randn((t, hkv, d), BF, 3)
+    slopes = slope_list(hq) if bias else None
+    outs = []
+    for junk in (0.0, 300.0, -1e30, math.nan):
+        q[377:] = junk
+        o, lse = bd.prefill_attn(q, k, v, offsets(lens), softcap=cap, slopes=slopes, with_lse=True)
+        outs.append((o[:377].clone(), lse[:377].clone()))
+    for o, lse in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])

@@ -261,6 +261,7 @@ struct ScoreMap {
   uint64_t bend[5];      // cap: coefficients of cap log2 e tanh(s scale / cap) / s in s^2
   uint64_t steps[16];    // slope times (2 i, 2 i + 1)
   float slope;           // slope log2 e
+  float weigh;           // cap: scale / cap, 0 in a row that does not exist
 };
 
 // z = [cap tanh(s / cap) or scale s] - slope |d0 - i|, in the log2 domain,
@@ -277,8 +278,9 @@ struct ScoreMap {
 // That branch's error is one of the cap (2^-21 of it), not of a small score.
 // Caps so far from the scale that the scaled coefficients would leave fp32's
 // range (at 1/sqrt(d): above 384 for d = 128, 567 for 64, and below 2e-5) take
-// tanh_exp2 as it is.  Hidden scores come as 0: they must neither choose the
-// form nor share a reciprocal.
+// tanh_exp2 as it is.  Hidden scores come as 0 (they must neither choose the
+// form nor share a reciprocal), and rows that do not exist (the next sequence's
+// queries) have no say in it.
 template <bool CAP, bool BIAS, bool LINEAR>
 __device__ __forceinline__ void map_chunk(float* s, const ScoreOpts& o, const ScoreMap& c,
                                           float d0, float sg) {
@@ -301,7 +303,7 @@ __device__ __forceinline__ void map_chunk(float* s, const ScoreOpts& o, const Sc
     big0 = fmaxf(big0, fmaxf(fabsf(s[i]), fabsf(s[i + 1])));
     big1 = fmaxf(big1, fmaxf(fabsf(s[i + 2]), fabsf(s[i + 3])));
   }
-  if (__all_sync(0xffffffffu, fmaxf(big0, big1) * o.scale <= o.bend_max)) {
+  if (__all_sync(0xffffffffu, !(fmaxf(big0, big1) * c.weigh > o.bend_max))) {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       const uint64_t x = pack2(s[i], s[i + 1]), u = mul2(x, x);
@@ -802,6 +804,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           map.bend[i] = pack2(bend[i] * unit, bend[i] * unit);
           unit *= p.o.scale * p.o.scale;
         }
+        map.weigh = live ? p.o.scale : 0.f;
         map.slope = BIAS ? __ldg(p.o.slopes + max(0, min(head, a.q_heads - 1))) * kLog2e : 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
