@@ -261,7 +261,8 @@ def _prepare_pages(case, seed, gen, lengths):
         start, keep = _kept(case, lengths)
         table, pages = _table(case, seed, totals, case["seqs"], 5)
         width = max(1, max(len(k) for k in keep))
-        state.update(kv_len=_int32(totals), start=_int32(start), n_keep=_int32([len(k) for k in keep]),
+        state.update(kv_len=_int32(totals), start=_int32(start),
+                     n_keep=_int32([len(k) for k in keep]),
                      keep=_int32([k + [0] * (width - len(k)) for k in keep]))
     pools = torch.empty((case["layers"], 2, pages, case["hkv"], page, case["d"]),
                         dtype=_dtype(case), device="cuda")
@@ -488,23 +489,25 @@ def _run_own(state):
     from wavelet_guided_sparse_gb300 import binding as wf
     case = state["case"]
     if case["op"] == "fork":
-        if "ws" not in state:
-            state["ws"] = wf.alloc_pages_workspace(state["caches"][0], state["table"],
+        if "ws" not in state:  # what a program keeps: its layers' handle, a workspace
+            state["layers"] = wf.page_pools(state["caches"])
+            state["ws"] = wf.alloc_pages_workspace(state["layers"], state["table"],
                                                    max_forks=len(state["src"]))
         call = dict(refs=state["refs"], ws=state["ws"])
-        wf.paged_fork(state["caches"], state["table"], src=state["src"], dst=state["dst"],
+        wf.paged_fork(state["layers"], state["table"], src=state["src"], dst=state["dst"],
                       kv_len=state["kv_len"], share_rows=state["share"], **call)
         forked = state["table"].clone()
-        wf.paged_release(state["caches"][0], state["table"], first=state["first"],
+        wf.paged_release(state["layers"], state["table"], first=state["first"],
                          end=state["end"], **call)
         return {"table": forked, "refs": state["refs"], "pools": state["pools"]}
     if case["op"] == "keep":
         if "ws" not in state:
-            state["ws"] = wf.alloc_pages_workspace(state["caches"][0], state["table"],
+            state["layers"] = wf.page_pools(state["caches"])
+            state["ws"] = wf.alloc_pages_workspace(state["layers"], state["table"],
                                                    max_keep=state["keep"].shape[1])
         call = dict(refs=state["refs"], ws=state["ws"])
-        wf.paged_reserve(state["caches"][0], state["table"], rows=state["kv_len"], **call)
-        wf.paged_keep(state["caches"], state["table"], kv_len=state["kv_len"],
+        wf.paged_reserve(state["layers"], state["table"], rows=state["kv_len"], **call)
+        wf.paged_keep(state["layers"], state["table"], kv_len=state["kv_len"],
                       start=state["start"], keep=state["keep"], n_keep=state["n_keep"], **call)
         return {"table": state["table"], "refs": state["refs"], "pools": state["pools"]}
     options = dict(softcap=case["cap"], slopes=state["slopes"], with_lse=True)
