@@ -29,6 +29,9 @@
  *   wf_paged_append        new rows into a paged cache, rotated on the way
  *   wf_paged_attn          §2.1 eq. (3) of new tokens over a whole paged cache
  *   wf_prefill_attn        §2.1 eq. (1) over packed prompts
+ *   wf_paged_reserve, wf_paged_fork, wf_paged_keep, wf_paged_release
+ *                          the pages themselves: taken, shared or copied,
+ *                          compacted, given back
  *
  * Readings fixed where the pages are silent: orthonormal Haar filters
  * g = [1/√2, 1/√2] on 0-based pairs (2n, 2n+1), so coarse position p at
@@ -91,7 +94,9 @@ enum {
   WF_DEV_OK = 0,
   WF_DEV_BAD_INDEX = 1,      /* an index outside [0, n_prompt) (or its level range) */
   WF_DEV_DUP_INDEX = 2,      /* a duplicate coarse survivor                         */
-  WF_DEV_WAIT_TIMEOUT = 4    /* a bounded wait on an asynchronous copy gave up      */
+  WF_DEV_WAIT_TIMEOUT = 4,   /* a bounded wait on an asynchronous copy gave up      */
+  WF_DEV_NO_PAGE = 8,        /* too few free pages                                  */
+  WF_DEV_SHARED_PAGE = 16    /* rows would move into a page that others hold too    */
 };
 
 /* Limits of this build. */
@@ -571,6 +576,93 @@ int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_
                   const void* K_pages, const void* V_pages, const int32_t* page_table,
                   const int32_t* kv_len, void* O, float* lse, void* workspace,
                   size_t workspace_bytes, void* stream);
+
+/* ---- Pages.  The pool's state is one count per page: refs [n_pages] int32
+ * (device, in/out), the number of page table entries that hold the page; 0
+ * means free.  A table entry without a page is negative.  The calls below keep
+ * both in step on the stream, without the host: pages are taken lowest first
+ * (the i-th entry that needs one gets the i-th lowest free page), so that
+ * results do not depend on timing.  One page table serves every layer: pools
+ * is a HOST array of n_pools device pointers (the K_pages and V_pages of each
+ * layer, 1..WF_MAX_POOLS of them, the same sizes all), read during the call.
+ * dims as in wf_paged_append (q_heads is not looked at).  Lengths of sequences
+ * are the caller's, as in wf_paged_append. */
+
+/* Most pools (K and V pages of a layer are two) of one call. */
+#define WF_MAX_POOLS 256
+
+/* Bytes of workspace for any of the calls below with at most max_forks forks
+ * and lists of max_keep rows (0: none of that kind).  Errors: WF_ERR_NULL,
+ * WF_ERR_SHAPE, WF_ERR_UNSUPPORTED. */
+int wf_pages_workspace_bytes(const wf_page_dims* dims, int32_t max_forks, int32_t max_keep,
+                             size_t* bytes);
+
+/* Pages for growing sequences: every entry of sequence s below ceil(rows[s] /
+ * page_size) that holds none takes a free page (sequence by sequence, entry by
+ * entry).
+ *   rows      : device, [n_seqs] int32; outside the table: clamped and flagged
+ *               WF_DEV_BAD_INDEX
+ *   refs, page_table : device, in/out
+ *   workspace : device, >= wf_pages_workspace_bytes(); too few free pages raise
+ *               WF_DEV_NO_PAGE in its status word, and the last entries stay
+ *               without one
+ * One launch.  Errors: as wf_paged_append. */
+int wf_paged_reserve(const wf_page_dims* dims, const int32_t* rows, int32_t* refs,
+                     int32_t* page_table, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Children of sequences.  Fork i makes sequence dst[i], which must hold no
+ * pages, a copy of sequence src[i] with its kv_len[src[i]] rows: the pages
+ * whose rows all lie below share_rows[i] are shared (one reference more), for
+ * the rest it takes free pages (fork by fork, entry by entry) and their rows
+ * are copied in every pool.  Entries behind them become -1.  By default all
+ * whole pages are shared, so that both may append; share_rows[i] = 0 copies
+ * everything, for callers that rewrite rows in place.
+ *   src, dst   : device, [n_forks] int32 sequences; a sequence outside the
+ *                table (WF_DEV_BAD_INDEX), a child that is also a parent or is
+ *                named twice (WF_DEV_DUP_INDEX): the fork is skipped
+ *   kv_len     : device, [n_seqs] int32 (clamped and flagged as above)
+ *   share_rows : device, nullable, [n_forks] int32
+ *   n_forks    : 0..WF_MAX_SEQS; 0 is a no-op
+ * A parent's entry outside the pool is flagged WF_DEV_BAD_INDEX (a shared one
+ * becomes -1, nothing is copied from it); too few free pages: as above.  Two
+ * launches.  Errors: as wf_paged_append. */
+int wf_paged_fork(const wf_page_dims* dims, int32_t n_forks, const int32_t* src,
+                  const int32_t* dst, const int32_t* kv_len, const int32_t* share_rows,
+                  int32_t* refs, int32_t* page_table, int32_t n_pools, void* const* pools,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Keeps some rows of each sequence and gives back the pages behind them: rows
+ * [0, start[s]) stay, rows keep[s][0 .. n_keep[s]) move up to start[s],
+ * start[s] + 1, ... in every pool (the accepted path of a drafted tree, the
+ * rows that a filter retains), and the pages behind the new length start[s] +
+ * n_keep[s] lose a reference and their entries become -1.
+ *   kv_len, start : device, [n_seqs] int32, 0 <= start <= kv_len
+ *   keep      : device, [n_seqs, max_keep] int32, rows in [start, kv_len),
+ *               strictly ascending; nullable together with n_keep (nothing
+ *               behind start is kept; n_pools may then be 0)
+ *   n_keep    : device, [n_seqs] int32, 0..max_keep
+ *   refs      : device, in/out, nullable: no page is given back, and none is
+ *               taken for shared
+ * A sequence whose list breaks these rules, or would move a row from or to
+ * where it has no page, is left as it was and flagged WF_DEV_BAD_INDEX; one
+ * that would move rows into a page that others hold too (copy it first:
+ * wf_paged_fork), likewise, WF_DEV_SHARED_PAGE.  Two launches.  Errors: as wf_paged_append. */
+int wf_paged_keep(const wf_page_dims* dims, const int32_t* kv_len, const int32_t* start,
+                  const int32_t* keep, int32_t max_keep, const int32_t* n_keep, int32_t* refs,
+                  int32_t* page_table, int32_t n_pools, void* const* pools, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Gives back pages: every page of sequence s all of whose rows lie in
+ * [first[s], end[s]) loses a reference and its entry becomes -1 (a whole
+ * sequence: 0, INT32_MAX; what a sliding window has left behind: its first
+ * tokens, the oldest visible row).  Entries without a page stay as they are.
+ *   first, end : device, [n_seqs] int32 (first >= end: nothing)
+ *   workspace  : device, nullable, >= 256 bytes: an entry outside the pool, or
+ *                a page without a reference, raises WF_DEV_BAD_INDEX
+ * One launch.  Errors: as wf_paged_append. */
+int wf_paged_release(const wf_page_dims* dims, const int32_t* first, const int32_t* end,
+                     int32_t* refs, int32_t* page_table, void* workspace, size_t workspace_bytes,
+                     void* stream);
 
 /* Attention of packed sequences over their own keys (§2.1 eq. (1) per
  * sequence; sequences never see each other).  Sequence s has query rows

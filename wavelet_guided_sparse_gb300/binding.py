@@ -23,6 +23,7 @@ STATUS_NAMES = {0: "WF_OK", 1: "WF_ERR_NULL", 2: "WF_ERR_SHAPE", 3: "WF_ERR_UNSU
                 4: "WF_ERR_WORKSPACE", 5: "WF_ERR_CUDA", 6: "WF_ERR_DEVICE_CHECK",
                 7: "WF_ERR_ALIGNMENT"}
 DEV_BAD_INDEX, DEV_DUP_INDEX, DEV_WAIT_TIMEOUT = 1, 2, 4
+DEV_NO_PAGE, DEV_SHARED_PAGE = 8, 16
 MAX_LEVELS = 12
 
 # Every symbol the header declares (checked by the host tests).
@@ -35,7 +36,9 @@ EXPORTS = ("wf_status_string", "wf_last_error_string", "wf_default_k_per_level",
            "wf_daubechies_lowpass", "wf_basis_workspace_bytes", "wf_dwt_lowpass_basis",
            "wf_step_basis",
            "wf_rope_inv_freq", "wf_paged_append", "wf_paged_attn_workspace_bytes",
-           "wf_paged_attn", "wf_prefill_attn")
+           "wf_paged_attn", "wf_prefill_attn",
+           "wf_pages_workspace_bytes", "wf_paged_reserve", "wf_paged_fork", "wf_paged_keep",
+           "wf_paged_release")
 
 
 class WfError(RuntimeError):
@@ -136,6 +139,13 @@ _SIGS = {
                                      _vp, _sz, _vp]),
     "wf_prefill_attn": (ctypes.c_int, [ctypes.POINTER(PrefillDims), _OPTSP, _vp, _i64, _vp, _i64,
                                        _vp, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "wf_pages_workspace_bytes": (ctypes.c_int, [_PDIMSP, _i32, _i32, ctypes.POINTER(_sz)]),
+    "wf_paged_reserve": (ctypes.c_int, [_PDIMSP, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "wf_paged_fork": (ctypes.c_int, [_PDIMSP, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+                                     ctypes.POINTER(_vp), _vp, _sz, _vp]),
+    "wf_paged_keep": (ctypes.c_int, [_PDIMSP, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32,
+                                     ctypes.POINTER(_vp), _vp, _sz, _vp]),
+    "wf_paged_release": (ctypes.c_int, [_PDIMSP, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -785,6 +795,152 @@ def prefill_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.
             k.data_ptr(), ks, v.data_ptr(), vs, cq, ck, o.data_ptr(),
             None if lse is None else lse.data_ptr(), wp, wn, _raw_stream(dev, stream)))
         return (o, lse) if with_lse else o
+
+
+# ---------------------------------------------------------------- pages
+def alloc_page_refs(n_pages: int, device) -> torch.Tensor:
+    """Reference counts [n_pages] int32 of a pool whose pages are all free."""
+    return torch.zeros(n_pages, dtype=torch.int32, device=device)
+
+
+def alloc_page_table(n_seqs: int, table_pages: int, device) -> torch.Tensor:
+    """A page table [n_seqs, table_pages] int32 of sequences without pages (-1)."""
+    return torch.full((n_seqs, table_pages), -1, dtype=torch.int32, device=device)
+
+
+class PagePools:
+    """The pages of every layer behind one page table, checked once (page_pools)."""
+
+    def __init__(self, caches):
+        caches = [caches] if isinstance(caches, dict) else list(caches)
+        if not caches:
+            raise ValueError("no cache given")
+        k = caches[0]["K"]
+        if k.dim() != 4 or not k.is_cuda:
+            raise ValueError("pages must be CUDA tensors [n_pages, kv_heads, page_size, head_dim]")
+        self.tensors = [c[n] for c in caches for n in ("K", "V")]   # kept alive
+        self.shape, self.dtype, self.device = k.shape, k.dtype, k.device
+        self.count = len(self.tensors)
+        self.pointers = (_vp * self.count)(*[
+            _need(t, f"pages of layer {i // 2}", k.shape, k.dtype, k.device)
+            for i, t in enumerate(self.tensors)])
+
+
+def page_pools(caches) -> PagePools:
+    """A handle of one cache {"K", "V"} or of a sequence of them (one for each
+    layer, the same sizes all), for programs that call paged_fork and paged_keep
+    often; these take the caches themselves, too."""
+    return caches if isinstance(caches, PagePools) else PagePools(caches)
+
+
+def _page_call(shape, dtype, device, page_table: torch.Tensor):
+    """Dims argument of a call on pages, its sequences, and the table's address."""
+    if page_table.dim() != 2:
+        raise ValueError("the page table must be [n_seqs, table_pages]")
+    n, width = page_table.shape
+    return (_page_dims(n, shape[1], shape[1], shape[3], shape[2], shape[0], width, dtype)[1], n,
+            _need(page_table, "page_table", page_table.shape, torch.int32, device))
+
+
+def _ints(t: Optional[torch.Tensor], name: str, shape: tuple, device):
+    return None if t is None else _need(t, name, shape, torch.int32, device)
+
+
+def alloc_pages_workspace(cache, page_table: torch.Tensor, max_forks: int = 0, max_keep: int = 0,
+                          stream=None) -> torch.Tensor:
+    """Workspace of the calls on pages for at most max_forks forks and lists of
+    max_keep rows (status word cleared); calls that may overlap need one each."""
+    with _On(page_table, stream):
+        k = cache.tensors[0] if isinstance(cache, PagePools) else cache["K"]
+        n = ctypes.c_size_t(0)
+        _check("wf_pages_workspace_bytes", lib().wf_pages_workspace_bytes(
+            _page_call(k.shape, k.dtype, k.device, page_table)[0], max_forks, max_keep,
+            ctypes.byref(n)))
+        ws = torch.empty(n.value, dtype=torch.uint8, device=k.device)
+        _check("wf_clear_device_status", lib().wf_clear_device_status(
+            ws.data_ptr(), ws.numel(), _raw_stream(k.device, stream)))
+        return ws
+
+
+def paged_reserve(cache, page_table: torch.Tensor, refs: torch.Tensor, rows: torch.Tensor,
+                  ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """wf_paged_reserve: sequence s of page_table (in place) gets pages for its
+    first rows[s] rows where it has none, the lowest free ones of refs (in
+    place).  ``cache``: one layer's {"K", "V"} (for the sizes) or page_pools()."""
+    with _On(page_table, stream):
+        k = cache.tensors[0] if isinstance(cache, PagePools) else cache["K"]
+        dev = k.device
+        dims, n, tp = _page_call(k.shape, k.dtype, dev, page_table)
+        if ws is None:
+            ws = alloc_pages_workspace(cache, page_table, stream=stream)
+        wp, wn = _ws_args(ws, dev)
+        _check("wf_paged_reserve", lib().wf_paged_reserve(
+            dims, _ints(rows, "rows", (n,), dev), _ints(refs, "refs", (k.shape[0],), dev), tp, wp,
+            wn, _raw_stream(dev, stream)))
+
+
+def paged_fork(caches, page_table: torch.Tensor, refs: torch.Tensor, src: torch.Tensor,
+               dst: torch.Tensor, kv_len: torch.Tensor,
+               share_rows: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """wf_paged_fork: sequence dst[i], which holds no pages, becomes a copy of
+    sequence src[i] (kv_len [n_seqs] rows each, of which the caller sets the
+    children's): whole pages below share_rows[i] (default: all whole pages) are
+    shared, the rest is copied in every layer of ``caches`` (one cache {"K",
+    "V"}, a sequence of them, or page_pools()).  page_table and refs in place."""
+    with _On(page_table, stream):
+        pools = page_pools(caches)
+        dev, n_forks = pools.device, src.numel()
+        dims, n, tp = _page_call(pools.shape, pools.dtype, dev, page_table)
+        if ws is None:
+            ws = alloc_pages_workspace(pools, page_table, max_forks=n_forks, stream=stream)
+        wp, wn = _ws_args(ws, dev)
+        _check("wf_paged_fork", lib().wf_paged_fork(
+            dims, n_forks, _ints(src, "src", (n_forks,), dev), _ints(dst, "dst", (n_forks,), dev),
+            _ints(kv_len, "kv_len", (n,), dev), _ints(share_rows, "share_rows", (n_forks,), dev),
+            _ints(refs, "refs", (pools.shape[0],), dev), tp, pools.count, pools.pointers, wp, wn,
+            _raw_stream(dev, stream)))
+
+
+def paged_keep(caches, page_table: torch.Tensor, kv_len: torch.Tensor, start: torch.Tensor,
+               keep: Optional[torch.Tensor] = None, n_keep: Optional[torch.Tensor] = None,
+               refs: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """wf_paged_keep: of each sequence's kv_len[s] rows the first start[s] stay,
+    rows keep[s, :n_keep[s]] (ascending, keep [n_seqs, max_keep]) move up behind
+    them in every layer of ``caches``, and the pages behind the new length
+    start[s] + n_keep[s] are given back to refs.  Without keep and n_keep
+    nothing behind start is kept; without refs no page is given back."""
+    with _On(page_table, stream):
+        pools = page_pools(caches)
+        dev = pools.device
+        dims, n, tp = _page_call(pools.shape, pools.dtype, dev, page_table)
+        if keep is not None and keep.dim() != 2:
+            raise ValueError("keep must be [n_seqs, max_keep]")
+        most = 0 if keep is None else keep.shape[1]
+        if ws is None:
+            ws = alloc_pages_workspace(pools, page_table, max_keep=most, stream=stream)
+        wp, wn = _ws_args(ws, dev)
+        _check("wf_paged_keep", lib().wf_paged_keep(
+            dims, _ints(kv_len, "kv_len", (n,), dev), _ints(start, "start", (n,), dev),
+            _ints(keep, "keep", (n, most), dev), most, _ints(n_keep, "n_keep", (n,), dev),
+            _ints(refs, "refs", (pools.shape[0],), dev), tp, pools.count, pools.pointers, wp, wn,
+            _raw_stream(dev, stream)))
+
+
+def paged_release(cache, page_table: torch.Tensor, refs: torch.Tensor, first: torch.Tensor,
+                  end: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """wf_paged_release: the pages of sequence s all of whose rows lie in
+    [first[s], end[s]) are given back (0, 2^31 - 1: the whole sequence).
+    ``cache``: one layer's {"K", "V"} (for the sizes) or page_pools()."""
+    with _On(page_table, stream):
+        k = cache.tensors[0] if isinstance(cache, PagePools) else cache["K"]
+        dev = k.device
+        dims, n, tp = _page_call(k.shape, k.dtype, dev, page_table)
+        wp, wn = _ws_args(ws, dev)
+        _check("wf_paged_release", lib().wf_paged_release(
+            dims, _ints(first, "first", (n,), dev), _ints(end, "end", (n,), dev),
+            _ints(refs, "refs", (k.shape[0],), dev), tp, wp, wn, _raw_stream(dev, stream)))
 
 
 def raw_call(name: str, *args) -> int:

@@ -223,6 +223,40 @@ struct PrefillArgs {
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_fma(const PrefillArgs& a, cudaStream_t stream);
 
+// The pages of a paged cache (wf_pages.cu; entry points in wf_pages_api.cu).
+struct PagesArgs {
+  int32_t *refs, *table;                  // refs nullable in keep
+  int32_t* status;
+  int n_seqs, kv_heads, head_dim, page_size, n_pages, table_pages, dtype;
+};
+// Key and value pages of every layer of a call (kernel parameter).
+struct PagePools {
+  void* at[WF_MAX_POOLS];
+  int n;
+};
+// Reserve: `units` = sequences, rows[s] of each.  Fork: units = forks, rows =
+// every sequence's length.  Scratch behind the status word.
+struct AllocArgs {
+  PagesArgs p;
+  const int32_t *rows, *src, *dst, *share;  // share nullable
+  int32_t *base, *list;                   // [units]; free pages by rank [n_pages]
+  int4* copies;                           // fork: (from, to, rows, -) by rank [n_pages]
+  int32_t* n_copies;
+  int units;
+};
+struct KeepArgs {
+  PagesArgs p;
+  const int32_t *kv_len, *start, *keep, *n_keep;  // keep and n_keep nullable together
+  int32_t* lines;                         // scratch: cache lines of the kept rows
+  int4* info;                             // scratch: [n_seqs]
+  int max_keep;
+};
+cudaError_t launch_reserve(const AllocArgs& x, cudaStream_t stream);
+cudaError_t launch_fork(const AllocArgs& x, const PagePools& pools, cudaStream_t stream);
+cudaError_t launch_release(const PagesArgs& a, const int32_t* first, const int32_t* end,
+                           cudaStream_t stream);
+cudaError_t launch_keep(const KeepArgs& x, const PagePools& pools, cudaStream_t stream);
+
 // Keys per tile of the paged attention's work list.
 constexpr int kPagedTile = 64;
 

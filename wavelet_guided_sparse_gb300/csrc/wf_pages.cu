@@ -1,0 +1,489 @@
+// The pages of a paged cache: taking free ones, sharing and copying them,
+// moving kept rows together, giving them back.
+//
+// refs[p] counts the page table entries that hold page p; a page with 0 is
+// free.  Free pages are taken lowest first: the i-th entry that needs a page
+// (sequence by sequence, entry by entry) gets the i-th lowest free one, so that
+// the result is a function of the inputs alone.
+//
+// alloc_kernel (reserve, fork) counts needs and free pages in one cluster,
+// each CTA and warp over a contiguous share of both, exchanges the counts
+// through distributed shared memory, lists the free pages by rank and fills
+// the entries from that list.  Up to kOneCta pages one CTA does it (no
+// cluster to gather: 1 us less), above that eight share the pass over refs.
+//
+// copy_pages_kernel moves what a fork copies: HBM-bound, each warp takes one
+// head's rows of a page (contiguous) of one pool and keeps eight 16-byte loads
+// a lane in flight.
+//
+// move_rows_kernel moves kept rows up in place.  Kept rows ascend, so row i
+// (destination start + i) never lands on the source of a later one, and a
+// group (a warp or a CTA) may read a step's rows, and the next step's, meet,
+// and write the first.  Rows are split into 128-byte pieces: each (sequence,
+// pool, head, piece) is one independent stream in order.
+#include <algorithm>
+
+#include "wf_attn.cuh"
+
+namespace wf {
+
+namespace {
+
+constexpr int kAllocThreads = 1024, kAllocWarps = kAllocThreads / 32, kAllocCluster = 8;
+constexpr int kOneCta = 16384;  // pages that one CTA counts alone
+constexpr int kSeqWords = WF_MAX_SEQS / 32;
+
+__device__ __forceinline__ int max_len(const PagesArgs& a) { return a.table_pages * a.page_size; }
+
+// A length clamped into a sequence's table; flags one outside.
+__device__ __forceinline__ int length_in(const PagesArgs& a, int n, bool say) {
+  if (say && (n < 0 || n > max_len(a))) raise_flag(a.status, WF_DEV_BAD_INDEX);
+  return min(max(n, 0), max_len(a));
+}
+
+// One reference less; flags a page that had none.
+__device__ __forceinline__ void drop_page(const PagesArgs& a, int page) {
+  if (page >= a.n_pages || atomicSub(a.refs + page, 1) <= 0) {
+    if (page < a.n_pages) atomicAdd(a.refs + page, 1);
+    raise_flag(a.status, WF_DEV_BAD_INDEX);
+  }
+}
+
+// Entries [first, end) of a sequence's table row, by threads thread, thread +
+// threads, ...: their pages lose a reference, the entries become -1.
+__device__ __forceinline__ void drop_entries(const PagesArgs& a, int s, int first, int end,
+                                             int thread, int threads) {
+  int32_t* row = a.table + static_cast<int64_t>(s) * a.table_pages;
+  for (int e = first + thread; e < end; e += threads) {
+    const int page = row[e];
+    if (page < 0) continue;
+    row[e] = -1;
+    drop_page(a, page);
+  }
+}
+
+// What a fork takes: parent, child, entries that are shared, entries in all.
+struct ForkUnit {
+  int src, dst, shared, entries, len;
+};
+
+struct AllocShared {
+  uint32_t is_src[kSeqWords], once[kSeqWords], twice[kSeqWords];
+  int warp_need[kAllocWarps], warp_free[kAllocWarps];
+  int need[kAllocCluster], free[kAllocCluster];  // every CTA's totals
+};
+
+__device__ __forceinline__ bool bit_of(const uint32_t* words, int i) {
+  return (words[i >> 5] >> (i & 31)) & 1;
+}
+
+// Fork i, or entries = 0 where it is unsound (a row outside the table, a child
+// that is also a parent, or one of two forks).
+__device__ __forceinline__ ForkUnit fork_unit(const AllocArgs& x, const AllocShared& sm, int i,
+                                              bool say) {
+  const PagesArgs& a = x.p;
+  ForkUnit u = {__ldg(x.src + i), __ldg(x.dst + i), 0, 0, 0};
+  if (static_cast<unsigned>(u.src) >= static_cast<unsigned>(a.n_seqs) ||
+      static_cast<unsigned>(u.dst) >= static_cast<unsigned>(a.n_seqs)) {
+    if (say) raise_flag(a.status, WF_DEV_BAD_INDEX);
+    u.dst = -1;
+    return u;
+  }
+  if (bit_of(sm.is_src, u.dst) || bit_of(sm.twice, u.dst)) {
+    if (say) raise_flag(a.status, WF_DEV_DUP_INDEX);
+    u.dst = -1;
+    return u;
+  }
+  u.len = length_in(a, __ldg(x.rows + u.src), say);
+  u.entries = (u.len + a.page_size - 1) / a.page_size;
+  const int share = x.share != nullptr ? min(max(__ldg(x.share + i), 0), u.len) : u.len;
+  u.shared = share / a.page_size;
+  return u;
+}
+
+// Entries of sequence s that a reserve has to fill.
+__device__ __forceinline__ int reserve_entries(const AllocArgs& x, int s, bool say) {
+  return (length_in(x.p, __ldg(x.rows + s), say) + x.p.page_size - 1) / x.p.page_size;
+}
+
+template <bool FORK>
+__global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x) {
+  __shared__ AllocShared sm;
+  const PagesArgs& a = x.p;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = static_cast<int>(cluster.num_blocks());
+  const int me = static_cast<int>(cluster.block_rank());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gw = me * kAllocWarps + warp, warps = ctas * kAllocWarps;
+  launch_dependents();
+  if (FORK) {
+    for (int i = threadIdx.x; i < kSeqWords; i += kAllocThreads)
+      sm.is_src[i] = sm.once[i] = sm.twice[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < x.units; i += kAllocThreads) {
+      const int s = __ldg(x.src + i), d = __ldg(x.dst + i);
+      if (static_cast<unsigned>(s) < static_cast<unsigned>(a.n_seqs))
+        atomicOr(&sm.is_src[s >> 5], 1u << (s & 31));
+      if (static_cast<unsigned>(d) < static_cast<unsigned>(a.n_seqs) &&
+          (atomicOr(&sm.once[d >> 5], 1u << (d & 31)) >> (d & 31) & 1))
+        atomicOr(&sm.twice[d >> 5], 1u << (d & 31));
+    }
+    __syncthreads();
+  }
+  // This warp's units and pages, both contiguous in order.
+  const int u0 = static_cast<int>(static_cast<int64_t>(x.units) * gw / warps);
+  const int u1 = static_cast<int>(static_cast<int64_t>(x.units) * (gw + 1) / warps);
+  const int p0 = static_cast<int>(static_cast<int64_t>(a.n_pages) * gw / warps);
+  const int p1 = static_cast<int>(static_cast<int64_t>(a.n_pages) * (gw + 1) / warps);
+  int need = 0;
+  for (int u = u0; u < u1; ++u) {
+    if (lane == 0) x.base[u] = need;  // within the warp
+    if (FORK) {
+      const ForkUnit f = fork_unit(x, sm, u, lane == 0);
+      need += f.entries - f.shared;
+    } else {
+      const int entries = reserve_entries(x, u, lane == 0);
+      const int32_t* row = a.table + static_cast<int64_t>(u) * a.table_pages;
+      for (int e = lane; e - lane < entries; e += 32)
+        need += __popc(__ballot_sync(0xffffffffu, e < entries && row[e] < 0));
+    }
+  }
+  int free = 0;
+#pragma unroll 4
+  for (int p = p0 + lane; p < p1; p += 32) free += a.refs[p] == 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) free += __shfl_xor_sync(0xffffffffu, free, o);
+  if (lane == 0) {
+    sm.warp_need[warp] = need;
+    sm.warp_free[warp] = free;
+  }
+  __syncthreads();
+  if (warp < 2) {  // exclusive sums over the CTA's warps; totals to every CTA
+    int* mine = warp == 0 ? sm.warp_need : sm.warp_free;
+    int* totals = warp == 0 ? sm.need : sm.free;
+    const int v = mine[lane], incl = warp_incl_scan(v);
+    mine[lane] = incl - v;
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
+    if (ctas == 1) {
+      if (lane == 0) totals[0] = total;
+    } else if (lane < ctas) {
+      *cluster.map_shared_rank(totals + me, lane) = total;
+    }
+  }
+  cluster.sync();
+  int need_before = sm.warp_need[warp], free_before = sm.warp_free[warp];
+  int total_need = 0, total_free = 0;
+  for (int c = 0; c < ctas; ++c) {
+    if (c < me) {
+      need_before += sm.need[c];
+      free_before += sm.free[c];
+    }
+    total_need += sm.need[c];
+    total_free += sm.free[c];
+  }
+  // The free pages by rank, as far as they are needed.
+  for (int p = p0; p < p1 && free_before < total_need; p += 32) {
+    const bool is = p + lane < p1 && a.refs[p + lane] == 0;
+    const unsigned hits = __ballot_sync(0xffffffffu, is);
+    const int rank = free_before + __popc(hits & ((1u << lane) - 1));
+    if (is && rank < total_need) x.list[rank] = p + lane;
+    free_before += __popc(hits);
+  }
+  if (total_need > total_free && gw == 0 && lane == 0) raise_flag(a.status, WF_DEV_NO_PAGE);
+  if (FORK && gw == 0 && lane == 0) *x.n_copies = min(total_need, total_free);
+  __threadfence();
+  cluster.sync();
+  for (int u = u0; u < u1; ++u) {
+    int rank = need_before + x.base[u];
+    if (FORK) {
+      const ForkUnit f = fork_unit(x, sm, u, false);
+      if (f.dst < 0) continue;
+      const int32_t* from = a.table + static_cast<int64_t>(f.src) * a.table_pages;
+      int32_t* to = a.table + static_cast<int64_t>(f.dst) * a.table_pages;
+      for (int e = lane; e < a.table_pages; e += 32) {
+        int page = -1;
+        if (e < f.entries) {
+          const int parent = from[e];
+          const bool there = static_cast<unsigned>(parent) < static_cast<unsigned>(a.n_pages);
+          if (!there) raise_flag(a.status, WF_DEV_BAD_INDEX);
+          if (e < f.shared) {
+            if (there) {
+              page = parent;
+              atomicAdd(a.refs + page, 1);
+            }
+          } else {
+            const int r = rank + e - f.shared;
+            if (r < total_free) {
+              page = x.list[r];
+              a.refs[page] = 1;
+              x.copies[r] = make_int4(there ? parent : -1, page,
+                                      min(a.page_size, f.len - e * a.page_size), 0);
+            }
+          }
+        }
+        to[e] = page;
+      }
+    } else {
+      const int entries = reserve_entries(x, u, false);
+      int32_t* row = a.table + static_cast<int64_t>(u) * a.table_pages;
+      for (int e = lane; e - lane < entries; e += 32) {
+        const bool lacks = e < entries && row[e] < 0;
+        const unsigned hits = __ballot_sync(0xffffffffu, lacks);
+        const int r = rank + __popc(hits & ((1u << lane) - 1));
+        if (lacks && r < total_free) {
+          row[e] = x.list[r];
+          a.refs[x.list[r]] = 1;
+        }
+        rank += __popc(hits);
+      }
+    }
+  }
+}
+
+// Whole rows of pages: unit = (copy, pool, head), a warp each.
+__global__ void __launch_bounds__(kThreads)
+    copy_pages_kernel(const AllocArgs x, const PagePools pools, int row_chunks) {
+  constexpr int kFly = 8;
+  wait_for_primary();
+  const PagesArgs& a = x.p;
+  const int lane = threadIdx.x & 31;
+  const int per_copy = pools.n * a.kv_heads;
+  const int64_t units = static_cast<int64_t>(*x.n_copies) * per_copy;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units;
+       u += step) {
+    const int copy = static_cast<int>(u / per_copy);
+    const int rest = static_cast<int>(u - static_cast<int64_t>(copy) * per_copy);
+    const int pool = rest / a.kv_heads, head = rest - pool * a.kv_heads;
+    const int4 c = x.copies[copy];
+    if (c.x < 0) continue;
+    uint4* base = static_cast<uint4*>(pools.at[pool]);
+    const int64_t line = static_cast<int64_t>(a.page_size) * row_chunks;  // chunks of a head's rows
+    const uint4* from = base + (static_cast<int64_t>(c.x) * a.kv_heads + head) * line;
+    uint4* to = base + (static_cast<int64_t>(c.y) * a.kv_heads + head) * line;
+    const int chunks = c.z * row_chunks;
+    for (int i = lane; i < chunks; i += 32 * kFly) {
+      uint4 v[kFly];
+#pragma unroll
+      for (int k = 0; k < kFly; ++k)
+        if (i + 32 * k < chunks) v[k] = __ldcs(from + i + 32 * k);
+#pragma unroll
+      for (int k = 0; k < kFly; ++k)
+        if (i + 32 * k < chunks) to[i + 32 * k] = v[k];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) release_kernel(const PagesArgs a, const int32_t* first,
+                                                           const int32_t* end) {
+  for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
+    const int lo = min(max(__ldg(first + s), 0), max_len(a));
+    const int hi = min(max(__ldg(end + s), 0), max_len(a));
+    // Pages all of whose rows lie in [lo, hi).
+    drop_entries(a, s, (lo + (a.page_size - 1)) / a.page_size, hi / a.page_size, threadIdx.x,
+                 kThreads);
+  }
+}
+
+// ---------------------------------------------------------------- kept rows
+// Checks one sequence's list, resolves the rows that move and leaves in
+// info[s] = (rows at the head that stay where they are, rows in all, new length
+// or -1 when the sequence is left as it was).
+__global__ void __launch_bounds__(kThreads) keep_plan_kernel(const KeepArgs x) {
+  const PagesArgs& a = x.p;
+  __shared__ int s_bad, s_shared, s_stay;
+  launch_dependents();
+  for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
+    __syncthreads();
+    if (threadIdx.x == 0) s_bad = s_shared = 0;
+    const int len = __ldg(x.kv_len + s), start = __ldg(x.start + s);
+    const int n = x.n_keep != nullptr ? __ldg(x.n_keep + s) : 0;
+    const bool sound = len >= 0 && len <= max_len(a) && start >= 0 && start <= len && n >= 0 &&
+                       n <= x.max_keep;
+    const int count = sound ? n : 0;
+    if (threadIdx.x == 0) s_stay = count;
+    __syncthreads();
+    const int32_t* keep = x.keep + static_cast<int64_t>(s) * x.max_keep;
+    const int32_t* row = a.table + static_cast<int64_t>(s) * a.table_pages;
+    bool bad = !sound, shared = false;
+    for (int i = threadIdx.x; i < count; i += kThreads) {
+      const int from = __ldg(keep + i);
+      if (from < (i > 0 ? __ldg(keep + i - 1) + 1 : start) || from >= len) {
+        bad = true;
+        continue;
+      }
+      if (from == start + i) continue;  // so are all before it
+      atomicMin(&s_stay, i);
+      const int to = row[(start + i) / a.page_size], page = row[from / a.page_size];
+      if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages) ||
+          static_cast<unsigned>(to) >= static_cast<unsigned>(a.n_pages))
+        bad = true;
+      else if (a.refs != nullptr && a.refs[to] > 1)
+        shared = true;
+      x.lines[static_cast<int64_t>(s) * x.max_keep + i] =
+          page * a.page_size + (from & (a.page_size - 1));
+    }
+    if (bad) s_bad = 1;
+    if (shared) s_shared = 1;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      if (s_bad) raise_flag(a.status, WF_DEV_BAD_INDEX);
+      if (s_shared) raise_flag(a.status, WF_DEV_SHARED_PAGE);
+      const bool skip = s_bad || s_shared;
+      x.info[s] = skip ? make_int4(0, 0, -1, 0) : make_int4(s_stay, count, start + count, start);
+    }
+  }
+}
+
+// Streams (sequence, pool, head, 128-byte piece of a row), each by GROUP
+// threads, kRows of them a step's rows side by side, kFly steps' worth in
+// flight twice.
+constexpr int kPiece = 8;  // 16-byte chunks
+template <int GROUP>
+__global__ void __launch_bounds__(kThreads)
+    move_rows_kernel(const KeepArgs x, const PagePools pools, int row_chunks, int page_shift) {
+  constexpr int kFly = 4, kSide = GROUP / kPiece, kStep = kFly * kSide;
+  const PagesArgs& a = x.p;
+  wait_for_primary();
+  const int thread = GROUP == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const int pieces = row_chunks / kPiece, heads = a.kv_heads;
+  const int per_seq = max(1, pools.n * heads * pieces);
+  const int64_t streams = static_cast<int64_t>(a.n_seqs) * per_seq;
+  const int groups = kThreads / GROUP;
+  const auto meet = [] {
+    if (GROUP == 32) __syncwarp(); else __syncthreads();
+  };
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / GROUP; w < streams;
+       w += static_cast<int64_t>(gridDim.x) * groups) {
+    const int s = static_cast<int>(w / per_seq);
+    const int rest = static_cast<int>(w - static_cast<int64_t>(s) * per_seq);
+    const int4 info = x.info[s];
+    if (rest == 0 && info.z >= 0 && a.refs != nullptr)
+      drop_entries(a, s, (info.z + a.page_size - 1) >> page_shift, a.table_pages, thread, GROUP);
+    if (info.x >= info.y) continue;  // the same for the whole group
+    const int piece = rest % pieces, head = rest / pieces % heads, pool = rest / pieces / heads;
+    uint4* base = static_cast<uint4*>(pools.at[pool]) + piece * kPiece + thread % kPiece;
+    const int32_t* lines = x.lines + static_cast<int64_t>(s) * x.max_keep;
+    const int32_t* row = a.table + static_cast<int64_t>(s) * a.table_pages;
+    // Chunk offset of a cache line (page * page_size + row) of this head.
+    const auto place = [&](int page, int r) {
+      return ((static_cast<int64_t>(page) * heads + head) * a.page_size + r) * row_chunks;
+    };
+    const int mask = a.page_size - 1;
+    uint4 v[2][kFly];
+    int next[kFly];
+    const auto read_lines = [&](int i0) {
+#pragma unroll
+      for (int k = 0; k < kFly; ++k) {
+        const int i = i0 + k * kSide + thread / kPiece;
+        next[k] = i < info.y ? lines[i] : -1;
+      }
+    };
+    const auto read_rows = [&](uint4* to) {
+#pragma unroll
+      for (int k = 0; k < kFly; ++k)
+        if (next[k] >= 0) to[k] = base[place(next[k] >> page_shift, next[k] & mask)];
+    };
+    const auto write_rows = [&](const uint4* from, int i0) {
+#pragma unroll
+      for (int k = 0; k < kFly; ++k) {
+        const int i = i0 + k * kSide + thread / kPiece, at = info.w + i;
+        if (i < info.y) base[place(row[at >> page_shift], at & mask)] = from[k];
+      }
+    };
+    int i = info.x;
+    read_lines(i);
+    read_rows(v[0]);
+    read_lines(i + kStep);
+    while (true) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        read_rows(v[b ^ 1]);
+        read_lines(i + 2 * kStep);
+        meet();  // every row of this step has been read
+        write_rows(v[b], i);
+        i += kStep;
+        if (i >= info.y) break;
+      }
+      if (i >= info.y) break;
+    }
+  }
+}
+
+int row_chunks_of(const PagesArgs& a) { return a.head_dim * (a.dtype == WF_BF16 ? 2 : 4) / 16; }
+
+cudaLaunchConfig_t config(unsigned grid, unsigned block, cudaStream_t stream,
+                          cudaLaunchAttribute* attr, int cluster, bool dependent) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  if (cluster > 1) {
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = cluster;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+  } else if (dependent) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+  }
+  return cfg;
+}
+
+template <bool FORK>
+cudaError_t launch_alloc(const AllocArgs& x, cudaStream_t stream) {
+  const int ctas = x.p.n_pages <= kOneCta ? 1 : kAllocCluster;
+  cudaLaunchAttribute attr = {};
+  const cudaLaunchConfig_t cfg = config(ctas, kAllocThreads, stream, &attr, ctas, false);
+  return cudaLaunchKernelEx(&cfg, alloc_kernel<FORK>, x);
+}
+
+unsigned grid_of(int64_t blocks) {
+  return static_cast<unsigned>(
+      std::max<int64_t>(1, std::min<int64_t>(blocks, 8 * device_sm_count())));
+}
+
+}  // namespace
+
+cudaError_t launch_reserve(const AllocArgs& x, cudaStream_t stream) {
+  return launch_alloc<false>(x, stream);
+}
+
+cudaError_t launch_fork(const AllocArgs& x, const PagePools& pools, cudaStream_t stream) {
+  const cudaError_t e = launch_alloc<true>(x, stream);
+  if (e != cudaSuccess) return e;
+  const int64_t most =
+      std::min<int64_t>(x.p.n_pages, static_cast<int64_t>(x.units) * x.p.table_pages);
+  cudaLaunchAttribute attr = {};
+  const cudaLaunchConfig_t cfg = config(grid_of(most * pools.n * x.p.kv_heads / kWarps + 1),
+                                        kThreads, stream, &attr, 1, true);
+  return cudaLaunchKernelEx(&cfg, copy_pages_kernel, x, pools, row_chunks_of(x.p));
+}
+
+cudaError_t launch_release(const PagesArgs& a, const int32_t* first, const int32_t* end,
+                           cudaStream_t stream) {
+  release_kernel<<<grid_of(a.n_seqs), kThreads, 0, stream>>>(a, first, end);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_keep(const KeepArgs& x, const PagePools& pools, cudaStream_t stream) {
+  keep_plan_kernel<<<grid_of(x.p.n_seqs), kThreads, 0, stream>>>(x);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int chunks = row_chunks_of(x.p);
+  int shift = 0;
+  while ((1 << shift) < x.p.page_size) ++shift;
+  // A warp a stream where lists are short (an accepted path), else a CTA.
+  const int64_t streams = static_cast<int64_t>(x.p.n_seqs) *
+                          std::max(1, pools.n * x.p.kv_heads * (chunks / kPiece));
+  const bool warps = x.max_keep <= 32;
+  cudaLaunchAttribute attr = {};
+  const cudaLaunchConfig_t cfg = config(grid_of(warps ? (streams + kWarps - 1) / kWarps : streams),
+                                        kThreads, stream, &attr, 1, true);
+  return warps ? cudaLaunchKernelEx(&cfg, move_rows_kernel<32>, x, pools, chunks, shift)
+               : cudaLaunchKernelEx(&cfg, move_rows_kernel<kThreads>, x, pools, chunks, shift);
+}
+
+}  // namespace wf
