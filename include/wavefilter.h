@@ -28,6 +28,8 @@
  *
  *   wf_paged_append        new rows into a paged cache, rotated on the way
  *   wf_paged_attn          §2.1 eq. (3) of new tokens over a whole paged cache
+ *   wf_paged_window_attn   over a sliding window of it and its first tokens
+ *   wf_paged_tree_attn     by the nodes of a drafted tree
  *   wf_prefill_attn        §2.1 eq. (1) over packed prompts
  *   wf_paged_reserve, wf_paged_fork, wf_paged_keep, wf_paged_release
  *                          the pages themselves: taken, shared or copied,
@@ -576,6 +578,54 @@ int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_
                   const void* K_pages, const void* V_pages, const int32_t* page_table,
                   const int32_t* kv_len, void* O, float* lse, void* workspace,
                   size_t workspace_bytes, void* stream);
+
+/* The same over a sliding window (and the first tokens) of each cache: key j of
+ * the query at position p counts when j < kv_len and (j < sinks or p - j <
+ * window), and besides j <= p (causal), or j < sinks or j - p < window (not
+ * causal).
+ *   window : >= 1; sinks : >= 0
+ *   page_table : entries of pages whose rows no query of the sequence sees are
+ *                not looked at, so that their pages may be gone
+ *                (wf_paged_release with first = sinks, end = kv_len - n_new -
+ *                window + 1)
+ *   workspace  : >= wf_paged_attn_workspace_bytes()
+ * Everything else as wf_paged_attn; values of rows that the window hides must
+ * be finite where their page holds one that some query sees.  opts->prefix
+ * must be NULL (WF_ERR_UNSUPPORTED). */
+int wf_paged_window_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t window,
+                         int32_t sinks, int32_t n_new, const void* Q, const void* K_pages,
+                         const void* V_pages, const int32_t* page_table, const int32_t* kv_len,
+                         void* O, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Bytes of workspace wf_paged_tree_attn needs, as
+ * wf_paged_attn_workspace_bytes. */
+int wf_paged_tree_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_nodes, size_t* bytes);
+
+/* Attention of a tree of drafted tokens of each sequence over its paged cache.
+ * The last rows of a sequence's cache are its nodes: with n = tree_len[s],
+ * node i is row kv_len[s] - n + i and query i.  It sees the rows before the
+ * nodes, its ancestors and itself.  It stands at position kv_len[s] - n + its
+ * depth (a root's is 0): what its rotation (the positions of wf_paged_append)
+ * and a distance bias go by; drafted keys stand at their nodes' positions.
+ *   n_nodes  : 1..64, most nodes of a sequence; Q, O and lse have n_nodes rows
+ *              a sequence
+ *   parents  : device, [n_seqs, n_nodes] int32: the parent of node i, below i,
+ *              or negative for none (a root; several are fine).  Another one is
+ *              flagged WF_DEV_BAD_INDEX and taken for none
+ *   tree_len : device, nullable, [n_seqs] int32, nodes of each sequence,
+ *              0..n_nodes (clamped and flagged otherwise; default n_nodes for
+ *              all).  Rows behind a sequence's nodes get O = 0, lse = -inf,
+ *              whatever their queries hold.  A sequence without nodes is idle,
+ *              and so, flagged, is one with fewer rows than nodes
+ *   opts     : causal must be set and prefix NULL (WF_ERR_UNSUPPORTED)
+ *   workspace: device, >= wf_paged_tree_attn_workspace_bytes()
+ * Everything else as wf_paged_attn. */
+int wf_paged_tree_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_nodes,
+                       const void* Q, const void* K_pages, const void* V_pages,
+                       const int32_t* page_table, const int32_t* kv_len, const int32_t* parents,
+                       const int32_t* tree_len, void* O, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 /* ---- Pages.  The pool's state is one count per page: refs [n_pages] int32
  * (device, in/out), the number of page table entries that hold the page; 0

@@ -37,6 +37,7 @@ EXPORTS = ("wf_status_string", "wf_last_error_string", "wf_default_k_per_level",
            "wf_step_basis",
            "wf_rope_inv_freq", "wf_paged_append", "wf_paged_attn_workspace_bytes",
            "wf_paged_attn", "wf_prefill_attn",
+           "wf_paged_window_attn", "wf_paged_tree_attn_workspace_bytes", "wf_paged_tree_attn",
            "wf_pages_workspace_bytes", "wf_paged_reserve", "wf_paged_fork", "wf_paged_keep",
            "wf_paged_release")
 
@@ -139,6 +140,11 @@ _SIGS = {
                                      _vp, _sz, _vp]),
     "wf_prefill_attn": (ctypes.c_int, [ctypes.POINTER(PrefillDims), _OPTSP, _vp, _i64, _vp, _i64,
                                        _vp, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "wf_paged_window_attn": (ctypes.c_int, [_PDIMSP, _OPTSP, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                            _vp, _vp, _vp, _vp, _sz, _vp]),
+    "wf_paged_tree_attn_workspace_bytes": (ctypes.c_int, [_PDIMSP, _i32, ctypes.POINTER(_sz)]),
+    "wf_paged_tree_attn": (ctypes.c_int, [_PDIMSP, _OPTSP, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                          _vp, _vp, _vp, _vp, _sz, _vp]),
     "wf_pages_workspace_bytes": (ctypes.c_int, [_PDIMSP, _i32, _i32, ctypes.POINTER(_sz)]),
     "wf_paged_reserve": (ctypes.c_int, [_PDIMSP, _vp, _vp, _vp, _vp, _sz, _vp]),
     "wf_paged_fork": (ctypes.c_int, [_PDIMSP, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
@@ -664,6 +670,13 @@ def _attn_opts(causal, prefix, softcap, slopes, scale, n_seqs: int, q_heads: int
     return opts
 
 
+def _reach(n: int, name: str, least: int) -> int:
+    """A count of keys; what 32 bits do not hold is as good as all."""
+    if n < least:
+        raise ValueError(f"{name} must be at least {least}")
+    return min(n, 2 ** 31 - 1)
+
+
 def _ws_args(ws: Optional[torch.Tensor], device):
     if ws is None:
         return None, 0
@@ -716,22 +729,32 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, cache: dict, page_table: torc
         return res
 
 
-def alloc_paged_attn_workspace(q: torch.Tensor, cache: dict, page_table: torch.Tensor,
-                               stream=None) -> torch.Tensor:
-    """Workspace of paged_attn for these tensors' sizes (status word cleared);
-    calls that may overlap need one each."""
+def _attn_workspace(entry: str, q: torch.Tensor, cache: dict, page_table: torch.Tensor, stream):
     with _On(q, stream):
         if q.dim() != 4:
             raise ValueError("q must be [n_seqs, n_new, q_heads, head_dim]")
         shape, table = _pages(cache, page_table, q.dtype, q.device)[:2]
         n = ctypes.c_size_t(0)
-        _check("wf_paged_attn_workspace_bytes", lib().wf_paged_attn_workspace_bytes(
+        _check(entry, getattr(lib(), entry)(
             _page_dims(table[0], q.shape[2], shape[1], shape[3], shape[2], shape[0], table[1],
                        q.dtype)[1], q.shape[1], ctypes.byref(n)))
         ws = torch.empty(n.value, dtype=torch.uint8, device=q.device)
         _check("wf_clear_device_status", lib().wf_clear_device_status(
             ws.data_ptr(), ws.numel(), _raw_stream(q.device, stream)))
         return ws
+
+
+def alloc_paged_attn_workspace(q: torch.Tensor, cache: dict, page_table: torch.Tensor,
+                               stream=None) -> torch.Tensor:
+    """Workspace of paged_attn and paged_window_attn for these tensors' sizes
+    (status word cleared); calls that may overlap need one each."""
+    return _attn_workspace("wf_paged_attn_workspace_bytes", q, cache, page_table, stream)
+
+
+def alloc_paged_tree_workspace(q: torch.Tensor, cache: dict, page_table: torch.Tensor,
+                               stream=None) -> torch.Tensor:
+    """The same for paged_tree_attn."""
+    return _attn_workspace("wf_paged_tree_attn_workspace_bytes", q, cache, page_table, stream)
 
 
 def paged_attn(q: torch.Tensor, cache: dict, page_table: torch.Tensor, kv_len: torch.Tensor,
@@ -760,6 +783,71 @@ def paged_attn(q: torch.Tensor, cache: dict, page_table: torch.Tensor, kv_len: t
             _page_dims(n, hq, shape[1], d, shape[2], shape[0], table[1], dt)[1],
             ctypes.byref(opts), n_new, qp, kp, vp, tp,
             _need(kv_len, "kv_len", (n,), torch.int32, dev), o.data_ptr(),
+            None if lse is None else lse.data_ptr(), wp, wn, _raw_stream(dev, stream)))
+        return (o, lse) if with_lse else o
+
+
+def paged_window_attn(q: torch.Tensor, cache: dict, page_table: torch.Tensor, kv_len: torch.Tensor,
+                      window: int, ws: Optional[torch.Tensor] = None, sinks: int = 0,
+                      causal: bool = True, softcap: float = 0.0,
+                      slopes: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                      out: Optional[torch.Tensor] = None, with_lse: bool = False, stream=None):
+    """wf_paged_window_attn: as paged_attn, but of the keys less than ``window``
+    positions away (behind a query, and before it if not ``causal``) and of the
+    first ``sinks`` ones only.  Pages that no query sees need not be there."""
+    with _On(q, stream):
+        if q.dim() != 4:
+            raise ValueError("q must be [n_seqs, n_new, q_heads, head_dim]")
+        dev, dt = q.device, q.dtype
+        shape, table, kp, vp, tp = _pages(cache, page_table, dt, dev)
+        n, n_new, hq, d = q.shape
+        qp = _need(q, "q", (table[0], n_new, hq, shape[3]), dt, dev)
+        opts = _attn_opts(causal, None, softcap, slopes, scale, n, hq, dev)
+        if ws is None:
+            ws = alloc_paged_attn_workspace(q, cache, page_table, stream)
+        wp, wn = _ws_args(ws, dev)
+        o = _out(out, "out", (n, n_new, hq, d), dt, dev)
+        lse = torch.empty((n, n_new, hq), dtype=torch.float32, device=dev) if with_lse else None
+        _check("wf_paged_window_attn", lib().wf_paged_window_attn(
+            _page_dims(n, hq, shape[1], d, shape[2], shape[0], table[1], dt)[1],
+            ctypes.byref(opts), _reach(window, "window", 1), _reach(sinks, "sinks", 0), n_new, qp,
+            kp, vp, tp,
+            _need(kv_len, "kv_len", (n,), torch.int32, dev), o.data_ptr(),
+            None if lse is None else lse.data_ptr(), wp, wn, _raw_stream(dev, stream)))
+        return (o, lse) if with_lse else o
+
+
+def paged_tree_attn(q: torch.Tensor, cache: dict, page_table: torch.Tensor, kv_len: torch.Tensor,
+                    parents: torch.Tensor, ws: Optional[torch.Tensor] = None,
+                    tree_len: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                    slopes: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, with_lse: bool = False, stream=None):
+    """wf_paged_tree_attn: q [n_seqs, n_nodes, q_heads, d], the nodes of each
+    sequence's drafted tree, the last rows of its cache of kv_len [n_seqs] rows.
+    parents [n_seqs, n_nodes] int32: a node's parent, before it, or negative;
+    tree_len [n_seqs]: nodes of each sequence (default: all n_nodes).  Nodes see
+    the rows before the tree, their ancestors and themselves; returns O like q
+    (and lse [n_seqs, n_nodes, q_heads] fp32 if ``with_lse``).  Append the nodes
+    with positions[node] = rows before the tree + depth."""
+    with _On(q, stream):
+        if q.dim() != 4:
+            raise ValueError("q must be [n_seqs, n_nodes, q_heads, head_dim]")
+        dev, dt = q.device, q.dtype
+        shape, table, kp, vp, tp = _pages(cache, page_table, dt, dev)
+        n, nodes, hq, d = q.shape
+        qp = _need(q, "q", (table[0], nodes, hq, shape[3]), dt, dev)
+        opts = _attn_opts(True, None, softcap, slopes, scale, n, hq, dev)
+        if ws is None:
+            ws = alloc_paged_tree_workspace(q, cache, page_table, stream)
+        wp, wn = _ws_args(ws, dev)
+        o = _out(out, "out", (n, nodes, hq, d), dt, dev)
+        lse = torch.empty((n, nodes, hq), dtype=torch.float32, device=dev) if with_lse else None
+        _check("wf_paged_tree_attn", lib().wf_paged_tree_attn(
+            _page_dims(n, hq, shape[1], d, shape[2], shape[0], table[1], dt)[1],
+            ctypes.byref(opts), nodes, qp, kp, vp, tp,
+            _need(kv_len, "kv_len", (n,), torch.int32, dev),
+            _need(parents, "parents", (n, nodes), torch.int32, dev),
+            _ints(tree_len, "tree_len", (n,), dev), o.data_ptr(),
             None if lse is None else lse.data_ptr(), wp, wn, _raw_stream(dev, stream)))
         return (o, lse) if with_lse else o
 

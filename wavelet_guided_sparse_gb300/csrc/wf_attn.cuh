@@ -8,6 +8,12 @@
 // and key j counts when j < len and (not causal, or j <= p, or j < prefix).
 // Kernels keep z in the log2 domain (times log2 e) in fp32; O = Σ 2^(z-m) v /
 // Σ 2^(z-m).  A row without a visible key yields O = 0, lse = -inf.
+//
+// With a window, key j < len counts when j < sinks or p - j < window, and
+// besides j <= p (causal) or j < sinks or j - p < window.  With a drafted tree,
+// the last rows of a sequence are its nodes: node i stands at the position
+// (rows before the nodes) + (its depth) and sees those rows, its ancestors and
+// itself.
 #pragma once
 
 #include <cmath>
@@ -137,27 +143,68 @@ __device__ __forceinline__ void wait_for_primary() {
 // its slot 2c (the unit its range starts inside of) or 2c + 1 (the unit its
 // range ends inside of), and the join kernel merges consecutive CTAs' slots
 // in order (fixed order: bit-identical from run to run).
+//
+// A window leaves a gap between the tiles of the first tokens and those of the
+// window: it is not part of the line.
+enum PagedMask : int { kMaskPlain, kMaskWindow, kMaskTree };
 struct WorkShape {
   int n_seqs;
   int units_per_seq;  // kv_heads * row blocks
   int tile;           // keys per tile
   int max_len;        // table_pages * page_size
+  int n_new, window, sinks;  // window: query rows of a sequence, its sizes
+  const int32_t* tree_len;   // tree: nullable, nodes of each sequence (default n_new)
 };
 
-// Tiles of one sequence: its length clamped into the table (a longer one is
-// flagged by the caller).
-__device__ __forceinline__ int seq_len_clamped(const int32_t* lens, int s, int max_len) {
-  return min(max(__ldg(lens + s), 0), max_len);
+// A sequence's length clamped into the table (a longer one is flagged by the
+// caller); 0 also for one without nodes, or without rows for them.
+template <int MASK = kMaskPlain>
+__device__ __forceinline__ int seq_len_clamped(const WorkShape& w, const int32_t* lens, int s) {
+  const int len = min(max(__ldg(lens + s), 0), w.max_len);
+  if (MASK != kMaskTree) return len;
+  const int nodes = w.tree_len != nullptr ? min(max(__ldg(w.tree_len + s), 0), w.n_new) : w.n_new;
+  return nodes == 0 || len < nodes ? 0 : len;
 }
 
-__device__ __forceinline__ int seq_tiles(const WorkShape& w, const int32_t* lens, int s) {
-  return (seq_len_clamped(lens, s, w.max_len) + w.tile - 1) / w.tile;
+// Window: the first key that the sequence's first query sees by the window, the
+// tiles of the first tokens, the tiles between.
+__device__ __forceinline__ int window_low(const WorkShape& w, int len) {
+  return max(0, len - w.n_new - w.window + 1);
+}
+__device__ __forceinline__ int sink_tiles(const WorkShape& w, int len) {
+  return (min(w.sinks, len) + w.tile - 1) / w.tile;
+}
+template <int MASK>
+__device__ __forceinline__ int window_gap(const WorkShape& w, int len) {
+  if (MASK != kMaskWindow) return 0;
+  return max(0, window_low(w, len) / w.tile - sink_tiles(w, len));
+}
+// The key tile at place t of the sequence's line.
+template <int MASK>
+__device__ __forceinline__ int key_tile(const WorkShape& w, int len, int t) {
+  if (MASK != kMaskWindow) return t;
+  return t < sink_tiles(w, len) ? t : t + window_gap<MASK>(w, len);
+}
+// Whether some query sees one of keys key .. key + rows - 1 (a page that a
+// window has left behind may be gone).
+template <int MASK>
+__device__ __forceinline__ bool box_needed(const WorkShape& w, int len, int key, int rows) {
+  return key < len &&
+         (MASK != kMaskWindow || key < w.sinks || key + rows > window_low(w, len));
+}
+
+// Tiles of a sequence of `len` keys.
+template <int MASK = kMaskPlain>
+__device__ __forceinline__ int tiles_of(const WorkShape& w, int len) {
+  return (len + w.tile - 1) / w.tile - window_gap<MASK>(w, len);
 }
 
 // Tiles of the whole call.  Whole warp.
+template <int MASK = kMaskPlain>
 __device__ __forceinline__ int64_t work_total(const WorkShape& w, const int32_t* lens) {
   int n = 0;  // fits: the host bounds n_seqs times the longest sequence's tiles
-  for (int s = threadIdx.x & 31; s < w.n_seqs; s += 32) n += seq_tiles(w, lens, s);
+  for (int s = threadIdx.x & 31; s < w.n_seqs; s += 32)
+    n += tiles_of<MASK>(w, seq_len_clamped<MASK>(w, lens, s));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return static_cast<int64_t>(n) * w.units_per_seq;
@@ -204,14 +251,15 @@ struct WorkUnit {
 };
 // The unit that holds tile `at` (0 <= at < total).  Whole warp, 32 sequences
 // a step.
+template <int MASK = kMaskPlain>
 __device__ __forceinline__ WorkUnit find_unit(const WorkShape& w, const int32_t* lens,
                                               int64_t at) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   WorkUnit u = {0, 0, 0, 1, 0};
   for (int s0 = 0; s0 < w.n_seqs; s0 += 32) {
-    const int len = s0 + lane < w.n_seqs ? seq_len_clamped(lens, s0 + lane, w.max_len) : 0;
-    const int t = (len + w.tile - 1) / w.tile;
+    const int len = s0 + lane < w.n_seqs ? seq_len_clamped<MASK>(w, lens, s0 + lane) : 0;
+    const int t = tiles_of<MASK>(w, len);
     const int incl = warp_incl_scan(t);
     const unsigned hit = __ballot_sync(
         0xffffffffu, static_cast<int64_t>(base + incl) * w.units_per_seq > at);
@@ -236,32 +284,39 @@ __device__ __forceinline__ WorkUnit find_unit(const WorkShape& w, const int32_t*
 // The unit after u (there is one: the caller stays below the total).  Whole
 // warp, which looks at 32 sequences a step for one with keys where the next one
 // is idle.
+template <int MASK = kMaskPlain>
 __device__ __forceinline__ void next_unit(const WorkShape& w, const int32_t* lens, WorkUnit& u) {
   u.begin += u.tiles;
   if (++u.unit < w.units_per_seq) return;
   u.unit = 0;
   const int lane = threadIdx.x & 31;
   ++u.seq;
-  u.len = u.seq < w.n_seqs ? seq_len_clamped(lens, u.seq, w.max_len) : 0;
+  u.len = u.seq < w.n_seqs ? seq_len_clamped<MASK>(w, lens, u.seq) : 0;
   for (int s0 = u.seq + 1; u.len == 0 && s0 < w.n_seqs; s0 += 32) {
-    const int len = s0 + lane < w.n_seqs ? seq_len_clamped(lens, s0 + lane, w.max_len) : 0;
+    const int len = s0 + lane < w.n_seqs ? seq_len_clamped<MASK>(w, lens, s0 + lane) : 0;
     const unsigned live = __ballot_sync(0xffffffffu, len > 0);
     if (live == 0) continue;
     u.seq = s0 + __ffs(live) - 1;
     u.len = __shfl_sync(0xffffffffu, len, __ffs(live) - 1);
   }
-  u.tiles = (u.len + w.tile - 1) / w.tile;
+  u.tiles = tiles_of<MASK>(w, u.len);
 }
 
 // Rows of a sequence without keys: O = 0, lse = -inf.  CTA c of n, threads
-// thread, thread + threads, ...; flags lengths outside the table.
-template <typename T>
-__device__ __forceinline__ void idle_sequences(const PagedArgs& a, int max_len, int c, int n,
-                                               int thread, int threads) {
+// thread, thread + threads, ...; flags lengths outside the table and trees that
+// have no rows.
+template <typename T, int MASK = kMaskPlain>
+__device__ __forceinline__ void idle_sequences(const PagedArgs& a, const WorkShape& w, int c,
+                                               int n, int thread, int threads) {
   for (int s = c; s < a.n_seqs; s += n) {
     const int len = __ldg(a.kv_len + s);
-    if (thread == 0 && (len < 0 || len > max_len)) raise_flag(a.status, WF_DEV_BAD_INDEX);
-    if (len > 0) continue;
+    bool bad = len < 0 || len > w.max_len;
+    if (MASK == kMaskTree) {
+      const int nodes = w.tree_len != nullptr ? __ldg(w.tree_len + s) : w.n_new;
+      bad |= nodes < 0 || nodes > w.n_new || (len > 0 && len < nodes);
+    }
+    if (thread == 0 && bad) raise_flag(a.status, WF_DEV_BAD_INDEX);
+    if (seq_len_clamped<MASK>(w, a.kv_len, s) > 0) continue;
     const int rows = a.n_new * a.q_heads;
     uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) +
                                         static_cast<int64_t>(s) * rows * a.head_dim);
@@ -272,6 +327,56 @@ __device__ __forceinline__ void idle_sequences(const PagedArgs& a, int max_len, 
         a.lse[static_cast<int64_t>(s) * rows + e] = -INFINITY;
   }
 }
+
+// The drafted tree of a sequence, two nodes a lane (node, node + 32): ancestors
+// (with the node itself) as bits, depth.  A parent that does not come before its
+// child is flagged and taken for none.
+struct TreeNodes {
+  int count;       // the sequence's nodes
+  uint64_t up[2];
+  // Whole warp: ancestors of ancestors in six doublings.
+  __device__ __forceinline__ void read(const WorkShape& w, const PagedArgs& a, int s, int lane,
+                                       bool say) {
+    count = w.tree_len != nullptr ? min(max(__ldg(w.tree_len + s), 0), w.n_new) : w.n_new;
+    int next[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int node = lane + 32 * h;
+      next[h] = node < count ? __ldg(a.parents + static_cast<int64_t>(s) * w.n_new + node) : -1;
+      if (next[h] >= node) {
+        if (say) raise_flag(a.status, WF_DEV_BAD_INDEX);
+        next[h] = -1;
+      }
+      up[h] = 1ull << node;
+    }
+#pragma unroll 1
+    for (int i = 0; i < 6; ++i) {
+      uint64_t more[2];
+      int after[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        more[h] = at(up, next[h]);
+        const int n0 = __shfl_sync(0xffffffffu, next[0], next[h] & 31);
+        const int n1 = __shfl_sync(0xffffffffu, next[1], next[h] & 31);
+        after[h] = next[h] & 32 ? n1 : n0;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (next[h] < 0) continue;
+        up[h] |= more[h];
+        next[h] = after[h];
+      }
+    }
+  }
+  __device__ __forceinline__ static uint64_t at(const uint64_t* v, int node) {
+    const uint64_t v0 = __shfl_sync(0xffffffffu, v[0], node & 31);
+    const uint64_t v1 = __shfl_sync(0xffffffffu, v[1], node & 31);
+    return node & 32 ? v1 : v0;
+  }
+  // Of any node a lane asks for (0..63; others get some value).  Whole warp.
+  __device__ __forceinline__ uint64_t ancestors(int node) const { return at(up, node); }
+  __device__ __forceinline__ int depth(int node) const { return __popcll(at(up, node)) - 1; }
+};
 
 // Kernel parameters of the paged attention.
 struct PagedParams {
@@ -288,6 +393,10 @@ inline PagedParams paged_params(const PagedArgs& a, const PagedPlan& plan) {
   p.w.units_per_seq = a.kv_heads * p.row_blocks;
   p.w.tile = kPagedTile;
   p.w.max_len = a.table_pages * a.page_size;
+  p.w.n_new = a.n_new;
+  p.w.window = a.window;
+  p.w.sinks = a.sinks;
+  p.w.tree_len = a.tree_len;
   p.o = score_opts(a.scale, a.softcap, a.causal, a.prefix, a.slopes);
   return p;
 }

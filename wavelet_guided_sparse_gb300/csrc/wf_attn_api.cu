@@ -95,6 +95,47 @@ wf::PagedArgs paged_args(const wf_page_dims* d, int n_new) {
   return a;
 }
 
+// What the paged attentions check and hand over alike.
+int paged_call(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_new, const void* Q,
+               const void* K_pages, const void* V_pages, const int32_t* page_table,
+               const int32_t* kv_len, void* O, float* lse, void* workspace, size_t workspace_bytes,
+               wf::PagedArgs* out) {
+  size_t need = 0;
+  int st = wf_paged_attn_workspace_bytes(dims, n_new, &need);
+  if (st != WF_OK) return st;
+  st = check_opts(opts, dims->head_dim);
+  if (st != WF_OK) return st;
+  if (Q == nullptr || K_pages == nullptr || V_pages == nullptr || page_table == nullptr ||
+      kv_len == nullptr || O == nullptr || workspace == nullptr)
+    return WF_ERR_NULL;
+  if (!aligned16(Q) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(O) ||
+      !aligned16(workspace) || !aligned4(page_table) || !aligned4(kv_len) || !aligned4(lse))
+    return WF_ERR_ALIGNMENT;
+  if (workspace_bytes < need) return WF_ERR_WORKSPACE;
+  wf::PagedArgs a = paged_args(dims, n_new);
+  a.q = Q;
+  a.k_pages = K_pages;
+  a.v_pages = V_pages;
+  a.table = page_table;
+  a.kv_len = kv_len;
+  a.o = O;
+  a.lse = lse;
+  a.status = static_cast<int32_t*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kHeaderBytes);
+  a.scale = scale_of(opts, dims->head_dim);
+  a.softcap = opts->softcap;
+  a.causal = opts->causal != 0;
+  a.prefix = opts->prefix;
+  a.slopes = opts->slopes;
+  *out = a;
+  return WF_OK;
+}
+
+int check_window(const wf_attn_opts* opts, int32_t window, int32_t sinks) {
+  if (window < 1 || sinks < 0) return WF_ERR_SHAPE;
+  return opts != nullptr && opts->prefix != nullptr ? WF_ERR_UNSUPPORTED : WF_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -181,34 +222,51 @@ int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_
                   const void* K_pages, const void* V_pages, const int32_t* page_table,
                   const int32_t* kv_len, void* O, float* lse, void* workspace,
                   size_t workspace_bytes, void* stream) {
-  size_t need = 0;
-  int st = wf_paged_attn_workspace_bytes(dims, n_new, &need);
+  wf::PagedArgs a;
+  const int st = paged_call(dims, opts, n_new, Q, K_pages, V_pages, page_table, kv_len, O, lse,
+                            workspace, workspace_bytes, &a);
   if (st != WF_OK) return st;
-  st = check_opts(opts, dims->head_dim);
-  if (st != WF_OK) return st;
-  if (Q == nullptr || K_pages == nullptr || V_pages == nullptr || page_table == nullptr ||
-      kv_len == nullptr || O == nullptr || workspace == nullptr)
-    return WF_ERR_NULL;
-  if (!aligned16(Q) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(O) ||
-      !aligned16(workspace) || !aligned4(page_table) || !aligned4(kv_len) || !aligned4(lse))
-    return WF_ERR_ALIGNMENT;
-  if (workspace_bytes < need) return WF_ERR_WORKSPACE;
-  wf::PagedArgs a = paged_args(dims, n_new);
-  a.q = Q;
-  a.k_pages = K_pages;
-  a.v_pages = V_pages;
-  a.table = page_table;
-  a.kv_len = kv_len;
-  a.o = O;
-  a.lse = lse;
-  a.status = static_cast<int32_t*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kHeaderBytes);
-  a.scale = scale_of(opts, dims->head_dim);
-  a.softcap = opts->softcap;
-  a.causal = opts->causal != 0;
-  a.prefix = opts->prefix;
-  a.slopes = opts->slopes;
   return cuda_status(wf::launch_paged_attn(a, wf::plan_paged(a, wf::device_sm_count()),
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+int wf_paged_window_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t window,
+                         int32_t sinks, int32_t n_new, const void* Q, const void* K_pages,
+                         const void* V_pages, const int32_t* page_table, const int32_t* kv_len,
+                         void* O, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  wf::PagedArgs a;
+  int st = check_window(opts, window, sinks);
+  if (st != WF_OK) return st;
+  st = paged_call(dims, opts, n_new, Q, K_pages, V_pages, page_table, kv_len, O, lse, workspace,
+                  workspace_bytes, &a);
+  if (st != WF_OK) return st;
+  // So large a window hides nothing; positions minus it stay within 32 bits.
+  a.window = std::min(window, INT32_MAX - 512);
+  a.sinks = sinks;
+  return cuda_status(wf::launch_paged_window(a, wf::plan_paged(a, wf::device_sm_count()),
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+int wf_paged_tree_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_nodes, size_t* bytes) {
+  return wf_paged_attn_workspace_bytes(dims, n_nodes, bytes);
+}
+
+int wf_paged_tree_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_nodes,
+                       const void* Q, const void* K_pages, const void* V_pages,
+                       const int32_t* page_table, const int32_t* kv_len, const int32_t* parents,
+                       const int32_t* tree_len, void* O, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (opts != nullptr && (opts->causal == 0 || opts->prefix != nullptr)) return WF_ERR_UNSUPPORTED;
+  wf::PagedArgs a;
+  const int st = paged_call(dims, opts, n_nodes, Q, K_pages, V_pages, page_table, kv_len, O, lse,
+                            workspace, workspace_bytes, &a);
+  if (st != WF_OK) return st;
+  if (parents == nullptr) return WF_ERR_NULL;
+  if (!aligned4(parents) || !aligned4(tree_len)) return WF_ERR_ALIGNMENT;
+  a.parents = parents;
+  a.tree_len = tree_len;
+  return cuda_status(wf::launch_paged_tree(a, wf::plan_paged(a, wf::device_sm_count()),
                                            static_cast<cudaStream_t>(stream)));
 }
 

@@ -183,7 +183,8 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs& a, const RopeTurns& turns, cudaStream_t stream);
 
-// Attention over a paged cache: n_new query rows per sequence.
+// Attention over a paged cache: n_new query rows per sequence; with a window
+// (window > 0), or the nodes of a drafted tree (parents).
 struct PagedArgs {
   const void *q, *k_pages, *v_pages;
   const int32_t *table, *kv_len;
@@ -196,6 +197,8 @@ struct PagedArgs {
   int causal;
   const int32_t* prefix;
   const float* slopes;
+  int window, sinks;
+  const int32_t *parents, *tree_len;      // tree_len nullable
 };
 // CTAs of the persistent grid, rows of a row block and workspace bytes of
 // the partials: functions of the sizes and the device alone.
@@ -205,6 +208,9 @@ struct PagedPlan {
 };
 PagedPlan plan_paged(const PagedArgs& a, int sm_count);
 cudaError_t launch_paged_attn(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
+// With a window, and of a drafted tree (wf_paged_window.cu, wf_paged_tree.cu).
+cudaError_t launch_paged_window(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
+cudaError_t launch_paged_tree(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
 
 // Attention over packed sequences with contiguous keys and values.
 struct PrefillArgs {
