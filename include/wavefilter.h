@@ -31,6 +31,7 @@
  *   wf_paged_window_attn   over a sliding window of it and its first tokens
  *   wf_paged_tree_attn     by the nodes of a drafted tree
  *   wf_prefill_attn        §2.1 eq. (1) over packed prompts
+ *   wf_prefill_window_attn over a sliding window and the first tokens of each
  *   wf_paged_reserve, wf_paged_fork, wf_paged_keep, wf_paged_release
  *                          the pages themselves: taken, shared or copied,
  *                          compacted, given back
@@ -732,6 +733,19 @@ int wf_prefill_attn(const wf_prefill_dims* dims, const wf_attn_opts* opts, const
                     int64_t q_stride, const void* K, int64_t k_stride, const void* V,
                     int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, void* O,
                     float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same over a sliding window and the first tokens of each sequence: of the
+ * keys as in wf_paged_window_attn, those j of the query at position p with j <
+ * sinks or p - j < window, and besides j <= p (causal), or j < sinks or j - p <
+ * window.
+ *   window : >= 1; sinks : >= 0
+ * Tiles of keys that no query sees are not read.  opts->prefix must be NULL
+ * (WF_ERR_UNSUPPORTED).  Everything else as wf_prefill_attn. */
+int wf_prefill_window_attn(const wf_prefill_dims* dims, const wf_attn_opts* opts, int32_t window,
+                           int32_t sinks, const void* Q, int64_t q_stride, const void* K,
+                           int64_t k_stride, const void* V, int64_t v_stride, const int32_t* cu_q,
+                           const int32_t* cu_k, void* O, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 /* Size of the device scratch array behind wf_step_static_scratch (48 MiB). */
 #define WF_STATIC_SCRATCH_BYTES (48u << 20)

@@ -38,6 +38,7 @@ EXPORTS = ("wf_status_string", "wf_last_error_string", "wf_default_k_per_level",
            "wf_rope_inv_freq", "wf_paged_append", "wf_paged_attn_workspace_bytes",
            "wf_paged_attn", "wf_prefill_attn",
            "wf_paged_window_attn", "wf_paged_tree_attn_workspace_bytes", "wf_paged_tree_attn",
+           "wf_prefill_window_attn",
            "wf_pages_workspace_bytes", "wf_paged_reserve", "wf_paged_fork", "wf_paged_keep",
            "wf_paged_release")
 
@@ -145,6 +146,9 @@ _SIGS = {
     "wf_paged_tree_attn_workspace_bytes": (ctypes.c_int, [_PDIMSP, _i32, ctypes.POINTER(_sz)]),
     "wf_paged_tree_attn": (ctypes.c_int, [_PDIMSP, _OPTSP, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                                           _vp, _vp, _vp, _vp, _sz, _vp]),
+    "wf_prefill_window_attn": (ctypes.c_int, [ctypes.POINTER(PrefillDims), _OPTSP, _i32, _i32, _vp,
+                                              _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                                              _sz, _vp]),
     "wf_pages_workspace_bytes": (ctypes.c_int, [_PDIMSP, _i32, _i32, ctypes.POINTER(_sz)]),
     "wf_paged_reserve": (ctypes.c_int, [_PDIMSP, _vp, _vp, _vp, _vp, _sz, _vp]),
     "wf_paged_fork": (ctypes.c_int, [_PDIMSP, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
@@ -882,6 +886,39 @@ def prefill_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.
             _prefill_dims(t, tk, docs, hq, hkv, d, dt)[1], ctypes.byref(opts), q.data_ptr(), qs,
             k.data_ptr(), ks, v.data_ptr(), vs, cq, ck, o.data_ptr(),
             None if lse is None else lse.data_ptr(), wp, wn, _raw_stream(dev, stream)))
+        return (o, lse) if with_lse else o
+
+
+def prefill_window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                        window: int, cu_k: Optional[torch.Tensor] = None, sinks: int = 0,
+                        causal: bool = True, softcap: float = 0.0,
+                        slopes: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                        out: Optional[torch.Tensor] = None, with_lse: bool = False,
+                        ws: Optional[torch.Tensor] = None, stream=None):
+    """wf_prefill_window_attn: as prefill_attn, but of the keys less than
+    ``window`` positions away (behind a query, and before it if not ``causal``)
+    and of the first ``sinks`` ones of a sequence only."""
+    with _On(q, stream):
+        if q.dim() != 3 or k.dim() != 3:
+            raise ValueError("q, k and v must be [rows, heads, head_dim]")
+        dev, dt = q.device, q.dtype
+        t, hq, d = q.shape
+        tk, hkv = k.shape[0], k.shape[1]
+        qs = _row_stride(q, "q", t, hq, d, dt, dev)
+        ks = _row_stride(k, "k", tk, hkv, d, dt, dev)
+        vs = _row_stride(v, "v", tk, hkv, d, dt, dev)
+        docs = cu_q.numel() - 1
+        cq = _need(cu_q, "cu_q", (docs + 1,), torch.int32, dev)
+        ck = cq if cu_k is None else _need(cu_k, "cu_k", (docs + 1,), torch.int32, dev)
+        opts = _attn_opts(causal, None, softcap, slopes, scale, docs, hq, dev)
+        o = _out(out, "out", (t, hq, d), dt, dev)
+        lse = torch.empty((t, hq), dtype=torch.float32, device=dev) if with_lse else None
+        wp, wn = _ws_args(ws, dev)
+        _check("wf_prefill_window_attn", lib().wf_prefill_window_attn(
+            _prefill_dims(t, tk, docs, hq, hkv, d, dt)[1], ctypes.byref(opts),
+            _reach(window, "window", 1), _reach(sinks, "sinks", 0), q.data_ptr(), qs, k.data_ptr(),
+            ks, v.data_ptr(), vs, cq, ck, o.data_ptr(), None if lse is None else lse.data_ptr(),
+            wp, wn, _raw_stream(dev, stream)))
         return (o, lse) if with_lse else o
 
 

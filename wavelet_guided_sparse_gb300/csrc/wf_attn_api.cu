@@ -136,6 +136,61 @@ int check_window(const wf_attn_opts* opts, int32_t window, int32_t sinks) {
   return opts != nullptr && opts->prefix != nullptr ? WF_ERR_UNSUPPORTED : WF_OK;
 }
 
+// What the packed-prompt attentions check and hand over alike; *out has no rows
+// where there is nothing to do.
+int prefill_call(const wf_prefill_dims* dims, const wf_attn_opts* opts, const void* Q,
+                 int64_t q_stride, const void* K, int64_t k_stride, const void* V, int64_t v_stride,
+                 const int32_t* cu_q, const int32_t* cu_k, void* O, float* lse, void* workspace,
+                 size_t workspace_bytes, wf::PrefillArgs* out) {
+  if (dims == nullptr) return WF_ERR_NULL;
+  int st = check_heads(dims->q_heads, dims->kv_heads, dims->head_dim, dims->dtype);
+  if (st != WF_OK) return st;
+  if (dims->rows_q < 0 || dims->rows_k < 0 || dims->n_docs < 1) return WF_ERR_SHAPE;
+  // Row blocks are counted in 32 bits; rows stay below a grid's limits.
+  if (dims->rows_q > (1 << 26) || dims->rows_k > (1 << 30) || dims->n_docs > (1 << 20))
+    return WF_ERR_UNSUPPORTED;
+  st = check_opts(opts, dims->head_dim);
+  if (st != WF_OK) return st;
+  *out = wf::PrefillArgs{};
+  if (dims->rows_q == 0) return WF_OK;
+  if (Q == nullptr || cu_q == nullptr || cu_k == nullptr || O == nullptr ||
+      (dims->rows_k > 0 && (K == nullptr || V == nullptr)))
+    return WF_ERR_NULL;
+  if (bad_stride(q_stride, dims->q_heads, dims->head_dim, dims->dtype) ||
+      bad_stride(k_stride, dims->kv_heads, dims->head_dim, dims->dtype) ||
+      bad_stride(v_stride, dims->kv_heads, dims->head_dim, dims->dtype))
+    return WF_ERR_SHAPE;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned16(workspace) ||
+      !aligned4(cu_q) || !aligned4(cu_k) || !aligned4(lse))
+    return WF_ERR_ALIGNMENT;
+  if (workspace != nullptr && workspace_bytes < kHeaderBytes) return WF_ERR_WORKSPACE;
+  wf::PrefillArgs& a = *out;
+  a.q = Q;
+  a.k = K;
+  a.v = V;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.o = O;
+  a.lse = lse;
+  a.status = static_cast<int32_t*>(workspace);
+  a.rows_q = dims->rows_q;
+  a.rows_k = dims->rows_k;
+  a.n_docs = dims->n_docs;
+  a.q_heads = dims->q_heads;
+  a.kv_heads = dims->kv_heads;
+  a.head_dim = dims->head_dim;
+  a.dtype = dims->dtype;
+  a.scale = scale_of(opts, dims->head_dim);
+  a.softcap = opts->softcap;
+  a.causal = opts->causal != 0;
+  a.prefix = opts->prefix;
+  a.slopes = opts->slopes;
+  return WF_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -274,51 +329,27 @@ int wf_prefill_attn(const wf_prefill_dims* dims, const wf_attn_opts* opts, const
                     int64_t q_stride, const void* K, int64_t k_stride, const void* V,
                     int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, void* O,
                     float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-  if (dims == nullptr) return WF_ERR_NULL;
-  int st = check_heads(dims->q_heads, dims->kv_heads, dims->head_dim, dims->dtype);
+  wf::PrefillArgs a;
+  const int st = prefill_call(dims, opts, Q, q_stride, K, k_stride, V, v_stride, cu_q, cu_k, O, lse,
+                              workspace, workspace_bytes, &a);
+  if (st != WF_OK || a.rows_q == 0) return st;
+  return cuda_status(wf::launch_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
+int wf_prefill_window_attn(const wf_prefill_dims* dims, const wf_attn_opts* opts, int32_t window,
+                           int32_t sinks, const void* Q, int64_t q_stride, const void* K,
+                           int64_t k_stride, const void* V, int64_t v_stride, const int32_t* cu_q,
+                           const int32_t* cu_k, void* O, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  int st = check_window(opts, window, sinks);
   if (st != WF_OK) return st;
-  if (dims->rows_q < 0 || dims->rows_k < 0 || dims->n_docs < 1) return WF_ERR_SHAPE;
-  // Row blocks are counted in 32 bits; rows stay below a grid's limits.
-  if (dims->rows_q > (1 << 26) || dims->rows_k > (1 << 30) || dims->n_docs > (1 << 20))
-    return WF_ERR_UNSUPPORTED;
-  st = check_opts(opts, dims->head_dim);
-  if (st != WF_OK) return st;
-  if (dims->rows_q == 0) return WF_OK;
-  if (Q == nullptr || cu_q == nullptr || cu_k == nullptr || O == nullptr ||
-      (dims->rows_k > 0 && (K == nullptr || V == nullptr)))
-    return WF_ERR_NULL;
-  if (bad_stride(q_stride, dims->q_heads, dims->head_dim, dims->dtype) ||
-      bad_stride(k_stride, dims->kv_heads, dims->head_dim, dims->dtype) ||
-      bad_stride(v_stride, dims->kv_heads, dims->head_dim, dims->dtype))
-    return WF_ERR_SHAPE;
-  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned16(workspace) ||
-      !aligned4(cu_q) || !aligned4(cu_k) || !aligned4(lse))
-    return WF_ERR_ALIGNMENT;
-  if (workspace != nullptr && workspace_bytes < kHeaderBytes) return WF_ERR_WORKSPACE;
-  wf::PrefillArgs a = {};
-  a.q = Q;
-  a.k = K;
-  a.v = V;
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.cu_q = cu_q;
-  a.cu_k = cu_k;
-  a.o = O;
-  a.lse = lse;
-  a.status = static_cast<int32_t*>(workspace);
-  a.rows_q = dims->rows_q;
-  a.rows_k = dims->rows_k;
-  a.n_docs = dims->n_docs;
-  a.q_heads = dims->q_heads;
-  a.kv_heads = dims->kv_heads;
-  a.head_dim = dims->head_dim;
-  a.dtype = dims->dtype;
-  a.scale = scale_of(opts, dims->head_dim);
-  a.softcap = opts->softcap;
-  a.causal = opts->causal != 0;
-  a.prefix = opts->prefix;
-  a.slopes = opts->slopes;
+  wf::PrefillArgs a;
+  st = prefill_call(dims, opts, Q, q_stride, K, k_stride, V, v_stride, cu_q, cu_k, O, lse,
+                    workspace, workspace_bytes, &a);
+  if (st != WF_OK || a.rows_q == 0) return st;
+  // So large a window hides nothing (positions lie in [-2^26, 2^30)).
+  a.window = std::min(window, (1 << 30) + (1 << 26) + 1);
+  a.sinks = sinks;
   return cuda_status(wf::launch_prefill(a, static_cast<cudaStream_t>(stream)));
 }
 

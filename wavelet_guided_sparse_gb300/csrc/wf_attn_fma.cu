@@ -50,13 +50,14 @@ struct FmaState {
 struct RowBlock {
   int row0, rows;  // first row and row count within the unit
   int g, n_q, len, prefix, head0;
+  int window, sinks;  // window 0: none
   __device__ __forceinline__ int pos(int r) const { return len - n_q + (row0 + r) / g; }
   __device__ __forceinline__ int head(int r) const { return head0 + (row0 + r) % g; }
 };
 
 // One 64-key tile (keys key0 .. key0 + 63, staged in shared memory, rows past
 // `len` zero) into the running state.
-template <int D, int RT>
+template <int D, int RT, bool WINDOW>
 __device__ __forceinline__ void fma_tile(FmaSmem<D, RT>& s, const RowBlock& b,
                                          const ScoreOpts& o, int key0, FmaState<D, RT>& st) {
   constexpr int RPT = RT / 16;
@@ -95,7 +96,10 @@ __device__ __forceinline__ void fma_tile(FmaSmem<D, RT>& s, const RowBlock& b,
       float x = z[r][j] * o.scale;
       if (o.cap > 0.f) x = o.cap * tanhf(x);
       x -= slope * kLog2e * fabsf(static_cast<float>(pos - key));
-      const bool seen = key < b.len && (!o.causal || key <= pos || key < b.prefix);
+      bool seen = key < b.len && (!o.causal || key <= pos || key < b.prefix);
+      if (WINDOW)
+        seen = seen && (key < b.sinks ||
+                        (pos - key < b.window && (o.causal || key - pos < b.window)));
       z[r][j] = seen ? x : -INFINITY;
       mx = fmaxf(mx, z[r][j]);
     }
@@ -201,7 +205,7 @@ struct PrefillParams {
   int capped;  // 1: the grid has fewer blocks than row blocks there might be
 };
 
-template <typename T, int D, int RT>
+template <typename T, int D, int RT, bool WINDOW>
 __global__ void __launch_bounds__(kThreads) prefill_fma_kernel(PrefillParams p) {
   extern __shared__ float4 smem4[];
   FmaSmem<D, RT>& s = *reinterpret_cast<FmaSmem<D, RT>*>(smem4);
@@ -229,10 +233,25 @@ __global__ void __launch_bounds__(kThreads) prefill_fma_kernel(PrefillParams p) 
     fma_load_q<T, D, RT>(s, b, static_cast<const T*>(a.q) + d.q0 * a.q_stride, a.q_stride);
     FmaState<D, RT> st;
     st.reset();
-    const int end = visible_end(b.len, b.pos(b.rows - 1), p.o.causal, b.prefix);
+    int end = visible_end(b.len, b.pos(b.rows - 1), p.o.causal, b.prefix);
+    // Window: the tiles between the first tokens and the first row's window are
+    // passed over, and those behind the last one's.
+    int sinks_end = 0, low = 0;
+    b.window = a.window;
+    b.sinks = a.sinks;
+    if (WINDOW) {
+      const int last = b.pos(b.rows - 1);
+      sinks_end = min(a.sinks, b.len);
+      low = max(0, b.pos(0) - a.window + 1) / KT * KT;
+      if (!p.o.causal && a.window < b.len - last) end = max(last + a.window, sinks_end);
+    }
     const T* kb = static_cast<const T*>(a.k) + d.k0 * a.k_stride + kvh * D;
     const T* vb = static_cast<const T*>(a.v) + d.k0 * a.v_stride + kvh * D;
     for (int key0 = 0; key0 < end; key0 += KT) {
+      if (WINDOW && key0 >= sinks_end && key0 < low) {
+        key0 = low - KT;
+        continue;
+      }
       __syncthreads();
       constexpr int C = D / Elem<T>::kPer16B;
       for (int e = threadIdx.x; e < KT * C; e += kThreads) {
@@ -242,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) prefill_fma_kernel(PrefillParams p) 
                             in ? vb + key * a.v_stride : nullptr);
       }
       __syncthreads();
-      fma_tile<D, RT>(s, b, p.o, key0, st);
+      fma_tile<D, RT, WINDOW>(s, b, p.o, key0, st);
     }
     const int64_t base = d.q0 * a.q_heads;
     fma_store<T, D, RT>(st, b, static_cast<T*>(a.o) + base * D,
@@ -250,17 +269,17 @@ __global__ void __launch_bounds__(kThreads) prefill_fma_kernel(PrefillParams p) 
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool WINDOW>
 cudaError_t launch_prefill_typed(PrefillParams& p, cudaStream_t stream) {
   constexpr int RT = 64;
-  const cudaError_t e = ensure_max_smem<prefill_fma_kernel<T, D, RT>>();
+  const cudaError_t e = ensure_max_smem<prefill_fma_kernel<T, D, RT, WINDOW>>();
   if (e != cudaSuccess) return e;
   const int64_t blocks = doc_blocks(p.a.rows_q, p.a.n_docs, RT, p.a.q_heads / p.a.kv_heads);
   // At most about 32 CTAs an SM (one runs at a time), each with every so many
   // row blocks.
   const int64_t most = std::max(1, 32 * device_sm_count() / p.a.kv_heads);
   p.capped = most < blocks;
-  prefill_fma_kernel<T, D, RT>
+  prefill_fma_kernel<T, D, RT, WINDOW>
       <<<dim3(static_cast<unsigned>(std::min(blocks, most)), p.a.kv_heads), kThreads, sizeof(FmaSmem<D, RT>),
          stream>>>(p);
   return cudaGetLastError();
@@ -272,8 +291,11 @@ cudaError_t launch_prefill_fma(const PrefillArgs& a, cudaStream_t stream) {
   PrefillParams p;
   p.a = a;
   p.o = score_opts(a.scale, a.softcap, a.causal, a.prefix, a.slopes);
-  return a.head_dim == 128 ? launch_prefill_typed<float, 128>(p, stream)
-                           : launch_prefill_typed<float, 64>(p, stream);
+  if (a.window > 0)
+    return a.head_dim == 128 ? launch_prefill_typed<float, 128, true>(p, stream)
+                             : launch_prefill_typed<float, 64, true>(p, stream);
+  return a.head_dim == 128 ? launch_prefill_typed<float, 128, false>(p, stream)
+                           : launch_prefill_typed<float, 64, false>(p, stream);
 }
 
 }  // namespace wf

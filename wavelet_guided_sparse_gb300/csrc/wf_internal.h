@@ -225,6 +225,7 @@ struct PrefillArgs {
   int causal;
   const int32_t* prefix;
   const float* slopes;
+  int window, sinks;                      // window 0: none
 };
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_fma(const PrefillArgs& a, cudaStream_t stream);

@@ -18,10 +18,12 @@
 // d = 128); keys and values pass through one ring of 128-row stages (tensor
 // copies, 128-byte swizzle).
 //
-// Visible keys of a row are always a prefix [0, limit) of its sequence
-// (limit = max(position + 1, prefix) under the causal mask), so a mask is a
-// word of bits per 32 keys, only on tiles that cross some limit, and tiles
-// behind every limit are never loaded.  The running maximum is set 8 (in log2)
+// Visible keys of a row are a prefix [0, limit) of its sequence (limit =
+// max(position + 1, prefix) under the causal mask), with a window a range [low,
+// limit) and the first tokens, so a mask is a word of bits per 32 keys, only on
+// tiles that cross some border, and tiles that no row sees are never loaded:
+// the key tiles of an item form a line, with a gap between the first tokens and
+// the window, walked from its last to its first.  The running maximum is set 8 (in log2)
 // above the score that raises it and raised again, O rescaled in tensor memory,
 // only by a score beyond that: after the first tiles O is hardly ever touched,
 // and the weights stay below 1, so that a value of the type's largest does not
@@ -90,13 +92,17 @@ struct PrefillTcParams {
 struct QueryTile {
   int head, row0, rows;  // head, first row within the sequence, rows (0: none)
   int end;               // keys some row sees
-  int tiles;             // key tiles
+  int tiles;             // key tiles (window: those of the line, see Item)
 };
 // One unit of work: two query tiles over their sequence's keys.
 struct Item {
   QueryTile qt[2];
   int q0, k0, n_k, shift, prefix;  // first row and key, keys, position of row 0
   int kvh, live;                   // key-value head; 0: no more items
+  // Window: the key tiles of the first tokens, and those behind them that no row
+  // sees.  The others form a line, whose tile j is key tile place(j).
+  int first, gap;
+  __device__ __forceinline__ int place(int j) const { return j < first ? j : j + gap; }
 };
 
 struct PreBarriers {
@@ -353,10 +359,20 @@ __device__ __forceinline__ void map_scores(float* s, const ScoreOpts& o, const S
     map_chunk<CAP, BIAS, false>(s, o, c, d0, 0.f);
 }
 
-// A chunk's keys from `n` on are hidden: their scores become `with`.  One bit a
-// key: bits of a register become predicates eight at once.
-__device__ __forceinline__ void hide_keys(float* s, int n, float with = -INFINITY) {
-  const uint32_t seen = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+// The lowest n bits (none, or all 32, for n outside).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+// The keys of a chunk that a row sees, one bit a key: those below `end`; window:
+// from `low` on, or below `sinks` (all relative to the chunk's first key).
+template <bool WINDOW>
+__device__ __forceinline__ uint32_t seen_keys(int end, int low, int sinks) {
+  const uint32_t seen = low_bits(end);
+  return WINDOW ? (seen & ~low_bits(low)) | low_bits(sinks) : seen;
+}
+// The keys of a chunk that are not seen are hidden: their scores become `with`.
+// Bits of a register become predicates eight at once.
+__device__ __forceinline__ void hide_keys(float* s, uint32_t seen, float with = -INFINITY) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) s[i] = (seen & (1u << i)) != 0 ? s[i] : with;
 }
@@ -458,6 +474,7 @@ __device__ __forceinline__ int64_t claimed_block(const uint4* from) {
 // An item by its index: heads run fastest, a sequence's row blocks from its
 // last (the longest under the causal mask) to its first.  False: behind the
 // last sequence.  Whole warp.
+template <bool WINDOW>
 __device__ __forceinline__ bool make_item(const PrefillTcParams& p, int64_t index,
                                           DocCursor& cursor, Item* out) {
   const PrefillArgs& a = p.a;
@@ -478,22 +495,30 @@ __device__ __forceinline__ bool make_item(const PrefillTcParams& p, int64_t inde
   it.n_k = doc.n_k;
   it.prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + doc.doc) : 0;
   it.shift = doc.n_k - doc.n_q;
+  if (WINDOW) {
+    // Both query tiles share the line: from the first row's window on.
+    const int low = max(0, it.shift + doc.block * block_rows - a.window + 1);
+    it.first = (min(a.sinks, doc.n_k) + kTileRows - 1) / kTileRows;
+    it.gap = max(0, low / kTileRows - it.first);
+  }
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     QueryTile& q = it.qt[t];
     q.head = p.pair_heads ? 2 * hx + t : hx;
     q.row0 = doc.block * block_rows + (p.pair_heads ? 0 : t * kTileRows);
     q.rows = max(0, min(kTileRows, doc.n_q - q.row0));
-    q.end = q.rows == 0 ? 0
-                        : max(0, visible_end(doc.n_k, it.shift + q.row0 + q.rows - 1, p.o.causal,
-                                             it.prefix));
+    const int last = it.shift + q.row0 + q.rows - 1;
+    q.end = q.rows == 0 ? 0 : max(0, visible_end(doc.n_k, last, p.o.causal, it.prefix));
+    if (WINDOW && q.rows > 0 && !p.o.causal && a.window < doc.n_k - last)
+      q.end = max(0, max(last + a.window, min(a.sinks, doc.n_k)));
     q.tiles = (q.end + kTileRows - 1) / kTileRows;
+    if (WINDOW) q.tiles = max(0, q.tiles - it.gap);
   }
   it.kvh = it.qt[0].head / (a.q_heads / a.kv_heads);
   return true;
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool WINDOW>
 __global__ void __launch_bounds__(kPreThreads, 1)
     prefill_tc_kernel(const __grid_constant__ PrefillTcParams p) {
   using Shape = PreShape<D>;
@@ -567,7 +592,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         // of the rows) are claimed and dropped.  Item 0 is looked at even if there
         // is none, for the offsets' sake.
         while (next >= stop || (next >= items && next > 0) ||
-               !make_item(p, next++, cursor, &it)) {
+               !make_item<WINDOW>(p, next++, cursor, &it)) {
           if (leader) {
             fence_proxy_async();
             mbar_arrive_expect_tx(&bars.claim, 16);
@@ -629,9 +654,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (leader && !(inject && fills == 0)) {
             unsigned char* dst = ring + st * kTileBytes;
             mbar_arrive_expect_tx(&bars.full[st], kTileBytes);
+            const int j = tiles - 1 - (f >> 1);
             for (int kb = 0; kb < D / 64; ++kb)
               tma_load_3d(dst + kb * (kTileRows * 128), (f & 1) ? &p.tv : &p.tk, kb * 64, it.kvh,
-                          it.k0 + (tiles - 1 - (f >> 1)) * kTileRows, &bars.full[st]);
+                          it.k0 + (WINDOW ? it.place(j) : j) * kTileRows, &bars.full[st]);
           }
           ++fills;
           if (++st == kStages) st = 0;
@@ -708,6 +734,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const int live = it.live;
         const int end[2] = {it.qt[0].end, it.qt[1].end};
         const int nt[2] = {it.qt[0].tiles, it.qt[1].tiles};
+        const int first = it.first, gap = it.gap;
+        // Keys of query tile t from the first of tile j on.
+        const auto keys_from = [&](int t, int j) {
+          if (!WINDOW) return end[t] - j * kTileRows;
+          if (gap > 0 && j < first) return a.sinks - j * kTileRows;
+          return end[t] - (j < first ? j : j + gap) * kTileRows;
+        };
         __syncwarp();
         if (leader) mbar_arrive(&bars.item_empty[k & 1]);
         if (!live) break;
@@ -718,7 +751,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const auto scores = [&](int t, int j, int st) {
           if (j == nt[t] - 1) ok = pre_wait(bars, &bars.q[t], used[t] & 1, a.status);
           if (!ok) return;
-          issue_qk(t, end[t] - j * kTileRows, st);
+          issue_qk(t, keys_from(t, j), st);
           if (j == 0 && leader) umma_commit(&bars.q_empty[t]);
         };
         ok = pre_wait(bars, &bars.full[st], parity, a.status);
@@ -746,7 +779,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               if (!ok) continue;
               ++np[t];
               tc_fence_after();
-              issue_pv(t, min(kTileRows, end[t] - j * kTileRows + 15) / 16, vs, j == nt[t] - 1);
+              issue_pv(t, min(kTileRows, keys_from(t, j) + 15) / 16, vs, j == nt[t] - 1);
               if (j == 0 && leader) umma_commit(&bars.o[t]);
             }
             if (ok && j > 0 && j - 1 < nt[t]) scores(t, j - 1, ks);
@@ -790,7 +823,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const bool live = row < rows && sound;
       const int64_t at = out_row * a.q_heads + head;
       const int pos = it.shift + row_at, live_item = it.live;
-      const int limit = live ? (p.o.causal ? min(n_k, max(pos + 1, it.prefix)) : n_k) : end;
+      int limit = live ? (p.o.causal ? min(n_k, max(pos + 1, it.prefix)) : n_k) : end;
+      // Window: the first key of it, and how many of the first tokens count.
+      int low = 0, sinks = 0, first = 0, gap = 0;
+      if (WINDOW && live) {
+        low = pos - a.window + 1;
+        sinks = min(a.sinks, limit);
+        if (!p.o.causal && a.window < n_k - pos) limit = pos + a.window;
+      }
+      if (WINDOW) {
+        first = it.first;
+        gap = it.gap;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.item_empty[k & 1]);
       if (!live_item) break;
@@ -818,13 +862,16 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (!ok) break;
         ++ns;
         tc_fence_after();
-        const int k0 = j * kTileRows;
+        const int k0 = (WINDOW && j >= first ? j + gap : j) * kTileRows;
         // Chunks of scores in rolled loops: with the tile unrolled the code of the
         // softmax groups would not stay in the instruction caches, and every
         // role, the products' warp first, would wait for its fetches.  A chunk's
         // weights go over columns already read.
-        const int rel = limit - k0;
-        const bool edge = __any_sync(0xffffffffu, rel < 128);
+        const int rel = limit - k0, rel_low = low - k0, rel_sinks = sinks - k0;
+        const bool edge = __any_sync(0xffffffffu, rel < 128 || (WINDOW && rel_low > 0));
+        const auto seen = [&](int c) {
+          return seen_keys<WINDOW>(rel - c, rel_low - c, rel_sinks - c);
+        };
         uint64_t sum0 = 0, sum1 = 0;
         if constexpr (CAP || BIAS) {
           // One pass.  The weights of a chunk are formed before the test on its
@@ -840,7 +887,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             for (int c = 0; c < 128; c += 32) {
               uint32_t r[32];
               tmem_ld32(s_addr + c, r);
-              hide_keys(reinterpret_cast<float*>(r), rel - c, 0.f);
+              hide_keys(reinterpret_cast<float*>(r), seen(c), 0.f);
               tmem_st32(s_addr + c, r);
             }
             tmem_wait_st();
@@ -855,7 +902,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                              : __all_sync(0xffffffffu, d0 >= 31.f) ? 1
                              : __all_sync(0xffffffffu, d0 <= 0.f)  ? -1 : 0;
             map_scores<CAP, BIAS>(s, p.o, map, d0, side);
-            if (edge) hide_keys(s, rel - c);
+            if (edge) hide_keys(s, seen(c));
             const float mc = chunk_max<32>(s);
             uint64_t add0, add1;
             while (true) {
@@ -900,8 +947,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             tmem_ld64(s_addr + c, r);
             float* s = reinterpret_cast<float*>(r);
             if (edge) {
-              hide_keys(s, rel - c);
-              hide_keys(s + 32, rel - c - 32);
+              hide_keys(s, seen(c));
+              hide_keys(s + 32, seen(c + 32));
               tmem_st32(s_addr + c, r);
               tmem_st32(s_addr + c + 32, r + 32);
             }
@@ -929,7 +976,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         l += a0 + a1;
         // Value rows behind the last key of the sequence, up to the product's end.
         if (n_k - k0 < kTileRows) {
-          const int r0 = n_k - k0, r1 = min(kTileRows, (end - k0 + 15) & ~15);
+          const int keys = WINDOW && gap > 0 && j < first ? a.sinks - k0 : end - k0;
+          const int r0 = n_k - k0, r1 = min(kTileRows, (keys + 15) & ~15);
           if (r0 < r1) {
             const uint32_t f = fill + 2 * (tiles - 1 - j) + 1;
             ok = pre_wait(bars, &bars.full[f % kStages], (f / kStages) & 1, a.status);
@@ -1030,26 +1078,28 @@ bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int heads, in
 // batch padded to 4096 sequences took 11 ms for the claims of empty ones, and
 // 63 us capped.)
 constexpr int kBlocksPerSm = 32;
-template <int D, bool CAP, bool BIAS>
+template <int D, bool CAP, bool BIAS, bool WINDOW>
 cudaError_t launch_tc(PrefillTcParams& p, cudaStream_t stream) {
-  const cudaError_t e = ensure_max_smem<prefill_tc_kernel<D, CAP, BIAS>>();
+  const cudaError_t e = ensure_max_smem<prefill_tc_kernel<D, CAP, BIAS, WINDOW>>();
   if (e != cudaSuccess) return e;
   const int block_rows = p.pair_heads ? kTileRows : 2 * kTileRows;
   const int64_t items = doc_blocks(p.a.rows_q, p.a.n_docs, block_rows, 1) *
                         (p.pair_heads ? p.a.q_heads / 2 : p.a.q_heads);
   const int64_t blocks = std::min<int64_t>(items, kBlocksPerSm * device_sm_count());
   p.capped = blocks < items;
-  prefill_tc_kernel<D, CAP, BIAS>
+  prefill_tc_kernel<D, CAP, BIAS, WINDOW>
       <<<static_cast<unsigned>(blocks), kPreThreads, PreShape<D>::kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool WINDOW>
 cudaError_t launch_tc_opts(PrefillTcParams& p, cudaStream_t stream) {
   const bool bias = p.o.slopes != nullptr;
   if (p.o.cap > 0.f)
-    return bias ? launch_tc<D, true, true>(p, stream) : launch_tc<D, true, false>(p, stream);
-  return bias ? launch_tc<D, false, true>(p, stream) : launch_tc<D, false, false>(p, stream);
+    return bias ? launch_tc<D, true, true, WINDOW>(p, stream)
+                : launch_tc<D, true, false, WINDOW>(p, stream);
+  return bias ? launch_tc<D, false, true, WINDOW>(p, stream)
+              : launch_tc<D, false, false, WINDOW>(p, stream);
 }
 
 }  // namespace
@@ -1069,7 +1119,11 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
       !encode_rows(&p.tv, keys ? a.v : a.q, keys ? a.rows_k : 1, a.kv_heads, a.head_dim,
                    a.v_stride))
     return cudaErrorInvalidValue;
-  return a.head_dim == 128 ? launch_tc_opts<128>(p, stream) : launch_tc_opts<64>(p, stream);
+  if (a.window > 0)
+    return a.head_dim == 128 ? launch_tc_opts<128, true>(p, stream)
+                             : launch_tc_opts<64, true>(p, stream);
+  return a.head_dim == 128 ? launch_tc_opts<128, false>(p, stream)
+                           : launch_tc_opts<64, false>(p, stream);
 }
 
 }  // namespace wf
