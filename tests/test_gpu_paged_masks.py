@@ -367,3 +367,59 @@ def test_append_verify_keep():
             a, b = (c[x][t[s, :-(-m // page)].long()].transpose(1, 2).flatten(0, 1)[:m]
                     for c, t in ((c0, t0), (c1, t1)))
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("nodes,hq,hkv", [(1, 4, 2), (20, 8, 2), (64, 16, 2)])
+def test_waits_that_run_out(nodes, hq, hkv):
+    cache, table = paged([900, 300], 16, hkv, 128, BF, 13)
+    t, q = i32(table.tolist()), randn((2, nodes, hq, 128), BF, 2)
+    ws = bd.alloc_paged_tree_workspace(q, cache, t)
+    tree = i32([random_tree(nodes, np.random.default_rng(nodes))] * 2)
+    call = lambda: bd.paged_tree_attn(q, cache, t, i32([900, 300]), tree, ws)
+    ref = call()
+    bd.inject_wait_timeout(300)
+    call()
+    assert bd.read_device_status(ws) == bd.DEV_WAIT_TIMEOUT
+    bd.clear_device_status(ws)
+    assert torch.equal(call(), ref) and bd.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("nodes,hq,hkv", [(30, 8, 2), (64, 16, 2)])
+def test_tree_over_missing_pages(nodes, hq, hkv):
+    """Rows of pages outside the pool do not count, and nothing they left behind does."""
+    n, page = 1000, 16
+    cache, table = paged([n], page, hkv, 64, BF, 17)
+    gone = [3, 20, 21, 22, 23, 40]
+    keep = np.ones(n, bool)
+    for e in gone:
+        table[0, e] = 10 ** 6 if e % 2 else -5
+        keep[e * page:(e + 1) * page] = False
+    tree = random_tree(nodes, np.random.default_rng(3))
+    q, t = randn((1, nodes, hq, 64), BF, 4), i32(table.tolist())
+    ws = bd.alloc_paged_tree_workspace(q, cache, t)
+    for _ in range(2):                                # stale stages of the first hold values
+        o, lse = bd.paged_tree_attn(q, cache, t, i32([n]), i32([tree]), ws, with_lse=True)
+        assert bd.read_device_status(ws) == bd.DEV_BAD_INDEX
+        k, v = rows_of(cache, np.where((table < 0) | (table > 10 ** 5), 0, table), 0, n)
+        seen, _ = tree_mask(n - nodes, tree)
+        ro, rl, ob, lb = attend_masked(f64(q[0]), k, v, BF, seen & keep[None])
+        check(f64(lse[0]), rl, lb, "lse")
+        check(f64(o[0]), ro, ob, "O")
+
+
+def test_long_cache_past_32_bit_offsets():
+    """A pool of more than 2^31 elements: the tree's pages lie at its far end."""
+    page, hkv, d = 256, 8, 128
+    pages = (1 << 31) // (page * hkv * d) + 40
+    cache = {x: torch.empty((pages, hkv, page, d), dtype=BF, device="cuda") for x in "KV"}
+    for i, x in enumerate("KV"):
+        cache[x][-12:] = randn((12, hkv, page, d), BF, i)
+    table = np.arange(pages - 1, pages - 12, -1)[None]
+    n, tree = 2700, random_tree(40, np.random.default_rng(5))
+    q = randn((1, 40, 32, d), BF, 6, 2.0)
+    o, lse = bd.paged_tree_attn(q, cache, i32(table.tolist()), i32([n]), i32([tree]), with_lse=True)
+    k, v = (np.concatenate([f64(cache[x][int(p)]) for p in table[0]], 1)[:, :n].transpose(1, 0, 2)
+            for x in "KV")
+    ro, rl, ob, lb = attend_masked(f64(q[0]), k, v, BF, tree_mask(n - 40, tree)[0])
+    check(f64(lse[0]), rl, lb, "lse")
+    check(f64(o[0]), ro, ob, "O")

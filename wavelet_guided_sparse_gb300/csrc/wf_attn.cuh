@@ -391,7 +391,7 @@ inline PagedParams paged_params(const PagedArgs& a, const PagedPlan& plan) {
   p.row_blocks = (a.q_heads / a.kv_heads * a.n_new + plan.row_block - 1) / plan.row_block;
   p.w.n_seqs = a.n_seqs;
   p.w.units_per_seq = a.kv_heads * p.row_blocks;
-  p.w.tile = kPagedTile;
+  p.w.tile = plan.tile;
   p.w.max_len = a.table_pages * a.page_size;
   p.w.n_new = a.n_new;
   p.w.window = a.window;

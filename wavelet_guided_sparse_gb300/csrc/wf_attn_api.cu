@@ -95,13 +95,25 @@ wf::PagedArgs paged_args(const wf_page_dims* d, int n_new) {
   return a;
 }
 
+using PlanFn = wf::PagedPlan (*)(const wf::PagedArgs&, int);
+
+int paged_bytes(const wf_page_dims* dims, int32_t n_new, PlanFn plan, size_t* bytes) {
+  const int st = check_page_dims(dims);
+  if (st != WF_OK) return st;
+  if (bytes == nullptr) return WF_ERR_NULL;
+  if (n_new < 1) return WF_ERR_SHAPE;
+  if (n_new > WF_MAX_GEN) return WF_ERR_UNSUPPORTED;
+  *bytes = kHeaderBytes + plan(paged_args(dims, n_new), wf::device_sm_count()).part_bytes;
+  return WF_OK;
+}
+
 // What the paged attentions check and hand over alike.
-int paged_call(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_new, const void* Q,
-               const void* K_pages, const void* V_pages, const int32_t* page_table,
+int paged_call(PlanFn plan, const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_new,
+               const void* Q, const void* K_pages, const void* V_pages, const int32_t* page_table,
                const int32_t* kv_len, void* O, float* lse, void* workspace, size_t workspace_bytes,
                wf::PagedArgs* out) {
   size_t need = 0;
-  int st = wf_paged_attn_workspace_bytes(dims, n_new, &need);
+  int st = paged_bytes(dims, n_new, plan, &need);
   if (st != WF_OK) return st;
   st = check_opts(opts, dims->head_dim);
   if (st != WF_OK) return st;
@@ -264,13 +276,7 @@ int wf_paged_append(const wf_page_dims* dims, int32_t n_rows, const void* Q, int
 }
 
 int wf_paged_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_new, size_t* bytes) {
-  const int st = check_page_dims(dims);
-  if (st != WF_OK) return st;
-  if (bytes == nullptr) return WF_ERR_NULL;
-  if (n_new < 1) return WF_ERR_SHAPE;
-  if (n_new > WF_MAX_GEN) return WF_ERR_UNSUPPORTED;
-  *bytes = kHeaderBytes + wf::plan_paged(paged_args(dims, n_new), wf::device_sm_count()).part_bytes;
-  return WF_OK;
+  return paged_bytes(dims, n_new, wf::plan_paged, bytes);
 }
 
 int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_new, const void* Q,
@@ -278,7 +284,7 @@ int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_
                   const int32_t* kv_len, void* O, float* lse, void* workspace,
                   size_t workspace_bytes, void* stream) {
   wf::PagedArgs a;
-  const int st = paged_call(dims, opts, n_new, Q, K_pages, V_pages, page_table, kv_len, O, lse,
+  const int st = paged_call(wf::plan_paged, dims, opts, n_new, Q, K_pages, V_pages, page_table, kv_len, O, lse,
                             workspace, workspace_bytes, &a);
   if (st != WF_OK) return st;
   return cuda_status(wf::launch_paged_attn(a, wf::plan_paged(a, wf::device_sm_count()),
@@ -293,7 +299,7 @@ int wf_paged_window_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int
   wf::PagedArgs a;
   int st = check_window(opts, window, sinks);
   if (st != WF_OK) return st;
-  st = paged_call(dims, opts, n_new, Q, K_pages, V_pages, page_table, kv_len, O, lse, workspace,
+  st = paged_call(wf::plan_paged, dims, opts, n_new, Q, K_pages, V_pages, page_table, kv_len, O, lse, workspace,
                   workspace_bytes, &a);
   if (st != WF_OK) return st;
   // So large a window hides nothing; positions minus it stay within 32 bits.
@@ -304,7 +310,7 @@ int wf_paged_window_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int
 }
 
 int wf_paged_tree_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_nodes, size_t* bytes) {
-  return wf_paged_attn_workspace_bytes(dims, n_nodes, bytes);
+  return paged_bytes(dims, n_nodes, wf::plan_paged_tree, bytes);
 }
 
 int wf_paged_tree_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_nodes,
@@ -314,14 +320,14 @@ int wf_paged_tree_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32
                        size_t workspace_bytes, void* stream) {
   if (opts != nullptr && (opts->causal == 0 || opts->prefix != nullptr)) return WF_ERR_UNSUPPORTED;
   wf::PagedArgs a;
-  const int st = paged_call(dims, opts, n_nodes, Q, K_pages, V_pages, page_table, kv_len, O, lse,
+  const int st = paged_call(wf::plan_paged_tree, dims, opts, n_nodes, Q, K_pages, V_pages, page_table, kv_len, O, lse,
                             workspace, workspace_bytes, &a);
   if (st != WF_OK) return st;
   if (parents == nullptr) return WF_ERR_NULL;
   if (!aligned4(parents) || !aligned4(tree_len)) return WF_ERR_ALIGNMENT;
   a.parents = parents;
   a.tree_len = tree_len;
-  return cuda_status(wf::launch_paged_tree(a, wf::plan_paged(a, wf::device_sm_count()),
+  return cuda_status(wf::launch_paged_tree(a, wf::plan_paged_tree(a, wf::device_sm_count()),
                                            static_cast<cudaStream_t>(stream)));
 }
 

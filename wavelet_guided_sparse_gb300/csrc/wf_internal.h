@@ -200,16 +200,17 @@ struct PagedArgs {
   int window, sinks;
   const int32_t *parents, *tree_len;      // tree_len nullable
 };
-// CTAs of the persistent grid, rows of a row block and workspace bytes of
-// the partials: functions of the sizes and the device alone.
+// CTAs of the persistent grid, rows of a row block, keys of a tile and
+// workspace bytes of the partials: functions of the sizes and the device alone.
 struct PagedPlan {
-  int ctas, row_block;
+  int ctas, row_block, tile;
   size_t part_bytes;
 };
 PagedPlan plan_paged(const PagedArgs& a, int sm_count);
 cudaError_t launch_paged_attn(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
 // With a window, and of a drafted tree (wf_paged_window.cu, wf_paged_tree.cu).
 cudaError_t launch_paged_window(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
+PagedPlan plan_paged_tree(const PagedArgs& a, int sm_count);
 cudaError_t launch_paged_tree(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
 
 // Attention over packed sequences with contiguous keys and values.

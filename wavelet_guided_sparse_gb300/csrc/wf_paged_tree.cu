@@ -1,10 +1,40 @@
-// Attention of drafted trees over a paged cache (kernels: wf_paged_kernel.cuh).
-#include "wf_paged_kernel.cuh"
+// Attention of drafted trees over a paged cache: plan and dispatch (kernels:
+// wf_paged_umma.cuh, and wf_paged_kernel.cuh for few rows and for fp32).
+#include "wf_paged_umma.cuh"
 
 namespace wf {
 
+namespace {
+
+// More rows than this a key head run on tcgen05 tiles of 128 rows (bf16; groups
+// of up to 128 heads, a node of which fits a tile).
+constexpr int kFewRows = 32;
+bool on_umma(const PagedArgs& a) {
+  const int g = a.q_heads / a.kv_heads;
+  return a.dtype == WF_BF16 && g <= kTileRows && g * a.n_new > kFewRows;
+}
+
+}  // namespace
+
+PagedPlan plan_paged_tree(const PagedArgs& a, int sm_count) {
+  if (!on_umma(a)) return plan_paged(a, sm_count);
+  PagedPlan p;
+  const int g = a.q_heads / a.kv_heads, nodes = kTileRows / g;
+  p.row_block = a.n_new > nodes ? 2 * nodes * g : kTileRows;
+  p.tile = kTileRows;
+  const int64_t units = static_cast<int64_t>(a.n_seqs) * a.kv_heads *
+                        ((g * a.n_new + p.row_block - 1) / p.row_block);
+  const int64_t tiles =
+      units * ((static_cast<int64_t>(a.table_pages) * a.page_size + p.tile - 1) / p.tile);
+  p.ctas = static_cast<int>(std::min<int64_t>(sm_count, tiles));
+  p.part_bytes = static_cast<size_t>(p.ctas) * 2 * p.row_block * (a.head_dim + 2) * sizeof(float);
+  return p;
+}
+
 cudaError_t launch_paged_tree(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
-  return launch_paged_mask<kMaskTree>(a, plan, stream);
+  if (!on_umma(a)) return launch_paged_mask<kMaskTree>(a, plan, stream);
+  return a.head_dim == 128 ? launch_umma_tree<128>(a, plan, stream)
+                           : launch_umma_tree<64>(a, plan, stream);
 }
 
 }  // namespace wf

@@ -36,7 +36,7 @@ inline bool encode_tile_map(CUtensorMap* map, CUtensorMapDataType type, const vo
                             const cuuint64_t* dims, const cuuint64_t* strides,
                             const cuuint32_t* box) {
   const EncodeTiledFn enc = tensormap_encoder();
-  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return enc != nullptr &&
          enc(map, type, rank, const_cast<void*>(base), dims, strides,
              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
