@@ -215,6 +215,15 @@ def test_lists_that_break_the_rules_leave_their_sequence_alone():
     m.check(bd.DEV_BAD_INDEX)
 
 
+def test_lists_longer_than_what_lies_behind_their_start():
+    m = Model(60, 6, 4, 16, seed=12)
+    lens = [96, 96, 90, 96]
+    m.reserve(lens)
+    lists = [[50, 51] * 40, [95] * 96, list(range(80, 90)) * 8, list(range(96))]
+    m.keep(lens, [50, 90, 80, 0], lists, skip=(0, 1, 2))
+    m.check(bd.DEV_BAD_INDEX)
+
+
 def test_shared_pages_are_not_written():
     m = Model(60, 6, 3, 16, seed=8)
     m.reserve([90, 0, 0])

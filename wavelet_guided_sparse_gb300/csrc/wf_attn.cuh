@@ -150,7 +150,7 @@ enum PagedMask : int { kMaskPlain, kMaskWindow, kMaskTree };
 struct WorkShape {
   int n_seqs;
   int units_per_seq;  // kv_heads * row blocks
-  int tile;           // keys per tile
+  int tile, tile_shift;  // keys per tile, their logarithm
   int max_len;        // table_pages * page_size
   int n_new, window, sinks;  // window: query rows of a sequence, its sizes
   const int32_t* tree_len;   // tree: nullable, nodes of each sequence (default n_new)
@@ -166,37 +166,37 @@ __device__ __forceinline__ int seq_len_clamped(const WorkShape& w, const int32_t
   return nodes == 0 || len < nodes ? 0 : len;
 }
 
-// Window: the first key that the sequence's first query sees by the window, the
-// tiles of the first tokens, the tiles between.
-__device__ __forceinline__ int window_low(const WorkShape& w, int len) {
-  return max(0, len - w.n_new - w.window + 1);
+// Tiles of a sequence of `len` keys.  Tile sizes are powers of two.
+__device__ __forceinline__ int tiles_up(const WorkShape& w, int keys) {
+  return (keys + w.tile - 1) >> w.tile_shift;
 }
-__device__ __forceinline__ int sink_tiles(const WorkShape& w, int len) {
-  return (min(w.sinks, len) + w.tile - 1) / w.tile;
-}
+// What a window leaves of a sequence: the first key that its first query sees by
+// the window, the tiles of the first tokens, and the tiles between that are not
+// in the line (without a window: none).
+struct Span {
+  int low, first, gap;
+  // The key tile at place t of the line.
+  __device__ __forceinline__ int place(int t) const { return t < first ? t : t + gap; }
+};
 template <int MASK>
-__device__ __forceinline__ int window_gap(const WorkShape& w, int len) {
-  if (MASK != kMaskWindow) return 0;
-  return max(0, window_low(w, len) / w.tile - sink_tiles(w, len));
-}
-// The key tile at place t of the sequence's line.
-template <int MASK>
-__device__ __forceinline__ int key_tile(const WorkShape& w, int len, int t) {
-  if (MASK != kMaskWindow) return t;
-  return t < sink_tiles(w, len) ? t : t + window_gap<MASK>(w, len);
+__device__ __forceinline__ Span span_of(const WorkShape& w, int len) {
+  Span x = {0, 0, 0};
+  if (MASK != kMaskWindow) return x;
+  x.low = max(0, len - w.n_new - w.window + 1);
+  x.first = tiles_up(w, min(w.sinks, len));
+  x.gap = max(0, (x.low >> w.tile_shift) - x.first);
+  return x;
 }
 // Whether some query sees one of keys key .. key + rows - 1 (a page that a
 // window has left behind may be gone).
 template <int MASK>
-__device__ __forceinline__ bool box_needed(const WorkShape& w, int len, int key, int rows) {
-  return key < len &&
-         (MASK != kMaskWindow || key < w.sinks || key + rows > window_low(w, len));
+__device__ __forceinline__ bool box_needed(const WorkShape& w, const Span& x, int len, int key,
+                                           int rows) {
+  return key < len && (MASK != kMaskWindow || key < w.sinks || key + rows > x.low);
 }
-
-// Tiles of a sequence of `len` keys.
 template <int MASK = kMaskPlain>
 __device__ __forceinline__ int tiles_of(const WorkShape& w, int len) {
-  return (len + w.tile - 1) / w.tile - window_gap<MASK>(w, len);
+  return tiles_up(w, len) - span_of<MASK>(w, len).gap;
 }
 
 // Tiles of the whole call.  Whole warp.
@@ -279,6 +279,22 @@ __device__ __forceinline__ WorkUnit find_unit(const WorkShape& w, const int32_t*
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
+  return u;
+}
+// Unit `n` of all (idle sequences' counted; tiles = 0 for theirs).  Whole warp.
+template <int MASK = kMaskPlain>
+__device__ __forceinline__ WorkUnit nth_unit(const WorkShape& w, const int32_t* lens, int n) {
+  WorkUnit u;
+  u.seq = n / w.units_per_seq;
+  u.unit = n - u.seq * w.units_per_seq;
+  u.len = seq_len_clamped<MASK>(w, lens, u.seq);
+  u.tiles = tiles_of<MASK>(w, u.len);
+  int before = 0;
+  for (int s = threadIdx.x & 31; s < u.seq; s += 32)
+    before += tiles_of<MASK>(w, seq_len_clamped<MASK>(w, lens, s));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  u.begin = static_cast<int64_t>(before) * w.units_per_seq + static_cast<int64_t>(u.unit) * u.tiles;
   return u;
 }
 // The unit after u (there is one: the caller stays below the total).  Whole
@@ -392,6 +408,8 @@ inline PagedParams paged_params(const PagedArgs& a, const PagedPlan& plan) {
   p.w.n_seqs = a.n_seqs;
   p.w.units_per_seq = a.kv_heads * p.row_blocks;
   p.w.tile = plan.tile;
+  p.w.tile_shift = 0;
+  while ((1 << p.w.tile_shift) < plan.tile) ++p.w.tile_shift;
   p.w.max_len = a.table_pages * a.page_size;
   p.w.n_new = a.n_new;
   p.w.window = a.window;

@@ -188,14 +188,14 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
     // Page-table entries of this lane's boxes of a tile (-1: nothing to copy),
     // only looked at when their copies are issued: the loads fly meanwhile.
     int page[NS];
+    Span span = span_of<MASK>(p.w, u.len);
     const auto read_entries = [&](const WorkUnit& x, int64_t at) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int box = sub + i * kSubs;
-        const int key = key_tile<MASK>(p.w, x.len, static_cast<int>(at - x.begin)) * KT +
-                        box * tp.box_rows;
+        const int key = span.place(static_cast<int>(at - x.begin)) * KT + box * tp.box_rows;
         page[i] = -1;
-        if (box < boxes && box_needed<MASK>(p.w, x.len, key, tp.box_rows))
+        if (box < boxes && box_needed<MASK>(p.w, span, x.len, key, tp.box_rows))
           page[i] = __ldg(a.table + static_cast<int64_t>(x.seq) * a.table_pages +
                           (key >> tp.page_shift));
       }
@@ -225,14 +225,14 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         ok = warp_wait(&bars.empty[st], phase, bars.wait, a.status);
         if (!ok) break;
       }
-      const int key0 = key_tile<MASK>(p.w, u.len, static_cast<int>(at - u.begin)) * KT;
+      const int key0 = span.place(static_cast<int>(at - u.begin)) * KT;
       unsigned live[NS];
       int parts = 0;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int box = sub + i * kSubs;
         if (page[i] < 0 || page[i] >= a.n_pages) {
-          if (box < boxes && box_needed<MASK>(p.w, u.len, key0 + box * tp.box_rows, tp.box_rows))
+          if (box < boxes && box_needed<MASK>(p.w, span, u.len, key0 + box * tp.box_rows, tp.box_rows))
             raise_flag(a.status, WF_DEV_BAD_INDEX);
           page[i] = -1;
         }
@@ -278,7 +278,10 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         phase ^= 1;
       }
       if (at + 1 < w1) {
-        if (at + 1 == u.begin + u.tiles) next_unit<MASK>(p.w, a.kv_len, u);
+        if (at + 1 == u.begin + u.tiles) {
+          next_unit<MASK>(p.w, a.kv_len, u);
+          span = span_of<MASK>(p.w, u.len);
+        }
         read_entries(u, at + 1);
       }
     }
@@ -381,12 +384,11 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) shut = max(shut, __shfl_xor_sync(0xffffffffu, shut, w));
       }
-      const int gap = window_gap<MASK>(p.w, len);
-      int key0 = (MASK == kMaskWindow ? key_tile<MASK>(p.w, len, tile0) : tile0) * KT +
-                 kg * Shape::kKeys;
+      const Span span = span_of<MASK>(p.w, len);
+      int key0 = span.place(tile0) * KT + kg * Shape::kKeys;
       for (int i = 0; i < tiles; ++i, key0 += KT) {
         if constexpr (MASK == kMaskWindow) {
-          if (i > 0 && gap > 0 && tile0 + i == sink_tiles(p.w, len)) key0 += gap * KT;
+          if (i > 0 && tile0 + i == span.first) key0 += span.gap * KT;
         }
         ok = ok && warp_wait(&bars.full[st], phase, bars.wait, a.status);
         if (!ok) break;  // given up: only the barriers below, in step with the other warps
@@ -737,7 +739,10 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
 
 // Join: the CTAs (c, .) merge the rows of the unit that starts inside CTA c's
 // range and ends behind it, from slot 2c + 1 and the slots 2(c + 1), ... of
-// the CTAs that hold the unit's other tiles.  Latency-bound (a row is two to
+// the CTAs that hold the unit's other tiles.  With fewer units than CTAs (few
+// long sequences, most of them split) CTAs (x, .) take unit x instead, so that
+// all of the grid has work (64 nodes over 4 x 32768 keys, 32 units of 256 rows:
+// JOINFIG).  Latency-bound (a row is two to
 // some tens of partials of d floats): as many of the eight warps share a row
 // as leave each about four partials, whose loads fly together; the lanes read
 // all maxima at once, and the warps of a row add up in their order.  Its
@@ -745,16 +750,25 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
 // have found their unit when that kernel ends.
 template <typename T, int D, int MASK>
 __global__ void __launch_bounds__(kThreads, 6)
-    paged_join_kernel(PagedParams p, int ctas, int RT) {
+    paged_join_kernel(PagedParams p, int ctas, int RT, int by_unit) {
   __shared__ float4 s_o[kWarps][D / 4];
   __shared__ float s_l[kWarps], s_m[kWarps];
   const PagedArgs& a = p.a;
   const int g = a.q_heads / a.kv_heads;
   const WorkSplit split(work_total<MASK>(p.w, a.kv_len), ctas);
-  const int c0 = blockIdx.x;
-  const int64_t w0 = split.begin(c0), w1 = split.begin(c0 + 1);
-  const bool any = w0 < w1;
-  const WorkUnit u = find_unit<MASK>(p.w, a.kv_len, any ? w1 - 1 : 0);
+  int c0 = blockIdx.x;
+  int64_t w0 = split.begin(c0), w1 = split.begin(c0 + 1);
+  bool any = w0 < w1;
+  WorkUnit u;
+  if (by_unit) {
+    u = nth_unit<MASK>(p.w, a.kv_len, blockIdx.x);
+    any = u.tiles > 0;
+    c0 = any ? split.owner(u.begin) : 0;
+    w0 = split.begin(c0);
+    w1 = split.begin(c0 + 1);
+  } else {
+    u = find_unit<MASK>(p.w, a.kv_len, any ? w1 - 1 : 0);
+  }
   const int64_t end = u.begin + u.tiles;
   const bool joins = any && u.begin >= w0 && end > w1;
   // This grid's end is all that the stream's next operation waits for, so it has
@@ -879,7 +893,11 @@ cudaError_t launch_join(const PagedArgs& a, const PagedPlan& plan, cudaStream_t 
   const int rows = std::min(plan.row_block, a.q_heads / a.kv_heads * a.n_new);
   cudaLaunchConfig_t cfg = {};
   // About eight CTAs an SM in all; each loops over its share of the rows.
-  cfg.gridDim = dim3(plan.ctas, std::max(1, std::min(rows, 8 * device_sm_count() / plan.ctas)));
+  const PagedParams p = paged_params(a, plan);
+  const int64_t units = static_cast<int64_t>(a.n_seqs) * p.w.units_per_seq;
+  const int by_unit = units < plan.ctas;
+  const int x = by_unit ? static_cast<int>(units) : plan.ctas;
+  cfg.gridDim = dim3(x, std::max(1, std::min(rows, 8 * device_sm_count() / x)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
@@ -887,8 +905,8 @@ cudaError_t launch_join(const PagedArgs& a, const PagedPlan& plan, cudaStream_t 
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, MASK>, paged_params(a, plan), plan.ctas,
-                            plan.row_block);
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, MASK>, p, plan.ctas, plan.row_block,
+                            by_unit);
 }
 
 template <typename T, int D, int MASK>

@@ -67,6 +67,8 @@ struct ForkUnit {
   int src, dst, shared, entries, len;
 };
 
+constexpr int kBatch = 8;  // loads of a lane that fly together
+
 struct AllocShared {
   uint32_t is_src[kSeqWords], once[kSeqWords], twice[kSeqWords];
   int warp_need[kAllocWarps], warp_free[kAllocWarps];
@@ -104,6 +106,17 @@ __device__ __forceinline__ ForkUnit fork_unit(const AllocArgs& x, const AllocSha
 // Entries of sequence s that a reserve has to fill.
 __device__ __forceinline__ int reserve_entries(const AllocArgs& x, int s, bool say) {
   return (length_in(x.p, __ldg(x.rows + s), say) + x.p.page_size - 1) / x.p.page_size;
+}
+
+// Words first + lane, first + 32 + lane, ... of an array that ends at `end`
+// (`with` behind it), all loads in flight together.
+__device__ __forceinline__ void read_batch(const int32_t* from, int first, int end, int lane,
+                                           int with, int (&got)[kBatch]) {
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    const int i = first + 32 * k + lane;
+    got[k] = i < end ? from[i] : with;
+  }
 }
 
 template <bool FORK>
@@ -144,15 +157,21 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
     } else {
       const int entries = reserve_entries(x, u, lane == 0);
       const int32_t* row = a.table + static_cast<int64_t>(u) * a.table_pages;
-      for (int e = lane; e - lane < entries; e += 32)
-        need += __popc(__ballot_sync(0xffffffffu, e < entries && row[e] < 0));
+      for (int e0 = 0; e0 < entries; e0 += 32 * kBatch) {
+        int got[kBatch];
+        read_batch(row, e0, entries, lane, 0, got);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) need += __popc(__ballot_sync(0xffffffffu, got[k] < 0));
+      }
     }
   }
   int free = 0;
-#pragma unroll 4
-  for (int p = p0 + lane; p < p1; p += 32) free += a.refs[p] == 0;
+  for (int p = p0; p < p1; p += 32 * kBatch) {
+    int got[kBatch];
+    read_batch(a.refs, p, p1, lane, 1, got);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) free += __shfl_xor_sync(0xffffffffu, free, o);
+    for (int k = 0; k < kBatch; ++k) free += __popc(__ballot_sync(0xffffffffu, got[k] == 0));
+  }
   if (lane == 0) {
     sm.warp_need[warp] = need;
     sm.warp_free[warp] = free;
@@ -182,12 +201,16 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
     total_free += sm.free[c];
   }
   // The free pages by rank, as far as they are needed.
-  for (int p = p0; p < p1 && free_before < total_need; p += 32) {
-    const bool is = p + lane < p1 && a.refs[p + lane] == 0;
-    const unsigned hits = __ballot_sync(0xffffffffu, is);
-    const int rank = free_before + __popc(hits & ((1u << lane) - 1));
-    if (is && rank < total_need) x.list[rank] = p + lane;
-    free_before += __popc(hits);
+  for (int p = p0; p < p1 && free_before < total_need; p += 32 * kBatch) {
+    int got[kBatch];
+    read_batch(a.refs, p, p1, lane, 1, got);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const unsigned hits = __ballot_sync(0xffffffffu, got[k] == 0);
+      const int rank = free_before + __popc(hits & ((1u << lane) - 1));
+      if (got[k] == 0 && rank < total_need) x.list[rank] = p + 32 * k + lane;
+      free_before += __popc(hits);
+    }
   }
   if (total_need > total_free && gw == 0 && lane == 0) raise_flag(a.status, WF_DEV_NO_PAGE);
   if (FORK && gw == 0 && lane == 0) *x.n_copies = min(total_need, total_free);
@@ -200,41 +223,55 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
       if (f.dst < 0) continue;
       const int32_t* from = a.table + static_cast<int64_t>(f.src) * a.table_pages;
       int32_t* to = a.table + static_cast<int64_t>(f.dst) * a.table_pages;
-      for (int e = lane; e < a.table_pages; e += 32) {
-        int page = -1;
-        if (e < f.entries) {
-          const int parent = from[e];
-          const bool there = static_cast<unsigned>(parent) < static_cast<unsigned>(a.n_pages);
-          if (!there) raise_flag(a.status, WF_DEV_BAD_INDEX);
-          if (e < f.shared) {
-            if (there) {
-              page = parent;
-              atomicAdd(a.refs + page, 1);
-            }
-          } else {
-            const int r = rank + e - f.shared;
-            if (r < total_free) {
-              page = x.list[r];
+      for (int e0 = 0; e0 < a.table_pages; e0 += 32 * kBatch) {
+        int parents[kBatch], fresh[kBatch];
+        read_batch(from, e0, f.entries, lane, -1, parents);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = rank + e0 + 32 * k + lane - f.shared;
+          fresh[k] = r >= rank && e0 + 32 * k + lane < f.entries && r < total_free ? x.list[r] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int e = e0 + 32 * k + lane, r = rank + e - f.shared;
+          if (e >= a.table_pages) continue;
+          int page = -1;
+          if (e < f.entries) {
+            const bool there =
+                static_cast<unsigned>(parents[k]) < static_cast<unsigned>(a.n_pages);
+            if (!there) raise_flag(a.status, WF_DEV_BAD_INDEX);
+            if (e < f.shared) {
+              if (there) {
+                page = parents[k];
+                atomicAdd(a.refs + page, 1);
+              }
+            } else if (r < total_free) {
+              page = fresh[k];
               a.refs[page] = 1;
-              x.copies[r] = make_int4(there ? parent : -1, page,
+              x.copies[r] = make_int4(there ? parents[k] : -1, page,
                                       min(a.page_size, f.len - e * a.page_size), 0);
             }
           }
+          to[e] = page;
         }
-        to[e] = page;
       }
     } else {
       const int entries = reserve_entries(x, u, false);
       int32_t* row = a.table + static_cast<int64_t>(u) * a.table_pages;
-      for (int e = lane; e - lane < entries; e += 32) {
-        const bool lacks = e < entries && row[e] < 0;
-        const unsigned hits = __ballot_sync(0xffffffffu, lacks);
-        const int r = rank + __popc(hits & ((1u << lane) - 1));
-        if (lacks && r < total_free) {
-          row[e] = x.list[r];
-          a.refs[x.list[r]] = 1;
+      for (int e0 = 0; e0 < entries; e0 += 32 * kBatch) {
+        int got[kBatch];
+        read_batch(row, e0, entries, lane, 0, got);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const unsigned hits = __ballot_sync(0xffffffffu, got[k] < 0);
+          const int r = rank + __popc(hits & ((1u << lane) - 1));
+          if (got[k] < 0 && r < total_free) {
+            const int page = x.list[r];
+            row[e0 + 32 * k + lane] = page;
+            a.refs[page] = 1;
+          }
+          rank += __popc(hits);
         }
-        rank += __popc(hits);
       }
     }
   }
@@ -289,9 +326,11 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const PagesArgs a, co
 // Checks one sequence's list, resolves the rows that move and leaves in
 // info[s] = (rows at the head that stay where they are, rows in all, new length
 // or -1 when the sequence is left as it was).
-__global__ void __launch_bounds__(kThreads) keep_plan_kernel(const KeepArgs x) {
+constexpr int kPlanThreads = 1024, kPlanBatch = 4;
+__global__ void __launch_bounds__(kPlanThreads) keep_plan_kernel(const KeepArgs x) {
   const PagesArgs& a = x.p;
   __shared__ int s_bad, s_shared, s_stay;
+  const int threads = blockDim.x;
   launch_dependents();
   for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
     __syncthreads();
@@ -306,22 +345,45 @@ __global__ void __launch_bounds__(kThreads) keep_plan_kernel(const KeepArgs x) {
     const int32_t* keep = x.keep + static_cast<int64_t>(s) * x.max_keep;
     const int32_t* row = a.table + static_cast<int64_t>(s) * a.table_pages;
     bool bad = !sound, shared = false;
-    for (int i = threadIdx.x; i < count; i += kThreads) {
-      const int from = __ldg(keep + i);
-      if (from < (i > 0 ? __ldg(keep + i - 1) + 1 : start) || from >= len) {
-        bad = true;
-        continue;
+    for (int i0 = threadIdx.x; i0 < count; i0 += threads * kPlanBatch) {
+      int from[kPlanBatch], prev[kPlanBatch], page[kPlanBatch], to[kPlanBatch];
+#pragma unroll
+      for (int k = 0; k < kPlanBatch; ++k) {
+        const int i = i0 + k * threads;
+        from[k] = i < count ? __ldg(keep + i) : -1;
+        prev[k] = i > 0 && i < count ? __ldg(keep + i - 1) : -1;
       }
-      if (from == start + i) continue;  // so are all before it
-      atomicMin(&s_stay, i);
-      const int to = row[(start + i) / a.page_size], page = row[from / a.page_size];
-      if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages) ||
-          static_cast<unsigned>(to) >= static_cast<unsigned>(a.n_pages))
-        bad = true;
-      else if (a.refs != nullptr && a.refs[to] > 1)
-        shared = true;
-      x.lines[static_cast<int64_t>(s) * x.max_keep + i] =
-          page * a.page_size + (from & (a.page_size - 1));
+      // from = -1: a row that stays (so do all before it), or none, or one that
+      // breaks the rules.  An ascending list's row i is start + i or behind it, so
+      // that start + i lies in the table too.
+#pragma unroll
+      for (int k = 0; k < kPlanBatch; ++k) {
+        const int i = i0 + k * threads;
+        page[k] = to[k] = 0;
+        if (i >= count) continue;
+        if (from[k] <= prev[k] || from[k] < start || from[k] - start < i || from[k] >= len) {
+          bad = true;
+          from[k] = -1;
+        } else if (from[k] - start == i) {
+          from[k] = -1;
+        } else {
+          page[k] = row[from[k] / a.page_size];
+          to[k] = row[(start + i) / a.page_size];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kPlanBatch; ++k) {
+        const int i = i0 + k * threads;
+        if (from[k] < 0) continue;
+        atomicMin(&s_stay, i);
+        if (static_cast<unsigned>(page[k]) >= static_cast<unsigned>(a.n_pages) ||
+            static_cast<unsigned>(to[k]) >= static_cast<unsigned>(a.n_pages))
+          bad = true;
+        else if (a.refs != nullptr && a.refs[to[k]] > 1)
+          shared = true;
+        x.lines[static_cast<int64_t>(s) * x.max_keep + i] =
+            page[k] * a.page_size + (from[k] & (a.page_size - 1));
+      }
     }
     if (bad) s_bad = 1;
     if (shared) s_shared = 1;
@@ -469,7 +531,8 @@ cudaError_t launch_release(const PagesArgs& a, const int32_t* first, const int32
 }
 
 cudaError_t launch_keep(const KeepArgs& x, const PagePools& pools, cudaStream_t stream) {
-  keep_plan_kernel<<<grid_of(x.p.n_seqs), kThreads, 0, stream>>>(x);
+  keep_plan_kernel<<<grid_of(x.p.n_seqs), x.max_keep > kThreads ? kPlanThreads : kThreads, 0,
+                     stream>>>(x);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int chunks = row_chunks_of(x.p);
