@@ -117,14 +117,26 @@ def test_window_edges_against_tiles(window, sinks):
                sinks, True, 0.0, False, seed=window + sinks)
 
 
+def check_same(got, want, bounds, what):
+    """Two results that each lie within `bounds` of the same exact ones."""
+    for x, y, b, name in zip(got, want, bounds, ("O", "lse")):
+        x, y = f64(x), f64(y)
+        with np.errstate(invalid="ignore"):
+            assert ((x == y) | (np.abs(x - y) <= 2 * b)).all(), f"{name} of {what}"
+
+
 def test_window_over_everything_is_the_plain_attention():
-    cache, table = paged([700, 64, 1], 16, 2, 128, BF, 5)
-    q, t, n = randn((3, 4, 8, 128), BF, 1), i32(table.tolist()), i32([700, 64, 1])
+    lens = [700, 64, 1]
+    cache, table = paged(lens, 16, 2, 128, BF, 5)
+    q, t, n = randn((3, 4, 8, 128), BF, 1), i32(table.tolist()), i32(lens)
     for causal in (True, False):
         a = bd.paged_attn(q, cache, t, n, causal=causal, with_lse=True)
         for sinks in (0, 3, 2000):
             b = bd.paged_window_attn(q, cache, t, n, 700, sinks=sinks, causal=causal, with_lse=True)
-            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+            for s, m in enumerate(lens):
+                seen = window_mask(m - 4 + np.arange(4), m, 700, sinks, causal)
+                ob, lb = attend_masked(f64(q[s]), *rows_of(cache, table, s, m), BF, seen)[2:]
+                check_same([x[s] for x in b], [x[s] for x in a], (ob, lb), f"sequence {s}")
 
 
 def test_window_of_released_pages():
@@ -246,6 +258,16 @@ def test_tree(case):
     run_tree(*TREES[case], seed=100 + case)
 
 
+@pytest.mark.parametrize("nodes,hq,hkv,page,bias", [
+    (20, 40, 10, 16, False), (26, 32, 8, 64, True), (64, 40, 10, 128, False), (33, 60, 15, 8, True)])
+def test_tree_of_many_tiles(nodes, hq, hkv, page, bias):
+    """Some tens of key tiles a CTA, in parts of several units."""
+    rng = np.random.default_rng(nodes)
+    lens = [9000, 7111, 70, 5002, 8200, 0, 6400]
+    trees = [random_tree(max(1, nodes - 3 * s), rng) if n else [] for s, n in enumerate(lens)]
+    run_tree(BF, 64, hq, hkv, page, lens, nodes, trees, 0.0, bias, seed=nodes)
+
+
 @pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 2), (12, 4), (24, 2)])
 def test_tree_edges_against_tiles(hq, hkv):
     """Trees that begin, end and lie across the borders of key tiles."""
@@ -256,14 +278,18 @@ def test_tree_edges_against_tiles(hq, hkv):
                  True, seed=nodes)
 
 
-def test_a_chain_is_the_causal_attention():
-    """A tree without branches sees what new tokens see, bit for bit where both
-    run the same rows."""
-    cache, table = paged([700, 64, 5], 16, 2, 128, BF, 5)
-    q, t, n = randn((3, 4, 8, 128), BF, 1), i32(table.tolist()), i32([700, 64, 5])
+@pytest.mark.parametrize("nodes", [1, 4, 40])
+def test_a_chain_is_the_causal_attention(nodes):
+    """A tree without branches sees what new tokens see."""
+    lens = [700, 64, 41]
+    cache, table = paged(lens, 16, 2, 128, BF, 5)
+    q, t, n = randn((3, nodes, 8, 128), BF, 1), i32(table.tolist()), i32(lens)
     a = bd.paged_attn(q, cache, t, n, with_lse=True)
-    b = bd.paged_tree_attn(q, cache, t, n, i32([[-1, 0, 1, 2]] * 3), with_lse=True)
-    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    b = bd.paged_tree_attn(q, cache, t, n, i32([list(range(-1, nodes - 1))] * 3), with_lse=True)
+    for s, m in enumerate(lens):
+        seen = tree_mask(m - nodes, list(range(-1, nodes - 1)))[0]
+        ob, lb = attend_masked(f64(q[s]), *rows_of(cache, table, s, m), BF, seen)[2:]
+        check_same([x[s] for x in b], [x[s] for x in a], (ob, lb), f"sequence {s}")
 
 
 def test_tree_flags():

@@ -737,17 +737,52 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
   }
 }
 
-// Join: the CTAs (c, .) merge the rows of the unit that starts inside CTA c's
-// range and ends behind it, from slot 2c + 1 and the slots 2(c + 1), ... of
-// the CTAs that hold the unit's other tiles.  With fewer units than CTAs (few
-// long sequences, most of them split) CTAs (x, .) take unit x instead, so that
-// all of the grid has work (64 nodes over 4 x 32768 keys, 32 units of 256 rows:
-// JOINFIG).  Latency-bound (a row is two to
-// some tens of partials of d floats): as many of the eight warps share a row
-// as leave each about four partials, whose loads fly together; the lanes read
-// all maxima at once, and the warps of a row add up in their order.  Its
-// registers are bounded so that its CTAs fit beside the split kernel's and
-// have found their unit when that kernel ends.
+// What a CTA of the joins has to merge: the unit that starts inside CTA c0's
+// range and ends behind it, in n parts (slot 2 c0 + 1 and the slots 2 (c0 + 1),
+// ... of the CTAs that hold its other tiles).  c0 is blockIdx.x; with fewer units
+// than CTAs (few long sequences, most of them split) blockIdx.x is the unit
+// instead, so that all of the grid has work.
+//
+// The join's end is all that the stream's next operation waits for, so it has to
+// imply the split kernel's end, with nothing to join too: the first CTA of every
+// range waits whatever it finds.  (All of them waiting, the rest held up the
+// joining CTAs behind them: 84.4 -> 85.6 us for one context of 131072 keys, 13.8
+// -> 15.4 for a short one.)
+struct JoinUnit {
+  WorkUnit u;
+  int c0, n;
+  bool joins;
+};
+template <int MASK>
+__device__ __forceinline__ JoinUnit join_unit(const PagedParams& p, int ctas, int RT,
+                                              int by_unit) {
+  const WorkSplit split(work_total<MASK>(p.w, p.a.kv_len), ctas);
+  JoinUnit x;
+  x.c0 = blockIdx.x;
+  int64_t w0 = split.begin(x.c0), w1 = split.begin(x.c0 + 1);
+  bool any = w0 < w1;
+  if (by_unit) {
+    x.u = nth_unit<MASK>(p.w, p.a.kv_len, blockIdx.x);
+    any = x.u.tiles > 0;
+    x.c0 = any ? split.owner(x.u.begin) : 0;
+    w0 = split.begin(x.c0);
+    w1 = split.begin(x.c0 + 1);
+  } else {
+    x.u = find_unit<MASK>(p.w, p.a.kv_len, any ? w1 - 1 : 0);
+  }
+  const int64_t end = x.u.begin + x.u.tiles;
+  x.joins = any && x.u.begin >= w0 && end > w1;
+  x.n = x.joins ? split.owner(end - 1) - x.c0 + 1 : 0;
+  if (x.joins || blockIdx.y == 0) wait_for_primary();
+  return x;
+}
+
+// Join of the plain form.  Latency-bound (a row is two to some tens of partials
+// of d floats): as many of the eight warps share a row as leave each about four
+// partials, whose loads fly together; the lanes read all maxima at once, and the
+// warps of a row add up in their order.  Its registers are bounded so that its
+// CTAs fit beside the split kernel's and have found their unit when that kernel
+// ends.
 template <typename T, int D, int MASK>
 __global__ void __launch_bounds__(kThreads, 6)
     paged_join_kernel(PagedParams p, int ctas, int RT, int by_unit) {
@@ -755,36 +790,16 @@ __global__ void __launch_bounds__(kThreads, 6)
   __shared__ float s_l[kWarps], s_m[kWarps];
   const PagedArgs& a = p.a;
   const int g = a.q_heads / a.kv_heads;
-  const WorkSplit split(work_total<MASK>(p.w, a.kv_len), ctas);
-  int c0 = blockIdx.x;
-  int64_t w0 = split.begin(c0), w1 = split.begin(c0 + 1);
-  bool any = w0 < w1;
-  WorkUnit u;
-  if (by_unit) {
-    u = nth_unit<MASK>(p.w, a.kv_len, blockIdx.x);
-    any = u.tiles > 0;
-    c0 = any ? split.owner(u.begin) : 0;
-    w0 = split.begin(c0);
-    w1 = split.begin(c0 + 1);
-  } else {
-    u = find_unit<MASK>(p.w, a.kv_len, any ? w1 - 1 : 0);
-  }
-  const int64_t end = u.begin + u.tiles;
-  const bool joins = any && u.begin >= w0 && end > w1;
-  // This grid's end is all that the stream's next operation waits for, so it has
-  // to imply the split kernel's end, with nothing to join too: the first CTA of
-  // every range waits whatever it finds.  (All of them waiting, the rest held up
-  // the joining CTAs behind them: 84.4 -> 85.6 us for one context of 131072 keys,
-  // 13.8 -> 15.4 for a short one.)
-  if (joins || blockIdx.y == 0) wait_for_primary();
-  if (!joins) return;
-  const int n = split.owner(end - 1) - c0 + 1;  // CTAs with tiles of the unit
+  const JoinUnit x = join_unit<MASK>(p, ctas, RT, by_unit);
+  if (!x.joins) return;
+  const WorkUnit& u = x.u;
+  const int n = x.n;
   const int share = n <= 4 ? 1 : n <= 8 ? 2 : n <= 16 ? 4 : 8;  // warps per row
   const int at_once = kWarps / share;                           // rows per pass
   const int row0 = (u.unit % p.row_blocks) * RT;
   const int rows = min(RT, g * a.n_new - row0);
   const int64_t stride = static_cast<int64_t>(RT) * (D + 2);
-  const float* first = a.part + (2 * static_cast<int64_t>(c0) + 1) * stride;
+  const float* first = a.part + (2 * static_cast<int64_t>(x.c0) + 1) * stride;
   const auto slot = [&](int i) { return first + (i == 0 ? 0 : (2 * i - 1) * stride); };
   const int kvh = u.unit / p.row_blocks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -845,6 +860,81 @@ __global__ void __launch_bounds__(kThreads, 6)
   }
 }
 
+// Join of the masked forms, a warp a row: the lanes read the maxima and sums of up
+// to 32 parts at once, beside the first eight parts themselves, so that a row of
+// few parts waits for memory once (the other join twice, and for each part beyond
+// four in turn: 64 nodes over 4 x 32768 keys 122 -> 114 us, 26 nodes over four
+// sequences of 300 to 1500 keys 22.4 -> 18.4).
+constexpr int kJoinThreads = 128;
+template <typename T, int D, int MASK>
+__global__ void __launch_bounds__(kJoinThreads, 8)
+    masked_join_kernel(PagedParams p, int ctas, int RT, int by_unit) {
+  const PagedArgs& a = p.a;
+  const int g = a.q_heads / a.kv_heads;
+  const JoinUnit x = join_unit<MASK>(p, ctas, RT, by_unit);
+  if (!x.joins) return;
+  const int n = x.n, kvh = x.u.unit / p.row_blocks;
+  const int row0 = (x.u.unit % p.row_blocks) * RT;
+  const int rows = min(RT, g * a.n_new - row0);
+  const int64_t stride = static_cast<int64_t>(RT) * (D + 2);
+  const float* first = a.part + (2 * static_cast<int64_t>(x.c0) + 1) * stride;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kFly = 8, V = 128 / D;  // loads in flight, parts of each
+  const int half = lane / (D / 4), col = lane % (D / 4) * 4;
+  const int step = gridDim.y * (kJoinThreads / 32);
+  for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < rows; r += step) {
+    const auto slot = [&](int i) { return first + (i == 0 ? 0 : (2 * i - 1) * stride); };
+    float m = -INFINITY, l = 0.f, f[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < n; c += 32) {
+      float4 v[kFly];
+      const auto read = [&](int k0) {
+#pragma unroll
+        for (int k = 0; k < kFly; ++k) {
+          const int i = c + k0 + k * V + half;
+          v[k] = i < min(n, c + 32) ? *reinterpret_cast<const float4*>(slot(i) + r * D + col)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      };
+      read(0);
+      const float2 y = c + lane < n
+                           ? *reinterpret_cast<const float2*>(slot(c + lane) + RT * D + 2 * r)
+                           : make_float2(-INFINITY, 0.f);
+      const float mx = fmaxf(m, warp_max(y.x)), base = mx == -INFINITY ? 0.f : mx;
+      const float old = fast_exp2(m - base), w = fast_exp2(y.x - base);
+      float sum = w * y.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      m = mx;
+      l = fmaf(l, old, sum);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] *= old;
+      for (int k0 = 0; k0 < min(32, n - c); k0 += kFly * V) {
+        if (k0 > 0) read(k0);
+#pragma unroll
+        for (int k = 0; k < kFly; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, (k0 + k * V + half) & 31);
+          f[0] = fmaf(wk, v[k].x, f[0]);
+          f[1] = fmaf(wk, v[k].y, f[1]);
+          f[2] = fmaf(wk, v[k].z, f[2]);
+          f[3] = fmaf(wk, v[k].w, f[3]);
+        }
+      }
+    }
+    if (D == 64) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] += __shfl_xor_sync(0xffffffffu, f[e], 16);
+    }
+    const float inv = inv_or_zero(l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] *= inv;
+    const int i = (row0 + r) / g, hd = (row0 + r) - i * g;
+    const int64_t at =
+        (static_cast<int64_t>(x.u.seq) * a.n_new + i) * a.q_heads + kvh * g + hd;
+    if (half == 0) store4(static_cast<T*>(a.o) + at * D + col, f);
+    if (a.lse != nullptr && lane == 0) a.lse[at] = row_lse(m, l);
+  }
+}
+
 template <typename T, int D, int R, int MASK, bool CAP, bool BIAS>
 cudaError_t launch_tc(const PagedTcParams& p, const PagedPlan& plan, cudaStream_t stream) {
   using Shape = PagedShape<T, D, R>;
@@ -882,7 +972,9 @@ cudaError_t launch_tc_rows(const PagedArgs& a, const PagedPlan& plan, cudaStream
       !encode_tile_map(&p.tv, type, a.v_pages, 2, dims, strides, box))
     return cudaErrorInvalidValue;
   if (plan.row_block == 16) return launch_tc_opts<T, D, 1, MASK>(p, plan, stream);
-  if (plan.row_block == 32) return launch_tc_opts<T, D, 2, MASK>(p, plan, stream);
+  // Trees of bf16 come here with a few rows, or with more than 128 (wf_paged_tree.cu).
+  if constexpr (MASK != kMaskTree || sizeof(T) == 4)
+    if (plan.row_block == 32) return launch_tc_opts<T, D, 2, MASK>(p, plan, stream);
   return launch_tc_opts<T, D, 4, MASK>(p, plan, stream);
 }
 
@@ -891,22 +983,27 @@ cudaError_t launch_tc_rows(const PagedArgs& a, const PagedPlan& plan, cudaStream
 template <typename T, int D, int MASK>
 cudaError_t launch_join(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
   const int rows = std::min(plan.row_block, a.q_heads / a.kv_heads * a.n_new);
-  cudaLaunchConfig_t cfg = {};
-  // About eight CTAs an SM in all; each loops over its share of the rows.
   const PagedParams p = paged_params(a, plan);
   const int64_t units = static_cast<int64_t>(a.n_seqs) * p.w.units_per_seq;
   const int by_unit = units < plan.ctas;
   const int x = by_unit ? static_cast<int>(units) : plan.ctas;
-  cfg.gridDim = dim3(x, std::max(1, std::min(rows, 8 * device_sm_count() / x)));
-  cfg.blockDim = dim3(kThreads);
+  cudaLaunchConfig_t cfg = {};
+  // About eight CTAs an SM in all; each loops over its share of the rows.
+  const int most = MASK == kMaskPlain ? rows : (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  cfg.gridDim = dim3(x, std::max(1, std::min(most, 8 * device_sm_count() / x)));
+  cfg.blockDim = dim3(MASK == kMaskPlain ? kThreads : kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, MASK>, p, plan.ctas, plan.row_block,
-                            by_unit);
+  if constexpr (MASK == kMaskPlain)
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, MASK>, p, plan.ctas, plan.row_block,
+                              by_unit);
+  else
+    return cudaLaunchKernelEx(&cfg, masked_join_kernel<T, D, MASK>, p, plan.ctas, plan.row_block,
+                              by_unit);
 }
 
 template <typename T, int D, int MASK>

@@ -17,8 +17,8 @@
 //         lanes, so that at a unit's end each group adds up half of the columns.
 // Products wait for keys ahead by one (PAIR) or two key tiles: K_0 .. K_{L-1},
 // then V_i and K_{i+L} for i = 0, 1, ...  Warp 0 issues every product, warp 1
-// every tensor copy (whole pages or 128-row parts of them), warps 2-3 see to idle
-// sequences.  Keys run from a part's last tile to its first: the drafted rows,
+// the tensor copies of queries and keys, warp 2 those of values (whole pages or
+// 128-row parts of them), warp 3 sees to idle sequences.  Keys run from a part's last tile to its first: the drafted rows,
 // the only ones with a mask, come first.  Weights, maximum and roundings as in
 // wf_prefill.cu.
 //
@@ -68,6 +68,7 @@ struct UmmaBarriers {
   uint64_t o[2], o_empty[2];   // output finished; read
   uint64_t drain;
   int valid[8];                // of a key tile, by its number: one bit a box
+  uint32_t issued[2][8];       // last fill of each stage by the copying warps, plus 1
   uint32_t tmem;
   WaitState wait;
 };
@@ -172,10 +173,12 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kUmmaIssueRegs));
     const bool leader = elect_one();
-    if (warp >= 2) {
-      idle_sequences<__nv_bfloat16, kMaskTree>(a, p.w, blockIdx.x, gridDim.x, threadIdx.x - 64, 64);
-    } else if (warp == 1) {
-      // ---- copies: lane = (box, column block) of a stage
+    if (warp == 3) {
+      idle_sequences<__nv_bfloat16, kMaskTree>(a, p.w, blockIdx.x, gridDim.x, lane, 32);
+    } else if (warp > 0) {
+      // ---- copies: lane = (box, column block) of a stage.  Both warps walk all
+      // fills; warp 1 issues queries and keys, warp 2 values.
+      const bool keys = warp == 1;
       const int boxes = kTileRows / tp.box_rows;
       const int box = lane / KB, kb = lane % KB;
       const uint32_t box_bytes = static_cast<uint32_t>(tp.box_rows) * 128;
@@ -183,6 +186,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       bool ok = true;
       uint32_t fills = 0, steps = 0, tiles = 0, units = 0;
       uint32_t step_of[kStages] = {};  // the step that frees each stage
+      uint32_t mine[kStages] = {};     // this warp's last fill of each, plus 1
       int st = 0;
       // This lane's page-table entry for key tile j (-1: nothing to copy).
       const auto entry = [&](int j) {
@@ -192,49 +196,59 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                            (key >> tp.page_shift))
                    : -1;
       };
-      const auto fill = [&](const CUtensorMap* map, int j, int page, int kvh, uint32_t step) {
-        if (fills >= kStages) {
-          uint32_t r = 0;
+      const auto fill = [&](bool key_fill, int j, int page, int kvh, uint32_t step) {
+        if (key_fill == keys) {
+          if (fills >= kStages) {
+            uint32_t r = 0;
 #pragma unroll
-          for (int i = 0; i < kStages; ++i) r = i == st ? step_of[i] : r;
-          ok = ok && warp_wait(&bars.done[r & 7], (r >> 3) & 1, bars.wait, a.status);
+            for (int i = 0; i < kStages; ++i) r = i == st ? step_of[i] : r;
+            ok = ok && warp_wait(&bars.done[r & 7], (r >> 3) & 1, bars.wait, a.status);
+          }
+          if (!ok) return;
+          const int key = j * kTileRows + box * tp.box_rows;
+          const unsigned live = __ballot_sync(
+              0xffffffffu, static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages));
+          if (!((live >> lane) & 1) && box < boxes && key < u.len)
+            raise_flag(a.status, WF_DEV_BAD_INDEX);
+          const bool issue = !(inject && fills == 0);
+          if (lane == 0 && issue) {
+            if (keys) {
+              int valid = (1 << boxes) - 1;
+              if (live != every)
+                for (int b = 0; b < boxes; ++b)
+                  if (!((live >> (b * KB)) & 1)) valid &= ~(1 << b);
+              bars.valid[tiles & 7] = valid;
+            }
+            mbar_arrive_expect_tx(&bars.full[st], __popc(live) * box_bytes);
+          }
+          __syncwarp();
+          if (issue && ((live >> lane) & 1))
+            tma_load_2d(ring + st * kTileBytes + kb * kBlock + box * box_bytes,
+                        keys ? &tp.tk : &tp.tv, kb * 64,
+                        (page * a.kv_heads + kvh) * a.page_size + (key & (a.page_size - 1)),
+                        &bars.full[st]);
+#pragma unroll
+          for (int i = 0; i < kStages; ++i)
+            if (i == st && issue) mine[i] = fills + 1;
         }
-        if (!ok) return;
 #pragma unroll
         for (int i = 0; i < kStages; ++i)
           if (i == st) step_of[i] = step;
-        const int key = j * kTileRows + box * tp.box_rows;
-        const unsigned live =
-            __ballot_sync(0xffffffffu, static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages));
-        if (!((live >> lane) & 1) && box < boxes && key < u.len)
-          raise_flag(a.status, WF_DEV_BAD_INDEX);
-        const bool issue = !(inject && fills == 0);
-        if (lane == 0 && issue) {
-          if (map == &tp.tk) {
-            int valid = (1 << boxes) - 1;
-            if (live != every)
-              for (int b = 0; b < boxes; ++b)
-                if (!((live >> (b * KB)) & 1)) valid &= ~(1 << b);
-            bars.valid[tiles & 7] = valid;
-          }
-          mbar_arrive_expect_tx(&bars.full[st], __popc(live) * box_bytes);
-        }
-        if (map == &tp.tk) ++tiles;
-        __syncwarp();
-        if (issue && ((live >> lane) & 1))
-          tma_load_2d(ring + st * kTileBytes + kb * kBlock + box * box_bytes, map, kb * 64,
-                      (page * a.kv_heads + kvh) * a.page_size + (key & (a.page_size - 1)),
-                      &bars.full[st]);
+        tiles += key_fill;
         ++fills;
         if (++st == kStages) st = 0;
       };
       for (int64_t at = w0; at < w1 && ok;) {
         const UnitPart x = unit_part(u, at, w1);
         const int n = x.j1 - x.j0, kvh = u.unit / p.row_blocks;
-        if (units > 0) ok = warp_wait(&bars.q_empty, (units - 1) & 1, bars.wait, a.status);
+        // Entries of the part's tiles i, i + 1, i + 2 (tile i is key tile j1 - 1 - i).
+        const auto entry_of = [&](int i) { return i < n ? entry(x.j1 - 1 - i) : -1; };
+        int e0 = entry_of(0), e1 = entry_of(1), e2 = entry_of(2);
+        if (keys && units > 0)
+          ok = warp_wait(&bars.q_empty, (units - 1) & 1, bars.wait, a.status);
         if (!ok) break;
         ++units;
-        if (leader) {
+        if (keys && leader) {
           const int nt = tiles_with_rows(u);
           const int node0 = (u.unit % p.row_blocks) * Shape::kQueryTiles * tp.tile_nodes;
           mbar_arrive_expect_tx(&bars.q, nt * tp.tile_rows * D * 2);
@@ -244,14 +258,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                           u.seq * a.n_new + node0 + t * tp.tile_nodes, &bars.q);
         }
         __syncwarp();
-        // Entries of the part's tiles i, i + 1, i + 2 (tile i is key tile j1 - 1 - i).
-        const auto entry_of = [&](int i) { return i < n ? entry(x.j1 - 1 - i) : -1; };
-        int e0 = entry_of(0), e1 = entry_of(1), e2 = entry_of(2);
-        for (int i = 0; i < kAhead && i < n; ++i) fill(&tp.tk, x.j1 - 1 - i, i ? e1 : e0, kvh, steps);
+        for (int i = 0; i < kAhead && i < n; ++i) fill(true, x.j1 - 1 - i, i ? e1 : e0, kvh, steps);
         for (int i = 0; i < n && ok; ++i) {
-          fill(&tp.tv, x.j1 - 1 - i, e0, kvh, steps + i);
+          fill(false, x.j1 - 1 - i, e0, kvh, steps + i);
           if (i + kAhead < n && ok)
-            fill(&tp.tk, x.j1 - 1 - i - kAhead, PAIR ? e1 : e2, kvh, steps + i);
+            fill(true, x.j1 - 1 - i - kAhead, PAIR ? e1 : e2, kvh, steps + i);
           e0 = e1;
           e1 = e2;
           e2 = entry_of(i + 3);
@@ -260,12 +271,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         at += n;
         if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
       }
-      // Nothing of this CTA's copies may land after it has gone, also where another
-      // role has given up behind this warp's last wait.
       if (leader) {
-        if (units > 0) mbar_wait_bounded(&bars.q, (units - 1) & 1, a.status);
-        for (uint32_t f = max(inject ? 1 : 0, static_cast<int>(fills) - kStages); f < fills; ++f)
-          mbar_wait_bounded(&bars.full[f % kStages], (f / kStages) & 1, a.status);
+        if (keys && units > 0) mbar_wait_bounded(&bars.q, (units - 1) & 1, a.status);
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) bars.issued[warp - 1][i] = mine[i];
       }
     } else {
       // ---- products: the whole warp walks the loop, one elected lane issues
@@ -676,6 +685,14 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, 512);
+  // Nothing of this CTA's copies may land after it has gone, also where a role has
+  // given up before their products.  A stage's last fill only: what either warp
+  // issued before it had been used, and its barrier has moved on.
+  if (threadIdx.x < kStages) {
+    const uint32_t last = max(bars.issued[0][threadIdx.x], bars.issued[1][threadIdx.x]);
+    if (last > 0)
+      mbar_wait_bounded(&bars.full[threadIdx.x], ((last - 1) / kStages) & 1, a.status);
+  }
 }
 
 template <int D, bool PAIR, bool CAP, bool BIAS>
