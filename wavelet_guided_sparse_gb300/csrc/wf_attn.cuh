@@ -154,6 +154,7 @@ struct WorkShape {
   int max_len;        // table_pages * page_size
   int n_new, window, sinks;  // window: query rows of a sequence, its sizes
   const int32_t* tree_len;   // tree: nullable, nodes of each sequence (default n_new)
+  int pad;                   // tree: what a unit costs beside its tiles, in tiles
 };
 
 // A sequence's length clamped into the table (a longer one is flagged by the
@@ -166,7 +167,7 @@ __device__ __forceinline__ int seq_len_clamped(const WorkShape& w, const int32_t
   return nodes == 0 || len < nodes ? 0 : len;
 }
 
-// Tiles of a sequence of `len` keys.  Tile sizes are powers of two.
+// Tiles of `keys` keys.  Tile sizes are powers of two.
 __device__ __forceinline__ int tiles_up(const WorkShape& w, int keys) {
   return (keys + w.tile - 1) >> w.tile_shift;
 }
@@ -194,9 +195,12 @@ __device__ __forceinline__ bool box_needed(const WorkShape& w, const Span& x, in
                                            int rows) {
   return key < len && (MASK != kMaskWindow || key < w.sinks || key + rows > x.low);
 }
+// Tiles of a sequence of `len` keys in the line.  A tree's units have w.pad empty
+// ones behind their own: many short units cost their CTAs more than their tiles.
 template <int MASK = kMaskPlain>
 __device__ __forceinline__ int tiles_of(const WorkShape& w, int len) {
-  return tiles_up(w, len) - span_of<MASK>(w, len).gap;
+  const int n = tiles_up(w, len) - span_of<MASK>(w, len).gap;
+  return MASK == kMaskTree && n > 0 ? n + w.pad : n;
 }
 
 // Tiles of the whole call.  Whole warp.
@@ -244,7 +248,7 @@ struct WorkSplit {
 };
 
 // A unit: its sequence and length, its index within the sequence, its tiles
-// and the first of them.
+// (with the pad behind them) and the first of them.
 struct WorkUnit {
   int seq, len, unit, tiles;
   int64_t begin;
@@ -350,10 +354,16 @@ __device__ __forceinline__ void idle_sequences(const PagedArgs& a, const WorkSha
 struct TreeNodes {
   int count;       // the sequence's nodes
   uint64_t up[2];
-  // Whole warp: ancestors of ancestors in six doublings.
+  __device__ __forceinline__ static int nodes(const WorkShape& w, int s) {
+    return w.tree_len != nullptr ? min(max(__ldg(w.tree_len + s), 0), w.n_new) : w.n_new;
+  }
+  // Whole warp: ancestors of ancestors in six doublings (not if only the count is
+  // wanted).
   __device__ __forceinline__ void read(const WorkShape& w, const PagedArgs& a, int s, int lane,
-                                       bool say) {
-    count = w.tree_len != nullptr ? min(max(__ldg(w.tree_len + s), 0), w.n_new) : w.n_new;
+                                       bool say, bool all = true) {
+    count = nodes(w, s);
+    up[0] = up[1] = 0;
+    if (!all) return;
     int next[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -415,6 +425,7 @@ inline PagedParams paged_params(const PagedArgs& a, const PagedPlan& plan) {
   p.w.window = a.window;
   p.w.sinks = a.sinks;
   p.w.tree_len = a.tree_len;
+  p.w.pad = plan.pad;
   p.o = score_opts(a.scale, a.softcap, a.causal, a.prefix, a.slopes);
   return p;
 }

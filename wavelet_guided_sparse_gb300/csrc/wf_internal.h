@@ -200,10 +200,11 @@ struct PagedArgs {
   int window, sinks;
   const int32_t *parents, *tree_len;      // tree_len nullable
 };
-// CTAs of the persistent grid, rows of a row block, keys of a tile and
-// workspace bytes of the partials: functions of the sizes and the device alone.
+// CTAs of the persistent grid, rows of a row block, keys of a tile, empty tiles
+// behind a unit's and workspace bytes of the partials: functions of the sizes and
+// the device alone.
 struct PagedPlan {
-  int ctas, row_block, tile;
+  int ctas, row_block, tile, pad;
   size_t part_bytes;
 };
 PagedPlan plan_paged(const PagedArgs& a, int sm_count);

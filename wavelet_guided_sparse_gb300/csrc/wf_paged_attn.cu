@@ -9,6 +9,7 @@ PagedPlan plan_paged(const PagedArgs& a, int sm_count) {
   const int rows = a.q_heads / a.kv_heads * a.n_new;
   p.row_block = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   p.tile = KT;
+  p.pad = 0;
   const int64_t units = static_cast<int64_t>(a.n_seqs) * a.kv_heads *
                         ((rows + p.row_block - 1) / p.row_block);
   const int64_t tiles =

@@ -770,7 +770,7 @@ __device__ __forceinline__ JoinUnit join_unit(const PagedParams& p, int ctas, in
   } else {
     x.u = find_unit<MASK>(p.w, p.a.kv_len, any ? w1 - 1 : 0);
   }
-  const int64_t end = x.u.begin + x.u.tiles;
+  const int64_t end = x.u.begin + x.u.tiles - (MASK == kMaskTree ? p.w.pad : 0);
   x.joins = any && x.u.begin >= w0 && end > w1;
   x.n = x.joins ? split.owner(end - 1) - x.c0 + 1 : 0;
   if (x.joins || blockIdx.y == 0) wait_for_primary();

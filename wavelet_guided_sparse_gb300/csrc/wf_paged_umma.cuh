@@ -82,16 +82,21 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, 
       : "memory");
 }
 
-// The part of a unit that a CTA holds: key tiles [j0, j1).
+// The part of a unit that a CTA holds: key tiles [j0, j1), none where only the
+// pad behind a unit's tiles lies in its range; `next`: where the next unit's begins.
 struct UnitPart {
   int j0, j1;
   bool all;
+  int64_t next;
 };
-__device__ __forceinline__ UnitPart unit_part(const WorkUnit& u, int64_t at, int64_t w1) {
+__device__ __forceinline__ UnitPart unit_part(const WorkShape& w, const WorkUnit& u, int64_t at,
+                                              int64_t w1) {
   UnitPart x;
+  const int tiles = u.tiles - w.pad;
+  x.next = min(w1, u.begin + u.tiles);
   x.j0 = static_cast<int>(at - u.begin);
-  x.j1 = static_cast<int>(min(w1, u.begin + u.tiles) - u.begin);
-  x.all = x.j0 == 0 && x.j1 == u.tiles;
+  x.j1 = max(x.j0, min(static_cast<int>(x.next - u.begin), tiles));
+  x.all = x.j0 == 0 && x.j1 == tiles;
   return x;
 }
 
@@ -239,15 +244,27 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         if (++st == kStages) st = 0;
       };
       for (int64_t at = w0; at < w1 && ok;) {
-        const UnitPart x = unit_part(u, at, w1);
+        const UnitPart x = unit_part(p.w, u, at, w1);
         const int n = x.j1 - x.j0, kvh = u.unit / p.row_blocks;
+        at = x.next;
+        if (n == 0) {
+          if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
+          continue;
+        }
         // Entries of the part's tiles i, i + 1, i + 2 (tile i is key tile j1 - 1 - i).
         const auto entry_of = [&](int i) { return i < n ? entry(x.j1 - 1 - i) : -1; };
         int e0 = entry_of(0), e1 = entry_of(1), e2 = entry_of(2);
-        if (keys && units > 0)
-          ok = warp_wait(&bars.q_empty, (units - 1) & 1, bars.wait, a.status);
+        // The queries' place is free only when the last part's last scores have been
+        // formed: keys first, but for the first part.
+        const auto first_keys = [&]() {
+          for (int i = 0; i < kAhead && i < n; ++i)
+            fill(true, x.j1 - 1 - i, i ? e1 : e0, kvh, steps);
+        };
+        if (units > 0) {
+          first_keys();
+          if (keys) ok = ok && warp_wait(&bars.q_empty, (units - 1) & 1, bars.wait, a.status);
+        }
         if (!ok) break;
-        ++units;
         if (keys && leader) {
           const int nt = tiles_with_rows(u);
           const int node0 = (u.unit % p.row_blocks) * Shape::kQueryTiles * tp.tile_nodes;
@@ -258,7 +275,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                           u.seq * a.n_new + node0 + t * tp.tile_nodes, &bars.q);
         }
         __syncwarp();
-        for (int i = 0; i < kAhead && i < n; ++i) fill(true, x.j1 - 1 - i, i ? e1 : e0, kvh, steps);
+        if (units++ == 0) first_keys();
         for (int i = 0; i < n && ok; ++i) {
           fill(false, x.j1 - 1 - i, e0, kvh, steps + i);
           if (i + kAhead < n && ok)
@@ -268,7 +285,6 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           e2 = entry_of(i + 3);
         }
         steps += n;
-        at += n;
         if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
       }
       if (leader) {
@@ -327,8 +343,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       };
       uint32_t used[2] = {0, 0}, np[2] = {0, 0}, step = 0, units = 0;
       for (int64_t at = w0; at < w1 && ok;) {
-        const UnitPart x = unit_part(u, at, w1);
+        const UnitPart x = unit_part(p.w, u, at, w1);
         const int n = x.j1 - x.j0, nt = tiles_with_rows(u);
+        at = x.next;
+        if (n == 0) {
+          if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
+          continue;
+        }
         const auto keys = [&](int i) { return u.len - (x.j1 - 1 - i) * kTileRows; };
         ok = warp_wait(&bars.q, units++ & 1, bars.wait, a.status);
         for (int i = 0; i < kAhead && i < n && ok; ++i) {
@@ -366,7 +387,6 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           if (leader) umma_commit(&bars.done[step & 7]);
           ++step;
         }
-        at += n;
         if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
       }
       // Every product, and every arrival it still owes, ends before tensor
@@ -390,8 +410,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     uint32_t ns = 0, no[2] = {0, 0}, fills = 0, tiles = 0, units = 0;
     bool ok = true;
     for (int64_t at = w0; at < w1;) {
-      const UnitPart x = unit_part(u, at, w1);
+      const UnitPart x = unit_part(p.w, u, at, w1);
       const int n = x.j1 - x.j0, nt = tiles_with_rows(u);
+      at = x.next;
+      if (n == 0) {
+        if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
+        continue;
+      }
       const int len = u.len, kvh = u.unit / p.row_blocks;
       const int row0 = (u.unit % p.row_blocks) * RT;
       // This thread's row: its node and head, whether it exists and has a node.
@@ -400,7 +425,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const bool there = row < rows;
       const int node = there ? r / g : 0, head = kvh * g + (there ? r - node * g : 0);
       TreeNodes tree;
-      tree.read(p.w, a, u.seq, lane, warp == 4);
+      // A part that ends before the drafted rows needs to know only how many there
+      // are (a distance bias: their depths).
+      tree.read(p.w, a, u.seq, lane, warp == 4,
+                BIAS || x.j1 * kTileRows > len - tree.nodes(p.w, u.seq));
       const bool live = there && node < tree.count;
       const bool warp_live = __any_sync(0xffffffffu, live);
       const int base = len - tree.count;
@@ -563,7 +591,6 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       // The fills' order: K_0 .. K_{L-1}, then V_i and K_{i+L}.
       fills += 2 * n;
       tiles += n;
-      at += n;
       const bool two = !PAIR && n > 1;  // both groups have summed up keys
       if (PAIR ? t < nt : true) {
 #pragma unroll
