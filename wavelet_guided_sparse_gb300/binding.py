@@ -2,7 +2,8 @@
 
 Argument marshalling only: torch tensors supply device memory and the current
 CUDA stream; every step of the path runs in the library's CUDA kernels.  If
-the library has not been built, :func:`lib` raises; there is no fallback.
+the library has not been built, :func:`lib` raises; there is no fallback.  The
+checks of drafted trees, windows and pages are compiled (``csrc/wf_torch.cpp``).
 """
 
 from __future__ import annotations
@@ -173,6 +174,30 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
         _LIB = handle
     return _LIB
+
+
+_CALLS = None
+
+
+def _calls():
+    """The compiled marshalling module (raises if it was not built)."""
+    global _CALLS
+    if _CALLS is None:
+        lib()
+        try:
+            from wavelet_guided_sparse_gb300 import _wf_torch
+        except ImportError as e:
+            raise RuntimeError("wavelet_guided_sparse_gb300/_wf_torch.so is missing: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        _CALLS = _wf_torch
+    return _CALLS
+
+
+def _result(fn: str, r):
+    """What a compiled call returned: its results, or a status that is not WF_OK."""
+    if type(r) is int:
+        _check(fn, r)
+    return r
 
 
 def _check(fn: str, status: int) -> None:
@@ -587,6 +612,8 @@ class _On:
             raise ValueError("expected CUDA tensors")
         self.ctx = None
         if stream is not None:
+            if stream.device != t.device:
+                raise ValueError(f"stream is on {stream.device}, tensors on {t.device}")
             self.ctx = torch.cuda.stream(stream)
         elif torch._C._cuda_getDevice() != t.device.index:
             self.ctx = torch.cuda.device(t.device)
@@ -800,25 +827,11 @@ def paged_window_attn(q: torch.Tensor, cache: dict, page_table: torch.Tensor, kv
     positions away (behind a query, and before it if not ``causal``) and of the
     first ``sinks`` ones only.  Pages that no query sees need not be there."""
     with _On(q, stream):
-        if q.dim() != 4:
-            raise ValueError("q must be [n_seqs, n_new, q_heads, head_dim]")
-        dev, dt = q.device, q.dtype
-        shape, table, kp, vp, tp = _pages(cache, page_table, dt, dev)
-        n, n_new, hq, d = q.shape
-        qp = _need(q, "q", (table[0], n_new, hq, shape[3]), dt, dev)
-        opts = _attn_opts(causal, None, softcap, slopes, scale, n, hq, dev)
         if ws is None:
             ws = alloc_paged_attn_workspace(q, cache, page_table, stream)
-        wp, wn = _ws_args(ws, dev)
-        o = _out(out, "out", (n, n_new, hq, d), dt, dev)
-        lse = torch.empty((n, n_new, hq), dtype=torch.float32, device=dev) if with_lse else None
-        _check("wf_paged_window_attn", lib().wf_paged_window_attn(
-            _page_dims(n, hq, shape[1], d, shape[2], shape[0], table[1], dt)[1],
-            ctypes.byref(opts), _reach(window, "window", 1), _reach(sinks, "sinks", 0), n_new, qp,
-            kp, vp, tp,
-            _need(kv_len, "kv_len", (n,), torch.int32, dev), o.data_ptr(),
-            None if lse is None else lse.data_ptr(), wp, wn, _raw_stream(dev, stream)))
-        return (o, lse) if with_lse else o
+        return _result("wf_paged_window_attn", _calls().paged_window(
+            q, cache["K"], cache["V"], page_table, kv_len, _reach(window, "window", 1),
+            _reach(sinks, "sinks", 0), ws, causal, softcap, slopes, scale, out, with_lse))
 
 
 def paged_tree_attn(q: torch.Tensor, cache: dict, page_table: torch.Tensor, kv_len: torch.Tensor,
@@ -834,26 +847,11 @@ def paged_tree_attn(q: torch.Tensor, cache: dict, page_table: torch.Tensor, kv_l
     (and lse [n_seqs, n_nodes, q_heads] fp32 if ``with_lse``).  Append the nodes
     with positions[node] = rows before the tree + depth."""
     with _On(q, stream):
-        if q.dim() != 4:
-            raise ValueError("q must be [n_seqs, n_nodes, q_heads, head_dim]")
-        dev, dt = q.device, q.dtype
-        shape, table, kp, vp, tp = _pages(cache, page_table, dt, dev)
-        n, nodes, hq, d = q.shape
-        qp = _need(q, "q", (table[0], nodes, hq, shape[3]), dt, dev)
-        opts = _attn_opts(True, None, softcap, slopes, scale, n, hq, dev)
         if ws is None:
             ws = alloc_paged_tree_workspace(q, cache, page_table, stream)
-        wp, wn = _ws_args(ws, dev)
-        o = _out(out, "out", (n, nodes, hq, d), dt, dev)
-        lse = torch.empty((n, nodes, hq), dtype=torch.float32, device=dev) if with_lse else None
-        _check("wf_paged_tree_attn", lib().wf_paged_tree_attn(
-            _page_dims(n, hq, shape[1], d, shape[2], shape[0], table[1], dt)[1],
-            ctypes.byref(opts), nodes, qp, kp, vp, tp,
-            _need(kv_len, "kv_len", (n,), torch.int32, dev),
-            _need(parents, "parents", (n, nodes), torch.int32, dev),
-            _ints(tree_len, "tree_len", (n,), dev), o.data_ptr(),
-            None if lse is None else lse.data_ptr(), wp, wn, _raw_stream(dev, stream)))
-        return (o, lse) if with_lse else o
+        return _result("wf_paged_tree_attn", _calls().paged_tree(
+            q, cache["K"], cache["V"], page_table, kv_len, parents, ws, tree_len, softcap, slopes,
+            scale, out, with_lse))
 
 
 def prefill_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
@@ -899,27 +897,9 @@ def prefill_window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q:
     ``window`` positions away (behind a query, and before it if not ``causal``)
     and of the first ``sinks`` ones of a sequence only."""
     with _On(q, stream):
-        if q.dim() != 3 or k.dim() != 3:
-            raise ValueError("q, k and v must be [rows, heads, head_dim]")
-        dev, dt = q.device, q.dtype
-        t, hq, d = q.shape
-        tk, hkv = k.shape[0], k.shape[1]
-        qs = _row_stride(q, "q", t, hq, d, dt, dev)
-        ks = _row_stride(k, "k", tk, hkv, d, dt, dev)
-        vs = _row_stride(v, "v", tk, hkv, d, dt, dev)
-        docs = cu_q.numel() - 1
-        cq = _need(cu_q, "cu_q", (docs + 1,), torch.int32, dev)
-        ck = cq if cu_k is None else _need(cu_k, "cu_k", (docs + 1,), torch.int32, dev)
-        opts = _attn_opts(causal, None, softcap, slopes, scale, docs, hq, dev)
-        o = _out(out, "out", (t, hq, d), dt, dev)
-        lse = torch.empty((t, hq), dtype=torch.float32, device=dev) if with_lse else None
-        wp, wn = _ws_args(ws, dev)
-        _check("wf_prefill_window_attn", lib().wf_prefill_window_attn(
-            _prefill_dims(t, tk, docs, hq, hkv, d, dt)[1], ctypes.byref(opts),
-            _reach(window, "window", 1), _reach(sinks, "sinks", 0), q.data_ptr(), qs, k.data_ptr(),
-            ks, v.data_ptr(), vs, cq, ck, o.data_ptr(), None if lse is None else lse.data_ptr(),
-            wp, wn, _raw_stream(dev, stream)))
-        return (o, lse) if with_lse else o
+        return _result("wf_prefill_window_attn", _calls().prefill_window(
+            q, k, v, cu_q, cu_k, _reach(window, "window", 1), _reach(sinks, "sinks", 0), causal,
+            softcap, slopes, scale, out, with_lse, ws))
 
 
 # ---------------------------------------------------------------- pages
@@ -944,11 +924,9 @@ class PagePools:
         if k.dim() != 4 or not k.is_cuda:
             raise ValueError("pages must be CUDA tensors [n_pages, kv_heads, page_size, head_dim]")
         self.tensors = [c[n] for c in caches for n in ("K", "V")]   # kept alive
-        self.shape, self.dtype, self.device = k.shape, k.dtype, k.device
-        self.count = len(self.tensors)
-        self.pointers = (_vp * self.count)(*[
+        self.pointers = bytes((_vp * len(self.tensors))(*[
             _need(t, f"pages of layer {i // 2}", k.shape, k.dtype, k.device)
-            for i, t in enumerate(self.tensors)])
+            for i, t in enumerate(self.tensors)]))
 
 
 def page_pools(caches) -> PagePools:
@@ -958,17 +936,9 @@ def page_pools(caches) -> PagePools:
     return caches if isinstance(caches, PagePools) else PagePools(caches)
 
 
-def _page_call(shape, dtype, device, page_table: torch.Tensor):
-    """Dims argument of a call on pages, its sequences, and the table's address."""
-    if page_table.dim() != 2:
-        raise ValueError("the page table must be [n_seqs, table_pages]")
-    n, width = page_table.shape
-    return (_page_dims(n, shape[1], shape[1], shape[3], shape[2], shape[0], width, dtype)[1], n,
-            _need(page_table, "page_table", page_table.shape, torch.int32, device))
-
-
-def _ints(t: Optional[torch.Tensor], name: str, shape: tuple, device):
-    return None if t is None else _need(t, name, shape, torch.int32, device)
+def _layer(cache) -> torch.Tensor:
+    """One layer's key pages."""
+    return cache.tensors[0] if isinstance(cache, PagePools) else cache["K"]
 
 
 def alloc_pages_workspace(cache, page_table: torch.Tensor, max_forks: int = 0, max_keep: int = 0,
@@ -976,10 +946,14 @@ def alloc_pages_workspace(cache, page_table: torch.Tensor, max_forks: int = 0, m
     """Workspace of the calls on pages for at most max_forks forks and lists of
     max_keep rows (status word cleared); calls that may overlap need one each."""
     with _On(page_table, stream):
-        k = cache.tensors[0] if isinstance(cache, PagePools) else cache["K"]
+        k = _layer(cache)
+        if k.dim() != 4 or page_table.dim() != 2:
+            raise ValueError("pages must be [n_pages, kv_heads, page_size, head_dim], "
+                             "the page table [n_seqs, table_pages]")
         n = ctypes.c_size_t(0)
         _check("wf_pages_workspace_bytes", lib().wf_pages_workspace_bytes(
-            _page_call(k.shape, k.dtype, k.device, page_table)[0], max_forks, max_keep,
+            _page_dims(page_table.shape[0], k.shape[1], k.shape[1], k.shape[3], k.shape[2],
+                       k.shape[0], page_table.shape[1], k.dtype)[1], max_forks, max_keep,
             ctypes.byref(n)))
         ws = torch.empty(n.value, dtype=torch.uint8, device=k.device)
         _check("wf_clear_device_status", lib().wf_clear_device_status(
@@ -993,15 +967,9 @@ def paged_reserve(cache, page_table: torch.Tensor, refs: torch.Tensor, rows: tor
     first rows[s] rows where it has none, the lowest free ones of refs (in
     place).  ``cache``: one layer's {"K", "V"} (for the sizes) or page_pools()."""
     with _On(page_table, stream):
-        k = cache.tensors[0] if isinstance(cache, PagePools) else cache["K"]
-        dev = k.device
-        dims, n, tp = _page_call(k.shape, k.dtype, dev, page_table)
         if ws is None:
             ws = alloc_pages_workspace(cache, page_table, stream=stream)
-        wp, wn = _ws_args(ws, dev)
-        _check("wf_paged_reserve", lib().wf_paged_reserve(
-            dims, _ints(rows, "rows", (n,), dev), _ints(refs, "refs", (k.shape[0],), dev), tp, wp,
-            wn, _raw_stream(dev, stream)))
+        _check("wf_paged_reserve", _calls().reserve(_layer(cache), page_table, refs, rows, ws))
 
 
 def paged_fork(caches, page_table: torch.Tensor, refs: torch.Tensor, src: torch.Tensor,
@@ -1015,16 +983,10 @@ def paged_fork(caches, page_table: torch.Tensor, refs: torch.Tensor, src: torch.
     "V"}, a sequence of them, or page_pools()).  page_table and refs in place."""
     with _On(page_table, stream):
         pools = page_pools(caches)
-        dev, n_forks = pools.device, src.numel()
-        dims, n, tp = _page_call(pools.shape, pools.dtype, dev, page_table)
         if ws is None:
-            ws = alloc_pages_workspace(pools, page_table, max_forks=n_forks, stream=stream)
-        wp, wn = _ws_args(ws, dev)
-        _check("wf_paged_fork", lib().wf_paged_fork(
-            dims, n_forks, _ints(src, "src", (n_forks,), dev), _ints(dst, "dst", (n_forks,), dev),
-            _ints(kv_len, "kv_len", (n,), dev), _ints(share_rows, "share_rows", (n_forks,), dev),
-            _ints(refs, "refs", (pools.shape[0],), dev), tp, pools.count, pools.pointers, wp, wn,
-            _raw_stream(dev, stream)))
+            ws = alloc_pages_workspace(pools, page_table, max_forks=src.numel(), stream=stream)
+        _check("wf_paged_fork", _calls().fork(pools.pointers, pools.tensors[0], page_table, refs, src,
+                                              dst, kv_len, share_rows, ws))
 
 
 def paged_keep(caches, page_table: torch.Tensor, kv_len: torch.Tensor, start: torch.Tensor,
@@ -1038,19 +1000,11 @@ def paged_keep(caches, page_table: torch.Tensor, kv_len: torch.Tensor, start: to
     nothing behind start is kept; without refs no page is given back."""
     with _On(page_table, stream):
         pools = page_pools(caches)
-        dev = pools.device
-        dims, n, tp = _page_call(pools.shape, pools.dtype, dev, page_table)
-        if keep is not None and keep.dim() != 2:
-            raise ValueError("keep must be [n_seqs, max_keep]")
-        most = 0 if keep is None else keep.shape[1]
         if ws is None:
+            most = 0 if keep is None else keep.shape[-1]
             ws = alloc_pages_workspace(pools, page_table, max_keep=most, stream=stream)
-        wp, wn = _ws_args(ws, dev)
-        _check("wf_paged_keep", lib().wf_paged_keep(
-            dims, _ints(kv_len, "kv_len", (n,), dev), _ints(start, "start", (n,), dev),
-            _ints(keep, "keep", (n, most), dev), most, _ints(n_keep, "n_keep", (n,), dev),
-            _ints(refs, "refs", (pools.shape[0],), dev), tp, pools.count, pools.pointers, wp, wn,
-            _raw_stream(dev, stream)))
+        _check("wf_paged_keep", _calls().keep(pools.pointers, pools.tensors[0], page_table, refs,
+                                              kv_len, start, keep, n_keep, ws))
 
 
 def paged_release(cache, page_table: torch.Tensor, refs: torch.Tensor, first: torch.Tensor,
@@ -1059,13 +1013,8 @@ def paged_release(cache, page_table: torch.Tensor, refs: torch.Tensor, first: to
     [first[s], end[s]) are given back (0, 2^31 - 1: the whole sequence).
     ``cache``: one layer's {"K", "V"} (for the sizes) or page_pools()."""
     with _On(page_table, stream):
-        k = cache.tensors[0] if isinstance(cache, PagePools) else cache["K"]
-        dev = k.device
-        dims, n, tp = _page_call(k.shape, k.dtype, dev, page_table)
-        wp, wn = _ws_args(ws, dev)
-        _check("wf_paged_release", lib().wf_paged_release(
-            dims, _ints(first, "first", (n,), dev), _ints(end, "end", (n,), dev),
-            _ints(refs, "refs", (k.shape[0],), dev), tp, wp, wn, _raw_stream(dev, stream)))
+        _check("wf_paged_release",
+               _calls().release(_layer(cache), page_table, refs, first, end, ws))
 
 
 def raw_call(name: str, *args) -> int:

@@ -2,22 +2,27 @@
 
 Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel, then the
 objects are linked into one shared library next to this file.  Only the
-``compute_103a``/``sm_103a`` target is generated.
+``compute_103a``/``sm_103a`` target is generated.  ``csrc/wf_torch.cpp``, the
+compiled argument marshalling of the small calls, becomes the Python module
+``_wf_torch`` beside it (host code only, against the installed torch).
 """
 
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwavefilter.so")
+MODULE = os.path.join(PKG, "_wf_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
@@ -35,30 +40,58 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def _module_flags(nvcc: str):
+    """Include and link flags of the Python module."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    inc = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), cuda,
+           sysconfig.get_paths()["include"]]
+    return ([f for d in inc for f in ("-I", d)],
+            ["-L", PKG, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+             "-lc10_cuda", "-l:libwavefilter.so", "-Wl,-rpath,$ORIGIN"])
+
+
+def _run(what: str, cmd, verbose: bool) -> None:
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{res.stderr}")
+    if verbose and res.stderr:
+        sys.stderr.write(res.stderr)
+
+
 def build(verbose: bool = False, extra_flags=()) -> str:
     """Compile every kernel source and link ``libwavefilter.so``; returns its path."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
 
+    inc, link = _module_flags(nvcc)
+    marshal = os.path.join(BUILD, "wf_torch.o")
+
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        cmd = [nvcc, *ARCH, *FLAGS, *extra_flags, "-c", src, "-o", obj]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{res.stderr}")
-        if verbose and res.stderr:
-            sys.stderr.write(res.stderr)
+        _run(f"nvcc on {os.path.basename(src)}",
+             [nvcc, *ARCH, *FLAGS, *extra_flags, "-c", src, "-o", obj], verbose)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as pool:
+    def compile_module():
+        _run("g++ on wf_torch.cpp", ["g++", "-O2", "-std=c++17", "-fPIC", *inc, "-c",
+                                     os.path.join(CSRC, "wf_torch.cpp"), "-o", marshal], verbose)
+
+    # The longest units first.
+    srcs.sort(key=os.path.getsize, reverse=True)
+    srcs.sort(key=lambda f: "paged" not in os.path.basename(f))
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as pool:
+        host = pool.submit(compile_module)
         objs = list(pool.map(compile_one, srcs))
+        host.result()
     tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stderr}")
+    _run("link", [nvcc, *ARCH, "-shared", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)
+    tmp = MODULE + ".tmp"
+    _run("link of the module", ["g++", "-shared", "-o", tmp, marshal, *link], verbose)
+    os.replace(tmp, MODULE)
     return LIB
 
 
