@@ -580,6 +580,10 @@ int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_
                   const int32_t* kv_len, void* O, float* lse, void* workspace,
                   size_t workspace_bytes, void* stream);
 
+/* Bytes of workspace wf_paged_window_attn needs, as
+ * wf_paged_attn_workspace_bytes. */
+int wf_paged_window_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_new, size_t* bytes);
+
 /* The same over a sliding window (and the first tokens) of each cache: key j of
  * the query at position p counts when j < kv_len and (j < sinks or p - j <
  * window), and besides j <= p (causal), or j < sinks or j - p < window (not
@@ -589,7 +593,7 @@ int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_
  *                not looked at, so that their pages may be gone
  *                (wf_paged_release with first = sinks, end = kv_len - n_new -
  *                window + 1)
- *   workspace  : >= wf_paged_attn_workspace_bytes()
+ *   workspace  : >= wf_paged_window_attn_workspace_bytes()
  * Everything else as wf_paged_attn; values of rows that the window hides must
  * be finite where their page holds one that some query sees.  opts->prefix
  * must be NULL (WF_ERR_UNSUPPORTED). */

@@ -117,6 +117,30 @@ def test_window_edges_against_tiles(window, sinks):
                sinks, True, 0.0, False, seed=window + sinks)
 
 
+@pytest.mark.parametrize("new,hq,hkv,page,window,sinks,causal,cap,bias", [
+    (32, 40, 10, 16, 5000, 4, False, 0.0, False), (64, 32, 8, 64, 3000, 200, True, 0.0, True),
+    (5, 60, 15, 8, 4000, 64, True, 20.0, True), (1, 32, 8, 128, 6000, 130, True, 0.0, False),
+    (64, 40, 10, 256, 1000, 1, False, 30.0, False)])
+def test_window_of_many_tiles(new, hq, hkv, page, window, sinks, causal, cap, bias):
+    """Some tens of key tiles a CTA, in parts of several units."""
+    run_window(BF, 64, hq, hkv, page, [9000, 7111, 70, 5002, 8200, 0, 6400], new, window, sinks,
+               causal, cap, bias, seed=new)
+
+
+@pytest.mark.parametrize("new,hq,hkv", [(1, 4, 2), (20, 8, 2), (64, 16, 2)])
+def test_window_waits_that_run_out(new, hq, hkv):
+    cache, table = paged([900, 300], 16, hkv, 128, BF, 13)
+    t, q = i32(table.tolist()), randn((2, new, hq, 128), BF, 2)
+    ws = bd.alloc_paged_attn_workspace(q, cache, t)
+    call = lambda: bd.paged_window_attn(q, cache, t, i32([900, 300]), 250, ws, sinks=70)
+    ref = call()
+    bd.inject_wait_timeout(300)
+    call()
+    assert bd.read_device_status(ws) == bd.DEV_WAIT_TIMEOUT
+    bd.clear_device_status(ws)
+    assert torch.equal(call(), ref) and bd.read_device_status(ws) == 0
+
+
 def check_same(got, want, bounds, what):
     """Two results that each lie within `bounds` of the same exact ones."""
     for x, y, b, name in zip(got, want, bounds, ("O", "lse")):

@@ -38,7 +38,7 @@ EXPORTS = ("wf_status_string", "wf_last_error_string", "wf_default_k_per_level",
            "wf_step_basis",
            "wf_rope_inv_freq", "wf_paged_append", "wf_paged_attn_workspace_bytes",
            "wf_paged_attn", "wf_prefill_attn",
-           "wf_paged_window_attn", "wf_paged_tree_attn_workspace_bytes", "wf_paged_tree_attn",
+           "wf_paged_window_attn", "wf_paged_window_attn_workspace_bytes", "wf_paged_tree_attn_workspace_bytes", "wf_paged_tree_attn",
            "wf_prefill_window_attn",
            "wf_pages_workspace_bytes", "wf_paged_reserve", "wf_paged_fork", "wf_paged_keep",
            "wf_paged_release")
@@ -144,6 +144,7 @@ _SIGS = {
                                        _vp, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "wf_paged_window_attn": (ctypes.c_int, [_PDIMSP, _OPTSP, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
                                             _vp, _vp, _vp, _vp, _sz, _vp]),
+    "wf_paged_window_attn_workspace_bytes": (ctypes.c_int, [_PDIMSP, _i32, ctypes.POINTER(_sz)]),
     "wf_paged_tree_attn_workspace_bytes": (ctypes.c_int, [_PDIMSP, _i32, ctypes.POINTER(_sz)]),
     "wf_paged_tree_attn": (ctypes.c_int, [_PDIMSP, _OPTSP, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                                           _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -760,16 +761,18 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, cache: dict, page_table: torc
         return res
 
 
-def _attn_workspace(entry: str, q: torch.Tensor, cache: dict, page_table: torch.Tensor, stream):
+def _attn_workspace(entries, q: torch.Tensor, cache: dict, page_table: torch.Tensor, stream):
     with _On(q, stream):
         if q.dim() != 4:
             raise ValueError("q must be [n_seqs, n_new, q_heads, head_dim]")
         shape, table = _pages(cache, page_table, q.dtype, q.device)[:2]
-        n = ctypes.c_size_t(0)
-        _check(entry, getattr(lib(), entry)(
-            _page_dims(table[0], q.shape[2], shape[1], shape[3], shape[2], shape[0], table[1],
-                       q.dtype)[1], q.shape[1], ctypes.byref(n)))
-        ws = torch.empty(n.value, dtype=torch.uint8, device=q.device)
+        most, n = 0, ctypes.c_size_t(0)
+        for entry in entries:
+            _check(entry, getattr(lib(), entry)(
+                _page_dims(table[0], q.shape[2], shape[1], shape[3], shape[2], shape[0], table[1],
+                           q.dtype)[1], q.shape[1], ctypes.byref(n)))
+            most = max(most, n.value)
+        ws = torch.empty(most, dtype=torch.uint8, device=q.device)
         _check("wf_clear_device_status", lib().wf_clear_device_status(
             ws.data_ptr(), ws.numel(), _raw_stream(q.device, stream)))
         return ws
@@ -779,13 +782,14 @@ def alloc_paged_attn_workspace(q: torch.Tensor, cache: dict, page_table: torch.T
                                stream=None) -> torch.Tensor:
     """Workspace of paged_attn and paged_window_attn for these tensors' sizes
     (status word cleared); calls that may overlap need one each."""
-    return _attn_workspace("wf_paged_attn_workspace_bytes", q, cache, page_table, stream)
+    return _attn_workspace(("wf_paged_attn_workspace_bytes",
+                            "wf_paged_window_attn_workspace_bytes"), q, cache, page_table, stream)
 
 
 def alloc_paged_tree_workspace(q: torch.Tensor, cache: dict, page_table: torch.Tensor,
                                stream=None) -> torch.Tensor:
     """The same for paged_tree_attn."""
-    return _attn_workspace("wf_paged_tree_attn_workspace_bytes", q, cache, page_table, stream)
+    return _attn_workspace(("wf_paged_tree_attn_workspace_bytes",), q, cache, page_table, stream)
 
 
 def paged_attn(q: torch.Tensor, cache: dict, page_table: torch.Tensor, kv_len: torch.Tensor,

@@ -154,7 +154,7 @@ struct WorkShape {
   int max_len;        // table_pages * page_size
   int n_new, window, sinks;  // window: query rows of a sequence, its sizes
   const int32_t* tree_len;   // tree: nullable, nodes of each sequence (default n_new)
-  int pad;                   // tree: what a unit costs beside its tiles, in tiles
+  int pad;                   // masked forms: what a unit costs beside its tiles, in tiles
 };
 
 // A sequence's length clamped into the table (a longer one is flagged by the
@@ -195,12 +195,13 @@ __device__ __forceinline__ bool box_needed(const WorkShape& w, const Span& x, in
                                            int rows) {
   return key < len && (MASK != kMaskWindow || key < w.sinks || key + rows > x.low);
 }
-// Tiles of a sequence of `len` keys in the line.  A tree's units have w.pad empty
-// ones behind their own: many short units cost their CTAs more than their tiles.
+// Tiles of a sequence of `len` keys in the line.  The masked forms' units have
+// w.pad empty ones behind their own: many short units cost their CTAs more than
+// their tiles.
 template <int MASK = kMaskPlain>
 __device__ __forceinline__ int tiles_of(const WorkShape& w, int len) {
   const int n = tiles_up(w, len) - span_of<MASK>(w, len).gap;
-  return MASK == kMaskTree && n > 0 ? n + w.pad : n;
+  return MASK != kMaskPlain && n > 0 ? n + w.pad : n;
 }
 
 // Tiles of the whole call.  Whole warp.

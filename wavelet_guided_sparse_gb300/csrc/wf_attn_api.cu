@@ -299,14 +299,18 @@ int wf_paged_window_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int
   wf::PagedArgs a;
   int st = check_window(opts, window, sinks);
   if (st != WF_OK) return st;
-  st = paged_call(wf::plan_paged, dims, opts, n_new, Q, K_pages, V_pages, page_table, kv_len, O, lse, workspace,
+  st = paged_call(wf::plan_paged_window, dims, opts, n_new, Q, K_pages, V_pages, page_table, kv_len, O, lse, workspace,
                   workspace_bytes, &a);
   if (st != WF_OK) return st;
   // So large a window hides nothing; positions minus it stay within 32 bits.
   a.window = std::min(window, INT32_MAX - 512);
   a.sinks = sinks;
-  return cuda_status(wf::launch_paged_window(a, wf::plan_paged(a, wf::device_sm_count()),
+  return cuda_status(wf::launch_paged_window(a, wf::plan_paged_window(a, wf::device_sm_count()),
                                              static_cast<cudaStream_t>(stream)));
+}
+
+int wf_paged_window_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_new, size_t* bytes) {
+  return paged_bytes(dims, n_new, wf::plan_paged_window, bytes);
 }
 
 int wf_paged_tree_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_nodes, size_t* bytes) {

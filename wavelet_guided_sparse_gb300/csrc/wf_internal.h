@@ -210,6 +210,7 @@ struct PagedPlan {
 PagedPlan plan_paged(const PagedArgs& a, int sm_count);
 cudaError_t launch_paged_attn(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
 // With a window, and of a drafted tree (wf_paged_window.cu, wf_paged_tree.cu).
+PagedPlan plan_paged_window(const PagedArgs& a, int sm_count);
 cudaError_t launch_paged_window(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
 PagedPlan plan_paged_tree(const PagedArgs& a, int sm_count);
 cudaError_t launch_paged_tree(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);

@@ -208,7 +208,19 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
     int row0 = 0, rows = 0, kvh = 0;
     bool ok = true;
     if (w0 < w1) read_entries(u, w0);
+    const auto advance = [&](int64_t at) {  // to the tile behind `at`
+      if (at + 1 >= w1) return;
+      if (at + 1 == u.begin + u.tiles) {
+        next_unit<MASK>(p.w, a.kv_len, u);
+        span = span_of<MASK>(p.w, u.len);
+      }
+      read_entries(u, at + 1);
+    };
     for (int64_t at = w0; at < w1; ++at) {
+      if (MASK != kMaskPlain && at >= u.begin + u.tiles - p.w.pad) {  // the unit's empty ones
+        advance(at);
+        continue;
+      }
       // A unit's query rows arrive with its first tile: the runs of rows that
       // one query's heads (or a part of them) form, one bulk copy each.
       const bool first = at == w0 || at == u.begin;
@@ -277,13 +289,7 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         st = 0;
         phase ^= 1;
       }
-      if (at + 1 < w1) {
-        if (at + 1 == u.begin + u.tiles) {
-          next_unit<MASK>(p.w, a.kv_len, u);
-          span = span_of<MASK>(p.w, u.len);
-        }
-        read_entries(u, at + 1);
-      }
+      advance(at);
     }
     // No copy may land after the CTA has gone, also where the consumers have
     // given up behind this warp's last wait.
@@ -316,7 +322,13 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
     uint32_t phase = 0;
     bool ok = true;
     for (int64_t at = w0; at < w1;) {
-      const int64_t end = min(w1, u.begin + u.tiles);
+      const int64_t last = u.begin + u.tiles - (MASK != kMaskPlain ? p.w.pad : 0);
+      const int64_t end = min(w1, last);
+      if (MASK != kMaskPlain && at >= end) {  // the unit's empty tiles
+        at = min(w1, u.begin + u.tiles);
+        if (at < w1) next_unit<MASK>(p.w, a.kv_len, u);
+        continue;
+      }
       const int len = u.len;
       const int prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + u.seq) : 0;
       const int kvh = u.unit / p.row_blocks;
@@ -375,7 +387,7 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
 
       const int tiles = static_cast<int>(end - at);
       const int tile0 = static_cast<int>(at - u.begin);
-      at = end;
+      at = MASK != kMaskPlain ? min(w1, u.begin + u.tiles) : end;
       // Keys from `shut` up to below `open` are visible to every row of the warp.
       int open = min(limit[0], limit[1]), shut = max(low[0], low[1]);
 #pragma unroll
@@ -690,7 +702,7 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         }
       }
       named_bar_sync(1, kConsumerThreads);
-      const bool all = end == u.begin + u.tiles && end - u.tiles >= w0;
+      const bool all = end == last && u.begin >= w0;
       // A partial: slot 2c when the unit began before this CTA, else 2c + 1.
       float* part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (u.begin >= w0 ? 1 : 0)) *
                                  RT * (D + 2);
@@ -770,7 +782,7 @@ __device__ __forceinline__ JoinUnit join_unit(const PagedParams& p, int ctas, in
   } else {
     x.u = find_unit<MASK>(p.w, p.a.kv_len, any ? w1 - 1 : 0);
   }
-  const int64_t end = x.u.begin + x.u.tiles - (MASK == kMaskTree ? p.w.pad : 0);
+  const int64_t end = x.u.begin + x.u.tiles - (MASK != kMaskPlain ? p.w.pad : 0);
   x.joins = any && x.u.begin >= w0 && end > w1;
   x.n = x.joins ? split.owner(end - 1) - x.c0 + 1 : 0;
   if (x.joins || blockIdx.y == 0) wait_for_primary();
@@ -972,8 +984,9 @@ cudaError_t launch_tc_rows(const PagedArgs& a, const PagedPlan& plan, cudaStream
       !encode_tile_map(&p.tv, type, a.v_pages, 2, dims, strides, box))
     return cudaErrorInvalidValue;
   if (plan.row_block == 16) return launch_tc_opts<T, D, 1, MASK>(p, plan, stream);
-  // Trees of bf16 come here with a few rows, or with more than 128 (wf_paged_tree.cu).
-  if constexpr (MASK != kMaskTree || sizeof(T) == 4)
+  // The masked forms of bf16 come here with a few rows, or with more than 128
+  // (wf_paged_umma.cuh).
+  if constexpr (MASK == kMaskPlain || sizeof(T) == 4)
     if (plan.row_block == 32) return launch_tc_opts<T, D, 2, MASK>(p, plan, stream);
   return launch_tc_opts<T, D, 4, MASK>(p, plan, stream);
 }
@@ -1010,6 +1023,16 @@ template <typename T, int D, int MASK>
 cudaError_t launch_masked(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
   const cudaError_t e = launch_tc_rows<T, D, MASK>(a, plan, stream);
   return e != cudaSuccess ? e : launch_join<T, D, MASK>(a, plan, stream);
+}
+
+// The masked forms' plan: what a unit costs its CTA beside its tiles, in tiles of 64
+// keys (two CTAs an SM, one): one token in a window of 4096 over 64 sequences of 200
+// to 32768 keys 117 -> 104 us; with 3 and 4 the same, for short contexts more.  fp32
+// units take twice as long as bf16 ones with a CTA an SM.
+inline PagedPlan plan_masked(const PagedArgs& a, int sm_count) {
+  PagedPlan p = plan_paged(a, sm_count);
+  p.pad = p.ctas > sm_count ? 2 : 4;
+  return p;
 }
 
 template <int MASK>

@@ -1,9 +1,10 @@
-// Drafted trees over a paged cache on the fifth-generation tensor cores (bf16):
-// the split kernel for trees whose g n_nodes query rows would make the paged
-// mma.sync kernel (wf_paged_kernel.cuh) read a cache once for every 64 of them.
+// Drafted trees and sliding windows over a paged cache on the fifth-generation
+// tensor cores (bf16): the split kernel where a sequence's g n_new query rows would
+// make the paged mma.sync kernel (wf_paged_kernel.cuh) read its cache once for
+// every 64 of them, and wherever its warps take turns in adding up.
 //
-// A unit is a (sequence, key-value head, row block); a row is (node, query
-// head), node-major, so that a tile of 128 rows holds 128 / g nodes with all
+// A unit is a (sequence, key-value head, row block); a row is (node or new token,
+// query head), node-major, so that a tile of 128 rows holds 128 / g nodes with all
 // their heads (one tensor copy; fewer rows where g does not divide 128).  The
 // 128-key tiles of all units form the line of wf_attn.cuh, divided evenly over a
 // persistent grid; parts of split units are joined by the paged join kernel.
@@ -18,8 +19,9 @@
 // Products wait for keys ahead by one (PAIR) or two key tiles: K_0 .. K_{L-1},
 // then V_i and K_{i+L} for i = 0, 1, ...  Warp 0 issues every product, warp 1
 // the tensor copies of queries and keys, warp 2 those of values (whole pages or
-// 128-row parts of them), warp 3 sees to idle sequences.  Keys run from a part's last tile to its first: the drafted rows,
-// the only ones with a mask, come first.  Weights, maximum and roundings as in
+// 128-row parts of them), warp 3 sees to idle sequences.  Keys run from a part's last tile to its first (the line of a
+// window's key tiles has a gap behind the first tokens), so that the drafted rows,
+// a tree's only ones with a mask, come first.  Weights, maximum and roundings as in
 // wf_prefill.cu.
 //
 // Rows behind a sequence's end and rows of bad pages get weights of exactly 0,
@@ -100,6 +102,14 @@ __device__ __forceinline__ UnitPart unit_part(const WorkShape& w, const WorkUnit
   return x;
 }
 
+// Keys from the first of tile j of the line on that count: up to the sequence's
+// end, or the first tokens'.
+template <int MASK>
+__device__ __forceinline__ int tile_keys(const WorkShape& w, const Span& x, int len, int j) {
+  if (MASK == kMaskWindow && x.gap > 0 && j < x.first) return w.sinks - j * kTileRows;
+  return len - x.place(j) * kTileRows;
+}
+
 // Bits of an ancestor mask for the 32 keys from `rel` nodes behind (before, if
 // negative) the first drafted row on; rows before it are seen by all.
 __device__ __forceinline__ uint32_t tree_bits(uint64_t up, int rel) {
@@ -115,7 +125,7 @@ __device__ __forceinline__ uint32_t box_bits(int valid, int c, int box_shift) {
   return bits;
 }
 
-template <int D, bool PAIR, bool CAP, bool BIAS>
+template <int D, bool PAIR, int MASK, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kUmmaThreads, 1)
     paged_umma_kernel(const __grid_constant__ UmmaParams tp) {
   using Shape = UmmaShape<D, PAIR>;
@@ -158,9 +168,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     prefetch_tensormap(&tp.tk);
     prefetch_tensormap(&tp.tv);
   }
-  const WorkSplit split(work_total<kMaskTree>(p.w, a.kv_len), gridDim.x);
+  const WorkSplit split(work_total<MASK>(p.w, a.kv_len), gridDim.x);
   const int64_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
-  WorkUnit u = find_unit<kMaskTree>(p.w, a.kv_len, w0);
+  WorkUnit u = find_unit<MASK>(p.w, a.kv_len, w0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kUmmaIssueRegs));
     const bool leader = elect_one();
     if (warp == 3) {
-      idle_sequences<__nv_bfloat16, kMaskTree>(a, p.w, blockIdx.x, gridDim.x, lane, 32);
+      idle_sequences<__nv_bfloat16, MASK>(a, p.w, blockIdx.x, gridDim.x, lane, 32);
     } else if (warp > 0) {
       // ---- copies: lane = (box, column block) of a stage.  Both warps walk all
       // fills; warp 1 issues queries and keys, warp 2 values.
@@ -193,10 +203,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       uint32_t step_of[kStages] = {};  // the step that frees each stage
       uint32_t mine[kStages] = {};     // this warp's last fill of each, plus 1
       int st = 0;
-      // This lane's page-table entry for key tile j (-1: nothing to copy).
+      Span span = span_of<MASK>(p.w, u.len);
+      // First row of this lane's box of tile j of the line, and its page-table entry
+      // (-1: nothing to copy).
+      const auto box_key = [&](int j) { return span.place(j) * kTileRows + box * tp.box_rows; };
       const auto entry = [&](int j) {
-        const int key = j * kTileRows + box * tp.box_rows;
-        return box < boxes && j >= 0 && key < u.len
+        const int key = box_key(j);
+        return box < boxes && box_needed<MASK>(p.w, span, u.len, key, tp.box_rows)
                    ? __ldg(a.table + static_cast<int64_t>(u.seq) * a.table_pages +
                            (key >> tp.page_shift))
                    : -1;
@@ -210,10 +223,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             ok = ok && warp_wait(&bars.done[r & 7], (r >> 3) & 1, bars.wait, a.status);
           }
           if (!ok) return;
-          const int key = j * kTileRows + box * tp.box_rows;
+          const int key = box_key(j);
           const unsigned live = __ballot_sync(
               0xffffffffu, static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages));
-          if (!((live >> lane) & 1) && box < boxes && key < u.len)
+          if (!((live >> lane) & 1) && box < boxes &&
+              box_needed<MASK>(p.w, span, u.len, key, tp.box_rows))
             raise_flag(a.status, WF_DEV_BAD_INDEX);
           const bool issue = !(inject && fills == 0);
           if (lane == 0 && issue) {
@@ -243,12 +257,16 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         ++fills;
         if (++st == kStages) st = 0;
       };
+      const auto to_next = [&]() {
+        next_unit<MASK>(p.w, a.kv_len, u);
+        span = span_of<MASK>(p.w, u.len);
+      };
       for (int64_t at = w0; at < w1 && ok;) {
         const UnitPart x = unit_part(p.w, u, at, w1);
         const int n = x.j1 - x.j0, kvh = u.unit / p.row_blocks;
         at = x.next;
         if (n == 0) {
-          if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
+          if (at < w1) to_next();
           continue;
         }
         // Entries of the part's tiles i, i + 1, i + 2 (tile i is key tile j1 - 1 - i).
@@ -285,7 +303,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           e2 = entry_of(i + 3);
         }
         steps += n;
-        if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
+        if (at < w1) to_next();
       }
       if (leader) {
         if (keys && units > 0) mbar_wait_bounded(&bars.q, (units - 1) & 1, a.status);
@@ -347,10 +365,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         const int n = x.j1 - x.j0, nt = tiles_with_rows(u);
         at = x.next;
         if (n == 0) {
-          if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
+          if (at < w1) next_unit<MASK>(p.w, a.kv_len, u);
           continue;
         }
-        const auto keys = [&](int i) { return u.len - (x.j1 - 1 - i) * kTileRows; };
+        const Span span = span_of<MASK>(p.w, u.len);
+        const auto keys = [&](int i) { return tile_keys<MASK>(p.w, span, u.len, x.j1 - 1 - i); };
         ok = warp_wait(&bars.q, units++ & 1, bars.wait, a.status);
         for (int i = 0; i < kAhead && i < n && ok; ++i) {
           const int ks = arrived();
@@ -387,7 +406,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           if (leader) umma_commit(&bars.done[step & 7]);
           ++step;
         }
-        if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
+        if (at < w1) next_unit<MASK>(p.w, a.kv_len, u);
       }
       // Every product, and every arrival it still owes, ends before tensor
       // memory is freed and the CTA goes.
@@ -414,7 +433,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const int n = x.j1 - x.j0, nt = tiles_with_rows(u);
       at = x.next;
       if (n == 0) {
-        if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
+        if (at < w1) next_unit<MASK>(p.w, a.kv_len, u);
         continue;
       }
       const int len = u.len, kvh = u.unit / p.row_blocks;
@@ -424,16 +443,31 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const int rows = min(tp.tile_rows, g * a.n_new - row0 - (PAIR ? t * tp.tile_rows : 0));
       const bool there = row < rows;
       const int node = there ? r / g : 0, head = kvh * g + (there ? r - node * g : 0);
+      const Span span = span_of<MASK>(p.w, len);
+      // Tree: the ancestors of this row's node among the drafted rows, from `base`
+      // on.  Window: the row sees keys from `low` up to `limit`, and the first ones.
       TreeNodes tree;
-      // A part that ends before the drafted rows needs to know only how many there
-      // are (a distance bias: their depths).
-      tree.read(p.w, a, u.seq, lane, warp == 4,
-                BIAS || x.j1 * kTileRows > len - tree.nodes(p.w, u.seq));
-      const bool live = there && node < tree.count;
+      uint64_t up = 0;
+      int base = len, low = 0, limit = len, first_keys = 0, pos;
+      bool live = there;
+      if constexpr (MASK == kMaskTree) {
+        // A part that ends before the drafted rows needs to know only how many there
+        // are (a distance bias: their depths).
+        base = len - tree.nodes(p.w, u.seq);
+        tree.read(p.w, a, u.seq, lane, warp == 4, BIAS || x.j1 * kTileRows > base);
+        live = there && node < tree.count;
+        up = tree.ancestors(node);
+        pos = base + tree.depth(node);
+      } else {
+        pos = len - a.n_new + node;
+        if (there) {
+          if (p.o.causal) limit = min(len, max(pos + 1, 0));
+          low = pos - p.w.window + 1;
+          first_keys = min(p.w.sinks, limit);
+          if (!p.o.causal && p.w.window < len - pos) limit = pos + p.w.window;
+        }
+      }
       const bool warp_live = __any_sync(0xffffffffu, live);
-      const int base = len - tree.count;
-      const uint64_t up = tree.ancestors(node);
-      const int pos = base + tree.depth(node);
       ScoreMap map;
       if (CAP || BIAS) {
         map.scale = pack2(p.o.scale, p.o.scale);
@@ -456,12 +490,18 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         if (!ok) break;
         ++ns;
         tc_fence_after();
-        const int k0 = (x.j1 - 1 - i) * kTileRows;
+        const int k0 = span.place(x.j1 - 1 - i) * kTileRows;
         const int valid = *reinterpret_cast<volatile int*>(&bars.valid[(tiles + i) & 7]);
-        const bool edge = valid != kAllValid || k0 + kTileRows > base;
+        const bool edge =
+            valid != kAllValid ||
+            (MASK == kMaskTree
+                 ? k0 + kTileRows > base
+                 : __any_sync(0xffffffffu, k0 + kTileRows > limit || k0 < low));
         const bool first = PAIR ? i == 0 : i == t;
         const auto seen = [&](int c) {
-          uint32_t bits = tree_bits(up, k0 + c - base);
+          uint32_t bits = MASK == kMaskTree
+                              ? tree_bits(up, k0 + c - base)
+                              : seen_keys<true>(limit - k0 - c, low - k0 - c, first_keys - k0 - c);
           if (valid != kAllValid) bits &= box_bits(valid, c, box_shift);
           return bits;
         };
@@ -486,7 +526,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             tmem_ld32(s_addr + c, w);
             float* s = reinterpret_cast<float*>(w);
             const float d0 = static_cast<float>(pos - k0 - c);
-            if (BIAS && k0 + c + 32 > base) {
+            if (MASK == kMaskTree && BIAS && k0 + c + 32 > base) {
               // Drafted keys stand at their nodes' depths.
               if (CAP) map_scores<CAP, false>(s, p.o, map, d0, 1);
 #pragma unroll
@@ -496,7 +536,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 s[e] = fmaf(s[e], CAP ? 1.f : mul, -map.slope * fabsf(static_cast<float>(away)));
               }
             } else {
-              map_scores<CAP, BIAS>(s, p.o, map, d0, 1);  // every row lies behind these keys
+              // A tree's rows lie behind these keys.
+              const int side = MASK == kMaskTree || !BIAS               ? 1
+                               : __all_sync(0xffffffffu, d0 >= 31.f) ? 1
+                               : __all_sync(0xffffffffu, d0 <= 0.f)  ? -1 : 0;
+              map_scores<CAP, BIAS>(s, p.o, map, d0, side);
             }
             if (edge) hide_keys(s, seen(c));
             const float mc = chunk_max<32>(s);
@@ -570,7 +614,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         l += a0 + a1;
         // Value rows behind the sequence's end, up to the product's, and those of
         // boxes without a page.
-        const int rows_end = min(kTileRows, (len - k0 + 15) & ~15);
+        const int rows_end = min(
+            kTileRows, (tile_keys<MASK>(p.w, span, len, x.j1 - 1 - i) + 15) & ~15);
         if (len - k0 < rows_end || valid != kAllValid) {
           const uint32_t f = fills + (i < n - kAhead ? i + kAhead : n) + i;
           ok = warp_wait(&bars.full[f % kStages], (f / kStages) & 1, bars.wait, a.status);
@@ -705,7 +750,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             a.lse[heads0 + node * a.q_heads + head - kvh * g] = row_lse(m, l);
         }
       }
-      if (at < w1) next_unit<kMaskTree>(p.w, a.kv_len, u);
+      if (at < w1) next_unit<MASK>(p.w, a.kv_len, u);
     }
   }
   __syncwarp();  // the issuing lanes rejoin their warps
@@ -722,27 +767,27 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   }
 }
 
-template <int D, bool PAIR, bool CAP, bool BIAS>
+template <int D, bool PAIR, int MASK, bool CAP, bool BIAS>
 cudaError_t launch_umma(const UmmaParams& p, const PagedPlan& plan, cudaStream_t stream) {
-  const cudaError_t e = ensure_max_smem<paged_umma_kernel<D, PAIR, CAP, BIAS>>();
+  const cudaError_t e = ensure_max_smem<paged_umma_kernel<D, PAIR, MASK, CAP, BIAS>>();
   if (e != cudaSuccess) return e;
-  paged_umma_kernel<D, PAIR, CAP, BIAS>
+  paged_umma_kernel<D, PAIR, MASK, CAP, BIAS>
       <<<plan.ctas, kUmmaThreads, UmmaShape<D, PAIR>::kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <int D, bool PAIR>
+template <int D, bool PAIR, int MASK>
 cudaError_t launch_umma_opts(const UmmaParams& p, const PagedPlan& plan, cudaStream_t stream) {
   const bool bias = p.p.o.slopes != nullptr;
   if (p.p.o.cap > 0.f)
-    return bias ? launch_umma<D, PAIR, true, true>(p, plan, stream)
-                : launch_umma<D, PAIR, true, false>(p, plan, stream);
-  return bias ? launch_umma<D, PAIR, false, true>(p, plan, stream)
-              : launch_umma<D, PAIR, false, false>(p, plan, stream);
+    return bias ? launch_umma<D, PAIR, MASK, true, true>(p, plan, stream)
+                : launch_umma<D, PAIR, MASK, true, false>(p, plan, stream);
+  return bias ? launch_umma<D, PAIR, MASK, false, true>(p, plan, stream)
+              : launch_umma<D, PAIR, MASK, false, false>(p, plan, stream);
 }
 
-template <int D>
-cudaError_t launch_umma_tree(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
+template <int D, int MASK>
+cudaError_t launch_umma_dim(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
   UmmaParams p;
   const int g = a.q_heads / a.kv_heads;
   p.p = paged_params(a, plan);
@@ -767,9 +812,44 @@ cudaError_t launch_umma_tree(const PagedArgs& a, const PagedPlan& plan, cudaStre
       !encode_tile_map(&p.tk, kType, a.k_pages, 2, dims, strides, box) ||
       !encode_tile_map(&p.tv, kType, a.v_pages, 2, dims, strides, box))
     return cudaErrorInvalidValue;
-  const cudaError_t e = a.n_new > p.tile_nodes ? launch_umma_opts<D, true>(p, plan, stream)
-                                               : launch_umma_opts<D, false>(p, plan, stream);
-  return e != cudaSuccess ? e : launch_join<__nv_bfloat16, D, kMaskTree>(a, plan, stream);
+  const cudaError_t e = a.n_new > p.tile_nodes ? launch_umma_opts<D, true, MASK>(p, plan, stream)
+                                               : launch_umma_opts<D, false, MASK>(p, plan, stream);
+  return e != cudaSuccess ? e : launch_join<__nv_bfloat16, D, MASK>(a, plan, stream);
+}
+
+// More rows than this a key head run here (bf16; groups of up to 128 heads, a node
+// of which fits a tile).  Up to four rows the warps of the other kernel add up in
+// one go: trees over four sequences of 300 to 1500 keys 14.6 us against 18 here,
+// but 24.8 against 18.9 for 16 rows; 16 sequences of 6800 keys 87 against 83.
+constexpr int kFewRows = 4;
+// What a unit costs its CTA beside its tiles (queries, output, the gap in the
+// products), in tiles: about 2 us against 1.6 a tile, 6 with two row tiles.  Trees
+// over 16 sequences of 1000 to 16384 keys: 101 -> 95 us.
+constexpr int kPadOne = 1, kPadPair = 3;
+inline bool on_umma(const PagedArgs& a) {
+  const int g = a.q_heads / a.kv_heads;
+  return a.dtype == WF_BF16 && g <= kTileRows && g * a.n_new > kFewRows;
+}
+
+inline PagedPlan plan_umma(const PagedArgs& a, int sm_count) {
+  PagedPlan p;
+  const int g = a.q_heads / a.kv_heads, nodes = kTileRows / g;
+  p.row_block = a.n_new > nodes ? 2 * nodes * g : kTileRows;
+  p.tile = kTileRows;
+  p.pad = a.n_new > nodes ? kPadPair : kPadOne;
+  const int64_t units = static_cast<int64_t>(a.n_seqs) * a.kv_heads *
+                        ((g * a.n_new + p.row_block - 1) / p.row_block);
+  const int64_t tiles =
+      units * ((static_cast<int64_t>(a.table_pages) * a.page_size + p.tile - 1) / p.tile);
+  p.ctas = static_cast<int>(std::min<int64_t>(sm_count, tiles));
+  p.part_bytes = static_cast<size_t>(p.ctas) * 2 * p.row_block * (a.head_dim + 2) * sizeof(float);
+  return p;
+}
+
+template <int MASK>
+cudaError_t launch_umma_mask(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream) {
+  return a.head_dim == 128 ? launch_umma_dim<128, MASK>(a, plan, stream)
+                           : launch_umma_dim<64, MASK>(a, plan, stream);
 }
 
 }  // namespace

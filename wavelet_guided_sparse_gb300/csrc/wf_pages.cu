@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
     total_need += sm.need[c];
     total_free += sm.free[c];
   }
+  if (total_need == 0 && !FORK) return;  // the same for all
   // The free pages by rank, as far as they are needed.
   for (int p = p0; p < p1 && free_before < total_need; p += 32 * kBatch) {
     int got[kBatch];
