@@ -17,6 +17,7 @@
 #pragma once
 
 #include <cmath>
+#include <utility>
 
 #include "wf_common.cuh"
 #include "wf_internal.h"
@@ -132,6 +133,24 @@ __device__ __forceinline__ void launch_dependents() {
 }
 __device__ __forceinline__ void wait_for_primary() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Launches a kernel that may start while the stream's last one still runs, whatever
+// that is: it touches global memory only behind wait_for_primary().  Hides the
+// launch and its setup, 1 to 2 us of a short call.
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int block, size_t smem,
+                                cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 // ---------------------------------------------------------------- paged work list

@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kThreads) prefill_fma_kernel(PrefillParams p) 
   const PrefillArgs& a = p.a;
   const int g = a.q_heads / a.kv_heads;
   const int kvh = blockIdx.y;
+  if (WINDOW) wait_for_primary();
   if (blockIdx.x == 0 && kvh == 0) {
     check_offsets(a.cu_q, a.n_docs, a.rows_q, a.status, threadIdx.x, kThreads);
     check_offsets(a.cu_k, a.n_docs, a.rows_k, a.status, threadIdx.x, kThreads);
@@ -311,9 +312,11 @@ cudaError_t launch_prefill_typed(PrefillParams& p, cudaStream_t stream) {
   // row blocks.
   const int64_t most = std::max(1, 32 * device_sm_count() / p.a.kv_heads);
   p.capped = most < blocks;
-  prefill_fma_kernel<T, D, RT, WINDOW>
-      <<<dim3(static_cast<unsigned>(std::min(blocks, most)), p.a.kv_heads), kThreads, sizeof(FmaSmem<D, RT>),
-         stream>>>(p);
+  const dim3 grid(static_cast<unsigned>(std::min(blocks, most)), p.a.kv_heads);
+  if constexpr (WINDOW)
+    return launch_early(prefill_fma_kernel<T, D, RT, WINDOW>, grid, kThreads,
+                        sizeof(FmaSmem<D, RT>), stream, p);
+  prefill_fma_kernel<T, D, RT, WINDOW><<<grid, kThreads, sizeof(FmaSmem<D, RT>), stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -167,6 +167,7 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
     bars.wait.init(inject ? tp.inject_polls : kWaitPolls);
     fence_mbar_init();
   }
+  if (MASK != kMaskPlain) wait_for_primary();
   const WorkSplit split(work_total<MASK>(p.w, a.kv_len), gridDim.x);
   const int64_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
   WorkUnit u = find_unit<MASK>(p.w, a.kv_len, w0);
@@ -883,6 +884,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8)
     masked_join_kernel(PagedParams p, int ctas, int RT, int by_unit) {
   const PagedArgs& a = p.a;
   const int g = a.q_heads / a.kv_heads;
+  launch_dependents();
   const JoinUnit x = join_unit<MASK>(p, ctas, RT, by_unit);
   if (!x.joins) return;
   const int n = x.n, kvh = x.u.unit / p.row_blocks;
@@ -952,6 +954,9 @@ cudaError_t launch_tc(const PagedTcParams& p, const PagedPlan& plan, cudaStream_
   using Shape = PagedShape<T, D, R>;
   const cudaError_t e = ensure_max_smem<paged_tc_kernel<T, D, R, MASK, CAP, BIAS>>();
   if (e != cudaSuccess) return e;
+  if constexpr (MASK != kMaskPlain)
+    return launch_early(paged_tc_kernel<T, D, R, MASK, CAP, BIAS>, dim3(plan.ctas),
+                        Shape::kThreadCount, Shape::kSmem, stream, p);
   paged_tc_kernel<T, D, R, MASK, CAP, BIAS>
       <<<plan.ctas, Shape::kThreadCount, Shape::kSmem, stream>>>(p);
   return cudaGetLastError();
@@ -1000,23 +1005,15 @@ cudaError_t launch_join(const PagedArgs& a, const PagedPlan& plan, cudaStream_t 
   const int64_t units = static_cast<int64_t>(a.n_seqs) * p.w.units_per_seq;
   const int by_unit = units < plan.ctas;
   const int x = by_unit ? static_cast<int>(units) : plan.ctas;
-  cudaLaunchConfig_t cfg = {};
   // About eight CTAs an SM in all; each loops over its share of the rows.
   const int most = MASK == kMaskPlain ? rows : (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  cfg.gridDim = dim3(x, std::max(1, std::min(most, 8 * device_sm_count() / x)));
-  cfg.blockDim = dim3(MASK == kMaskPlain ? kThreads : kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  const dim3 grid(x, std::max(1, std::min(most, 8 * device_sm_count() / x)));
   if constexpr (MASK == kMaskPlain)
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, MASK>, p, plan.ctas, plan.row_block,
-                              by_unit);
+    return launch_early(paged_join_kernel<T, D, MASK>, grid, kThreads, 0, stream, p, plan.ctas,
+                        plan.row_block, by_unit);
   else
-    return cudaLaunchKernelEx(&cfg, masked_join_kernel<T, D, MASK>, p, plan.ctas, plan.row_block,
-                              by_unit);
+    return launch_early(masked_join_kernel<T, D, MASK>, grid, kJoinThreads, 0, stream, p, plan.ctas,
+                        plan.row_block, by_unit);
 }
 
 template <typename T, int D, int MASK>

@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     prefetch_tensormap(&tp.tk);
     prefetch_tensormap(&tp.tv);
   }
+  wait_for_primary();
   const WorkSplit split(work_total<MASK>(p.w, a.kv_len), gridDim.x);
   const int64_t w0 = split.begin(blockIdx.x), w1 = split.begin(blockIdx.x + 1);
   WorkUnit u = find_unit<MASK>(p.w, a.kv_len, w0);
@@ -771,9 +772,8 @@ template <int D, bool PAIR, int MASK, bool CAP, bool BIAS>
 cudaError_t launch_umma(const UmmaParams& p, const PagedPlan& plan, cudaStream_t stream) {
   const cudaError_t e = ensure_max_smem<paged_umma_kernel<D, PAIR, MASK, CAP, BIAS>>();
   if (e != cudaSuccess) return e;
-  paged_umma_kernel<D, PAIR, MASK, CAP, BIAS>
-      <<<plan.ctas, kUmmaThreads, UmmaShape<D, PAIR>::kSmem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(paged_umma_kernel<D, PAIR, MASK, CAP, BIAS>, dim3(plan.ctas), kUmmaThreads,
+                      UmmaShape<D, PAIR>::kSmem, stream, p);
 }
 
 template <int D, bool PAIR, int MASK>

@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gw = me * kAllocWarps + warp, warps = ctas * kAllocWarps;
   launch_dependents();
+  wait_for_primary();
   if (FORK) {
     for (int i = threadIdx.x; i < kSeqWords; i += kAllocThreads)
       sm.is_src[i] = sm.once[i] = sm.twice[i] = 0;
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
 __global__ void __launch_bounds__(kThreads)
     copy_pages_kernel(const AllocArgs x, const PagePools pools, int row_chunks) {
   constexpr int kFly = 8;
+  launch_dependents();
   wait_for_primary();
   const PagesArgs& a = x.p;
   const int lane = threadIdx.x & 31;
@@ -314,6 +316,8 @@ __global__ void __launch_bounds__(kThreads)
 
 __global__ void __launch_bounds__(kThreads) release_kernel(const PagesArgs a, const int32_t* first,
                                                            const int32_t* end) {
+  launch_dependents();
+  wait_for_primary();
   for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
     const int lo = min(max(__ldg(first + s), 0), max_len(a));
     const int hi = min(max(__ldg(end + s), 0), max_len(a));
@@ -333,6 +337,7 @@ __global__ void __launch_bounds__(kPlanThreads) keep_plan_kernel(const KeepArgs 
   __shared__ int s_bad, s_shared, s_stay;
   const int threads = blockDim.x;
   launch_dependents();
+  wait_for_primary();
   for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
     __syncthreads();
     if (threadIdx.x == 0) s_bad = s_shared = 0;
@@ -407,6 +412,7 @@ __global__ void __launch_bounds__(kThreads)
     move_rows_kernel(const KeepArgs x, const PagePools pools, int row_chunks, int page_shift) {
   constexpr int kFly = 4, kSide = GROUP / kPiece, kStep = kFly * kSide;
   const PagesArgs& a = x.p;
+  launch_dependents();
   wait_for_primary();
   const int thread = GROUP == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int pieces = row_chunks / kPiece, heads = a.kv_heads;
@@ -475,37 +481,26 @@ __global__ void __launch_bounds__(kThreads)
 
 int row_chunks_of(const PagesArgs& a) { return a.head_dim * (a.dtype == WF_BF16 ? 2 : 4) / 16; }
 
-cudaLaunchConfig_t config(unsigned grid, unsigned block, cudaStream_t stream,
-                          cudaLaunchAttribute* attr, int cluster, bool dependent) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  if (cluster > 1) {
-    attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = cluster;
-    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
-  } else if (dependent) {
-    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr->val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
-  }
-  return cfg;
-}
-
-template <bool FORK>
-cudaError_t launch_alloc(const AllocArgs& x, cudaStream_t stream) {
-  const int ctas = x.p.n_pages <= kOneCta ? 1 : kAllocCluster;
-  cudaLaunchAttribute attr = {};
-  const cudaLaunchConfig_t cfg = config(ctas, kAllocThreads, stream, &attr, ctas, false);
-  return cudaLaunchKernelEx(&cfg, alloc_kernel<FORK>, x);
-}
-
 unsigned grid_of(int64_t blocks) {
   return static_cast<unsigned>(
       std::max<int64_t>(1, std::min<int64_t>(blocks, 8 * device_sm_count())));
+}
+
+// A pool of many pages takes a cluster.
+template <bool FORK>
+cudaError_t launch_alloc(const AllocArgs& x, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(x.p.n_pages <= kOneCta ? 1 : kAllocCluster);
+  cfg.blockDim = dim3(kAllocThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {cfg.gridDim.x, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = cfg.gridDim.x == 1 ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, alloc_kernel<FORK>, x);
 }
 
 }  // namespace
@@ -519,22 +514,19 @@ cudaError_t launch_fork(const AllocArgs& x, const PagePools& pools, cudaStream_t
   if (e != cudaSuccess) return e;
   const int64_t most =
       std::min<int64_t>(x.p.n_pages, static_cast<int64_t>(x.units) * x.p.table_pages);
-  cudaLaunchAttribute attr = {};
-  const cudaLaunchConfig_t cfg = config(grid_of(most * pools.n * x.p.kv_heads / kWarps + 1),
-                                        kThreads, stream, &attr, 1, true);
-  return cudaLaunchKernelEx(&cfg, copy_pages_kernel, x, pools, row_chunks_of(x.p));
+  return launch_early(copy_pages_kernel, dim3(grid_of(most * pools.n * x.p.kv_heads / kWarps + 1)),
+                      kThreads, 0, stream, x, pools, row_chunks_of(x.p));
 }
 
 cudaError_t launch_release(const PagesArgs& a, const int32_t* first, const int32_t* end,
                            cudaStream_t stream) {
-  release_kernel<<<grid_of(a.n_seqs), kThreads, 0, stream>>>(a, first, end);
-  return cudaGetLastError();
+  return launch_early(release_kernel, dim3(grid_of(a.n_seqs)), kThreads, 0, stream, a, first, end);
 }
 
 cudaError_t launch_keep(const KeepArgs& x, const PagePools& pools, cudaStream_t stream) {
-  keep_plan_kernel<<<grid_of(x.p.n_seqs), x.max_keep > kThreads ? kPlanThreads : kThreads, 0,
-                     stream>>>(x);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_early(keep_plan_kernel, dim3(grid_of(x.p.n_seqs)),
+                   x.max_keep > kThreads ? kPlanThreads : kThreads, 0, stream, x);
   if (e != cudaSuccess) return e;
   const int chunks = row_chunks_of(x.p);
   int shift = 0;
@@ -543,11 +535,11 @@ cudaError_t launch_keep(const KeepArgs& x, const PagePools& pools, cudaStream_t 
   const int64_t streams = static_cast<int64_t>(x.p.n_seqs) *
                           std::max(1, pools.n * x.p.kv_heads * (chunks / kPiece));
   const bool warps = x.max_keep <= 32;
-  cudaLaunchAttribute attr = {};
-  const cudaLaunchConfig_t cfg = config(grid_of(warps ? (streams + kWarps - 1) / kWarps : streams),
-                                        kThreads, stream, &attr, 1, true);
-  return warps ? cudaLaunchKernelEx(&cfg, move_rows_kernel<32>, x, pools, chunks, shift)
-               : cudaLaunchKernelEx(&cfg, move_rows_kernel<kThreads>, x, pools, chunks, shift);
+  const dim3 grid(grid_of(warps ? (streams + kWarps - 1) / kWarps : streams));
+  return warps ? launch_early(move_rows_kernel<32>, grid, kThreads, 0, stream, x, pools, chunks,
+                              shift)
+               : launch_early(move_rows_kernel<kThreads>, grid, kThreads, 0, stream, x, pools,
+                              chunks, shift);
 }
 
 }  // namespace wf

@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (WINDOW) wait_for_primary();
   const uint32_t tmem = bars.tmem;
   const uint32_t tS[2] = {tmem, tmem + 128};
   const uint32_t tO[2] = {tmem + 256, tmem + 256 + D};
@@ -747,6 +748,10 @@ cudaError_t launch_tc(PrefillTcParams& p, cudaStream_t stream) {
                         (p.pair_heads ? p.a.q_heads / 2 : p.a.q_heads);
   const int64_t blocks = std::min<int64_t>(items, kBlocksPerSm * device_sm_count());
   p.capped = blocks < items;
+  if constexpr (WINDOW)
+    return launch_early(prefill_tc_kernel<D, CAP, BIAS, WINDOW>,
+                        dim3(static_cast<unsigned>(blocks)), kPreThreads, PreShape<D>::kSmem,
+                        stream, p);
   prefill_tc_kernel<D, CAP, BIAS, WINDOW>
       <<<static_cast<unsigned>(blocks), kPreThreads, PreShape<D>::kSmem, stream>>>(p);
   return cudaGetLastError();
