@@ -261,18 +261,20 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
       const int entries = reserve_entries(x, u, false);
       int32_t* row = a.table + static_cast<int64_t>(u) * a.table_pages;
       for (int e0 = 0; e0 < entries; e0 += 32 * kBatch) {
-        int got[kBatch];
+        int got[kBatch], page[kBatch];
         read_batch(row, e0, entries, lane, 0, got);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const unsigned hits = __ballot_sync(0xffffffffu, got[k] < 0);
           const int r = rank + __popc(hits & ((1u << lane) - 1));
-          if (got[k] < 0 && r < total_free) {
-            const int page = x.list[r];
-            row[e0 + 32 * k + lane] = page;
-            a.refs[page] = 1;
-          }
+          page[k] = got[k] < 0 && r < total_free ? x.list[r] : -1;
           rank += __popc(hits);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (page[k] < 0) continue;
+          row[e0 + 32 * k + lane] = page[k];
+          a.refs[page[k]] = 1;
         }
       }
     }
