@@ -37,6 +37,7 @@
 // 91 %.  32 heads of keys, a block of 32 tokens, two sequences of 65536 keys:
 // 324 us, 98 %.  The same block over 8 heads of keys (128 rows, two row blocks),
 // 16 sequences of 8192 keys: 238 us, 33 % of one read.
+// A window of 4096 over 64 sequences of 200 to 32768 keys, one new token: 104 us, 86 %.
 // A few hundred keys: 14 us, of which the split kernel's code, tables and
 // first tile take 9 and the join 5.  fp32, 16 sequences of 8192 keys: 320 us,
 // 49 %, bound by the tf32 products (the FMA pipes took 783).

@@ -27,6 +27,15 @@
 // Rows behind a sequence's end and rows of bad pages get weights of exactly 0,
 // and their value rows, up to the product's end, are cleared in shared memory.
 // Query rows without a node compute something and are written as O = 0.
+//
+// Measured (32 query heads, 8 of keys, d = 128; bound by HBM, whose share is of one
+// read of the cache): trees of 26 nodes over 16 sequences of 1000 to 16384 keys 95
+// us, 68 %; of 64 nodes over four of 32768 keys 111 us, 72 %, with capped scores 160,
+// with cap and bias 198 (the scores' mapping); 26 nodes over one of 131072 keys 94
+// us, 84 %.  What is missing: 5 us to the first scores, 1.5 us an output (a CTA's
+// units follow one another), 6 us of join, and CTAs that end 5 us apart.  Up to 128
+// rows need 64 flops a byte, which one softmax group could not feed: the two groups
+// take 2900 cycles for two key tiles, 256 rows for one.
 #pragma once
 
 #include <algorithm>

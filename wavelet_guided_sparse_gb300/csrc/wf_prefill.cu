@@ -48,7 +48,9 @@
 // 2 x 128 x 128 scores and the two hand-overs between the roles fill the
 // rest.  A short sequence adds per item its first tile (2200 cycles, whose
 // masks cost twice) and the output (2700): packed prompts of 20 to 3000 rows
-// 194 us, 53 %.  With cap and bias the mapping of the scores (8 FMA results
+// 194 us, 53 %.  With a window of 4096: one prompt of 32768 rows 1450 us, 75 %; of
+// 1024 (ten key tiles an item, of which eight's worth is visible): 24 prompts of 20
+// to 8192 rows 325 us, 52 %.  With cap and bias the mapping of the scores (8 FMA results
 // each, at 128 a cycle and SM) lies on the same chain: 616 us for 8192 causal
 // rows, 2329 us (49 %) for 16384.
 #include <algorithm>
