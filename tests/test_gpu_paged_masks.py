@@ -365,6 +365,60 @@ def test_tree_captured_with_new_lengths(nodes, hq, hkv):
     assert bd.read_device_status(ws) == 0
 
 
+# ------------------------------------------------------------------ both
+def test_visible_nans_and_infinities_show_and_hidden_ones_do_not():
+    """A key that holds NaN shows in the rows that see it and in no other; an infinite
+    value in its column of the rows that see it (the column's other rows meet it with
+    weights of 0: values that a mask hides must be finite); a key of the opposite
+    sign of infinity weighs nothing."""
+    n, nodes, hq, hkv, d = 700, 24, 8, 2, 128
+    tree = [-1, 0, 1, -1] + [3] * 20
+    cache, table = paged([n], 16, hkv, d, BF, 21)
+    t, q = i32(table.tolist()), randn((1, nodes, hq, d), BF, 22).abs()
+    at = lambda row: (int(table[0, row // 16]), slice(None), row % 16)
+    base = n - nodes
+    cache["K"][at(base + 1)] = math.nan                 # node 1: seen by nodes 1 and 2
+    cache["V"][at(base + 3) + (5,)] = math.inf          # node 3: seen by itself and 4..
+    cache["K"][at(300)] = -math.inf                     # all rows: weight 0
+    o, lse = bd.paged_tree_attn(q, cache, t, i32([n]), i32([tree]), with_lse=True)
+    bad = torch.zeros(nodes, dtype=torch.bool, device="cuda")
+    bad[1:3] = True
+    assert lse[0, bad].isnan().all() and lse[0, ~bad].isfinite().all()
+    assert o[0, bad].isnan().all()
+    assert (o[0, 3:, :, 5] == math.inf).all()
+    assert o[0, ~bad][:, :, 6:].isfinite().all() and o[0, ~bad][:, :, :5].isfinite().all()
+    # A window that ends before them sees none of it.
+    w = bd.paged_window_attn(q[:, :8].contiguous(), cache, t, i32([base]), 200)
+    assert w.isfinite().all()
+    w = bd.paged_window_attn(q[:, :8].contiguous(), cache, t, i32([base + 3]), 100)
+    assert w[0, 7].isnan().all() and w[0, :6].isfinite().all()
+
+
+def test_two_streams_at_once():
+    calls, want = [], []
+    for s in range(2):
+        cache, table = paged([3000, 900, 2500], 16, 4, 128, BF, 31 + s)
+        t, lens = i32(table.tolist()), i32([3000, 900, 2500])
+        q = randn((3, 20, 16, 128), BF, 33 + s)
+        tree = i32([random_tree(20, np.random.default_rng(s + i)) for i in range(3)])
+        wt = bd.alloc_paged_tree_workspace(q, cache, t)
+        ww = bd.alloc_paged_attn_workspace(q, cache, t)
+        calls.append(lambda stream, q=q, cache=cache, t=t, lens=lens, tree=tree, wt=wt, ww=ww: (
+            bd.paged_tree_attn(q, cache, t, lens, tree, wt, stream=stream),
+            bd.paged_window_attn(q, cache, t, lens, 700, ww, sinks=9, stream=stream)))
+        want.append(calls[-1](None))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for s in range(2):
+            got[s].append(calls[s](streams[s]))
+    torch.cuda.synchronize()
+    for s in range(2):
+        for r in got[s]:
+            assert all(torch.equal(x, y) for x, y in zip(r, want[s]))
+
+
 # ------------------------------------------------------------------ a drafting step
 def test_append_verify_keep():
     """Drafted tokens filed at their depths, verified, the accepted path kept: the

@@ -182,6 +182,28 @@ def test_large_pools_take_the_lowest_pages_in_order():
     m.check()
 
 
+def test_captured_calls_on_a_large_pool():
+    m = Model(40000, 40, 3, 8, 1, 64, BF, 1, seed=14)
+    held = np.random.default_rng(3).permutation(40000)[:39000].tolist()
+    for p in held:
+        m.r[p] = 1
+    m.refs.copy_(i32(m.r))
+    rows, first, end = i32([300, 0, 77]), i32([0] * 3), i32([MAX] * 3)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bd.paged_reserve(m.caches[0], m.table, m.refs, rows, m.ws)
+        taken = m.table.clone()
+        bd.paged_release(m.caches[0], m.table, m.refs, first, end, m.ws)
+    free = [p for p in range(40000) if m.r[p] == 0]
+    want = [free[:38] + [-1] * 2, [-1] * 40, free[38:48] + [-1] * 30]
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert taken.tolist() == want
+        m.check()
+
+
 def test_too_few_pages():
     m = Model(10, 6, 3, 8, seed=4)
     m.reserve([40, 48, 0])                            # 5 + 6 of 10

@@ -33,9 +33,10 @@
 // us, 68 %; of 64 nodes over four of 32768 keys 111 us, 72 %, with capped scores 160,
 // with cap and bias 198 (the scores' mapping); 26 nodes over one of 131072 keys 94
 // us, 84 %.  What is missing: 5 us to the first scores, 1.5 us an output (a CTA's
-// units follow one another), 6 us of join, and CTAs that end 5 us apart.  Up to 128
-// rows need 64 flops a byte, which one softmax group could not feed: the two groups
-// take 2900 cycles for two key tiles, 256 rows for one.
+// units follow one another), 6 us of join, and CTAs that end 5 us apart.  A softmax
+// group takes about 2900 cycles a key tile of 128 rows, as long as HBM needs for its
+// copy: with 128 rows two groups on alternate tiles leave room for the waits between
+// the roles, with 256 they are the whole of it.
 #pragma once
 
 #include <algorithm>
