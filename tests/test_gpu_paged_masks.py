@@ -95,6 +95,8 @@ WINDOWS = [
     (BF, 128, 8, 2, 64, [600, 64, 33, 0], 64, 40, 0, True, 30.0, True),   # four blocks
     (BF, 64, 1, 1, 8, [3, 2], 8, 4, 2, True, 0.0, False),                 # rows before any key
     (BF, 64, 1, 1, 8, [3, 2], 8, 4, 1, False, 0.0, False),                # rows without a key
+    (BF, 64, 130, 1, 16, [700, 40], 2, 100, 3, True, 0.0, True),          # 130 heads a key head
+    (BF, 128, 6, 6, 16, [300, 0, 65], 3, 70, 2, True, 30.0, True),        # three rows a key head
     (BF, 128, 16, 1, 128, [2000], 1, 10 ** 12, 5, True, 0.0, False),      # all of it
     (BF, 128, 4, 1, 32, [2000, 40], 2, 300, 10 ** 12, True, 0.0, False),
     (F32, 64, 2, 2, 32, [1056, 4000], 32, 256, 64, False, 0.0, False),
@@ -269,6 +271,8 @@ TREES = [
                                              random_tree(1, RNG)], 0.0, False),
     (BF, 64, 32, 8, 8, [100, 2500], 50, [random_tree(50, RNG), random_tree(47, RNG)], 0.0, False),
     (BF, 128, 40, 1, 16, [777], 20, [random_tree(20, RNG)], 0.0, True),   # 800 rows a key head
+    (BF, 64, 130, 1, 16, [700, 40], 2, [[-1, 0], [-1, -1]], 20.0, True),  # 130 heads a key head
+    (BF, 128, 6, 6, 16, [300, 0, 65], 3, [[-1, 0, 0], [], [-1, -1]], 30.0, True),  # three rows
     (F32, 64, 2, 2, 32, [1056, 13], 13, [random_tree(13, RNG), random_tree(13, RNG)], 0.0, False),
     (F32, 128, 4, 1, 16, [5, 0, 333], 5, [random_tree(5, RNG), random_tree(5, RNG),
                                           random_tree(3, RNG)], 30.0, True),
@@ -392,6 +396,16 @@ def test_visible_nans_and_infinities_show_and_hidden_ones_do_not():
     assert w.isfinite().all()
     w = bd.paged_window_attn(q[:, :8].contiguous(), cache, t, i32([base + 3]), 100)
     assert w[0, 7].isnan().all() and w[0, :6].isfinite().all()
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (2, 2)])
+def test_many_sequences_with_idle_ones_between(hq, hkv):
+    rng = np.random.default_rng(hq)
+    lens = [int(rng.integers(0, 300)) if rng.random() < 0.6 else 0 for _ in range(150)]
+    run_window(BF, 64, hq, hkv, 8, lens, 2, 70, 5, True, 0.0, False, seed=hq)
+    lens = [n and max(n, 4) for n in lens]
+    run_tree(BF, 64, hq, hkv, 8, lens, 4, [random_tree(int(rng.integers(1, 5)), rng) if n else []
+                                           for n in lens], 0.0, False, seed=hq)
 
 
 def test_two_streams_at_once():

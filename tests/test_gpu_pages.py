@@ -204,6 +204,36 @@ def test_captured_calls_on_a_large_pool():
         m.check()
 
 
+def test_pools_past_32_bit_offsets():
+    """More than 2^31 elements a pool: rows at its far end are copied and moved."""
+    page, hkv, d = 256, 8, 128
+    pages = (1 << 31) // (page * hkv * d) + 40
+    cache = {x: torch.empty((pages, hkv, page, d), dtype=BF, device="cuda") for x in "KV"}
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for x in cache.values():
+        x[-12:].normal_(generator=g)
+    refs = torch.ones(pages, dtype=torch.int32, device="cuda")
+    table = bd.alloc_page_table(2, 6, "cuda")
+    refs[-12:] = 0
+    ws = bd.alloc_pages_workspace(cache, table, max_forks=1, max_keep=600)
+    bd.paged_reserve(cache, table, refs, i32([1300, 0]), ws)
+    assert table[0].tolist() == list(range(pages - 12, pages - 6))
+    bd.paged_fork(cache, table, refs, i32([0]), i32([1]), i32([1300, 0]), i32([0]), ws)
+    assert table[1].tolist() == list(range(pages - 6, pages))
+    rows = {x: [t[table[s].long()].transpose(1, 2).flatten(0, 1)[:1300].clone() for s in (0, 1)]
+            for x, t in cache.items()}
+    for x in rows.values():
+        assert torch.equal(x[0], x[1])
+    kept = sorted(np.random.default_rng(2).choice(1300, 600, replace=False).tolist())
+    bd.paged_keep(cache, table, i32([1300, 1300]), i32([0, 1300]), i32([kept, [0] * 600]),
+                  i32([600, 0]), refs, ws)
+    assert bd.read_device_status(ws) == 0 and (refs[-12:] == 0).sum() == 3
+    for x, t in cache.items():
+        got = t[table[0, :3].long()].transpose(1, 2).flatten(0, 1)[:600]
+        assert torch.equal(got, rows[x][0][kept])
+        assert torch.equal(t[table[1].long()].transpose(1, 2).flatten(0, 1)[:1300], rows[x][1])
+
+
 def test_too_few_pages():
     m = Model(10, 6, 3, 8, seed=4)
     m.reserve([40, 48, 0])                            # 5 + 6 of 10
