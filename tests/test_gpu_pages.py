@@ -182,6 +182,20 @@ def test_large_pools_take_the_lowest_pages_in_order():
     m.check()
 
 
+@pytest.mark.parametrize("pages", [12000, 20000])
+def test_more_pages_at_once_than_one_list_holds(pages):
+    m = Model(pages, 1500, 5, 8, 1, 64, BF, 1, seed=pages)
+    held = np.random.default_rng(5).permutation(pages)[:1500].tolist()
+    for p in held:
+        m.r[p] = 1
+    m.refs.copy_(i32(m.r))
+    m.reserve([12000, 9001, 8, 11999, 0])             # 4127 pages: one CTA, a cluster
+    m.check()
+    m.release([8, 0, 0, 16, 0], [11992, 0, MAX, 800, 0])
+    m.reserve([12000, 10000, 0, 0, 0])
+    m.check()
+
+
 def test_captured_calls_on_a_large_pool():
     m = Model(40000, 40, 3, 8, 1, 64, BF, 1, seed=14)
     held = np.random.default_rng(3).permutation(40000)[:39000].tolist()

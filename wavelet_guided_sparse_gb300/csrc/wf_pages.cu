@@ -9,8 +9,8 @@
 // alloc_kernel (reserve, fork) counts needs and free pages in one cluster,
 // each CTA and warp over a contiguous share of both, exchanges the counts
 // through distributed shared memory, lists the free pages by rank and fills
-// the entries from that list.  Up to kOneCta pages one CTA does it (no
-// cluster to gather: 1 us less), above that eight share the pass over refs.
+// the entries from that list.  Up to kOneCta pages one CTA does it, its list in
+// shared memory (2 us less), above that eight share the pass over refs.
 //
 // copy_pages_kernel moves what a fork copies: HBM-bound, each warp takes one
 // head's rows of a page (contiguous) of one pool and keeps eight 16-byte loads
@@ -24,10 +24,10 @@
 //
 // Measured (8 heads of keys, d = 128, bf16).  Four sequences of 16384 rows copied in
 // 4 layers: 338 us with the release, 92 % of the copy rate.  4096 of 32768 rows of
-// four sequences moved in 4 layers: 80 us, the copy rate (in one CTA a stream; its
-// plan 6 us before it, the reserve of the next rows 8).  Small calls are launches and
-// dependent loads: reserve and keep of 16 accepted paths in 8 layers 14 us, 32 forks
-// of shared pages in 8 layers with their release 15.
+// four sequences moved in 4 layers: 80 us, the copy rate (in one CTA a stream; with
+// plan and launches 94).  Small calls are launches and dependent loads: reserve and
+// keep of 16 accepted paths in 8 layers 13 us, 32 forks of shared pages in 8 layers
+// with their release 14.
 #include <algorithm>
 
 #include "wf_attn.cuh"
@@ -75,11 +75,13 @@ struct ForkUnit {
 };
 
 constexpr int kBatch = 8;  // loads of a lane that fly together
+constexpr int kLocalList = 4096;  // free pages that one CTA lists in shared memory
 
 struct AllocShared {
   uint32_t is_src[kSeqWords], once[kSeqWords], twice[kSeqWords];
   int warp_need[kAllocWarps], warp_free[kAllocWarps];
   int need[kAllocCluster], free[kAllocCluster];  // every CTA's totals
+  int list[kLocalList];                          // one CTA: its free pages by rank
 };
 
 __device__ __forceinline__ bool bit_of(const uint32_t* words, int i) {
@@ -156,6 +158,9 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
   const int u1 = static_cast<int>(static_cast<int64_t>(x.units) * (gw + 1) / warps);
   const int p0 = static_cast<int>(static_cast<int64_t>(a.n_pages) * gw / warps);
   const int p1 = static_cast<int>(static_cast<int64_t>(a.n_pages) * (gw + 1) / warps);
+  // This warp's first counts, kept: of a small pool all of them.
+  int refs0[kBatch];
+  read_batch(a.refs, p0, p1, lane, 1, refs0);
   int need = 0;
   for (int u = u0; u < u1; ++u) {
     if (lane == 0) x.base[u] = need;  // within the warp
@@ -176,7 +181,9 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
   int free = 0;
   for (int p = p0; p < p1; p += 32 * kBatch) {
     int got[kBatch];
-    read_batch(a.refs, p, p1, lane, 1, got);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) got[k] = refs0[k];
+    if (p != p0) read_batch(a.refs, p, p1, lane, 1, got);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) free += __popc(__ballot_sync(0xffffffffu, got[k] == 0));
   }
@@ -210,21 +217,29 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
   }
   if (total_need == 0 && !FORK) return;  // the same for all
   // The free pages by rank, as far as they are needed.
+  const bool local = ctas == 1 && total_need <= kLocalList;
+  int* list = local ? sm.list : x.list;
   for (int p = p0; p < p1 && free_before < total_need; p += 32 * kBatch) {
     int got[kBatch];
-    read_batch(a.refs, p, p1, lane, 1, got);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) got[k] = refs0[k];
+    if (p != p0) read_batch(a.refs, p, p1, lane, 1, got);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const unsigned hits = __ballot_sync(0xffffffffu, got[k] == 0);
       const int rank = free_before + __popc(hits & ((1u << lane) - 1));
-      if (got[k] == 0 && rank < total_need) x.list[rank] = p + 32 * k + lane;
+      if (got[k] == 0 && rank < total_need) list[rank] = p + 32 * k + lane;
       free_before += __popc(hits);
     }
   }
   if (total_need > total_free && gw == 0 && lane == 0) raise_flag(a.status, WF_DEV_NO_PAGE);
   if (FORK && gw == 0 && lane == 0) *x.n_copies = min(total_need, total_free);
-  __threadfence();
-  cluster.sync();
+  if (local) {
+    __syncthreads();
+  } else {
+    __threadfence();
+    cluster.sync();
+  }
   for (int u = u0; u < u1; ++u) {
     int rank = need_before + x.base[u];
     if (FORK) {
@@ -238,7 +253,7 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const int r = rank + e0 + 32 * k + lane - f.shared;
-          fresh[k] = r >= rank && e0 + 32 * k + lane < f.entries && r < total_free ? x.list[r] : -1;
+          fresh[k] = r >= rank && e0 + 32 * k + lane < f.entries && r < total_free ? list[r] : -1;
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
@@ -274,7 +289,7 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
         for (int k = 0; k < kBatch; ++k) {
           const unsigned hits = __ballot_sync(0xffffffffu, got[k] < 0);
           const int r = rank + __popc(hits & ((1u << lane) - 1));
-          page[k] = got[k] < 0 && r < total_free ? x.list[r] : -1;
+          page[k] = got[k] < 0 && r < total_free ? list[r] : -1;
           rank += __popc(hits);
         }
 #pragma unroll
@@ -350,6 +365,19 @@ __global__ void __launch_bounds__(kPlanThreads) keep_plan_kernel(const KeepArgs 
   for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
     __syncthreads();
     if (threadIdx.x == 0) s_bad = s_shared = 0;
+    const int32_t* keep = x.keep + static_cast<int64_t>(s) * x.max_keep;
+    const int32_t* row = a.table + static_cast<int64_t>(s) * a.table_pages;
+    // The list's first rows come in beside its length.
+    int from[kPlanBatch], prev[kPlanBatch];
+    const auto read_rows = [&](int i0) {
+#pragma unroll
+      for (int k = 0; k < kPlanBatch; ++k) {
+        const int i = i0 + k * threads;
+        from[k] = i < x.max_keep ? __ldg(keep + i) : -1;
+        prev[k] = i > 0 && i < x.max_keep ? __ldg(keep + i - 1) : -1;
+      }
+    };
+    read_rows(threadIdx.x);
     const int len = __ldg(x.kv_len + s), start = __ldg(x.start + s);
     const int n = x.n_keep != nullptr ? __ldg(x.n_keep + s) : 0;
     const bool sound = len >= 0 && len <= max_len(a) && start >= 0 && start <= len && n >= 0 &&
@@ -357,17 +385,10 @@ __global__ void __launch_bounds__(kPlanThreads) keep_plan_kernel(const KeepArgs 
     const int count = sound ? n : 0;
     if (threadIdx.x == 0) s_stay = count;
     __syncthreads();
-    const int32_t* keep = x.keep + static_cast<int64_t>(s) * x.max_keep;
-    const int32_t* row = a.table + static_cast<int64_t>(s) * a.table_pages;
     bool bad = !sound, shared = false;
     for (int i0 = threadIdx.x; i0 < count; i0 += threads * kPlanBatch) {
-      int from[kPlanBatch], prev[kPlanBatch], page[kPlanBatch], to[kPlanBatch];
-#pragma unroll
-      for (int k = 0; k < kPlanBatch; ++k) {
-        const int i = i0 + k * threads;
-        from[k] = i < count ? __ldg(keep + i) : -1;
-        prev[k] = i > 0 && i < count ? __ldg(keep + i - 1) : -1;
-      }
+      int page[kPlanBatch], to[kPlanBatch];
+      if (i0 != threadIdx.x) read_rows(i0);
       // from = -1: a row that stays (so do all before it), or none, or one that
       // breaks the rules.  An ascending list's row i is start + i or behind it, so
       // that start + i lies in the table too.
@@ -375,7 +396,10 @@ __global__ void __launch_bounds__(kPlanThreads) keep_plan_kernel(const KeepArgs 
       for (int k = 0; k < kPlanBatch; ++k) {
         const int i = i0 + k * threads;
         page[k] = to[k] = 0;
-        if (i >= count) continue;
+        if (i >= count) {
+          from[k] = -1;
+          continue;
+        }
         if (from[k] <= prev[k] || from[k] < start || from[k] - start < i || from[k] >= len) {
           bad = true;
           from[k] = -1;
