@@ -29,8 +29,8 @@
 // Query rows without a node compute something and are written as O = 0.
 //
 // Measured (32 query heads, 8 of keys, d = 128; bound by HBM, whose share is of one
-// read of the cache): trees of 26 nodes over 16 sequences of 1000 to 16384 keys 95
-// us, 68 %; of 64 nodes over four of 32768 keys 111 us, 72 %, with capped scores 160,
+// read of the cache): trees of 26 nodes over 16 sequences of 1000 to 16384 keys 88
+// us, 74 %; of 64 nodes over four of 32768 keys 111 us, 72 %, with capped scores 160,
 // with cap and bias 198 (the scores' mapping); 26 nodes over one of 131072 keys 94
 // us, 84 %.  What is missing: 5 us to the first scores, 1.5 us an output (a CTA's
 // units follow one another), 6 us of join, and CTAs that end 5 us apart.  A softmax
@@ -833,9 +833,10 @@ cudaError_t launch_umma_dim(const PagedArgs& a, const PagedPlan& plan, cudaStrea
 // but 24.8 against 18.9 for 16 rows; 16 sequences of 6800 keys 87 against 83.
 constexpr int kFewRows = 4;
 // What a unit costs its CTA beside its tiles (queries, output, the gap in the
-// products), in tiles: about 2 us against 1.6 a tile, 6 with two row tiles.  Trees
-// over 16 sequences of 1000 to 16384 keys: 101 -> 95 us.
-constexpr int kPadOne = 1, kPadPair = 3;
+// products and in its copies), in tiles.  Trees of 26 nodes over 16 sequences of 1000
+// to 16384 keys: 101 us without, 96, 93, 90, 88, 88 with 1 to 5; of 64 nodes over 24 of
+// 540 to 25890 keys: 232 without, 216, 205, 196 with 1 to 3, 199 with 5.
+constexpr int kPadOne = 4, kPadPair = 3;
 inline bool on_umma(const PagedArgs& a) {
   const int g = a.q_heads / a.kv_heads;
   return a.dtype == WF_BF16 && g <= kTileRows && g * a.n_new > kFewRows;
