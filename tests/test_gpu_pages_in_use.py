@@ -1,0 +1,168 @@
+"""GPU checks of calls on pages beside the attentions that read them: as a serving
+loop strings them together, captured and replayed, over windows that give back
+what they leave behind."""
+
+import numpy as np
+import pytest
+import torch
+
+from wavelet_guided_sparse_gb300 import binding as bd
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+MAX = 2 ** 31 - 1
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def randn(shape, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+def random_tree(n, rng):
+    return [-1] + [int(rng.integers(-1, i)) if rng.random() < 0.5 else i - 1 for i in range(1, n)]
+
+
+class Serving:
+    """Two sequences that draft and keep, and the child of one, over shared pages:
+    every tensor of a step is there before it, so that it can be captured."""
+    SEQS, NODES, PAGE, WIDTH, PAGES = 3, 7, 16, 40, 110
+    WINDOW, SINKS = 50, 5
+
+    def __init__(self, dtype, hq, hkv, d):
+        self.freq = bd.rope_inv_freq(d)
+        self.layers = [{x: randn((self.PAGES, hkv, self.PAGE, d), dtype, 10 * i + j)
+                        for j, x in enumerate("KV")} for i in range(2)]
+        self.pools = bd.page_pools(self.layers)
+        self.table = bd.alloc_page_table(self.SEQS, self.WIDTH, "cuda")
+        self.refs = bd.alloc_page_refs(self.PAGES, "cuda")
+        self.ws = bd.alloc_pages_workspace(self.pools, self.table, max_forks=1,
+                                           max_keep=self.NODES)
+        s, n = self.SEQS, self.NODES
+        self.k, self.v = torch.empty((2, 2 * n, hkv, d), dtype=dtype, device="cuda")
+        self.q = torch.empty((s, n, hq, d), dtype=dtype, device="cuda")
+        names = ("held", "grown", "drafted", "kept", "first", "end", "zero", "over")
+        self.i = {x: torch.zeros(s, dtype=torch.int32, device="cuda") for x in names}
+        self.i["over"].fill_(MAX)
+        self.cu, self.pos = i32([0, n, 2 * n, 2 * n]), i32([0] * (2 * n))
+        self.parents, self.lists = i32([[-1] * n] * s), i32([[0] * n] * s)
+        self.count, self.nodes = i32([0] * s), i32([n, n, 0])
+        self.src, self.dst = i32([0]), i32([2])
+        self.tree_ws = bd.alloc_paged_tree_workspace(self.q, self.layers[0], self.table)
+        self.token_ws = bd.alloc_paged_attn_workspace(self.q[:, :1].contiguous(), self.layers[0],
+                                                      self.table)
+        self.q1 = torch.empty((s, 1, hq, d), dtype=dtype, device="cuda")
+        self.tree, self.token = torch.empty_like(self.q), torch.empty_like(self.q1)
+
+    def fill(self, step, held):
+        """New drafts and lists for the two sequences; returns what they hold then."""
+        rng = np.random.default_rng(step)
+        n, s = self.NODES, self.SEQS
+        for x, seed in ((self.k, 1), (self.v, 2), (self.q, 3), (self.q1, 4)):
+            x.copy_(randn(x.shape, x.dtype, 100 * step + seed))
+        count = [int(rng.integers(1, n + 1)) for _ in range(2)]
+        lists = [sorted(rng.choice(n, c, replace=False).tolist()) for c in count]
+        total, kept = [h + n for h in held], [h + c for h, c in zip(held, count)]
+        self.i["held"].copy_(i32(held + [0]))
+        self.i["drafted"].copy_(i32(total + [0]))
+        self.i["kept"].copy_(i32(kept + [kept[0]]))
+        self.i["first"].copy_(i32([self.SINKS] * 2 + [0]))
+        self.i["end"].copy_(i32([m - self.WINDOW for m in kept] + [MAX]))
+        self.parents.copy_(i32([random_tree(n, rng) for _ in range(s)]))
+        self.pos.copy_(i32([h + int(rng.integers(0, 4)) for h in held for _ in range(n)]))
+        self.lists.copy_(i32([[h + r for r in x] + [0] * (n - len(x))
+                              for h, x in zip(held + [0], lists + [[]])]))
+        self.count.copy_(i32(count + [0]))
+        return kept
+
+    def step(self, pause=lambda: None):
+        def calls():
+            yield bd.paged_reserve(self.pools, self.table, self.refs, self.i["drafted"], self.ws)
+            for c in self.layers:
+                yield bd.paged_append(self.k, self.v, c, self.table, self.cu, self.i["held"],
+                                      inv_freq=self.freq, positions=self.pos, ws=self.ws)
+            yield bd.paged_tree_attn(self.q, self.layers[1], self.table, self.i["drafted"],
+                                     self.parents, self.tree_ws, tree_len=self.nodes,
+                                     out=self.tree)
+            yield bd.paged_keep(self.pools, self.table, self.i["drafted"], self.i["held"],
+                                self.lists, self.count, self.refs, self.ws)
+            yield bd.paged_fork(self.pools, self.table, self.refs, self.src, self.dst,
+                                self.i["kept"], ws=self.ws)
+            yield bd.paged_window_attn(self.q1, self.layers[0], self.table, self.i["kept"],
+                                       self.WINDOW, self.token_ws, sinks=self.SINKS,
+                                       out=self.token)
+            yield bd.paged_release(self.pools, self.table, self.refs, self.i["first"],
+                                   self.i["end"], self.ws)
+        for _ in calls():
+            pause()
+
+    def everything(self):
+        return [self.table, self.refs, self.tree, self.token, *self.pools.tensors]
+
+    def status(self):
+        return [bd.read_device_status(w) for w in (self.ws, self.tree_ws, self.token_ws)]
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [(BF, 8, 2, 128), (BF, 2, 2, 64), (F32, 4, 2, 64)])
+def test_a_captured_serving_loop_is_the_same_calls_one_by_one(dtype, hq, hkv, d):
+    """Kernels that follow one another at once, over tables, counts and rows that the last
+    one has just written, replayed with other lengths and lists."""
+    a, b = Serving(dtype, hq, hkv, d), Serving(dtype, hq, hkv, d)
+    held = [90, 33]
+    for x in (a, b):
+        for w in (x.tree_ws, x.token_ws):
+            w.zero_()
+    graph = torch.cuda.CUDAGraph()
+    a.fill(0, held)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        a.step()
+    for step in range(12):
+        a.fill(step, held)
+        kept = b.fill(step, held)
+        torch.cuda.synchronize()
+        graph.replay()
+        b.step(torch.cuda.synchronize)
+        torch.cuda.synchronize()
+        for x, y in zip(a.everything(), b.everything()):
+            assert torch.equal(x, y), step
+        held = kept
+        assert a.status() == b.status() == [0, 0, 0], step
+
+
+def test_captured_on_two_streams_that_meet():
+    """A call launched early behind an event of another stream waits for both."""
+    hkv, d, n = 2, 64, 300
+    cache = {x: randn((30, hkv, 16, d), BF, i) for i, x in enumerate("KV")}
+    table, lens = i32([list(range(25))]), i32([n])
+    q, new = randn((1, 6, 4, d), BF, 5), randn((2, 6, hkv, d), BF, 6)
+    tree = i32([[-1, 0, 0, 1, 2, 2]])
+    ws = bd.alloc_paged_tree_workspace(q, cache, table)
+    out, copy = torch.empty_like(q), torch.empty_like(q)
+    side = torch.cuda.Stream()
+
+    def calls():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):                # the last six rows, from the other stream
+            bd.paged_append(new[0], new[1], cache, table, i_cu, i_len)
+        copy.copy_(q)
+        here.wait_stream(side)
+        bd.paged_tree_attn(copy, cache, table, lens, tree, ws, out=out)
+
+    i_cu, i_len = i32([0, 6]), i32([n - 6])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for seed in range(5):
+        new.copy_(randn(new.shape, BF, 20 + seed))
+        q.copy_(randn(q.shape, BF, 40 + seed))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, bd.paged_tree_attn(q, cache, table, lens, tree))
+    assert bd.read_device_status(ws) == 0

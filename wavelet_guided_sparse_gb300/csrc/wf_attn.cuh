@@ -134,9 +134,24 @@ __device__ __forceinline__ void launch_dependents() {
 __device__ __forceinline__ void wait_for_primary() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+// How a kernel reads what an earlier one of its stream may write.  The read-only
+// path is for data that nothing writes while the kernel lives, and the compiler may
+// move such a load above a wait: a kernel launched early, which lives while the
+// last one still writes, reads by ordinary loads behind wait_for_primary().
+enum ReadKind : int {
+  kReadConst,    // ordinary launch: the read-only path
+  kReadOrdered,  // launched early, behind wait_for_primary()
+  kReadL2        // launched early, before it, of what was complete before: past L1
+};
+template <int READ, typename T>
+__device__ __forceinline__ T load_input(const T* p) {
+  if constexpr (READ == kReadConst) return __ldg(p);
+  if constexpr (READ == kReadL2) return __ldcg(p);
+  return *p;
+}
 // Launches a kernel that may start while the stream's last one still runs, whatever
-// that is: it touches global memory only behind wait_for_primary().  Hides the
-// launch and its setup, 1 to 2 us of a short call.
+// that is: it touches global memory only behind wait_for_primary(), by ordinary
+// loads.  Hides the launch and its setup, 1 to 2 us of a short call.
 template <typename... P, typename... A>
 inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int block, size_t smem,
                                 cudaStream_t stream, A&&... args) {
@@ -166,6 +181,8 @@ inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int block, size
 // A window leaves a gap between the tiles of the first tokens and those of the
 // window: it is not part of the line.
 enum PagedMask : int { kMaskPlain, kMaskWindow, kMaskTree };
+// The masked forms' split kernels are launched early.
+constexpr int read_of(int mask) { return mask == kMaskPlain ? kReadConst : kReadOrdered; }
 struct WorkShape {
   int n_seqs;
   int units_per_seq;  // kv_heads * row blocks
@@ -178,11 +195,13 @@ struct WorkShape {
 
 // A sequence's length clamped into the table (a longer one is flagged by the
 // caller); 0 also for one without nodes, or without rows for them.
-template <int MASK = kMaskPlain>
+template <int MASK = kMaskPlain, int READ = read_of(MASK)>
 __device__ __forceinline__ int seq_len_clamped(const WorkShape& w, const int32_t* lens, int s) {
-  const int len = min(max(__ldg(lens + s), 0), w.max_len);
+  const int len = min(max(load_input<READ>(lens + s), 0), w.max_len);
   if (MASK != kMaskTree) return len;
-  const int nodes = w.tree_len != nullptr ? min(max(__ldg(w.tree_len + s), 0), w.n_new) : w.n_new;
+  const int nodes = w.tree_len != nullptr
+                        ? min(max(load_input<READ>(w.tree_len + s), 0), w.n_new)
+                        : w.n_new;
   return nodes == 0 || len < nodes ? 0 : len;
 }
 
@@ -224,11 +243,11 @@ __device__ __forceinline__ int tiles_of(const WorkShape& w, int len) {
 }
 
 // Tiles of the whole call.  Whole warp.
-template <int MASK = kMaskPlain>
+template <int MASK = kMaskPlain, int READ = read_of(MASK)>
 __device__ __forceinline__ int64_t work_total(const WorkShape& w, const int32_t* lens) {
   int n = 0;  // fits: the host bounds n_seqs times the longest sequence's tiles
   for (int s = threadIdx.x & 31; s < w.n_seqs; s += 32)
-    n += tiles_of<MASK>(w, seq_len_clamped<MASK>(w, lens, s));
+    n += tiles_of<MASK>(w, seq_len_clamped<MASK, READ>(w, lens, s));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return static_cast<int64_t>(n) * w.units_per_seq;
@@ -275,14 +294,14 @@ struct WorkUnit {
 };
 // The unit that holds tile `at` (0 <= at < total).  Whole warp, 32 sequences
 // a step.
-template <int MASK = kMaskPlain>
+template <int MASK = kMaskPlain, int READ = read_of(MASK)>
 __device__ __forceinline__ WorkUnit find_unit(const WorkShape& w, const int32_t* lens,
                                               int64_t at) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   WorkUnit u = {0, 0, 0, 1, 0};
   for (int s0 = 0; s0 < w.n_seqs; s0 += 32) {
-    const int len = s0 + lane < w.n_seqs ? seq_len_clamped<MASK>(w, lens, s0 + lane) : 0;
+    const int len = s0 + lane < w.n_seqs ? seq_len_clamped<MASK, READ>(w, lens, s0 + lane) : 0;
     const int t = tiles_of<MASK>(w, len);
     const int incl = warp_incl_scan(t);
     const unsigned hit = __ballot_sync(
@@ -306,16 +325,16 @@ __device__ __forceinline__ WorkUnit find_unit(const WorkShape& w, const int32_t*
   return u;
 }
 // Unit `n` of all (idle sequences' counted; tiles = 0 for theirs).  Whole warp.
-template <int MASK = kMaskPlain>
+template <int MASK = kMaskPlain, int READ = read_of(MASK)>
 __device__ __forceinline__ WorkUnit nth_unit(const WorkShape& w, const int32_t* lens, int n) {
   WorkUnit u;
   u.seq = n / w.units_per_seq;
   u.unit = n - u.seq * w.units_per_seq;
-  u.len = seq_len_clamped<MASK>(w, lens, u.seq);
+  u.len = seq_len_clamped<MASK, READ>(w, lens, u.seq);
   u.tiles = tiles_of<MASK>(w, u.len);
   int before = 0;
   for (int s = threadIdx.x & 31; s < u.seq; s += 32)
-    before += tiles_of<MASK>(w, seq_len_clamped<MASK>(w, lens, s));
+    before += tiles_of<MASK>(w, seq_len_clamped<MASK, READ>(w, lens, s));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   u.begin = static_cast<int64_t>(before) * w.units_per_seq + static_cast<int64_t>(u.unit) * u.tiles;
@@ -349,10 +368,10 @@ template <typename T, int MASK = kMaskPlain>
 __device__ __forceinline__ void idle_sequences(const PagedArgs& a, const WorkShape& w, int c,
                                                int n, int thread, int threads) {
   for (int s = c; s < a.n_seqs; s += n) {
-    const int len = __ldg(a.kv_len + s);
+    const int len = load_input<read_of(MASK)>(a.kv_len + s);
     bool bad = len < 0 || len > w.max_len;
     if (MASK == kMaskTree) {
-      const int nodes = w.tree_len != nullptr ? __ldg(w.tree_len + s) : w.n_new;
+      const int nodes = w.tree_len != nullptr ? load_input<read_of(MASK)>(w.tree_len + s) : w.n_new;
       bad |= nodes < 0 || nodes > w.n_new || (len > 0 && len < nodes);
     }
     if (thread == 0 && bad) raise_flag(a.status, WF_DEV_BAD_INDEX);
@@ -368,14 +387,16 @@ __device__ __forceinline__ void idle_sequences(const PagedArgs& a, const WorkSha
   }
 }
 
-// The drafted tree of a sequence, two nodes a lane (node, node + 32): ancestors
+// The drafted tree of a sequence (a kernel launched early reads it), two nodes a lane (node, node + 32): ancestors
 // (with the node itself) as bits, depth.  A parent that does not come before its
 // child is flagged and taken for none.
 struct TreeNodes {
   int count;       // the sequence's nodes
   uint64_t up[2];
   __device__ __forceinline__ static int nodes(const WorkShape& w, int s) {
-    return w.tree_len != nullptr ? min(max(__ldg(w.tree_len + s), 0), w.n_new) : w.n_new;
+    return w.tree_len != nullptr
+               ? min(max(load_input<kReadOrdered>(w.tree_len + s), 0), w.n_new)
+               : w.n_new;
   }
   // Whole warp: ancestors of ancestors in six doublings (not if only the count is
   // wanted).
@@ -388,7 +409,9 @@ struct TreeNodes {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int node = lane + 32 * h;
-      next[h] = node < count ? __ldg(a.parents + static_cast<int64_t>(s) * w.n_new + node) : -1;
+      next[h] = node < count ? load_input<kReadOrdered>(
+                                   a.parents + static_cast<int64_t>(s) * w.n_new + node)
+                             : -1;
       if (next[h] >= node) {
         if (say) raise_flag(a.status, WF_DEV_BAD_INDEX);
         next[h] = -1;
@@ -466,18 +489,21 @@ struct DocBlock {
   int n_q, n_k;     // its rows and keys
   int64_t q0, k0;   // its first row and key
 };
+template <int READ = kReadConst>
 __device__ __forceinline__ int doc_span(const int32_t* cu, int i, int rows, int* first) {
-  const int a = min(max(__ldg(cu + i), 0), rows), b = min(max(__ldg(cu + i + 1), 0), rows);
+  const int a = min(max(load_input<READ>(cu + i), 0), rows);
+  const int b = min(max(load_input<READ>(cu + i + 1), 0), rows);
   *first = a;
   return max(b - a, 0);
 }
 // Row blocks of all sequences.  Whole warp.
+template <int READ = kReadConst>
 __device__ __forceinline__ int64_t doc_total(const PrefillArgs& a, int rows, int g) {
   int64_t n = 0;
 #pragma unroll 4
   for (int d = threadIdx.x & 31; d < a.n_docs; d += 32) {
     int first;
-    n += (static_cast<int64_t>(doc_span(a.cu_q, d, a.rows_q, &first)) * g + rows - 1) / rows;
+    n += (static_cast<int64_t>(doc_span<READ>(a.cu_q, d, a.rows_q, &first)) * g + rows - 1) / rows;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -489,6 +515,7 @@ struct DocCursor {
   int d0;
   int64_t base;
 };
+template <int READ = kReadConst>
 __device__ __forceinline__ bool find_doc_block(const PrefillArgs& a, int64_t at, int rows, int g,
                                                DocCursor& cursor, DocBlock* out) {
   const int lane = threadIdx.x & 31;
@@ -497,7 +524,7 @@ __device__ __forceinline__ bool find_doc_block(const PrefillArgs& a, int64_t at,
   int64_t base = cursor.base;
   for (int d0 = cursor.d0; d0 < a.n_docs; d0 += 32) {
     int first = 0, n = 0;
-    if (d0 + lane < a.n_docs) n = doc_span(a.cu_q, d0 + lane, a.rows_q, &first);
+    if (d0 + lane < a.n_docs) n = doc_span<READ>(a.cu_q, d0 + lane, a.rows_q, &first);
     const int blocks = static_cast<int>((static_cast<int64_t>(n) * g + rows - 1) / rows);
     const int incl = warp_incl_scan(blocks);
     const unsigned hit = __ballot_sync(0xffffffffu, base + incl > at);
@@ -508,7 +535,7 @@ __device__ __forceinline__ bool find_doc_block(const PrefillArgs& a, int64_t at,
       out->q0 = __shfl_sync(0xffffffffu, first, src);
       out->n_q = __shfl_sync(0xffffffffu, n, src);
       int k0 = 0;
-      out->n_k = doc_span(a.cu_k, out->doc, a.rows_k, &k0);
+      out->n_k = doc_span<READ>(a.cu_k, out->doc, a.rows_k, &k0);
       out->k0 = k0;
       cursor = {d0, base};
       return true;
@@ -520,10 +547,11 @@ __device__ __forceinline__ bool find_doc_block(const PrefillArgs& a, int64_t at,
 }
 
 // Flags offsets that are not ascending within [0, rows] (one block checks).
+template <int READ = kReadConst>
 __device__ __forceinline__ void check_offsets(const int32_t* cu, int n, int rows, int32_t* status,
                                               int thread, int threads) {
   for (int i = thread; i < n; i += threads) {
-    const int a = __ldg(cu + i), b = __ldg(cu + i + 1);
+    const int a = load_input<READ>(cu + i), b = load_input<READ>(cu + i + 1);
     if (a < 0 || b < a || b > rows) raise_flag(status, WF_DEV_BAD_INDEX);
   }
 }

@@ -22,6 +22,9 @@ namespace {
 
 constexpr int KT = 64;  // keys per tile
 
+// The windowed kernel is launched early.
+constexpr int read_of_window(bool window) { return window ? kReadOrdered : kReadConst; }
+
 template <int D, int RT>
 struct FmaSmem {
   float q[RT][D + 4];
@@ -88,7 +91,9 @@ __device__ __forceinline__ void fma_tile(FmaSmem<D, RT>& s, const RowBlock& b,
   for (int r = 0; r < RPT; ++r) {
     const int row = ty * RPT + r;
     const int pos = b.pos(row);
-    const float slope = o.slopes != nullptr && row < b.rows ? __ldg(o.slopes + b.head(row)) : 0.f;
+    const float slope = o.slopes != nullptr && row < b.rows
+                            ? load_input<read_of_window(WINDOW)>(o.slopes + b.head(row))
+                            : 0.f;
     float mx = st.m[r];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -165,19 +170,18 @@ __device__ __forceinline__ void fma_store(const FmaState<D, RT>& st, const RowBl
   }
 }
 
-template <typename T, int D, int RT>
+template <int READ, typename T, int D, int RT>
 __device__ __forceinline__ void fma_load_q(FmaSmem<D, RT>& s, const RowBlock& b, const T* q,
                                            int64_t stride) {
+  static_assert(sizeof(T) == 4, "rows of fp32");
   constexpr int V = Elem<T>::kPer16B, C = D / V;
   for (int e = threadIdx.x; e < RT * C; e += kThreads) {
     const int r = e / C, c = e % C;
-    float f[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = 0.f;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < b.rows)
-      load16_f32(q + static_cast<int64_t>((b.row0 + r) / b.g) * stride + b.head(r) * D + c * V, f);
-#pragma unroll
-    for (int i = 0; i < V; ++i) s.q[r][c * V + i] = f[i];
+      f = load_input<READ>(reinterpret_cast<const float4*>(
+          q + static_cast<int64_t>((b.row0 + r) / b.g) * stride + b.head(r) * D + c * V));
+    *reinterpret_cast<float4*>(&s.q[r][c * V]) = f;
   }
 }
 
@@ -212,26 +216,27 @@ __global__ void __launch_bounds__(kThreads) prefill_fma_kernel(PrefillParams p) 
   const PrefillArgs& a = p.a;
   const int g = a.q_heads / a.kv_heads;
   const int kvh = blockIdx.y;
+  constexpr int kRead = read_of_window(WINDOW);
   if (WINDOW) wait_for_primary();
   if (blockIdx.x == 0 && kvh == 0) {
-    check_offsets(a.cu_q, a.n_docs, a.rows_q, a.status, threadIdx.x, kThreads);
-    check_offsets(a.cu_k, a.n_docs, a.rows_k, a.status, threadIdx.x, kThreads);
+    check_offsets<kRead>(a.cu_q, a.n_docs, a.rows_q, a.status, threadIdx.x, kThreads);
+    check_offsets<kRead>(a.cu_k, a.n_docs, a.rows_k, a.status, threadIdx.x, kThreads);
   }
   DocCursor cursor = {0, 0};
-  const int64_t total = p.capped ? doc_total(a, RT, g) : gridDim.x;
+  const int64_t total = p.capped ? doc_total<kRead>(a, RT, g) : gridDim.x;
   for (int64_t at = blockIdx.x; at < total; at += gridDim.x) {
     DocBlock d;
-    if (!find_doc_block(a, at, RT, g, cursor, &d)) return;
+    if (!find_doc_block<kRead>(a, at, RT, g, cursor, &d)) return;
     if (at != blockIdx.x) __syncthreads();  // the last block's rows have been read
     RowBlock b;
     b.g = g;
     b.n_q = d.n_q;
     b.len = d.n_k;
-    b.prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + d.doc) : 0;
+    b.prefix = p.o.prefix != nullptr ? load_input<kRead>(p.o.prefix + d.doc) : 0;
     b.row0 = d.block * RT;
     b.rows = min(RT, d.n_q * g - b.row0);
     b.head0 = kvh * g;
-    fma_load_q<T, D, RT>(s, b, static_cast<const T*>(a.q) + d.q0 * a.q_stride, a.q_stride);
+    fma_load_q<kRead, T, D, RT>(s, b, static_cast<const T*>(a.q) + d.q0 * a.q_stride, a.q_stride);
     FmaState<D, RT> st;
     st.reset();
     int end = visible_end(b.len, b.pos(b.rows - 1), p.o.causal, b.prefix);
@@ -260,8 +265,8 @@ __global__ void __launch_bounds__(kThreads) prefill_fma_kernel(PrefillParams p) 
           const int e = threadIdx.x + i * kThreads, j = e / C, c = e % C, key = key0 + j;
           kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
           if (key >= b.len) continue;
-          kr[i] = __ldg(reinterpret_cast<const uint4*>(kb + key * a.k_stride) + c);
-          vr[i] = __ldg(reinterpret_cast<const uint4*>(vb + key * a.v_stride) + c);
+          kr[i] = load_input<kRead>(reinterpret_cast<const uint4*>(kb + key * a.k_stride) + c);
+          vr[i] = load_input<kRead>(reinterpret_cast<const uint4*>(vb + key * a.v_stride) + c);
         }
       };
       const auto next = [&](int key0) {  // the next tile that some row sees

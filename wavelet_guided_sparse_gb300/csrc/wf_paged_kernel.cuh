@@ -198,8 +198,8 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         const int key = span.place(static_cast<int>(at - x.begin)) * KT + box * tp.box_rows;
         page[i] = -1;
         if (box < boxes && box_needed<MASK>(p.w, span, x.len, key, tp.box_rows))
-          page[i] = __ldg(a.table + static_cast<int64_t>(x.seq) * a.table_pages +
-                          (key >> tp.page_shift));
+          page[i] = load_input<read_of(MASK)>(
+              a.table + static_cast<int64_t>(x.seq) * a.table_pages + (key >> tp.page_shift));
       }
     };
     unsigned every[NS];  // the lanes with a part of a full stage
@@ -332,7 +332,8 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
         continue;
       }
       const int len = u.len;
-      const int prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + u.seq) : 0;
+      const int prefix =
+          p.o.prefix != nullptr ? load_input<read_of(MASK)>(p.o.prefix + u.seq) : 0;
       const int kvh = u.unit / p.row_blocks;
       const int row0 = (u.unit % p.row_blocks) * RT;
       const int rows = min(RT, g * a.n_new - row0);
@@ -362,7 +363,7 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
           low[h] = pos[h] - p.w.window + 1;
           if (!p.o.causal && p.w.window < len - pos[h]) limit[h] = pos[h] + p.w.window;
         }
-        slope[h] = BIAS ? __ldg(p.o.slopes + kvh * g + hd) * kLog2e : 0.f;
+        slope[h] = BIAS ? load_input<read_of(MASK)>(p.o.slopes + kvh * g + hd) * kLog2e : 0.f;
       }
       // The unit's query rows arrive with its first tile.
       ok = ok && warp_wait(&bars.full[st], phase, bars.wait, a.status);
@@ -501,7 +502,8 @@ __launch_bounds__(PagedShape<T, D, R>::kThreadCount, PagedShape<T, D, R>::kCtasP
                 for (int c = 0; c < D / 4; ++c) {
                   const float4 x = *reinterpret_cast<const float4*>(
                       key + (c >> 3) * (KT * 128) + (((c & 7) ^ (r & 7)) << 4));
-                  const float4 y = __ldg(reinterpret_cast<const float4*>(row[e >> 1]) + c);
+                  const float4 y =
+                      load_input<read_of(MASK)>(reinterpret_cast<const float4*>(row[e >> 1]) + c);
                   sum = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, sum))));
                 }
                 s[n][e] = sum;
@@ -767,22 +769,27 @@ struct JoinUnit {
   int c0, n;
   bool joins;
 };
+//
+// It finds its unit before the split kernel ends.  The masked forms' split kernels
+// let it start behind their own wait, so that the lengths are complete by then and
+// stay as they are; they are read past L1, which nothing has ordered yet.
 template <int MASK>
 __device__ __forceinline__ JoinUnit join_unit(const PagedParams& p, int ctas, int RT,
                                               int by_unit) {
-  const WorkSplit split(work_total<MASK>(p.w, p.a.kv_len), ctas);
+  constexpr int kRead = MASK == kMaskPlain ? kReadConst : kReadL2;
+  const WorkSplit split(work_total<MASK, kRead>(p.w, p.a.kv_len), ctas);
   JoinUnit x;
   x.c0 = blockIdx.x;
   int64_t w0 = split.begin(x.c0), w1 = split.begin(x.c0 + 1);
   bool any = w0 < w1;
   if (by_unit) {
-    x.u = nth_unit<MASK>(p.w, p.a.kv_len, blockIdx.x);
+    x.u = nth_unit<MASK, kRead>(p.w, p.a.kv_len, blockIdx.x);
     any = x.u.tiles > 0;
     x.c0 = any ? split.owner(x.u.begin) : 0;
     w0 = split.begin(x.c0);
     w1 = split.begin(x.c0 + 1);
   } else {
-    x.u = find_unit<MASK>(p.w, p.a.kv_len, any ? w1 - 1 : 0);
+    x.u = find_unit<MASK, kRead>(p.w, p.a.kv_len, any ? w1 - 1 : 0);
   }
   const int64_t end = x.u.begin + x.u.tiles - (MASK != kMaskPlain ? p.w.pad : 0);
   x.joins = any && x.u.begin >= w0 && end > w1;

@@ -221,8 +221,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const auto entry = [&](int j) {
         const int key = box_key(j);
         return box < boxes && box_needed<MASK>(p.w, span, u.len, key, tp.box_rows)
-                   ? __ldg(a.table + static_cast<int64_t>(u.seq) * a.table_pages +
-                           (key >> tp.page_shift))
+                   ? load_input<kReadOrdered>(a.table +
+                                              static_cast<int64_t>(u.seq) * a.table_pages +
+                                              (key >> tp.page_shift))
                    : -1;
       };
       const auto fill = [&](bool key_fill, int j, int page, int kvh, uint32_t step) {
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           unit *= p.o.scale * p.o.scale;
         }
         map.weigh = live ? p.o.scale : 0.f;
-        map.slope = BIAS ? __ldg(p.o.slopes + head) * kLog2e : 0.f;
+        map.slope = BIAS ? load_input<kReadOrdered>(p.o.slopes + head) * kLog2e : 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           map.steps[i] = pack2(map.slope * (2 * i), map.slope * (2 * i + 1));

@@ -40,6 +40,9 @@ constexpr int kAllocThreads = 1024, kAllocWarps = kAllocThreads / 32, kAllocClus
 constexpr int kOneCta = 16384;  // pages that one CTA counts alone
 constexpr int kSeqWords = WF_MAX_SEQS / 32;
 
+// Every kernel here is launched early.
+__device__ __forceinline__ int ld(const int32_t* p) { return load_input<kReadOrdered>(p); }
+
 __device__ __forceinline__ int max_len(const PagesArgs& a) { return a.table_pages * a.page_size; }
 
 // A length clamped into a sequence's table; flags one outside.
@@ -93,7 +96,7 @@ __device__ __forceinline__ bool bit_of(const uint32_t* words, int i) {
 __device__ __forceinline__ ForkUnit fork_unit(const AllocArgs& x, const AllocShared& sm, int i,
                                               bool say) {
   const PagesArgs& a = x.p;
-  ForkUnit u = {__ldg(x.src + i), __ldg(x.dst + i), 0, 0, 0};
+  ForkUnit u = {ld(x.src + i), ld(x.dst + i), 0, 0, 0};
   if (static_cast<unsigned>(u.src) >= static_cast<unsigned>(a.n_seqs) ||
       static_cast<unsigned>(u.dst) >= static_cast<unsigned>(a.n_seqs)) {
     if (say) raise_flag(a.status, WF_DEV_BAD_INDEX);
@@ -105,16 +108,16 @@ __device__ __forceinline__ ForkUnit fork_unit(const AllocArgs& x, const AllocSha
     u.dst = -1;
     return u;
   }
-  u.len = length_in(a, __ldg(x.rows + u.src), say);
+  u.len = length_in(a, ld(x.rows + u.src), say);
   u.entries = (u.len + a.page_size - 1) / a.page_size;
-  const int share = x.share != nullptr ? min(max(__ldg(x.share + i), 0), u.len) : u.len;
+  const int share = x.share != nullptr ? min(max(ld(x.share + i), 0), u.len) : u.len;
   u.shared = share / a.page_size;
   return u;
 }
 
 // Entries of sequence s that a reserve has to fill.
 __device__ __forceinline__ int reserve_entries(const AllocArgs& x, int s, bool say) {
-  return (length_in(x.p, __ldg(x.rows + s), say) + x.p.page_size - 1) / x.p.page_size;
+  return (length_in(x.p, ld(x.rows + s), say) + x.p.page_size - 1) / x.p.page_size;
 }
 
 // Words first + lane, first + 32 + lane, ... of an array that ends at `end`
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
       sm.is_src[i] = sm.once[i] = sm.twice[i] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < x.units; i += kAllocThreads) {
-      const int s = __ldg(x.src + i), d = __ldg(x.dst + i);
+      const int s = ld(x.src + i), d = ld(x.dst + i);
       if (static_cast<unsigned>(s) < static_cast<unsigned>(a.n_seqs))
         atomicOr(&sm.is_src[s >> 5], 1u << (s & 31));
       if (static_cast<unsigned>(d) < static_cast<unsigned>(a.n_seqs) &&
@@ -343,8 +346,8 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const PagesArgs a, co
   launch_dependents();
   wait_for_primary();
   for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
-    const int lo = min(max(__ldg(first + s), 0), max_len(a));
-    const int hi = min(max(__ldg(end + s), 0), max_len(a));
+    const int lo = min(max(ld(first + s), 0), max_len(a));
+    const int hi = min(max(ld(end + s), 0), max_len(a));
     // Pages all of whose rows lie in [lo, hi).
     drop_entries(a, s, (lo + (a.page_size - 1)) / a.page_size, hi / a.page_size, threadIdx.x,
                  kThreads);
@@ -373,13 +376,13 @@ __global__ void __launch_bounds__(kPlanThreads) keep_plan_kernel(const KeepArgs 
 #pragma unroll
       for (int k = 0; k < kPlanBatch; ++k) {
         const int i = i0 + k * threads;
-        from[k] = i < x.max_keep ? __ldg(keep + i) : -1;
-        prev[k] = i > 0 && i < x.max_keep ? __ldg(keep + i - 1) : -1;
+        from[k] = i < x.max_keep ? ld(keep + i) : -1;
+        prev[k] = i > 0 && i < x.max_keep ? ld(keep + i - 1) : -1;
       }
     };
     read_rows(threadIdx.x);
-    const int len = __ldg(x.kv_len + s), start = __ldg(x.start + s);
-    const int n = x.n_keep != nullptr ? __ldg(x.n_keep + s) : 0;
+    const int len = ld(x.kv_len + s), start = ld(x.start + s);
+    const int n = x.n_keep != nullptr ? ld(x.n_keep + s) : 0;
     const bool sound = len >= 0 && len <= max_len(a) && start >= 0 && start <= len && n >= 0 &&
                        n <= x.max_keep;
     const int count = sound ? n : 0;

@@ -149,6 +149,9 @@ __device__ __forceinline__ int64_t claimed_block(const uint4* from) {
   return ok ? static_cast<int64_t>(x) : -1;
 }
 
+// The windowed kernel is launched early.
+constexpr int read_of_window(bool window) { return window ? kReadOrdered : kReadConst; }
+
 // An item by its index: heads run fastest, a sequence's row blocks from its
 // last (the longest under the causal mask) to its first.  False: behind the
 // last sequence.  Whole warp.
@@ -157,21 +160,22 @@ __device__ __forceinline__ bool make_item(const PrefillTcParams& p, int64_t inde
                                           DocCursor& cursor, Item* out) {
   const PrefillArgs& a = p.a;
   Item& it = *out;
+  constexpr int kRead = read_of_window(WINDOW);
   const int heads = p.pair_heads ? a.q_heads / 2 : a.q_heads;
   const int block_rows = p.pair_heads ? kTileRows : 2 * kTileRows;
   if (index == 0) {
-    check_offsets(a.cu_q, a.n_docs, a.rows_q, a.status, threadIdx.x & 31, 32);
-    check_offsets(a.cu_k, a.n_docs, a.rows_k, a.status, threadIdx.x & 31, 32);
+    check_offsets<kRead>(a.cu_q, a.n_docs, a.rows_q, a.status, threadIdx.x & 31, 32);
+    check_offsets<kRead>(a.cu_k, a.n_docs, a.rows_k, a.status, threadIdx.x & 31, 32);
   }
   DocBlock doc;
-  if (!find_doc_block(a, index / heads, block_rows, 1, cursor, &doc)) return false;
+  if (!find_doc_block<kRead>(a, index / heads, block_rows, 1, cursor, &doc)) return false;
   it.live = 1;
   const int hx = static_cast<int>(index % heads);
   doc.block = (doc.n_q + block_rows - 1) / block_rows - 1 - doc.block;
   it.q0 = static_cast<int>(doc.q0);
   it.k0 = static_cast<int>(doc.k0);
   it.n_k = doc.n_k;
-  it.prefix = p.o.prefix != nullptr ? __ldg(p.o.prefix + doc.doc) : 0;
+  it.prefix = p.o.prefix != nullptr ? load_input<kRead>(p.o.prefix + doc.doc) : 0;
   it.shift = doc.n_k - doc.n_q;
   if (WINDOW) {
     // Both query tiles share the line: from the first row's window on.
@@ -257,8 +261,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       DocCursor cursor = {0, 0};
       int64_t grain = 1, items = INT64_MAX;  // (not counted)
       if (p.capped) {
-        items = p.pair_heads ? doc_total(a, kTileRows, 1) * (a.q_heads / 2)
-                             : doc_total(a, 2 * kTileRows, 1) * a.q_heads;
+        constexpr int kRead = read_of_window(WINDOW);
+        items = p.pair_heads ? doc_total<kRead>(a, kTileRows, 1) * (a.q_heads / 2)
+                             : doc_total<kRead>(a, 2 * kTileRows, 1) * a.q_heads;
         grain = max(grain, (items + gridDim.x - 1) / gridDim.x);
       }
       int64_t next = blockIdx.x * grain, stop = next + grain;
@@ -528,7 +533,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           unit *= p.o.scale * p.o.scale;
         }
         map.weigh = live ? p.o.scale : 0.f;
-        map.slope = BIAS ? __ldg(p.o.slopes + max(0, min(head, a.q_heads - 1))) * kLog2e : 0.f;
+        map.slope = BIAS ? load_input<read_of_window(WINDOW)>(
+                               p.o.slopes + max(0, min(head, a.q_heads - 1))) * kLog2e
+                         : 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           map.steps[i] = pack2(map.slope * (2 * i), map.slope * (2 * i + 1));
