@@ -166,3 +166,19 @@ def test_captured_on_two_streams_that_meet():
         torch.cuda.synchronize()
         assert torch.equal(out, bd.paged_tree_attn(q, cache, table, lens, tree))
     assert bd.read_device_status(ws) == 0
+
+
+def test_more_entries_than_32_bits_count():
+    """Sequences that want 2^31 pages in all: those that there are go to the first ones."""
+    seqs, width = 4096, 1 << 19
+    cache = {x: torch.empty((60, 1, 8, 64), dtype=BF, device="cuda") for x in "KV"}
+    table = bd.alloc_page_table(seqs, width, "cuda")
+    refs = bd.alloc_page_refs(60, "cuda")
+    refs[7] = 1
+    ws = bd.alloc_pages_workspace(cache, table)
+    bd.paged_reserve(cache, table, refs, i32([8 * width] * seqs), ws)
+    assert bd.read_device_status(ws) == bd.DEV_NO_PAGE
+    want = [p for p in range(60) if p != 7]
+    assert table[0, :59].tolist() == want and (refs == 1).all()
+    table[0, :59] = -1
+    assert all((part == -1).all() for part in table.split(256))

@@ -120,6 +120,22 @@ __device__ __forceinline__ int reserve_entries(const AllocArgs& x, int s, bool s
   return (length_in(x.p, ld(x.rows + s), say) + x.p.page_size - 1) / x.p.page_size;
 }
 
+// Sums of needs are cut at `most`, one page more than there are: the entries of a call
+// may be more than 32 bits count, and behind the last page it does not matter how
+// many want one.
+__device__ __forceinline__ int sum_cut(int a, int b, int most) { return min(a + b, most); }
+// Sums of a warp's values up to each lane's, its own left out; `total`: all.
+__device__ __forceinline__ int sums_before(int v, int most, int lane, int* total) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v = sum_cut(v, x, most);
+  }
+  *total = __shfl_sync(0xffffffffu, v, 31);
+  const int before = __shfl_up_sync(0xffffffffu, v, 1);
+  return lane == 0 ? 0 : before;
+}
+
 // Words first + lane, first + 32 + lane, ... of an array that ends at `end`
 // (`with` behind it), all loads in flight together.
 __device__ __forceinline__ void read_batch(const int32_t* from, int first, int end, int lane,
@@ -164,12 +180,14 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
   // This warp's first counts, kept: of a small pool all of them.
   int refs0[kBatch];
   read_batch(a.refs, p0, p1, lane, 1, refs0);
+  const int most = a.n_pages + 1;
   int need = 0;
   for (int u = u0; u < u1; ++u) {
     if (lane == 0) x.base[u] = need;  // within the warp
+    int more = 0;
     if (FORK) {
       const ForkUnit f = fork_unit(x, sm, u, lane == 0);
-      need += f.entries - f.shared;
+      more = f.entries - f.shared;
     } else {
       const int entries = reserve_entries(x, u, lane == 0);
       const int32_t* row = a.table + static_cast<int64_t>(u) * a.table_pages;
@@ -177,9 +195,10 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
         int got[kBatch];
         read_batch(row, e0, entries, lane, 0, got);
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) need += __popc(__ballot_sync(0xffffffffu, got[k] < 0));
+        for (int k = 0; k < kBatch; ++k) more += __popc(__ballot_sync(0xffffffffu, got[k] < 0));
       }
     }
+    need = sum_cut(need, more, most);
   }
   int free = 0;
   for (int p = p0; p < p1; p += 32 * kBatch) {
@@ -198,9 +217,8 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
   if (warp < 2) {  // exclusive sums over the CTA's warps; totals to every CTA
     int* mine = warp == 0 ? sm.warp_need : sm.warp_free;
     int* totals = warp == 0 ? sm.need : sm.free;
-    const int v = mine[lane], incl = warp_incl_scan(v);
-    mine[lane] = incl - v;
-    const int total = __shfl_sync(0xffffffffu, incl, 31);
+    int total;
+    mine[lane] = sums_before(mine[lane], most, lane, &total);
     if (ctas == 1) {
       if (lane == 0) totals[0] = total;
     } else if (lane < ctas) {
@@ -212,10 +230,10 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
   int total_need = 0, total_free = 0;
   for (int c = 0; c < ctas; ++c) {
     if (c < me) {
-      need_before += sm.need[c];
+      need_before = sum_cut(need_before, sm.need[c], most);
       free_before += sm.free[c];
     }
-    total_need += sm.need[c];
+    total_need = sum_cut(total_need, sm.need[c], most);
     total_free += sm.free[c];
   }
   if (total_need == 0 && !FORK) return;  // the same for all
@@ -244,7 +262,7 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
     cluster.sync();
   }
   for (int u = u0; u < u1; ++u) {
-    int rank = need_before + x.base[u];
+    int rank = sum_cut(need_before, x.base[u], most);
     if (FORK) {
       const ForkUnit f = fork_unit(x, sm, u, false);
       if (f.dst < 0) continue;
