@@ -245,7 +245,7 @@ __device__ __forceinline__ int tiles_of(const WorkShape& w, int len) {
 // Tiles of the whole call.  Whole warp.
 template <int MASK = kMaskPlain, int READ = read_of(MASK)>
 __device__ __forceinline__ int64_t work_total(const WorkShape& w, const int32_t* lens) {
-  int n = 0;  // fits: the host bounds n_seqs times the longest sequence's tiles
+  int n = 0;  // fits: the host bounds n_seqs times the longest sequence's tiles and pad
   for (int s = threadIdx.x & 31; s < w.n_seqs; s += 32)
     n += tiles_of<MASK>(w, seq_len_clamped<MASK, READ>(w, lens, s));
 #pragma unroll

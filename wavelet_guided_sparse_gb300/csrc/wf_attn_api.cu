@@ -123,6 +123,10 @@ int paged_call(PlanFn plan, const wf_page_dims* dims, const wf_attn_opts* opts, 
   if (!aligned16(Q) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(O) ||
       !aligned16(workspace) || !aligned4(page_table) || !aligned4(kv_len) || !aligned4(lse))
     return WF_ERR_ALIGNMENT;
+  // Tiles of all sequences, with the empty ones behind a unit's, are counted in 32 bits.
+  const wf::PagedPlan p = plan(paged_args(dims, n_new), wf::device_sm_count());
+  const int64_t len = static_cast<int64_t>(dims->table_pages) * dims->page_size;
+  if (((len + p.tile - 1) / p.tile + p.pad) * dims->n_seqs > INT32_MAX) return WF_ERR_UNSUPPORTED;
   if (workspace_bytes < need) return WF_ERR_WORKSPACE;
   wf::PagedArgs a = paged_args(dims, n_new);
   a.q = Q;
