@@ -32,8 +32,8 @@
  *   wf_paged_tree_attn     by the nodes of a drafted tree
  *   wf_prefill_attn        §2.1 eq. (1) over packed prompts
  *   wf_prefill_window_attn over a sliding window and the first tokens of each
- *   wf_paged_reserve, wf_paged_fork, wf_paged_keep, wf_paged_release
- *                          the pages themselves: taken, shared or copied,
+ *   wf_paged_reserve, wf_paged_reserve_from, wf_paged_fork, wf_paged_keep,
+ *   wf_paged_release       the pages themselves: taken, shared or copied,
  *                          compacted, given back
  *
  * Readings fixed where the pages are silent: orthonormal Haar filters
@@ -592,7 +592,7 @@ int wf_paged_window_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_new
  *   page_table : entries of pages whose rows no query of the sequence sees are
  *                not looked at, so that their pages may be gone
  *                (wf_paged_release with first = sinks, end = kv_len - n_new -
- *                window + 1)
+ *                window + 1; the sequence then grows by wf_paged_reserve_from)
  *   workspace  : >= wf_paged_window_attn_workspace_bytes()
  * Everything else as wf_paged_attn; values of rows that the window hides must
  * be finite where their page holds one that some query sees.  opts->prefix
@@ -664,6 +664,17 @@ int wf_pages_workspace_bytes(const wf_page_dims* dims, int32_t max_forks, int32_
  * One launch.  Errors: as wf_paged_append. */
 int wf_paged_reserve(const wf_page_dims* dims, const int32_t* rows, int32_t* refs,
                      int32_t* page_table, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same for rows [from_rows[s], rows[s]) only: entries of pages all of whose
+ * rows lie below from_rows[s] stay as they are and are not read.  With the rows
+ * that a sequence holds already it takes pages for its new ones, and none for those
+ * that wf_paged_release has given back behind a window (wf_paged_reserve would take
+ * them all again).
+ *   from_rows : device, nullable (0), [n_seqs] int32; outside the table: clamped
+ *               and flagged WF_DEV_BAD_INDEX; from_rows >= rows: nothing */
+int wf_paged_reserve_from(const wf_page_dims* dims, const int32_t* from_rows, const int32_t* rows,
+                          int32_t* refs, int32_t* page_table, void* workspace,
+                          size_t workspace_bytes, void* stream);
 
 /* Children of sequences.  Fork i makes sequence dst[i], which must hold no
  * pages, a copy of sequence src[i] with its kv_len[src[i]] rows: the pages

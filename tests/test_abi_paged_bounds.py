@@ -5,7 +5,7 @@ import os
 
 import pytest
 
-from test_abi_dense import OK, UNSUPPORTED, WORKSPACE, opts, pages
+from test_abi_dense import ALIGNMENT, NULL, ODD2, OK, P, UNSUPPORTED, WORKSPACE, opts, pages
 from test_abi_paged_masks import tree, window
 from wavelet_guided_sparse_gb300 import binding as bd
 
@@ -30,3 +30,19 @@ def test_tiles_and_pads_fit_32_bits(lib, call, table_pages, dtype, new, refused)
     n = ctypes.c_size_t(0)
     assert lib.wf_paged_attn_workspace_bytes(ctypes.byref(d), new, ctypes.byref(n)) == OK
     assert call(lib, d, opts(), new=new, wsb=0) == (UNSUPPORTED if refused else WORKSPACE)
+
+
+def test_reserve_from(lib):
+    d = pages()
+    n = ctypes.c_size_t(0)
+    assert lib.wf_pages_workspace_bytes(ctypes.byref(d), 0, 0, ctypes.byref(n)) == OK
+
+    def call(dims=d, start=P, rows=P, refs=P, table=P, ws=P, wsb=1 << 40):
+        return lib.wf_paged_reserve_from(ctypes.byref(dims), start, rows, refs, table, ws, wsb, None)
+
+    for name in ("rows", "refs", "table", "ws"):
+        assert call(**{name: None}) == NULL
+    for name in ("start", "rows", "refs", "table", "ws"):
+        assert call(**{name: ODD2}) == ALIGNMENT
+    assert call(start=None, wsb=n.value - 1) == WORKSPACE
+    assert call(pages(page_size=48)) == UNSUPPORTED

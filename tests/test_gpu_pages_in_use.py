@@ -6,6 +6,8 @@ import numpy as np
 import pytest
 import torch
 
+from dense_common import check, f64
+from mask_common import attend_masked, window_mask
 from wavelet_guided_sparse_gb300 import binding as bd
 
 pytestmark = pytest.mark.gpu
@@ -182,3 +184,75 @@ def test_more_entries_than_32_bits_count():
     assert table[0, :59].tolist() == want and (refs == 1).all()
     table[0, :59] = -1
     assert all((part == -1).all() for part in table.split(256))
+
+
+def test_reserve_from_what_is_held():
+    """Entries below the first new row stay as they are, the others are filled in order."""
+    page, width, seqs, pages = 8, 700, 6, 3000
+    cache = {x: torch.empty((pages, 1, page, 64), dtype=BF, device="cuda") for x in "KV"}
+    rng = np.random.default_rng(4)
+    order = rng.permutation(pages)[:2000].tolist()
+    table = np.full((seqs, width), -1)
+    refs = [0] * pages
+    for s in range(seqs):
+        for e in range(width):
+            if rng.random() < 0.4:
+                table[s, e] = order.pop()
+                refs[table[s, e]] = 1
+    start = [0, 3, 8 * 300, 8 * 300 + 1, 5600, 40]
+    rows = [50, 4, 8 * 300, 8 * 600, 5600, 5598]
+    got_t, got_r = i32(table.tolist()), i32(refs)
+    ws = bd.alloc_pages_workspace(cache, got_t)
+    bd.paged_reserve(cache, got_t, got_r, i32(rows), ws, from_rows=i32(start))
+    for s in range(seqs):
+        for e in range(start[s] // page, -(-rows[s] // page) if rows[s] > start[s] else 0):
+            if table[s, e] < 0:
+                table[s, e] = refs.index(0)
+                refs[table[s, e]] = 1
+    assert got_t.tolist() == table.tolist() and got_r.tolist() == refs
+    assert bd.read_device_status(ws) == 0
+    for bad in (-1, width * page + 1):
+        bd.clear_device_status(ws)
+        bd.paged_reserve(cache, got_t, got_r, i32([0] * seqs), ws, from_rows=i32([bad] * seqs))
+        assert bd.read_device_status(ws) == bd.DEV_BAD_INDEX
+    assert got_t.tolist() == table.tolist()
+
+
+@pytest.mark.parametrize("dtype,new,hq,hkv,d", [(BF, 1, 8, 2, 64), (BF, 7, 4, 2, 128),
+                                                (F32, 5, 2, 1, 64)])
+def test_a_window_in_a_pool_of_its_own_size(dtype, new, hq, hkv, d):
+    """Sequences several windows long, in pages for little more than one window each."""
+    page, window, sinks, steps = 16, 100, 20, 600 // new + 1
+    # A sequence's first tokens, its window with the last and the new rows, a page cut at the end.
+    pool = 2 * (-(-sinks // page) + -(-(window + 2 * new - 1) // page) + 1)
+    cache = {x: torch.full((pool, hkv, page, d), float("nan"), dtype=dtype, device="cuda")
+             for x in "KV"}
+    table, refs = bd.alloc_page_table(2, 60, "cuda"), bd.alloc_page_refs(pool, "cuda")
+    ws = bd.alloc_pages_workspace(cache, table)
+    held = [0, 37]
+    past = [[torch.zeros((0, hkv, d), dtype=dtype, device="cuda") for _ in "KV"] for _ in held]
+    first = randn((2, 37, hkv, d), dtype, 1)
+    bd.paged_reserve(cache, table, refs, i32(held), ws)
+    bd.paged_append(first[0], first[1], cache, table, i32([0, 0, 37]), i32([0, 0]), ws=ws)
+    past[1] = [first[0], first[1]]
+    qs = randn((2, new, hq, d), dtype, 2)
+    ws_attn = bd.alloc_paged_attn_workspace(qs, cache, table)
+    for step in range(steps):
+        k, v = randn((2, 2 * new, hkv, d), dtype, 10 + step)
+        lens, grown = i32(held), i32([h + new for h in held])
+        bd.paged_reserve(cache, table, refs, grown, ws, from_rows=lens)
+        bd.paged_append(k, v, cache, table, i32([0, new, 2 * new]), lens, ws=ws)
+        o = bd.paged_window_attn(qs, cache, table, grown, window, ws_attn, sinks=sinks)
+        bd.paged_release(cache, table, refs, i32([sinks] * 2), grown - new - window + 1, ws)
+        for s in range(2):
+            past[s] = [torch.cat((x, y[s * new:(s + 1) * new])) for x, y in zip(past[s], (k, v))]
+        held = [h + new for h in held]
+        if step % 40 and step + 1 < steps:
+            continue
+        for s, n in enumerate(held):
+            seen = window_mask(n - new + np.arange(new), n, window, sinks, True)
+            ro, _, ob, _ = attend_masked(f64(qs[s]), *[f64(x) for x in past[s]], dtype, seen)
+            check(f64(o[s]), ro, ob, f"O of sequence {s}, step {step}")
+    assert held[0] > 5 * window
+    assert bd.read_device_status(ws) == 0 and bd.read_device_status(ws_attn) == 0
+    assert refs.sum() == (table >= 0).sum() and refs.max() == 1

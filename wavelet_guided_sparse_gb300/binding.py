@@ -40,8 +40,8 @@ EXPORTS = ("wf_status_string", "wf_last_error_string", "wf_default_k_per_level",
            "wf_paged_attn", "wf_prefill_attn",
            "wf_paged_window_attn", "wf_paged_window_attn_workspace_bytes", "wf_paged_tree_attn_workspace_bytes", "wf_paged_tree_attn",
            "wf_prefill_window_attn",
-           "wf_pages_workspace_bytes", "wf_paged_reserve", "wf_paged_fork", "wf_paged_keep",
-           "wf_paged_release")
+           "wf_pages_workspace_bytes", "wf_paged_reserve", "wf_paged_reserve_from", "wf_paged_fork",
+           "wf_paged_keep", "wf_paged_release")
 
 
 class WfError(RuntimeError):
@@ -153,6 +153,7 @@ _SIGS = {
                                               _sz, _vp]),
     "wf_pages_workspace_bytes": (ctypes.c_int, [_PDIMSP, _i32, _i32, ctypes.POINTER(_sz)]),
     "wf_paged_reserve": (ctypes.c_int, [_PDIMSP, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "wf_paged_reserve_from": (ctypes.c_int, [_PDIMSP, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "wf_paged_fork": (ctypes.c_int, [_PDIMSP, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
                                      ctypes.POINTER(_vp), _vp, _sz, _vp]),
     "wf_paged_keep": (ctypes.c_int, [_PDIMSP, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32,
@@ -966,14 +967,19 @@ def alloc_pages_workspace(cache, page_table: torch.Tensor, max_forks: int = 0, m
 
 
 def paged_reserve(cache, page_table: torch.Tensor, refs: torch.Tensor, rows: torch.Tensor,
-                  ws: Optional[torch.Tensor] = None, stream=None) -> None:
+                  ws: Optional[torch.Tensor] = None, stream=None,
+                  from_rows: Optional[torch.Tensor] = None) -> None:
     """wf_paged_reserve: sequence s of page_table (in place) gets pages for its
     first rows[s] rows where it has none, the lowest free ones of refs (in
-    place).  ``cache``: one layer's {"K", "V"} (for the sizes) or page_pools()."""
+    place).  With ``from_rows`` (wf_paged_reserve_from) for rows from_rows[s] to
+    rows[s] only: the new ones of a sequence that has given back what a window
+    left behind.  ``cache``: one layer's {"K", "V"} (for the sizes) or
+    page_pools()."""
     with _On(page_table, stream):
         if ws is None:
             ws = alloc_pages_workspace(cache, page_table, stream=stream)
-        _check("wf_paged_reserve", _calls().reserve(_layer(cache), page_table, refs, rows, ws))
+        _check("wf_paged_reserve", _calls().reserve(_layer(cache), page_table, refs, rows, ws,
+                                                   from_rows))
 
 
 def paged_fork(caches, page_table: torch.Tensor, refs: torch.Tensor, src: torch.Tensor,

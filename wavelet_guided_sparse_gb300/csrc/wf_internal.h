@@ -244,11 +244,11 @@ struct PagePools {
   void* at[WF_MAX_POOLS];
   int n;
 };
-// Reserve: `units` = sequences, rows[s] of each.  Fork: units = forks, rows =
-// every sequence's length.  Scratch behind the status word.
+// Reserve: `units` = sequences, rows [from[s], rows[s]) of each (from nullable: 0).
+// Fork: units = forks, rows = every sequence's length.  Scratch behind the status word.
 struct AllocArgs {
   PagesArgs p;
-  const int32_t *rows, *src, *dst, *share;  // share nullable
+  const int32_t *from, *rows, *src, *dst, *share;  // from and share nullable
   int32_t *base, *list;                   // [units]; free pages by rank [n_pages]
   int4* copies;                           // fork: (from, to, rows, -) by rank [n_pages]
   int32_t* n_copies;

@@ -115,9 +115,15 @@ __device__ __forceinline__ ForkUnit fork_unit(const AllocArgs& x, const AllocSha
   return u;
 }
 
-// Entries of sequence s that a reserve has to fill.
-__device__ __forceinline__ int reserve_entries(const AllocArgs& x, int s, bool say) {
-  return (length_in(x.p, ld(x.rows + s), say) + x.p.page_size - 1) / x.p.page_size;
+// Entries [first, end) of sequence s, of which a reserve fills those without a page.
+struct ReserveUnit {
+  int first, end;
+};
+__device__ __forceinline__ ReserveUnit reserve_unit(const AllocArgs& x, int s, bool say) {
+  const int from = x.from != nullptr ? length_in(x.p, ld(x.from + s), say) : 0;
+  const int rows = length_in(x.p, ld(x.rows + s), say);
+  if (from >= rows) return {0, 0};
+  return {from / x.p.page_size, (rows + x.p.page_size - 1) / x.p.page_size};
 }
 
 // Sums of needs are cut at `most`, one page more than there are: the entries of a call
@@ -189,11 +195,11 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
       const ForkUnit f = fork_unit(x, sm, u, lane == 0);
       more = f.entries - f.shared;
     } else {
-      const int entries = reserve_entries(x, u, lane == 0);
+      const ReserveUnit r = reserve_unit(x, u, lane == 0);
       const int32_t* row = a.table + static_cast<int64_t>(u) * a.table_pages;
-      for (int e0 = 0; e0 < entries; e0 += 32 * kBatch) {
+      for (int e0 = r.first; e0 < r.end; e0 += 32 * kBatch) {
         int got[kBatch];
-        read_batch(row, e0, entries, lane, 0, got);
+        read_batch(row, e0, r.end, lane, 0, got);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) more += __popc(__ballot_sync(0xffffffffu, got[k] < 0));
       }
@@ -301,11 +307,11 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
         }
       }
     } else {
-      const int entries = reserve_entries(x, u, false);
+      const ReserveUnit unit = reserve_unit(x, u, false);
       int32_t* row = a.table + static_cast<int64_t>(u) * a.table_pages;
-      for (int e0 = 0; e0 < entries; e0 += 32 * kBatch) {
+      for (int e0 = unit.first; e0 < unit.end; e0 += 32 * kBatch) {
         int got[kBatch], page[kBatch];
-        read_batch(row, e0, entries, lane, 0, got);
+        read_batch(row, e0, unit.end, lane, 0, got);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const unsigned hits = __ballot_sync(0xffffffffu, got[k] < 0);

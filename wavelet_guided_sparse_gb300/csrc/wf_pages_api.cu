@@ -94,17 +94,26 @@ int wf_pages_workspace_bytes(const wf_page_dims* dims, int32_t max_forks, int32_
 
 int wf_paged_reserve(const wf_page_dims* dims, const int32_t* rows, int32_t* refs,
                      int32_t* page_table, void* workspace, size_t workspace_bytes, void* stream) {
+  return wf_paged_reserve_from(dims, nullptr, rows, refs, page_table, workspace, workspace_bytes,
+                               stream);
+}
+
+int wf_paged_reserve_from(const wf_page_dims* dims, const int32_t* from_rows, const int32_t* rows,
+                          int32_t* refs, int32_t* page_table, void* workspace,
+                          size_t workspace_bytes, void* stream) {
   wf_page_dims d;
   const int st = check_pages(dims, &d);
   if (st != WF_OK) return st;
   if (rows == nullptr || refs == nullptr || page_table == nullptr || workspace == nullptr)
     return WF_ERR_NULL;
-  if (!aligned4(rows) || !aligned4(refs) || !aligned4(page_table) || !aligned16(workspace))
+  if (!aligned4(from_rows) || !aligned4(rows) || !aligned4(refs) || !aligned4(page_table) ||
+      !aligned16(workspace))
     return WF_ERR_ALIGNMENT;
   const Scratch s = scratch_of(&d, d.n_seqs, 0, false);
   if (workspace_bytes < s.alloc_end) return WF_ERR_WORKSPACE;
   wf::AllocArgs x = {};
   x.p = pages_args(d, refs, page_table, workspace);
+  x.from = from_rows;
   x.rows = rows;
   x.base = at<int32_t>(workspace, kHeaderBytes);
   x.list = at<int32_t>(workspace, s.list);

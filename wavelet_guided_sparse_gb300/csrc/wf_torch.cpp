@@ -315,13 +315,14 @@ Pointers pointers(PyObject* o) {
   return {reinterpret_cast<void* const*>(data), static_cast<int32_t>(bytes / sizeof(void*))};
 }
 
-// K, page_table, refs, rows, ws
+// K, page_table, refs, rows, ws, from_rows
 PyObject* reserve(PyObject* const* a) {
   const Pages p = pages(a[0], a[2], a[1]);
   const int32_t* rows = ints(a[3], "rows", {p.n_seqs}, p.dev);
   const Workspace ws = workspace(a[4], p.dev);
-  return status(
-      wf_paged_reserve(&p.dims, rows, p.refs, p.table, ws.at, ws.bytes, stream_of(p.dev)));
+  const int32_t* from = ints_or_none(a[5], "from_rows", {p.n_seqs}, p.dev);
+  return status(wf_paged_reserve_from(&p.dims, from, rows, p.refs, p.table, ws.at, ws.bytes,
+                                      stream_of(p.dev)));
 }
 
 // pointers, K, page_table, refs, src, dst, kv_len, share_rows, ws
@@ -389,7 +390,7 @@ PyMethodDef method(const char* name) {
 PyMethodDef kMethods[] = {method<paged_tree, 13>("paged_tree"),
                           method<paged_window, 14>("paged_window"),
                           method<prefill_window, 14>("prefill_window"),
-                          method<reserve, 5>("reserve"),
+                          method<reserve, 6>("reserve"),
                           method<fork, 9>("fork"),
                           method<keep, 9>("keep"),
                           method<release, 6>("release"),
