@@ -689,9 +689,10 @@ int wf_paged_reserve_from(const wf_page_dims* dims, const int32_t* from_rows, co
  *   kv_len     : device, [n_seqs] int32 (clamped and flagged as above)
  *   share_rows : device, nullable, [n_forks] int32
  *   n_forks    : 0..WF_MAX_SEQS; 0 is a no-op
- * A parent's entry outside the pool is flagged WF_DEV_BAD_INDEX (a shared one
- * becomes -1, nothing is copied from it); too few free pages: as above.  Two
- * launches.  Errors: as wf_paged_append. */
+ * An entry that the parent has no page for (negative: what a window has left
+ * behind) stays without one in the child.  One outside the pool is flagged
+ * WF_DEV_BAD_INDEX (a shared one becomes -1, nothing is copied from it); too few
+ * free pages: as above.  Two launches.  Errors: as wf_paged_append. */
 int wf_paged_fork(const wf_page_dims* dims, int32_t n_forks, const int32_t* src,
                   const int32_t* dst, const int32_t* kv_len, const int32_t* share_rows,
                   int32_t* refs, int32_t* page_table, int32_t n_pools, void* const* pools,

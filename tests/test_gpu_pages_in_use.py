@@ -256,3 +256,50 @@ def test_a_window_in_a_pool_of_its_own_size(dtype, new, hq, hkv, d):
     assert held[0] > 5 * window
     assert bd.read_device_status(ws) == 0 and bd.read_device_status(ws_attn) == 0
     assert refs.sum() == (table >= 0).sum() and refs.max() == 1
+
+
+@pytest.mark.parametrize("share", [None, 0, 150, 500])
+def test_a_windowed_sequence_forks_as_it_is(share):
+    """What the parent has given back stays without a page in the child: no flag, no page taken,
+    and the child's window is the parent's."""
+    page, hkv, d, window, sinks, n = 16, 2, 64, 100, 20, 700
+    cache = {x: randn((150, hkv, page, d), BF, i) for i, x in enumerate("KV")}
+    table, refs = bd.alloc_page_table(3, 60, "cuda"), bd.alloc_page_refs(150, "cuda")
+    ws = bd.alloc_pages_workspace(cache, table, max_forks=2)
+    bd.paged_reserve(cache, table, refs, i32([n, 0, 0]), ws)
+    bd.paged_release(cache, table, refs, i32([sinks, 0, 0]), i32([n - window, 0, 0]), ws)
+    held = refs.sum().item()
+    before = table.tolist()[0]
+    rows = None if share is None else i32([share] * 2)
+    bd.paged_fork(cache, table, refs, i32([0, 0]), i32([1, 2]), i32([n, 0, 0]), rows, ws)
+    assert bd.read_device_status(ws) == 0
+    got = table.tolist()
+    assert got[0] == before
+    shared = (n if share is None else share) // page
+    free = iter(sorted(set(range(150)) - {p for p in before if p >= 0}))
+    for child in (1, 2):
+        for e, p in enumerate(before):
+            assert got[child][e] == (p if p < 0 or e < shared else next(free))
+    counts = [0] * 150
+    for p in got[0] + got[1] + got[2]:
+        if p >= 0:
+            counts[p] += 1
+    assert refs.tolist() == counts and sum(counts) == 3 * held
+    q = randn((1, 1, 4, d), BF, 9).expand(3, 1, 4, d).contiguous()
+    o = bd.paged_window_attn(q, cache, table, i32([n] * 3), window, sinks=sinks)
+    assert torch.equal(o[0], o[1]) and torch.equal(o[0], o[2])
+
+
+def test_a_fork_of_entries_outside_the_pool_is_flagged():
+    cache = {x: randn((30, 1, 8, 64), BF, i) for i, x in enumerate("KV")}
+    table, refs = bd.alloc_page_table(2, 6, "cuda"), bd.alloc_page_refs(30, "cuda")
+    ws = bd.alloc_pages_workspace(cache, table, max_forks=1)
+    bd.paged_reserve(cache, table, refs, i32([41, 0]), ws)
+    table[0, 1] = table[0, 4] = 30
+    bd.paged_fork(cache, table, refs, i32([0]), i32([1]), i32([41, 0]), i32([24]), ws)
+    assert bd.read_device_status(ws) == bd.DEV_BAD_INDEX
+    # Entry 1 was to be shared; 3, 4 and 5 take fresh pages, into that of 4 nothing is copied.
+    assert table[1].tolist() == [0, -1, 2, 6, 7, 8]
+    assert refs.tolist() == [2, 1, 2, 1, 1, 1, 1, 1, 1] + [0] * 21
+    for x in cache.values():
+        assert torch.equal(x[6], x[3]) and torch.equal(x[8, :, :1], x[5, :, :1])

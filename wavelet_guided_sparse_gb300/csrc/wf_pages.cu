@@ -45,6 +45,8 @@ __device__ __forceinline__ int ld(const int32_t* p) { return load_input<kReadOrd
 
 __device__ __forceinline__ int max_len(const PagesArgs& a) { return a.table_pages * a.page_size; }
 
+__device__ __forceinline__ int page_shift(const PagesArgs& a) { return __ffs(a.page_size) - 1; }
+
 // A length clamped into a sequence's table; flags one outside.
 __device__ __forceinline__ int length_in(const PagesArgs& a, int n, bool say) {
   if (say && (n < 0 || n > max_len(a))) raise_flag(a.status, WF_DEV_BAD_INDEX);
@@ -92,7 +94,8 @@ __device__ __forceinline__ bool bit_of(const uint32_t* words, int i) {
 }
 
 // Fork i, or entries = 0 where it is unsound (a row outside the table, a child
-// that is also a parent, or one of two forks).
+// that is also a parent, or one of two forks).  Entries that a parent has no page for
+// (what a window left behind) cost none and stay without one.
 __device__ __forceinline__ ForkUnit fork_unit(const AllocArgs& x, const AllocShared& sm, int i,
                                               bool say) {
   const PagesArgs& a = x.p;
@@ -109,9 +112,10 @@ __device__ __forceinline__ ForkUnit fork_unit(const AllocArgs& x, const AllocSha
     return u;
   }
   u.len = length_in(a, ld(x.rows + u.src), say);
-  u.entries = (u.len + a.page_size - 1) / a.page_size;
+  const int shift = page_shift(a);
+  u.entries = (u.len + a.page_size - 1) >> shift;
   const int share = x.share != nullptr ? min(max(ld(x.share + i), 0), u.len) : u.len;
-  u.shared = share / a.page_size;
+  u.shared = share >> shift;
   return u;
 }
 
@@ -119,11 +123,15 @@ __device__ __forceinline__ ForkUnit fork_unit(const AllocArgs& x, const AllocSha
 struct ReserveUnit {
   int first, end;
 };
+template <bool FROM>
 __device__ __forceinline__ ReserveUnit reserve_unit(const AllocArgs& x, int s, bool say) {
-  const int from = x.from != nullptr ? length_in(x.p, ld(x.from + s), say) : 0;
-  const int rows = length_in(x.p, ld(x.rows + s), say);
-  if (from >= rows) return {0, 0};
-  return {from / x.p.page_size, (rows + x.p.page_size - 1) / x.p.page_size};
+  const int shift = page_shift(x.p), rows = length_in(x.p, ld(x.rows + s), say);
+  ReserveUnit u = {0, (rows + x.p.page_size - 1) >> shift};
+  if (FROM) {
+    const int from = length_in(x.p, ld(x.from + s), say);
+    u.first = from < rows ? from >> shift : u.end;
+  }
+  return u;
 }
 
 // Sums of needs are cut at `most`, one page more than there are: the entries of a call
@@ -153,7 +161,8 @@ __device__ __forceinline__ void read_batch(const int32_t* from, int first, int e
   }
 }
 
-template <bool FORK>
+// FROM: a reserve with a lower bound of rows (one kernel for both costs each 0.3 us).
+template <bool FORK, bool FROM>
 __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x) {
   __shared__ AllocShared sm;
   const PagesArgs& a = x.p;
@@ -186,16 +195,29 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
   // This warp's first counts, kept: of a small pool all of them.
   int refs0[kBatch];
   read_batch(a.refs, p0, p1, lane, 1, refs0);
+  // What this warp's first unit is, kept too: behind the barriers its words would come
+  // from L2 once more.
   const int most = a.n_pages + 1;
+  ForkUnit fork0 = {};
+  ReserveUnit unit0 = {};
   int need = 0;
   for (int u = u0; u < u1; ++u) {
     if (lane == 0) x.base[u] = need;  // within the warp
     int more = 0;
     if (FORK) {
       const ForkUnit f = fork_unit(x, sm, u, lane == 0);
-      more = f.entries - f.shared;
+      if (u == u0) fork0 = f;
+      const int32_t* from = a.table + static_cast<int64_t>(max(f.src, 0)) * a.table_pages;
+      for (int e0 = f.shared; e0 < f.entries; e0 += 32 * kBatch) {
+        int parents[kBatch];
+        read_batch(from, e0, f.entries, lane, -1, parents);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          more += __popc(__ballot_sync(0xffffffffu, parents[k] >= 0));
+      }
     } else {
-      const ReserveUnit r = reserve_unit(x, u, lane == 0);
+      const ReserveUnit r = reserve_unit<FROM>(x, u, lane == 0);
+      if (u == u0) unit0 = r;
       const int32_t* row = a.table + static_cast<int64_t>(u) * a.table_pages;
       for (int e0 = r.first; e0 < r.end; e0 += 32 * kBatch) {
         int got[kBatch];
@@ -270,44 +292,46 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
   for (int u = u0; u < u1; ++u) {
     int rank = sum_cut(need_before, x.base[u], most);
     if (FORK) {
-      const ForkUnit f = fork_unit(x, sm, u, false);
+      const ForkUnit f = u == u0 ? fork0 : fork_unit(x, sm, u, false);
       if (f.dst < 0) continue;
       const int32_t* from = a.table + static_cast<int64_t>(f.src) * a.table_pages;
       int32_t* to = a.table + static_cast<int64_t>(f.dst) * a.table_pages;
       for (int e0 = 0; e0 < a.table_pages; e0 += 32 * kBatch) {
-        int parents[kBatch], fresh[kBatch];
+        int parents[kBatch], place[kBatch], fresh[kBatch];
         read_batch(from, e0, f.entries, lane, -1, parents);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          const int r = rank + e0 + 32 * k + lane - f.shared;
-          fresh[k] = r >= rank && e0 + 32 * k + lane < f.entries && r < total_free ? list[r] : -1;
+          const bool wants = parents[k] >= 0 && e0 + 32 * k + lane >= f.shared;
+          const unsigned hits = __ballot_sync(0xffffffffu, wants);
+          place[k] = rank + __popc(hits & ((1u << lane) - 1));
+          fresh[k] = wants && place[k] < total_free ? list[place[k]] : -1;
+          rank += __popc(hits);
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          const int e = e0 + 32 * k + lane, r = rank + e - f.shared;
+          const int e = e0 + 32 * k + lane;
           if (e >= a.table_pages) continue;
           int page = -1;
-          if (e < f.entries) {
-            const bool there =
-                static_cast<unsigned>(parents[k]) < static_cast<unsigned>(a.n_pages);
+          if (parents[k] >= 0) {
+            const bool there = parents[k] < a.n_pages;
             if (!there) raise_flag(a.status, WF_DEV_BAD_INDEX);
             if (e < f.shared) {
               if (there) {
                 page = parents[k];
                 atomicAdd(a.refs + page, 1);
               }
-            } else if (r < total_free) {
+            } else if (fresh[k] >= 0) {
               page = fresh[k];
               a.refs[page] = 1;
-              x.copies[r] = make_int4(there ? parents[k] : -1, page,
-                                      min(a.page_size, f.len - e * a.page_size), 0);
+              x.copies[place[k]] = make_int4(there ? parents[k] : -1, page,
+                                             min(a.page_size, f.len - e * a.page_size), 0);
             }
           }
           to[e] = page;
         }
       }
     } else {
-      const ReserveUnit unit = reserve_unit(x, u, false);
+      const ReserveUnit unit = u == u0 ? unit0 : reserve_unit<FROM>(x, u, false);
       int32_t* row = a.table + static_cast<int64_t>(u) * a.table_pages;
       for (int e0 = unit.first; e0 < unit.end; e0 += 32 * kBatch) {
         int got[kBatch], page[kBatch];
@@ -547,7 +571,7 @@ unsigned grid_of(int64_t blocks) {
 }
 
 // A pool of many pages takes a cluster.
-template <bool FORK>
+template <bool FORK, bool FROM>
 cudaError_t launch_alloc(const AllocArgs& x, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(x.p.n_pages <= kOneCta ? 1 : kAllocCluster);
@@ -560,17 +584,18 @@ cudaError_t launch_alloc(const AllocArgs& x, cudaStream_t stream) {
   attr[1].val.clusterDim = {cfg.gridDim.x, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = cfg.gridDim.x == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, alloc_kernel<FORK>, x);
+  return cudaLaunchKernelEx(&cfg, alloc_kernel<FORK, FROM>, x);
 }
 
 }  // namespace
 
 cudaError_t launch_reserve(const AllocArgs& x, cudaStream_t stream) {
-  return launch_alloc<false>(x, stream);
+  return x.from != nullptr ? launch_alloc<false, true>(x, stream)
+                           : launch_alloc<false, false>(x, stream);
 }
 
 cudaError_t launch_fork(const AllocArgs& x, const PagePools& pools, cudaStream_t stream) {
-  const cudaError_t e = launch_alloc<true>(x, stream);
+  const cudaError_t e = launch_alloc<true, false>(x, stream);
   if (e != cudaSuccess) return e;
   const int64_t most =
       std::min<int64_t>(x.p.n_pages, static_cast<int64_t>(x.units) * x.p.table_pages);
