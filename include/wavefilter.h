@@ -684,8 +684,9 @@ int wf_paged_reserve_from(const wf_page_dims* dims, const int32_t* from_rows, co
  * whole pages are shared, so that both may append; share_rows[i] = 0 copies
  * everything, for callers that rewrite rows in place.
  *   src, dst   : device, [n_forks] int32 sequences; a sequence outside the
- *                table (WF_DEV_BAD_INDEX), a child that is also a parent or is
- *                named twice (WF_DEV_DUP_INDEX): the fork is skipped
+ *                table or a child that holds a page (WF_DEV_BAD_INDEX), a child
+ *                that is also a parent or is named twice (WF_DEV_DUP_INDEX): the
+ *                fork is skipped
  *   kv_len     : device, [n_seqs] int32 (clamped and flagged as above)
  *   share_rows : device, nullable, [n_forks] int32
  *   n_forks    : 0..WF_MAX_SEQS; 0 is a no-op

@@ -303,3 +303,21 @@ def test_a_fork_of_entries_outside_the_pool_is_flagged():
     assert refs.tolist() == [2, 1, 2, 1, 1, 1, 1, 1, 1] + [0] * 21
     for x in cache.values():
         assert torch.equal(x[6], x[3]) and torch.equal(x[8, :, :1], x[5, :, :1])
+
+
+@pytest.mark.parametrize("width", [6, 700])
+def test_a_fork_into_a_child_with_pages_is_skipped(width):
+    """Its references would be lost; the other forks of the call go on."""
+    cache = {x: randn((60, 1, 8, 64), BF, i) for i, x in enumerate("KV")}
+    table, refs = bd.alloc_page_table(5, width, "cuda"), bd.alloc_page_refs(60, "cuda")
+    ws = bd.alloc_pages_workspace(cache, table, max_forks=3)
+    bd.paged_reserve(cache, table, refs, i32([41, 0, 0, 0, 9]), ws)
+    table[1, width - 1], refs[50] = 50, 1             # one page, behind everything
+    bd.paged_fork(cache, table, refs, i32([0, 0, 0]), i32([1, 2, 4]), i32([41, 0, 0, 0, 9]),
+                  i32([0, 16, 0]), ws)
+    assert bd.read_device_status(ws) == bd.DEV_BAD_INDEX
+    rest = [-1] * (width - 6)
+    assert table.tolist() == [[0, 1, 2, 3, 4, 5] + rest, [-1] * (width - 1) + [50],
+                              [0, 1, 8, 9, 10, 11] + rest, [-1] * width,
+                              [6, 7] + [-1] * (width - 2)]
+    assert refs.tolist() == [2, 2] + [1] * 10 + [0] * 38 + [1] + [0] * 9

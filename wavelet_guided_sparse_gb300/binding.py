@@ -986,7 +986,7 @@ def paged_fork(caches, page_table: torch.Tensor, refs: torch.Tensor, src: torch.
                dst: torch.Tensor, kv_len: torch.Tensor,
                share_rows: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                stream=None) -> None:
-    """wf_paged_fork: sequence dst[i], which holds no pages, becomes a copy of
+    """wf_paged_fork: sequence dst[i], which must hold no pages, becomes a copy of
     sequence src[i] (kv_len [n_seqs] rows each, of which the caller sets the
     children's): whole pages below share_rows[i] (default: all whole pages) are
     shared, the rest is copied in every layer of ``caches`` (one cache {"K",

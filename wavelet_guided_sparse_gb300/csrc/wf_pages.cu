@@ -202,18 +202,30 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
   ReserveUnit unit0 = {};
   int need = 0;
   for (int u = u0; u < u1; ++u) {
-    if (lane == 0) x.base[u] = need;  // within the warp
     int more = 0;
+    bool skip = false;
     if (FORK) {
       const ForkUnit f = fork_unit(x, sm, u, lane == 0);
       if (u == u0) fork0 = f;
+      skip = f.dst < 0;
       const int32_t* from = a.table + static_cast<int64_t>(max(f.src, 0)) * a.table_pages;
-      for (int e0 = f.shared; e0 < f.entries; e0 += 32 * kBatch) {
-        int parents[kBatch];
+      const int32_t* to = a.table + static_cast<int64_t>(max(f.dst, 0)) * a.table_pages;
+      bool held = false;
+      for (int e0 = 0; e0 < a.table_pages && !skip; e0 += 32 * kBatch) {
+        int parents[kBatch], children[kBatch];
         read_batch(from, e0, f.entries, lane, -1, parents);
+        read_batch(to, e0, a.table_pages, lane, -1, children);
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          more += __popc(__ballot_sync(0xffffffffu, parents[k] >= 0));
+        for (int k = 0; k < kBatch; ++k) {
+          held |= children[k] >= 0;
+          more += __popc(__ballot_sync(0xffffffffu, parents[k] >= 0 &&
+                                                        e0 + 32 * k + lane >= f.shared));
+        }
+      }
+      if (__any_sync(0xffffffffu, held)) {  // its references would be lost
+        if (lane == 0) raise_flag(a.status, WF_DEV_BAD_INDEX);
+        skip = true;
+        more = 0;
       }
     } else {
       const ReserveUnit r = reserve_unit<FROM>(x, u, lane == 0);
@@ -226,6 +238,7 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
         for (int k = 0; k < kBatch; ++k) more += __popc(__ballot_sync(0xffffffffu, got[k] < 0));
       }
     }
+    if (lane == 0) x.base[u] = skip ? -1 : need;  // within the warp
     need = sum_cut(need, more, most);
   }
   int free = 0;
@@ -290,10 +303,11 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
     cluster.sync();
   }
   for (int u = u0; u < u1; ++u) {
-    int rank = sum_cut(need_before, x.base[u], most);
+    const int base = x.base[u];
+    if (FORK && base < 0) continue;
+    int rank = sum_cut(need_before, base, most);
     if (FORK) {
       const ForkUnit f = u == u0 ? fork0 : fork_unit(x, sm, u, false);
-      if (f.dst < 0) continue;
       const int32_t* from = a.table + static_cast<int64_t>(f.src) * a.table_pages;
       int32_t* to = a.table + static_cast<int64_t>(f.dst) * a.table_pages;
       for (int e0 = 0; e0 < a.table_pages; e0 += 32 * kBatch) {
