@@ -639,7 +639,8 @@ int wf_paged_tree_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32
  * (the i-th entry that needs one gets the i-th lowest free page), so that
  * results do not depend on timing.  One page table serves every layer: pools
  * is a HOST array of n_pools device pointers (the K_pages and V_pages of each
- * layer, 1..WF_MAX_POOLS of them, the same sizes all), read during the call.
+ * layer, 1..WF_MAX_POOLS of them, the same sizes all; none may overlap another, one
+ * that is named twice is taken once), read during the call.
  * dims as in wf_paged_append (q_heads is not looked at).  Lengths of sequences
  * are the caller's, as in wf_paged_append. */
 

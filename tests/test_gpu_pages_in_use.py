@@ -321,3 +321,26 @@ def test_a_fork_into_a_child_with_pages_is_skipped(width):
                               [0, 1, 8, 9, 10, 11] + rest, [-1] * width,
                               [6, 7] + [-1] * (width - 2)]
     assert refs.tolist() == [2, 2] + [1] * 10 + [0] * 38 + [1] + [0] * 9
+
+
+@pytest.mark.parametrize("most", [20, 300])
+@pytest.mark.parametrize("same", ["layer", "values"])
+def test_a_pool_named_twice_is_moved_once(most, same):
+    """Rows move up in place: a second stream over the same ones would read what the first has
+    written."""
+    page, hkv, d, n = 16, 4, 128, 900
+    k, v = (randn((60, hkv, page, d), BF, i) for i in range(2))
+    layers = [{"K": k, "V": v}] * 3 if same == "layer" else [{"K": k, "V": k}]
+    table, refs = bd.alloc_page_table(1, 60, "cuda"), bd.alloc_page_refs(60, "cuda")
+    ws = bd.alloc_pages_workspace(layers[0], table, max_keep=most)
+    for seed in range(10):
+        bd.paged_reserve(layers[0], table, refs, i32([n]), ws)
+        rows = {x: t[table[0, :57].long()].transpose(1, 2).flatten(0, 1)[:n].clone()
+                for x, t in (("K", k), ("V", v))}
+        kept = sorted(np.random.default_rng(seed).choice(n, most, replace=False).tolist())
+        bd.paged_keep(layers, table, i32([n]), i32([0]), i32([kept]), i32([most]), refs, ws)
+        assert bd.read_device_status(ws) == 0
+        for x, t in (("K", k), ("V", v))[:2 if same == "layer" else 1]:
+            got = t[table[0, :-(-most // page)].long()].transpose(1, 2).flatten(0, 1)[:most]
+            assert torch.equal(got, rows[x][kept])
+        bd.paged_release(layers[0], table, refs, i32([0]), i32([MAX]), ws)

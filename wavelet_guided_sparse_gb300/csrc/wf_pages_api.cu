@@ -56,17 +56,24 @@ wf::PagesArgs pages_args(const wf_page_dims& d, int32_t* refs, int32_t* table, v
   return a;
 }
 
+// A pool that is named twice (a layer given again, keys that are the values) is taken
+// once: two streams would move its rows at the same time.
 int check_pools(int n_pools, void* const* pools, bool needed, wf::PagePools* out) {
   out->n = 0;
   if (n_pools < 0 || (needed && n_pools == 0)) return WF_ERR_SHAPE;
   if (n_pools > WF_MAX_POOLS) return WF_ERR_UNSUPPORTED;
   if (n_pools > 0 && pools == nullptr) return WF_ERR_NULL;
+  uintptr_t highest = 0;
   for (int i = 0; i < n_pools; ++i) {
     if (pools[i] == nullptr) return WF_ERR_NULL;
     if (!aligned16(pools[i])) return WF_ERR_ALIGNMENT;
-    out->at[i] = pools[i];
+    bool again = false;
+    if (reinterpret_cast<uintptr_t>(pools[i]) <= highest)
+      for (int j = 0; j < out->n; ++j) again |= out->at[j] == pools[i];
+    if (again) continue;
+    out->at[out->n++] = pools[i];
+    highest = std::max(highest, reinterpret_cast<uintptr_t>(pools[i]));
   }
-  out->n = n_pools;
   return WF_OK;
 }
 
