@@ -4,7 +4,8 @@ Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel, then the
 objects are linked into one shared library next to this file.  Only the
 ``compute_103a``/``sm_103a`` target is generated.  ``csrc/wf_torch.cpp``, the
 compiled argument marshalling of the small calls, becomes the Python module
-``_wf_torch`` beside it (host code only, against the installed torch).
+``_wf_torch`` beside it (host code only, against the installed torch).  The
+library needs no torch: where none is installed it is all that is built.
 """
 
 from __future__ import annotations
@@ -41,8 +42,11 @@ def sources():
 
 
 def _module_flags(nvcc: str):
-    """Include and link flags of the Python module."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """Include and link flags of the Python module; None without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = os.path.dirname(spec.origin)
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
     inc = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
            os.path.join(torch, "include", "torch", "csrc", "api", "include"), cuda,
@@ -61,12 +65,13 @@ def _run(what: str, cmd, verbose: bool) -> None:
 
 
 def build(verbose: bool = False, extra_flags=()) -> str:
-    """Compile every kernel source and link ``libwavefilter.so``; returns its path."""
+    """Compile every kernel source and link ``libwavefilter.so``, then (where torch is
+    installed) ``_wf_torch.so``; returns the library's path."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
 
-    inc, link = _module_flags(nvcc)
+    module = _module_flags(nvcc)
     marshal = os.path.join(BUILD, "wf_torch.o")
 
     def compile_one(src):
@@ -76,22 +81,23 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     def compile_module():
-        _run("g++ on wf_torch.cpp", ["g++", "-O2", "-std=c++17", "-fPIC", *inc, "-c",
+        _run("g++ on wf_torch.cpp", ["g++", "-O2", "-std=c++17", "-fPIC", *module[0], "-c",
                                      os.path.join(CSRC, "wf_torch.cpp"), "-o", marshal], verbose)
 
     # The longest units first.
     srcs.sort(key=os.path.getsize, reverse=True)
     srcs.sort(key=lambda f: "paged" not in os.path.basename(f))
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as pool:
-        host = pool.submit(compile_module)
+        host = pool.submit(compile_module) if module is not None else None
         objs = list(pool.map(compile_one, srcs))
-        host.result()
     tmp = LIB + ".tmp"
     _run("link", [nvcc, *ARCH, "-shared", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)
-    tmp = MODULE + ".tmp"
-    _run("link of the module", ["g++", "-shared", "-o", tmp, marshal, *link], verbose)
-    os.replace(tmp, MODULE)
+    if host is not None:
+        host.result()
+        tmp = MODULE + ".tmp"
+        _run("link of the module", ["g++", "-shared", "-o", tmp, marshal, *module[1]], verbose)
+        os.replace(tmp, MODULE)
     return LIB
 
 
