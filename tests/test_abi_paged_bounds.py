@@ -20,12 +20,12 @@ def lib():
 
 @pytest.mark.parametrize("call", [window, tree])
 @pytest.mark.parametrize("table_pages,dtype,new,refused", [
-    (131071, 1, 1, True),      # (524284 tiles of 64 keys + 4) x 4096 sequences > 2^31 - 1
-    (131071, 1, 64, True),
-    (131071, 0, 64, False),    # tiles of 128 keys
-    (131070, 1, 1, False)])    # (524280 + 4) x 4096
+    (262143, 1, 1, True),      # (524286 tiles of 64 keys + 2) x 4096 sequences > 2^31 - 1
+    (262143, 1, 64, True),
+    (262143, 0, 64, False),    # tiles of 128 keys
+    (262142, 1, 1, False)])    # (524284 + 2) x 4096
 def test_tiles_and_pads_fit_32_bits(lib, call, table_pages, dtype, new, refused):
-    d = pages(n_seqs=4096, table_pages=table_pages, page_size=256, n_pages=10, kv_heads=1,
+    d = pages(n_seqs=4096, table_pages=table_pages, page_size=128, n_pages=10, kv_heads=1,
               q_heads=1, head_dim=64, dtype=dtype)
     n = ctypes.c_size_t(0)
     assert lib.wf_paged_attn_workspace_bytes(ctypes.byref(d), new, ctypes.byref(n)) == OK

@@ -1030,13 +1030,16 @@ cudaError_t launch_masked(const PagedArgs& a, const PagedPlan& plan, cudaStream_
   return e != cudaSuccess ? e : launch_join<T, D, MASK>(a, plan, stream);
 }
 
-// The masked forms' plan: what a unit costs its CTA beside its tiles, in tiles of 64
-// keys (two CTAs an SM, one): one token in a window of 4096 over 64 sequences of 200
-// to 32768 keys 117 -> 104 us; with 3 and 4 the same, for short contexts more.  fp32
-// units take twice as long as bf16 ones with a CTA an SM.
+// The masked forms' plan.  A unit costs its CTA about two tiles of 64 keys beside its own,
+// bf16 and fp32 alike (us with pads of 0, 2, 4, 6; 32 query heads over 8, d = 128): bf16,
+// one node, 24 sequences of 540 to 25890 keys 124, 121, 121, 126, four of 300 to 1500 14.6,
+// 12.1, 12.1, 12.0; fp32, one token in a window of 2048 over 32 sequences of 200 to 16384
+// 178, 154, 156, 161, over four of 300 to 1500 21.8, 21.9, 21.3, 22.8, trees of 8 nodes over
+// 16 of 1000 to 16384 530, 504, 505, 513.
+constexpr int kPadFew = 2;
 inline PagedPlan plan_masked(const PagedArgs& a, int sm_count) {
   PagedPlan p = plan_paged(a, sm_count);
-  p.pad = p.ctas > sm_count ? 2 : 4;
+  p.pad = kPadFew;
   return p;
 }
 
