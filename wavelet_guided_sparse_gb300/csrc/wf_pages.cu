@@ -205,21 +205,29 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
     int more = 0;
     bool skip = false;
     if (FORK) {
+      // Both rows' first entries come in beside the parent's length.
+      const auto row_of = [&](int s) {
+        return a.table + static_cast<int64_t>(min(max(s, 0), a.n_seqs - 1)) * a.table_pages;
+      };
+      const int32_t *from = row_of(ld(x.src + u)), *to = row_of(ld(x.dst + u));
+      int parents[kBatch], children[kBatch];
+      read_batch(from, 0, a.table_pages, lane, -1, parents);
+      read_batch(to, 0, a.table_pages, lane, -1, children);
       const ForkUnit f = fork_unit(x, sm, u, lane == 0);
       if (u == u0) fork0 = f;
       skip = f.dst < 0;
-      const int32_t* from = a.table + static_cast<int64_t>(max(f.src, 0)) * a.table_pages;
-      const int32_t* to = a.table + static_cast<int64_t>(max(f.dst, 0)) * a.table_pages;
       bool held = false;
       for (int e0 = 0; e0 < a.table_pages && !skip; e0 += 32 * kBatch) {
-        int parents[kBatch], children[kBatch];
-        read_batch(from, e0, f.entries, lane, -1, parents);
-        read_batch(to, e0, a.table_pages, lane, -1, children);
+        if (e0 > 0) {
+          read_batch(from, e0, a.table_pages, lane, -1, parents);
+          read_batch(to, e0, a.table_pages, lane, -1, children);
+        }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
+          const int e = e0 + 32 * k + lane;
           held |= children[k] >= 0;
-          more += __popc(__ballot_sync(0xffffffffu, parents[k] >= 0 &&
-                                                        e0 + 32 * k + lane >= f.shared));
+          more += __popc(
+              __ballot_sync(0xffffffffu, parents[k] >= 0 && e >= f.shared && e < f.entries));
         }
       }
       if (__any_sync(0xffffffffu, held)) {  // its references would be lost
