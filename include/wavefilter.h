@@ -182,8 +182,8 @@ int wf_step_plan(const wf_dims* dims, const int32_t* k_per_level, wf_plan* plan)
 /* Fault injection for tests of the bounded device waits (no counterpart in
  * the paper).  Arms a one-shot injection consumed by the next kernel launch
  * that streams keys through mbarrier-counted copies (the separate DWT launch
- * of wf_step / wf_dwt_lowpass, the single-launch wf_step, wf_paged_attn, or
- * wf_prefill_attn of bf16): in its first CTA the first copy of the ring is
+ * of wf_step / wf_dwt_lowpass, the single-launch wf_step, the paged attentions,
+ * or the packed-prompt ones of bf16): in its first CTA the first copy of the ring is
  * never issued and the wait for it gives up after `polls` polls (polls >= 1),
  * which raises WF_DEV_WAIT_TIMEOUT in the workspace status word.  Every copy that was issued is still waited
  * for, so none is in flight when the kernel ends; the launch returns WF_OK,
@@ -622,7 +622,8 @@ int wf_paged_tree_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_nodes
  *              0..n_nodes (clamped and flagged otherwise; default n_nodes for
  *              all).  Rows behind a sequence's nodes get O = 0, lse = -inf,
  *              whatever their queries hold.  A sequence without nodes is idle,
- *              and so, flagged, is one with fewer rows than nodes
+ *              one without rows too (kv_len 0, whatever its tree_len), and so,
+ *              flagged, is one with fewer rows than nodes
  *   opts     : causal must be set and prefix NULL (WF_ERR_UNSUPPORTED)
  *   workspace: device, >= wf_paged_tree_attn_workspace_bytes()
  * Everything else as wf_paged_attn. */
@@ -703,8 +704,9 @@ int wf_paged_fork(const wf_page_dims* dims, int32_t n_forks, const int32_t* src,
 /* Keeps some rows of each sequence and gives back the pages behind them: rows
  * [0, start[s]) stay, rows keep[s][0 .. n_keep[s]) move up to start[s],
  * start[s] + 1, ... in every pool (the accepted path of a drafted tree, the
- * rows that a filter retains), and the pages behind the new length start[s] +
- * n_keep[s] lose a reference and their entries become -1.
+ * tokens that a caller's policy retains: one list for all heads), and the pages
+ * behind the new length start[s] + n_keep[s] lose a reference and their entries
+ * become -1.
  *   kv_len, start : device, [n_seqs] int32, 0 <= start <= kv_len
  *   keep      : device, [n_seqs, max_keep] int32, rows in [start, kv_len),
  *               strictly ascending; nullable together with n_keep (nothing

@@ -38,8 +38,8 @@ EXPORTS = ("wf_status_string", "wf_last_error_string", "wf_default_k_per_level",
            "wf_step_basis",
            "wf_rope_inv_freq", "wf_paged_append", "wf_paged_attn_workspace_bytes",
            "wf_paged_attn", "wf_prefill_attn",
-           "wf_paged_window_attn", "wf_paged_window_attn_workspace_bytes", "wf_paged_tree_attn_workspace_bytes", "wf_paged_tree_attn",
-           "wf_prefill_window_attn",
+           "wf_paged_window_attn", "wf_paged_window_attn_workspace_bytes",
+           "wf_paged_tree_attn_workspace_bytes", "wf_paged_tree_attn", "wf_prefill_window_attn",
            "wf_pages_workspace_bytes", "wf_paged_reserve", "wf_paged_reserve_from", "wf_paged_fork",
            "wf_paged_keep", "wf_paged_release")
 

@@ -387,8 +387,8 @@ __device__ __forceinline__ void idle_sequences(const PagedArgs& a, const WorkSha
   }
 }
 
-// The drafted tree of a sequence (a kernel launched early reads it), two nodes a lane (node, node + 32): ancestors
-// (with the node itself) as bits, depth.  A parent that does not come before its
+// The drafted tree of a sequence (a kernel launched early reads it), two nodes a lane
+// (node, node + 32): ancestors (with the node itself) as bits, depth.  A parent that does not come before its
 // child is flagged and taken for none.
 struct TreeNodes {
   int count;       // the sequence's nodes

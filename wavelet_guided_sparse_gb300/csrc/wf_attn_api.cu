@@ -288,8 +288,8 @@ int wf_paged_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_
                   const int32_t* kv_len, void* O, float* lse, void* workspace,
                   size_t workspace_bytes, void* stream) {
   wf::PagedArgs a;
-  const int st = paged_call(wf::plan_paged, dims, opts, n_new, Q, K_pages, V_pages, page_table, kv_len, O, lse,
-                            workspace, workspace_bytes, &a);
+  const int st = paged_call(wf::plan_paged, dims, opts, n_new, Q, K_pages, V_pages, page_table,
+                            kv_len, O, lse, workspace, workspace_bytes, &a);
   if (st != WF_OK) return st;
   return cuda_status(wf::launch_paged_attn(a, wf::plan_paged(a, wf::device_sm_count()),
                                            static_cast<cudaStream_t>(stream)));
@@ -303,22 +303,22 @@ int wf_paged_window_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int
   wf::PagedArgs a;
   int st = check_window(opts, window, sinks);
   if (st != WF_OK) return st;
-  st = paged_call(wf::plan_paged_window, dims, opts, n_new, Q, K_pages, V_pages, page_table, kv_len, O, lse, workspace,
-                  workspace_bytes, &a);
+  st = paged_call(wf::plan_paged_masked, dims, opts, n_new, Q, K_pages, V_pages, page_table, kv_len,
+                  O, lse, workspace, workspace_bytes, &a);
   if (st != WF_OK) return st;
   // So large a window hides nothing; positions minus it stay within 32 bits.
   a.window = std::min(window, INT32_MAX - 512);
   a.sinks = sinks;
-  return cuda_status(wf::launch_paged_window(a, wf::plan_paged_window(a, wf::device_sm_count()),
+  return cuda_status(wf::launch_paged_window(a, wf::plan_paged_masked(a, wf::device_sm_count()),
                                              static_cast<cudaStream_t>(stream)));
 }
 
 int wf_paged_window_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_new, size_t* bytes) {
-  return paged_bytes(dims, n_new, wf::plan_paged_window, bytes);
+  return paged_bytes(dims, n_new, wf::plan_paged_masked, bytes);
 }
 
 int wf_paged_tree_attn_workspace_bytes(const wf_page_dims* dims, int32_t n_nodes, size_t* bytes) {
-  return paged_bytes(dims, n_nodes, wf::plan_paged_tree, bytes);
+  return paged_bytes(dims, n_nodes, wf::plan_paged_masked, bytes);
 }
 
 int wf_paged_tree_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32_t n_nodes,
@@ -328,14 +328,14 @@ int wf_paged_tree_attn(const wf_page_dims* dims, const wf_attn_opts* opts, int32
                        size_t workspace_bytes, void* stream) {
   if (opts != nullptr && (opts->causal == 0 || opts->prefix != nullptr)) return WF_ERR_UNSUPPORTED;
   wf::PagedArgs a;
-  const int st = paged_call(wf::plan_paged_tree, dims, opts, n_nodes, Q, K_pages, V_pages, page_table, kv_len, O, lse,
-                            workspace, workspace_bytes, &a);
+  const int st = paged_call(wf::plan_paged_masked, dims, opts, n_nodes, Q, K_pages, V_pages,
+                            page_table, kv_len, O, lse, workspace, workspace_bytes, &a);
   if (st != WF_OK) return st;
   if (parents == nullptr) return WF_ERR_NULL;
   if (!aligned4(parents) || !aligned4(tree_len)) return WF_ERR_ALIGNMENT;
   a.parents = parents;
   a.tree_len = tree_len;
-  return cuda_status(wf::launch_paged_tree(a, wf::plan_paged_tree(a, wf::device_sm_count()),
+  return cuda_status(wf::launch_paged_tree(a, wf::plan_paged_masked(a, wf::device_sm_count()),
                                            static_cast<cudaStream_t>(stream)));
 }
 

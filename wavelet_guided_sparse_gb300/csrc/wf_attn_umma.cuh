@@ -1,6 +1,6 @@
 // Pieces of the dense attentions on the fifth-generation tensor cores (bf16;
-// packed prompts, wf_prefill.cu, and drafted trees over pages,
-// wf_paged_umma.cu): tensor-memory accesses, operand descriptors, the scores'
+// packed prompts, wf_prefill.cu, and drafted trees and windows over pages,
+// wf_paged_umma.cuh): tensor-memory accesses, operand descriptors, the scores'
 // mapping and mask, weights and the running maximum, all for 128-row tiles with
 // one softmax thread a query row.
 #pragma once
@@ -278,7 +278,10 @@ __device__ __forceinline__ float chunk_max(const float* s) {
   return fmaxf(a, b);
 }
 
-// Weights 2^(s mul - m), packed to bf16; their sum in fp32, in two parts.
+// Weights 2^(s mul - m), packed to bf16 (half a step, 2^-8 relative each: the type
+// that the tensor cores take beside bf16 values; two parts of a weight would double the
+// product with the values and the columns that it is read from); their sum, before that
+// rounding, in fp32, in two parts.
 template <int N>
 __device__ __forceinline__ void chunk_weights(const float* s, float mul, float m, uint32_t* pk,
                                               uint64_t& sum0, uint64_t& sum1) {

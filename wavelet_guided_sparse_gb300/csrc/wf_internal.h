@@ -209,10 +209,10 @@ struct PagedPlan {
 };
 PagedPlan plan_paged(const PagedArgs& a, int sm_count);
 cudaError_t launch_paged_attn(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
-// With a window, and of a drafted tree (wf_paged_window.cu, wf_paged_tree.cu).
-PagedPlan plan_paged_window(const PagedArgs& a, int sm_count);
+// With a window, and of a drafted tree (wf_paged_window.cu, wf_paged_tree.cu), with one
+// plan for both.
+PagedPlan plan_paged_masked(const PagedArgs& a, int sm_count);
 cudaError_t launch_paged_window(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
-PagedPlan plan_paged_tree(const PagedArgs& a, int sm_count);
 cudaError_t launch_paged_tree(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
 
 // Attention over packed sequences with contiguous keys and values.

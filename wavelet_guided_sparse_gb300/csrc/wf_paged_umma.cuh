@@ -19,20 +19,24 @@
 // Products wait for keys ahead by one (PAIR) or two key tiles: K_0 .. K_{L-1},
 // then V_i and K_{i+L} for i = 0, 1, ...  Warp 0 issues every product, warp 1
 // the tensor copies of queries and keys, warp 2 those of values (whole pages or
-// 128-row parts of them), warp 3 sees to idle sequences.  Keys run from a part's last tile to its first (the line of a
-// window's key tiles has a gap behind the first tokens), so that the drafted rows,
-// a tree's only ones with a mask, come first.  Weights, maximum and roundings as in
-// wf_prefill.cu.
+// 128-row parts of them), warp 3 sees to idle sequences.  Keys run from a part's last
+// tile to its first (the line of a window's key tiles has a gap behind the first
+// tokens), so that the drafted rows, a tree's only ones with a mask, come first.
+// Weights, maximum and roundings as in wf_prefill.cu: a weight meets one rounding to
+// bf16, also with 5 to 16 rows, where the mma.sync kernel takes it in two parts
+// (relative error against 64 bits 0.0020 to 0.0023 in place of 0.0017, the output's
+// own rounding; that kernel needs 24.8 us where this one takes 18.9, see kFewRows).
 //
 // Rows behind a sequence's end and rows of bad pages get weights of exactly 0,
 // and their value rows, up to the product's end, are cleared in shared memory.
 // Query rows without a node compute something and are written as O = 0.
 //
 // Measured (32 query heads, 8 of keys, d = 128; bound by HBM, whose share is of one
-// read of the cache): trees of 26 nodes over 16 sequences of 1000 to 16384 keys 88
-// us, 74 %; of 64 nodes over four of 32768 keys 111 us, 72 %, with capped scores 160,
-// with cap and bias 198 (the scores' mapping); 26 nodes over one of 131072 keys 94
-// us, 84 %.  What is missing: 5 us to the first scores, 1.5 us an output (a CTA's
+// read of the cache): trees of 26 nodes over 16 sequences of 1000 to 16384 keys 91
+// us, 71 %; of 64 nodes over four of 32768 keys 111 us, 72 %, with capped scores 161,
+// with cap and bias 200 (the scores' mapping); 26 nodes over one of 131072 keys 95
+// us, 83 %.  What is missing: 6 us to the first scores (lengths, tables and queries are
+// read behind the last kernel's end), 1.5 us an output (a CTA's
 // units follow one another), 6 us of join, and CTAs that end 5 us apart.  A softmax
 // group takes about 2900 cycles a key tile of 128 rows, as long as HBM needs for its
 // copy: with 128 rows two groups on alternate tiles leave room for the waits between

@@ -5,7 +5,7 @@
 
 namespace wf {
 
-PagedPlan plan_paged_window(const PagedArgs& a, int sm_count) {
+PagedPlan plan_paged_masked(const PagedArgs& a, int sm_count) {
   return on_umma(a) ? plan_umma(a, sm_count) : plan_masked(a, sm_count);
 }
 

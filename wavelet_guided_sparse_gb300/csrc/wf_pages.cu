@@ -2,9 +2,11 @@
 // moving kept rows together, giving them back.
 //
 // refs[p] counts the page table entries that hold page p; a page with 0 is
-// free.  Free pages are taken lowest first: the i-th entry that needs a page
-// (sequence by sequence, entry by entry) gets the i-th lowest free one, so that
-// the result is a function of the inputs alone.
+// free.  Entries without a page are negative; a reserve fills them from a row on (those
+// that a window has given back lie below it), a fork leaves them as they are.  Free
+// pages are taken lowest first: the i-th entry that needs a page (sequence by sequence,
+// entry by entry) gets the i-th lowest free one, so that the result is a function of
+// the inputs alone.
 //
 // alloc_kernel (reserve, fork) counts needs and free pages in one cluster,
 // each CTA and warp over a contiguous share of both, exchanges the counts
@@ -26,8 +28,8 @@
 // 4 layers: 338 us with the release, 92 % of the copy rate.  4096 of 32768 rows of
 // four sequences moved in 4 layers: 80 us, the copy rate (in one CTA a stream; with
 // plan and launches 94).  Small calls are launches and dependent loads: reserve and
-// keep of 16 accepted paths in 8 layers 13 us, 32 forks of shared pages in 8 layers
-// with their release 14.
+// keep of 16 accepted paths in 8 layers 13.5 us, 32 forks of shared pages in 8 layers
+// with their release 15.7.
 #include <algorithm>
 
 #include "wf_attn.cuh"
