@@ -344,3 +344,17 @@ def test_a_pool_named_twice_is_moved_once(most, same):
             got = t[table[0, :-(-most // page)].long()].transpose(1, 2).flatten(0, 1)[:most]
             assert torch.equal(got, rows[x][kept])
         bd.paged_release(layers[0], table, refs, i32([0]), i32([MAX]), ws)
+
+
+@pytest.mark.parametrize("width", [40, 700])
+def test_entries_behind_a_childs_rows_become_minus_one(width):
+    """Whatever negative number said that there was no page."""
+    cache = {x: randn((60, 1, 8, 64), BF, i) for i, x in enumerate("KV")}
+    table, refs = bd.alloc_page_table(4, width, "cuda"), bd.alloc_page_refs(60, "cuda")
+    ws = bd.alloc_pages_workspace(cache, table, max_forks=2)
+    bd.paged_reserve(cache, table, refs, i32([41, 0, 0, 0]), ws)
+    table[2], table[3, 1::3] = -9, -2
+    bd.paged_fork(cache, table, refs, i32([0, 0]), i32([2, 3]), i32([41, 0, 0, 0]), i32([41, 16]), ws)
+    assert bd.read_device_status(ws) == 0
+    rest = [-1] * (width - 6)
+    assert table[2:].tolist() == [[0, 1, 2, 3, 4, 6] + rest, [0, 1, 7, 8, 9, 10] + rest]

@@ -29,7 +29,7 @@
 // four sequences moved in 4 layers: 80 us, the copy rate (in one CTA a stream; with
 // plan and launches 94).  Small calls are launches and dependent loads: reserve and
 // keep of 16 accepted paths in 8 layers 13.5 us, 32 forks of shared pages in 8 layers
-// with their release 15.7.
+// with their release 15.5.
 #include <algorithm>
 
 #include "wf_attn.cuh"
@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
   const int most = a.n_pages + 1;
   ForkUnit fork0 = {};
   ReserveUnit unit0 = {};
+  bool odd = false;  // some child's row holds negative entries that are not -1
   int need = 0;
   for (int u = u0; u < u1; ++u) {
     int more = 0;
@@ -220,14 +221,20 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
       skip = f.dst < 0;
       bool held = false;
       for (int e0 = 0; e0 < a.table_pages && !skip; e0 += 32 * kBatch) {
+        const bool count = e0 < f.entries && e0 + 32 * kBatch > f.shared;
         if (e0 > 0) {
-          read_batch(from, e0, a.table_pages, lane, -1, parents);
+          if (count) read_batch(from, e0, f.entries, lane, -1, parents);
           read_batch(to, e0, a.table_pages, lane, -1, children);
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          const int e = e0 + 32 * k + lane;
           held |= children[k] >= 0;
+          odd |= children[k] < -1;
+        }
+        if (!count) continue;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int e = e0 + 32 * k + lane;
           more += __popc(
               __ballot_sync(0xffffffffu, parents[k] >= 0 && e >= f.shared && e < f.entries));
         }
@@ -320,7 +327,9 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const AllocArgs x)
       const ForkUnit f = u == u0 ? fork0 : fork_unit(x, sm, u, false);
       const int32_t* from = a.table + static_cast<int64_t>(f.src) * a.table_pages;
       int32_t* to = a.table + static_cast<int64_t>(f.dst) * a.table_pages;
-      for (int e0 = 0; e0 < a.table_pages; e0 += 32 * kBatch) {
+      // Behind the entries the child's are -1 already, as a rule.
+      const int end = __any_sync(0xffffffffu, odd) ? a.table_pages : f.entries;
+      for (int e0 = 0; e0 < end; e0 += 32 * kBatch) {
         int parents[kBatch], place[kBatch], fresh[kBatch];
         read_batch(from, e0, f.entries, lane, -1, parents);
 #pragma unroll
