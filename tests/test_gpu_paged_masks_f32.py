@@ -108,3 +108,17 @@ def test_visible_nans_and_infinities_show_and_hidden_ones_do_not(nodes, hq, hkv)
     assert w.isfinite().all()
     w = bd.paged_window_attn(q[:, :4].contiguous(), cache, t, i32([base + 3]), 100)
     assert w[0, 3].isnan().all() and w[0, :2].isfinite().all()
+
+
+@pytest.mark.parametrize("seqs,every", [(129, 1), (300, 3), (4096, 61), (1000, 997)])
+@pytest.mark.parametrize("dtype,hq,nodes", [(BF, 2, 2), (BF, 4, 6), (F32, 2, 3)])
+def test_live_sequences_far_apart(dtype, hq, nodes, seqs, every):
+    """Units are found past blocks of sequences, idle ones and whole idle blocks among them."""
+    rng = np.random.default_rng(seqs + nodes)
+    at = [s for s in range(seqs) if s % every == every // 2]
+    lens = [0] * seqs
+    for s in at:
+        lens[s] = int(rng.integers(nodes, 200))
+    trees = [random_tree(int(rng.integers(1, nodes + 1)), rng) if n else [] for n in lens]
+    run_tree(dtype, 64, hq, 2, 8, lens, nodes, trees, 0.0, False, seed=seqs)
+    run_window(dtype, 64, hq, 2, 8, lens, nodes, 40, 3, True, 0.0, False, seed=seqs + 1)

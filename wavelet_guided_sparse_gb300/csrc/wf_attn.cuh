@@ -195,14 +195,18 @@ struct WorkShape {
 
 // A sequence's length clamped into the table (a longer one is flagged by the
 // caller); 0 also for one without nodes, or without rows for them.
+template <int MASK>
+__device__ __forceinline__ int clamp_len(const WorkShape& w, int len, int nodes) {
+  len = min(max(len, 0), w.max_len);
+  if (MASK != kMaskTree) return len;
+  nodes = min(max(nodes, 0), w.n_new);
+  return nodes == 0 || len < nodes ? 0 : len;
+}
 template <int MASK = kMaskPlain, int READ = read_of(MASK)>
 __device__ __forceinline__ int seq_len_clamped(const WorkShape& w, const int32_t* lens, int s) {
-  const int len = min(max(load_input<READ>(lens + s), 0), w.max_len);
-  if (MASK != kMaskTree) return len;
-  const int nodes = w.tree_len != nullptr
-                        ? min(max(load_input<READ>(w.tree_len + s), 0), w.n_new)
-                        : w.n_new;
-  return nodes == 0 || len < nodes ? 0 : len;
+  const int nodes = MASK == kMaskTree && w.tree_len != nullptr ? load_input<READ>(w.tree_len + s)
+                                                               : w.n_new;
+  return clamp_len<MASK>(w, load_input<READ>(lens + s), nodes);
 }
 
 // Tiles of `keys` keys.  Tile sizes are powers of two.
@@ -246,6 +250,7 @@ __device__ __forceinline__ int tiles_of(const WorkShape& w, int len) {
 template <int MASK = kMaskPlain, int READ = read_of(MASK)>
 __device__ __forceinline__ int64_t work_total(const WorkShape& w, const int32_t* lens) {
   int n = 0;  // fits: the host bounds n_seqs times the longest sequence's tiles and pad
+#pragma unroll 4
   for (int s = threadIdx.x & 31; s < w.n_seqs; s += 32)
     n += tiles_of<MASK>(w, seq_len_clamped<MASK, READ>(w, lens, s));
 #pragma unroll
@@ -300,8 +305,26 @@ __device__ __forceinline__ WorkUnit find_unit(const WorkShape& w, const int32_t*
   const int lane = threadIdx.x & 31;
   int base = 0;
   WorkUnit u = {0, 0, 0, 1, 0};
-  for (int s0 = 0; s0 < w.n_seqs; s0 += 32) {
-    const int len = s0 + lane < w.n_seqs ? seq_len_clamped<MASK, READ>(w, lens, s0 + lane) : 0;
+  // Ordinary loads stay behind the warp's votes: the next lengths come in a step ahead.
+  const auto length = [&](int s) {
+    return s < w.n_seqs ? seq_len_clamped<MASK, READ>(w, lens, s) : 0;
+  };
+  int first = 0;
+  if constexpr (READ != kReadConst) {
+    // So blocks of 128 sequences that end before the tile are passed by their sums.
+    for (; first + 128 < w.n_seqs; first += 128) {
+      int n = 0;
+#pragma unroll
+      for (int k = 0; k < 128; k += 32) n += tiles_of<MASK>(w, length(first + k + lane));
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (static_cast<int64_t>(base + n) * w.units_per_seq > at) break;
+      base += n;
+    }
+  }
+  int ahead = READ == kReadConst ? 0 : length(first + lane);
+  for (int s0 = first; s0 < w.n_seqs; s0 += 32) {
+    const int len = READ == kReadConst ? length(s0 + lane) : ahead;
+    if (READ != kReadConst) ahead = length(s0 + 32 + lane);
     const int t = tiles_of<MASK>(w, len);
     const int incl = warp_incl_scan(t);
     const unsigned hit = __ballot_sync(
@@ -367,15 +390,24 @@ __device__ __forceinline__ void next_unit(const WorkShape& w, const int32_t* len
 template <typename T, int MASK = kMaskPlain>
 __device__ __forceinline__ void idle_sequences(const PagedArgs& a, const WorkShape& w, int c,
                                                int n, int thread, int threads) {
+  // The next sequence's words come in ahead of this one's stores (ordinary loads would
+  // wait behind them).
+  int next_len = 0, next_nodes = w.n_new;
+  const auto read = [&](int s) {
+    if (s >= a.n_seqs) return;
+    next_len = load_input<read_of(MASK)>(a.kv_len + s);
+    if (MASK == kMaskTree && w.tree_len != nullptr)
+      next_nodes = load_input<read_of(MASK)>(w.tree_len + s);
+  };
+  read(c);
   for (int s = c; s < a.n_seqs; s += n) {
-    const int len = load_input<read_of(MASK)>(a.kv_len + s);
-    bool bad = len < 0 || len > w.max_len;
-    if (MASK == kMaskTree) {
-      const int nodes = w.tree_len != nullptr ? load_input<read_of(MASK)>(w.tree_len + s) : w.n_new;
-      bad |= nodes < 0 || nodes > w.n_new || (len > 0 && len < nodes);
-    }
+    const int len = next_len, nodes = next_nodes;
+    read(s + n);
+    const bool bad = len < 0 || len > w.max_len ||
+                     (MASK == kMaskTree &&
+                      (nodes < 0 || nodes > w.n_new || (len > 0 && len < nodes)));
     if (thread == 0 && bad) raise_flag(a.status, WF_DEV_BAD_INDEX);
-    if (seq_len_clamped<MASK>(w, a.kv_len, s) > 0) continue;
+    if (clamp_len<MASK>(w, len, nodes) > 0) continue;
     const int rows = a.n_new * a.q_heads;
     uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) +
                                         static_cast<int64_t>(s) * rows * a.head_dim);
